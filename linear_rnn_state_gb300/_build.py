@@ -29,9 +29,11 @@ DEBUG_SOURCES = ["wkv7_api.cu", "wkv7_fwd2.cu", "wkv7_fwd3.cu", "wkv7_bwd2.cu", 
 
 SOURCES = ["wkv7_api.cu", "wkv7_fwd2.cu", "wkv7_fwd3.cu", "wkv7_bwd2.cu", "wkv7_bwd3.cu", "wkv7_bwd4.cu",
            "wkv7_bwd4_f32.cu", "rwkv8_api.cu",
-           "rwkv8_fwd.cu", "rwkv8_bwd.cu", "rwkv8_bwd_split.cu", "rwkv8_state.cu", "rwkv8_chunk.cu", "wkv7_epilogue.cu"]
+           "rwkv8_fwd.cu", "rwkv8_bwd.cu", "rwkv8_bwd_split.cu", "rwkv8_state.cu", "rwkv8_chunk.cu", "wkv7_epilogue.cu",
+           "gdr_api.cu", "gdr_prep.cu", "gdr_fwd.cu", "gdr_bwd.cu", "gdr_grad.cu", "gdr_step.cu", "blocknorm_api.cu",
+           "blocknorm.cu"]
 HEADERS = ["wkv7_common.cuh", "wkv7_launch.h", "wkv7_mma.cuh", "wkv7_scaled.cuh", "wkv7_tmem.cuh", "wkv7_decay.cuh",
-           "rwkv8_launch.h", "rwkv8_split.cuh"]
+           "rwkv8_launch.h", "rwkv8_split.cuh", "api_check.h", "gdr_launch.h", "gdr_common.cuh", "blocknorm_launch.h"]
 
 ARCH = ["-gencode", "arch=compute_103a,code=sm_103a"]
 NVCC_FLAGS = ARCH + ["-O3", "-lineinfo", "-std=c++17", "-Xcompiler", "-fPIC", "-cudart", "shared",
@@ -60,7 +62,7 @@ def build(force: bool = False, verbose: bool = False, extra_flags=()) -> str:
     """Compile every .cu to an object (in parallel) and link libwkv7.so."""
     os.makedirs(BUILD_DIR, exist_ok=True)
     headers = [os.path.join(CSRC, h) for h in HEADERS] + [os.path.join(INCLUDE, h)
-                                                          for h in ("wkv7.h", "rwkv8.h", "wkv7_debug.h")]
+                                                          for h in ("wkv7.h", "rwkv8.h", "wkv7_debug.h", "gdr.h", "blocknorm.h")]
     objs, dobjs, jobs = [], [], []
     for src in SOURCES:
         s = os.path.join(CSRC, src)

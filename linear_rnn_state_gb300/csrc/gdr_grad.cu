@@ -1,0 +1,466 @@
+// The gated delta rule's gradients of q, k, g and beta, every chunk and value
+// head at once, from the images the chains left: the state before the chunk
+// (S0) and u, the carried gradient after it (dS1), lam and do.
+//
+// With r_ij = e^(G_i - G_j), F_ij = scale r_ij do_i.u_j, E_ij = r_ij lam_i.u_j
+// (j < i), f_i = scale do_i.u_i and the columns' beta:
+//   dq   = scale e^G do S0 + (F beta) k          + f beta k
+//   read = -e^G lam S0 - (E beta) k              (k where it reads the state)
+//   w    = F^T q - E^T k + e^(Gc - G) u dS1      + f q
+//   dk   = read + beta w,   dbeta = k.w          (k where it writes)
+//   dG   = q.dq + k.read - beta k.w, Gc's own + <S1, dS1>; dg = its suffix sum
+// The terms with f cancel in dG and are left out of the sums that form it: a
+// sequence of one token has dg = 0 exactly, as it should. The terms of a pair
+// (i, j) cancel in dg_t for t outside (j, i], and do so to fp32 rounding,
+// because both sums are formed from the same images of F and E.
+// <S1, dS1> = e^Gc <S0, dS1> + sum_j beta_j k_j.(e^(Gc - G_j) u_j dS1).
+//
+// Value heads that share a key head write fp32 terms that a second kernel adds
+// in the order of the heads (no atomics), with the gradient of the
+// normalisation of q and k.
+#include "gdr_common.cuh"
+
+namespace gdr {
+namespace {
+
+constexpr int kThreads = 256;
+
+template <int P, int KP>
+struct Tile {
+  __half s[2 * kVt * KP], ds[2 * kVt * KP];
+  __half u[2 * kC * kVt], l[2 * kC * kVt];
+  __half d[P * kC * kVt];
+};
+struct Pairs {  // F and E as operands: columns times beta ks, and rows times qs or ks
+  __half fb[2 * kC * kC], eb[2 * kC * kC], f[2 * kC * kC], e[2 * kC * kC];
+};
+template <typename T, int KP>
+struct GradSmem {
+  static constexpr int P = In<T>::kParts;
+  __half q[P * kC * KP], k[P * kC * KP];
+  union {
+    Tile<P, KP> tile[2];
+    Pairs pairs;  // once the tiles are used up
+  };
+  Scal scal;
+  Rows rows;
+  float fd[kC];             // f_i
+  float dot[2][5][kC];      // the row sums of a half of the keys
+  float red[8][4];
+  float sdot[8];
+  float dG[kC];
+  uint64_t bar[3];
+};
+
+template <int P, int KP>
+__device__ __forceinline__ float2 pick2(const __half* s, int row, int col) {
+  const int at = img<true>(kC, row, col);
+  float2 x = unpack_f16(*reinterpret_cast<const uint32_t*>(s + at));
+  if constexpr (P == 2) {
+    const float2 y = unpack_f16(*reinterpret_cast<const uint32_t*>(s + kC * KP + at));
+    x.x += y.x, x.y += y.y;
+  }
+  return x;
+}
+
+template <int N>
+__device__ __forceinline__ void zero(float (&x)[N][4]) {
+#pragma unroll
+  for (int n = 0; n < N; ++n)
+#pragma unroll
+    for (int e = 0; e < 4; ++e) x[n][e] = 0.f;
+}
+template <int N>
+__device__ __forceinline__ void add(float (&x)[N][4], const float (&y)[N][4], float f) {
+#pragma unroll
+  for (int n = 0; n < N; ++n)
+#pragma unroll
+    for (int e = 0; e < 4; ++e) x[n][e] = fmaf(f, y[n][e], x[n][e]);
+}
+
+template <typename T, int KP, bool kShared>
+__global__ void __launch_bounds__(kThreads) grad_kernel(const Args a) {
+  extern __shared__ __align__(128) unsigned char raw[];
+  using Smem = GradSmem<T, KP>;
+  constexpr int P = In<T>::kParts, kNt = KP / 16;  // n8 tiles of a warp's half of the keys
+  Smem& sm = *reinterpret_cast<Smem*>(raw);
+  const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5, wr = warp & 3, wc = warp >> 2;
+  const int g4 = lane >> 2, t4 = lane & 3;
+  const int slot = blockIdx.x / a.s.Hv, hv = blockIdx.x % a.s.Hv, hk = hv / (a.s.Hv / a.s.Hk);
+  ChunkAt c;
+  if (!chunk_at(a.s, slot, c)) return;
+  const int vts = (a.s.V + kVt - 1) / kVt, K = a.s.K;
+  const size_t at_k = (size_t)slot * a.s.Hk + hk, at_v = (size_t)slot * a.s.Hv + hv;
+  constexpr int image = P * kC * KP * 2;
+  constexpr uint32_t kTileBytes = sizeof(Tile<P, KP>);
+
+  auto load = [&](int v) {
+    Tile<P, KP>& t = sm.tile[v & 1];
+    uint64_t* bar = &sm.bar[v & 1];
+    const size_t at = at_v * vts + v;
+    mbar_arrive_expect_tx(bar, kTileBytes);
+    bulk_load(t.s, a.b.s_img + at * sizeof(t.s), sizeof(t.s), bar);
+    bulk_load(t.ds, a.b.ds_img + at * sizeof(t.ds), sizeof(t.ds), bar);
+    bulk_load(t.u, a.b.u_img + at * sizeof(t.u), sizeof(t.u), bar);
+    bulk_load(t.l, a.b.l_img + at * sizeof(t.l), sizeof(t.l), bar);
+    bulk_load(t.d, a.b.do_img + at * sizeof(t.d), sizeof(t.d), bar);
+  };
+  if (tid == 0) {
+    for (int s = 0; s < 3; ++s) mbar_init(&sm.bar[s], 1);
+    wkv7::fence_mbar_init();
+    load(0);
+    if (vts > 1) load(1);
+    mbar_arrive_expect_tx(&sm.bar[2], 2 * image + sizeof(Scal) + sizeof(Rows));
+    bulk_load(sm.q, a.b.q_img + at_k * image, image, &sm.bar[2]);
+    bulk_load(sm.k, a.b.k_img + at_k * image, image, &sm.bar[2]);
+    bulk_load(&sm.scal, a.b.scal + at_v, sizeof(Scal), &sm.bar[2]);
+    bulk_load(&sm.rows, a.b.rows + at_k, sizeof(Rows), &sm.bar[2]);
+  }
+  __syncthreads();
+
+  const int key0 = wc * (KP / 2);
+  float dq[kNt][4], rd[kNt][4], w[kNt][4], F[4][4], E[4][4];
+  zero(dq), zero(rd), zero(w), zero(F), zero(E);
+  float sdot = 0.f;
+  for (int v = 0; v < vts; ++v) {
+    Tile<P, KP>& t = sm.tile[v & 1];
+    const size_t at = at_v * vts + v;
+    const float2 su = a.b.su[at];
+    const float4 dsl = a.b.dsl[at];
+    if (!mbar_wait_bounded(a.status, &sm.bar[v & 1], (v >> 1) & 1)) return;
+    Frag<P> fd[2];
+    Frag<2> fl[2];
+#pragma unroll
+    for (int kt = 0; kt < 2; ++kt) {
+      a_mk<P, false>(fd[kt], t.d, kC, kC * kVt, 16 * wr, 16 * kt, lane);
+      a_mk<2, false>(fl[kt], t.l, kC, kC * kVt, 16 * wr, 16 * kt, lane);
+    }
+    const float f1 = dsl.z * su.x, f2 = dsl.y * su.x, f3 = su.y * dsl.x;
+#pragma unroll
+    for (int nt = 0; nt < kNt; nt += 2) {
+      float x[4][4];
+      zero(x);
+#pragma unroll
+      for (int kt = 0; kt < 2; ++kt) {
+        Frag<2> fs;
+        b_kn<2, true>(fs, t.s, kVt, kVt * KP, key0 + 8 * nt, 16 * kt, lane);
+        mma_parts<P, 2>(x[0], x[1], fd[kt], fs);
+        mma_parts<2, 2>(x[2], x[3], fl[kt], fs);
+      }
+#pragma unroll
+      for (int h = 0; h < 2; ++h)
+#pragma unroll
+        for (int e = 0; e < 4; ++e) {
+          dq[nt + h][e] = fmaf(f1, x[h][e], dq[nt + h][e]);
+          rd[nt + h][e] = fmaf(f2, x[2 + h][e], rd[nt + h][e]);
+        }
+    }
+#pragma unroll
+    for (int b = 0; b < 2; ++b) {
+      const int jb = 2 * wc + b;
+      if (jb <= wr) {
+        float x[4][4];
+        zero(x);
+#pragma unroll
+        for (int kt = 0; kt < 2; ++kt) {
+          Frag<2> fu;
+          b_nk<2, false>(fu, t.u, kC, kC * kVt, 16 * jb, 16 * kt, lane);
+          mma_parts<P, 2>(x[0], x[1], fd[kt], fu);
+          mma_parts<2, 2>(x[2], x[3], fl[kt], fu);
+        }
+#pragma unroll
+        for (int h = 0; h < 2; ++h)
+#pragma unroll
+          for (int e = 0; e < 4; ++e) {
+            F[2 * b + h][e] = fmaf(dsl.z * su.y, x[h][e], F[2 * b + h][e]);
+            E[2 * b + h][e] = fmaf(dsl.y * su.y, x[2 + h][e], E[2 * b + h][e]);
+          }
+      }
+    }
+    {
+      Frag<2> fu[2];
+#pragma unroll
+      for (int kt = 0; kt < 2; ++kt) a_mk<2, false>(fu[kt], t.u, kC, kC * kVt, 16 * wr, 16 * kt, lane);
+#pragma unroll
+      for (int nt = 0; nt < kNt; nt += 2) {
+        float x[2][4];
+        zero(x);
+#pragma unroll
+        for (int kt = 0; kt < 2; ++kt) {
+          Frag<2> fs;
+          b_kn<2, true>(fs, t.ds, kVt, kVt * KP, key0 + 8 * nt, 16 * kt, lane);
+          mma_parts<2, 2>(x[0], x[1], fu[kt], fs);
+        }
+#pragma unroll
+        for (int h = 0; h < 2; ++h)
+#pragma unroll
+          for (int e = 0; e < 4; ++e) w[nt + h][e] = fmaf(f3, x[h][e], w[nt + h][e]);
+      }
+    }
+    // <S0, dS1>: the same place of both images
+    float sd = 0.f;
+#pragma unroll
+    for (int i = 0; i < kVt * KP / 8 / kThreads; ++i) {
+      const int at8 = (i * kThreads + tid) * 8;
+      const uint4 x0 = *reinterpret_cast<const uint4*>(t.s + at8), x1 = *reinterpret_cast<const uint4*>(t.s + kVt * KP + at8);
+      const uint4 y0 = *reinterpret_cast<const uint4*>(t.ds + at8), y1 = *reinterpret_cast<const uint4*>(t.ds + kVt * KP + at8);
+      const uint32_t xs[8] = {x0.x, x0.y, x0.z, x0.w, x1.x, x1.y, x1.z, x1.w};
+      const uint32_t ys[8] = {y0.x, y0.y, y0.z, y0.w, y1.x, y1.y, y1.z, y1.w};
+#pragma unroll
+      for (int e = 0; e < 4; ++e) {
+        const float2 xh = unpack_f16(xs[e]), xl = unpack_f16(xs[4 + e]), yh = unpack_f16(ys[e]), yl = unpack_f16(ys[4 + e]);
+        sd = fmaf(xh.x + xl.x, yh.x + yl.x, sd);
+        sd = fmaf(xh.y + xl.y, yh.y + yl.y, sd);
+      }
+    }
+    sdot = fmaf(sd, su.x * dsl.x, sdot);
+    __syncthreads();
+    if (tid == 0 && v + 2 < vts) load(v + 2);
+  }
+  if (!mbar_wait_bounded(a.status, &sm.bar[2], 0)) return;
+  const Scal& sc = sm.scal;
+  const Rows& rows = sm.rows;
+
+  // F and E with their decays; the diagonal of F apart
+  float mx[4] = {0.f, 0.f, 0.f, 0.f};
+  const int i0 = 16 * wr + g4;
+#pragma unroll
+  for (int n = 0; n < 4; ++n)
+#pragma unroll
+    for (int e = 0; e < 4; ++e) {
+      const int i = i0 + 8 * (e >> 1), j = 32 * wc + 8 * n + 2 * t4 + (e & 1);
+      if (j == i) sm.fd[i] = a.s.scale * F[n][e];
+      const float r = j < i ? expf((sc.gh[i] - sc.gh[j]) + (sc.gl[i] - sc.gl[j])) : 0.f;
+      F[n][e] = j < i ? a.s.scale * r * F[n][e] : 0.f;
+      E[n][e] = j < i ? r * E[n][e] : 0.f;
+      const float cb = sc.beta[j] * rows.ks[j];
+      mx[0] = abs_max(mx[0], F[n][e] * cb), mx[1] = abs_max(mx[1], E[n][e] * cb);
+      mx[2] = abs_max(mx[2], F[n][e] * rows.qs[i]), mx[3] = abs_max(mx[3], E[n][e] * rows.ks[i]);
+    }
+#pragma unroll
+  for (int m = 0; m < 4; ++m) {
+    mx[m] = warp_max_abs(mx[m]);
+    if (lane == 0) sm.red[warp][m] = mx[m];
+  }
+  sdot = wkv7::group_allreduce<32>(sdot);
+  if (lane == 0) sm.sdot[warp] = sdot;
+  __syncthreads();
+  float scale[4];
+#pragma unroll
+  for (int m = 0; m < 4; ++m) {
+    float x = sm.red[0][m];
+#pragma unroll
+    for (int i = 1; i < 8; ++i) x = abs_max(x, sm.red[i][m]);
+    scale[m] = pow2_scale(x);
+  }
+#pragma unroll
+  for (int n = 0; n < 4; ++n)
+#pragma unroll
+    for (int h = 0; h < 2; ++h) {
+      const int i = i0 + 8 * h, j = 32 * wc + 8 * n + 2 * t4;
+      const float c0 = sc.beta[j] * rows.ks[j], c1 = sc.beta[j + 1] * rows.ks[j + 1], x0 = F[n][2 * h], x1 = F[n][2 * h + 1],
+                  y0 = E[n][2 * h], y1 = E[n][2 * h + 1], rq = rows.qs[i], rk = rows.ks[i];
+      put2<true>(sm.pairs.fb, kC, kC * kC, i, j, (x0 * c0) * scale[0], (x1 * c1) * scale[0]);
+      put2<true>(sm.pairs.eb, kC, kC * kC, i, j, (y0 * c0) * scale[1], (y1 * c1) * scale[1]);
+      put2<true>(sm.pairs.f, kC, kC * kC, i, j, (x0 * rq) * scale[2], (x1 * rq) * scale[2]);
+      put2<true>(sm.pairs.e, kC, kC * kC, i, j, (y0 * rk) * scale[3], (y1 * rk) * scale[3]);
+    }
+  __syncthreads();
+
+  float ex[2];  // e^(Gc - G) of the thread's rows
+#pragma unroll
+  for (int h = 0; h < 2; ++h) {
+    const int i = i0 + 8 * h;
+    ex[h] = expf((sc.gh[kC - 1] - sc.gh[i]) + (sc.gl[kC - 1] - sc.gl[i]));
+  }
+  float dot[5][2];  // q.dq, k.read, k.w, beta k.(e^(Gc - G) u dS1), q.k
+#pragma unroll
+  for (int m = 0; m < 5; ++m) dot[m][0] = dot[m][1] = 0.f;
+#pragma unroll
+  for (int nt = 0; nt < kNt; nt += 2) {
+    float x[2][4], y[2][4], z[2][4], q[2][4];
+    zero(x), zero(y), zero(z), zero(q);
+#pragma unroll
+    for (int kt = 0; kt < 4; ++kt) {
+      Frag<P> fk;
+      b_kn<P, true>(fk, sm.k, kC, kC * KP, key0 + 8 * nt, 16 * kt, lane);
+      if (kt <= wr) {
+        Frag<2> f, e;
+        a_mk<2, true>(f, sm.pairs.fb, kC, kC * kC, 16 * wr, 16 * kt, lane);
+        a_mk<2, true>(e, sm.pairs.eb, kC, kC * kC, 16 * wr, 16 * kt, lane);
+        mma_parts<2, P>(x[0], x[1], f, fk);
+        mma_parts<2, P>(y[0], y[1], e, fk);
+      }
+      if (kt >= wr) {
+        Frag<2> f, e;
+        Frag<P> fq;
+        b_kn<P, true>(fq, sm.q, kC, kC * KP, key0 + 8 * nt, 16 * kt, lane);
+        a_km<2, true>(f, sm.pairs.f, kC, kC * kC, 16 * wr, 16 * kt, lane);
+        a_km<2, true>(e, sm.pairs.e, kC, kC * kC, 16 * wr, 16 * kt, lane);
+        mma_parts<2, P>(q[0], q[1], f, fq);
+        mma_parts<2, P>(z[0], z[1], e, fk);
+      }
+    }
+#pragma unroll
+    for (int b = 0; b < 2; ++b)
+#pragma unroll
+      for (int h = 0; h < 2; ++h) {
+        const int i = i0 + 8 * h, col = key0 + 8 * (nt + b) + 2 * t4;
+        const float2 qh = pick2<P, KP>(sm.q, i, col), kh = pick2<P, KP>(sm.k, i, col);
+        const float qq[2] = {qh.x * rows.qs[i], qh.y * rows.qs[i]}, kk[2] = {kh.x * rows.ks[i], kh.y * rows.ks[i]};
+#pragma unroll
+        for (int e = 0; e < 2; ++e) {
+          const int at = 2 * h + e;
+          const float s = a.s.scale * sc.eg[i] * dq[nt + b][at], tail = ex[h] * w[nt + b][at];
+          const float d = fmaf(x[b][at], pow2_inverse(scale[0]), s);
+          const float r = -fmaf(y[b][at], pow2_inverse(scale[1]), sc.eg[i] * rd[nt + b][at]);
+          const float ww = fmaf(q[b][at], pow2_inverse(scale[2]), fmaf(-z[b][at], pow2_inverse(scale[3]), tail));
+          dot[0][h] = fmaf(qq[e], d, dot[0][h]);
+          dot[1][h] = fmaf(kk[e], r, dot[1][h]);
+          dot[2][h] = fmaf(kk[e], ww, dot[2][h]);
+          dot[3][h] = fmaf(kk[e], tail, dot[3][h]);
+          dot[4][h] = fmaf(qq[e], kk[e], dot[4][h]);
+          dq[nt + b][at] = fmaf(sm.fd[i] * sc.beta[i], kk[e], d);
+          rd[nt + b][at] = fmaf(sc.beta[i], fmaf(sm.fd[i], qq[e], ww), r);  // dk
+        }
+      }
+  }
+#pragma unroll
+  for (int m = 0; m < 5; ++m)
+#pragma unroll
+    for (int h = 0; h < 2; ++h) {
+      float x = wkv7::group_allreduce<4>(dot[m][h]);
+      if (t4 == 0) sm.dot[wc][m][i0 + 8 * h] = x;
+    }
+  __syncthreads();
+  const size_t tok = (size_t)c.b * a.s.T + c.t0;
+  if (tid < kC) {
+    const int i = tid;
+    const float b = sc.beta[i], qd = sm.dot[0][0][i] + sm.dot[1][0][i], kr = sm.dot[0][1][i] + sm.dot[1][1][i],
+                kw = sm.dot[0][2][i] + sm.dot[1][2][i], qk = sm.dot[0][4][i] + sm.dot[1][4][i];
+    sm.dG[i] = qd + kr - b * kw;
+    if (i < c.len) a.dbeta[(tok + i) * a.s.Hv + hv] = fmaf(sm.fd[i], qk, kw);
+  }
+  __syncthreads();
+  if (warp == 0) {  // dg: the suffix sums, two tokens a lane
+    float x = (sm.dot[0][3][2 * lane] + sm.dot[1][3][2 * lane]) * sc.beta[2 * lane] +
+              (sm.dot[0][3][2 * lane + 1] + sm.dot[1][3][2 * lane + 1]) * sc.beta[2 * lane + 1];
+    x = wkv7::group_allreduce<32>(x);
+    float s0 = sm.sdot[0];
+#pragma unroll
+    for (int i = 1; i < 8; ++i) s0 += sm.sdot[i];
+    const float d0 = sm.dG[2 * lane], d1 = sm.dG[2 * lane + 1] + (lane == 31 ? fmaf(sc.egc, s0, x) : 0.f);
+    float s = d0 + d1;
+#pragma unroll
+    for (int o = 1; o < 32; o <<= 1) {
+      const float y = __shfl_down_sync(0xffffffffu, s, o);
+      if (lane + o < 32) s += y;
+    }
+    const float after = __shfl_down_sync(0xffffffffu, s, 1);
+    const float s1 = d1 + (lane < 31 ? after : 0.f);
+    if (2 * lane < c.len) a.dg[(tok + 2 * lane) * a.s.Hv + hv] = s;
+    if (2 * lane + 1 < c.len) a.dg[(tok + 2 * lane + 1) * a.s.Hv + hv] = s1;
+  }
+#pragma unroll
+  for (int h = 0; h < 2; ++h) {
+    const int i = i0 + 8 * h;
+    if (i >= c.len) continue;
+    float nq = 0.f, nk = 0.f;  // q.dq and k.dk of the whole row
+    const bool norm = !kShared && a.s.l2norm;
+    if (norm) {
+      const float b = sc.beta[i], f = sm.fd[i], qk = sm.dot[0][4][i] + sm.dot[1][4][i];
+      nq = fmaf(f * b, qk, sm.dot[0][0][i] + sm.dot[1][0][i]);
+      nk = fmaf(b, fmaf(f, qk, sm.dot[0][2][i] + sm.dot[1][2][i]), sm.dot[0][1][i] + sm.dot[1][1][i]);
+    }
+#pragma unroll
+    for (int nt = 0; nt < kNt; ++nt) {
+      const int col = key0 + 8 * nt + 2 * t4;
+      if (col >= K) continue;
+      float x0 = dq[nt][2 * h], x1 = dq[nt][2 * h + 1], y0 = rd[nt][2 * h], y1 = rd[nt][2 * h + 1];
+      if constexpr (kShared) {
+        const size_t at = ((tok + i) * a.s.Hv + hv) * K + col;
+        store2(a.b.dq_part + at, x0, x1);
+        store2(a.b.dk_part + at, y0, y1);
+      } else {
+        if (norm) {
+          const float2 qh = pick2<P, KP>(sm.q, i, col), kh = pick2<P, KP>(sm.k, i, col);
+          const float rq = rows.rq[i], rk = rows.rk[i];
+          x0 = rq * fmaf(-qh.x * rows.qs[i], nq, x0), x1 = rq * fmaf(-qh.y * rows.qs[i], nq, x1);
+          y0 = rk * fmaf(-kh.x * rows.ks[i], nk, y0), y1 = rk * fmaf(-kh.y * rows.ks[i], nk, y1);
+        }
+        const size_t at = ((tok + i) * a.s.Hk + hk) * K + col;
+        store2(static_cast<T*>(a.dq) + at, x0, x1);
+        store2(static_cast<T*>(a.dk) + at, y0, y1);
+      }
+    }
+  }
+}
+
+// dq and dk of a key head: its value heads' terms in order, then the gradient
+// of the normalisation. 16 lanes a row of q or k, eight keys a lane.
+template <typename T>
+__global__ void __launch_bounds__(256) join_kernel(const Args a) {
+  const size_t rows = (size_t)a.s.B * a.s.T * a.s.Hk;
+  const size_t id = ((size_t)blockIdx.x * 256 + threadIdx.x) >> 4;
+  const int cl = threadIdx.x & 15, group = a.s.Hv / a.s.Hk, K = a.s.K;
+  const bool is_k = id >= rows, in = id < 2 * rows && cl * 8 < K;
+  const size_t row = is_k ? id - rows : id;
+  float d[8] = {0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f}, x[8] = {0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f};
+  if (in) {
+    const float* part = (is_k ? a.b.dk_part : a.b.dq_part) + row * group * K + cl * 8;
+    for (int g = 0; g < group; ++g) {
+      float y[8];
+      load8(y, part + (size_t)g * K);
+#pragma unroll
+      for (int e = 0; e < 8; ++e) d[e] += y[e];
+    }
+  }
+  if (a.s.l2norm) {
+    if (in) {
+      const size_t tok = row / a.s.Hk, b = tok / a.s.T, t = tok % a.s.T, h = row % a.s.Hk;
+      load8(x, static_cast<const T*>(is_k ? a.k : a.q) + b * (is_k ? a.s.k_b : a.s.q_b) + t * (is_k ? a.s.k_t : a.s.q_t) + h * K + cl * 8);
+    }
+    float s2 = 0.f, xd = 0.f;
+#pragma unroll
+    for (int e = 0; e < 8; ++e) s2 = fmaf(x[e], x[e], s2), xd = fmaf(x[e], d[e], xd);
+    s2 = wkv7::group_allreduce<16>(s2), xd = wkv7::group_allreduce<16>(xd);
+    const float r = 1.f / sqrtf(s2 + 1e-6f), f = r * r * xd;
+#pragma unroll
+    for (int e = 0; e < 8; ++e) d[e] = r * fmaf(-f, x[e], d[e]);
+  }
+  if (in) {
+    T* out = static_cast<T*>(is_k ? a.dk : a.dq) + row * K + cl * 8;
+#pragma unroll
+    for (int e = 0; e < 4; ++e) store2(out + 2 * e, d[2 * e], d[2 * e + 1]);
+  }
+}
+
+template <typename T, int KP, bool kShared>
+cudaError_t launch(const Args& a, cudaStream_t stream) {
+  constexpr size_t smem = sizeof(GradSmem<T, KP>);
+  auto kernel = grad_kernel<T, KP, kShared>;
+  cudaError_t e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem);
+  if (e != cudaSuccess) return e;
+  kernel<<<(unsigned)((size_t)a.s.slots * a.s.Hv), kThreads, smem, stream>>>(a);
+  if ((e = cudaGetLastError()) != cudaSuccess) return e;
+  if (kShared) {
+    const size_t rows = 2 * (size_t)a.s.B * a.s.T * a.s.Hk;
+    join_kernel<T><<<(unsigned)((rows * 16 + 255) / 256), 256, 0, stream>>>(a);
+    e = cudaGetLastError();
+  }
+  return e;
+}
+template <typename T, int KP>
+cudaError_t pick(const Args& a, cudaStream_t s) {
+  return a.s.Hv == a.s.Hk ? launch<T, KP, false>(a, s) : launch<T, KP, true>(a, s);
+}
+
+}  // namespace
+
+cudaError_t launch_grad(const Args& a, bool bf16, cudaStream_t stream) {
+  const bool wide = padded_k(a.s.K) == 128;
+  if (bf16) return wide ? pick<__nv_bfloat16, 128>(a, stream) : pick<__nv_bfloat16, 64>(a, stream);
+  return wide ? pick<float, 128>(a, stream) : pick<float, 64>(a, stream);
+}
+
+}  // namespace gdr

@@ -1,0 +1,122 @@
+// Internal launch interface of the gated delta rule between the C ABI
+// (gdr_api.cu) and its kernels, and the layout of what they hand on.
+#pragma once
+
+#include <cuda_runtime.h>
+#include <stddef.h>
+#include <stdint.h>
+
+namespace gdr {
+
+constexpr int kC = 64;        // tokens of a chunk
+constexpr int kVt = 32;       // value columns of a tile
+constexpr int kMaxDim = 128;  // largest head size
+
+// What a call's sequences and heads look like.
+struct Shape {
+  int B, T, Hk, Hv, K, V;
+  int nseq;             // sequences: B, or those packed in the one batch row
+  const int* starts;    // device [nseq + 1], or null
+  int slots;            // chunk slots: an upper bound of the chunks, see slot_count
+  int l2norm;
+  float scale;
+  long long q_b, q_t, k_b, k_t, v_b, v_t;  // element strides of a batch row and of a token
+};
+
+// Every sequence's chunks get slots of their own. Dense: batch * ceil(T / 64).
+// Packed: a sequence that starts at token x is given the slots from x / 64 + s
+// on (s its number): x / 64 + ceil(len / 64) <= (x + len) / 64 + 1, so the next
+// sequence's slots start after them, and T / 64 + nseq are enough.
+inline long long slot_count(int B, int T, int nseq, bool packed) {
+  return packed ? (long long)T / kC + nseq : (long long)B * ((T + kC - 1) / kC);
+}
+
+inline int padded_k(int K) { return K <= 64 ? 64 : 128; }
+inline int v_tiles(int V) { return (V + kVt - 1) / kVt; }
+
+// Scalars of a chunk: per key head (Rows) and per value head (Scal).
+struct Rows {        // of the 64 tokens, the actual q is qs * image (and k is ks * image)
+  float qs[kC], ks[kC];
+  float rq[kC], rk[kC];  // 1 / |q|, 1 / |k| with l2norm, else 1
+};
+struct Scal {
+  float eg[kC];    // e^G, G the running sum of g in the chunk
+  float wr[kC];    // beta e^(Gc - G), Gc the chunk's whole sum
+  float gh[kC], gl[kC];  // G as an unrounded sum of two floats
+  float beta[kC];
+  // scales of the T and P images (their inverses) and bounds, all of magnitudes
+  float inv_t, inv_p;
+  float t_sum, p_sum;  // 64 times the largest of |T|, |P|
+  float k_read;        // max e^G sum|k|
+  float k_write;       // sum |wr| max|k|
+  float wk_max;        // max |wr| ks
+  float k_back;        // max |wr| sum|k|
+  float q_sum, k_sum;  // sum |scale| e^G max|q|, sum e^G max|k|
+  float ek_max, eq_max;  // max e^G ks, max |scale| e^G qs
+  float egc;           // e^Gc
+  float pad[19];
+};
+static_assert(sizeof(Scal) % 128 == 0 && sizeof(Rows) % 128 == 0, "bulk copies");
+
+struct Layout {
+  int Kp, vt, parts;
+  size_t n_k, n_v, n_t;           // (slot, key head), (slot, value head), (slot, value head, tile) counts
+  size_t kq_img, st_img, u_img, do_img;  // bytes of one image
+  static constexpr size_t tp_img = 2 * kC * kC * 2;
+};
+inline Layout layout(const Shape& s, bool bf16) {
+  Layout l;
+  l.Kp = padded_k(s.K);
+  l.vt = v_tiles(s.V);
+  l.parts = bf16 ? 1 : 2;
+  l.n_k = (size_t)s.slots * s.Hk;
+  l.n_v = (size_t)s.slots * s.Hv;
+  l.n_t = l.n_v * l.vt;
+  l.kq_img = (size_t)l.parts * kC * l.Kp * 2;
+  l.st_img = (size_t)2 * kVt * l.Kp * 2;
+  l.u_img = (size_t)2 * kC * kVt * 2;
+  l.do_img = (size_t)l.parts * kC * kVt * 2;
+  return l;
+}
+
+// The regions of the caller's `saved` buffer (first line: always; second: for a
+// backward) and of the backward's workspace.
+struct Buffers {
+  char *k_img, *q_img, *t_img, *p_img;
+  Rows* rows;
+  Scal* scal;
+  char *s_img, *u_img;  // the state before each chunk and the chunk's u, a tile of value columns each
+  float2* su;           // the inverse scales of those two images
+  char *ds_img, *l_img, *do_img;  // the carried gradient after each chunk, lambda and do
+  float4* dsl;                    // the inverse scales of those three
+  float *dq_part, *dk_part;       // [B][T][Hv][K] terms of shared heads' gradients, or null
+};
+
+struct Args {
+  Shape s;
+  const void *q, *k, *v, *d_o;
+  const float *g, *beta, *s_init, *dS_final;
+  void *o, *dq, *dk, *dv;
+  float *s_final, *dg, *dbeta, *dS_init;
+  Buffers b;
+  unsigned* status;
+};
+
+cudaError_t launch_prep(const Args& a, bool bf16, cudaStream_t stream);
+cudaError_t launch_fwd(const Args& a, bool bf16, bool save, cudaStream_t stream);
+cudaError_t launch_bwd(const Args& a, bool bf16, cudaStream_t stream);
+cudaError_t launch_grad(const Args& a, bool bf16, cudaStream_t stream);
+
+struct StepArgs {
+  const void *q, *k, *v;
+  const float *g, *beta;
+  float* state;        // [slots][Hv][V][K]
+  const int* slots;    // [R], negative: skip; or null for 0 .. R-1
+  void* o;
+  int R, T, Hk, Hv, K, V, n_slots, l2norm;
+  float scale;
+  long long q_b, q_t, k_b, k_t, v_b, v_t;
+};
+cudaError_t launch_step(const StepArgs& a, bool bf16, cudaStream_t stream);
+
+}  // namespace gdr

@@ -1,0 +1,263 @@
+// What the gated delta rule's chunks need before the states are known, for
+// every chunk of 64 tokens and key head at once.
+//
+// With G the running sum of g in the chunk and r_ij = e^(G_i - G_j) (j <= i):
+//   L_ij = beta_j r_ij k_i.k_j  (j < i),    T = (I + L)^-1
+//   P_ij = scale beta_j r_ij q_i.k_j  (j <= i)
+// so that with S0 the state before the chunk u = T (v - e^G S0 k) and
+// o = scale e^G S0 q + P u. The kernel writes q, k, T and P as the images that
+// the chain kernels copy into shared memory, with their scales and the bounds
+// the chains need (gdr_launch.h, Rows and Scal).
+//
+// The decay ratios. G is summed in double and kept as two floats, and r_ij is
+// the exponential of a difference, never a product of e^G_i with e^-G_j, so
+// that strong decays neither overflow nor lose the small differences. g below
+// -200 counts as -200 (e^-200 is 0 in fp32 either way), which makes -inf a
+// reset of the state instead of inf - inf.
+//
+// T by forward substitution in fp32, one column a thread.
+#include "gdr_common.cuh"
+
+namespace gdr {
+namespace {
+
+constexpr int kThreads = 128;
+constexpr int kLd = 68;  // row stride of the fp32 64 x 64 tiles: rows stay 16-byte aligned
+
+template <typename T, int KP>
+struct PrepSmem {
+  static constexpr int P = In<T>::kParts;
+  __half q[P * kC * KP], k[P * kC * KP];
+  union {
+    float L[kC * kLd];
+    float wide[kC * kLd];
+  };
+  __half out[2 * kC * kC];
+  Rows rows;
+  Scal scal;
+  float q_max[kC], k_max[kC], k_sum[kC];
+  float red[8];
+};
+
+__device__ __forceinline__ void copy16(void* dst, const void* src, int bytes, int tid) {
+  for (int i = tid; i < bytes / 16; i += kThreads)
+    reinterpret_cast<uint4*>(dst)[i] = reinterpret_cast<const uint4*>(src)[i];
+}
+
+// One of q, k: 64 rows into an image, each row scaled by a power of two.
+template <typename T, int KP>
+__device__ __forceinline__ void load_rows(__half* image, float* inv, float* rn, float* mx, float* sm, const T* src,
+                                          long long stride_t, int len, int K, int l2norm, int tid) {
+  constexpr int P = In<T>::kParts, kLanes = KP / 8, kPass = kThreads / kLanes;
+  const int cl = tid % kLanes, part = kC * KP;
+#pragma unroll 2
+  for (int row = tid / kLanes; row < kC; row += kPass) {
+    float x[8] = {0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f};
+    if (row < len && cl * 8 < K) load8(x, src + (size_t)row * stride_t + cl * 8);
+    float m = 0.f, s1 = 0.f, s2 = 0.f;
+#pragma unroll
+    for (int e = 0; e < 8; ++e) m = abs_max(m, x[e]), s1 += fabsf(x[e]), s2 = fmaf(x[e], x[e], s2);
+#pragma unroll
+    for (int o = 1; o < kLanes; o <<= 1) {
+      m = abs_max(m, __shfl_xor_sync(0xffffffffu, m, o));
+      s1 += __shfl_xor_sync(0xffffffffu, s1, o);
+      s2 += __shfl_xor_sync(0xffffffffu, s2, o);
+    }
+    const float sc = pow2_scale(m), r = l2norm ? 1.f / sqrtf(s2 + 1e-6f) : 1.f;
+    uint32_t hi[4], lo[4];
+#pragma unroll
+    for (int e = 0; e < 4; ++e) split2<P>(x[2 * e] * sc, x[2 * e + 1] * sc, hi[e], lo[e]);
+    const int at = img<true>(kC, row, cl * 8);
+    *reinterpret_cast<uint4*>(image + at) = make_uint4(hi[0], hi[1], hi[2], hi[3]);
+    if constexpr (P == 2) *reinterpret_cast<uint4*>(image + part + at) = make_uint4(lo[0], lo[1], lo[2], lo[3]);
+    if (cl == 0) inv[row] = pow2_inverse(sc) * r, rn[row] = r, mx[row] = m * r, sm[row] = s1 * r;
+  }
+}
+
+// Largest of the block's values; every thread gets it. `red` is reused: a
+// barrier stands before and after.
+__device__ __forceinline__ float block_max(float x, float* red, int tid) {
+  x = warp_max_abs(x);
+  __syncthreads();
+  if ((tid & 31) == 0) red[tid >> 5] = x;
+  __syncthreads();
+  float m = red[0];
+#pragma unroll
+  for (int w = 1; w < kThreads / 32; ++w) m = abs_max(m, red[w]);
+  return m;
+}
+
+template <typename T, int KP>
+__global__ void __launch_bounds__(kThreads) prep_kernel(const Args a) {
+  extern __shared__ __align__(128) unsigned char raw[];
+  PrepSmem<T, KP>& sm = *reinterpret_cast<PrepSmem<T, KP>*>(raw);
+  constexpr int P = In<T>::kParts;
+  const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
+  const int slot = blockIdx.x / a.s.Hk, hk = blockIdx.x % a.s.Hk;
+  ChunkAt c;
+  if (!chunk_at(a.s, slot, c)) return;
+  const size_t at_k = (size_t)slot * a.s.Hk + hk;
+  load_rows<T, KP>(sm.q, sm.rows.qs, sm.rows.rq, sm.q_max, sm.wide,
+                   static_cast<const T*>(a.q) + c.b * a.s.q_b + c.t0 * a.s.q_t + hk * a.s.K, a.s.q_t, c.len, a.s.K,
+                   a.s.l2norm, tid);
+  load_rows<T, KP>(sm.k, sm.rows.ks, sm.rows.rk, sm.k_max, sm.k_sum,
+                   static_cast<const T*>(a.k) + c.b * a.s.k_b + c.t0 * a.s.k_t + hk * a.s.K, a.s.k_t, c.len, a.s.K,
+                   a.s.l2norm, tid);
+  __syncthreads();
+  const int image = P * kC * KP * 2;
+  copy16(a.b.q_img + at_k * image, sm.q, image, tid);
+  copy16(a.b.k_img + at_k * image, sm.k, image, tid);
+  copy16(a.b.rows + at_k, &sm.rows, sizeof(Rows), tid);
+
+  // q k^T and k k^T, the 16 rows of a warp against the columns up to them
+  float qk[8][4], kk[8][4];
+#pragma unroll
+  for (int n = 0; n < 8; ++n)
+#pragma unroll
+    for (int e = 0; e < 4; ++e) qk[n][e] = kk[n][e] = 0.f;
+#pragma unroll
+  for (int kt = 0; kt < KP / 16; ++kt) {
+    Frag<P> fq, fk;
+    a_mk<P, true>(fq, sm.q, kC, kC * KP, 16 * warp, 16 * kt, lane);
+    a_mk<P, true>(fk, sm.k, kC, kC * KP, 16 * warp, 16 * kt, lane);
+#pragma unroll
+    for (int n = 0; n < 4; ++n)
+      if (n <= warp) {
+        Frag<P> fb;
+        b_nk<P, true>(fb, sm.k, kC, kC * KP, 16 * n, 16 * kt, lane);
+        mma_parts<P, P>(qk[2 * n], qk[2 * n + 1], fq, fb);
+        mma_parts<P, P>(kk[2 * n], kk[2 * n + 1], fk, fb);
+      }
+  }
+
+  const int g4 = lane >> 2, t4 = lane & 3, group = a.s.Hv / a.s.Hk;
+  for (int hg = 0; hg < group; ++hg) {
+    const int hv = hk * group + hg;
+    const size_t at_v = (size_t)slot * a.s.Hv + hv;
+    if (warp == 0) {  // the running sum of g, two tokens a lane
+      const size_t gat = ((size_t)c.b * a.s.T + c.t0) * a.s.Hv + hv;
+      double x[2];
+#pragma unroll
+      for (int e = 0; e < 2; ++e) {
+        const int i = 2 * lane + e;
+        const float gi = i < c.len ? a.g[gat + (size_t)i * a.s.Hv] : 0.f;
+        x[e] = gi < -200.f ? -200.f : gi;
+        sm.scal.beta[i] = i < c.len ? a.beta[gat + (size_t)i * a.s.Hv] : 0.f;
+      }
+      double s = x[0] + x[1];
+#pragma unroll
+      for (int o = 1; o < 32; o <<= 1) {
+        const double y = __shfl_up_sync(0xffffffffu, s, o);
+        if (lane >= o) s += y;
+      }
+      const double G[2] = {s - x[1], s}, Gc = __shfl_sync(0xffffffffu, s, 31);
+      float kr = 0.f, kw = 0.f, wk = 0.f, kb = 0.f, qsum = 0.f, ksum = 0.f, ek = 0.f, eq = 0.f;
+#pragma unroll
+      for (int e = 0; e < 2; ++e) {
+        const int i = 2 * lane + e;
+        const float hi = (float)G[e], lo = (float)(G[e] - hi), th = (float)(Gc - G[e]), tl = (float)(Gc - G[e] - th);
+        const float eg = expf(hi) * (1.f + lo), w = expf(th) * (1.f + tl) * sm.scal.beta[i];
+        sm.scal.gh[i] = hi, sm.scal.gl[i] = lo, sm.scal.eg[i] = eg, sm.scal.wr[i] = w;
+        const float sc = fabsf(a.s.scale) * eg, aw = fabsf(w);
+        kr = abs_max(kr, eg * sm.k_sum[i]), kw += aw * sm.k_max[i], wk = abs_max(wk, aw * sm.rows.ks[i]);
+        kb = abs_max(kb, aw * sm.k_sum[i]), qsum += sc * sm.q_max[i], ksum += eg * sm.k_max[i];
+        ek = abs_max(ek, eg * sm.rows.ks[i]), eq = abs_max(eq, sc * sm.rows.qs[i]);
+      }
+      kr = warp_max_abs(kr), wk = warp_max_abs(wk), kb = warp_max_abs(kb), ek = warp_max_abs(ek), eq = warp_max_abs(eq);
+      kw = wkv7::group_allreduce<32>(kw), qsum = wkv7::group_allreduce<32>(qsum), ksum = wkv7::group_allreduce<32>(ksum);
+      if (lane == 31) {
+        const float ch = (float)Gc, cl = (float)(Gc - ch);
+        Scal& o = sm.scal;
+        o.egc = expf(ch) * (1.f + cl);
+        o.k_read = kr, o.k_write = kw, o.wk_max = wk, o.k_back = kb, o.q_sum = qsum, o.k_sum = ksum, o.ek_max = ek;
+        o.eq_max = eq;
+      }
+    }
+    __syncthreads();
+    float p[8][4], pm = 0.f;
+#pragma unroll
+    for (int n = 0; n < 8; ++n)
+      if (n < 2 * warp + 2) {
+#pragma unroll
+        for (int e = 0; e < 4; ++e) {
+          const int i = 16 * warp + g4 + 8 * (e >> 1), j = 8 * n + 2 * t4 + (e & 1);
+          float r = 0.f;
+          if (j <= i) r = expf((sm.scal.gh[i] - sm.scal.gh[j]) + (sm.scal.gl[i] - sm.scal.gl[j])) * sm.rows.ks[j];
+          const float rb = r * sm.scal.beta[j];
+          p[n][e] = j <= i ? a.s.scale * (sm.rows.qs[i] * qk[n][e]) * rb : 0.f;
+          pm = abs_max(pm, p[n][e]);
+          sm.L[i * kLd + j] = j < i ? sm.rows.ks[i] * kk[n][e] * rb : 0.f;
+        }
+      } else {
+#pragma unroll
+        for (int e = 0; e < 4; ++e) p[n][e] = 0.f;
+      }
+    pm = block_max(pm, sm.red, tid);
+    const float ps = pow2_scale(pm);
+#pragma unroll
+    for (int n = 0; n < 8; ++n)
+#pragma unroll
+      for (int h = 0; h < 2; ++h)
+        put2<true>(sm.out, kC, kC * kC, 16 * warp + g4 + 8 * h, 8 * n + 2 * t4, p[n][2 * h] * ps, p[n][2 * h + 1] * ps);
+    __syncthreads();
+    copy16(a.b.p_img + at_v * Layout::tp_img, sm.out, Layout::tp_img, tid);
+
+    // column j of T: T[i][j] = [i == j] - sum_{m < i} L[i][m] T[m][j]
+    float col[kC], tm = 0.f;
+    if (tid < kC) {
+#pragma unroll
+      for (int i = 0; i < kC; ++i) {
+        float x0 = i == tid ? 1.f : 0.f, x1 = 0.f, x2 = 0.f, x3 = 0.f;
+#pragma unroll
+        for (int m = 0; m < i; m += 4) {
+          const float4 l = *reinterpret_cast<const float4*>(sm.L + i * kLd + m);
+          x0 = fmaf(-l.x, col[m], x0);
+          if (m + 1 < i) x1 = fmaf(-l.y, col[m + 1], x1);
+          if (m + 2 < i) x2 = fmaf(-l.z, col[m + 2], x2);
+          if (m + 3 < i) x3 = fmaf(-l.w, col[m + 3], x3);
+        }
+        col[i] = i < tid ? 0.f : (x0 + x1) + (x2 + x3);
+        tm = abs_max(tm, col[i]);
+      }
+    }
+    tm = block_max(tm, sm.red, tid);  // its barriers also stand between the copy of P and the writes of T
+    const float ts = pow2_scale(tm);
+    if (tid < kC) {
+#pragma unroll
+      for (int i = 0; i < kC; ++i) {
+        const float x = col[i] * ts;
+        const __half h = __float2half_rn(x);
+        const int at = img<true>(kC, i, tid);
+        sm.out[at] = h;
+        sm.out[at + kC * kC] = __float2half_rn(x - __half2float(h));
+      }
+    }
+    if (tid == 0) {
+      sm.scal.inv_p = pow2_inverse(ps), sm.scal.inv_t = pow2_inverse(ts);
+      sm.scal.p_sum = kC * pm, sm.scal.t_sum = kC * tm;
+    }
+    __syncthreads();
+    copy16(a.b.t_img + at_v * Layout::tp_img, sm.out, Layout::tp_img, tid);
+    copy16(a.b.scal + at_v, &sm.scal, sizeof(Scal), tid);
+    __syncthreads();
+  }
+}
+
+template <typename T, int KP>
+cudaError_t launch(const Args& a, cudaStream_t stream) {
+  constexpr size_t smem = sizeof(PrepSmem<T, KP>);
+  cudaError_t e = cudaFuncSetAttribute(prep_kernel<T, KP>, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem);
+  if (e != cudaSuccess) return e;
+  prep_kernel<T, KP><<<(unsigned)((size_t)a.s.slots * a.s.Hk), kThreads, smem, stream>>>(a);
+  return cudaGetLastError();
+}
+
+}  // namespace
+
+cudaError_t launch_prep(const Args& a, bool bf16, cudaStream_t stream) {
+  const bool wide = padded_k(a.s.K) == 128;
+  if (bf16) return wide ? launch<__nv_bfloat16, 128>(a, stream) : launch<__nv_bfloat16, 64>(a, stream);
+  return wide ? launch<float, 128>(a, stream) : launch<float, 64>(a, stream);
+}
+
+}  // namespace gdr

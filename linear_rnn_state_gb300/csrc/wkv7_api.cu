@@ -496,6 +496,7 @@ int backward_impl(bool bf16, const void* const in[7], const float* s_init, const
 // Error hook for the other entry points of the library (rwkv8_api.cu): the
 // message goes to the same thread-local slot wkv7_last_error() reads.
 int api_fail(int code, const char* msg) { return fail(code, "%s", msg); }
+int api_status_word(unsigned** out) { return status_word(out); }
 
 // ======================================== backward without allocation ===
 //

@@ -1,0 +1,225 @@
+"""Python binding of the gated delta rule's C ABI (include/gdr.h).
+
+Argument checks and marshalling only: the recurrence runs in the CUDA kernels
+of libwkv7.so (the same library as the WKV7 scan). The raw functions carry the
+C names and take integer device addresses; ``forward``, ``backward`` and
+``step`` take torch tensors, allocate the outputs and workspaces with torch on
+the stream they run on (torch's current stream unless ``stream`` is given) and
+call the raw functions there. There is no CPU path.
+
+    S_t = e^{g_t} S_{t-1} + beta_t (v_t - e^{g_t} S_{t-1} k_t) k_t^T,   o_t = scale S_t q_t
+
+q, k [B][T][Hk][K]; v, o [B][T][Hv][V] (float32 or bfloat16); g, beta [B][T][Hv]
+and states [n][Hv][V][K] float32. q, k, v may be slices of a wider tensor.
+"""
+from __future__ import annotations
+
+import contextlib
+import ctypes
+
+from . import wkv7
+
+CHUNK = 64  # tokens of a chunk
+
+# C functions declared in include/gdr.h, with their argument counts.
+EXPORTS = {
+    "gdr_saved_bytes": 9,
+    "gdr_backward_bytes": 8,
+    "gdr_forward": 22,
+    "gdr_forward_bf16": 22,
+    "gdr_backward": 27,
+    "gdr_backward_bf16": 27,
+    "gdr_step": 18,
+    "gdr_step_bf16": 18,
+}
+
+_typed = set()
+
+
+def load(path: str | None = None):
+    """The loaded library with the gdr_* signatures set."""
+    lib = wkv7.load(path)
+    if id(lib) not in _typed:
+        vp, i, f = ctypes.c_void_p, ctypes.c_int, ctypes.c_float
+        lib.gdr_saved_bytes.argtypes = [i] * 9
+        lib.gdr_backward_bytes.argtypes = [i] * 8
+        for name in ("gdr_saved_bytes", "gdr_backward_bytes"):
+            getattr(lib, name).restype = ctypes.c_size_t
+        for suffix in ("", "_bf16"):
+            getattr(lib, "gdr_forward" + suffix).argtypes = [vp] * 11 + [f] + [i] * 9 + [vp]
+            getattr(lib, "gdr_backward" + suffix).argtypes = [vp] * 17 + [f] + [i] * 8 + [vp]
+            getattr(lib, "gdr_step" + suffix).argtypes = [vp] * 9 + [f] + [i] * 7 + [vp]
+            for name in ("gdr_forward", "gdr_backward", "gdr_step"):
+                getattr(lib, name + suffix).restype = i
+        _typed.add(id(lib))
+    return lib
+
+
+# ------------------------------------------------------- torch helpers ---
+
+def _addr(t):
+    return None if t is None else t.data_ptr()
+
+
+@contextlib.contextmanager
+def _on(stream):
+    """Makes `stream` torch's current one (so that what is allocated belongs to
+    it) and yields its handle."""
+    import torch
+
+    if stream is None:
+        yield torch.cuda.current_stream().cuda_stream
+    else:
+        with torch.cuda.stream(stream):
+            yield stream.cuda_stream
+
+
+def _check_tensor(name, t, shape, dtype, device, dense=True):
+    if tuple(t.shape) != tuple(shape):
+        raise ValueError(f"{name} must have the shape {tuple(shape)}, got {tuple(t.shape)}")
+    if t.dtype != dtype:
+        raise TypeError(f"{name} must be {dtype}, got {t.dtype}")
+    if t.device != device:
+        raise ValueError(f"{name} is on {t.device}, not on {device}")
+    if dense and not t.is_contiguous():
+        raise ValueError(f"{name} must be contiguous")
+
+
+def _check_device(t):
+    import torch
+
+    if t.device.type != "cuda":
+        raise ValueError(f"tensors must be on a CUDA device, got {t.device}")
+    if t.device.index != torch.cuda.current_device():
+        raise ValueError(f"tensors are on {t.device}, but the current device is cuda:{torch.cuda.current_device()}")
+
+
+def _strides(*ts):
+    """The strides of q, k, v for the C call, or None where all are dense."""
+    if all(t.is_contiguous() for t in ts):
+        return None
+    for name, t in zip("qkv", ts):
+        D = t.shape[3]
+        if (t.shape[3] > 1 and t.stride(3) != 1) or (t.shape[2] > 1 and t.stride(2) != D):
+            raise ValueError(f"{name}: a token's heads must be dense (strides {t.stride()})")
+    return (ctypes.c_longlong * 6)(*(x for t in ts for x in (t.stride(0), t.stride(1))))
+
+
+def _inputs(q, k, v, g, beta):
+    """Checks the inputs against each other; returns bf16, (B, T, Hk, Hv, K, V), device."""
+    import torch
+
+    bf16 = wkv7._inputs_dtype(q)
+    if q.dim() != 4 or v.dim() != 4:
+        raise ValueError("q, k and v must be [B][T][heads][size]")
+    B, T, Hk, K = q.shape
+    Hv, V = v.shape[2:]
+    dev = q.device
+    _check_device(q)
+    _check_tensor("k", k, (B, T, Hk, K), q.dtype, dev, False)
+    _check_tensor("v", v, (B, T, Hv, V), q.dtype, dev, False)
+    _check_tensor("g", g, (B, T, Hv), torch.float32, dev)
+    _check_tensor("beta", beta, (B, T, Hv), torch.float32, dev)
+    return bf16, (B, T, Hk, Hv, K, V), dev
+
+
+def _sequences(seq_starts, B, dev):
+    """(states, nseq of the C call)."""
+    import torch
+
+    if seq_starts is None:
+        return B, -1
+    if seq_starts.dim() != 1 or seq_starts.numel() < 1:
+        raise ValueError("seq_starts must hold the sequences' starts and the last one's end")
+    n = seq_starts.numel() - 1
+    _check_tensor("seq_starts", seq_starts, (n + 1,), torch.int32, dev)
+    return n, n
+
+
+def saved_bytes(B, T, Hk, Hv, K, V, nseq=-1, *, bf16, for_backward) -> int:
+    return load().gdr_saved_bytes(B, T, Hk, Hv, K, V, nseq, int(bf16), int(for_backward))
+
+
+def forward(q, k, v, g, beta, s_init=None, *, scale: float | None = None, qk_l2norm: bool = False, seq_starts=None,
+            want_saved: bool = True, want_s_final: bool = True, stream=None):
+    """The recurrence over whole sequences, in chunks. scale: K ** -0.5 unless
+    given. qk_l2norm divides q and k by their lengths. seq_starts (int32,
+    one more than the sequences; B = 1) gives packed sequences' starts.
+    Returns (o, s_final, saved); saved is what ``backward`` needs (None
+    without want_saved)."""
+    import torch
+
+    lib = load()
+    bf16, dims, dev = _inputs(q, k, v, g, beta)
+    B, T, Hk, Hv, K, V = dims
+    n, nseq = _sequences(seq_starts, B, dev)
+    if s_init is not None:
+        _check_tensor("s_init", s_init, (n, Hv, V, K), torch.float32, dev)
+    with _on(stream) as handle:
+        o = torch.empty((B, T, Hv, V), dtype=q.dtype, device=dev)
+        s_final = torch.empty((n, Hv, V, K), dtype=torch.float32, device=dev) if want_s_final else None
+        saved = torch.empty(lib.gdr_saved_bytes(*dims, nseq, bf16, want_saved), dtype=torch.uint8, device=dev)
+        fn = lib.gdr_forward_bf16 if bf16 else lib.gdr_forward
+        wkv7._check(fn(*(_addr(x) for x in (q, k, v, g, beta, s_init, seq_starts, o, s_final, saved)), _strides(q, k, v),
+                       K ** -0.5 if scale is None else scale, qk_l2norm, want_saved, *dims, nseq, handle))
+    return o, s_final, saved if want_saved else None
+
+
+def backward(q, k, v, g, beta, do, saved, *, dS_final=None, want_dS_init: bool = True, scale: float | None = None,
+             qk_l2norm: bool = False, seq_starts=None, stream=None):
+    """Gradients of sum <do, o> + <dS_final, s_final>, with the ``saved`` of a
+    ``forward`` of the same inputs and options. Returns dict dq, dk, dv (the
+    inputs' type), dg, dbeta and dS_init (float32; None without
+    want_dS_init)."""
+    import torch
+
+    lib = load()
+    bf16, dims, dev = _inputs(q, k, v, g, beta)
+    B, T, Hk, Hv, K, V = dims
+    n, nseq = _sequences(seq_starts, B, dev)
+    _check_tensor("do", do, (B, T, Hv, V), q.dtype, dev)
+    if dS_final is not None:
+        _check_tensor("dS_final", dS_final, (n, Hv, V, K), torch.float32, dev)
+    need = lib.gdr_saved_bytes(*dims, nseq, bf16, 1)
+    if saved is None:
+        raise ValueError("saved must be what forward(..., want_saved=True) returned")
+    _check_tensor("saved", saved, (need,), torch.uint8, dev)
+    with _on(stream) as handle:
+        grads = {
+            "dq": torch.empty((B, T, Hk, K), dtype=q.dtype, device=dev),
+            "dk": torch.empty((B, T, Hk, K), dtype=q.dtype, device=dev),
+            "dv": torch.empty((B, T, Hv, V), dtype=q.dtype, device=dev),
+            "dg": torch.empty((B, T, Hv), dtype=torch.float32, device=dev),
+            "dbeta": torch.empty((B, T, Hv), dtype=torch.float32, device=dev),
+            "dS_init": torch.empty((n, Hv, V, K), dtype=torch.float32, device=dev) if want_dS_init else None,
+        }
+        work = torch.empty(lib.gdr_backward_bytes(*dims, nseq, bf16), dtype=torch.uint8, device=dev)
+        fn = lib.gdr_backward_bf16 if bf16 else lib.gdr_backward
+        wkv7._check(fn(*(_addr(x) for x in (q, k, v, g, beta, do, dS_final, seq_starts, saved, work)),
+                       *(_addr(grads[m]) for m in ("dq", "dk", "dv", "dg", "dbeta", "dS_init")), _strides(q, k, v),
+                       K ** -0.5 if scale is None else scale, qk_l2norm, *dims, nseq, handle))
+    return grads
+
+
+def step(q, k, v, g, beta, state, *, slots=None, scale: float | None = None, qk_l2norm: bool = False, stream=None):
+    """The recurrence for the next token (or few) of each request: q, k
+    [R][T][Hk][K], v [R][T][Hv][V], g, beta [R][T][Hv]. ``state`` [n][Hv][V][K]
+    float32 is updated in place; slots (int32 [R]) names each request's state,
+    each at most once, a negative one to skip the request (its o is 0); None:
+    request r has state r. Returns o."""
+    import torch
+
+    lib = load()
+    bf16, dims, dev = _inputs(q, k, v, g, beta)
+    R, T, Hk, Hv, K, V = dims
+    if state.dim() != 4:
+        raise ValueError("state must be [n][Hv][V][K]")
+    _check_tensor("state", state, (state.shape[0], Hv, V, K), torch.float32, dev)
+    if slots is not None:
+        _check_tensor("slots", slots, (R,), torch.int32, dev)
+    with _on(stream) as handle:
+        o = torch.empty((R, T, Hv, V), dtype=q.dtype, device=dev)
+        fn = lib.gdr_step_bf16 if bf16 else lib.gdr_step
+        wkv7._check(fn(*(_addr(x) for x in (q, k, v, g, beta, state, slots, o)), _strides(q, k, v),
+                       K ** -0.5 if scale is None else scale, qk_l2norm, *dims, state.shape[0], handle))
+    return o
