@@ -20,7 +20,9 @@
 // other) whose eight 16-byte pieces are permuted by the row (piece ^ (row &
 // 7)), or rows of 64 bytes permuted by (row >> 1) & 3, so that ldmatrix reads
 // eight rows from eight different bank groups and a whole tile moves by one
-// bulk copy. The hi part comes first, then the lo part.
+// bulk copy. A lower triangular 64 x 64 tile keeps only its ten lower 16 x 16
+// blocks (tri), each with rows of 32 bytes whose two pieces are swapped in
+// every other four rows. The hi part comes first, then the lo part.
 #pragma once
 
 #include <cuda_bf16.h>
@@ -122,6 +124,11 @@ __device__ __forceinline__ int img(int rows, int row, int col) {
     return row * 32 + ((((col >> 3) & 3) ^ ((row >> 1) & 3)) << 3) + (col & 7);
 }
 
+// Lower triangular images: the block (i, j), j <= i < 4, and a place in it.
+constexpr int kTriPart = 10 * 256;
+__device__ __forceinline__ int tri_block(int i, int j) { return (i * (i + 1) / 2 + j) * 256; }
+__device__ __forceinline__ int tri_at(int row, int col) { return row * 16 + (((col >> 3) ^ ((row >> 2) & 1)) << 3) + (col & 7); }
+
 __device__ __forceinline__ void ldsm4(uint32_t (&r)[4], const __half* p) {
   asm volatile("ldmatrix.sync.aligned.m8n8.x4.shared.b16 {%0,%1,%2,%3}, [%4];"
                : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3])
@@ -173,6 +180,26 @@ __device__ __forceinline__ void b_kn(Frag<kP>& f, const __half* s, int rows, int
   ldsm4t(f.h, p);
   if constexpr (kP == 2) ldsm4t(f.l, p + part);
 }
+// A fragments from a lower triangular pair image: its block (i, j), or that
+// block transposed (A[m][k] = X[16 i + k][16 j + m]).
+__device__ __forceinline__ void a_tri(Frag<2>& f, const __half* s, int i, int j, int lane) {
+  const __half* p = s + tri_block(i, j) + tri_at(lane & 15, (lane >> 4) * 8);
+  ldsm4(f.h, p);
+  ldsm4(f.l, p + kTriPart);
+}
+__device__ __forceinline__ void a_tri_t(Frag<2>& f, const __half* s, int i, int j, int lane) {
+  const __half* p = s + tri_block(i, j) + tri_at((lane & 7) + (lane >> 4) * 8, ((lane >> 3) & 1) * 8);
+  ldsm4t(f.h, p);
+  ldsm4t(f.l, p + kTriPart);
+}
+__device__ __forceinline__ void put2_tri(__half* s, int row, int col, float x0, float x1) {
+  uint32_t hi, lo;
+  split2<2>(x0, x1, hi, lo);
+  const int at = tri_block(row >> 4, col >> 4) + tri_at(row & 15, col & 15);
+  *reinterpret_cast<uint32_t*>(s + at) = hi;
+  *reinterpret_cast<uint32_t*>(s + at + kTriPart) = lo;
+}
+
 // Two n8 tiles += a b, the small terms first.
 __device__ __forceinline__ void mma_pair(float (&d0)[4], float (&d1)[4], const uint32_t (&a)[4], const uint32_t (&b)[4]) {
   mma16(d0, a, b[0], b[1]);
@@ -218,6 +245,31 @@ __device__ __forceinline__ void bulk_store(void* dst, const void* src, uint32_t 
 __device__ __forceinline__ void bulk_commit() { asm volatile("cp.async.bulk.commit_group;" ::: "memory"); }
 __device__ __forceinline__ void bulk_wait_read() { asm volatile("cp.async.bulk.wait_group.read 0;" ::: "memory"); }
 __device__ __forceinline__ void bulk_wait_all() { asm volatile("cp.async.bulk.wait_group 0;" ::: "memory"); }
+
+__device__ __forceinline__ void bulk_prefetch(const void* src, uint32_t bytes) {
+  asm volatile("cp.async.bulk.prefetch.L2.global [%0], %1;" ::"l"(src), "r"(bytes) : "memory");
+}
+__device__ __forceinline__ void prefetch_l2(const void* p) { asm volatile("prefetch.global.L2 [%0];" ::"l"(p)); }
+__device__ __forceinline__ void mbar_arrive(uint64_t* bar) {
+  asm volatile("mbarrier.arrive.shared::cta.b64 _, [%0];" ::"r"(smem_addr(bar)) : "memory");
+}
+// Barrier of 256 threads; id 1 and up.
+__device__ __forceinline__ void group_barrier(int id) { asm volatile("bar.sync %0, 256;" ::"r"(id) : "memory"); }
+
+template <int N>
+__device__ __forceinline__ float max_of(const float (&x)[N]) {
+  float m = x[0];
+#pragma unroll
+  for (int i = 1; i < N; ++i) m = abs_max(m, x[i]);
+  return m;
+}
+template <int N>
+__device__ __forceinline__ void zero(float (&x)[N][4]) {
+#pragma unroll
+  for (int n = 0; n < N; ++n)
+#pragma unroll
+    for (int e = 0; e < 4; ++e) x[n][e] = 0.f;
+}
 
 // --------------------------------------------------- sequences and chunks ---
 

@@ -23,19 +23,21 @@
 namespace gdr {
 namespace {
 
-constexpr int kThreads = 256;
+// Warps: four times 16 rows by a warp for every 32 keys.
+template <int KP>
+constexpr int kThreads = KP / 32 * 128;
 
 template <int P, int KP>
-struct Tile {
+struct alignas(128) Tile {
   __half s[2 * kVt * KP], ds[2 * kVt * KP];
   __half u[2 * kC * kVt], l[2 * kC * kVt];
   __half d[P * kC * kVt];
 };
-struct Pairs {  // F and E as operands: columns times beta ks, and rows times qs or ks
-  __half fb[2 * kC * kC], eb[2 * kC * kC], f[2 * kC * kC], e[2 * kC * kC];
+struct alignas(128) Pairs {  // F and E as operands: columns times beta ks, and rows times qs or ks
+  __half fb[2 * kTriPart], eb[2 * kTriPart], f[2 * kTriPart], e[2 * kTriPart];
 };
 template <typename T, int KP>
-struct GradSmem {
+struct alignas(128) GradSmem {
   static constexpr int P = In<T>::kParts;
   __half q[P * kC * KP], k[P * kC * KP];
   union {
@@ -45,9 +47,9 @@ struct GradSmem {
   Scal scal;
   Rows rows;
   float fd[kC];             // f_i
-  float dot[2][5][kC];      // the row sums of a half of the keys
-  float red[8][4];
-  float sdot[8];
+  float dot[5][KP / 32][kC];  // the row sums of 32 keys each
+  float red[KP / 8][4];
+  float sdot[KP / 8];
   float dG[kC];
   uint64_t bar[3];
 };
@@ -64,27 +66,20 @@ __device__ __forceinline__ float2 pick2(const __half* s, int row, int col) {
 }
 
 template <int N>
-__device__ __forceinline__ void zero(float (&x)[N][4]) {
+__device__ __forceinline__ float row_sum(const float (&x)[N][kC], int i) {
+  float s = x[0][i];
 #pragma unroll
-  for (int n = 0; n < N; ++n)
-#pragma unroll
-    for (int e = 0; e < 4; ++e) x[n][e] = 0.f;
-}
-template <int N>
-__device__ __forceinline__ void add(float (&x)[N][4], const float (&y)[N][4], float f) {
-#pragma unroll
-  for (int n = 0; n < N; ++n)
-#pragma unroll
-    for (int e = 0; e < 4; ++e) x[n][e] = fmaf(f, y[n][e], x[n][e]);
+  for (int n = 1; n < N; ++n) s += x[n][i];
+  return s;
 }
 
 template <typename T, int KP, bool kShared>
-__global__ void __launch_bounds__(kThreads) grad_kernel(const Args a) {
+__global__ void __launch_bounds__(kThreads<KP>, KP == 64 ? 2 : 1) grad_kernel(const Args a) {
   extern __shared__ __align__(128) unsigned char raw[];
   using Smem = GradSmem<T, KP>;
-  constexpr int P = In<T>::kParts, kNt = KP / 16;  // n8 tiles of a warp's half of the keys
+  constexpr int P = In<T>::kParts, kWc = KP / 32, kNt = 4, kNf = 4 / kWc;  // n8 tiles of keys, 16-blocks of F's columns
   Smem& sm = *reinterpret_cast<Smem*>(raw);
-  const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5, wr = warp & 3, wc = warp >> 2;
+  const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5, wc = warp >> 2, wr = wc & 1 ? 3 - (warp & 3) : warp & 3;
   const int g4 = lane >> 2, t4 = lane & 3;
   const int slot = blockIdx.x / a.s.Hv, hv = blockIdx.x % a.s.Hv, hk = hv / (a.s.Hv / a.s.Hk);
   ChunkAt c;
@@ -118,8 +113,8 @@ __global__ void __launch_bounds__(kThreads) grad_kernel(const Args a) {
   }
   __syncthreads();
 
-  const int key0 = wc * (KP / 2);
-  float dq[kNt][4], rd[kNt][4], w[kNt][4], F[4][4], E[4][4];
+  const int key0 = wc * 32;
+  float dq[kNt][4], rd[kNt][4], w[kNt][4], F[2 * kNf][4], E[2 * kNf][4];
   zero(dq), zero(rd), zero(w), zero(F), zero(E);
   float sdot = 0.f;
   for (int v = 0; v < vts; ++v) {
@@ -156,8 +151,8 @@ __global__ void __launch_bounds__(kThreads) grad_kernel(const Args a) {
         }
     }
 #pragma unroll
-    for (int b = 0; b < 2; ++b) {
-      const int jb = 2 * wc + b;
+    for (int b = 0; b < kNf; ++b) {
+      const int jb = kNf * wc + b;
       if (jb <= wr) {
         float x[4][4];
         zero(x);
@@ -200,8 +195,8 @@ __global__ void __launch_bounds__(kThreads) grad_kernel(const Args a) {
     // <S0, dS1>: the same place of both images
     float sd = 0.f;
 #pragma unroll
-    for (int i = 0; i < kVt * KP / 8 / kThreads; ++i) {
-      const int at8 = (i * kThreads + tid) * 8;
+    for (int i = 0; i < kVt * KP / 8 / kThreads<KP>; ++i) {
+      const int at8 = (i * kThreads<KP> + tid) * 8;
       const uint4 x0 = *reinterpret_cast<const uint4*>(t.s + at8), x1 = *reinterpret_cast<const uint4*>(t.s + kVt * KP + at8);
       const uint4 y0 = *reinterpret_cast<const uint4*>(t.ds + at8), y1 = *reinterpret_cast<const uint4*>(t.ds + kVt * KP + at8);
       const uint32_t xs[8] = {x0.x, x0.y, x0.z, x0.w, x1.x, x1.y, x1.z, x1.w};
@@ -225,10 +220,10 @@ __global__ void __launch_bounds__(kThreads) grad_kernel(const Args a) {
   float mx[4] = {0.f, 0.f, 0.f, 0.f};
   const int i0 = 16 * wr + g4;
 #pragma unroll
-  for (int n = 0; n < 4; ++n)
+  for (int n = 0; n < 2 * kNf; ++n)
 #pragma unroll
     for (int e = 0; e < 4; ++e) {
-      const int i = i0 + 8 * (e >> 1), j = 32 * wc + 8 * n + 2 * t4 + (e & 1);
+      const int i = i0 + 8 * (e >> 1), j = 16 * kNf * wc + 8 * n + 2 * t4 + (e & 1);
       if (j == i) sm.fd[i] = a.s.scale * F[n][e];
       const float r = j < i ? expf((sc.gh[i] - sc.gh[j]) + (sc.gl[i] - sc.gl[j])) : 0.f;
       F[n][e] = j < i ? a.s.scale * r * F[n][e] : 0.f;
@@ -250,20 +245,21 @@ __global__ void __launch_bounds__(kThreads) grad_kernel(const Args a) {
   for (int m = 0; m < 4; ++m) {
     float x = sm.red[0][m];
 #pragma unroll
-    for (int i = 1; i < 8; ++i) x = abs_max(x, sm.red[i][m]);
+    for (int i = 1; i < KP / 8; ++i) x = abs_max(x, sm.red[i][m]);
     scale[m] = pow2_scale(x);
   }
 #pragma unroll
-  for (int n = 0; n < 4; ++n)
+  for (int n = 0; n < 2 * kNf; ++n)
 #pragma unroll
     for (int h = 0; h < 2; ++h) {
-      const int i = i0 + 8 * h, j = 32 * wc + 8 * n + 2 * t4;
+      if (kNf * wc + n / 2 > wr) continue;  // above the diagonal blocks
+      const int i = i0 + 8 * h, j = 16 * kNf * wc + 8 * n + 2 * t4;
       const float c0 = sc.beta[j] * rows.ks[j], c1 = sc.beta[j + 1] * rows.ks[j + 1], x0 = F[n][2 * h], x1 = F[n][2 * h + 1],
                   y0 = E[n][2 * h], y1 = E[n][2 * h + 1], rq = rows.qs[i], rk = rows.ks[i];
-      put2<true>(sm.pairs.fb, kC, kC * kC, i, j, (x0 * c0) * scale[0], (x1 * c1) * scale[0]);
-      put2<true>(sm.pairs.eb, kC, kC * kC, i, j, (y0 * c0) * scale[1], (y1 * c1) * scale[1]);
-      put2<true>(sm.pairs.f, kC, kC * kC, i, j, (x0 * rq) * scale[2], (x1 * rq) * scale[2]);
-      put2<true>(sm.pairs.e, kC, kC * kC, i, j, (y0 * rk) * scale[3], (y1 * rk) * scale[3]);
+      put2_tri(sm.pairs.fb, i, j, (x0 * c0) * scale[0], (x1 * c1) * scale[0]);
+      put2_tri(sm.pairs.eb, i, j, (y0 * c0) * scale[1], (y1 * c1) * scale[1]);
+      put2_tri(sm.pairs.f, i, j, (x0 * rq) * scale[2], (x1 * rq) * scale[2]);
+      put2_tri(sm.pairs.e, i, j, (y0 * rk) * scale[3], (y1 * rk) * scale[3]);
     }
   __syncthreads();
 
@@ -286,8 +282,8 @@ __global__ void __launch_bounds__(kThreads) grad_kernel(const Args a) {
       b_kn<P, true>(fk, sm.k, kC, kC * KP, key0 + 8 * nt, 16 * kt, lane);
       if (kt <= wr) {
         Frag<2> f, e;
-        a_mk<2, true>(f, sm.pairs.fb, kC, kC * kC, 16 * wr, 16 * kt, lane);
-        a_mk<2, true>(e, sm.pairs.eb, kC, kC * kC, 16 * wr, 16 * kt, lane);
+        a_tri(f, sm.pairs.fb, wr, kt, lane);
+        a_tri(e, sm.pairs.eb, wr, kt, lane);
         mma_parts<2, P>(x[0], x[1], f, fk);
         mma_parts<2, P>(y[0], y[1], e, fk);
       }
@@ -295,8 +291,8 @@ __global__ void __launch_bounds__(kThreads) grad_kernel(const Args a) {
         Frag<2> f, e;
         Frag<P> fq;
         b_kn<P, true>(fq, sm.q, kC, kC * KP, key0 + 8 * nt, 16 * kt, lane);
-        a_km<2, true>(f, sm.pairs.f, kC, kC * kC, 16 * wr, 16 * kt, lane);
-        a_km<2, true>(e, sm.pairs.e, kC, kC * kC, 16 * wr, 16 * kt, lane);
+        a_tri_t(f, sm.pairs.f, kt, wr, lane);
+        a_tri_t(e, sm.pairs.e, kt, wr, lane);
         mma_parts<2, P>(q[0], q[1], f, fq);
         mma_parts<2, P>(z[0], z[1], e, fk);
       }
@@ -330,25 +326,24 @@ __global__ void __launch_bounds__(kThreads) grad_kernel(const Args a) {
 #pragma unroll
     for (int h = 0; h < 2; ++h) {
       float x = wkv7::group_allreduce<4>(dot[m][h]);
-      if (t4 == 0) sm.dot[wc][m][i0 + 8 * h] = x;
+      if (t4 == 0) sm.dot[m][wc][i0 + 8 * h] = x;
     }
   __syncthreads();
   const size_t tok = (size_t)c.b * a.s.T + c.t0;
   if (tid < kC) {
     const int i = tid;
-    const float b = sc.beta[i], qd = sm.dot[0][0][i] + sm.dot[1][0][i], kr = sm.dot[0][1][i] + sm.dot[1][1][i],
-                kw = sm.dot[0][2][i] + sm.dot[1][2][i], qk = sm.dot[0][4][i] + sm.dot[1][4][i];
+    const float b = sc.beta[i], qd = row_sum(sm.dot[0], i), kr = row_sum(sm.dot[1], i), kw = row_sum(sm.dot[2], i),
+                qk = row_sum(sm.dot[4], i);
     sm.dG[i] = qd + kr - b * kw;
     if (i < c.len) a.dbeta[(tok + i) * a.s.Hv + hv] = fmaf(sm.fd[i], qk, kw);
   }
   __syncthreads();
   if (warp == 0) {  // dg: the suffix sums, two tokens a lane
-    float x = (sm.dot[0][3][2 * lane] + sm.dot[1][3][2 * lane]) * sc.beta[2 * lane] +
-              (sm.dot[0][3][2 * lane + 1] + sm.dot[1][3][2 * lane + 1]) * sc.beta[2 * lane + 1];
+    float x = row_sum(sm.dot[3], 2 * lane) * sc.beta[2 * lane] + row_sum(sm.dot[3], 2 * lane + 1) * sc.beta[2 * lane + 1];
     x = wkv7::group_allreduce<32>(x);
     float s0 = sm.sdot[0];
 #pragma unroll
-    for (int i = 1; i < 8; ++i) s0 += sm.sdot[i];
+    for (int i = 1; i < KP / 8; ++i) s0 += sm.sdot[i];
     const float d0 = sm.dG[2 * lane], d1 = sm.dG[2 * lane + 1] + (lane == 31 ? fmaf(sc.egc, s0, x) : 0.f);
     float s = d0 + d1;
 #pragma unroll
@@ -368,9 +363,9 @@ __global__ void __launch_bounds__(kThreads) grad_kernel(const Args a) {
     float nq = 0.f, nk = 0.f;  // q.dq and k.dk of the whole row
     const bool norm = !kShared && a.s.l2norm;
     if (norm) {
-      const float b = sc.beta[i], f = sm.fd[i], qk = sm.dot[0][4][i] + sm.dot[1][4][i];
-      nq = fmaf(f * b, qk, sm.dot[0][0][i] + sm.dot[1][0][i]);
-      nk = fmaf(b, fmaf(f, qk, sm.dot[0][2][i] + sm.dot[1][2][i]), sm.dot[0][1][i] + sm.dot[1][1][i]);
+      const float b = sc.beta[i], f = sm.fd[i], qk = row_sum(sm.dot[4], i);
+      nq = fmaf(f * b, qk, row_sum(sm.dot[0], i));
+      nk = fmaf(b, fmaf(f, qk, row_sum(sm.dot[2], i)), row_sum(sm.dot[1], i));
     }
 #pragma unroll
     for (int nt = 0; nt < kNt; ++nt) {
@@ -441,7 +436,7 @@ cudaError_t launch(const Args& a, cudaStream_t stream) {
   auto kernel = grad_kernel<T, KP, kShared>;
   cudaError_t e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem);
   if (e != cudaSuccess) return e;
-  kernel<<<(unsigned)((size_t)a.s.slots * a.s.Hv), kThreads, smem, stream>>>(a);
+  kernel<<<(unsigned)((size_t)a.s.slots * a.s.Hv), kThreads<KP>, smem, stream>>>(a);
   if ((e = cudaGetLastError()) != cudaSuccess) return e;
   if (kShared) {
     const size_t rows = 2 * (size_t)a.s.B * a.s.T * a.s.Hk;

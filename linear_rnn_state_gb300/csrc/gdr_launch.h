@@ -34,6 +34,10 @@ inline long long slot_count(int B, int T, int nseq, bool packed) {
 inline int padded_k(int K) { return K <= 64 ? 64 : 128; }
 inline int v_tiles(int V) { return (V + kVt - 1) / kVt; }
 
+// Whether a chain's block takes two tiles of value columns (they share the
+// chunk's images in shared memory) or one (its own SM while there are enough).
+inline bool two_tiles(const Shape& s) { return v_tiles(s.V) > 1 && (long long)s.nseq * s.Hv * v_tiles(s.V) > 152; }
+
 // Scalars of a chunk: per key head (Rows) and per value head (Scal).
 struct Rows {        // of the 64 tokens, the actual q is qs * image (and k is ks * image)
   float qs[kC], ks[kC];
@@ -62,7 +66,7 @@ struct Layout {
   int Kp, vt, parts;
   size_t n_k, n_v, n_t;           // (slot, key head), (slot, value head), (slot, value head, tile) counts
   size_t kq_img, st_img, u_img, do_img;  // bytes of one image
-  static constexpr size_t tp_img = 2 * kC * kC * 2;
+  static constexpr size_t tp_img = 2 * 10 * 16 * 16 * 2;  // T or P: the lower ten blocks of 16 x 16
 };
 inline Layout layout(const Shape& s, bool bf16) {
   Layout l;

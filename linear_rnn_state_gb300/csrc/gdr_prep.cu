@@ -15,27 +15,30 @@
 // -200 counts as -200 (e^-200 is 0 in fp32 either way), which makes -inf a
 // reset of the state instead of inf - inf.
 //
-// T by forward substitution in fp32, one column a thread.
+// T in fp32: the four diagonal 16 x 16 blocks by forward substitution, a column
+// a thread, then blocks joined two by two, [T1 0; -T2 L21 T1 T2], 16 and then
+// 32 wide.
 #include "gdr_common.cuh"
 
 namespace gdr {
 namespace {
 
 constexpr int kThreads = 128;
+constexpr int kLx = 36;
 constexpr int kLd = 68;  // row stride of the fp32 64 x 64 tiles: rows stay 16-byte aligned
 
 template <typename T, int KP>
-struct PrepSmem {
+struct alignas(128) PrepSmem {
   static constexpr int P = In<T>::kParts;
   __half q[P * kC * KP], k[P * kC * KP];
+  float L[kC * kLd];  // L, and then T in its place
   union {
-    float L[kC * kLd];
-    float wide[kC * kLd];
+    __half out[2 * kTriPart];  // the image of P, then of T
+    float x[32 * kLx];         // L21 T1 in between
   };
-  __half out[2 * kC * kC];
   Rows rows;
   Scal scal;
-  float q_max[kC], k_max[kC], k_sum[kC];
+  float q_max[kC], q_sum[kC], k_max[kC], k_sum[kC];
   float red[8];
 };
 
@@ -87,8 +90,41 @@ __device__ __forceinline__ float block_max(float x, float* red, int tid) {
   return m;
 }
 
+// X[i][j] = sign sum_m A[i][m] B[m][j] for the thread's R rows from r and C
+// columns from c, m < N; rows of A and B 16-byte aligned.
+template <int R, int C, int N>
+__device__ __forceinline__ void small_product(float (&x)[R][C], const float* A, int lda, const float* B, int ldb, int r, int c) {
+#pragma unroll
+  for (int i = 0; i < R; ++i)
+#pragma unroll
+    for (int j = 0; j < C; ++j) x[i][j] = 0.f;
+#pragma unroll 4
+  for (int m = 0; m < N; m += 4) {
+    float4 a[R];
+#pragma unroll
+    for (int i = 0; i < R; ++i) a[i] = *reinterpret_cast<const float4*>(A + (r + i) * lda + m);
+#pragma unroll
+    for (int q = 0; q < 4; ++q) {
+      float b[C];
+      if constexpr (C == 4) {
+        const float4 v = *reinterpret_cast<const float4*>(B + (m + q) * ldb + c);
+        b[0] = v.x, b[1] = v.y, b[2] = v.z, b[3] = v.w;
+      } else {
+        const float2 v = *reinterpret_cast<const float2*>(B + (m + q) * ldb + c);
+        b[0] = v.x, b[1] = v.y;
+      }
+#pragma unroll
+      for (int i = 0; i < R; ++i) {
+        const float s = q == 0 ? a[i].x : q == 1 ? a[i].y : q == 2 ? a[i].z : a[i].w;
+#pragma unroll
+        for (int j = 0; j < C; ++j) x[i][j] = fmaf(s, b[j], x[i][j]);
+      }
+    }
+  }
+}
+
 template <typename T, int KP>
-__global__ void __launch_bounds__(kThreads) prep_kernel(const Args a) {
+__global__ void __launch_bounds__(kThreads, 4) prep_kernel(const Args a) {
   extern __shared__ __align__(128) unsigned char raw[];
   PrepSmem<T, KP>& sm = *reinterpret_cast<PrepSmem<T, KP>*>(raw);
   constexpr int P = In<T>::kParts;
@@ -97,7 +133,7 @@ __global__ void __launch_bounds__(kThreads) prep_kernel(const Args a) {
   ChunkAt c;
   if (!chunk_at(a.s, slot, c)) return;
   const size_t at_k = (size_t)slot * a.s.Hk + hk;
-  load_rows<T, KP>(sm.q, sm.rows.qs, sm.rows.rq, sm.q_max, sm.wide,
+  load_rows<T, KP>(sm.q, sm.rows.qs, sm.rows.rq, sm.q_max, sm.q_sum,
                    static_cast<const T*>(a.q) + c.b * a.s.q_b + c.t0 * a.s.q_t + hk * a.s.K, a.s.q_t, c.len, a.s.K,
                    a.s.l2norm, tid);
   load_rows<T, KP>(sm.k, sm.rows.ks, sm.rows.rk, sm.k_max, sm.k_sum,
@@ -196,41 +232,81 @@ __global__ void __launch_bounds__(kThreads) prep_kernel(const Args a) {
     const float ps = pow2_scale(pm);
 #pragma unroll
     for (int n = 0; n < 8; ++n)
+      if (n < 2 * warp + 2)
 #pragma unroll
-      for (int h = 0; h < 2; ++h)
-        put2<true>(sm.out, kC, kC * kC, 16 * warp + g4 + 8 * h, 8 * n + 2 * t4, p[n][2 * h] * ps, p[n][2 * h + 1] * ps);
+        for (int h = 0; h < 2; ++h)
+          put2_tri(sm.out, 16 * warp + g4 + 8 * h, 8 * n + 2 * t4, p[n][2 * h] * ps, p[n][2 * h + 1] * ps);
     __syncthreads();
     copy16(a.b.p_img + at_v * Layout::tp_img, sm.out, Layout::tp_img, tid);
 
-    // column j of T: T[i][j] = [i == j] - sum_{m < i} L[i][m] T[m][j]
-    float col[kC], tm = 0.f;
+    // T in the place of L: diagonal blocks, then the blocks left of them
     if (tid < kC) {
+      float* D = sm.L + (tid & 48) * (kLd + 1);
+      const int j = tid & 15;
+      float col[16];
 #pragma unroll
-      for (int i = 0; i < kC; ++i) {
-        float x0 = i == tid ? 1.f : 0.f, x1 = 0.f, x2 = 0.f, x3 = 0.f;
+      for (int i = 0; i < 16; ++i) {
+        float x0 = i == j ? 1.f : 0.f, x1 = 0.f;
 #pragma unroll
         for (int m = 0; m < i; m += 4) {
-          const float4 l = *reinterpret_cast<const float4*>(sm.L + i * kLd + m);
+          const float4 l = *reinterpret_cast<const float4*>(D + i * kLd + m);
           x0 = fmaf(-l.x, col[m], x0);
           if (m + 1 < i) x1 = fmaf(-l.y, col[m + 1], x1);
-          if (m + 2 < i) x2 = fmaf(-l.z, col[m + 2], x2);
-          if (m + 3 < i) x3 = fmaf(-l.w, col[m + 3], x3);
+          if (m + 2 < i) x0 = fmaf(-l.z, col[m + 2], x0);
+          if (m + 3 < i) x1 = fmaf(-l.w, col[m + 3], x1);
         }
-        col[i] = i < tid ? 0.f : (x0 + x1) + (x2 + x3);
-        tm = abs_max(tm, col[i]);
+        col[i] = i < j ? 0.f : x0 + x1;
       }
-    }
-    tm = block_max(tm, sm.red, tid);  // its barriers also stand between the copy of P and the writes of T
-    const float ts = pow2_scale(tm);
-    if (tid < kC) {
+      __syncwarp();
 #pragma unroll
-      for (int i = 0; i < kC; ++i) {
-        const float x = col[i] * ts;
-        const __half h = __float2half_rn(x);
-        const int at = img<true>(kC, i, tid);
-        sm.out[at] = h;
-        sm.out[at + kC * kC] = __float2half_rn(x - __half2float(h));
-      }
+      for (int i = 0; i < 16; ++i) D[i * kLd + j] = col[i];
+    }
+    __syncthreads();
+    {
+      const int pair = tid >> 6, r = ((tid >> 3) & 7) * 2, cc = (tid & 7) * 2;
+      float* T1 = sm.L + 32 * pair * (kLd + 1);
+      float *L21 = T1 + 16 * kLd, *X = sm.x + 16 * pair * kLx;
+      float x[2][2];
+      small_product<2, 2, 16>(x, L21, kLd, T1, kLd, r, cc);
+#pragma unroll
+      for (int i = 0; i < 2; ++i) *reinterpret_cast<float2*>(X + (r + i) * kLx + cc) = make_float2(x[i][0], x[i][1]);
+      __syncthreads();
+      small_product<2, 2, 16>(x, L21 + 16, kLd, X, kLx, r, cc);
+#pragma unroll
+      for (int i = 0; i < 2; ++i) *reinterpret_cast<float2*>(L21 + (r + i) * kLd + cc) = make_float2(-x[i][0], -x[i][1]);
+    }
+    __syncthreads();
+    {
+      const int r = (tid >> 3) * 2, cc = (tid & 7) * 4;
+      float *L21 = sm.L + 32 * kLd, x[2][4];
+      // the 16 x 16 block above the diagonal of T1 and of T2 still holds what L's buffer held
+      *reinterpret_cast<float4*>(sm.L + 32 * (tid >> 6) * (kLd + 1) + ((tid >> 2) & 15) * kLd + 16 + (tid & 3) * 4) =
+          make_float4(0.f, 0.f, 0.f, 0.f);
+      __syncthreads();
+      small_product<2, 4, 32>(x, L21, kLd, sm.L, kLd, r, cc);
+#pragma unroll
+      for (int i = 0; i < 2; ++i) *reinterpret_cast<float4*>(sm.x + (r + i) * kLx + cc) = make_float4(x[i][0], x[i][1], x[i][2], x[i][3]);
+      __syncthreads();
+      small_product<2, 4, 32>(x, L21 + 32, kLd, sm.x, kLx, r, cc);
+#pragma unroll
+      for (int i = 0; i < 2; ++i) *reinterpret_cast<float4*>(L21 + (r + i) * kLd + cc) = make_float4(-x[i][0], -x[i][1], -x[i][2], -x[i][3]);
+    }
+    __syncthreads();
+    // two neighbours of a row at a time: ten blocks of 128 pairs
+    float2 tv[10];
+    float tm = 0.f;
+#pragma unroll
+    for (int b = 0; b < 10; ++b) {
+      const int ib = b < 1 ? 0 : b < 3 ? 1 : b < 6 ? 2 : 3, jb = b - ib * (ib + 1) / 2;
+      tv[b] = *reinterpret_cast<const float2*>(sm.L + (16 * ib + (tid >> 3)) * kLd + 16 * jb + 2 * (tid & 7));
+      tm = abs_max(abs_max(tm, tv[b].x), tv[b].y);
+    }
+    tm = block_max(tm, sm.red, tid);
+    const float ts = pow2_scale(tm);
+#pragma unroll
+    for (int b = 0; b < 10; ++b) {
+      const int ib = b < 1 ? 0 : b < 3 ? 1 : b < 6 ? 2 : 3, jb = b - ib * (ib + 1) / 2;
+      put2_tri(sm.out, 16 * ib + (tid >> 3), 16 * jb + 2 * (tid & 7), tv[b].x * ts, tv[b].y * ts);
     }
     if (tid == 0) {
       sm.scal.inv_p = pow2_inverse(ps), sm.scal.inv_t = pow2_inverse(ts);
