@@ -1,309 +1,226 @@
 // The gated delta rule's backward chain: the carried gradient dS of the state,
 // from the last chunk to the first, and dv.
 //
-// Eight warps per sequence, value head and tile of 32 value columns, as in the
-// forward chain (gdr_fwd.cu), whose images of q, k, T and P it reads again:
-//   y   = P^T do + wr k dS1^T          (the gradient of u)
-//   lam = T^T y = dv
-//   dS0 = e^Gc dS1 + sum_i scale e^Gi do_i q_i^T - sum_i e^Gi lam_i k_i^T
+// For the 16 rows of the state that a warp owns (gdr_chain.cuh), with the
+// images of q, k, T and P that the forward used, all transposed:
+//   y^T   = do^T P + wk (dS1 k^T)              (the gradient of u)
+//   lam^T = y^T T = dv^T
+//   dS0   = e^Gc dS1 + (scale e^G do)^T q - (e^G lam)^T k
 // It leaves the images of dS1, lam and do for the gradients of q, k, g and beta
-// (gdr_grad.cu). Scales come from bounds, as in the forward:
-// |y| <= p_sum max|do| + k_back max|dS1|, |lam| <= t_sum max|y|,
-// |dS0| <= e^Gc max|dS1| + q_sum max|do| + k_sum max|lam|.
-// The next chunk's do is fetched a step ahead and its image written before the
-// step's last barrier; that of scale e^G do, needed late, at the step's start.
+// (gdr_grad.cu). fp16 pairs throughout: dS, lam and do enter fp32 results.
+//
+// Bound, as the forward, by the tensor pipe: 292 mma of 8 cycles a step, warp
+// and scheduler at 64 keys (bfloat16).
 #include "gdr_chain.cuh"
 
 namespace gdr {
 namespace {
 
-template <int P, int KP>
-struct alignas(128) BwdTile {
-  __half s[2 * kVt * KP];
-  __half y[2 * kC * kVt], lw[2 * kC * kVt], dw[2 * kC * kVt];
-  __half d[P * kC * kVt];
-  float m_s[8], m_y[8], m_l[8], m_d[8];
+template <typename T, int KP>
+struct alignas(128) BwdWarp {
+  unsigned char rows[2][kRowsBytes<T>];  // do of this and the next chunk; then dv
+  __half s[2 * kVt * KP], l[2 * kVt * kC], d[In<T>::kParts * kVt * kC];  // images on their way out
 };
-template <typename T, int KP, int kTiles>
+template <typename T, int KP>
 struct BwdSmem {
-  Images<In<T>::kParts, KP> im;
-  BwdTile<In<T>::kParts, KP> tile[kTiles];
+  Images<In<T>::kParts, KP, 2> im;
+  BwdWarp<T, KP> w[kMaxWarps];
 };
 
-template <typename T, int KP, int kTiles>
-__global__ void __launch_bounds__(kTiles * kGroupThreads, kTiles == 1 && sizeof(BwdSmem<T, KP, 1>) <= 113 * 1024 ? 2 : 1)
-    bwd_kernel(const Args a) {
+template <typename T, int KP>
+__global__ void __launch_bounds__((kMaxWarps + 1) * 32, sizeof(BwdSmem<T, KP>) <= 113 * 1024 ? 2 : 1) bwd_kernel(const Args a) {
   extern __shared__ __align__(128) unsigned char raw[];
-  using Smem = BwdSmem<T, KP, kTiles>;
-  constexpr int P = In<T>::kParts, kNt = KP / 32;
+  using Smem = BwdSmem<T, KP>;
+  constexpr int P = In<T>::kParts, kNt = KP / 8;
   Smem& sm = *reinterpret_cast<Smem*>(raw);
-  const int vts = (a.s.V + kVt - 1) / kVt, sets = (vts + kTiles - 1) / kTiles;
+  const int warps = blockDim.x / 32 - 1, warp = threadIdx.x >> 5, lane = threadIdx.x & 31, t4 = lane & 3;
+  const int vts = (a.s.V + kVt - 1) / kVt, sets = (vts + warps - 1) / warps;
   const int set = blockIdx.x % sets, hv = blockIdx.x / sets % a.s.Hv, seq = blockIdx.x / (sets * a.s.Hv);
   const int hk = hv / (a.s.Hv / a.s.Hk);
   const SeqRange sq = seq_range(a.s, seq);
   const int n = (sq.t1 - sq.t0 + kC - 1) / kC;
   const int K = a.s.K, V = a.s.V;
-  const int group = threadIdx.x / kGroupThreads, tid = threadIdx.x % kGroupThreads, lane = tid & 31, warp = tid >> 5;
-  // step s works on chunk n - 1 - s
-  const Filler<P, KP> fill{sm.im, a, sq.slot + n - 1, -1, n, hk, hv, min(kTiles, vts - set * kTiles)};
-  if (threadIdx.x == 0) fill.start();
+  auto& im = sm.im;
+  if (threadIdx.x == 0) init_images(im, min(warps, vts - set * warps));
   __syncthreads();
-  const int vt = set * kTiles + group;
-  if (vt >= vts) return;
-  Images<P, KP>& im = sm.im;
-  BwdTile<P, KP>& tl = sm.tile[group];
-  const int wc = warp >> 2, wr = wc ? 3 - (warp & 3) : warp & 3, g4 = lane >> 2, t4 = lane & 3;
-  const int bar = group + 1;
-
-  const int key0 = wr * (KP / 4), i0 = 16 * wr + g4;
-  const size_t state_at = ((size_t)seq * a.s.Hv + hv) * V;
-  float S[kNt][4];
-#pragma unroll
-  for (int nt = 0; nt < kNt; ++nt)
-#pragma unroll
-    for (int h = 0; h < 2; ++h) {
-      const int row = vt * kVt + 16 * wc + g4 + 8 * h, key = key0 + 8 * nt + 2 * t4;
-      float2 x = make_float2(0.f, 0.f);
-      if (a.dS_final && row < V && key < K) x = *reinterpret_cast<const float2*>(a.dS_final + (state_at + row) * K + key);
-      S[nt][2 * h] = x.x, S[nt][2 * h + 1] = x.y;
-    }
-
-  // do of a chunk: rows 16 wr + g4 (+ 8), columns 16 wc + 8 nt + 2 t4 (+ 1)
-  const long long row_t = (long long)a.s.Hv * V;
-  const T* do_at = static_cast<const T*>(a.d_o) + (size_t)sq.b * a.s.T * row_t + (size_t)hv * V + vt * kVt;
-  T* dv_at = static_cast<T*>(a.dv) + (size_t)sq.b * a.s.T * row_t + (size_t)hv * V + vt * kVt;
-  float2 d[2][2];
-  auto load_do = [&](int c) {
-#pragma unroll
-    for (int h = 0; h < 2; ++h)
-#pragma unroll
-      for (int nt = 0; nt < 2; ++nt) {
-        const int t = sq.t0 + c * kC + i0 + 8 * h, col = 16 * wc + 8 * nt + 2 * t4;
-        d[h][nt] = make_float2(0.f, 0.f);
-        if (t < sq.t1 && vt * kVt + col < V) d[h][nt] = load2(do_at + t * row_t + col);
-      }
-  };
-  auto ask_do = [&](int c) {
-    if (c >= 0) ask_rows(do_at, row_t, sq.t0 + c * kC, sq.t1, tid);
-  };
-  auto max_do = [&] {
-    float m = 0.f;
-#pragma unroll
-    for (int h = 0; h < 2; ++h)
-#pragma unroll
-      for (int nt = 0; nt < 2; ++nt) m = abs_max(abs_max(m, d[h][nt].x), d[h][nt].y);
-    m = warp_max_abs(m);
-    if (lane == 0) tl.m_d[warp] = m;
-  };
-  float mD = 0.f, sD = 1.f;  // of the do whose image is in place
-  auto put_do = [&] {
-    mD = max_of(tl.m_d);
-    sD = pow2_scale(mD);
-#pragma unroll
-    for (int h = 0; h < 2; ++h)
-#pragma unroll
-      for (int nt = 0; nt < 2; ++nt)
-        put2_p<P, false>(tl.d, kC, kC * kVt, i0 + 8 * h, 16 * wc + 8 * nt + 2 * t4, d[h][nt].x * sD, d[h][nt].y * sD);
-  };
-  float s_max = 0.f;
-#pragma unroll
-  for (int nt = 0; nt < kNt; ++nt) s_max = abs_max(s_max, max_of(S[nt]));
-  s_max = warp_max_abs(s_max);
-  if (lane == 0) tl.m_s[warp] = s_max;
-  if (n > 0) {
-    load_do(n - 1);
-    ask_do(n - 2);
-    ask_do(n - 3);
-    max_do();
+  if (warp == warps) {
+    if (lane == 0) fill_images(im, a, sq.slot + n - 1, -1, n, hk, hv);
+    return;
   }
-  group_barrier(bar);
-  float sS = pow2_scale(max_of(tl.m_s));
-  auto put_state = [&](float scale) {
-#pragma unroll
-    for (int nt = 0; nt < kNt; ++nt)
-#pragma unroll
-      for (int h = 0; h < 2; ++h)
-        put2<true>(tl.s, kVt, kVt * KP, 16 * wc + g4 + 8 * h, key0 + 8 * nt + 2 * t4, S[nt][2 * h] * scale,
-                   S[nt][2 * h + 1] * scale);
+  const int vt = set * warps + warp;
+  if (vt >= vts) return;
+  BwdWarp<T, KP>& mine = sm.w[warp];
+  const int cols = V - vt * kVt;
+  const size_t state_at = (((size_t)seq * a.s.Hv + hv) * V + vt * kVt) * K;
+  const size_t first = (((size_t)sq.b * a.s.T + sq.t0) * a.s.Hv + hv) * V + vt * kVt;
+  const T* do_at = static_cast<const T*>(a.d_o) + first;
+  T* dv_at = static_cast<T*>(a.dv) + first;
+  const long long row_t = (long long)a.s.Hv * V;
+  const int tokens = sq.t1 - sq.t0;
+  // chunk c's rows: where they start and how many there are
+  auto ask = [&](int c) {
+    if (c >= 0) rows_ask(do_at + c * kC * row_t, row_t, tokens - c * kC, lane);
   };
-  put_state(sS);
-  if (n > 0) put_do();
-  wkv7::fence_proxy_async_smem();
-  group_barrier(bar);
+
+  float S[kNt][4];
+  load_state(S, a.dS_final ? a.dS_final + state_at : nullptr, cols, K, lane);
+  float s_max = warp_max(S);
+  if (n > 0) rows_in(mine.rows[0], do_at + (n - 1) * kC * row_t, row_t, tokens - (n - 1) * kC, cols, lane);
+  copy_commit();
+  ask(n - 2), ask(n - 3);
 
   for (int s = 0; s < n; ++s) {
-    const int c = n - 1 - s;
-    const size_t slot = sq.slot + c, at_t = (slot * a.s.Hv + hv) * vts + vt;
-    const uint32_t use = s & 1;
-    if (!mbar_wait_bounded(a.status, &im.full_k[use], (s >> 1) & 1)) return;
-    const Scal& sc = im.scal[use];
-    const Rows& rows = im.rows[use];
-    const __half* kimg = im.k[use];
-    const float mS = max_of(tl.m_s), mDo = mD, inv_s = pow2_inverse(sS), inv_d = pow2_inverse(sD);
-    if (tid == 0) {
-      bulk_store(a.b.ds_img + at_t * sizeof(tl.s), tl.s, sizeof(tl.s));
-      bulk_store(a.b.do_img + at_t * sizeof(tl.d), tl.d, sizeof(tl.d));
-      bulk_commit();
-    }
+    const int c = n - 1 - s, use = s & 1, len = tokens - c * kC;
+    const size_t at_t = ((sq.slot + c) * a.s.Hv + hv) * vts + vt;
+    if (c > 0) rows_in(mine.rows[use ^ 1], do_at + (c - 1) * kC * row_t, row_t, kC, cols, lane);
+    copy_commit();
+    ask(c - 3);
+    if (lane == 0) bulk_wait_read();  // the images of the step before are out
+    __syncwarp();
+    const Scal& sc = im.sc(use);
+    const float sS = pow2_scale(s_max), inv_s = pow2_inverse(sS);
 
-    // y = P^T do + wr k dS1^T
-    float x[2][4], y[2][4];
-    zero(x), zero(y);
+    // dS1 k^T
+    float y[8][4];
+    zero(y);
+    if (!mbar_wait_bounded(a.status, &im.full_k[use], (s >> 1) & 1)) return;
 #pragma unroll
     for (int kt = 0; kt < KP / 16; ++kt) {
-      Frag<P> fk;
       Frag<2> fs;
-      a_mk<P, true>(fk, kimg, kC, kC * KP, 16 * wr, 16 * kt, lane);
-      b_nk<2, true>(fs, tl.s, kVt, kVt * KP, 16 * wc, 16 * kt, lane);
-      mma_parts<P, 2>(x[0], x[1], fk, fs);
+      to_a(fs, S[2 * kt], S[2 * kt + 1], sS);
+      put_a(mine.s, kVt * KP, 16 * kt, fs, lane);
+      Frag<P> fk[4];
+#pragma unroll
+      for (int nb = 0; nb < 4; ++nb) b_nk<P>(fk[nb], im.k[use], kC, kC * KP, 16 * nb, 16 * kt, lane);
+      mma_row<4>(y, fs, fk);
     }
+    copy_wait<1>();
+    __syncwarp();
+    float d[8][4];
+    rows_get(d, mine.rows[use], lane, do_at);
+    const float sD = pow2_scale(warp_max(d)), inv_d = pow2_inverse(sD);
+
+    // y = P^T do + wk k dS1^T
+    float x[8][4];
+    zero(x);
     if (!mbar_wait_bounded(a.status, &im.full_p, use)) return;
 #pragma unroll
-    for (int kt = 0; kt < 4; ++kt)
-      if (kt >= wr) {
-        Frag<2> fp;
-        Frag<P> fd;
-        a_tri_t(fp, im.p, kt, wr, lane);
-        b_kn<P, false>(fd, tl.d, kC, kC * kVt, 16 * wc, 16 * kt, lane);
-        mma_parts<2, P>(y[0], y[1], fp, fd);
-      }
-    const float sY = pow2_scale(sc.p_sum * mDo + sc.k_back * mS), sDW = pow2_scale(mDo * sc.eq_max);
-    float y_max = 0.f;
+    for (int i = 0; i < 4; ++i) {
+      Frag<P> fd;
+      to_a(fd, d[2 * i], d[2 * i + 1], sD);
+      put_a(mine.d, kVt * kC, 16 * i, fd, lane);
+      Frag<2> fp[4];
 #pragma unroll
-    for (int h = 0; h < 2; ++h) {
-      const float f = sc.wr[i0 + 8 * h] * rows.ks[i0 + 8 * h] * inv_s, fp = sc.inv_p * inv_d;
-      const float df = a.s.scale * sc.eg[i0 + 8 * h] * rows.qs[i0 + 8 * h];
+      for (int j = 0; j <= i; ++j) b_tri_kn<2>(fp[j], im.p, i, j, lane);
+      mma_row<4>(x, fd, fp, 0, i + 1);
+    }
+    give_up(&im.free_p, lane);
+    const float fp = sc.inv_p * inv_d;
 #pragma unroll
-      for (int nt = 0; nt < 2; ++nt) {
-        const int col = 16 * wc + 8 * nt + 2 * t4;
-        const float y0 = fmaf(f, x[nt][2 * h], fp * y[nt][2 * h]), y1 = fmaf(f, x[nt][2 * h + 1], fp * y[nt][2 * h + 1]);
-        y_max = abs_max(abs_max(y_max, y0), y1);
-        put2<false>(tl.y, kC, kC * kVt, i0 + 8 * h, col, y0 * sY, y1 * sY);
-        put2<false>(tl.dw, kC, kC * kVt, i0 + 8 * h, col, (d[h][nt].x * df) * sDW, (d[h][nt].y * df) * sDW);
+    for (int nt = 0; nt < 8; ++nt) {
+      const float2 f = *reinterpret_cast<const float2*>(sc.wk + 8 * nt + 2 * t4);
+#pragma unroll
+      for (int h = 0; h < 4; h += 2) {
+        y[nt][h] = fmaf(f.x * inv_s, y[nt][h], fp * x[nt][h]);
+        y[nt][h + 1] = fmaf(f.y * inv_s, y[nt][h + 1], fp * x[nt][h + 1]);
       }
     }
-    y_max = warp_max_abs(y_max);
-    if (lane == 0) tl.m_y[warp] = y_max;
-    group_barrier(bar);
-    if (tid == 0 && s + 1 < n && fill.last(im.done_p)) fill.p(s + 1);
-    if (s + 1 < n) load_do(c - 1);
-    ask_do(c - 3);
+    const float sY = pow2_scale(warp_max(y));
 
     // lam = T^T y
-    float l[2][4];
-    zero(l);
+    zero(x);
     if (!mbar_wait_bounded(a.status, &im.full_t, use)) return;
 #pragma unroll
-    for (int kt = 0; kt < 4; ++kt)
-      if (kt >= wr) {
-        Frag<2> ft, fy;
-        a_tri_t(ft, im.t, kt, wr, lane);
-        b_kn<2, false>(fy, tl.y, kC, kC * kVt, 16 * wc, 16 * kt, lane);
-        mma_parts<2, 2>(l[0], l[1], ft, fy);
-      }
-    const float fl = sc.inv_t * pow2_inverse(sY), bound = sc.t_sum * max_of(tl.m_y);
-    const float sL = pow2_scale(bound), sLW = pow2_scale(bound * sc.ek_max);
-    float l_max = 0.f;
-    __half* l_at = reinterpret_cast<__half*>(a.b.l_img + at_t * (2 * kC * kVt * 2));
+    for (int i = 0; i < 4; ++i) {
+      Frag<2> fy;
+      to_a(fy, y[2 * i], y[2 * i + 1], sY);
+      Frag<2> ft[4];
 #pragma unroll
-    for (int h = 0; h < 2; ++h) {
-      const float w = sc.eg[i0 + 8 * h] * rows.ks[i0 + 8 * h];
-      const int t = sq.t0 + c * kC + i0 + 8 * h;
-#pragma unroll
-      for (int nt = 0; nt < 2; ++nt) {
-        const float l0 = l[nt][2 * h] * fl, l1 = l[nt][2 * h + 1] * fl;
-        l_max = abs_max(abs_max(l_max, l0), l1);
-        const int col = 16 * wc + 8 * nt + 2 * t4;
-        put2<false>(tl.lw, kC, kC * kVt, i0 + 8 * h, col, (l0 * w) * sLW, (l1 * w) * sLW);
-        put2<false>(l_at, kC, kC * kVt, i0 + 8 * h, col, l0 * sL, l1 * sL);  // in global memory
-        if (t < sq.t1 && vt * kVt + col < V) store2(dv_at + t * row_t + col, l0, l1);
-      }
+      for (int j = 0; j <= i; ++j) b_tri_kn<2>(ft[j], im.t, i, j, lane);
+      mma_row<4>(x, fy, ft, 0, i + 1);
     }
-    l_max = warp_max_abs(l_max);
-    if (lane == 0) tl.m_l[warp] = l_max;
-    if (s + 1 < n) max_do();
-    if (tid == 0) {
-      a.b.dsl[at_t] = make_float4(inv_s, pow2_inverse(sL), inv_d, 0.f);
-      bulk_wait_read();  // the images of dS and do are written anew after this barrier
+    give_up(&im.free_t, lane);
+    const float fl = sc.inv_t * pow2_inverse(sY);
+#pragma unroll
+    for (int nt = 0; nt < 8; ++nt)
+#pragma unroll
+      for (int e = 0; e < 4; ++e) x[nt][e] *= fl;
+    const float sL = pow2_scale(warp_max(x));
+#pragma unroll
+    for (int j = 0; j < 4; ++j) {
+      Frag<2> f;
+      to_a(f, x[2 * j], x[2 * j + 1], sL);
+      put_a(mine.l, kVt * kC, 16 * j, f, lane);
     }
-    group_barrier(bar);
-    if (tid == 0 && s + 1 < n && fill.last(im.done_t)) {
-      fill.t(s + 1);
-      fill.ask(s + 3);
-    }
-
-    // dS0
-    {
-      float d1[kNt][4], d2[kNt][4];
-      zero(d1), zero(d2);
-      if (!mbar_wait_bounded(a.status, &im.full_q, use)) return;
-#pragma unroll
-      for (int kt = 0; kt < 4; ++kt) {
-        Frag<2> fd, fw;
-        a_km<2, false>(fd, tl.dw, kC, kC * kVt, 16 * wc, 16 * kt, lane);
-        a_km<2, false>(fw, tl.lw, kC, kC * kVt, 16 * wc, 16 * kt, lane);
-#pragma unroll
-        for (int nt = 0; nt < kNt; nt += 2) {
-          Frag<P> fq, fk;
-          b_kn<P, true>(fq, im.q, kC, kC * KP, key0 + 8 * nt, 16 * kt, lane);
-          b_kn<P, true>(fk, kimg, kC, kC * KP, key0 + 8 * nt, 16 * kt, lane);
-          mma_parts<2, P>(d1[nt], d1[nt + 1], fd, fq);
-          mma_parts<2, P>(d2[nt], d2[nt + 1], fw, fk);
-        }
-      }
-      const float inv_dw = pow2_inverse(sDW), inv_lw = pow2_inverse(sLW);
-      s_max = 0.f;
-#pragma unroll
-      for (int nt = 0; nt < kNt; ++nt)
-#pragma unroll
-        for (int e = 0; e < 4; ++e) {
-          S[nt][e] = fmaf(d1[nt][e], inv_dw, fmaf(-d2[nt][e], inv_lw, sc.egc * S[nt][e]));
-          s_max = abs_max(s_max, S[nt][e]);
-        }
-    }
-    sS = pow2_scale(sc.egc * mS + sc.q_sum * mDo + sc.k_sum * max_of(tl.m_l));
-    put_state(sS);
-    if (s + 1 < n) put_do();
-    s_max = warp_max_abs(s_max);
-    if (lane == 0) tl.m_s[warp] = s_max;
     wkv7::fence_proxy_async_smem();
-    group_barrier(bar);
-    if (tid == 0 && s + 1 < n && fill.last(im.done_k[use])) {
-      fill.q(s + 1);
-      if (s + 2 < n) fill.k(s + 2);
+    __syncwarp();
+    if (lane == 0) {
+      bulk_store(a.b.ds_img + at_t * sizeof(mine.s), mine.s, sizeof(mine.s));
+      bulk_store(a.b.do_img + at_t * sizeof(mine.d), mine.d, sizeof(mine.d));
+      bulk_store(a.b.l_img + at_t * sizeof(mine.l), mine.l, sizeof(mine.l));
+      bulk_commit();
+      a.b.dsl[at_t] = make_float4(inv_s, pow2_inverse(sL), inv_d, 0.f);
     }
-  }
-  if (tid == 0) bulk_wait_all();
+    rows_out(x, mine.rows[use], dv_at + (size_t)c * kC * row_t, row_t, len, cols, lane);
 
-  if (a.dS_init) {
+    // dS0, both products at one scale, kept below 2^60 of dS1's
+#pragma unroll
+    for (int nt = 0; nt < 8; ++nt) {
+      const float2 f = *reinterpret_cast<const float2*>(sc.ek + 8 * nt + 2 * t4), fd = *reinterpret_cast<const float2*>(sc.eq + 8 * nt + 2 * t4);
+#pragma unroll
+      for (int h = 0; h < 4; h += 2) {
+        x[nt][h] *= -f.x, x[nt][h + 1] *= -f.y;
+        d[nt][h] *= fd.x, d[nt][h + 1] *= fd.y;
+      }
+    }
+    const float sW = fminf(pow2_scale(abs_max(warp_max(x), warp_max(d))), sS * 0x1p60f), egc = sc.egc * sW;
 #pragma unroll
     for (int nt = 0; nt < kNt; ++nt)
 #pragma unroll
-      for (int h = 0; h < 2; ++h) {
-        const int row = vt * kVt + 16 * wc + g4 + 8 * h, key = key0 + 8 * nt + 2 * t4;
-        if (row < V && key < K)
-          *reinterpret_cast<float2*>(a.dS_init + (state_at + row) * K + key) = make_float2(S[nt][2 * h], S[nt][2 * h + 1]);
-      }
+      for (int e = 0; e < 4; ++e) S[nt][e] *= egc;
+    if (!mbar_wait_bounded(a.status, &im.full_q, use)) return;
+#pragma unroll
+    for (int j = 0; j < 4; ++j) {
+      Frag<2> fl2, fd;
+      to_a(fl2, x[2 * j], x[2 * j + 1], sW);
+      to_a(fd, d[2 * j], d[2 * j + 1], sW);
+      Frag<P> fb[KP / 16];
+#pragma unroll
+      for (int nb = 0; nb < KP / 16; ++nb) b_kn<P>(fb[nb], im.k[use], kC, kC * KP, 16 * nb, 16 * j, lane);
+      mma_row<KP / 16>(S, fl2, fb);
+#pragma unroll
+      for (int nb = 0; nb < KP / 16; ++nb) b_kn<P>(fb[nb], im.q, kC, kC * KP, 16 * nb, 16 * j, lane);
+      mma_row<KP / 16>(S, fd, fb);
+    }
+    give_up(&im.free_q, lane);
+    give_up(&im.free_k[use], lane);
+    const float inv_w = pow2_inverse(sW);
+#pragma unroll
+    for (int nt = 0; nt < kNt; ++nt)
+#pragma unroll
+      for (int e = 0; e < 4; ++e) S[nt][e] *= inv_w;
+    s_max = warp_max(S);
   }
+  if (lane == 0) bulk_wait_all();
+  if (a.dS_init) store_state(S, a.dS_init + state_at, cols, K, lane);
 }
 
-template <typename T, int KP, int kTiles>
-cudaError_t launch(const Args& a, cudaStream_t stream) {
-  constexpr size_t smem = sizeof(BwdSmem<T, KP, kTiles>);
-  auto kernel = bwd_kernel<T, KP, kTiles>;
-  cudaError_t e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem);
-  if (e != cudaSuccess) return e;
-  const int sets = (v_tiles(a.s.V) + kTiles - 1) / kTiles;
-  kernel<<<(unsigned)((size_t)a.s.nseq * a.s.Hv * sets), kTiles * kGroupThreads, smem, stream>>>(a);
-  return cudaGetLastError();
-}
 template <typename T, int KP>
-cudaError_t pick(const Args& a, cudaStream_t s) {
-  return two_tiles(a.s) ? launch<T, KP, 2>(a, s) : launch<T, KP, 1>(a, s);
+cudaError_t launch(const Args& a, cudaStream_t stream) {
+  const int warps = chain_warps(a.s);
+  constexpr size_t most = sizeof(BwdSmem<T, KP>);
+  static_assert(most <= 227 * 1024, "shared memory of a block");
+  auto kernel = bwd_kernel<T, KP>;
+  cudaError_t e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)most);
+  if (e != cudaSuccess) return e;
+  const int sets = (v_tiles(a.s.V) + warps - 1) / warps;
+  const size_t smem = most - (kMaxWarps - warps) * sizeof(BwdWarp<T, KP>);
+  kernel<<<(unsigned)((size_t)a.s.nseq * a.s.Hv * sets), (warps + 1) * 32, smem, stream>>>(a);
+  return cudaGetLastError();
 }
 template <typename T>
 cudaError_t pick(const Args& a, cudaStream_t s) {
-  return padded_k(a.s.K) == 128 ? pick<T, 128>(a, s) : pick<T, 64>(a, s);
+  return padded_k(a.s.K) == 128 ? launch<T, 128>(a, s) : launch<T, 64>(a, s);
 }
 
 }  // namespace

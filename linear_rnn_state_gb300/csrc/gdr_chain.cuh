@@ -1,96 +1,237 @@
-// What the forward and the backward chain of the gated delta rule share: the
-// images of a chunk in shared memory, read by one or two groups of eight warps,
-// each with a tile of 32 value columns.
+// What the forward and the backward chain of the gated delta rule share.
 //
-// q, T and P have one place each and k two: each is filled again as soon as
-// every group is past its last use in the step, which leaves half a step or
-// more for the copy, and a block of one group with 64-wide keys in 113 KB, so
-// that two share an SM. The thread that finds its group to be the last issues
-// the copy, so nobody waits to fill.
+// A warp owns 16 rows of the state (value columns) and all keys, and keeps them
+// as the accumulator of its products. With the rows as the m of every product
+// (S k^T, r T^T, u P^T, w^T k are 16 x 64 or 16 x keys) the result of one is,
+// packed to fp16 pairs, the A operand of the next (to_a): the whole step runs
+// in registers, warps never wait for one another, and every scale is the exact
+// maximum of the warp's own values. Only the chunk's images of q, k, T and P
+// come from shared memory, read by all warps of the block, which take the same
+// head's rows. (Measured before: tiles of 16 tokens by 16 columns a warp, with
+// each intermediate in shared memory, spent 42 % of a step on shared-memory
+// reads and another 25 % at three barriers.)
+//
+// One more warp fills the images by bulk copies: q, T and P have one place each
+// and k two, each filled again as soon as every warp is past its last use in
+// the step.
 #pragma once
 
 #include "gdr_common.cuh"
 
 namespace gdr {
 
-constexpr int kGroupThreads = 256;
+constexpr int kMaxWarps = 4;  // compute warps of a block
 
-template <int P, int KP>
+// pT: parts of the P image that the chain reads.
+template <int P, int KP, int pT>
 struct alignas(128) Images {
   __half k[2][P * kC * KP];
   __half q[P * kC * KP];
-  __half t[2 * kTriPart], p[2 * kTriPart];
-  Scal scal[2];
-  Rows rows[2];
+  __half t[2 * kTriPart], p[pT * kTriPart];
+  unsigned char scal[2][kChainScal];
   uint64_t full_k[2], full_q, full_t, full_p;
-  // groups past their last use, ever. k has a count a place: a group may be a step ahead in it
-  unsigned done_k[2], done_t, done_p;
+  uint64_t free_k[2], free_q, free_t, free_p;
+  __device__ __forceinline__ const Scal& sc(int place) const { return *reinterpret_cast<const Scal*>(scal[place]); }
 };
 
-// Fills the images of steps 0 .. n - 1, whose chunk slots are slot0 + s or,
-// backwards, slot0 - s.
-template <int P, int KP>
-struct Filler {
-  static constexpr int image = P * kC * KP * 2, tri = Layout::tp_img;
-  Images<P, KP>& m;
-  const Args& a;
-  long long slot0;
-  int direction, n, hk, hv, groups;
+template <int P, int KP, int pT>
+__device__ __forceinline__ void init_images(Images<P, KP, pT>& m, int warps) {
+  for (uint64_t* b : {&m.full_k[0], &m.full_k[1], &m.full_q, &m.full_t, &m.full_p}) mbar_init(b, 1);
+  for (uint64_t* b : {&m.free_k[0], &m.free_k[1], &m.free_q, &m.free_t, &m.free_p}) mbar_init(b, warps);
+  wkv7::fence_mbar_init();
+}
 
-  __device__ __forceinline__ size_t at_k(int s) const { return (size_t)(slot0 + (long long)direction * s) * a.s.Hk + hk; }
-  __device__ __forceinline__ size_t at_v(int s) const { return (size_t)(slot0 + (long long)direction * s) * a.s.Hv + hv; }
-  __device__ __forceinline__ void k(int s) const {
+// The filling thread: images of steps 0 .. n - 1, whose chunk slots are slot0 +
+// s or, backwards, slot0 - s. Later steps are asked into L2 two steps ahead.
+template <int P, int KP, int pT>
+__device__ __forceinline__ void fill_images(Images<P, KP, pT>& m, const Args& a, long long slot0, int direction, int n, int hk,
+                                            int hv) {
+  constexpr int image = P * kC * KP * 2, tri = kTriPart * 2;
+  auto at_k = [&](int s) { return (size_t)(slot0 + (long long)direction * s) * a.s.Hk + hk; };
+  auto at_v = [&](int s) { return (size_t)(slot0 + (long long)direction * s) * a.s.Hv + hv; };
+  auto k = [&](int s) {
     uint64_t* bar = &m.full_k[s & 1];
-    mbar_arrive_expect_tx(bar, image + sizeof(Rows) + sizeof(Scal));
+    mbar_arrive_expect_tx(bar, image + kChainScal);
     bulk_load(m.k[s & 1], a.b.k_img + at_k(s) * image, image, bar);
-    bulk_load(&m.rows[s & 1], a.b.rows + at_k(s), sizeof(Rows), bar);
-    bulk_load(&m.scal[s & 1], a.b.scal + at_v(s), sizeof(Scal), bar);
-  }
-  __device__ __forceinline__ void q(int s) const {
+    bulk_load(m.scal[s & 1], a.b.scal + at_v(s), kChainScal, bar);
+  };
+  auto q = [&](int s) {
     mbar_arrive_expect_tx(&m.full_q, image);
     bulk_load(m.q, a.b.q_img + at_k(s) * image, image, &m.full_q);
-  }
-  __device__ __forceinline__ void t(int s) const {
-    mbar_arrive_expect_tx(&m.full_t, tri);
-    bulk_load(m.t, a.b.t_img + at_v(s) * tri, tri, &m.full_t);
-  }
-  __device__ __forceinline__ void p(int s) const {
-    mbar_arrive_expect_tx(&m.full_p, tri);
-    bulk_load(m.p, a.b.p_img + at_v(s) * tri, tri, &m.full_p);
-  }
-  // Asks step s into L2.
-  __device__ __forceinline__ void ask(int s) const {
+  };
+  auto t = [&](int s) {
+    mbar_arrive_expect_tx(&m.full_t, 2 * tri);
+    bulk_load(m.t, a.b.t_img + at_v(s) * Layout::tp_img, 2 * tri, &m.full_t);
+  };
+  auto p = [&](int s) {
+    mbar_arrive_expect_tx(&m.full_p, pT * tri);
+    bulk_load(m.p, a.b.p_img + at_v(s) * Layout::tp_img, pT * tri, &m.full_p);
+  };
+  auto ask = [&](int s) {
     if (s >= n) return;
     bulk_prefetch(a.b.k_img + at_k(s) * image, image);
     bulk_prefetch(a.b.q_img + at_k(s) * image, image);
-    bulk_prefetch(a.b.t_img + at_v(s) * tri, tri);
-    bulk_prefetch(a.b.p_img + at_v(s) * tri, tri);
-    bulk_prefetch(a.b.scal + at_v(s), sizeof(Scal));
+    bulk_prefetch(a.b.t_img + at_v(s) * Layout::tp_img, 2 * tri);
+    bulk_prefetch(a.b.p_img + at_v(s) * Layout::tp_img, pT * tri);
+    bulk_prefetch(a.b.scal + at_v(s), kChainScal);
+  };
+  auto given_up = [&](uint64_t* bar, int use) { return mbar_wait_bounded(a.status, bar, use & 1); };
+  if (n <= 0) return;
+  k(0), q(0), t(0), p(0);
+  if (n > 1) k(1);
+  ask(2);
+  for (int s = 1; s < n; ++s) {  // in the order in which step s - 1 gives the places up
+    if (direction > 0) {
+      if (!given_up(&m.free_q, s - 1)) return;
+      q(s);
+      if (!given_up(&m.free_t, s - 1)) return;
+      t(s);
+      if (!given_up(&m.free_p, s - 1)) return;
+      p(s);
+    } else {
+      if (!given_up(&m.free_p, s - 1)) return;
+      p(s);
+      if (!given_up(&m.free_t, s - 1)) return;
+      t(s);
+      if (!given_up(&m.free_q, s - 1)) return;
+      q(s);
+    }
+    if (!given_up(&m.free_k[(s - 1) & 1], (s - 1) >> 1)) return;
+    if (s + 1 < n) k(s + 1);
+    ask(s + 2);
   }
-  __device__ __forceinline__ void start() const {
-    for (uint64_t* b : {&m.full_k[0], &m.full_k[1], &m.full_q, &m.full_t, &m.full_p}) mbar_init(b, 1);
-    m.done_k[0] = m.done_k[1] = m.done_t = m.done_p = 0;
-    wkv7::fence_mbar_init();
-    if (n <= 0) return;
-    k(0), p(0), t(0), q(0);
-    if (n > 1) k(1);
-    ask(2);
-  }
-  // One thread of a group calls this after a barrier that every warp of it
-  // reaches past its last use: whether the other groups are past theirs too.
-  __device__ __forceinline__ bool last(unsigned& done) const {
-    if (groups == 1) return true;
-    __threadfence_block();
-    const bool l = (atomicAdd(&done, 1u) + 1) % groups == 0;
-    __threadfence_block();
-    return l;
-  }
-};
+}
+// A warp is past its last read of a place.
+__device__ __forceinline__ void give_up(uint64_t* bar, int lane) {
+  __syncwarp();
+  if (lane == 0) mbar_arrive(bar);
+}
 
-// Asks for the rows of v (or do) of one chunk into L2: a thread a row.
+// ------------------------------------------- 64 tokens x 16 value columns ---
+//
+// A warp's part of v or do, by asynchronous copies into its own buffer, and its
+// part of o or dv out of it. In registers they are the transpose, x[nt] the
+// accumulator tile of rows (columns of v) by tokens 8 nt .. 8 nt + 7: for
+// bfloat16 ldmatrix and stmatrix transpose on the way, fp32 goes by words, its
+// rows 80 bytes apart so that the four tokens of an access differ by 8 banks.
+
 template <typename T>
-__device__ __forceinline__ void ask_rows(const T* base, long long stride_t, int t0, int t1, int tid) {
-  if (tid < kC && t0 + tid < t1) prefetch_l2(base + (t0 + tid) * stride_t);
+constexpr int kRowsBytes = sizeof(T) == 2 ? kC * 32 : kC * 80;
+
+__device__ __forceinline__ void copy_async16(void* dst, const void* src, bool there) {
+  const int bytes = there ? 16 : 0;  // 0: sixteen bytes of zeros
+  asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(smem_addr(dst)), "l"(src), "r"(bytes) : "memory");
+}
+__device__ __forceinline__ void copy_commit() { asm volatile("cp.async.commit_group;" ::: "memory"); }
+template <int kLeft>
+__device__ __forceinline__ void copy_wait() {
+  asm volatile("cp.async.wait_group %0;" ::"n"(kLeft) : "memory");
+}
+
+// rows points at token 0 of the chunk; len of its tokens and cols of the 16 columns exist.
+template <typename T>
+__device__ __forceinline__ void rows_in(unsigned char* buf, const T* rows, long long stride_t, int len, int cols, int lane) {
+  constexpr int kPer = 16 / sizeof(T), kPieces = 16 / kPer;  // values and pieces of 16 bytes
+#pragma unroll
+  for (int i = 0; i < kC * kPieces / 32; ++i) {
+    const int id = i * 32 + lane, row = id / kPieces, c = id % kPieces;
+    const bool there = row < len && c * kPer < cols;
+    unsigned char* dst = sizeof(T) == 2 ? buf + 2 * tri_at(row, c * 8) : buf + row * 80 + c * 16;
+    copy_async16(dst, there ? rows + row * stride_t + c * kPer : rows, there);
+  }
+}
+__device__ __forceinline__ void rows_get(float (&x)[8][4], const unsigned char* buf, int lane, const __nv_bfloat16*) {
+#pragma unroll
+  for (int q = 0; q < 4; ++q) {
+    uint32_t r[4];
+    ldsm4t(r, reinterpret_cast<const __half*>(buf) + tri_at(16 * q + (lane & 15), (lane >> 4) * 8));
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+      float* y = &x[2 * q + (i & 1)][i & 2];
+      y[0] = __uint_as_float(r[i] << 16), y[1] = __uint_as_float(r[i] & 0xFFFF0000u);
+    }
+  }
+}
+__device__ __forceinline__ void rows_get(float (&x)[8][4], const unsigned char* buf, int lane, const float*) {
+  const float* s = reinterpret_cast<const float*>(buf);
+#pragma unroll
+  for (int nt = 0; nt < 8; ++nt)
+#pragma unroll
+    for (int e = 0; e < 4; ++e) x[nt][e] = s[(8 * nt + 2 * (lane & 3) + (e & 1)) * 20 + (lane >> 2) + 8 * (e >> 1)];
+}
+__device__ __forceinline__ void rows_put(const float (&x)[8][4], unsigned char* buf, int lane, const __nv_bfloat16*) {
+#pragma unroll
+  for (int q = 0; q < 4; ++q) {
+    uint32_t r[4];
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+      const float* y = &x[2 * q + (i & 1)][i & 2];
+      const __nv_bfloat162 v = __floats2bfloat162_rn(y[0], y[1]);
+      r[i] = *reinterpret_cast<const uint32_t*>(&v);
+    }
+    stsm4t(reinterpret_cast<__half*>(buf) + tri_at(16 * q + (lane & 15), (lane >> 4) * 8), r);
+  }
+}
+__device__ __forceinline__ void rows_put(const float (&x)[8][4], unsigned char* buf, int lane, const float*) {
+  float* s = reinterpret_cast<float*>(buf);
+#pragma unroll
+  for (int nt = 0; nt < 8; ++nt)
+#pragma unroll
+    for (int e = 0; e < 4; ++e) s[(8 * nt + 2 * (lane & 3) + (e & 1)) * 20 + (lane >> 2) + 8 * (e >> 1)] = x[nt][e];
+}
+// x to memory by way of buf.
+template <typename T>
+__device__ __forceinline__ void rows_out(const float (&x)[8][4], unsigned char* buf, T* rows, long long stride_t, int len,
+                                         int cols, int lane) {
+  constexpr int kPer = 16 / sizeof(T), kPieces = 16 / kPer;
+  rows_put(x, buf, lane, rows);
+  __syncwarp();
+#pragma unroll
+  for (int i = 0; i < kC * kPieces / 32; ++i) {
+    const int id = i * 32 + lane, row = id / kPieces, c = id % kPieces;
+    const unsigned char* src = sizeof(T) == 2 ? buf + 2 * tri_at(row, c * 8) : buf + row * 80 + c * 16;
+    if (row < len && c * kPer < cols) *reinterpret_cast<uint4*>(rows + row * stride_t + c * kPer) = *reinterpret_cast<const uint4*>(src);
+  }
+  __syncwarp();
+}
+// Asks for a chunk's rows into L2.
+template <typename T>
+__device__ __forceinline__ void rows_ask(const T* rows, long long stride_t, int len, int lane) {
+#pragma unroll
+  for (int i = 0; i < kC / 32; ++i)
+    if (i * 32 + lane < len) prefetch_l2(rows + (i * 32 + lane) * stride_t);
+}
+
+// The state of a warp: rows row0 + g4 (+ 8), keys 8 nt + 2 t4 (+ 1).
+template <int N>
+__device__ __forceinline__ void load_state(float (&S)[N][4], const float* src, int rows, int K, int lane) {
+#pragma unroll
+  for (int nt = 0; nt < N; ++nt)
+#pragma unroll
+    for (int h = 0; h < 2; ++h) {
+      const int row = (lane >> 2) + 8 * h, key = 8 * nt + 2 * (lane & 3);
+      float2 x = make_float2(0.f, 0.f);
+      if (src && row < rows && key < K) x = *reinterpret_cast<const float2*>(src + (size_t)row * K + key);
+      S[nt][2 * h] = x.x, S[nt][2 * h + 1] = x.y;
+    }
+}
+template <int N>
+__device__ __forceinline__ void store_state(const float (&S)[N][4], float* dst, int rows, int K, int lane) {
+#pragma unroll
+  for (int nt = 0; nt < N; ++nt)
+#pragma unroll
+    for (int h = 0; h < 2; ++h) {
+      const int row = (lane >> 2) + 8 * h, key = 8 * nt + 2 * (lane & 3);
+      if (row < rows && key < K) *reinterpret_cast<float2*>(dst + (size_t)row * K + key) = make_float2(S[nt][2 * h], S[nt][2 * h + 1]);
+    }
+}
+
+// Compute warps of a block: four, one a scheduler, unless that leaves most SMs
+// without a block; then two.
+inline int chain_warps(const Shape& s) {
+  const long long tiles = v_tiles(s.V);
+  const int w = tiles < kMaxWarps ? (int)tiles : kMaxWarps;
+  return w > 2 && (long long)s.nseq * s.Hv * ((tiles + w - 1) / w) <= 152 / 2 ? 2 : w;
 }
 
 }  // namespace gdr

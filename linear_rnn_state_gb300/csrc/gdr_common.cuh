@@ -18,9 +18,8 @@
 // Images. A tile lives in global memory exactly as in shared memory: rows of
 // 128 bytes (64 fp16 values; wider tiles are several such panels one after the
 // other) whose eight 16-byte pieces are permuted by the row (piece ^ (row &
-// 7)), or rows of 64 bytes permuted by (row >> 1) & 3, so that ldmatrix reads
-// eight rows from eight different bank groups and a whole tile moves by one
-// bulk copy. A lower triangular 64 x 64 tile keeps only its ten lower 16 x 16
+// 7)), so that ldmatrix reads eight rows from eight different bank groups and a
+// whole tile moves by one bulk copy. A lower triangular 64 x 64 tile keeps only its ten lower 16 x 16
 // blocks (tri), each with rows of 32 bytes whose two pieces are swapped in
 // every other four rows. The hi part comes first, then the lo part.
 #pragma once
@@ -92,12 +91,11 @@ __device__ __forceinline__ void split2(float a, float b, uint32_t& hi, uint32_t&
   }
 }
 
-// The power of two s with bound * s in [2^13, 2^14), its exponent held to
-// +-120 so that s and 1/s are normal floats (0 gives 2^120: everything the
-// bound covers is 0; infinity and NaN give 2^-114, and the values themselves
-// carry the infinity or NaN into the products).
-__device__ __forceinline__ float pow2_scale(float bound) {
-  int e = (int)((__float_as_uint(bound) >> 23) & 255u) - 127;
+// The power of two s with largest * s in [2^13, 2^14), its exponent held to
+// +-120 so that s and 1/s are normal floats (0 gives 2^120; infinity and NaN
+// give 2^-114, and the values themselves carry them into the products).
+__device__ __forceinline__ float pow2_scale(float largest) {
+  int e = (int)((__float_as_uint(largest) >> 23) & 255u) - 127;
   e = 13 - e;
   e = e > 120 ? 120 : (e < -120 ? -120 : e);
   return __uint_as_float((uint32_t)(e + 127) << 23);
@@ -114,14 +112,9 @@ __device__ __forceinline__ float abs_max(float m, float x) {  // keeps NaN
 
 // ------------------------------------------------------------- images ----
 
-// Offset (in halves) of (row, col) in an image of `rows` rows. kWide: panels
-// of 64 columns with 128-byte rows; otherwise 32 columns with 64-byte rows.
-template <bool kWide>
+// Offset (in halves) of (row, col) in an image of `rows` rows.
 __device__ __forceinline__ int img(int rows, int row, int col) {
-  if constexpr (kWide)
-    return (col >> 6) * rows * 64 + row * 64 + ((((col >> 3) & 7) ^ (row & 7)) << 3) + (col & 7);
-  else
-    return row * 32 + ((((col >> 3) & 3) ^ ((row >> 1) & 3)) << 3) + (col & 7);
+  return (col >> 6) * rows * 64 + row * 64 + ((((col >> 3) & 7) ^ (row & 7)) << 3) + (col & 7);
 }
 
 // Lower triangular images: the block (i, j), j <= i < 4, and a place in it.
@@ -138,6 +131,16 @@ __device__ __forceinline__ void ldsm4t(uint32_t (&r)[4], const __half* p) {
   asm volatile("ldmatrix.sync.aligned.m8n8.x4.trans.shared.b16 {%0,%1,%2,%3}, [%4];"
                : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3])
                : "r"(smem_addr(p)));
+}
+__device__ __forceinline__ void stsm4(__half* p, const uint32_t (&r)[4]) {
+  asm volatile("stmatrix.sync.aligned.m8n8.x4.shared.b16 [%0], {%1,%2,%3,%4};" ::"r"(smem_addr(p)), "r"(r[0]), "r"(r[1]),
+               "r"(r[2]), "r"(r[3])
+               : "memory");
+}
+__device__ __forceinline__ void stsm4t(void* p, const uint32_t (&r)[4]) {
+  asm volatile("stmatrix.sync.aligned.m8n8.x4.trans.shared.b16 [%0], {%1,%2,%3,%4};" ::"r"(smem_addr(p)), "r"(r[0]),
+               "r"(r[1]), "r"(r[2]), "r"(r[3])
+               : "memory");
 }
 __device__ __forceinline__ void mma16(float (&d)[4], const uint32_t (&a)[4], uint32_t b0, uint32_t b1) {
   asm("mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, "
@@ -156,27 +159,27 @@ struct Frag {
   uint32_t h[4];
   uint32_t l[kP == 2 ? 4 : 1];
 };
-template <int kP, bool kWide>
+template <int kP>
 __device__ __forceinline__ void a_mk(Frag<kP>& f, const __half* s, int rows, int part, int m0, int k0, int lane) {
-  const __half* p = s + img<kWide>(rows, m0 + (lane & 15), k0 + (lane >> 4) * 8);
+  const __half* p = s + img(rows, m0 + (lane & 15), k0 + (lane >> 4) * 8);
   ldsm4(f.h, p);
   if constexpr (kP == 2) ldsm4(f.l, p + part);
 }
-template <int kP, bool kWide>
+template <int kP>
 __device__ __forceinline__ void a_km(Frag<kP>& f, const __half* s, int rows, int part, int m0, int k0, int lane) {
-  const __half* p = s + img<kWide>(rows, k0 + (lane & 7) + (lane >> 4) * 8, m0 + ((lane >> 3) & 1) * 8);
+  const __half* p = s + img(rows, k0 + (lane & 7) + (lane >> 4) * 8, m0 + ((lane >> 3) & 1) * 8);
   ldsm4t(f.h, p);
   if constexpr (kP == 2) ldsm4t(f.l, p + part);
 }
-template <int kP, bool kWide>
+template <int kP>
 __device__ __forceinline__ void b_nk(Frag<kP>& f, const __half* s, int rows, int part, int n0, int k0, int lane) {
-  const __half* p = s + img<kWide>(rows, n0 + (lane & 7) + (lane >> 4) * 8, k0 + ((lane >> 3) & 1) * 8);
+  const __half* p = s + img(rows, n0 + (lane & 7) + (lane >> 4) * 8, k0 + ((lane >> 3) & 1) * 8);
   ldsm4(f.h, p);
   if constexpr (kP == 2) ldsm4(f.l, p + part);
 }
-template <int kP, bool kWide>
+template <int kP>
 __device__ __forceinline__ void b_kn(Frag<kP>& f, const __half* s, int rows, int part, int n0, int k0, int lane) {
-  const __half* p = s + img<kWide>(rows, k0 + (lane & 15), n0 + (lane >> 4) * 8);
+  const __half* p = s + img(rows, k0 + (lane & 15), n0 + (lane >> 4) * 8);
   ldsm4t(f.h, p);
   if constexpr (kP == 2) ldsm4t(f.l, p + part);
 }
@@ -191,6 +194,19 @@ __device__ __forceinline__ void a_tri_t(Frag<2>& f, const __half* s, int i, int 
   const __half* p = s + tri_block(i, j) + tri_at((lane & 7) + (lane >> 4) * 8, ((lane >> 3) & 1) * 8);
   ldsm4t(f.h, p);
   ldsm4t(f.l, p + kTriPart);
+}
+// B fragments of the block (i, j): B[k][n] = X[16 i + n][16 j + k], or X[16 i + k][16 j + n].
+template <int kP>
+__device__ __forceinline__ void b_tri_nk(Frag<kP>& f, const __half* s, int i, int j, int lane) {
+  const __half* p = s + tri_block(i, j) + tri_at((lane & 7) + (lane >> 4) * 8, ((lane >> 3) & 1) * 8);
+  ldsm4(f.h, p);
+  if constexpr (kP == 2) ldsm4(f.l, p + kTriPart);
+}
+template <int kP>
+__device__ __forceinline__ void b_tri_kn(Frag<kP>& f, const __half* s, int i, int j, int lane) {
+  const __half* p = s + tri_block(i, j) + tri_at(lane & 15, (lane >> 4) * 8);
+  ldsm4t(f.h, p);
+  if constexpr (kP == 2) ldsm4t(f.l, p + kTriPart);
 }
 __device__ __forceinline__ void put2_tri(__half* s, int row, int col, float x0, float x1) {
   uint32_t hi, lo;
@@ -212,22 +228,54 @@ __device__ __forceinline__ void mma_parts(float (&d0)[4], float (&d1)[4], const 
   mma_pair(d0, d1, a.h, b.h);
 }
 
-// Stores (x0, x1) at (row, col), (row, col + 1) of a two-part image.
-template <bool kWide>
-__device__ __forceinline__ void put2(__half* s, int rows, int part, int row, int col, float x0, float x1) {
-  uint32_t hi, lo;
-  split2<2>(x0, x1, hi, lo);
-  const int at = img<kWide>(rows, row, col);
-  *reinterpret_cast<uint32_t*>(s + at) = hi;
-  *reinterpret_cast<uint32_t*>(s + at + part) = lo;
+// N pairs of n8 tiles += a b[n]: part by part over all of them, so that two mma
+// on one accumulator stand 2 N apart (a dependent mma waits about 33 cycles, an
+// independent one 8).
+template <int N, int kA, int kB, int kTilesOf>
+__device__ __forceinline__ void mma_row(float (&d)[kTilesOf][4], const Frag<kA>& a, const Frag<kB> (&b)[N], int first = 0, int end = N) {
+  if constexpr (kA == 2)
+#pragma unroll
+    for (int n = 0; n < N; ++n)
+      if (n >= first && n < end) mma_pair(d[2 * n], d[2 * n + 1], a.l, b[n].h);
+  if constexpr (kB == 2)
+#pragma unroll
+    for (int n = 0; n < N; ++n)
+      if (n >= first && n < end) mma_pair(d[2 * n], d[2 * n + 1], a.h, b[n].l);
+#pragma unroll
+  for (int n = 0; n < N; ++n)
+    if (n >= first && n < end) mma_pair(d[2 * n], d[2 * n + 1], a.h, b[n].h);
 }
-template <int kP, bool kWide>
-__device__ __forceinline__ void put2_p(__half* s, int rows, int part, int row, int col, float x0, float x1) {
-  uint32_t hi, lo = 0;
-  split2<kP>(x0, x1, hi, lo);
-  const int at = img<kWide>(rows, row, col);
-  *reinterpret_cast<uint32_t*>(s + at) = hi;
-  if constexpr (kP == 2) *reinterpret_cast<uint32_t*>(s + at + part) = lo;
+// As mma_row, with the hi part of a alone where b has one part.
+template <int N, int kA, int kB, int kTilesOf>
+__device__ __forceinline__ void mma_row_out(float (&d)[kTilesOf][4], const Frag<kA>& a, const Frag<kB> (&b)[N], int first = 0) {
+  if constexpr (kB == 2) {
+    mma_row<N, kA, kB>(d, a, b, first);
+  } else {
+#pragma unroll
+    for (int n = 0; n < N; ++n)
+      if (n >= first) mma_pair(d[2 * n], d[2 * n + 1], a.h, b[n].h);
+  }
+}
+
+// Two accumulator tiles (16 rows, columns k0 .. k0+7 and k0+8 .. k0+15) times s
+// as the A fragment of a product over those columns.
+template <int kP>
+__device__ __forceinline__ void to_a(Frag<kP>& f, const float (&x)[4], const float (&y)[4], float s) {
+  uint32_t l[4];
+  split2<kP>(x[0] * s, x[1] * s, f.h[0], l[0]);
+  split2<kP>(x[2] * s, x[3] * s, f.h[1], l[1]);
+  split2<kP>(y[0] * s, y[1] * s, f.h[2], l[2]);
+  split2<kP>(y[2] * s, y[3] * s, f.h[3], l[3]);
+  if constexpr (kP == 2)
+#pragma unroll
+    for (int i = 0; i < 4; ++i) f.l[i] = l[i];
+}
+// An A fragment into an image of 16 rows, where a_mk would read it.
+template <int kP>
+__device__ __forceinline__ void put_a(__half* s, int part, int k0, const Frag<kP>& f, int lane) {
+  __half* p = s + img(16, lane & 15, k0 + (lane >> 4) * 8);
+  stsm4(p, f.h);
+  if constexpr (kP == 2) stsm4(p + part, f.l);
 }
 
 // ---------------------------------------------------------- bulk copies ---
@@ -249,19 +297,18 @@ __device__ __forceinline__ void bulk_wait_all() { asm volatile("cp.async.bulk.wa
 __device__ __forceinline__ void bulk_prefetch(const void* src, uint32_t bytes) {
   asm volatile("cp.async.bulk.prefetch.L2.global [%0], %1;" ::"l"(src), "r"(bytes) : "memory");
 }
-__device__ __forceinline__ void prefetch_l2(const void* p) { asm volatile("prefetch.global.L2 [%0];" ::"l"(p)); }
 __device__ __forceinline__ void mbar_arrive(uint64_t* bar) {
   asm volatile("mbarrier.arrive.shared::cta.b64 _, [%0];" ::"r"(smem_addr(bar)) : "memory");
 }
-// Barrier of 256 threads; id 1 and up.
-__device__ __forceinline__ void group_barrier(int id) { asm volatile("bar.sync %0, 256;" ::"r"(id) : "memory"); }
-
+__device__ __forceinline__ void prefetch_l2(const void* p) { asm volatile("prefetch.global.L2 [%0];" ::"l"(p)); }
 template <int N>
-__device__ __forceinline__ float max_of(const float (&x)[N]) {
-  float m = x[0];
+__device__ __forceinline__ float warp_max(const float (&x)[N][4]) {
+  float m = 0.f;
 #pragma unroll
-  for (int i = 1; i < N; ++i) m = abs_max(m, x[i]);
-  return m;
+  for (int n = 0; n < N; ++n)
+#pragma unroll
+    for (int e = 0; e < 4; ++e) m = abs_max(m, x[n][e]);
+  return warp_max_abs(m);
 }
 template <int N>
 __device__ __forceinline__ void zero(float (&x)[N][4]) {

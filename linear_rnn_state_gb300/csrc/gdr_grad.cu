@@ -28,11 +28,12 @@ template <int KP>
 constexpr int kThreads = KP / 32 * 128;
 
 template <int P, int KP>
-struct alignas(128) Tile {
+struct alignas(128) Tile {  // of 16 value columns
   __half s[2 * kVt * KP], ds[2 * kVt * KP];
-  __half u[2 * kC * kVt], l[2 * kC * kVt];
-  __half d[P * kC * kVt];
+  __half u[2 * kVt * kC], l[2 * kVt * kC];
+  __half d[P * kVt * kC];
 };
+constexpr int kStages = 4;
 struct alignas(128) Pairs {  // F and E as operands: columns times beta ks, and rows times qs or ks
   __half fb[2 * kTriPart], eb[2 * kTriPart], f[2 * kTriPart], e[2 * kTriPart];
 };
@@ -41,7 +42,7 @@ struct alignas(128) GradSmem {
   static constexpr int P = In<T>::kParts;
   __half q[P * kC * KP], k[P * kC * KP];
   union {
-    Tile<P, KP> tile[2];
+    Tile<P, KP> tile[kStages];
     Pairs pairs;  // once the tiles are used up
   };
   Scal scal;
@@ -51,12 +52,12 @@ struct alignas(128) GradSmem {
   float red[KP / 8][4];
   float sdot[KP / 8];
   float dG[kC];
-  uint64_t bar[3];
+  uint64_t bar[kStages + 1];
 };
 
 template <int P, int KP>
 __device__ __forceinline__ float2 pick2(const __half* s, int row, int col) {
-  const int at = img<true>(kC, row, col);
+  const int at = img(kC, row, col);
   float2 x = unpack_f16(*reinterpret_cast<const uint32_t*>(s + at));
   if constexpr (P == 2) {
     const float2 y = unpack_f16(*reinterpret_cast<const uint32_t*>(s + kC * KP + at));
@@ -90,8 +91,8 @@ __global__ void __launch_bounds__(kThreads<KP>, KP == 64 ? 2 : 1) grad_kernel(co
   constexpr uint32_t kTileBytes = sizeof(Tile<P, KP>);
 
   auto load = [&](int v) {
-    Tile<P, KP>& t = sm.tile[v & 1];
-    uint64_t* bar = &sm.bar[v & 1];
+    Tile<P, KP>& t = sm.tile[v % kStages];
+    uint64_t* bar = &sm.bar[v % kStages];
     const size_t at = at_v * vts + v;
     mbar_arrive_expect_tx(bar, kTileBytes);
     bulk_load(t.s, a.b.s_img + at * sizeof(t.s), sizeof(t.s), bar);
@@ -101,15 +102,14 @@ __global__ void __launch_bounds__(kThreads<KP>, KP == 64 ? 2 : 1) grad_kernel(co
     bulk_load(t.d, a.b.do_img + at * sizeof(t.d), sizeof(t.d), bar);
   };
   if (tid == 0) {
-    for (int s = 0; s < 3; ++s) mbar_init(&sm.bar[s], 1);
+    for (int s = 0; s <= kStages; ++s) mbar_init(&sm.bar[s], 1);
     wkv7::fence_mbar_init();
-    load(0);
-    if (vts > 1) load(1);
-    mbar_arrive_expect_tx(&sm.bar[2], 2 * image + sizeof(Scal) + sizeof(Rows));
-    bulk_load(sm.q, a.b.q_img + at_k * image, image, &sm.bar[2]);
-    bulk_load(sm.k, a.b.k_img + at_k * image, image, &sm.bar[2]);
-    bulk_load(&sm.scal, a.b.scal + at_v, sizeof(Scal), &sm.bar[2]);
-    bulk_load(&sm.rows, a.b.rows + at_k, sizeof(Rows), &sm.bar[2]);
+    for (int v = 0; v < kStages && v < vts; ++v) load(v);
+    mbar_arrive_expect_tx(&sm.bar[kStages], 2 * image + sizeof(Scal) + sizeof(Rows));
+    bulk_load(sm.q, a.b.q_img + at_k * image, image, &sm.bar[kStages]);
+    bulk_load(sm.k, a.b.k_img + at_k * image, image, &sm.bar[kStages]);
+    bulk_load(&sm.scal, a.b.scal + at_v, sizeof(Scal), &sm.bar[kStages]);
+    bulk_load(&sm.rows, a.b.rows + at_k, sizeof(Rows), &sm.bar[kStages]);
   }
   __syncthreads();
 
@@ -118,36 +118,34 @@ __global__ void __launch_bounds__(kThreads<KP>, KP == 64 ? 2 : 1) grad_kernel(co
   zero(dq), zero(rd), zero(w), zero(F), zero(E);
   float sdot = 0.f;
   for (int v = 0; v < vts; ++v) {
-    Tile<P, KP>& t = sm.tile[v & 1];
+    Tile<P, KP>& t = sm.tile[v % kStages];
     const size_t at = at_v * vts + v;
     const float2 su = a.b.su[at];
     const float4 dsl = a.b.dsl[at];
-    if (!mbar_wait_bounded(a.status, &sm.bar[v & 1], (v >> 1) & 1)) return;
-    Frag<P> fd[2];
-    Frag<2> fl[2];
-#pragma unroll
-    for (int kt = 0; kt < 2; ++kt) {
-      a_mk<P, false>(fd[kt], t.d, kC, kC * kVt, 16 * wr, 16 * kt, lane);
-      a_mk<2, false>(fl[kt], t.l, kC, kC * kVt, 16 * wr, 16 * kt, lane);
-    }
+    if (!mbar_wait_bounded(a.status, &sm.bar[v % kStages], (v / kStages) & 1)) return;
+    Frag<P> fd;
+    Frag<2> fl, fu;
+    a_km<P>(fd, t.d, kVt, kVt * kC, 16 * wr, 0, lane);
+    a_km<2>(fl, t.l, kVt, kVt * kC, 16 * wr, 0, lane);
+    a_km<2>(fu, t.u, kVt, kVt * kC, 16 * wr, 0, lane);
     const float f1 = dsl.z * su.x, f2 = dsl.y * su.x, f3 = su.y * dsl.x;
 #pragma unroll
     for (int nt = 0; nt < kNt; nt += 2) {
-      float x[4][4];
+      Frag<2> fs, fds;
+      float x[6][4];
       zero(x);
-#pragma unroll
-      for (int kt = 0; kt < 2; ++kt) {
-        Frag<2> fs;
-        b_kn<2, true>(fs, t.s, kVt, kVt * KP, key0 + 8 * nt, 16 * kt, lane);
-        mma_parts<P, 2>(x[0], x[1], fd[kt], fs);
-        mma_parts<2, 2>(x[2], x[3], fl[kt], fs);
-      }
+      b_kn<2>(fs, t.s, kVt, kVt * KP, key0 + 8 * nt, 0, lane);
+      b_kn<2>(fds, t.ds, kVt, kVt * KP, key0 + 8 * nt, 0, lane);
+      mma_parts<P, 2>(x[0], x[1], fd, fs);
+      mma_parts<2, 2>(x[2], x[3], fl, fs);
+      mma_parts<2, 2>(x[4], x[5], fu, fds);
 #pragma unroll
       for (int h = 0; h < 2; ++h)
 #pragma unroll
         for (int e = 0; e < 4; ++e) {
           dq[nt + h][e] = fmaf(f1, x[h][e], dq[nt + h][e]);
           rd[nt + h][e] = fmaf(f2, x[2 + h][e], rd[nt + h][e]);
+          w[nt + h][e] = fmaf(f3, x[4 + h][e], w[nt + h][e]);
         }
     }
 #pragma unroll
@@ -156,13 +154,10 @@ __global__ void __launch_bounds__(kThreads<KP>, KP == 64 ? 2 : 1) grad_kernel(co
       if (jb <= wr) {
         float x[4][4];
         zero(x);
-#pragma unroll
-        for (int kt = 0; kt < 2; ++kt) {
-          Frag<2> fu;
-          b_nk<2, false>(fu, t.u, kC, kC * kVt, 16 * jb, 16 * kt, lane);
-          mma_parts<P, 2>(x[0], x[1], fd[kt], fu);
-          mma_parts<2, 2>(x[2], x[3], fl[kt], fu);
-        }
+        Frag<2> fj;
+        b_kn<2>(fj, t.u, kVt, kVt * kC, 16 * jb, 0, lane);
+        mma_parts<P, 2>(x[0], x[1], fd, fj);
+        mma_parts<2, 2>(x[2], x[3], fl, fj);
 #pragma unroll
         for (int h = 0; h < 2; ++h)
 #pragma unroll
@@ -172,47 +167,24 @@ __global__ void __launch_bounds__(kThreads<KP>, KP == 64 ? 2 : 1) grad_kernel(co
           }
       }
     }
-    {
-      Frag<2> fu[2];
+    {  // <S0, dS1>: the same four values of both images
+      static_assert(kVt * KP == 4 * kThreads<KP>, "four values a thread");
+      const uint2 x0 = *reinterpret_cast<const uint2*>(t.s + 4 * tid), x1 = *reinterpret_cast<const uint2*>(t.s + kVt * KP + 4 * tid);
+      const uint2 y0 = *reinterpret_cast<const uint2*>(t.ds + 4 * tid), y1 = *reinterpret_cast<const uint2*>(t.ds + kVt * KP + 4 * tid);
+      const uint32_t xs[4] = {x0.x, x0.y, x1.x, x1.y}, ys[4] = {y0.x, y0.y, y1.x, y1.y};
+      float sd = 0.f;
 #pragma unroll
-      for (int kt = 0; kt < 2; ++kt) a_mk<2, false>(fu[kt], t.u, kC, kC * kVt, 16 * wr, 16 * kt, lane);
-#pragma unroll
-      for (int nt = 0; nt < kNt; nt += 2) {
-        float x[2][4];
-        zero(x);
-#pragma unroll
-        for (int kt = 0; kt < 2; ++kt) {
-          Frag<2> fs;
-          b_kn<2, true>(fs, t.ds, kVt, kVt * KP, key0 + 8 * nt, 16 * kt, lane);
-          mma_parts<2, 2>(x[0], x[1], fu[kt], fs);
-        }
-#pragma unroll
-        for (int h = 0; h < 2; ++h)
-#pragma unroll
-          for (int e = 0; e < 4; ++e) w[nt + h][e] = fmaf(f3, x[h][e], w[nt + h][e]);
-      }
-    }
-    // <S0, dS1>: the same place of both images
-    float sd = 0.f;
-#pragma unroll
-    for (int i = 0; i < kVt * KP / 8 / kThreads<KP>; ++i) {
-      const int at8 = (i * kThreads<KP> + tid) * 8;
-      const uint4 x0 = *reinterpret_cast<const uint4*>(t.s + at8), x1 = *reinterpret_cast<const uint4*>(t.s + kVt * KP + at8);
-      const uint4 y0 = *reinterpret_cast<const uint4*>(t.ds + at8), y1 = *reinterpret_cast<const uint4*>(t.ds + kVt * KP + at8);
-      const uint32_t xs[8] = {x0.x, x0.y, x0.z, x0.w, x1.x, x1.y, x1.z, x1.w};
-      const uint32_t ys[8] = {y0.x, y0.y, y0.z, y0.w, y1.x, y1.y, y1.z, y1.w};
-#pragma unroll
-      for (int e = 0; e < 4; ++e) {
-        const float2 xh = unpack_f16(xs[e]), xl = unpack_f16(xs[4 + e]), yh = unpack_f16(ys[e]), yl = unpack_f16(ys[4 + e]);
+      for (int e = 0; e < 2; ++e) {
+        const float2 xh = unpack_f16(xs[e]), xl = unpack_f16(xs[2 + e]), yh = unpack_f16(ys[e]), yl = unpack_f16(ys[2 + e]);
         sd = fmaf(xh.x + xl.x, yh.x + yl.x, sd);
         sd = fmaf(xh.y + xl.y, yh.y + yl.y, sd);
       }
+      sdot = fmaf(sd, su.x * dsl.x, sdot);
     }
-    sdot = fmaf(sd, su.x * dsl.x, sdot);
     __syncthreads();
-    if (tid == 0 && v + 2 < vts) load(v + 2);
+    if (tid == 0 && v + kStages < vts) load(v + kStages);
   }
-  if (!mbar_wait_bounded(a.status, &sm.bar[2], 0)) return;
+  if (!mbar_wait_bounded(a.status, &sm.bar[kStages], 0)) return;
   const Scal& sc = sm.scal;
   const Rows& rows = sm.rows;
 
@@ -279,7 +251,7 @@ __global__ void __launch_bounds__(kThreads<KP>, KP == 64 ? 2 : 1) grad_kernel(co
 #pragma unroll
     for (int kt = 0; kt < 4; ++kt) {
       Frag<P> fk;
-      b_kn<P, true>(fk, sm.k, kC, kC * KP, key0 + 8 * nt, 16 * kt, lane);
+      b_kn<P>(fk, sm.k, kC, kC * KP, key0 + 8 * nt, 16 * kt, lane);
       if (kt <= wr) {
         Frag<2> f, e;
         a_tri(f, sm.pairs.fb, wr, kt, lane);
@@ -290,7 +262,7 @@ __global__ void __launch_bounds__(kThreads<KP>, KP == 64 ? 2 : 1) grad_kernel(co
       if (kt >= wr) {
         Frag<2> f, e;
         Frag<P> fq;
-        b_kn<P, true>(fq, sm.q, kC, kC * KP, key0 + 8 * nt, 16 * kt, lane);
+        b_kn<P>(fq, sm.q, kC, kC * KP, key0 + 8 * nt, 16 * kt, lane);
         a_tri_t(f, sm.pairs.f, kt, wr, lane);
         a_tri_t(e, sm.pairs.e, kt, wr, lane);
         mma_parts<2, P>(q[0], q[1], f, fq);

@@ -9,7 +9,7 @@
 namespace gdr {
 
 constexpr int kC = 64;        // tokens of a chunk
-constexpr int kVt = 32;       // value columns of a tile
+constexpr int kVt = 16;       // value columns (rows of the state) of a tile
 constexpr int kMaxDim = 128;  // largest head size
 
 // What a call's sequences and heads look like.
@@ -34,32 +34,25 @@ inline long long slot_count(int B, int T, int nseq, bool packed) {
 inline int padded_k(int K) { return K <= 64 ? 64 : 128; }
 inline int v_tiles(int V) { return (V + kVt - 1) / kVt; }
 
-// Whether a chain's block takes two tiles of value columns (they share the
-// chunk's images in shared memory) or one (its own SM while there are enough).
-inline bool two_tiles(const Shape& s) { return v_tiles(s.V) > 1 && (long long)s.nseq * s.Hv * v_tiles(s.V) > 152; }
-
 // Scalars of a chunk: per key head (Rows) and per value head (Scal).
 struct Rows {        // of the 64 tokens, the actual q is qs * image (and k is ks * image)
   float qs[kC], ks[kC];
   float rq[kC], rk[kC];  // 1 / |q|, 1 / |k| with l2norm, else 1
 };
 struct Scal {
-  float eg[kC];    // e^G, G the running sum of g in the chunk
-  float wr[kC];    // beta e^(Gc - G), Gc the chunk's whole sum
+  // with G the running sum of g in the chunk and Gc its whole sum:
+  float ek[kC];  // e^G ks
+  float wk[kC];  // beta e^(Gc - G) ks
+  float eq[kC];  // scale e^G qs
+  float inv_t, inv_p;  // the inverse scales of the T and P images
+  float egc;           // e^Gc
+  float pad[29];
+  // up to here for the chains, from here on for the gradients
+  float eg[kC];          // e^G
   float gh[kC], gl[kC];  // G as an unrounded sum of two floats
   float beta[kC];
-  // scales of the T and P images (their inverses) and bounds, all of magnitudes
-  float inv_t, inv_p;
-  float t_sum, p_sum;  // 64 times the largest of |T|, |P|
-  float k_read;        // max e^G sum|k|
-  float k_write;       // sum |wr| max|k|
-  float wk_max;        // max |wr| ks
-  float k_back;        // max |wr| sum|k|
-  float q_sum, k_sum;  // sum |scale| e^G max|q|, sum e^G max|k|
-  float ek_max, eq_max;  // max e^G ks, max |scale| e^G qs
-  float egc;           // e^Gc
-  float pad[19];
 };
+constexpr size_t kChainScal = 3 * kC * sizeof(float) + 128;
 static_assert(sizeof(Scal) % 128 == 0 && sizeof(Rows) % 128 == 0, "bulk copies");
 
 struct Layout {
@@ -78,8 +71,8 @@ inline Layout layout(const Shape& s, bool bf16) {
   l.n_t = l.n_v * l.vt;
   l.kq_img = (size_t)l.parts * kC * l.Kp * 2;
   l.st_img = (size_t)2 * kVt * l.Kp * 2;
-  l.u_img = (size_t)2 * kC * kVt * 2;
-  l.do_img = (size_t)l.parts * kC * kVt * 2;
+  l.u_img = (size_t)2 * kVt * kC * 2;
+  l.do_img = (size_t)l.parts * kVt * kC * 2;
   return l;
 }
 

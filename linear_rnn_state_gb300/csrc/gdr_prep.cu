@@ -6,8 +6,8 @@
 //   P_ij = scale beta_j r_ij q_i.k_j  (j <= i)
 // so that with S0 the state before the chunk u = T (v - e^G S0 k) and
 // o = scale e^G S0 q + P u. The kernel writes q, k, T and P as the images that
-// the chain kernels copy into shared memory, with their scales and the bounds
-// the chains need (gdr_launch.h, Rows and Scal).
+// the chain kernels copy into shared memory, with their scales and the tokens'
+// factors (gdr_launch.h, Rows and Scal).
 //
 // The decay ratios. G is summed in double and kept as two floats, and r_ij is
 // the exponential of a difference, never a product of e^G_i with e^-G_j, so
@@ -38,7 +38,6 @@ struct alignas(128) PrepSmem {
   };
   Rows rows;
   Scal scal;
-  float q_max[kC], q_sum[kC], k_max[kC], k_sum[kC];
   float red[8];
 };
 
@@ -49,31 +48,30 @@ __device__ __forceinline__ void copy16(void* dst, const void* src, int bytes, in
 
 // One of q, k: 64 rows into an image, each row scaled by a power of two.
 template <typename T, int KP>
-__device__ __forceinline__ void load_rows(__half* image, float* inv, float* rn, float* mx, float* sm, const T* src,
-                                          long long stride_t, int len, int K, int l2norm, int tid) {
+__device__ __forceinline__ void load_rows(__half* image, float* inv, float* rn, const T* src, long long stride_t, int len,
+                                          int K, int l2norm, int tid) {
   constexpr int P = In<T>::kParts, kLanes = KP / 8, kPass = kThreads / kLanes;
   const int cl = tid % kLanes, part = kC * KP;
 #pragma unroll 2
   for (int row = tid / kLanes; row < kC; row += kPass) {
     float x[8] = {0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f};
     if (row < len && cl * 8 < K) load8(x, src + (size_t)row * stride_t + cl * 8);
-    float m = 0.f, s1 = 0.f, s2 = 0.f;
+    float m = 0.f, s2 = 0.f;
 #pragma unroll
-    for (int e = 0; e < 8; ++e) m = abs_max(m, x[e]), s1 += fabsf(x[e]), s2 = fmaf(x[e], x[e], s2);
+    for (int e = 0; e < 8; ++e) m = abs_max(m, x[e]), s2 = fmaf(x[e], x[e], s2);
 #pragma unroll
     for (int o = 1; o < kLanes; o <<= 1) {
       m = abs_max(m, __shfl_xor_sync(0xffffffffu, m, o));
-      s1 += __shfl_xor_sync(0xffffffffu, s1, o);
       s2 += __shfl_xor_sync(0xffffffffu, s2, o);
     }
     const float sc = pow2_scale(m), r = l2norm ? 1.f / sqrtf(s2 + 1e-6f) : 1.f;
     uint32_t hi[4], lo[4];
 #pragma unroll
     for (int e = 0; e < 4; ++e) split2<P>(x[2 * e] * sc, x[2 * e + 1] * sc, hi[e], lo[e]);
-    const int at = img<true>(kC, row, cl * 8);
+    const int at = img(kC, row, cl * 8);
     *reinterpret_cast<uint4*>(image + at) = make_uint4(hi[0], hi[1], hi[2], hi[3]);
     if constexpr (P == 2) *reinterpret_cast<uint4*>(image + part + at) = make_uint4(lo[0], lo[1], lo[2], lo[3]);
-    if (cl == 0) inv[row] = pow2_inverse(sc) * r, rn[row] = r, mx[row] = m * r, sm[row] = s1 * r;
+    if (cl == 0) inv[row] = pow2_inverse(sc) * r, rn[row] = r;
   }
 }
 
@@ -133,10 +131,10 @@ __global__ void __launch_bounds__(kThreads, 4) prep_kernel(const Args a) {
   ChunkAt c;
   if (!chunk_at(a.s, slot, c)) return;
   const size_t at_k = (size_t)slot * a.s.Hk + hk;
-  load_rows<T, KP>(sm.q, sm.rows.qs, sm.rows.rq, sm.q_max, sm.q_sum,
+  load_rows<T, KP>(sm.q, sm.rows.qs, sm.rows.rq,
                    static_cast<const T*>(a.q) + c.b * a.s.q_b + c.t0 * a.s.q_t + hk * a.s.K, a.s.q_t, c.len, a.s.K,
                    a.s.l2norm, tid);
-  load_rows<T, KP>(sm.k, sm.rows.ks, sm.rows.rk, sm.k_max, sm.k_sum,
+  load_rows<T, KP>(sm.k, sm.rows.ks, sm.rows.rk,
                    static_cast<const T*>(a.k) + c.b * a.s.k_b + c.t0 * a.s.k_t + hk * a.s.K, a.s.k_t, c.len, a.s.K,
                    a.s.l2norm, tid);
   __syncthreads();
@@ -154,13 +152,13 @@ __global__ void __launch_bounds__(kThreads, 4) prep_kernel(const Args a) {
 #pragma unroll
   for (int kt = 0; kt < KP / 16; ++kt) {
     Frag<P> fq, fk;
-    a_mk<P, true>(fq, sm.q, kC, kC * KP, 16 * warp, 16 * kt, lane);
-    a_mk<P, true>(fk, sm.k, kC, kC * KP, 16 * warp, 16 * kt, lane);
+    a_mk<P>(fq, sm.q, kC, kC * KP, 16 * warp, 16 * kt, lane);
+    a_mk<P>(fk, sm.k, kC, kC * KP, 16 * warp, 16 * kt, lane);
 #pragma unroll
     for (int n = 0; n < 4; ++n)
       if (n <= warp) {
         Frag<P> fb;
-        b_nk<P, true>(fb, sm.k, kC, kC * KP, 16 * n, 16 * kt, lane);
+        b_nk<P>(fb, sm.k, kC, kC * KP, 16 * n, 16 * kt, lane);
         mma_parts<P, P>(qk[2 * n], qk[2 * n + 1], fq, fb);
         mma_parts<P, P>(kk[2 * n], kk[2 * n + 1], fk, fb);
       }
@@ -187,26 +185,17 @@ __global__ void __launch_bounds__(kThreads, 4) prep_kernel(const Args a) {
         if (lane >= o) s += y;
       }
       const double G[2] = {s - x[1], s}, Gc = __shfl_sync(0xffffffffu, s, 31);
-      float kr = 0.f, kw = 0.f, wk = 0.f, kb = 0.f, qsum = 0.f, ksum = 0.f, ek = 0.f, eq = 0.f;
 #pragma unroll
       for (int e = 0; e < 2; ++e) {
         const int i = 2 * lane + e;
         const float hi = (float)G[e], lo = (float)(G[e] - hi), th = (float)(Gc - G[e]), tl = (float)(Gc - G[e] - th);
         const float eg = expf(hi) * (1.f + lo), w = expf(th) * (1.f + tl) * sm.scal.beta[i];
-        sm.scal.gh[i] = hi, sm.scal.gl[i] = lo, sm.scal.eg[i] = eg, sm.scal.wr[i] = w;
-        const float sc = fabsf(a.s.scale) * eg, aw = fabsf(w);
-        kr = abs_max(kr, eg * sm.k_sum[i]), kw += aw * sm.k_max[i], wk = abs_max(wk, aw * sm.rows.ks[i]);
-        kb = abs_max(kb, aw * sm.k_sum[i]), qsum += sc * sm.q_max[i], ksum += eg * sm.k_max[i];
-        ek = abs_max(ek, eg * sm.rows.ks[i]), eq = abs_max(eq, sc * sm.rows.qs[i]);
+        sm.scal.gh[i] = hi, sm.scal.gl[i] = lo, sm.scal.eg[i] = eg;
+        sm.scal.ek[i] = eg * sm.rows.ks[i], sm.scal.wk[i] = w * sm.rows.ks[i], sm.scal.eq[i] = a.s.scale * eg * sm.rows.qs[i];
       }
-      kr = warp_max_abs(kr), wk = warp_max_abs(wk), kb = warp_max_abs(kb), ek = warp_max_abs(ek), eq = warp_max_abs(eq);
-      kw = wkv7::group_allreduce<32>(kw), qsum = wkv7::group_allreduce<32>(qsum), ksum = wkv7::group_allreduce<32>(ksum);
       if (lane == 31) {
         const float ch = (float)Gc, cl = (float)(Gc - ch);
-        Scal& o = sm.scal;
-        o.egc = expf(ch) * (1.f + cl);
-        o.k_read = kr, o.k_write = kw, o.wk_max = wk, o.k_back = kb, o.q_sum = qsum, o.k_sum = ksum, o.ek_max = ek;
-        o.eq_max = eq;
+        sm.scal.egc = expf(ch) * (1.f + cl);
       }
     }
     __syncthreads();
@@ -310,7 +299,6 @@ __global__ void __launch_bounds__(kThreads, 4) prep_kernel(const Args a) {
     }
     if (tid == 0) {
       sm.scal.inv_p = pow2_inverse(ps), sm.scal.inv_t = pow2_inverse(ts);
-      sm.scal.p_sum = kC * pm, sm.scal.t_sum = kC * tm;
     }
     __syncthreads();
     copy16(a.b.t_img + at_v * Layout::tp_img, sm.out, Layout::tp_img, tid);
