@@ -47,9 +47,8 @@ struct alignas(128) GradSmem {
   };
   Scal scal;
   Rows rows;
-  float fd[kC];             // f_i
-  float dot[5][KP / 32][kC];  // the row sums of 32 keys each
-  float red[KP / 8][4];
+  float fd[kC];               // f_i
+  float dot[4][KP / 32][kC];  // row sums of 32 keys each: q.dq, k.read, k.w, k.(e^(Gc - G) u dS1)
   float sdot[KP / 8];
   float dG[kC];
   uint64_t bar[kStages + 1];
@@ -116,7 +115,7 @@ __global__ void __launch_bounds__(kThreads<KP>, KP == 64 ? 2 : 1) grad_kernel(co
   const int key0 = wc * 32;
   float dq[kNt][4], rd[kNt][4], w[kNt][4], F[2 * kNf][4], E[2 * kNf][4];
   zero(dq), zero(rd), zero(w), zero(F), zero(E);
-  float sdot = 0.f;
+  float sdot = 0.f, du = 0.f, lu = 0.f;
   for (int v = 0; v < vts; ++v) {
     Tile<P, KP>& t = sm.tile[v % kStages];
     const size_t at = at_v * vts + v;
@@ -181,69 +180,71 @@ __global__ void __launch_bounds__(kThreads<KP>, KP == 64 ? 2 : 1) grad_kernel(co
       }
       sdot = fmaf(sd, su.x * dsl.x, sdot);
     }
-    __syncthreads();
-    if (tid == 0 && v + kStages < vts) load(v + kStages);
+    if (v + kStages < vts) {
+      __syncthreads();
+      if (tid == 0) load(v + kStages);
+    }
+    du += dsl.z * su.y, lu += dsl.y * su.y;
   }
   if (!mbar_wait_bounded(a.status, &sm.bar[kStages], 0)) return;
   const Scal& sc = sm.scal;
   const Rows& rows = sm.rows;
 
-  // F and E with their decays; the diagonal of F apart
-  float mx[4] = {0.f, 0.f, 0.f, 0.f};
+  // F and E with their decays and factors; the diagonal of F apart. Images hold
+  // magnitudes below 2^14, so |do.u| and |lam.u| are below 16 2^28 times the sum
+  // of their tiles' inverse scales: a bound for the scales, with no maximum to
+  // wait for (loose by some 2^6).
+  const float scale[4] = {pow2_scale(sc.fb_max * (du * 0x1p32f)), pow2_scale(sc.eb_max * (lu * 0x1p32f)),
+                          pow2_scale(sc.f_max * (du * 0x1p32f)), pow2_scale(sc.e_max * (lu * 0x1p32f))};
   const int i0 = 16 * wr + g4;
-#pragma unroll
-  for (int n = 0; n < 2 * kNf; ++n)
-#pragma unroll
-    for (int e = 0; e < 4; ++e) {
-      const int i = i0 + 8 * (e >> 1), j = 16 * kNf * wc + 8 * n + 2 * t4 + (e & 1);
-      if (j == i) sm.fd[i] = a.s.scale * F[n][e];
-      const float r = j < i ? expf((sc.gh[i] - sc.gh[j]) + (sc.gl[i] - sc.gl[j])) : 0.f;
-      F[n][e] = j < i ? a.s.scale * r * F[n][e] : 0.f;
-      E[n][e] = j < i ? r * E[n][e] : 0.f;
-      const float cb = sc.beta[j] * rows.ks[j];
-      mx[0] = abs_max(mx[0], F[n][e] * cb), mx[1] = abs_max(mx[1], E[n][e] * cb);
-      mx[2] = abs_max(mx[2], F[n][e] * rows.qs[i]), mx[3] = abs_max(mx[3], E[n][e] * rows.ks[i]);
-    }
-#pragma unroll
-  for (int m = 0; m < 4; ++m) {
-    mx[m] = warp_max_abs(mx[m]);
-    if (lane == 0) sm.red[warp][m] = mx[m];
-  }
   sdot = wkv7::group_allreduce<32>(sdot);
   if (lane == 0) sm.sdot[warp] = sdot;
-  __syncthreads();
-  float scale[4];
+  __syncthreads();  // the tiles are used up
+  const bool near = sc.near != 0.f;
 #pragma unroll
-  for (int m = 0; m < 4; ++m) {
-    float x = sm.red[0][m];
-#pragma unroll
-    for (int i = 1; i < KP / 8; ++i) x = abs_max(x, sm.red[i][m]);
-    scale[m] = pow2_scale(x);
-  }
-#pragma unroll
-  for (int n = 0; n < 2 * kNf; ++n)
+  for (int n = 0; n < 2 * kNf; ++n) {
+    const int jb = kNf * wc + n / 2;
+    if (jb > wr) continue;  // above the diagonal blocks
+    const int j = 16 * kNf * wc + 8 * n + 2 * t4;
+    const float c0 = sc.beta[j] * rows.ks[j], c1 = sc.beta[j + 1] * rows.ks[j + 1];
 #pragma unroll
     for (int h = 0; h < 2; ++h) {
-      if (kNf * wc + n / 2 > wr) continue;  // above the diagonal blocks
-      const int i = i0 + 8 * h, j = 16 * kNf * wc + 8 * n + 2 * t4;
-      const float c0 = sc.beta[j] * rows.ks[j], c1 = sc.beta[j + 1] * rows.ks[j + 1], x0 = F[n][2 * h], x1 = F[n][2 * h + 1],
-                  y0 = E[n][2 * h], y1 = E[n][2 * h + 1], rq = rows.qs[i], rk = rows.ks[i];
-      put2_tri(sm.pairs.fb, i, j, (x0 * c0) * scale[0], (x1 * c1) * scale[0]);
-      put2_tri(sm.pairs.eb, i, j, (y0 * c0) * scale[1], (y1 * c1) * scale[1]);
-      put2_tri(sm.pairs.f, i, j, (x0 * rq) * scale[2], (x1 * rq) * scale[2]);
-      put2_tri(sm.pairs.e, i, j, (y0 * rk) * scale[3], (y1 * rk) * scale[3]);
+      const int i = i0 + 8 * h;
+      float r0, r1;
+      if (near) {
+        r0 = sc.fa[i] * sc.fb[j], r1 = sc.fa[i] * sc.fb[j + 1];
+      } else {
+        r0 = j <= i ? expf((sc.gh[i] - sc.gh[j]) + (sc.gl[i] - sc.gl[j])) : 0.f;
+        r1 = j + 1 <= i ? expf((sc.gh[i] - sc.gh[j + 1]) + (sc.gl[i] - sc.gl[j + 1])) : 0.f;
+      }
+      float x0 = a.s.scale * r0 * F[n][2 * h], x1 = a.s.scale * r1 * F[n][2 * h + 1], y0 = r0 * E[n][2 * h], y1 = r1 * E[n][2 * h + 1];
+      if (jb == wr) {
+        if (j == i) sm.fd[i] = a.s.scale * F[n][2 * h];
+        if (j + 1 == i) sm.fd[i] = a.s.scale * F[n][2 * h + 1];
+        x0 = j < i ? x0 : 0.f, x1 = j + 1 < i ? x1 : 0.f, y0 = j < i ? y0 : 0.f, y1 = j + 1 < i ? y1 : 0.f;
+      }
+      const float q = rows.qs[i] * scale[2], k = rows.ks[i] * scale[3];
+      put2_tri(sm.pairs.fb, i, j, x0 * (c0 * scale[0]), x1 * (c1 * scale[0]));
+      put2_tri(sm.pairs.eb, i, j, y0 * (c0 * scale[1]), y1 * (c1 * scale[1]));
+      put2_tri(sm.pairs.f, i, j, x0 * q, x1 * q);
+      put2_tri(sm.pairs.e, i, j, y0 * k, y1 * k);
     }
+  }
   __syncthreads();
 
-  float ex[2];  // e^(Gc - G) of the thread's rows
+  // of the thread's two rows: e^(Gc - G), e^G, scale e^G, beta, f, f beta, qs, ks
+  float ex[2], eg[2], sg[2], beta[2], fdi[2], fb[2], qs[2], ks[2];
 #pragma unroll
   for (int h = 0; h < 2; ++h) {
     const int i = i0 + 8 * h;
     ex[h] = expf((sc.gh[kC - 1] - sc.gh[i]) + (sc.gl[kC - 1] - sc.gl[i]));
+    eg[h] = sc.eg[i], sg[h] = a.s.scale * eg[h], beta[h] = sc.beta[i], fdi[h] = sm.fd[i], fb[h] = fdi[h] * beta[h];
+    qs[h] = rows.qs[i], ks[h] = rows.ks[i];
   }
-  float dot[5][2];  // q.dq, k.read, k.w, beta k.(e^(Gc - G) u dS1), q.k
+  const float inv[4] = {pow2_inverse(scale[0]), pow2_inverse(scale[1]), pow2_inverse(scale[2]), pow2_inverse(scale[3])};
+  float dot[4][2];
 #pragma unroll
-  for (int m = 0; m < 5; ++m) dot[m][0] = dot[m][1] = 0.f;
+  for (int m = 0; m < 4; ++m) dot[m][0] = dot[m][1] = 0.f;
 #pragma unroll
   for (int nt = 0; nt < kNt; nt += 2) {
     float x[2][4], y[2][4], z[2][4], q[2][4];
@@ -275,26 +276,25 @@ __global__ void __launch_bounds__(kThreads<KP>, KP == 64 ? 2 : 1) grad_kernel(co
       for (int h = 0; h < 2; ++h) {
         const int i = i0 + 8 * h, col = key0 + 8 * (nt + b) + 2 * t4;
         const float2 qh = pick2<P, KP>(sm.q, i, col), kh = pick2<P, KP>(sm.k, i, col);
-        const float qq[2] = {qh.x * rows.qs[i], qh.y * rows.qs[i]}, kk[2] = {kh.x * rows.ks[i], kh.y * rows.ks[i]};
+        const float qq[2] = {qh.x * qs[h], qh.y * qs[h]}, kk[2] = {kh.x * ks[h], kh.y * ks[h]};
 #pragma unroll
         for (int e = 0; e < 2; ++e) {
           const int at = 2 * h + e;
-          const float s = a.s.scale * sc.eg[i] * dq[nt + b][at], tail = ex[h] * w[nt + b][at];
-          const float d = fmaf(x[b][at], pow2_inverse(scale[0]), s);
-          const float r = -fmaf(y[b][at], pow2_inverse(scale[1]), sc.eg[i] * rd[nt + b][at]);
-          const float ww = fmaf(q[b][at], pow2_inverse(scale[2]), fmaf(-z[b][at], pow2_inverse(scale[3]), tail));
+          const float tail = ex[h] * w[nt + b][at];
+          const float d = fmaf(x[b][at], inv[0], sg[h] * dq[nt + b][at]);
+          const float r = fmaf(y[b][at], -inv[1], -eg[h] * rd[nt + b][at]);
+          const float ww = fmaf(q[b][at], inv[2], fmaf(z[b][at], -inv[3], tail));
           dot[0][h] = fmaf(qq[e], d, dot[0][h]);
           dot[1][h] = fmaf(kk[e], r, dot[1][h]);
           dot[2][h] = fmaf(kk[e], ww, dot[2][h]);
           dot[3][h] = fmaf(kk[e], tail, dot[3][h]);
-          dot[4][h] = fmaf(qq[e], kk[e], dot[4][h]);
-          dq[nt + b][at] = fmaf(sm.fd[i] * sc.beta[i], kk[e], d);
-          rd[nt + b][at] = fmaf(sc.beta[i], fmaf(sm.fd[i], qq[e], ww), r);  // dk
+          dq[nt + b][at] = fmaf(fb[h], kk[e], d);
+          rd[nt + b][at] = fmaf(beta[h], fmaf(fdi[h], qq[e], ww), r);  // dk
         }
       }
   }
 #pragma unroll
-  for (int m = 0; m < 5; ++m)
+  for (int m = 0; m < 4; ++m)
 #pragma unroll
     for (int h = 0; h < 2; ++h) {
       float x = wkv7::group_allreduce<4>(dot[m][h]);
@@ -304,10 +304,9 @@ __global__ void __launch_bounds__(kThreads<KP>, KP == 64 ? 2 : 1) grad_kernel(co
   const size_t tok = (size_t)c.b * a.s.T + c.t0;
   if (tid < kC) {
     const int i = tid;
-    const float b = sc.beta[i], qd = row_sum(sm.dot[0], i), kr = row_sum(sm.dot[1], i), kw = row_sum(sm.dot[2], i),
-                qk = row_sum(sm.dot[4], i);
+    const float b = sc.beta[i], qd = row_sum(sm.dot[0], i), kr = row_sum(sm.dot[1], i), kw = row_sum(sm.dot[2], i);
     sm.dG[i] = qd + kr - b * kw;
-    if (i < c.len) a.dbeta[(tok + i) * a.s.Hv + hv] = fmaf(sm.fd[i], qk, kw);
+    if (i < c.len) a.dbeta[(tok + i) * a.s.Hv + hv] = fmaf(sm.fd[i], rows.qk[i], kw);
   }
   __syncthreads();
   if (warp == 0) {  // dg: the suffix sums, two tokens a lane
@@ -335,7 +334,7 @@ __global__ void __launch_bounds__(kThreads<KP>, KP == 64 ? 2 : 1) grad_kernel(co
     float nq = 0.f, nk = 0.f;  // q.dq and k.dk of the whole row
     const bool norm = !kShared && a.s.l2norm;
     if (norm) {
-      const float b = sc.beta[i], f = sm.fd[i], qk = row_sum(sm.dot[4], i);
+      const float b = sc.beta[i], f = sm.fd[i], qk = rows.qk[i];
       nq = fmaf(f * b, qk, row_sum(sm.dot[0], i));
       nk = fmaf(b, fmaf(f, qk, row_sum(sm.dot[2], i)), row_sum(sm.dot[1], i));
     }

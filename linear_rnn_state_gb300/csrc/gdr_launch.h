@@ -38,6 +38,7 @@ inline int v_tiles(int V) { return (V + kVt - 1) / kVt; }
 struct Rows {        // of the 64 tokens, the actual q is qs * image (and k is ks * image)
   float qs[kC], ks[kC];
   float rq[kC], rk[kC];  // 1 / |q|, 1 / |k| with l2norm, else 1
+  float qk[kC];          // q.k
 };
 struct Scal {
   // with G the running sum of g in the chunk and Gc its whole sum:
@@ -46,12 +47,17 @@ struct Scal {
   float eq[kC];  // scale e^G qs
   float inv_t, inv_p;  // the inverse scales of the T and P images
   float egc;           // e^Gc
-  float pad[29];
+  float near;          // 1: G spans at most kNear in the chunk, and fa, fb hold
+  float f_max, e_max;  // bounds of |F|, |E| and their factors over |do.u|, |lam.u| (gdr_grad.cu)
+  float fb_max, eb_max;
+  float pad[24];
   // up to here for the chains, from here on for the gradients
   float eg[kC];          // e^G
   float gh[kC], gl[kC];  // G as an unrounded sum of two floats
+  float fa[kC], fb[kC];  // e^(G - m), e^(m - G), m the middle of G's range: e^(G_i - G_j) = fa_i fb_j
   float beta[kC];
 };
+constexpr float kNear = 60.f;  // e^+-30 leaves the products of fa, fb and any factors far from overflow
 constexpr size_t kChainScal = 3 * kC * sizeof(float) + 128;
 static_assert(sizeof(Scal) % 128 == 0 && sizeof(Rows) % 128 == 0, "bulk copies");
 

@@ -9,11 +9,12 @@
 // the chain kernels copy into shared memory, with their scales and the tokens'
 // factors (gdr_launch.h, Rows and Scal).
 //
-// The decay ratios. G is summed in double and kept as two floats, and r_ij is
-// the exponential of a difference, never a product of e^G_i with e^-G_j, so
-// that strong decays neither overflow nor lose the small differences. g below
-// -200 counts as -200 (e^-200 is 0 in fp32 either way), which makes -inf a
-// reset of the state instead of inf - inf.
+// The decay ratios. G is summed in double and kept as two floats, so that no
+// difference of it is rounded. g below -200 counts as -200 (e^-200 is 0 in fp32
+// either way), which makes -inf a reset of the state instead of inf - inf.
+// Where G spans at most 60 in the chunk, r_ij is the product of a row's and a
+// column's factor, two multiplications an element; elsewhere it is the
+// exponential of the difference, which strong decays cannot overflow.
 //
 // T in fp32: the four diagonal 16 x 16 blocks by forward substitution, a column
 // a thread, then blocks joined two by two, [T1 0; -T2 L21 T1 T2], 16 and then
@@ -31,49 +32,85 @@ template <typename T, int KP>
 struct alignas(128) PrepSmem {
   static constexpr int P = In<T>::kParts;
   __half q[P * kC * KP], k[P * kC * KP];
-  float L[kC * kLd];  // L, and then T in its place
-  union {
-    __half out[2 * kTriPart];  // the image of P, then of T
-    float x[32 * kLx];         // L21 T1 in between
-  };
+  float L[kC * kLd];            // L, and then T in its place
+  float x[32 * kLx];            // L21 T1 in between
+  __half out[2 * kTriPart];     // the image of P, then of T
   Rows rows;
   Scal scal;
+  float pa[kC], la[kC], cb[kC];  // scale qs fa, ks fa, beta ks fb: P_ij = (q_i.k_j) pa_i cb_j where G is near
   float red[8];
 };
 
-__device__ __forceinline__ void copy16(void* dst, const void* src, int bytes, int tid) {
-  for (int i = tid; i < bytes / 16; i += kThreads)
-    reinterpret_cast<uint4*>(dst)[i] = reinterpret_cast<const uint4*>(src)[i];
-}
-
-// One of q, k: 64 rows into an image, each row scaled by a power of two.
+// One of q, k: 64 rows into an image, each row scaled by a power of two. A lane
+// has eight columns of every kPass-th row; all its loads are issued at once.
 template <typename T, int KP>
-__device__ __forceinline__ void load_rows(__half* image, float* inv, float* rn, const T* src, long long stride_t, int len,
-                                          int K, int l2norm, int tid) {
-  constexpr int P = In<T>::kParts, kLanes = KP / 8, kPass = kThreads / kLanes;
-  const int cl = tid % kLanes, part = kC * KP;
-#pragma unroll 2
-  for (int row = tid / kLanes; row < kC; row += kPass) {
-    float x[8] = {0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f};
-    if (row < len && cl * 8 < K) load8(x, src + (size_t)row * stride_t + cl * 8);
-    float m = 0.f, s2 = 0.f;
+struct RowLoader {
+  static constexpr int P = In<T>::kParts, kLanes = KP / 8, kPass = kThreads / kLanes, kOwn = kC / kPass;
+  uint4 raw[kOwn][P];
+  __device__ __forceinline__ void load(const T* src, long long stride_t, int len, int K, int tid) {
+    const int cl = tid % kLanes;
 #pragma unroll
-    for (int e = 0; e < 8; ++e) m = abs_max(m, x[e]), s2 = fmaf(x[e], x[e], s2);
+    for (int i = 0; i < kOwn; ++i) {
+      const int row = tid / kLanes + i * kPass;
+      const bool in = row < len && cl * 8 < K;
 #pragma unroll
-    for (int o = 1; o < kLanes; o <<= 1) {
-      m = abs_max(m, __shfl_xor_sync(0xffffffffu, m, o));
-      s2 += __shfl_xor_sync(0xffffffffu, s2, o);
+      for (int p = 0; p < P; ++p)
+        raw[i][p] = in ? reinterpret_cast<const uint4*>(src + (size_t)row * stride_t + cl * 8)[p] : make_uint4(0, 0, 0, 0);
     }
-    const float sc = pow2_scale(m), r = l2norm ? 1.f / sqrtf(s2 + 1e-6f) : 1.f;
-    uint32_t hi[4], lo[4];
-#pragma unroll
-    for (int e = 0; e < 4; ++e) split2<P>(x[2 * e] * sc, x[2 * e + 1] * sc, hi[e], lo[e]);
-    const int at = img(kC, row, cl * 8);
-    *reinterpret_cast<uint4*>(image + at) = make_uint4(hi[0], hi[1], hi[2], hi[3]);
-    if constexpr (P == 2) *reinterpret_cast<uint4*>(image + part + at) = make_uint4(lo[0], lo[1], lo[2], lo[3]);
-    if (cl == 0) inv[row] = pow2_inverse(sc) * r, rn[row] = r;
   }
-}
+  __device__ __forceinline__ void values(float (&x)[8], int i) const {
+#pragma unroll
+    for (int p = 0; p < P; ++p) {
+      const uint32_t w[4] = {raw[i][p].x, raw[i][p].y, raw[i][p].z, raw[i][p].w};
+#pragma unroll
+      for (int e = 0; e < 4; ++e)
+        if constexpr (P == 1)
+          x[2 * e] = __uint_as_float(w[e] << 16), x[2 * e + 1] = __uint_as_float(w[e] & 0xFFFF0000u);
+        else
+          x[4 * p + e] = __uint_as_float(w[e]);
+    }
+  }
+  // The row's largest magnitude, over its lanes.
+  __device__ __forceinline__ float largest(int i) const {
+    uint32_t m = 0, lo = 0;
+#pragma unroll
+    for (int p = 0; p < P; ++p) {
+      const uint32_t w[4] = {raw[i][p].x, raw[i][p].y, raw[i][p].z, raw[i][p].w};
+#pragma unroll
+      for (int e = 0; e < 4; ++e) {
+        m = max(m, w[e] & 0x7FFFFFFFu);  // magnitudes are ordered as their bits
+        if constexpr (P == 1) lo = max(lo, (w[e] << 16) & 0x7FFFFFFFu);
+      }
+    }
+    if constexpr (P == 1) m = max(m & 0xFFFF0000u, lo);
+#pragma unroll
+    for (int o = 1; o < kLanes; o <<= 1) m = max(m, __shfl_xor_sync(0xffffffffu, m, o));
+    return __uint_as_float(m);
+  }
+  __device__ __forceinline__ void store(__half* image, float* inv, float* rn, int l2norm, int tid) const {
+    const int cl = tid % kLanes;
+#pragma unroll
+    for (int i = 0; i < kOwn; ++i) {
+      const int row = tid / kLanes + i * kPass;
+      const float sc = pow2_scale(largest(i));
+      float x[8], r = 1.f;
+      values(x, i);
+      if (l2norm) {
+        float s2 = 0.f;
+#pragma unroll
+        for (int e = 0; e < 8; ++e) s2 = fmaf(x[e], x[e], s2);
+        r = 1.f / sqrtf(wkv7::group_allreduce<kLanes>(s2) + 1e-6f);
+      }
+      uint32_t hi[4], lo[4];
+#pragma unroll
+      for (int e = 0; e < 4; ++e) split2<P>(x[2 * e] * sc, x[2 * e + 1] * sc, hi[e], lo[e]);
+      const int at = img(kC, row, cl * 8);
+      *reinterpret_cast<uint4*>(image + at) = make_uint4(hi[0], hi[1], hi[2], hi[3]);
+      if constexpr (P == 2) *reinterpret_cast<uint4*>(image + kC * KP + at) = make_uint4(lo[0], lo[1], lo[2], lo[3]);
+      if (cl == 0) inv[row] = pow2_inverse(sc) * r, rn[row] = r;
+    }
+  }
+};
 
 // Largest of the block's values; every thread gets it. `red` is reused: a
 // barrier stands before and after.
@@ -131,17 +168,36 @@ __global__ void __launch_bounds__(kThreads, 4) prep_kernel(const Args a) {
   ChunkAt c;
   if (!chunk_at(a.s, slot, c)) return;
   const size_t at_k = (size_t)slot * a.s.Hk + hk;
-  load_rows<T, KP>(sm.q, sm.rows.qs, sm.rows.rq,
-                   static_cast<const T*>(a.q) + c.b * a.s.q_b + c.t0 * a.s.q_t + hk * a.s.K, a.s.q_t, c.len, a.s.K,
-                   a.s.l2norm, tid);
-  load_rows<T, KP>(sm.k, sm.rows.ks, sm.rows.rk,
-                   static_cast<const T*>(a.k) + c.b * a.s.k_b + c.t0 * a.s.k_t + hk * a.s.K, a.s.k_t, c.len, a.s.K,
-                   a.s.l2norm, tid);
+  const int g4 = lane >> 2, t4 = lane & 3, group = a.s.Hv / a.s.Hk;
+  float gin[2] = {0.f, 0.f}, bin[2] = {0.f, 0.f};  // warp 0: g and beta of tokens 2 lane, 2 lane + 1
+  auto load_gates = [&](int hv) {
+    if (warp == 0)
+#pragma unroll
+      for (int e = 0; e < 2; ++e)
+        if (2 * lane + e < c.len) {
+          const size_t at = ((size_t)c.b * a.s.T + c.t0 + 2 * lane + e) * a.s.Hv + hv;
+          gin[e] = a.g[at], bin[e] = a.beta[at];
+        }
+  };
+  load_gates(hk * group);
+  {
+    const T* q = static_cast<const T*>(a.q) + c.b * a.s.q_b + c.t0 * a.s.q_t + hk * a.s.K;
+    const T* k = static_cast<const T*>(a.k) + c.b * a.s.k_b + c.t0 * a.s.k_t + hk * a.s.K;
+    RowLoader<T, KP> lq, lk;
+    lq.load(q, a.s.q_t, c.len, a.s.K, tid);
+    if (P == 1) lk.load(k, a.s.k_t, c.len, a.s.K, tid);  // fp32 rows are too many registers for both at once
+    lq.store(sm.q, sm.rows.qs, sm.rows.rq, a.s.l2norm, tid);
+    if (P == 2) lk.load(k, a.s.k_t, c.len, a.s.K, tid);
+    lk.store(sm.k, sm.rows.ks, sm.rows.rk, a.s.l2norm, tid);
+  }
+  wkv7::fence_proxy_async_smem();
   __syncthreads();
-  const int image = P * kC * KP * 2;
-  copy16(a.b.q_img + at_k * image, sm.q, image, tid);
-  copy16(a.b.k_img + at_k * image, sm.k, image, tid);
-  copy16(a.b.rows + at_k, &sm.rows, sizeof(Rows), tid);
+  constexpr int image = P * kC * KP * 2;
+  if (tid == 0) {
+    bulk_store(a.b.q_img + at_k * image, sm.q, image);
+    bulk_store(a.b.k_img + at_k * image, sm.k, image);
+    bulk_commit();
+  }
 
   // q k^T and k k^T, the 16 rows of a warp against the columns up to them
   float qk[8][4], kk[8][4];
@@ -164,20 +220,18 @@ __global__ void __launch_bounds__(kThreads, 4) prep_kernel(const Args a) {
       }
   }
 
-  const int g4 = lane >> 2, t4 = lane & 3, group = a.s.Hv / a.s.Hk;
+#pragma unroll
+  for (int n = 0; n < 8; ++n)
+#pragma unroll
+    for (int e = 0; e < 4; ++e) {
+      const int i = 16 * warp + g4 + 8 * (e >> 1);
+      if (8 * n + 2 * t4 + (e & 1) == i) sm.rows.qk[i] = qk[n][e] * sm.rows.qs[i] * sm.rows.ks[i];
+    }
   for (int hg = 0; hg < group; ++hg) {
     const int hv = hk * group + hg;
     const size_t at_v = (size_t)slot * a.s.Hv + hv;
     if (warp == 0) {  // the running sum of g, two tokens a lane
-      const size_t gat = ((size_t)c.b * a.s.T + c.t0) * a.s.Hv + hv;
-      double x[2];
-#pragma unroll
-      for (int e = 0; e < 2; ++e) {
-        const int i = 2 * lane + e;
-        const float gi = i < c.len ? a.g[gat + (size_t)i * a.s.Hv] : 0.f;
-        x[e] = gi < -200.f ? -200.f : gi;
-        sm.scal.beta[i] = i < c.len ? a.beta[gat + (size_t)i * a.s.Hv] : 0.f;
-      }
+      const double x[2] = {gin[0] < -200.f ? -200.f : gin[0], gin[1] < -200.f ? -200.f : gin[1]};
       double s = x[0] + x[1];
 #pragma unroll
       for (int o = 1; o < 32; o <<= 1) {
@@ -185,38 +239,75 @@ __global__ void __launch_bounds__(kThreads, 4) prep_kernel(const Args a) {
         if (lane >= o) s += y;
       }
       const double G[2] = {s - x[1], s}, Gc = __shfl_sync(0xffffffffu, s, 31);
+      float top = fmaxf((float)G[0], (float)G[1]), low = fminf((float)G[0], (float)G[1]);
+#pragma unroll
+      for (int o = 1; o < 32; o <<= 1) {
+        top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, o));
+        low = fminf(low, __shfl_xor_sync(0xffffffffu, low, o));
+      }
+      const float mid = 0.5f * (top + low);
+      float bk = 0.f, qm = 0.f, km = 0.f;
 #pragma unroll
       for (int e = 0; e < 2; ++e) {
         const int i = 2 * lane + e;
-        const float hi = (float)G[e], lo = (float)(G[e] - hi), th = (float)(Gc - G[e]), tl = (float)(Gc - G[e] - th);
-        const float eg = expf(hi) * (1.f + lo), w = expf(th) * (1.f + tl) * sm.scal.beta[i];
-        sm.scal.gh[i] = hi, sm.scal.gl[i] = lo, sm.scal.eg[i] = eg;
-        sm.scal.ek[i] = eg * sm.rows.ks[i], sm.scal.wk[i] = w * sm.rows.ks[i], sm.scal.eq[i] = a.s.scale * eg * sm.rows.qs[i];
+        const float b = bin[e], hi = (float)G[e], lo = (float)(G[e] - hi), th = (float)(Gc - G[e]), tl = (float)(Gc - G[e] - th);
+        const float mh = (float)(G[e] - mid), ml = (float)(G[e] - mid - mh);
+        const float eg = expf(hi) * (1.f + lo), w = expf(th) * (1.f + tl) * b, fa = expf(mh) * (1.f + ml), fb = expf(-mh) * (1.f - ml);
+        const float qs = sm.rows.qs[i], ks = sm.rows.ks[i];
+        Scal& o = sm.scal;
+        o.beta[i] = b, o.gh[i] = hi, o.gl[i] = lo, o.eg[i] = eg, o.fa[i] = fa, o.fb[i] = fb;
+        o.ek[i] = eg * ks, o.wk[i] = w * ks, o.eq[i] = a.s.scale * eg * qs;
+        sm.pa[i] = a.s.scale * qs * fa, sm.la[i] = ks * fa, sm.cb[i] = b * ks * fb;
+        bk = abs_max(bk, b * ks), qm = abs_max(qm, qs), km = abs_max(km, ks);
       }
+      bk = warp_max_abs(bk), qm = warp_max_abs(qm), km = warp_max_abs(km);
+      // the largest e^(G_i - G_j), j <= i, is 1 unless some g is positive
+      const bool grows = __any_sync(0xffffffffu, x[0] > 0 || x[1] > 0);
       if (lane == 31) {
-        const float ch = (float)Gc, cl = (float)(Gc - ch);
-        sm.scal.egc = expf(ch) * (1.f + cl);
+        const float ch = (float)Gc, cl = (float)(Gc - ch), r = grows ? expf(top - low) : 1.f, sr = fabsf(a.s.scale) * r;
+        Scal& o = sm.scal;
+        o.egc = expf(ch) * (1.f + cl);
+        o.near = top - low <= kNear ? 1.f : 0.f;
+        o.fb_max = sr * bk, o.eb_max = r * bk, o.f_max = sr * qm, o.e_max = r * km;
       }
     }
     __syncthreads();
+    if (hg + 1 < group) load_gates(hv + 1);
     float p[8][4], pm = 0.f;
+    if (sm.scal.near != 0.f) {
 #pragma unroll
-    for (int n = 0; n < 8; ++n)
-      if (n < 2 * warp + 2) {
+      for (int n = 0; n < 8; ++n)
+        if (n < 2 * warp + 2) {
+          const float2 cb = *reinterpret_cast<const float2*>(sm.cb + 8 * n + 2 * t4);
 #pragma unroll
-        for (int e = 0; e < 4; ++e) {
-          const int i = 16 * warp + g4 + 8 * (e >> 1), j = 8 * n + 2 * t4 + (e & 1);
-          float r = 0.f;
-          if (j <= i) r = expf((sm.scal.gh[i] - sm.scal.gh[j]) + (sm.scal.gl[i] - sm.scal.gl[j])) * sm.rows.ks[j];
-          const float rb = r * sm.scal.beta[j];
-          p[n][e] = j <= i ? a.s.scale * (sm.rows.qs[i] * qk[n][e]) * rb : 0.f;
-          pm = abs_max(pm, p[n][e]);
-          sm.L[i * kLd + j] = j < i ? sm.rows.ks[i] * kk[n][e] * rb : 0.f;
+          for (int h = 0; h < 2; ++h) {
+            const int i = 16 * warp + g4 + 8 * h, j = 8 * n + 2 * t4;
+            const float pa = sm.pa[i], la = sm.la[i];
+            float x0 = qk[n][2 * h] * pa * cb.x, x1 = qk[n][2 * h + 1] * pa * cb.y;
+            float y0 = kk[n][2 * h] * la * cb.x, y1 = kk[n][2 * h + 1] * la * cb.y;
+            if (n >= 2 * warp) {  // the diagonal block
+              x0 = j <= i ? x0 : 0.f, x1 = j + 1 <= i ? x1 : 0.f;
+              y0 = j < i ? y0 : 0.f, y1 = j + 1 < i ? y1 : 0.f;
+            }
+            p[n][2 * h] = x0, p[n][2 * h + 1] = x1;
+            pm = abs_max(abs_max(pm, x0), x1);
+            *reinterpret_cast<float2*>(sm.L + i * kLd + j) = make_float2(y0, y1);
+          }
         }
-      } else {
+    } else {
 #pragma unroll
-        for (int e = 0; e < 4; ++e) p[n][e] = 0.f;
-      }
+      for (int n = 0; n < 8; ++n)
+        if (n < 2 * warp + 2)
+#pragma unroll
+          for (int e = 0; e < 4; ++e) {
+            const int i = 16 * warp + g4 + 8 * (e >> 1), j = 8 * n + 2 * t4 + (e & 1);
+            float r = 0.f;
+            if (j <= i) r = expf((sm.scal.gh[i] - sm.scal.gh[j]) + (sm.scal.gl[i] - sm.scal.gl[j])) * (sm.scal.beta[j] * sm.rows.ks[j]);
+            p[n][e] = j <= i ? a.s.scale * (sm.rows.qs[i] * qk[n][e]) * r : 0.f;
+            pm = abs_max(pm, p[n][e]);
+            sm.L[i * kLd + j] = j < i ? sm.rows.ks[i] * kk[n][e] * r : 0.f;
+          }
+    }
     pm = block_max(pm, sm.red, tid);
     const float ps = pow2_scale(pm);
 #pragma unroll
@@ -225,8 +316,12 @@ __global__ void __launch_bounds__(kThreads, 4) prep_kernel(const Args a) {
 #pragma unroll
         for (int h = 0; h < 2; ++h)
           put2_tri(sm.out, 16 * warp + g4 + 8 * h, 8 * n + 2 * t4, p[n][2 * h] * ps, p[n][2 * h + 1] * ps);
+    wkv7::fence_proxy_async_smem();
     __syncthreads();
-    copy16(a.b.p_img + at_v * Layout::tp_img, sm.out, Layout::tp_img, tid);
+    if (tid == 0) {
+      bulk_store(a.b.p_img + at_v * Layout::tp_img, sm.out, Layout::tp_img);
+      bulk_commit();
+    }
 
     // T in the place of L: diagonal blocks, then the blocks left of them
     if (tid < kC) {
@@ -290,6 +385,7 @@ __global__ void __launch_bounds__(kThreads, 4) prep_kernel(const Args a) {
       tv[b] = *reinterpret_cast<const float2*>(sm.L + (16 * ib + (tid >> 3)) * kLd + 16 * jb + 2 * (tid & 7));
       tm = abs_max(abs_max(tm, tv[b].x), tv[b].y);
     }
+    if (tid == 0) bulk_wait_read();  // P is out
     tm = block_max(tm, sm.red, tid);
     const float ts = pow2_scale(tm);
 #pragma unroll
@@ -300,11 +396,18 @@ __global__ void __launch_bounds__(kThreads, 4) prep_kernel(const Args a) {
     if (tid == 0) {
       sm.scal.inv_p = pow2_inverse(ps), sm.scal.inv_t = pow2_inverse(ts);
     }
+    wkv7::fence_proxy_async_smem();
     __syncthreads();
-    copy16(a.b.t_img + at_v * Layout::tp_img, sm.out, Layout::tp_img, tid);
-    copy16(a.b.scal + at_v, &sm.scal, sizeof(Scal), tid);
-    __syncthreads();
+    if (tid == 0) {
+      bulk_store(a.b.t_img + at_v * Layout::tp_img, sm.out, Layout::tp_img);
+      bulk_store(a.b.scal + at_v, &sm.scal, sizeof(Scal));
+      if (hg == 0) bulk_store(a.b.rows + at_k, &sm.rows, sizeof(Rows));
+      bulk_commit();
+      bulk_wait_read();  // T and the scalars are out
+    }
+    if (hg + 1 < group) __syncthreads();
   }
+  if (tid == 0) bulk_wait_all();
 }
 
 template <typename T, int KP>
