@@ -3,219 +3,299 @@
 //
 // For the 16 rows of the state that a warp owns (gdr_chain.cuh), with the
 // images of q, k, T and P that the forward used, all transposed:
-//   y^T   = do^T P + wk (dS1 k^T)              (the gradient of u)
+//   y^T   = do^T P (helper) + wk (dS1 k^T)          the gradient of u
 //   lam^T = y^T T = dv^T
-//   dS0   = e^Gc dS1 + (scale e^G do)^T q - (e^G lam)^T k
-// It leaves the images of dS1, lam and do for the gradients of q, k, g and beta
-// (gdr_grad.cu). fp16 pairs throughout: dS, lam and do enter fp32 results.
-//
-// Bound, as the forward, by the tensor pipe: 292 mma of 8 cycles a step, warp
-// and scheduler at 64 keys (bfloat16).
+//   dS0   = e^Gc dS1 + (scale e^G do)^T q (helper) - (e^G lam)^T k
+// The helper's two products do not wait for the chain: it makes them a step
+// ahead. It leaves the images of dS1, lam and do for the gradients of q, k, g
+// and beta (gdr_grad.cu). fp16 pairs throughout: dS, lam and do enter fp32
+// results.
 #include "gdr_chain.cuh"
 
 namespace gdr {
 namespace {
 
+// What a chain and its helper share.
 template <typename T, int KP>
-struct alignas(128) BwdWarp {
-  unsigned char rows[2][kRowsBytes<T>];  // do of this and the next chunk; then dv
-  __half s[2 * kVt * KP], l[2 * kVt * kC], d[In<T>::kParts * kVt * kC];  // images on their way out
+struct alignas(128) BwdPair {
+  unsigned char d[2][kRowsBytes<T>], dv[kRowsBytes<T>];
+  __half s[2 * kVt * KP], l[2 * kVt * kC], d_img[In<T>::kParts * kVt * kC];  // images of dS1, lam, do
+  float4 y[8 * 32], g[KP / 8 * 32];  // do^T P and (scale e^G do)^T q, as accumulator tiles
+  float inv_s, inv_l;
+  uint64_t full_s, full_l, full_y, full_g, free_s, free_l, free_y, free_g;
 };
+// fp32 images of 128 keys leave room for two
+template <typename T, int KP>
+constexpr int kBwdChains = sizeof(T) * KP <= 256 ? 4 : 2;
 template <typename T, int KP>
 struct BwdSmem {
   Images<In<T>::kParts, KP, 2> im;
-  BwdWarp<T, KP> w[kMaxWarps];
+  BwdPair<T, KP> pair[kBwdChains<T, KP>];
 };
 
 template <typename T, int KP>
-__global__ void __launch_bounds__((kMaxWarps + 1) * 32, sizeof(BwdSmem<T, KP>) <= 113 * 1024 ? 2 : 1) bwd_kernel(const Args a) {
+__global__ void __launch_bounds__((2 * kBwdChains<T, KP> + 1) * 32, 1) bwd_kernel(const Args a) {
   extern __shared__ __align__(128) unsigned char raw[];
-  using Smem = BwdSmem<T, KP>;
   constexpr int P = In<T>::kParts, kNt = KP / 8;
-  Smem& sm = *reinterpret_cast<Smem*>(raw);
-  const int warps = blockDim.x / 32 - 1, warp = threadIdx.x >> 5, lane = threadIdx.x & 31, t4 = lane & 3;
-  const int vts = (a.s.V + kVt - 1) / kVt, sets = (vts + warps - 1) / warps;
+  BwdSmem<T, KP>& sm = *reinterpret_cast<BwdSmem<T, KP>*>(raw);
+  const int chains = blockDim.x / 64, warp = threadIdx.x >> 5, lane = threadIdx.x & 31, t4 = lane & 3;
+  const int vts = (a.s.V + kVt - 1) / kVt, sets = (vts + chains - 1) / chains;
   const int set = blockIdx.x % sets, hv = blockIdx.x / sets % a.s.Hv, seq = blockIdx.x / (sets * a.s.Hv);
   const int hk = hv / (a.s.Hv / a.s.Hk);
   const SeqRange sq = seq_range(a.s, seq);
   const int n = (sq.t1 - sq.t0 + kC - 1) / kC;
   const int K = a.s.K, V = a.s.V;
   auto& im = sm.im;
-  if (threadIdx.x == 0) init_images(im, min(warps, vts - set * warps));
+  if (threadIdx.x == 0) {
+    init_images(im, min(chains, vts - set * chains));
+    for (int i = 0; i < chains; ++i) {
+      BwdPair<T, KP>& p = sm.pair[i];
+      for (uint64_t* b : {&p.full_s, &p.full_l, &p.full_y, &p.full_g, &p.free_s, &p.free_l, &p.free_y, &p.free_g}) mbar_init(b, 1);
+    }
+    wkv7::fence_mbar_init();
+  }
   __syncthreads();
-  if (warp == warps) {
+  if (warp == 2 * chains) {
     if (lane == 0) fill_images(im, a, sq.slot + n - 1, -1, n, hk, hv);
     return;
   }
-  const int vt = set * warps + warp;
+  const int own = warp % chains, vt = set * chains + own;
   if (vt >= vts) return;
-  BwdWarp<T, KP>& mine = sm.w[warp];
-  const int cols = V - vt * kVt;
-  const size_t state_at = (((size_t)seq * a.s.Hv + hv) * V + vt * kVt) * K;
+  BwdPair<T, KP>& pr = sm.pair[own];
+  const int cols = V - vt * kVt, tokens = sq.t1 - sq.t0;
+
+  // step s works on chunk n - 1 - s
+  if (warp < chains) {  // ------------------------------------------------ chain
+    const size_t state_at = (((size_t)seq * a.s.Hv + hv) * V + vt * kVt) * K;
+    float S[kNt][4];
+    load_state(S, a.dS_final ? a.dS_final + state_at : nullptr, cols, K, lane);
+    float s_max = warp_max(S);
+    for (int s = 0; s < n; ++s) {
+      const int use = s & 1;
+      const Scal& sc = im.sc(use);
+      const float sS = pow2_scale(s_max), inv_s = pow2_inverse(sS);
+      // dS1 k^T
+      float x[8][4];
+      zero(x);
+      if (!mbar_wait_bounded(a.status, &im.full_k[use], (s >> 1) & 1)) return;
+      if (s > 0 && !mbar_wait_bounded(a.status, &pr.free_s, use ^ 1)) return;
+#pragma unroll
+      for (int kt = 0; kt < KP / 16; ++kt) {
+        Frag<2> fs;
+        to_a(fs, S[2 * kt], S[2 * kt + 1], sS);
+        put_a(pr.s, kVt * KP, 16 * kt, fs, lane);
+        Frag<P> fk[4];
+#pragma unroll
+        for (int nb = 0; nb < 4; ++nb) b_nk<P>(fk[nb], im.k[use], kC, kC * KP, 16 * nb, 16 * kt, lane);
+        mma_row<4>(x, fs, fk);
+      }
+      if (lane == 0) pr.inv_s = inv_s;
+      wkv7::fence_proxy_async_smem();
+      signal(&pr.full_s, lane);
+
+      // y
+      if (!mbar_wait_bounded(a.status, &pr.full_y, use)) return;
+#pragma unroll
+      for (int nt = 0; nt < 8; ++nt) {
+        const float2 f = *reinterpret_cast<const float2*>(sc.wk + 8 * nt + 2 * t4);
+        const float4 y = pr.y[nt * 32 + lane];
+        const float f0 = f.x * inv_s, f1 = f.y * inv_s;
+        x[nt][0] = fmaf(f0, x[nt][0], y.x), x[nt][1] = fmaf(f1, x[nt][1], y.y);
+        x[nt][2] = fmaf(f0, x[nt][2], y.z), x[nt][3] = fmaf(f1, x[nt][3], y.w);
+      }
+      signal(&pr.free_y, lane);
+      const float sY = pow2_scale(warp_max(x));
+
+      // lam = T^T y
+      float l[8][4];
+      zero(l);
+      if (!mbar_wait_bounded(a.status, &im.full_t, use)) return;
+#pragma unroll
+      for (int i = 0; i < 4; ++i) {
+        Frag<2> fy, ft[4];
+        to_a(fy, x[2 * i], x[2 * i + 1], sY);
+#pragma unroll
+        for (int j = 0; j <= i; ++j) b_tri_kn<2>(ft[j], im.t, i, j, lane);
+        mma_row<4>(l, fy, ft, 0, i + 1);
+      }
+      signal(&im.free_t, lane);
+      const float fl = sc.inv_t * pow2_inverse(sY);
+#pragma unroll
+      for (int nt = 0; nt < 8; ++nt)
+#pragma unroll
+        for (int e = 0; e < 4; ++e) l[nt][e] *= fl;
+      const float sL = pow2_scale(warp_max(l));
+      if (s > 0 && !mbar_wait_bounded(a.status, &pr.free_l, use ^ 1)) return;
+#pragma unroll
+      for (int j = 0; j < 4; ++j) {
+        Frag<2> f;
+        to_a(f, l[2 * j], l[2 * j + 1], sL);
+        put_a(pr.l, kVt * kC, 16 * j, f, lane);
+      }
+      if (lane == 0) pr.inv_l = pow2_inverse(sL);
+      wkv7::fence_proxy_async_smem();
+      signal(&pr.full_l, lane);
+
+      // dS0, the product at its own scale, kept below 2^60 of dS1's
+#pragma unroll
+      for (int nt = 0; nt < 8; ++nt) {
+        const float2 f = *reinterpret_cast<const float2*>(sc.ek + 8 * nt + 2 * t4);
+#pragma unroll
+        for (int h = 0; h < 4; h += 2) l[nt][h] *= -f.x, l[nt][h + 1] *= -f.y;
+      }
+      const float sW = fminf(pow2_scale(warp_max(l)), sS * 0x1p60f), egc = sc.egc * sW;
+#pragma unroll
+      for (int nt = 0; nt < kNt; ++nt)
+#pragma unroll
+        for (int e = 0; e < 4; ++e) S[nt][e] *= egc;
+#pragma unroll
+      for (int j = 0; j < 4; ++j) {
+        Frag<2> fw;
+        to_a(fw, l[2 * j], l[2 * j + 1], sW);
+        Frag<P> fk[KP / 16];
+#pragma unroll
+        for (int nb = 0; nb < KP / 16; ++nb) b_kn<P>(fk[nb], im.k[use], kC, kC * KP, 16 * nb, 16 * j, lane);
+        mma_row<KP / 16>(S, fw, fk);
+      }
+      signal(&im.free_k[use], lane);
+      const float inv_w = pow2_inverse(sW);
+      if (!mbar_wait_bounded(a.status, &pr.full_g, use)) return;
+#pragma unroll
+      for (int nt = 0; nt < kNt; ++nt) {
+        const float4 g = pr.g[nt * 32 + lane];
+        S[nt][0] = fmaf(S[nt][0], inv_w, g.x), S[nt][1] = fmaf(S[nt][1], inv_w, g.y);
+        S[nt][2] = fmaf(S[nt][2], inv_w, g.z), S[nt][3] = fmaf(S[nt][3], inv_w, g.w);
+      }
+      signal(&pr.free_g, lane);
+      s_max = warp_max(S);
+    }
+    if (a.dS_init) store_state(S, a.dS_init + state_at, cols, K, lane);
+    return;
+  }
+
+  // ------------------------------------------------------------------- helper
   const size_t first = (((size_t)sq.b * a.s.T + sq.t0) * a.s.Hv + hv) * V + vt * kVt;
   const T* do_at = static_cast<const T*>(a.d_o) + first;
   T* dv_at = static_cast<T*>(a.dv) + first;
   const long long row_t = (long long)a.s.Hv * V;
-  const int tokens = sq.t1 - sq.t0;
-  // chunk c's rows: where they start and how many there are
-  auto ask = [&](int c) {
-    if (c >= 0) rows_ask(do_at + c * kC * row_t, row_t, tokens - c * kC, lane);
-  };
-
-  float S[kNt][4];
-  load_state(S, a.dS_final ? a.dS_final + state_at : nullptr, cols, K, lane);
-  float s_max = warp_max(S);
-  if (n > 0) rows_in(mine.rows[0], do_at + (n - 1) * kC * row_t, row_t, tokens - (n - 1) * kC, cols, lane);
-  copy_commit();
-  ask(n - 2), ask(n - 3);
-
-  for (int s = 0; s < n; ++s) {
-    const int c = n - 1 - s, use = s & 1, len = tokens - c * kC;
-    const size_t at_t = ((sq.slot + c) * a.s.Hv + hv) * vts + vt;
-    if (c > 0) rows_in(mine.rows[use ^ 1], do_at + (c - 1) * kC * row_t, row_t, kC, cols, lane);
+  auto fetch = [&](int s) {  // do of step s, and a request for a later one
+    const int c = n - 1 - s;
+    if (c >= 0) rows_in(pr.d[s & 1], do_at + c * kC * row_t, row_t, tokens - c * kC, cols, lane);
     copy_commit();
-    ask(c - 3);
-    if (lane == 0) bulk_wait_read();  // the images of the step before are out
-    __syncwarp();
+    if (c >= 2) rows_ask(do_at + (c - 2) * kC * row_t, row_t, kC, lane);
+  };
+  float inv_d = 0.f;
+  // What step s needs of do: its image, do^T P and (scale e^G do)^T q.
+  auto ahead = [&](int s) {
+    const int use = s & 1;
     const Scal& sc = im.sc(use);
-    const float sS = pow2_scale(s_max), inv_s = pow2_inverse(sS);
-
-    // dS1 k^T
-    float y[8][4];
-    zero(y);
-    if (!mbar_wait_bounded(a.status, &im.full_k[use], (s >> 1) & 1)) return;
-#pragma unroll
-    for (int kt = 0; kt < KP / 16; ++kt) {
-      Frag<2> fs;
-      to_a(fs, S[2 * kt], S[2 * kt + 1], sS);
-      put_a(mine.s, kVt * KP, 16 * kt, fs, lane);
-      Frag<P> fk[4];
-#pragma unroll
-      for (int nb = 0; nb < 4; ++nb) b_nk<P>(fk[nb], im.k[use], kC, kC * KP, 16 * nb, 16 * kt, lane);
-      mma_row<4>(y, fs, fk);
-    }
+    const size_t at_t = ((sq.slot + n - 1 - s) * a.s.Hv + hv) * vts + vt;
     copy_wait<1>();
     __syncwarp();
-    float d[8][4];
-    rows_get(d, mine.rows[use], lane, do_at);
-    const float sD = pow2_scale(warp_max(d)), inv_d = pow2_inverse(sD);
-
-    // y = P^T do + wk k dS1^T
-    float x[8][4];
+    float d[8][4], x[8][4];
+    rows_get(d, pr.d[use], lane, do_at);
+    __syncwarp();
+    fetch(s + 2);
+    const float sD = pow2_scale(warp_max(d));
+    inv_d = pow2_inverse(sD);
     zero(x);
-    if (!mbar_wait_bounded(a.status, &im.full_p, use)) return;
+    if (!mbar_wait_bounded(a.status, &im.full_k[use], (s >> 1) & 1)) return false;
+    if (!mbar_wait_bounded(a.status, &im.full_p, use)) return false;
+    if (lane == 0) bulk_wait_read();  // the images of dS and do of the step before are out
+    __syncwarp();
+    if (s > 0) signal(&pr.free_s, lane);
 #pragma unroll
     for (int i = 0; i < 4; ++i) {
       Frag<P> fd;
-      to_a(fd, d[2 * i], d[2 * i + 1], sD);
-      put_a(mine.d, kVt * kC, 16 * i, fd, lane);
       Frag<2> fp[4];
+      to_a(fd, d[2 * i], d[2 * i + 1], sD);
+      put_a(pr.d_img, kVt * kC, 16 * i, fd, lane);
 #pragma unroll
       for (int j = 0; j <= i; ++j) b_tri_kn<2>(fp[j], im.p, i, j, lane);
       mma_row<4>(x, fd, fp, 0, i + 1);
     }
-    give_up(&im.free_p, lane);
-    const float fp = sc.inv_p * inv_d;
-#pragma unroll
-    for (int nt = 0; nt < 8; ++nt) {
-      const float2 f = *reinterpret_cast<const float2*>(sc.wk + 8 * nt + 2 * t4);
-#pragma unroll
-      for (int h = 0; h < 4; h += 2) {
-        y[nt][h] = fmaf(f.x * inv_s, y[nt][h], fp * x[nt][h]);
-        y[nt][h + 1] = fmaf(f.y * inv_s, y[nt][h + 1], fp * x[nt][h + 1]);
-      }
-    }
-    const float sY = pow2_scale(warp_max(y));
-
-    // lam = T^T y
-    zero(x);
-    if (!mbar_wait_bounded(a.status, &im.full_t, use)) return;
-#pragma unroll
-    for (int i = 0; i < 4; ++i) {
-      Frag<2> fy;
-      to_a(fy, y[2 * i], y[2 * i + 1], sY);
-      Frag<2> ft[4];
-#pragma unroll
-      for (int j = 0; j <= i; ++j) b_tri_kn<2>(ft[j], im.t, i, j, lane);
-      mma_row<4>(x, fy, ft, 0, i + 1);
-    }
-    give_up(&im.free_t, lane);
-    const float fl = sc.inv_t * pow2_inverse(sY);
-#pragma unroll
-    for (int nt = 0; nt < 8; ++nt)
-#pragma unroll
-      for (int e = 0; e < 4; ++e) x[nt][e] *= fl;
-    const float sL = pow2_scale(warp_max(x));
-#pragma unroll
-    for (int j = 0; j < 4; ++j) {
-      Frag<2> f;
-      to_a(f, x[2 * j], x[2 * j + 1], sL);
-      put_a(mine.l, kVt * kC, 16 * j, f, lane);
-    }
+    signal(&im.free_p, lane);
     wkv7::fence_proxy_async_smem();
     __syncwarp();
     if (lane == 0) {
-      bulk_store(a.b.ds_img + at_t * sizeof(mine.s), mine.s, sizeof(mine.s));
-      bulk_store(a.b.do_img + at_t * sizeof(mine.d), mine.d, sizeof(mine.d));
-      bulk_store(a.b.l_img + at_t * sizeof(mine.l), mine.l, sizeof(mine.l));
+      bulk_store(a.b.do_img + at_t * sizeof(pr.d_img), pr.d_img, sizeof(pr.d_img));
       bulk_commit();
-      a.b.dsl[at_t] = make_float4(inv_s, pow2_inverse(sL), inv_d, 0.f);
     }
-    rows_out(x, mine.rows[use], dv_at + (size_t)c * kC * row_t, row_t, len, cols, lane);
-
-    // dS0, both products at one scale, kept below 2^60 of dS1's
+    if (s > 0 && !mbar_wait_bounded(a.status, &pr.free_y, use ^ 1)) return false;
+    tiles_put(pr.y, x, sc.inv_p * inv_d, lane);
+    signal(&pr.full_y, lane);
 #pragma unroll
     for (int nt = 0; nt < 8; ++nt) {
-      const float2 f = *reinterpret_cast<const float2*>(sc.ek + 8 * nt + 2 * t4), fd = *reinterpret_cast<const float2*>(sc.eq + 8 * nt + 2 * t4);
+      const float2 f = *reinterpret_cast<const float2*>(sc.eq + 8 * nt + 2 * t4);
 #pragma unroll
-      for (int h = 0; h < 4; h += 2) {
-        x[nt][h] *= -f.x, x[nt][h + 1] *= -f.y;
-        d[nt][h] *= fd.x, d[nt][h + 1] *= fd.y;
-      }
+      for (int h = 0; h < 4; h += 2) d[nt][h] *= f.x, d[nt][h + 1] *= f.y;
     }
-    const float sW = fminf(pow2_scale(abs_max(warp_max(x), warp_max(d))), sS * 0x1p60f), egc = sc.egc * sW;
-#pragma unroll
-    for (int nt = 0; nt < kNt; ++nt)
-#pragma unroll
-      for (int e = 0; e < 4; ++e) S[nt][e] *= egc;
-    if (!mbar_wait_bounded(a.status, &im.full_q, use)) return;
+    const float sW = pow2_scale(warp_max(d));
+    float g[kNt][4];
+    zero(g);
+    if (!mbar_wait_bounded(a.status, &im.full_q, use)) return false;
 #pragma unroll
     for (int j = 0; j < 4; ++j) {
-      Frag<2> fl2, fd;
-      to_a(fl2, x[2 * j], x[2 * j + 1], sW);
+      Frag<2> fd;
       to_a(fd, d[2 * j], d[2 * j + 1], sW);
-      Frag<P> fb[KP / 16];
+      Frag<P> fq[KP / 16];
 #pragma unroll
-      for (int nb = 0; nb < KP / 16; ++nb) b_kn<P>(fb[nb], im.k[use], kC, kC * KP, 16 * nb, 16 * j, lane);
-      mma_row<KP / 16>(S, fl2, fb);
-#pragma unroll
-      for (int nb = 0; nb < KP / 16; ++nb) b_kn<P>(fb[nb], im.q, kC, kC * KP, 16 * nb, 16 * j, lane);
-      mma_row<KP / 16>(S, fd, fb);
+      for (int nb = 0; nb < KP / 16; ++nb) b_kn<P>(fq[nb], im.q, kC, kC * KP, 16 * nb, 16 * j, lane);
+      mma_row<KP / 16>(g, fd, fq);
     }
-    give_up(&im.free_q, lane);
-    give_up(&im.free_k[use], lane);
-    const float inv_w = pow2_inverse(sW);
+    signal(&im.free_q, lane);
+    signal(&im.free_k[use], lane);
+    if (s > 0 && !mbar_wait_bounded(a.status, &pr.free_g, use ^ 1)) return false;
+    tiles_put(pr.g, g, pow2_inverse(sW), lane);
+    signal(&pr.full_g, lane);
+    return true;
+  };
+  fetch(0), fetch(1);
+  if (n > 0 && !ahead(0)) return;
+  for (int s = 0; s < n; ++s) {
+    const int c = n - 1 - s, use = s & 1;
+    const size_t at_t = ((sq.slot + c) * a.s.Hv + hv) * vts + vt;
+    const float inv_do = inv_d;
+    if (!mbar_wait_bounded(a.status, &pr.full_s, use)) return;
+    const float inv_s = pr.inv_s;
+    if (lane == 0) {
+      bulk_store(a.b.ds_img + at_t * sizeof(pr.s), pr.s, sizeof(pr.s));
+      bulk_commit();
+    }
+    if (s + 1 < n && !ahead(s + 1)) return;
+
+    if (!mbar_wait_bounded(a.status, &pr.full_l, use)) return;
+    const float inv_l = pr.inv_l;
+    if (lane == 0) {
+      bulk_store(a.b.l_img + at_t * sizeof(pr.l), pr.l, sizeof(pr.l));
+      bulk_commit();
+      a.b.dsl[at_t] = make_float4(inv_s, inv_l, inv_do, 0.f);
+    }
+    float x[8][4];
 #pragma unroll
-    for (int nt = 0; nt < kNt; ++nt)
-#pragma unroll
-      for (int e = 0; e < 4; ++e) S[nt][e] *= inv_w;
-    s_max = warp_max(S);
+    for (int j = 0; j < 4; ++j) {
+      Frag<2> f;
+      a_mk<2>(f, pr.l, kVt, kVt * kC, 0, 16 * j, lane);
+      from_a(x[2 * j], x[2 * j + 1], f, inv_l);
+    }
+    rows_out(x, pr.dv, dv_at + (size_t)c * kC * row_t, row_t, tokens - c * kC, cols, lane);
+    if (lane == 0) bulk_wait_read();
+    signal(&pr.free_l, lane);
   }
   if (lane == 0) bulk_wait_all();
-  if (a.dS_init) store_state(S, a.dS_init + state_at, cols, K, lane);
 }
 
 template <typename T, int KP>
 cudaError_t launch(const Args& a, cudaStream_t stream) {
-  const int warps = chain_warps(a.s);
-  constexpr size_t most = sizeof(BwdSmem<T, KP>);
-  static_assert(most <= 227 * 1024, "shared memory of a block");
+  constexpr int most = kBwdChains<T, KP>;
+  constexpr size_t all = sizeof(BwdSmem<T, KP>);
+  static_assert(all <= 227 * 1024, "shared memory of a block");
   auto kernel = bwd_kernel<T, KP>;
-  cudaError_t e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)most);
+  cudaError_t e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)all);
   if (e != cudaSuccess) return e;
-  const int sets = (v_tiles(a.s.V) + warps - 1) / warps;
-  const size_t smem = most - (kMaxWarps - warps) * sizeof(BwdWarp<T, KP>);
-  kernel<<<(unsigned)((size_t)a.s.nseq * a.s.Hv * sets), (warps + 1) * 32, smem, stream>>>(a);
+  const int chains = chain_warps(a.s, most), sets = (v_tiles(a.s.V) + chains - 1) / chains;
+  const size_t smem = all - (most - chains) * sizeof(BwdPair<T, KP>);
+  kernel<<<(unsigned)((size_t)a.s.nseq * a.s.Hv * sets), (2 * chains + 1) * 32, smem, stream>>>(a);
   return cudaGetLastError();
 }
 template <typename T>

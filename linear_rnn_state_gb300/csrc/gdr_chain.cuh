@@ -11,16 +11,22 @@
 // each intermediate in shared memory, spent 42 % of a step on shared-memory
 // reads and another 25 % at three barriers.)
 //
-// One more warp fills the images by bulk copies: q, T and P have one place each
-// and k two, each filled again as soon as every warp is past its last use in
-// the step.
+// A warp alone on its scheduler pays every latency of its step, so the step is
+// cut in two: the chain's warp makes only what the next state waits for, and a
+// helper warp beside it (on the same scheduler) makes the rest, o in the forward
+// and the products with do in the backward, and moves the rows and images to and
+// from memory. They meet through the images in shared memory, with a barrier for
+// each one full and one free again.
+//
+// One more warp fills the chunk's images by bulk copies: q, T and P have one
+// place each and k two, each filled again as soon as its readers are past their
+// last use in the step.
 #pragma once
 
 #include "gdr_common.cuh"
 
 namespace gdr {
 
-constexpr int kMaxWarps = 4;  // compute warps of a block
 
 // pT: parts of the P image that the chain reads.
 template <int P, int KP, int pT>
@@ -34,11 +40,13 @@ struct alignas(128) Images {
   __device__ __forceinline__ const Scal& sc(int place) const { return *reinterpret_cast<const Scal*>(scal[place]); }
 };
 
+// Chains and helpers read k's place (it has the scalars too), one side of them
+// the others.
 template <int P, int KP, int pT>
-__device__ __forceinline__ void init_images(Images<P, KP, pT>& m, int warps) {
+__device__ __forceinline__ void init_images(Images<P, KP, pT>& m, int chains) {
   for (uint64_t* b : {&m.full_k[0], &m.full_k[1], &m.full_q, &m.full_t, &m.full_p}) mbar_init(b, 1);
-  for (uint64_t* b : {&m.free_k[0], &m.free_k[1], &m.free_q, &m.free_t, &m.free_p}) mbar_init(b, warps);
-  wkv7::fence_mbar_init();
+  for (uint64_t* b : {&m.free_q, &m.free_t, &m.free_p}) mbar_init(b, chains);
+  for (uint64_t* b : {&m.free_k[0], &m.free_k[1]}) mbar_init(b, 2 * chains);
 }
 
 // The filling thread: images of steps 0 .. n - 1, whose chunk slots are slot0 +
@@ -91,20 +99,37 @@ __device__ __forceinline__ void fill_images(Images<P, KP, pT>& m, const Args& a,
     } else {
       if (!given_up(&m.free_p, s - 1)) return;
       p(s);
-      if (!given_up(&m.free_t, s - 1)) return;
-      t(s);
       if (!given_up(&m.free_q, s - 1)) return;
       q(s);
+      if (!given_up(&m.free_t, s - 1)) return;
+      t(s);
     }
     if (!given_up(&m.free_k[(s - 1) & 1], (s - 1) >> 1)) return;
     if (s + 1 < n) k(s + 1);
     ask(s + 2);
   }
 }
-// A warp is past its last read of a place.
-__device__ __forceinline__ void give_up(uint64_t* bar, int lane) {
+// What a warp did before is done for whoever waits on the barrier: its last read
+// of a place, or its writes of one.
+__device__ __forceinline__ void signal(uint64_t* bar, int lane) {
   __syncwarp();
   if (lane == 0) mbar_arrive(bar);
+}
+
+// Accumulator tiles handed from one warp to another as they are.
+template <int N>
+__device__ __forceinline__ void tiles_put(float4* buf, const float (&x)[N][4], float s, int lane) {
+#pragma unroll
+  for (int n = 0; n < N; ++n) buf[n * 32 + lane] = make_float4(x[n][0] * s, x[n][1] * s, x[n][2] * s, x[n][3] * s);
+}
+// An image's fragments (a_mk) back to accumulator tiles.
+__device__ __forceinline__ void from_a(float (&x)[4], float (&y)[4], const Frag<2>& f, float s) {
+#pragma unroll
+  for (int i = 0; i < 4; ++i) {
+    const float2 h = unpack_f16(f.h[i]), l = unpack_f16(f.l[i]);
+    float* z = i < 2 ? &x[2 * i] : &y[2 * (i - 2)];
+    z[0] = (h.x + l.x) * s, z[1] = (h.y + l.y) * s;
+  }
 }
 
 // ------------------------------------------- 64 tokens x 16 value columns ---
@@ -226,11 +251,15 @@ __device__ __forceinline__ void store_state(const float (&S)[N][4], float* dst, 
     }
 }
 
-// Compute warps of a block: four, one a scheduler, unless that leaves most SMs
-// without a block; then two.
-inline int chain_warps(const Shape& s) {
+__device__ __forceinline__ void copy_arrive(uint64_t* bar) {  // once this lane's copies so far have landed
+  asm volatile("cp.async.mbarrier.arrive.noinc.shared::cta.b64 [%0];" ::"r"(smem_addr(bar)) : "memory");
+}
+
+// Chains of a block: as many as `most`, one a scheduler, unless that leaves half
+// the SMs without a block; then two.
+inline int chain_warps(const Shape& s, int most) {
   const long long tiles = v_tiles(s.V);
-  const int w = tiles < kMaxWarps ? (int)tiles : kMaxWarps;
+  const int w = tiles < most ? (int)tiles : most;
   return w > 2 && (long long)s.nseq * s.Hv * ((tiles + w - 1) / w) <= 152 / 2 ? 2 : w;
 }
 

@@ -3,10 +3,10 @@
 // With T, P, the decays and the images of q and k from the parallel pass
 // (gdr_prep.cu), for the 16 rows of the state that a warp owns (gdr_chain.cuh),
 // all transposed (rows: value columns):
-//   r^T = v^T - e^G (S0 k^T)
-//   u^T = r^T T^T
-//   o^T = scale e^G (S0 q^T) + u^T P^T
-//   S1  = e^Gc S0 + (wk u)^T k
+//   r^T = v^T - e^G (S0 k^T)                    chain
+//   u^T = r^T T^T                               chain
+//   S1  = e^Gc S0 + (wk u)^T k                  chain
+//   o^T = scale e^G (S0 q^T) + u^T P^T          helper
 // T and P have their lower blocks only: a block (i, j) meets only the tokens j
 // of r and the tokens i of the result.
 //
@@ -14,218 +14,256 @@
 // bfloat16 calls takes S0, u and P with their hi part alone (11 bits against
 // the 8 that o is rounded to: 0.0003 of o's error of 0.0017), which saves 72 of
 // 312 mma a step at 64 keys.
-//
-// Bound by the tensor pipe of the four schedulers, one warp each: 240 mma of 8
-// cycles a step and 64 keys, with the conversions between products beside them.
 #include "gdr_chain.cuh"
 
 namespace gdr {
 namespace {
 
-template <typename T, int KP, bool kSave>
-struct alignas(128) FwdWarp {
-  unsigned char rows[2][kRowsBytes<T>];       // v of this and the next chunk; then o
-  __half s[kSave ? 2 * kVt * KP : 64], u[kSave ? 2 * kVt * kC : 64];  // images on their way out
+// What a chain and its helper share.
+template <typename T, int KP>
+struct alignas(128) FwdPair {
+  unsigned char v[2][kRowsBytes<T>], o[kRowsBytes<T>];
+  __half s[2 * kVt * KP], u[2 * kVt * kC];  // images of S0 and u
+  float inv_s, inv_u;
+  uint64_t full_s, full_u, full_v[2], free_s, free_u;
 };
-template <typename T, int KP, bool kSave>
+template <typename T, int KP>
+constexpr int kFwdChains = 4;
+template <typename T, int KP>
 struct FwdSmem {
   Images<In<T>::kParts, KP, In<T>::kParts> im;
-  FwdWarp<T, KP, kSave> w[kMaxWarps];
+  FwdPair<T, KP> pair[kFwdChains<T, KP>];
 };
 
 template <typename T, int KP, bool kSave>
-__global__ void __launch_bounds__((kMaxWarps + 1) * 32, sizeof(FwdSmem<T, KP, kSave>) <= 113 * 1024 ? 2 : 1) fwd_kernel(const Args a) {
+__global__ void __launch_bounds__((2 * kFwdChains<T, KP> + 1) * 32, 1) fwd_kernel(const Args a) {
   extern __shared__ __align__(128) unsigned char raw[];
-  using Smem = FwdSmem<T, KP, kSave>;
   constexpr int P = In<T>::kParts, kNt = KP / 8;
-  Smem& sm = *reinterpret_cast<Smem*>(raw);
-  const int warps = blockDim.x / 32 - 1, warp = threadIdx.x >> 5, lane = threadIdx.x & 31, t4 = lane & 3;
-  const int vts = (a.s.V + kVt - 1) / kVt, sets = (vts + warps - 1) / warps;
+  FwdSmem<T, KP>& sm = *reinterpret_cast<FwdSmem<T, KP>*>(raw);
+  const int chains = blockDim.x / 64, warp = threadIdx.x >> 5, lane = threadIdx.x & 31, t4 = lane & 3;
+  const int vts = (a.s.V + kVt - 1) / kVt, sets = (vts + chains - 1) / chains;
   const int set = blockIdx.x % sets, hv = blockIdx.x / sets % a.s.Hv, seq = blockIdx.x / (sets * a.s.Hv);
   const int hk = hv / (a.s.Hv / a.s.Hk);
   const SeqRange sq = seq_range(a.s, seq);
   const int n = (sq.t1 - sq.t0 + kC - 1) / kC;
   const int K = a.s.K, V = a.s.V;
   auto& im = sm.im;
-  if (threadIdx.x == 0) init_images(im, min(warps, vts - set * warps));
+  if (threadIdx.x == 0) {
+    init_images(im, min(chains, vts - set * chains));
+    for (int i = 0; i < chains; ++i) {
+      FwdPair<T, KP>& p = sm.pair[i];
+      for (uint64_t* b : {&p.full_s, &p.full_u, &p.free_s, &p.free_u}) mbar_init(b, 1);
+      mbar_init(&p.full_v[0], 32), mbar_init(&p.full_v[1], 32);
+    }
+    wkv7::fence_mbar_init();
+  }
   __syncthreads();
-  if (warp == warps) {
+  if (warp == 2 * chains) {
     if (lane == 0) fill_images(im, a, sq.slot, 1, n, hk, hv);
     return;
   }
-  const int vt = set * warps + warp;
+  const int own = warp % chains, vt = set * chains + own;
   if (vt >= vts) return;
-  FwdWarp<T, KP, kSave>& mine = sm.w[warp];
-  const int cols = V - vt * kVt;
-  const size_t state_at = (((size_t)seq * a.s.Hv + hv) * V + vt * kVt) * K;
+  FwdPair<T, KP>& pr = sm.pair[own];
+  const int cols = V - vt * kVt, tokens = sq.t1 - sq.t0;
   const T* v_at = static_cast<const T*>(a.v) + sq.b * a.s.v_b + sq.t0 * a.s.v_t + (size_t)hv * V + vt * kVt;
-  T* o_at = static_cast<T*>(a.o) + (((size_t)sq.b * a.s.T + sq.t0) * a.s.Hv + hv) * V + vt * kVt;
-  const long long o_t = (long long)a.s.Hv * V;
-  const int tokens = sq.t1 - sq.t0;
 
-  float S[kNt][4];
-  load_state(S, a.s_init ? a.s_init + state_at : nullptr, cols, K, lane);
-  float s_max = warp_max(S);
-  if (n > 0) rows_in(mine.rows[0], v_at, a.s.v_t, tokens, cols, lane);
-  copy_commit();
-  if (n > 1) rows_ask(v_at + kC * a.s.v_t, a.s.v_t, tokens - kC, lane);
-  if (n > 2) rows_ask(v_at + 2 * kC * a.s.v_t, a.s.v_t, tokens - 2 * kC, lane);
-
-  for (int c = 0; c < n; ++c) {
-    const int use = c & 1, len = tokens - c * kC;
-    const size_t at_t = ((sq.slot + c) * a.s.Hv + hv) * vts + vt;
-    if (c + 1 < n) rows_in(mine.rows[use ^ 1], v_at + (c + 1) * kC * a.s.v_t, a.s.v_t, len - kC, cols, lane);
-    copy_commit();
-    if (c + 3 < n) rows_ask(v_at + (c + 3) * kC * a.s.v_t, a.s.v_t, len - 3 * kC, lane);
-    if constexpr (kSave) {
-      if (lane == 0) bulk_wait_read();  // the images of the step before are out
-      __syncwarp();
-    }
-    const Scal& sc = im.sc(use);
-    const float sS = pow2_scale(s_max), inv_s = pow2_inverse(sS);
-
-    // S0 k^T and S0 q^T
-    float x[8][4], o[8][4];
-    zero(x), zero(o);
-    if (!mbar_wait_bounded(a.status, &im.full_k[use], (c >> 1) & 1)) return;
-    if (!mbar_wait_bounded(a.status, &im.full_q, use)) return;
+  if (warp < chains) {  // ------------------------------------------------ chain
+    const size_t state_at = (((size_t)seq * a.s.Hv + hv) * V + vt * kVt) * K;
+    float S[kNt][4];
+    load_state(S, a.s_init ? a.s_init + state_at : nullptr, cols, K, lane);
+    float s_max = warp_max(S);
+    for (int c = 0; c < n; ++c) {
+      const int use = c & 1;
+      const Scal& sc = im.sc(use);
+      const float sS = pow2_scale(s_max), inv_s = pow2_inverse(sS);
+      // S0 k^T
+      float x[8][4];
+      zero(x);
+      if (!mbar_wait_bounded(a.status, &im.full_k[use], (c >> 1) & 1)) return;
+      if (c > 0 && !mbar_wait_bounded(a.status, &pr.free_s, use ^ 1)) return;
 #pragma unroll
-    for (int kt = 0; kt < KP / 16; ++kt) {
-      Frag<2> fs;
-      to_a(fs, S[2 * kt], S[2 * kt + 1], sS);
-      if constexpr (kSave) put_a(mine.s, kVt * KP, 16 * kt, fs, lane);
-      Frag<P> fb[4];
+      for (int kt = 0; kt < KP / 16; ++kt) {
+        Frag<2> fs;
+        to_a(fs, S[2 * kt], S[2 * kt + 1], sS);
+        put_a(pr.s, kVt * KP, 16 * kt, fs, lane);
+        Frag<P> fk[4];
 #pragma unroll
-      for (int nb = 0; nb < 4; ++nb) b_nk<P>(fb[nb], im.k[use], kC, kC * KP, 16 * nb, 16 * kt, lane);
-      mma_row<4>(x, fs, fb);
-#pragma unroll
-      for (int nb = 0; nb < 4; ++nb) b_nk<P>(fb[nb], im.q, kC, kC * KP, 16 * nb, 16 * kt, lane);
-      mma_row_out<4>(o, fs, fb);
-    }
-    give_up(&im.free_q, lane);
-    if constexpr (kSave) {
-      wkv7::fence_proxy_async_smem();
-      __syncwarp();
-      if (lane == 0) {
-        bulk_store(a.b.s_img + at_t * sizeof(mine.s), mine.s, sizeof(mine.s));
-        bulk_commit();
+        for (int nb = 0; nb < 4; ++nb) b_nk<P>(fk[nb], im.k[use], kC, kC * KP, 16 * nb, 16 * kt, lane);
+        mma_row<4>(x, fs, fk);
       }
-    }
+      if (lane == 0) pr.inv_s = inv_s;
+      if (kSave) wkv7::fence_proxy_async_smem();
+      signal(&pr.full_s, lane);
 
-    // r
-    copy_wait<1>();
-    __syncwarp();
-    {
-      float v[8][4];
-      rows_get(v, mine.rows[use], lane, v_at);
+      // r
+      if (!mbar_wait_bounded(a.status, &pr.full_v[use], (c >> 1) & 1)) return;
+      {
+        float v[8][4];
+        rows_get(v, pr.v[use], lane, v_at);
 #pragma unroll
-      for (int nt = 0; nt < 8; ++nt) {
-        const float2 f = *reinterpret_cast<const float2*>(sc.ek + 8 * nt + 2 * t4), fo = *reinterpret_cast<const float2*>(sc.eq + 8 * nt + 2 * t4);
+        for (int nt = 0; nt < 8; ++nt) {
+          const float2 f = *reinterpret_cast<const float2*>(sc.ek + 8 * nt + 2 * t4);
+          const float f0 = -f.x * inv_s, f1 = -f.y * inv_s;
 #pragma unroll
-        for (int h = 0; h < 4; h += 2) {
-          x[nt][h] = fmaf(-f.x * inv_s, x[nt][h], v[nt][h]), x[nt][h + 1] = fmaf(-f.y * inv_s, x[nt][h + 1], v[nt][h + 1]);
-          o[nt][h] *= fo.x * inv_s, o[nt][h + 1] *= fo.y * inv_s;
+          for (int h = 0; h < 4; h += 2) {
+            x[nt][h] = fmaf(f0, x[nt][h], v[nt][h]), x[nt][h + 1] = fmaf(f1, x[nt][h + 1], v[nt][h + 1]);
+          }
         }
       }
-    }
-    const float sR = pow2_scale(warp_max(x));
+      const float sR = pow2_scale(warp_max(x));
 
-    // u = T r
-    float u[8][4];
-    zero(u);
-    if (!mbar_wait_bounded(a.status, &im.full_t, use)) return;
+      // u = T r
+      float u[8][4];
+      zero(u);
+      if (!mbar_wait_bounded(a.status, &im.full_t, use)) return;
 #pragma unroll
-    for (int j = 0; j < 4; ++j) {
-      Frag<2> fr;
-      to_a(fr, x[2 * j], x[2 * j + 1], sR);
-      Frag<2> ft[4];
+      for (int j = 0; j < 4; ++j) {
+        Frag<2> fr, ft[4];
+        to_a(fr, x[2 * j], x[2 * j + 1], sR);
 #pragma unroll
-      for (int i = j; i < 4; ++i) b_tri_nk<2>(ft[i], im.t, i, j, lane);
-      mma_row<4>(u, fr, ft, j);
+        for (int i = j; i < 4; ++i) b_tri_nk<2>(ft[i], im.t, i, j, lane);
+        mma_row<4>(u, fr, ft, j);
+      }
+      signal(&im.free_t, lane);
+      const float fu = sc.inv_t * pow2_inverse(sR);
+#pragma unroll
+      for (int nt = 0; nt < 8; ++nt)
+#pragma unroll
+        for (int e = 0; e < 4; ++e) u[nt][e] *= fu;
+      const float sU = pow2_scale(warp_max(u));
+      if (c > 0 && !mbar_wait_bounded(a.status, &pr.free_u, use ^ 1)) return;
+#pragma unroll
+      for (int j = 0; j < 4; ++j) {
+        Frag<2> f;
+        to_a(f, u[2 * j], u[2 * j + 1], sU);
+        put_a(pr.u, kVt * kC, 16 * j, f, lane);
+      }
+      if (lane == 0) pr.inv_u = pow2_inverse(sU);
+      if (kSave) wkv7::fence_proxy_async_smem();
+      signal(&pr.full_u, lane);
+
+      // S1: the products are added to S0 at their own scale, which is kept
+      // below 2^60 of S0's so that S0 stays finite in it
+#pragma unroll
+      for (int nt = 0; nt < 8; ++nt) {
+        const float2 f = *reinterpret_cast<const float2*>(sc.wk + 8 * nt + 2 * t4);
+#pragma unroll
+        for (int h = 0; h < 4; h += 2) u[nt][h] *= f.x, u[nt][h + 1] *= f.y;
+      }
+      const float sW = fminf(pow2_scale(warp_max(u)), sS * 0x1p60f), egc = sc.egc * sW;
+#pragma unroll
+      for (int nt = 0; nt < kNt; ++nt)
+#pragma unroll
+        for (int e = 0; e < 4; ++e) S[nt][e] *= egc;
+#pragma unroll
+      for (int j = 0; j < 4; ++j) {
+        Frag<2> fw;
+        to_a(fw, u[2 * j], u[2 * j + 1], sW);
+        Frag<P> fk[KP / 16];
+#pragma unroll
+        for (int nb = 0; nb < KP / 16; ++nb) b_kn<P>(fk[nb], im.k[use], kC, kC * KP, 16 * nb, 16 * j, lane);
+        mma_row<KP / 16>(S, fw, fk);
+      }
+      signal(&im.free_k[use], lane);
+      const float inv_w = pow2_inverse(sW);
+#pragma unroll
+      for (int nt = 0; nt < kNt; ++nt)
+#pragma unroll
+        for (int e = 0; e < 4; ++e) S[nt][e] *= inv_w;
+      s_max = warp_max(S);
     }
-    give_up(&im.free_t, lane);
-    const float fu = sc.inv_t * pow2_inverse(sR);
+    if (a.s_final) store_state(S, a.s_final + state_at, cols, K, lane);
+    return;
+  }
+
+  // ------------------------------------------------------------------- helper
+  T* o_at = static_cast<T*>(a.o) + (((size_t)sq.b * a.s.T + sq.t0) * a.s.Hv + hv) * V + vt * kVt;
+  const long long o_t = (long long)a.s.Hv * V;
+  auto fetch = [&](int c) {  // v of chunk c, and a request for a later one
+    if (c < n) {
+      rows_in(pr.v[c & 1], v_at + c * kC * a.s.v_t, a.s.v_t, tokens - c * kC, cols, lane);
+      copy_arrive(&pr.full_v[c & 1]);
+    }
+    if (c + 2 < n) rows_ask(v_at + (c + 2) * kC * a.s.v_t, a.s.v_t, tokens - (c + 2) * kC, lane);
+  };
+  fetch(0), fetch(1);
+  for (int c = 0; c < n; ++c) {
+    const int use = c & 1;
+    const size_t at_t = ((sq.slot + c) * a.s.Hv + hv) * vts + vt;
+    const Scal& sc = im.sc(use);
+    // S0 q^T
+    float o[8][4], x[8][4];
+    zero(o), zero(x);
+    if (!mbar_wait_bounded(a.status, &im.full_k[use], (c >> 1) & 1)) return;
+    if (!mbar_wait_bounded(a.status, &im.full_q, use)) return;
+    if (!mbar_wait_bounded(a.status, &pr.full_s, use)) return;
+    if (kSave && lane == 0) {
+      bulk_store(a.b.s_img + at_t * sizeof(pr.s), pr.s, sizeof(pr.s));
+      bulk_commit();
+    }
 #pragma unroll
-    for (int nt = 0; nt < 8; ++nt)
+    for (int kt = 0; kt < KP / 16; ++kt) {
+      Frag<P> fs, fq[4];
+      a_mk<P>(fs, pr.s, kVt, kVt * KP, 0, 16 * kt, lane);
 #pragma unroll
-      for (int e = 0; e < 4; ++e) u[nt][e] *= fu;
-    const float sU = pow2_scale(warp_max(u));
-    if constexpr (kSave)
-      if (lane == 0) a.b.su[at_t] = make_float2(inv_s, pow2_inverse(sU));
+      for (int nb = 0; nb < 4; ++nb) b_nk<P>(fq[nb], im.q, kC, kC * KP, 16 * nb, 16 * kt, lane);
+      mma_row<4>(o, fs, fq);
+    }
+    signal(&im.free_q, lane);
+    const float inv_s = pr.inv_s, inv_p = sc.inv_p;
+#pragma unroll
+    for (int nt = 0; nt < 8; ++nt) {
+      const float2 f = *reinterpret_cast<const float2*>(sc.eq + 8 * nt + 2 * t4);
+#pragma unroll
+      for (int h = 0; h < 4; h += 2) o[nt][h] *= f.x * inv_s, o[nt][h + 1] *= f.y * inv_s;
+    }
+    signal(&im.free_k[use], lane);
+    if (kSave && lane == 0) bulk_wait_read();
+    signal(&pr.free_s, lane);
 
     // P u
-    zero(x);
+    if (!mbar_wait_bounded(a.status, &pr.full_u, use)) return;
+    fetch(c + 2);  // the chain is past v of this step
+    const float inv_u = pr.inv_u;
+    if (kSave && lane == 0) {
+      bulk_store(a.b.u_img + at_t * sizeof(pr.u), pr.u, sizeof(pr.u));
+      bulk_commit();
+      a.b.su[at_t] = make_float2(inv_s, inv_u);
+    }
     if (!mbar_wait_bounded(a.status, &im.full_p, use)) return;
 #pragma unroll
     for (int j = 0; j < 4; ++j) {
-      Frag<(kSave || P == 2) ? 2 : 1> fp;
-      to_a(fp, u[2 * j], u[2 * j + 1], sU);
-      if constexpr (kSave) put_a(mine.u, kVt * kC, 16 * j, fp, lane);
-      Frag<P> ft[4];
+      Frag<P> fu, fp[4];
+      a_mk<P>(fu, pr.u, kVt, kVt * kC, 0, 16 * j, lane);
 #pragma unroll
-      for (int i = j; i < 4; ++i) b_tri_nk<P>(ft[i], im.p, i, j, lane);
-      mma_row_out<4>(x, fp, ft, j);
+      for (int i = j; i < 4; ++i) b_tri_nk<P>(fp[i], im.p, i, j, lane);
+      mma_row<4>(x, fu, fp, j);
     }
-    give_up(&im.free_p, lane);
-    if constexpr (kSave) {
-      wkv7::fence_proxy_async_smem();
-      __syncwarp();
-      if (lane == 0) {
-        bulk_store(a.b.u_img + at_t * sizeof(mine.u), mine.u, sizeof(mine.u));
-        bulk_commit();
-      }
-    }
-    const float fo = sc.inv_p * pow2_inverse(sU);
+    signal(&im.free_p, lane);
+    const float fo = inv_p * inv_u;
 #pragma unroll
-    for (int nt = 0; nt < 8; ++nt) {
-      const float2 f = *reinterpret_cast<const float2*>(sc.wk + 8 * nt + 2 * t4);
+    for (int nt = 0; nt < 8; ++nt)
 #pragma unroll
-      for (int h = 0; h < 4; h += 2) {
-        o[nt][h] = fmaf(fo, x[nt][h], o[nt][h]), o[nt][h + 1] = fmaf(fo, x[nt][h + 1], o[nt][h + 1]);
-        u[nt][h] *= f.x, u[nt][h + 1] *= f.y;
-      }
-    }
-
-    // S1: the products are added to S0 at their own scale, which is kept below
-    // 2^60 of S0's so that S0 stays finite in it
-    const float sW = fminf(pow2_scale(warp_max(u)), sS * 0x1p60f), egc = sc.egc * sW;
-#pragma unroll
-    for (int nt = 0; nt < kNt; ++nt)
-#pragma unroll
-      for (int e = 0; e < 4; ++e) S[nt][e] *= egc;
-#pragma unroll
-    for (int j = 0; j < 4; ++j) {
-      Frag<2> fw;
-      to_a(fw, u[2 * j], u[2 * j + 1], sW);
-      Frag<P> fk[KP / 16];
-#pragma unroll
-      for (int nb = 0; nb < KP / 16; ++nb) b_kn<P>(fk[nb], im.k[use], kC, kC * KP, 16 * nb, 16 * j, lane);
-      mma_row<KP / 16>(S, fw, fk);
-    }
-    give_up(&im.free_k[use], lane);
-    const float inv_w = pow2_inverse(sW);
-#pragma unroll
-    for (int nt = 0; nt < kNt; ++nt)
-#pragma unroll
-      for (int e = 0; e < 4; ++e) S[nt][e] *= inv_w;
-    s_max = warp_max(S);
-    rows_out(o, mine.rows[use], o_at + (size_t)c * kC * o_t, o_t, len, cols, lane);
+      for (int e = 0; e < 4; ++e) o[nt][e] = fmaf(fo, x[nt][e], o[nt][e]);
+    if (kSave && lane == 0) bulk_wait_read();
+    signal(&pr.free_u, lane);
+    rows_out(o, pr.o, o_at + (size_t)c * kC * o_t, o_t, tokens - c * kC, cols, lane);
   }
   if (kSave && lane == 0) bulk_wait_all();
-  if (a.s_final) store_state(S, a.s_final + state_at, cols, K, lane);
 }
 
 template <typename T, int KP, bool kSave>
 cudaError_t launch(const Args& a, cudaStream_t stream) {
-  const int warps = chain_warps(a.s);
-  constexpr size_t most = sizeof(FwdSmem<T, KP, kSave>);
-  static_assert(most <= 227 * 1024, "shared memory of a block");
+  constexpr int most = kFwdChains<T, KP>;
+  constexpr size_t all = sizeof(FwdSmem<T, KP>);
+  static_assert(all <= 227 * 1024, "shared memory of a block");
   auto kernel = fwd_kernel<T, KP, kSave>;
-  cudaError_t e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)most);
+  cudaError_t e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)all);
   if (e != cudaSuccess) return e;
-  const int sets = (v_tiles(a.s.V) + warps - 1) / warps;
-  const size_t smem = most - (kMaxWarps - warps) * sizeof(FwdWarp<T, KP, kSave>);
-  kernel<<<(unsigned)((size_t)a.s.nseq * a.s.Hv * sets), (warps + 1) * 32, smem, stream>>>(a);
+  const int chains = chain_warps(a.s, most), sets = (v_tiles(a.s.V) + chains - 1) / chains;
+  const size_t smem = all - (most - chains) * sizeof(FwdPair<T, KP>);
+  kernel<<<(unsigned)((size_t)a.s.nseq * a.s.Hv * sets), (2 * chains + 1) * 32, smem, stream>>>(a);
   return cudaGetLastError();
 }
 template <typename T>
