@@ -18,10 +18,14 @@ namespace {
 // What a chain and its helper share.
 template <typename T, int KP>
 struct alignas(128) BwdPair {
-  unsigned char d[2][kRowsBytes<T>], dv[kRowsBytes<T>];
-  __half s[2 * kVt * KP], l[2 * kVt * kC], d_img[In<T>::kParts * kVt * kC];  // images of dS1, lam, do
-  float4 y[8 * 32], g[KP / 8 * 32];  // do^T P and (scale e^G do)^T q, as accumulator tiles
-  float inv_s, inv_l;
+  unsigned char d[2][kRowsBytes<T>];
+  union {  // the helper's ways to memory
+    unsigned char dv[kRowsBytes<T>];
+    __half l_img[2 * kVt * kC];
+  };
+  __half s[2 * kVt * KP], d_img[In<T>::kParts * kVt * kC];  // images of dS1 and do
+  float4 l[8 * 32], y[8 * 32], g[KP / 8 * 32];  // lam, do^T P and (scale e^G do)^T q, as accumulator tiles
+  float inv_s;
   uint64_t full_s, full_l, full_y, full_g, free_s, free_l, free_y, free_g;
 };
 // fp32 images of 128 keys leave room for two
@@ -70,6 +74,7 @@ __global__ void __launch_bounds__((2 * kBwdChains<T, KP> + 1) * 32, 1) bwd_kerne
     float S[kNt][4];
     load_state(S, a.dS_final ? a.dS_final + state_at : nullptr, cols, K, lane);
     float s_max = warp_max(S);
+    Asked has_k(&im.full_k[0], 0);
     for (int s = 0; s < n; ++s) {
       const int use = s & 1;
       const Scal& sc = im.sc(use);
@@ -77,8 +82,9 @@ __global__ void __launch_bounds__((2 * kBwdChains<T, KP> + 1) * 32, 1) bwd_kerne
       // dS1 k^T
       float x[8][4];
       zero(x);
-      if (!mbar_wait_bounded(a.status, &im.full_k[use], (s >> 1) & 1)) return;
-      if (s > 0 && !mbar_wait_bounded(a.status, &pr.free_s, use ^ 1)) return;
+      const Asked has_s(&pr.free_s, use ^ 1), has_y(&pr.full_y, use), has_t(&im.full_t, use);
+      if (!has_k.wait(a.status)) return;
+      if (s > 0 && !has_s.wait(a.status)) return;
 #pragma unroll
       for (int kt = 0; kt < KP / 16; ++kt) {
         Frag<2> fs;
@@ -94,7 +100,7 @@ __global__ void __launch_bounds__((2 * kBwdChains<T, KP> + 1) * 32, 1) bwd_kerne
       signal(&pr.full_s, lane);
 
       // y
-      if (!mbar_wait_bounded(a.status, &pr.full_y, use)) return;
+      if (!has_y.wait(a.status)) return;
 #pragma unroll
       for (int nt = 0; nt < 8; ++nt) {
         const float2 f = *reinterpret_cast<const float2*>(sc.wk + 8 * nt + 2 * t4);
@@ -109,7 +115,7 @@ __global__ void __launch_bounds__((2 * kBwdChains<T, KP> + 1) * 32, 1) bwd_kerne
       // lam = T^T y
       float l[8][4];
       zero(l);
-      if (!mbar_wait_bounded(a.status, &im.full_t, use)) return;
+      if (!has_t.wait(a.status)) return;
 #pragma unroll
       for (int i = 0; i < 4; ++i) {
         Frag<2> fy, ft[4];
@@ -118,22 +124,14 @@ __global__ void __launch_bounds__((2 * kBwdChains<T, KP> + 1) * 32, 1) bwd_kerne
         for (int j = 0; j <= i; ++j) b_tri_kn<2>(ft[j], im.t, i, j, lane);
         mma_row<4>(l, fy, ft, 0, i + 1);
       }
-      signal(&im.free_t, lane);
+      const Asked has_l(&pr.free_l, use ^ 1), has_g(&pr.full_g, use);
       const float fl = sc.inv_t * pow2_inverse(sY);
 #pragma unroll
       for (int nt = 0; nt < 8; ++nt)
 #pragma unroll
         for (int e = 0; e < 4; ++e) l[nt][e] *= fl;
-      const float sL = pow2_scale(warp_max(l));
-      if (s > 0 && !mbar_wait_bounded(a.status, &pr.free_l, use ^ 1)) return;
-#pragma unroll
-      for (int j = 0; j < 4; ++j) {
-        Frag<2> f;
-        to_a(f, l[2 * j], l[2 * j + 1], sL);
-        put_a(pr.l, kVt * kC, 16 * j, f, lane);
-      }
-      if (lane == 0) pr.inv_l = pow2_inverse(sL);
-      wkv7::fence_proxy_async_smem();
+      if (s > 0 && !has_l.wait(a.status)) return;
+      tiles_put(pr.l, l, 1.f, lane);
       signal(&pr.full_l, lane);
 
       // dS0, the product at its own scale, kept below 2^60 of dS1's
@@ -157,9 +155,10 @@ __global__ void __launch_bounds__((2 * kBwdChains<T, KP> + 1) * 32, 1) bwd_kerne
         for (int nb = 0; nb < KP / 16; ++nb) b_kn<P>(fk[nb], im.k[use], kC, kC * KP, 16 * nb, 16 * j, lane);
         mma_row<KP / 16>(S, fw, fk);
       }
+      has_k = Asked(&im.full_k[use ^ 1], (s + 1) >> 1);
       signal(&im.free_k[use], lane);
       const float inv_w = pow2_inverse(sW);
-      if (!mbar_wait_bounded(a.status, &pr.full_g, use)) return;
+      if (!has_g.wait(a.status)) return;
 #pragma unroll
       for (int nt = 0; nt < kNt; ++nt) {
         const float4 g = pr.g[nt * 32 + lane];
@@ -265,22 +264,26 @@ __global__ void __launch_bounds__((2 * kBwdChains<T, KP> + 1) * 32, 1) bwd_kerne
     if (s + 1 < n && !ahead(s + 1)) return;
 
     if (!mbar_wait_bounded(a.status, &pr.full_l, use)) return;
-    const float inv_l = pr.inv_l;
-    if (lane == 0) {
-      bulk_store(a.b.l_img + at_t * sizeof(pr.l), pr.l, sizeof(pr.l));
-      bulk_commit();
-      a.b.dsl[at_t] = make_float4(inv_s, inv_l, inv_do, 0.f);
-    }
     float x[8][4];
+    tiles_get(x, pr.l, lane);
+    signal(&pr.free_l, lane);
+    const float sL = pow2_scale(warp_max(x));
 #pragma unroll
     for (int j = 0; j < 4; ++j) {
       Frag<2> f;
-      a_mk<2>(f, pr.l, kVt, kVt * kC, 0, 16 * j, lane);
-      from_a(x[2 * j], x[2 * j + 1], f, inv_l);
+      to_a(f, x[2 * j], x[2 * j + 1], sL);
+      put_a(pr.l_img, kVt * kC, 16 * j, f, lane);
     }
+    wkv7::fence_proxy_async_smem();
+    __syncwarp();
+    if (lane == 0) {
+      bulk_store(a.b.l_img + at_t * sizeof(pr.l_img), pr.l_img, sizeof(pr.l_img));
+      bulk_commit();
+      a.b.dsl[at_t] = make_float4(inv_s, pow2_inverse(sL), inv_do, 0.f);
+      bulk_wait_read();
+    }
+    __syncwarp();
     rows_out(x, pr.dv, dv_at + (size_t)c * kC * row_t, row_t, tokens - c * kC, cols, lane);
-    if (lane == 0) bulk_wait_read();
-    signal(&pr.free_l, lane);
   }
   if (lane == 0) bulk_wait_all();
 }

@@ -36,16 +36,16 @@ struct alignas(128) Images {
   __half t[2 * kTriPart], p[pT * kTriPart];
   unsigned char scal[2][kChainScal];
   uint64_t full_k[2], full_q, full_t, full_p;
-  uint64_t free_k[2], free_q, free_t, free_p;
+  uint64_t free_k[2], free_q, free_p;
   __device__ __forceinline__ const Scal& sc(int place) const { return *reinterpret_cast<const Scal*>(scal[place]); }
 };
 
-// Chains and helpers read k's place (it has the scalars too), one side of them
-// the others.
+// Chains and helpers read k's place (it has the scalars too), helpers q and P,
+// chains T, which goes free with k.
 template <int P, int KP, int pT>
 __device__ __forceinline__ void init_images(Images<P, KP, pT>& m, int chains) {
   for (uint64_t* b : {&m.full_k[0], &m.full_k[1], &m.full_q, &m.full_t, &m.full_p}) mbar_init(b, 1);
-  for (uint64_t* b : {&m.free_q, &m.free_t, &m.free_p}) mbar_init(b, chains);
+  for (uint64_t* b : {&m.free_q, &m.free_p}) mbar_init(b, chains);
   for (uint64_t* b : {&m.free_k[0], &m.free_k[1]}) mbar_init(b, 2 * chains);
 }
 
@@ -92,23 +92,31 @@ __device__ __forceinline__ void fill_images(Images<P, KP, pT>& m, const Args& a,
     if (direction > 0) {
       if (!given_up(&m.free_q, s - 1)) return;
       q(s);
-      if (!given_up(&m.free_t, s - 1)) return;
-      t(s);
-      if (!given_up(&m.free_p, s - 1)) return;
-      p(s);
     } else {
       if (!given_up(&m.free_p, s - 1)) return;
       p(s);
       if (!given_up(&m.free_q, s - 1)) return;
       q(s);
-      if (!given_up(&m.free_t, s - 1)) return;
-      t(s);
     }
     if (!given_up(&m.free_k[(s - 1) & 1], (s - 1) >> 1)) return;
+    t(s);
     if (s + 1 < n) k(s + 1);
+    if (direction > 0) {
+      if (!given_up(&m.free_p, s - 1)) return;
+      p(s);
+    }
     ask(s + 2);
   }
 }
+// A barrier asked early (a try_wait takes some 85 cycles to answer) and waited
+// for only where the answer was no.
+struct Asked {
+  uint64_t* bar;
+  uint32_t parity;
+  bool there;
+  __device__ __forceinline__ Asked(uint64_t* b, uint32_t p) : bar(b), parity(p & 1), there(wkv7::mbar_try_wait(b, p & 1)) {}
+  __device__ __forceinline__ bool wait(unsigned* status) const { return there || mbar_wait_bounded(status, bar, parity); }
+};
 // What a warp did before is done for whoever waits on the barrier: its last read
 // of a place, or its writes of one.
 __device__ __forceinline__ void signal(uint64_t* bar, int lane) {
@@ -118,20 +126,18 @@ __device__ __forceinline__ void signal(uint64_t* bar, int lane) {
 
 // Accumulator tiles handed from one warp to another as they are.
 template <int N>
+__device__ __forceinline__ void tiles_get(float (&x)[N][4], const float4* buf, int lane) {
+#pragma unroll
+  for (int n = 0; n < N; ++n) {
+    const float4 v = buf[n * 32 + lane];
+    x[n][0] = v.x, x[n][1] = v.y, x[n][2] = v.z, x[n][3] = v.w;
+  }
+}
+template <int N>
 __device__ __forceinline__ void tiles_put(float4* buf, const float (&x)[N][4], float s, int lane) {
 #pragma unroll
   for (int n = 0; n < N; ++n) buf[n * 32 + lane] = make_float4(x[n][0] * s, x[n][1] * s, x[n][2] * s, x[n][3] * s);
 }
-// An image's fragments (a_mk) back to accumulator tiles.
-__device__ __forceinline__ void from_a(float (&x)[4], float (&y)[4], const Frag<2>& f, float s) {
-#pragma unroll
-  for (int i = 0; i < 4; ++i) {
-    const float2 h = unpack_f16(f.h[i]), l = unpack_f16(f.l[i]);
-    float* z = i < 2 ? &x[2 * i] : &y[2 * (i - 2)];
-    z[0] = (h.x + l.x) * s, z[1] = (h.y + l.y) * s;
-  }
-}
-
 // ------------------------------------------- 64 tokens x 16 value columns ---
 //
 // A warp's part of v or do, by asynchronous copies into its own buffer, and its

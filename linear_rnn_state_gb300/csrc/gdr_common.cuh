@@ -303,12 +303,13 @@ __device__ __forceinline__ void mbar_arrive(uint64_t* bar) {
 __device__ __forceinline__ void prefetch_l2(const void* p) { asm volatile("prefetch.global.L2 [%0];" ::"l"(p)); }
 template <int N>
 __device__ __forceinline__ float warp_max(const float (&x)[N][4]) {
-  float m[4] = {0.f, 0.f, 0.f, 0.f};  // four chains of max
+  // four chains of max; a NaN is passed over here and carries itself into the products
+  float m[4] = {0.f, 0.f, 0.f, 0.f};
 #pragma unroll
   for (int n = 0; n < N; ++n)
 #pragma unroll
-    for (int e = 0; e < 4; ++e) m[e] = abs_max(m[e], x[n][e]);
-  return warp_max_abs(abs_max(abs_max(m[0], m[1]), abs_max(m[2], m[3])));
+    for (int e = 0; e < 4; ++e) m[e] = fmaxf(m[e], fabsf(x[n][e]));
+  return warp_max_abs(fmaxf(fmaxf(m[0], m[1]), fmaxf(m[2], m[3])));
 }
 template <int N>
 __device__ __forceinline__ void zero(float (&x)[N][4]) {

@@ -22,9 +22,14 @@ namespace {
 // What a chain and its helper share.
 template <typename T, int KP>
 struct alignas(128) FwdPair {
-  unsigned char v[2][kRowsBytes<T>], o[kRowsBytes<T>];
-  __half s[2 * kVt * KP], u[2 * kVt * kC];  // images of S0 and u
-  float inv_s, inv_u;
+  unsigned char v[2][kRowsBytes<T>];
+  union {  // the helper's ways to memory
+    unsigned char o[kRowsBytes<T>];
+    __half u_img[2 * kVt * kC];
+  };
+  __half s[2 * kVt * KP];  // the image of S0
+  float4 u[8 * 32];        // u as accumulator tiles
+  float inv_s;
   uint64_t full_s, full_u, full_v[2], free_s, free_u;
 };
 template <typename T, int KP>
@@ -73,6 +78,7 @@ __global__ void __launch_bounds__((2 * kFwdChains<T, KP> + 1) * 32, 1) fwd_kerne
     float S[kNt][4];
     load_state(S, a.s_init ? a.s_init + state_at : nullptr, cols, K, lane);
     float s_max = warp_max(S);
+    Asked has_k(&im.full_k[0], 0);
     for (int c = 0; c < n; ++c) {
       const int use = c & 1;
       const Scal& sc = im.sc(use);
@@ -80,8 +86,9 @@ __global__ void __launch_bounds__((2 * kFwdChains<T, KP> + 1) * 32, 1) fwd_kerne
       // S0 k^T
       float x[8][4];
       zero(x);
-      if (!mbar_wait_bounded(a.status, &im.full_k[use], (c >> 1) & 1)) return;
-      if (c > 0 && !mbar_wait_bounded(a.status, &pr.free_s, use ^ 1)) return;
+      const Asked has_s(&pr.free_s, use ^ 1), has_v(&pr.full_v[use], c >> 1), has_t(&im.full_t, use);
+      if (!has_k.wait(a.status)) return;
+      if (c > 0 && !has_s.wait(a.status)) return;
 #pragma unroll
       for (int kt = 0; kt < KP / 16; ++kt) {
         Frag<2> fs;
@@ -97,7 +104,7 @@ __global__ void __launch_bounds__((2 * kFwdChains<T, KP> + 1) * 32, 1) fwd_kerne
       signal(&pr.full_s, lane);
 
       // r
-      if (!mbar_wait_bounded(a.status, &pr.full_v[use], (c >> 1) & 1)) return;
+      if (!has_v.wait(a.status)) return;
       {
         float v[8][4];
         rows_get(v, pr.v[use], lane, v_at);
@@ -116,7 +123,7 @@ __global__ void __launch_bounds__((2 * kFwdChains<T, KP> + 1) * 32, 1) fwd_kerne
       // u = T r
       float u[8][4];
       zero(u);
-      if (!mbar_wait_bounded(a.status, &im.full_t, use)) return;
+      if (!has_t.wait(a.status)) return;
 #pragma unroll
       for (int j = 0; j < 4; ++j) {
         Frag<2> fr, ft[4];
@@ -125,22 +132,14 @@ __global__ void __launch_bounds__((2 * kFwdChains<T, KP> + 1) * 32, 1) fwd_kerne
         for (int i = j; i < 4; ++i) b_tri_nk<2>(ft[i], im.t, i, j, lane);
         mma_row<4>(u, fr, ft, j);
       }
-      signal(&im.free_t, lane);
+      const Asked has_u(&pr.free_u, use ^ 1);
       const float fu = sc.inv_t * pow2_inverse(sR);
 #pragma unroll
       for (int nt = 0; nt < 8; ++nt)
 #pragma unroll
         for (int e = 0; e < 4; ++e) u[nt][e] *= fu;
-      const float sU = pow2_scale(warp_max(u));
-      if (c > 0 && !mbar_wait_bounded(a.status, &pr.free_u, use ^ 1)) return;
-#pragma unroll
-      for (int j = 0; j < 4; ++j) {
-        Frag<2> f;
-        to_a(f, u[2 * j], u[2 * j + 1], sU);
-        put_a(pr.u, kVt * kC, 16 * j, f, lane);
-      }
-      if (lane == 0) pr.inv_u = pow2_inverse(sU);
-      if (kSave) wkv7::fence_proxy_async_smem();
+      if (c > 0 && !has_u.wait(a.status)) return;
+      tiles_put(pr.u, u, 1.f, lane);
       signal(&pr.full_u, lane);
 
       // S1: the products are added to S0 at their own scale, which is kept
@@ -165,6 +164,7 @@ __global__ void __launch_bounds__((2 * kFwdChains<T, KP> + 1) * 32, 1) fwd_kerne
         for (int nb = 0; nb < KP / 16; ++nb) b_kn<P>(fk[nb], im.k[use], kC, kC * KP, 16 * nb, 16 * j, lane);
         mma_row<KP / 16>(S, fw, fk);
       }
+      has_k = Asked(&im.full_k[use ^ 1], (c + 1) >> 1);
       signal(&im.free_k[use], lane);
       const float inv_w = pow2_inverse(sW);
 #pragma unroll
@@ -224,30 +224,39 @@ __global__ void __launch_bounds__((2 * kFwdChains<T, KP> + 1) * 32, 1) fwd_kerne
 
     // P u
     if (!mbar_wait_bounded(a.status, &pr.full_u, use)) return;
+    float u[8][4];
+    tiles_get(u, pr.u, lane);
+    signal(&pr.free_u, lane);
     fetch(c + 2);  // the chain is past v of this step
-    const float inv_u = pr.inv_u;
-    if (kSave && lane == 0) {
-      bulk_store(a.b.u_img + at_t * sizeof(pr.u), pr.u, sizeof(pr.u));
-      bulk_commit();
-      a.b.su[at_t] = make_float2(inv_s, inv_u);
-    }
+    const float sU = pow2_scale(warp_max(u)), inv_u = pow2_inverse(sU);
     if (!mbar_wait_bounded(a.status, &im.full_p, use)) return;
 #pragma unroll
     for (int j = 0; j < 4; ++j) {
-      Frag<P> fu, fp[4];
-      a_mk<P>(fu, pr.u, kVt, kVt * kC, 0, 16 * j, lane);
+      Frag<kSave ? 2 : P> fu;
+      Frag<P> fp[4];
+      to_a(fu, u[2 * j], u[2 * j + 1], sU);
+      if constexpr (kSave) put_a(pr.u_img, kVt * kC, 16 * j, fu, lane);
 #pragma unroll
       for (int i = j; i < 4; ++i) b_tri_nk<P>(fp[i], im.p, i, j, lane);
-      mma_row<4>(x, fu, fp, j);
+      mma_row_out<4>(x, fu, fp, j);
     }
     signal(&im.free_p, lane);
+    if (kSave) {
+      wkv7::fence_proxy_async_smem();
+      __syncwarp();
+      if (lane == 0) {
+        bulk_store(a.b.u_img + at_t * sizeof(pr.u_img), pr.u_img, sizeof(pr.u_img));
+        bulk_commit();
+        a.b.su[at_t] = make_float2(inv_s, inv_u);
+      }
+    }
     const float fo = inv_p * inv_u;
 #pragma unroll
     for (int nt = 0; nt < 8; ++nt)
 #pragma unroll
       for (int e = 0; e < 4; ++e) o[nt][e] = fmaf(fo, x[nt][e], o[nt][e]);
     if (kSave && lane == 0) bulk_wait_read();
-    signal(&pr.free_u, lane);
+    __syncwarp();
     rows_out(o, pr.o, o_at + (size_t)c * kC * o_t, o_t, tokens - c * kC, cols, lane);
   }
   if (kSave && lane == 0) bulk_wait_all();
