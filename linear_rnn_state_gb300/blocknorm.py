@@ -13,7 +13,7 @@ from __future__ import annotations
 import ctypes
 
 from . import gdr, wkv7
-from .gdr import _addr, _check_device, _check_tensor, _on
+from .gdr import _addr, _check_device, _check_tensor, _is_bf16, _On
 
 # C functions declared in include/blocknorm.h, with their argument counts.
 EXPORTS = {
@@ -25,11 +25,17 @@ EXPORTS = {
 }
 
 _typed = set()
+_lib = None
 
 
 def load(path: str | None = None):
     """The loaded library with the blocknorm_* signatures set."""
+    global _lib
     lib = wkv7.load(path)
+    if path is None:
+        _lib = lib
+    if gdr._torch is None:
+        gdr._setup()
     if id(lib) not in _typed:
         vp, i, n, f = ctypes.c_void_p, ctypes.c_int, ctypes.c_longlong, ctypes.c_float
         lib.blocknorm_add_forward.argtypes = [vp] * 7 + [n] * 3 + [i, f, i, i, vp]
@@ -47,7 +53,12 @@ def load(path: str | None = None):
 def _rows(name, t, inner):
     """(rows, elements from row to row) of a tensor whose last `inner`
     dimensions are a row: dense inside, all rows equally far apart."""
-    dense, inside = 1, 1
+    if t.is_contiguous():
+        stride = 1
+        for d in t.shape[t.dim() - inner:]:
+            stride *= d
+        return t.numel() // stride if stride else 0, stride
+    dense = 1
     for d in range(t.dim() - 1, t.dim() - 1 - inner, -1):
         if t.shape[d] > 1 and t.stride(d) != dense:
             raise ValueError(f"{name}: a row must be dense (strides {t.stride()})")
@@ -63,21 +74,17 @@ def _rows(name, t, inner):
 
 
 def _types(x, residual):
-    import torch
-
-    r = wkv7._inputs_dtype(residual)
+    r = _is_bf16("residual", residual)
     if x is None:
         return r, r
-    a = wkv7._inputs_dtype(x)
-    if not a and r:
+    a = _is_bf16("x", x)
+    if r and not a:
         raise TypeError("a float32 x needs a float32 residual")
     return a, r
 
 
 def _vector(name, t, D, dev):
-    import torch
-
-    _check_tensor(name, t, (D,), torch.float32, dev)
+    _check_tensor(name, t, (D,), gdr._torch.float32, dev)
 
 
 def add_forward(x, residual, weight, scale=None, *, eps: float = 1e-6, stream=None):
@@ -85,12 +92,11 @@ def add_forward(x, residual, weight, scale=None, *, eps: float = 1e-6, stream=No
     residual [...][D]; weight and scale (None: 1) [D] float32. Returns
     (h, n, rstd): h of residual's type (residual itself without x), n of x's
     type (residual's without x), rstd [...] float32 for the backward."""
-    import torch
-
-    lib = load()
+    lib = _lib or load()
+    torch = gdr._torch
     bf16, rbf16 = _types(x, residual)
     D, dev = residual.shape[-1], residual.device
-    _check_device(residual)
+    _check_device(dev)
     rows, rs = _rows("residual", residual, 1)
     xs = D
     if x is not None:
@@ -99,7 +105,7 @@ def add_forward(x, residual, weight, scale=None, *, eps: float = 1e-6, stream=No
     _vector("weight", weight, D, dev)
     if scale is not None:
         _vector("scale", scale, D, dev)
-    with _on(stream) as handle:
+    with _On(stream, dev) as handle:
         n = torch.empty(residual.shape, dtype=residual.dtype if x is None else x.dtype, device=dev)
         h = None if x is None else torch.empty(residual.shape, dtype=residual.dtype, device=dev)
         rstd = torch.empty(residual.shape[:-1], dtype=torch.float32, device=dev)
@@ -111,12 +117,11 @@ def add_forward(x, residual, weight, scale=None, *, eps: float = 1e-6, stream=No
 def add_backward(x, residual, weight, rstd, dn, dh=None, scale=None, *, stream=None):
     """Gradients of sum <dn, n> + <dh, h> (dh None: 0). Returns dict dresidual,
     dx (None without x), dweight and dscale (None without scale)."""
-    import torch
-
-    lib = load()
+    lib = _lib or load()
+    torch = gdr._torch
     bf16, rbf16 = _types(x, residual)
     D, dev = residual.shape[-1], residual.device
-    _check_device(residual)
+    _check_device(dev)
     rows, rs = _rows("residual", residual, 1)
     xs, xt = D, residual.dtype
     if x is not None:
@@ -129,7 +134,7 @@ def add_backward(x, residual, weight, rstd, dn, dh=None, scale=None, *, stream=N
         _check_tensor("dh", dh, residual.shape, residual.dtype, dev)
     if scale is not None:
         _vector("scale", scale, D, dev)
-    with _on(stream) as handle:
+    with _On(stream, dev) as handle:
         dres = torch.empty(residual.shape, dtype=residual.dtype, device=dev)
         # without a scale x's gradient is the residual's; it is written apart only in another type
         own_dx = x is not None and (scale is not None or xt != residual.dtype)
@@ -143,10 +148,10 @@ def add_backward(x, residual, weight, rstd, dn, dh=None, scale=None, *, stream=N
 
 
 def _gated(o, z, weight):
-    bf16 = wkv7._inputs_dtype(o)
+    bf16 = _is_bf16("o", o)
     if o.dim() < 2:
         raise ValueError("o must be [...][H][D]")
-    _check_device(o)
+    _check_device(o.device)
     H, D = o.shape[-2:]
     _check_tensor("z", z, o.shape, o.dtype, o.device, False)
     _vector("weight", weight, D, o.device)
@@ -157,13 +162,13 @@ def _gated(o, z, weight):
 def gated_forward(o, z, weight, *, eps: float = 1e-6, stream=None):
     """The gated norm after a block, a head at a time: o, z [...][H][D], weight
     [D] float32. Returns (y, rstd), rstd [...][H] float32 for the backward."""
-    import torch
-
-    lib = load()
+    lib = _lib or load()
+    torch = gdr._torch
     bf16, tokens, H, D, os_, zs = _gated(o, z, weight)
-    with _on(stream) as handle:
-        y = torch.empty(o.shape, dtype=o.dtype, device=o.device)
-        rstd = torch.empty(o.shape[:-1], dtype=torch.float32, device=o.device)
+    dev = o.device
+    with _On(stream, dev) as handle:
+        y = torch.empty(o.shape, dtype=o.dtype, device=dev)
+        rstd = torch.empty(o.shape[:-1], dtype=torch.float32, device=dev)
         wkv7._check(lib.blocknorm_gated_forward(*(_addr(t) for t in (o, z, weight, y, rstd)), os_, zs, tokens, H, D, eps,
                                                 bf16, handle))
     return y, rstd
@@ -171,16 +176,16 @@ def gated_forward(o, z, weight, *, eps: float = 1e-6, stream=None):
 
 def gated_backward(o, z, weight, rstd, dy, *, stream=None):
     """Gradients of sum <dy, y>. Returns dict do, dz, dweight."""
-    import torch
-
-    lib = load()
+    lib = _lib or load()
+    torch = gdr._torch
     bf16, tokens, H, D, os_, zs = _gated(o, z, weight)
+    dev = o.device
     _check_tensor("rstd", rstd, o.shape[:-1], torch.float32, o.device)
     _check_tensor("dy", dy, o.shape, o.dtype, o.device)
-    with _on(stream) as handle:
-        do, dz = (torch.empty(o.shape, dtype=o.dtype, device=o.device) for _ in range(2))
-        dw = torch.empty(D, dtype=torch.float32, device=o.device)
-        part = torch.empty(lib.blocknorm_part_bytes(tokens * H, D, 1), dtype=torch.uint8, device=o.device)
+    with _On(stream, dev) as handle:
+        do, dz = (torch.empty(o.shape, dtype=o.dtype, device=dev) for _ in range(2))
+        dw = torch.empty(D, dtype=torch.float32, device=dev)
+        part = torch.empty(lib.blocknorm_part_bytes(tokens * H, D, 1), dtype=torch.uint8, device=dev)
         wkv7._check(lib.blocknorm_gated_backward(*(_addr(t) for t in (o, z, weight, rstd, dy, do, dz, dw, part)), os_, zs,
                                                  tokens, H, D, bf16, handle))
     return {"do": do, "dz": dz, "dweight": dw}

@@ -110,6 +110,14 @@ __device__ __forceinline__ float group_sum(float x, float* red) {
 
 __device__ __forceinline__ float sigmoid(float z) { return __fdividef(1.f, 1.f + __expf(-z)); }
 
+// Where row `row` of an input starts: `t` elements from token to token, H rows a
+// token (dense where t is H * D, which takes no division).
+__device__ __forceinline__ long long row_at(const Args& p, long long row, long long t) {
+  if (t == (long long)p.H * p.D) return row * p.D;
+  const unsigned r = (unsigned)row, tok = r / (unsigned)p.H;
+  return (long long)tok * t + (long long)(r - tok * p.H) * p.D;
+}
+
 // kGate: the gated norm (a = o, b = z); otherwise the add norm (a = x, b = residual).
 template <typename TA, typename TB, bool kGate, int kGroup, int kVec, bool kWhole>
 __global__ void __launch_bounds__(kThreads) forward_kernel(const Args p) {
@@ -118,10 +126,9 @@ __global__ void __launch_bounds__(kThreads) forward_kernel(const Args p) {
   const int tg = threadIdx.x % kGroup;
   const long long row = (long long)blockIdx.x * kRows + threadIdx.x / kGroup;
   const bool in = row < p.rows;
-  const long long tok = in ? row / p.H : 0, head = in ? row % p.H : 0;
   const int D = p.D;
-  const TA* ra = static_cast<const TA*>(p.a) + tok * p.a_t + head * D;
-  const TB* rb = p.b ? static_cast<const TB*>(p.b) + tok * p.b_t + head * D : nullptr;
+  const TA* ra = static_cast<const TA*>(p.a) + (in ? row_at(p, row, p.a_t) : 0);
+  const TB* rb = p.b ? static_cast<const TB*>(p.b) + (in ? row_at(p, row, p.b_t) : 0) : nullptr;
   float h[kVec][8], z[kGate ? kVec : 1][8], s2 = 0.f;
 #pragma unroll
   for (int v = 0; v < kVec; ++v) {
@@ -184,9 +191,8 @@ __global__ void __launch_bounds__(kThreads) backward_kernel(const Args p) {
   for (long long base = (long long)blockIdx.x * kRows; base < p.rows; base += (long long)gridDim.x * kRows) {
     const long long row = base + sub;
     const bool in = row < p.rows;
-    const long long tok = in ? row / p.H : 0, head = in ? row % p.H : 0;
-    const TA* ra = static_cast<const TA*>(p.a) + tok * p.a_t + head * D;
-    const TB* rb = p.b ? static_cast<const TB*>(p.b) + tok * p.b_t + head * D : nullptr;
+    const TA* ra = static_cast<const TA*>(p.a) + (in ? row_at(p, row, p.a_t) : 0);
+    const TB* rb = p.b ? static_cast<const TB*>(p.b) + (in ? row_at(p, row, p.b_t) : 0) : nullptr;
     const TA* rg = static_cast<const TA*>(p.dout) + (in ? row : 0) * D;
     const float r = in ? p.rstd[row] : 0.f;
     float u[kVec][8], t[kVec][8], x[kVec][8], c1 = 0.f;  // x: of the add norm; dz's factor of the gated

@@ -294,7 +294,8 @@ cudaError_t launch(const Args& a, cudaStream_t stream) {
   constexpr size_t all = sizeof(BwdSmem<T, KP>);
   static_assert(all <= 227 * 1024, "shared memory of a block");
   auto kernel = bwd_kernel<T, KP>;
-  cudaError_t e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)all);
+  static std::atomic<unsigned long long> done{0};
+  cudaError_t e = allow_smem(reinterpret_cast<const void*>(kernel), all, done);
   if (e != cudaSuccess) return e;
   const int chains = chain_warps(a.s, most), sets = (v_tiles(a.s.V) + chains - 1) / chains;
   const size_t smem = all - (most - chains) * sizeof(BwdPair<T, KP>);

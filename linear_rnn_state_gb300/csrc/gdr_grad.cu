@@ -405,7 +405,8 @@ template <typename T, int KP, bool kShared>
 cudaError_t launch(const Args& a, cudaStream_t stream) {
   constexpr size_t smem = sizeof(GradSmem<T, KP>);
   auto kernel = grad_kernel<T, KP, kShared>;
-  cudaError_t e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem);
+  static std::atomic<unsigned long long> done{0};
+  cudaError_t e = allow_smem(reinterpret_cast<const void*>(kernel), smem, done);
   if (e != cudaSuccess) return e;
   kernel<<<(unsigned)((size_t)a.s.slots * a.s.Hv), kThreads<KP>, smem, stream>>>(a);
   if ((e = cudaGetLastError()) != cudaSuccess) return e;

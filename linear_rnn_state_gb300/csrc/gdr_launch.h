@@ -2,6 +2,8 @@
 // (gdr_api.cu) and its kernels, and the layout of what they hand on.
 #pragma once
 
+#include <atomic>
+
 #include <cuda_runtime.h>
 #include <stddef.h>
 #include <stdint.h>
@@ -109,6 +111,18 @@ cudaError_t launch_prep(const Args& a, bool bf16, cudaStream_t stream);
 cudaError_t launch_fwd(const Args& a, bool bf16, bool save, cudaStream_t stream);
 cudaError_t launch_bwd(const Args& a, bool bf16, cudaStream_t stream);
 cudaError_t launch_grad(const Args& a, bool bf16, cudaStream_t stream);
+
+// Allows a kernel its dynamic shared memory, once a device; `done` belongs to the kernel.
+inline cudaError_t allow_smem(const void* kernel, size_t bytes, std::atomic<unsigned long long>& done) {
+  int dev = 0;
+  cudaError_t e = cudaGetDevice(&dev);
+  if (e != cudaSuccess) return e;
+  const unsigned long long bit = 1ull << (dev & 63);
+  if (done.load(std::memory_order_acquire) & bit) return cudaSuccess;
+  e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)bytes);
+  if (e == cudaSuccess) done.fetch_or(bit, std::memory_order_release);
+  return e;
+}
 
 struct StepArgs {
   const void *q, *k, *v;

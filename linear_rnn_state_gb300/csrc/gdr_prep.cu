@@ -413,7 +413,8 @@ __global__ void __launch_bounds__(kThreads, 4) prep_kernel(const Args a) {
 template <typename T, int KP>
 cudaError_t launch(const Args& a, cudaStream_t stream) {
   constexpr size_t smem = sizeof(PrepSmem<T, KP>);
-  cudaError_t e = cudaFuncSetAttribute(prep_kernel<T, KP>, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem);
+  static std::atomic<unsigned long long> done{0};
+  cudaError_t e = allow_smem(reinterpret_cast<const void*>(prep_kernel<T, KP>), smem, done);
   if (e != cudaSuccess) return e;
   prep_kernel<T, KP><<<(unsigned)((size_t)a.s.slots * a.s.Hk), kThreads, smem, stream>>>(a);
   return cudaGetLastError();

@@ -6,13 +6,15 @@
 // all keys) belongs to a group of lanes with four keys each; rows do not meet,
 // so a thread keeps eight rows in registers over all tokens of the call. Both
 // products take the state before the update, S' q = e^g S q + u (k.q), so their
-// sums are reduced together.
+// sums are reduced together: sixteen sums over 32 lanes, half of what is left
+// handed over at each step, so that each lane ends with one row's (16 shuffles
+// and eight to hand the rows' u back, against 80 for each sum on its own).
 #include "gdr_common.cuh"
 
 namespace gdr {
 namespace {
 
-constexpr int kThreads = 128, kRows = 8;
+constexpr int kThreads = 128;
 
 __device__ __forceinline__ float4 load4(const __nv_bfloat16* p) {
   const uint2 u = *reinterpret_cast<const uint2*>(p);
@@ -31,7 +33,7 @@ __device__ __forceinline__ void store1(float* p, float x) { *p = x; }
 // kLanes lanes a row: 4 kLanes >= K.
 template <typename T, int kLanes>
 __global__ void __launch_bounds__(kThreads) step_kernel(const StepArgs a) {
-  constexpr int kSub = 32 / kLanes, kWarpRows = kRows * kSub, kBlockRows = kWarpRows * (kThreads / 32);
+  constexpr int kRows = kLanes >= 16 ? 8 : 4, kSub = 32 / kLanes, kStep = kLanes / (2 * kRows), kWarpRows = kRows * kSub, kBlockRows = kWarpRows * (kThreads / 32);
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, sub = lane / kLanes, cl = lane % kLanes;
   const int tiles = (a.V + kBlockRows - 1) / kBlockRows;
   const int tile = blockIdx.x % tiles, hv = blockIdx.x / tiles % a.Hv, r = blockIdx.x / (tiles * a.Hv);
@@ -45,7 +47,7 @@ __global__ void __launch_bounds__(kThreads) step_kernel(const StepArgs a) {
 #pragma unroll
   for (int i = 0; i < kRows; ++i) {
     const int row = row0 + i * kSub;
-    S[i] = live && key_in && row < a.V ? *reinterpret_cast<const float4*>(state + (size_t)row * a.K) : make_float4(0.f, 0.f, 0.f, 0.f);
+    S[i] = live && key_in && row < a.V ? __ldcs(reinterpret_cast<const float4*>(state + (size_t)row * a.K)) : make_float4(0.f, 0.f, 0.f, 0.f);
   }
   for (int t = 0; t < a.T; ++t) {
     float4 q = make_float4(0.f, 0.f, 0.f, 0.f), k = q;
@@ -55,10 +57,10 @@ __global__ void __launch_bounds__(kThreads) step_kernel(const StepArgs a) {
     }
     const size_t tok = (size_t)r * a.T + t;
     const float decay = expf(a.g[tok * a.Hv + hv]), beta = a.beta[tok * a.Hv + hv];
+    // each lane ends with the sums of its row `mine`
+    const int mine = cl / kStep % kRows, row = row0 + mine * kSub;
     const T* v = static_cast<const T*>(a.v) + r * a.v_b + t * a.v_t + (size_t)hv * a.V;
-    float vs[kRows];
-#pragma unroll
-    for (int i = 0; i < kRows; ++i) vs[i] = row0 + i * kSub < a.V ? load1(v + row0 + i * kSub) : 0.f;
+    const float vr = row < a.V ? load1(v + row) : 0.f;
     float kq = wkv7::group_allreduce<kLanes>(dot4(q, k, 0.f));
     float rq = a.scale, rk = 1.f;
     if (a.l2norm) {
@@ -66,33 +68,47 @@ __global__ void __launch_bounds__(kThreads) step_kernel(const StepArgs a) {
       rk = 1.f / sqrtf(wkv7::group_allreduce<kLanes>(dot4(k, k, 0.f)) + 1e-6f);
     }
     kq *= rk * rq;
-    float out = 0.f;
+    const bool second = cl >= kLanes / 2;  // S q rather than S k
+    float x[kRows];
 #pragma unroll
     for (int i = 0; i < kRows; ++i) {
-      const float sk = wkv7::group_allreduce<kLanes>(dot4(S[i], k, 0.f)), sq = wkv7::group_allreduce<kLanes>(dot4(S[i], q, 0.f));
-      const float u = beta * fmaf(-decay, sk * rk, vs[i]), uk = u * rk;
-      S[i].x = fmaf(uk, k.x, decay * S[i].x);
-      S[i].y = fmaf(uk, k.y, decay * S[i].y);
-      S[i].z = fmaf(uk, k.z, decay * S[i].z);
-      S[i].w = fmaf(uk, k.w, decay * S[i].w);
-      const float o = fmaf(u, kq, decay * (sq * rq));
-      if (cl == i) out = o;
+      const float sk = dot4(S[i], k, 0.f), sq = dot4(S[i], q, 0.f);
+      x[i] = (second ? sq : sk) + __shfl_xor_sync(0xffffffffu, second ? sk : sq, kLanes / 2);
     }
-    // lane i of a group has row i's o
-    const int row = row0 + cl * kSub;
-    if (cl < kRows && row < a.V) store1(static_cast<T*>(a.o) + (tok * a.Hv + hv) * a.V + row, live ? out : 0.f);
+    int bit = kLanes / 4;
+#pragma unroll
+    for (int n = kRows / 2; n >= 1; n /= 2, bit /= 2) {
+      const bool up = cl & bit;
+#pragma unroll
+      for (int i = 0; i < n; ++i) x[i] = (up ? x[i + n] : x[i]) + __shfl_xor_sync(0xffffffffu, up ? x[i] : x[i + n], bit);
+    }
+#pragma unroll
+    for (; bit >= 1; bit /= 2) x[0] += __shfl_xor_sync(0xffffffffu, x[0], bit);
+    const float other = __shfl_xor_sync(0xffffffffu, x[0], kLanes / 2);
+    const float sk = second ? other : x[0], sq = second ? x[0] : other;
+    const float u = beta * fmaf(-decay, sk * rk, vr), uk = u * rk;
+    if (cl < kLanes / 2 && cl % kStep == 0 && row < a.V)
+      store1(static_cast<T*>(a.o) + (tok * a.Hv + hv) * a.V + row, live ? fmaf(u, kq, decay * (sq * rq)) : 0.f);
+#pragma unroll
+    for (int i = 0; i < kRows; ++i) {
+      const float w = __shfl_sync(0xffffffffu, uk, i * kStep, kLanes);
+      S[i].x = fmaf(w, k.x, decay * S[i].x);
+      S[i].y = fmaf(w, k.y, decay * S[i].y);
+      S[i].z = fmaf(w, k.z, decay * S[i].z);
+      S[i].w = fmaf(w, k.w, decay * S[i].w);
+    }
   }
   if (live && key_in)
 #pragma unroll
     for (int i = 0; i < kRows; ++i) {
       const int row = row0 + i * kSub;
-      if (row < a.V) *reinterpret_cast<float4*>(state + (size_t)row * a.K) = S[i];
+      if (row < a.V) __stcs(reinterpret_cast<float4*>(state + (size_t)row * a.K), S[i]);
     }
 }
 
 template <typename T, int kLanes>
 cudaError_t launch(const StepArgs& a, cudaStream_t stream) {
-  constexpr int rows = kRows * (32 / kLanes) * (kThreads / 32);
+  constexpr int rows = (kLanes >= 16 ? 8 : 4) * (32 / kLanes) * (kThreads / 32);
   step_kernel<T, kLanes><<<(unsigned)((size_t)a.R * a.Hv * ((a.V + rows - 1) / rows)), kThreads, 0, stream>>>(a);
   return cudaGetLastError();
 }

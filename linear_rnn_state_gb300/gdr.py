@@ -14,7 +14,6 @@ and states [n][Hv][V][K] float32. q, k, v may be slices of a wider tensor.
 """
 from __future__ import annotations
 
-import contextlib
 import ctypes
 
 from . import wkv7
@@ -34,11 +33,15 @@ EXPORTS = {
 }
 
 _typed = set()
+_lib = None
 
 
 def load(path: str | None = None):
     """The loaded library with the gdr_* signatures set."""
+    global _lib
     lib = wkv7.load(path)
+    if path is None:
+        _lib = lib
     if id(lib) not in _typed:
         vp, i, f = ctypes.c_void_p, ctypes.c_int, ctypes.c_float
         lib.gdr_saved_bytes.argtypes = [i] * 9
@@ -56,28 +59,51 @@ def load(path: str | None = None):
 
 
 # ------------------------------------------------------- torch helpers ---
+#
+# A decoding step takes a few microseconds on the GPU, so the host's part is kept
+# small: every check is one comparison on the way through, and what can be looked
+# up once is.
+
+_torch = _raw_stream = None
+
+
+def _setup():
+    """torch and the lookup of its current stream's handle, once."""
+    global _torch, _raw_stream
+    import torch
+
+    _raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream", None) or (
+        lambda index: torch.cuda.current_stream(index).cuda_stream)
+    _torch = torch
+    return torch
+
 
 def _addr(t):
     return None if t is None else t.data_ptr()
 
 
-@contextlib.contextmanager
-def _on(stream):
-    """Makes `stream` torch's current one (so that what is allocated belongs to
-    it) and yields its handle."""
-    import torch
+class _On:
+    """Makes `stream` torch's current one, so that what is allocated belongs to
+    it; `handle` is its handle. None: the current stream as it is."""
 
-    if stream is None:
-        yield torch.cuda.current_stream().cuda_stream
-    else:
-        with torch.cuda.stream(stream):
-            yield stream.cuda_stream
+    def __init__(self, stream, device):
+        self.context = None if stream is None else _torch.cuda.stream(stream)
+        self.handle = _raw_stream(device.index) if stream is None else stream.cuda_stream
+
+    def __enter__(self):
+        if self.context is not None:
+            self.context.__enter__()
+        return self.handle
+
+    def __exit__(self, *exc):
+        if self.context is not None:
+            self.context.__exit__(*exc)
 
 
 def _check_tensor(name, t, shape, dtype, device, dense=True):
-    if tuple(t.shape) != tuple(shape):
+    if t.shape != shape:
         raise ValueError(f"{name} must have the shape {tuple(shape)}, got {tuple(t.shape)}")
-    if t.dtype != dtype:
+    if t.dtype is not dtype:
         raise TypeError(f"{name} must be {dtype}, got {t.dtype}")
     if t.device != device:
         raise ValueError(f"{name} is on {t.device}, not on {device}")
@@ -85,54 +111,57 @@ def _check_tensor(name, t, shape, dtype, device, dense=True):
         raise ValueError(f"{name} must be contiguous")
 
 
-def _check_device(t):
-    import torch
-
-    if t.device.type != "cuda":
-        raise ValueError(f"tensors must be on a CUDA device, got {t.device}")
-    if t.device.index != torch.cuda.current_device():
-        raise ValueError(f"tensors are on {t.device}, but the current device is cuda:{torch.cuda.current_device()}")
+def _check_device(device):
+    if device.type != "cuda":
+        raise ValueError(f"tensors must be on a CUDA device, got {device}")
+    if device.index != _torch.cuda.current_device():
+        raise ValueError(f"tensors are on {device}, but the current device is cuda:{_torch.cuda.current_device()}")
 
 
-def _strides(*ts):
+def _is_bf16(name, t):
+    if t.dtype is _torch.bfloat16:
+        return 1
+    if t.dtype is _torch.float32:
+        return 0
+    raise TypeError(f"{name} must be float32 or bfloat16, got {t.dtype}")
+
+
+def _strides(q, k, v):
     """The strides of q, k, v for the C call, or None where all are dense."""
-    if all(t.is_contiguous() for t in ts):
+    if q.is_contiguous() and k.is_contiguous() and v.is_contiguous():
         return None
-    for name, t in zip("qkv", ts):
+    for name, t in zip("qkv", (q, k, v)):
         D = t.shape[3]
         if (t.shape[3] > 1 and t.stride(3) != 1) or (t.shape[2] > 1 and t.stride(2) != D):
             raise ValueError(f"{name}: a token's heads must be dense (strides {t.stride()})")
-    return (ctypes.c_longlong * 6)(*(x for t in ts for x in (t.stride(0), t.stride(1))))
+    return (ctypes.c_longlong * 6)(*(x for t in (q, k, v) for x in (t.stride(0), t.stride(1))))
 
 
 def _inputs(q, k, v, g, beta):
     """Checks the inputs against each other; returns bf16, (B, T, Hk, Hv, K, V), device."""
-    import torch
-
-    bf16 = wkv7._inputs_dtype(q)
+    if _torch is None:
+        _setup()
+    bf16, dtype, dev = _is_bf16("q", q), q.dtype, q.device
     if q.dim() != 4 or v.dim() != 4:
         raise ValueError("q, k and v must be [B][T][heads][size]")
     B, T, Hk, K = q.shape
-    Hv, V = v.shape[2:]
-    dev = q.device
-    _check_device(q)
-    _check_tensor("k", k, (B, T, Hk, K), q.dtype, dev, False)
-    _check_tensor("v", v, (B, T, Hv, V), q.dtype, dev, False)
-    _check_tensor("g", g, (B, T, Hv), torch.float32, dev)
-    _check_tensor("beta", beta, (B, T, Hv), torch.float32, dev)
+    Hv, V = v.shape[2], v.shape[3]
+    _check_device(dev)
+    _check_tensor("k", k, q.shape, dtype, dev, False)
+    _check_tensor("v", v, (B, T, Hv, V), dtype, dev, False)
+    _check_tensor("g", g, (B, T, Hv), _torch.float32, dev)
+    _check_tensor("beta", beta, (B, T, Hv), _torch.float32, dev)
     return bf16, (B, T, Hk, Hv, K, V), dev
 
 
 def _sequences(seq_starts, B, dev):
     """(states, nseq of the C call)."""
-    import torch
-
     if seq_starts is None:
         return B, -1
     if seq_starts.dim() != 1 or seq_starts.numel() < 1:
         raise ValueError("seq_starts must hold the sequences' starts and the last one's end")
     n = seq_starts.numel() - 1
-    _check_tensor("seq_starts", seq_starts, (n + 1,), torch.int32, dev)
+    _check_tensor("seq_starts", seq_starts, (n + 1,), _torch.int32, dev)
     return n, n
 
 
@@ -147,18 +176,16 @@ def forward(q, k, v, g, beta, s_init=None, *, scale: float | None = None, qk_l2n
     one more than the sequences; B = 1) gives packed sequences' starts.
     Returns (o, s_final, saved); saved is what ``backward`` needs (None
     without want_saved)."""
-    import torch
-
-    lib = load()
+    lib = _lib or load()
     bf16, dims, dev = _inputs(q, k, v, g, beta)
     B, T, Hk, Hv, K, V = dims
     n, nseq = _sequences(seq_starts, B, dev)
     if s_init is not None:
-        _check_tensor("s_init", s_init, (n, Hv, V, K), torch.float32, dev)
-    with _on(stream) as handle:
-        o = torch.empty((B, T, Hv, V), dtype=q.dtype, device=dev)
-        s_final = torch.empty((n, Hv, V, K), dtype=torch.float32, device=dev) if want_s_final else None
-        saved = torch.empty(lib.gdr_saved_bytes(*dims, nseq, bf16, want_saved), dtype=torch.uint8, device=dev)
+        _check_tensor("s_init", s_init, (n, Hv, V, K), _torch.float32, dev)
+    with _On(stream, dev) as handle:
+        o = _torch.empty((B, T, Hv, V), dtype=q.dtype, device=dev)
+        s_final = _torch.empty((n, Hv, V, K), dtype=_torch.float32, device=dev) if want_s_final else None
+        saved = _torch.empty(lib.gdr_saved_bytes(*dims, nseq, bf16, want_saved), dtype=_torch.uint8, device=dev)
         fn = lib.gdr_forward_bf16 if bf16 else lib.gdr_forward
         wkv7._check(fn(*(_addr(x) for x in (q, k, v, g, beta, s_init, seq_starts, o, s_final, saved)), _strides(q, k, v),
                        K ** -0.5 if scale is None else scale, qk_l2norm, want_saved, *dims, nseq, handle))
@@ -171,29 +198,27 @@ def backward(q, k, v, g, beta, do, saved, *, dS_final=None, want_dS_init: bool =
     ``forward`` of the same inputs and options. Returns dict dq, dk, dv (the
     inputs' type), dg, dbeta and dS_init (float32; None without
     want_dS_init)."""
-    import torch
-
-    lib = load()
+    lib = _lib or load()
     bf16, dims, dev = _inputs(q, k, v, g, beta)
     B, T, Hk, Hv, K, V = dims
     n, nseq = _sequences(seq_starts, B, dev)
     _check_tensor("do", do, (B, T, Hv, V), q.dtype, dev)
     if dS_final is not None:
-        _check_tensor("dS_final", dS_final, (n, Hv, V, K), torch.float32, dev)
+        _check_tensor("dS_final", dS_final, (n, Hv, V, K), _torch.float32, dev)
     need = lib.gdr_saved_bytes(*dims, nseq, bf16, 1)
     if saved is None:
         raise ValueError("saved must be what forward(..., want_saved=True) returned")
-    _check_tensor("saved", saved, (need,), torch.uint8, dev)
-    with _on(stream) as handle:
+    _check_tensor("saved", saved, (need,), _torch.uint8, dev)
+    with _On(stream, dev) as handle:
         grads = {
-            "dq": torch.empty((B, T, Hk, K), dtype=q.dtype, device=dev),
-            "dk": torch.empty((B, T, Hk, K), dtype=q.dtype, device=dev),
-            "dv": torch.empty((B, T, Hv, V), dtype=q.dtype, device=dev),
-            "dg": torch.empty((B, T, Hv), dtype=torch.float32, device=dev),
-            "dbeta": torch.empty((B, T, Hv), dtype=torch.float32, device=dev),
-            "dS_init": torch.empty((n, Hv, V, K), dtype=torch.float32, device=dev) if want_dS_init else None,
+            "dq": _torch.empty((B, T, Hk, K), dtype=q.dtype, device=dev),
+            "dk": _torch.empty((B, T, Hk, K), dtype=q.dtype, device=dev),
+            "dv": _torch.empty((B, T, Hv, V), dtype=q.dtype, device=dev),
+            "dg": _torch.empty((B, T, Hv), dtype=_torch.float32, device=dev),
+            "dbeta": _torch.empty((B, T, Hv), dtype=_torch.float32, device=dev),
+            "dS_init": _torch.empty((n, Hv, V, K), dtype=_torch.float32, device=dev) if want_dS_init else None,
         }
-        work = torch.empty(lib.gdr_backward_bytes(*dims, nseq, bf16), dtype=torch.uint8, device=dev)
+        work = _torch.empty(lib.gdr_backward_bytes(*dims, nseq, bf16), dtype=_torch.uint8, device=dev)
         fn = lib.gdr_backward_bf16 if bf16 else lib.gdr_backward
         wkv7._check(fn(*(_addr(x) for x in (q, k, v, g, beta, do, dS_final, seq_starts, saved, work)),
                        *(_addr(grads[m]) for m in ("dq", "dk", "dv", "dg", "dbeta", "dS_init")), _strides(q, k, v),
@@ -207,19 +232,21 @@ def step(q, k, v, g, beta, state, *, slots=None, scale: float | None = None, qk_
     float32 is updated in place; slots (int32 [R]) names each request's state,
     each at most once, a negative one to skip the request (its o is 0); None:
     request r has state r. Returns o."""
-    import torch
-
-    lib = load()
+    lib = _lib or load()
     bf16, dims, dev = _inputs(q, k, v, g, beta)
     R, T, Hk, Hv, K, V = dims
     if state.dim() != 4:
         raise ValueError("state must be [n][Hv][V][K]")
-    _check_tensor("state", state, (state.shape[0], Hv, V, K), torch.float32, dev)
+    n = state.shape[0]
+    _check_tensor("state", state, (n, Hv, V, K), _torch.float32, dev)
     if slots is not None:
-        _check_tensor("slots", slots, (R,), torch.int32, dev)
-    with _on(stream) as handle:
-        o = torch.empty((R, T, Hv, V), dtype=q.dtype, device=dev)
+        _check_tensor("slots", slots, (R,), _torch.int32, dev)
+    with _On(stream, dev) as handle:
+        o = _torch.empty((R, T, Hv, V), dtype=q.dtype, device=dev)
         fn = lib.gdr_step_bf16 if bf16 else lib.gdr_step
-        wkv7._check(fn(*(_addr(x) for x in (q, k, v, g, beta, state, slots, o)), _strides(q, k, v),
-                       K ** -0.5 if scale is None else scale, qk_l2norm, *dims, state.shape[0], handle))
+        rc = fn(q.data_ptr(), k.data_ptr(), v.data_ptr(), g.data_ptr(), beta.data_ptr(), state.data_ptr(), _addr(slots),
+                o.data_ptr(), _strides(q, k, v), K ** -0.5 if scale is None else scale, qk_l2norm, R, T, Hk, Hv, K, V, n,
+                handle)
+    if rc:
+        wkv7._check(rc)
     return o
