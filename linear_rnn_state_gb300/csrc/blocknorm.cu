@@ -20,6 +20,7 @@
 #include <cuda_bf16.h>
 
 #include "blocknorm_launch.h"
+#include "gdr_launch.h"
 
 namespace blocknorm {
 namespace {
@@ -180,6 +181,7 @@ __global__ void __launch_bounds__(kThreads) backward_kernel(const Args p) {
   constexpr int kRows = kThreads / kGroup, kSums = kGate ? 1 : 2;
   __shared__ float join[kRows > 1 ? kSums * kThreads * 8 : 1];
   const int tg = threadIdx.x % kGroup, sub = threadIdx.x / kGroup, D = p.D;
+  gdr::grid_go();
   float dw[kVec][8], ds[kGate ? 1 : kVec][8];
 #pragma unroll
   for (int v = 0; v < kVec; ++v)
@@ -303,6 +305,7 @@ __global__ void __launch_bounds__(kThreads) backward_kernel(const Args p) {
 // The partial rows' sums, column by column: 32 columns a block, eight threads each.
 __global__ void __launch_bounds__(kThreads) sums_kernel(const float* part, int parts, int sums, int D, float* dw, float* ds) {
   __shared__ float red[8][33];
+  gdr::grid_wait();
   const int x = threadIdx.x & 31, y = threadIdx.x >> 5, c = blockIdx.x * 32 + x, n = sums * D;
   float s = 0.f;
   if (c < n)
@@ -332,8 +335,8 @@ cudaError_t launch(const Args& p, bool backward, cudaStream_t s) {
   cudaError_t e = cudaGetLastError();
   if (e != cudaSuccess) return e;
   const int sums = kGate ? 1 : 2;
-  sums_kernel<<<(sums * p.D + 31) / 32, kThreads, 0, s>>>(p.part, parts, sums, p.D, p.dw, p.dscale);
-  return cudaGetLastError();
+  return gdr::launch_after(true, sums_kernel, (unsigned)((sums * p.D + 31) / 32), (unsigned)kThreads, 0, s, (const float*)p.part, parts, sums, p.D,
+                           p.dw, p.dscale);
 }
 // A group of threads is the least power of two with eight values each; rows
 // wider than 2048 take more pieces a thread.

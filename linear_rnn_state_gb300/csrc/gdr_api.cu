@@ -136,6 +136,7 @@ int forward_impl(bool bf16, const void* q, const void* k, const void* v, const f
   if (!rows) return copy_state(s_final, s_init, state, stream);
   a.s.starts = starts;
   a.s.l2norm = l2norm, a.s.scale = scale;
+  a.small = is_small(a.s);
   a.s.q_b = st[0], a.s.q_t = st[1], a.s.k_b = st[2], a.s.k_t = st[3], a.s.v_b = st[4], a.s.v_t = st[5];
   a.q = q, a.k = k, a.v = v, a.g = g, a.beta = beta, a.s_init = s_init, a.o = o, a.s_final = s_final;
   if ((rc = wkv7::api_status_word(&a.status))) return rc;
@@ -173,6 +174,7 @@ int backward_impl(bool bf16, const void* q, const void* k, const void* v, const 
   if (!rows) return copy_state(dS_init, dS_final, state, stream);
   a.s.starts = starts;
   a.s.l2norm = l2norm, a.s.scale = scale;
+  a.small = is_small(a.s);
   a.s.q_b = st[0], a.s.q_t = st[1], a.s.k_b = st[2], a.s.k_t = st[3], a.s.v_b = st[4], a.s.v_t = st[5];
   a.q = q, a.k = k, a.v = v, a.g = g, a.beta = beta, a.d_o = d_o, a.dS_final = dS_final;
   a.dq = dq, a.dk = dk, a.dv = dv, a.dg = dg, a.dbeta = dbeta, a.dS_init = dS_init;

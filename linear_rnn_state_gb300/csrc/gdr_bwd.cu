@@ -59,6 +59,7 @@ __global__ void __launch_bounds__((2 * kBwdChains<T, KP> + 1) * 32, 1) bwd_kerne
     wkv7::fence_mbar_init();
   }
   __syncthreads();
+  if (a.small) grid_go();
   if (warp == 2 * chains) {
     if (lane == 0) fill_images(im, a, sq.slot + n - 1, -1, n, hk, hv);
     return;

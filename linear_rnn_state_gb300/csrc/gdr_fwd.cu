@@ -62,6 +62,7 @@ __global__ void __launch_bounds__((2 * kFwdChains<T, KP> + 1) * 32, 1) fwd_kerne
     }
     wkv7::fence_mbar_init();
   }
+  grid_wait();
   __syncthreads();
   if (warp == 2 * chains) {
     if (lane == 0) fill_images(im, a, sq.slot, 1, n, hk, hv);
@@ -273,8 +274,7 @@ cudaError_t launch(const Args& a, cudaStream_t stream) {
   if (e != cudaSuccess) return e;
   const int chains = chain_warps(a.s, most), sets = (v_tiles(a.s.V) + chains - 1) / chains;
   const size_t smem = all - (most - chains) * sizeof(FwdPair<T, KP>);
-  kernel<<<(unsigned)((size_t)a.s.nseq * a.s.Hv * sets), (2 * chains + 1) * 32, smem, stream>>>(a);
-  return cudaGetLastError();
+  return launch_after(a.small, kernel, (unsigned)((size_t)a.s.nseq * a.s.Hv * sets), (2 * chains + 1) * 32, smem, stream, a);
 }
 template <typename T>
 cudaError_t pick(const Args& a, bool save, cudaStream_t s) {

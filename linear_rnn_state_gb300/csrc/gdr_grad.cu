@@ -83,7 +83,9 @@ __global__ void __launch_bounds__(kThreads<KP>, KP == 64 ? 2 : 1) grad_kernel(co
   const int g4 = lane >> 2, t4 = lane & 3;
   const int slot = blockIdx.x / a.s.Hv, hv = blockIdx.x % a.s.Hv, hk = hv / (a.s.Hv / a.s.Hk);
   ChunkAt c;
+  if (a.small) grid_go();
   if (!chunk_at(a.s, slot, c)) return;
+  grid_wait();
   const int vts = (a.s.V + kVt - 1) / kVt, K = a.s.K;
   const size_t at_k = (size_t)slot * a.s.Hk + hk, at_v = (size_t)slot * a.s.Hv + hv;
   constexpr int image = P * kC * KP * 2;
@@ -366,6 +368,7 @@ __global__ void __launch_bounds__(kThreads<KP>, KP == 64 ? 2 : 1) grad_kernel(co
 // of the normalisation. 16 lanes a row of q or k, eight keys a lane.
 template <typename T>
 __global__ void __launch_bounds__(256) join_kernel(const Args a) {
+  grid_wait();
   const size_t rows = (size_t)a.s.B * a.s.T * a.s.Hk;
   const size_t id = ((size_t)blockIdx.x * 256 + threadIdx.x) >> 4;
   const int cl = threadIdx.x & 15, group = a.s.Hv / a.s.Hk, K = a.s.K;
@@ -408,12 +411,11 @@ cudaError_t launch(const Args& a, cudaStream_t stream) {
   static std::atomic<unsigned long long> done{0};
   cudaError_t e = allow_smem(reinterpret_cast<const void*>(kernel), smem, done);
   if (e != cudaSuccess) return e;
-  kernel<<<(unsigned)((size_t)a.s.slots * a.s.Hv), kThreads<KP>, smem, stream>>>(a);
-  if ((e = cudaGetLastError()) != cudaSuccess) return e;
+  e = launch_after(a.small, kernel, (unsigned)((size_t)a.s.slots * a.s.Hv), kThreads<KP>, smem, stream, a);
+  if (e != cudaSuccess) return e;
   if (kShared) {
     const size_t rows = 2 * (size_t)a.s.B * a.s.T * a.s.Hk;
-    join_kernel<T><<<(unsigned)((rows * 16 + 255) / 256), 256, 0, stream>>>(a);
-    e = cudaGetLastError();
+    e = launch_after(a.small, join_kernel<T>, (unsigned)((rows * 16 + 255) / 256), 256, 0, stream, a);
   }
   return e;
 }

@@ -165,6 +165,7 @@ __global__ void __launch_bounds__(kThreads, 4) prep_kernel(const Args a) {
   constexpr int P = In<T>::kParts;
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
   const int slot = blockIdx.x / a.s.Hk, hk = blockIdx.x % a.s.Hk;
+  if (a.small) grid_go();
   ChunkAt c;
   if (!chunk_at(a.s, slot, c)) return;
   const size_t at_k = (size_t)slot * a.s.Hk + hk;

@@ -141,17 +141,22 @@ def _inputs(q, k, v, g, beta):
     """Checks the inputs against each other; returns bf16, (B, T, Hk, Hv, K, V), device."""
     if _torch is None:
         _setup()
-    bf16, dtype, dev = _is_bf16("q", q), q.dtype, q.device
+    dtype, dev, f32 = q.dtype, q.device, _torch.float32
     if q.dim() != 4 or v.dim() != 4:
         raise ValueError("q, k and v must be [B][T][heads][size]")
-    B, T, Hk, K = q.shape
+    B, T, Hk, K = shape = q.shape
     Hv, V = v.shape[2], v.shape[3]
-    _check_device(dev)
-    _check_tensor("k", k, q.shape, dtype, dev, False)
-    _check_tensor("v", v, (B, T, Hv, V), dtype, dev, False)
-    _check_tensor("g", g, (B, T, Hv), _torch.float32, dev)
-    _check_tensor("beta", beta, (B, T, Hv), _torch.float32, dev)
-    return bf16, (B, T, Hk, Hv, K, V), dev
+    rows = (B, T, Hv)
+    if not (dev.type == "cuda" and dev.index == _torch.cuda.current_device() and k.shape == shape and v.shape == (B, T, Hv, V)
+            and g.shape == rows and beta.shape == rows and k.dtype is dtype and v.dtype is dtype and g.dtype is f32
+            and beta.dtype is f32 and k.device == dev and v.device == dev and g.device == dev and beta.device == dev
+            and g.is_contiguous() and beta.is_contiguous()):  # say which
+        _check_device(dev)
+        _check_tensor("k", k, shape, dtype, dev, False)
+        _check_tensor("v", v, (B, T, Hv, V), dtype, dev, False)
+        _check_tensor("g", g, rows, f32, dev)
+        _check_tensor("beta", beta, rows, f32, dev)
+    return 1 if dtype is _torch.bfloat16 else _is_bf16("q", q), (B, T, Hk, Hv, K, V), dev
 
 
 def _sequences(seq_starts, B, dev):
