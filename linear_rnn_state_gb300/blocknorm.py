@@ -19,8 +19,8 @@ from .gdr import _addr, _check_device, _check_tensor, _is_bf16, _On
 EXPORTS = {
     "blocknorm_add_forward": 15,
     "blocknorm_add_backward": 19,
-    "blocknorm_gated_forward": 12,
-    "blocknorm_gated_backward": 15,
+    "blocknorm_gated_forward": 13,
+    "blocknorm_gated_backward": 16,
     "blocknorm_part_bytes": 3,
 }
 

@@ -58,6 +58,7 @@ int blocknorm_add_forward(const void* x, const void* residual, const float* weig
                           int bf16, int residual_bf16, void* stream) {
   int rc = check_dims(rows, 1, D);
   if (rc || (rc = check_types(bf16, residual_bf16))) return rc;
+  if (!rows) return WKV7_OK;  // whose buffers may all be NULL
   const int es = bf16 ? 2 : 4, rs = residual_bf16 ? 2 : 4;
   const unsigned long long m = (unsigned long long)rows * D, vec = (unsigned long long)D * 4;
   unsigned long long xb = 0, rb = 0;
@@ -71,7 +72,6 @@ int blocknorm_add_forward(const void* x, const void* residual, const float* weig
   const Span outs[3] = {{n, m * es, "n", true}, {h, m * rs, "h", x != nullptr}, {rstd, (unsigned long long)rows * 4, "rstd", false}};
   if (over && !residual) return fail(WKV7_ERR_INVALID, "residual must not be NULL");
   if ((rc = api::check_spans(ins, outs))) return rc;
-  if (!rows) return WKV7_OK;
   Args p{};
   p.a = x, p.b = residual, p.w = weight, p.scale = scale, p.out = n, p.h = h, p.rstd = rstd;
   p.rows = rows, p.a_t = x_stride, p.b_t = residual_stride, p.H = 1, p.D = D, p.eps = eps;
@@ -84,8 +84,14 @@ int blocknorm_add_backward(const void* x, const void* residual, const float* wei
                            int D, int bf16, int residual_bf16, void* stream) {
   int rc = check_dims(rows, 1, D);
   if (rc || (rc = check_types(bf16, residual_bf16))) return rc;
+  const unsigned long long vec = (unsigned long long)D * 4;
+  if (!rows) {  // no terms: the sums are 0, and every other buffer may be NULL
+    const Span none[1] = {{nullptr, 0, "", false}};
+    const Span sums[2] = {{dweight, vec, "dweight", true}, {dscale, vec, "dscale", false}};
+    return (rc = api::check_spans(none, sums)) ? rc : zero_sums(dweight, dscale, D, static_cast<cudaStream_t>(stream));
+  }
   const int es = bf16 ? 2 : 4, rs = residual_bf16 ? 2 : 4;
-  const unsigned long long m = (unsigned long long)rows * D, vec = (unsigned long long)D * 4;
+  const unsigned long long m = (unsigned long long)rows * D;
   unsigned long long xb = 0, rb = 0;
   if (!x) x_stride = D;
   if (x && (rc = span_bytes(&xb, &x_stride, rows, D, es, "x"))) return rc;
@@ -97,7 +103,6 @@ int blocknorm_add_backward(const void* x, const void* residual, const float* wei
   const Span outs[5] = {{dresidual, m * rs, "dresidual", true}, {dx, m * es, "dx", scale != nullptr}, {dweight, vec, "dweight", true},
                         {dscale, vec, "dscale", false}, {part, rows ? blocknorm_part_bytes(rows, D, 2) : 0, "part", true}};
   if ((rc = api::check_spans(ins, outs))) return rc;
-  if (!rows) return zero_sums(dweight, dscale, D, static_cast<cudaStream_t>(stream));
   Args p{};
   p.a = x, p.b = residual, p.w = weight, p.scale = scale, p.rstd = const_cast<float*>(rstd), p.dout = dn, p.dh = dh;
   p.da = dx, p.db = dresidual, p.dw = dweight, p.dscale = dscale, p.part = static_cast<float*>(part);

@@ -326,8 +326,12 @@ __global__ void __launch_bounds__(kThreads<KP>, KP == 64 ? 2 : 1) grad_kernel(co
     }
     const float after = __shfl_down_sync(0xffffffffu, s, 1);
     const float s1 = d1 + (lane < 31 ? after : 0.f);
-    if (2 * lane < c.len) a.dg[(tok + 2 * lane) * a.s.Hv + hv] = s;
-    if (2 * lane + 1 < c.len) a.dg[(tok + 2 * lane + 1) * a.s.Hv + hv] = s1;
+    // where e^g is 0 in fp32 (-inf, a reset) so is dg, without the sums' rounding
+    const int i = 2 * lane;
+    const float g0 = i ? (sc.gh[i] - sc.gh[i - 1]) + (sc.gl[i] - sc.gl[i - 1]) : sc.gh[0];
+    const float g1 = (sc.gh[i + 1] - sc.gh[i]) + (sc.gl[i + 1] - sc.gl[i]);
+    if (i < c.len) a.dg[(tok + i) * a.s.Hv + hv] = g0 < -150.f ? 0.f : s;
+    if (i + 1 < c.len) a.dg[(tok + i + 1) * a.s.Hv + hv] = g1 < -150.f ? 0.f : s1;
   }
 #pragma unroll
   for (int h = 0; h < 2; ++h) {
