@@ -82,22 +82,10 @@ def _addr(t):
     return None if t is None else t.data_ptr()
 
 
-class _On:
-    """Makes `stream` torch's current one, so that what is allocated belongs to
-    it; `handle` is its handle. None: the current stream as it is."""
-
-    def __init__(self, stream, device):
-        self.context = None if stream is None else _torch.cuda.stream(stream)
-        self.handle = _raw_stream(device.index) if stream is None else stream.cuda_stream
-
-    def __enter__(self):
-        if self.context is not None:
-            self.context.__enter__()
-        return self.handle
-
-    def __exit__(self, *exc):
-        if self.context is not None:
-            self.context.__exit__(*exc)
+def _on(stream, fn, *args, **kw):
+    """fn with `stream` torch's current one, so that what it allocates belongs to it."""
+    with (_torch or _setup()).cuda.stream(stream):
+        return fn(*args, **kw)
 
 
 def _check_tensor(name, t, shape, dtype, device, dense=True):
@@ -181,19 +169,24 @@ def forward(q, k, v, g, beta, s_init=None, *, scale: float | None = None, qk_l2n
     one more than the sequences; B = 1) gives packed sequences' starts.
     Returns (o, s_final, saved); saved is what ``backward`` needs (None
     without want_saved)."""
+    if stream is not None:
+        return _on(stream, forward, q, k, v, g, beta, s_init, scale=scale, qk_l2norm=qk_l2norm, seq_starts=seq_starts,
+                   want_saved=want_saved, want_s_final=want_s_final)
     lib = _lib or load()
     bf16, dims, dev = _inputs(q, k, v, g, beta)
     B, T, Hk, Hv, K, V = dims
     n, nseq = _sequences(seq_starts, B, dev)
     if s_init is not None:
         _check_tensor("s_init", s_init, (n, Hv, V, K), _torch.float32, dev)
-    with _On(stream, dev) as handle:
-        o = _torch.empty((B, T, Hv, V), dtype=q.dtype, device=dev)
-        s_final = _torch.empty((n, Hv, V, K), dtype=_torch.float32, device=dev) if want_s_final else None
-        saved = _torch.empty(lib.gdr_saved_bytes(*dims, nseq, bf16, want_saved), dtype=_torch.uint8, device=dev)
-        fn = lib.gdr_forward_bf16 if bf16 else lib.gdr_forward
-        wkv7._check(fn(*(_addr(x) for x in (q, k, v, g, beta, s_init, seq_starts, o, s_final, saved)), _strides(q, k, v),
-                       K ** -0.5 if scale is None else scale, qk_l2norm, want_saved, *dims, nseq, handle))
+    o = _torch.empty((B, T, Hv, V), dtype=q.dtype, device=dev)
+    s_final = _torch.empty((n, Hv, V, K), dtype=_torch.float32, device=dev) if want_s_final else None
+    saved = _torch.empty(lib.gdr_saved_bytes(B, T, Hk, Hv, K, V, nseq, bf16, want_saved), dtype=_torch.uint8, device=dev)
+    rc = (lib.gdr_forward_bf16 if bf16 else lib.gdr_forward)(
+        q.data_ptr(), k.data_ptr(), v.data_ptr(), g.data_ptr(), beta.data_ptr(), _addr(s_init), _addr(seq_starts), o.data_ptr(),
+        _addr(s_final), saved.data_ptr(), _strides(q, k, v), K ** -0.5 if scale is None else scale, qk_l2norm, want_saved, B, T,
+        Hk, Hv, K, V, nseq, _raw_stream(dev.index))
+    if rc:
+        wkv7._check(rc)
     return o, s_final, saved if want_saved else None
 
 
@@ -203,6 +196,9 @@ def backward(q, k, v, g, beta, do, saved, *, dS_final=None, want_dS_init: bool =
     ``forward`` of the same inputs and options. Returns dict dq, dk, dv (the
     inputs' type), dg, dbeta and dS_init (float32; None without
     want_dS_init)."""
+    if stream is not None:
+        return _on(stream, backward, q, k, v, g, beta, do, saved, dS_final=dS_final, want_dS_init=want_dS_init, scale=scale,
+                   qk_l2norm=qk_l2norm, seq_starts=seq_starts)
     lib = _lib or load()
     bf16, dims, dev = _inputs(q, k, v, g, beta)
     B, T, Hk, Hv, K, V = dims
@@ -214,20 +210,16 @@ def backward(q, k, v, g, beta, do, saved, *, dS_final=None, want_dS_init: bool =
     if saved is None:
         raise ValueError("saved must be what forward(..., want_saved=True) returned")
     _check_tensor("saved", saved, (need,), _torch.uint8, dev)
-    with _On(stream, dev) as handle:
-        grads = {
-            "dq": _torch.empty((B, T, Hk, K), dtype=q.dtype, device=dev),
-            "dk": _torch.empty((B, T, Hk, K), dtype=q.dtype, device=dev),
-            "dv": _torch.empty((B, T, Hv, V), dtype=q.dtype, device=dev),
-            "dg": _torch.empty((B, T, Hv), dtype=_torch.float32, device=dev),
-            "dbeta": _torch.empty((B, T, Hv), dtype=_torch.float32, device=dev),
-            "dS_init": _torch.empty((n, Hv, V, K), dtype=_torch.float32, device=dev) if want_dS_init else None,
-        }
-        work = _torch.empty(lib.gdr_backward_bytes(*dims, nseq, bf16), dtype=_torch.uint8, device=dev)
-        fn = lib.gdr_backward_bf16 if bf16 else lib.gdr_backward
-        wkv7._check(fn(*(_addr(x) for x in (q, k, v, g, beta, do, dS_final, seq_starts, saved, work)),
-                       *(_addr(grads[m]) for m in ("dq", "dk", "dv", "dg", "dbeta", "dS_init")), _strides(q, k, v),
-                       K ** -0.5 if scale is None else scale, qk_l2norm, *dims, nseq, handle))
+    def empty(like, dtype=_torch.float32):
+        return _torch.empty(like, dtype=dtype, device=dev)
+
+    grads = {"dq": empty(q.shape, q.dtype), "dk": empty(q.shape, q.dtype), "dv": empty(v.shape, q.dtype), "dg": empty(g.shape),
+             "dbeta": empty(g.shape), "dS_init": empty((n, Hv, V, K)) if want_dS_init else None}
+    work = empty(lib.gdr_backward_bytes(*dims, nseq, bf16), _torch.uint8)
+    fn = lib.gdr_backward_bf16 if bf16 else lib.gdr_backward
+    wkv7._check(fn(*(_addr(x) for x in (q, k, v, g, beta, do, dS_final, seq_starts, saved, work)),
+                   *(_addr(x) for x in grads.values()), _strides(q, k, v), K ** -0.5 if scale is None else scale, qk_l2norm, *dims,
+                   nseq, _raw_stream(dev.index)))
     return grads
 
 
@@ -237,21 +229,20 @@ def step(q, k, v, g, beta, state, *, slots=None, scale: float | None = None, qk_
     float32 is updated in place; slots (int32 [R]) names each request's state,
     each at most once, a negative one to skip the request (its o is 0); None:
     request r has state r. Returns o."""
+    if stream is not None:
+        return _on(stream, step, q, k, v, g, beta, state, slots=slots, scale=scale, qk_l2norm=qk_l2norm)
     lib = _lib or load()
-    bf16, dims, dev = _inputs(q, k, v, g, beta)
-    R, T, Hk, Hv, K, V = dims
-    if state.dim() != 4:
-        raise ValueError("state must be [n][Hv][V][K]")
-    n = state.shape[0]
-    _check_tensor("state", state, (n, Hv, V, K), _torch.float32, dev)
+    bf16, (R, T, Hk, Hv, K, V), dev = _inputs(q, k, v, g, beta)
+    shape = state.shape
+    n = shape[0] if len(shape) == 4 else 0
+    if not (shape == (n, Hv, V, K) and state.dtype is _torch.float32 and state.device == dev and state.is_contiguous()):
+        _check_tensor("state", state, (n, Hv, V, K), _torch.float32, dev)
     if slots is not None:
         _check_tensor("slots", slots, (R,), _torch.int32, dev)
-    with _On(stream, dev) as handle:
-        o = _torch.empty((R, T, Hv, V), dtype=q.dtype, device=dev)
-        fn = lib.gdr_step_bf16 if bf16 else lib.gdr_step
-        rc = fn(q.data_ptr(), k.data_ptr(), v.data_ptr(), g.data_ptr(), beta.data_ptr(), state.data_ptr(), _addr(slots),
-                o.data_ptr(), _strides(q, k, v), K ** -0.5 if scale is None else scale, qk_l2norm, R, T, Hk, Hv, K, V, n,
-                handle)
+    o = _torch.empty((R, T, Hv, V), dtype=q.dtype, device=dev)
+    rc = (lib.gdr_step_bf16 if bf16 else lib.gdr_step)(
+        q.data_ptr(), k.data_ptr(), v.data_ptr(), g.data_ptr(), beta.data_ptr(), state.data_ptr(), _addr(slots), o.data_ptr(),
+        _strides(q, k, v), K ** -0.5 if scale is None else scale, qk_l2norm, R, T, Hk, Hv, K, V, n, _raw_stream(dev.index))
     if rc:
         wkv7._check(rc)
     return o
