@@ -77,7 +77,7 @@ size_t place_saved(Buffers& b, const Shape& s, bool bf16, bool for_backward, cha
   if (for_backward) {
     b.s_img = take(l.n_t * l.st_img);
     b.u_img = take(l.n_t * l.u_img);
-    b.su = reinterpret_cast<float2*>(take(l.n_t * sizeof(float2)));
+    b.su = reinterpret_cast<float4*>(take(l.n_t * sizeof(float4)));
   }
   return at - p;
 }

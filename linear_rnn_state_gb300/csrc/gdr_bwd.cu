@@ -82,7 +82,6 @@ __global__ void __launch_bounds__((2 * kBwdChains<T, KP> + 1) * 32, 1) bwd_kerne
       const float sS = pow2_scale(s_max), inv_s = pow2_inverse(sS);
       // dS1 k^T
       float x[8][4];
-      zero(x);
       const Asked has_s(&pr.free_s, use ^ 1), has_y(&pr.full_y, use), has_t(&im.full_t, use);
       if (!has_k.wait(a.status)) return;
       if (s > 0 && !has_s.wait(a.status)) return;
@@ -94,7 +93,10 @@ __global__ void __launch_bounds__((2 * kBwdChains<T, KP> + 1) * 32, 1) bwd_kerne
         Frag<P> fk[4];
 #pragma unroll
         for (int nb = 0; nb < 4; ++nb) b_nk<P>(fk[nb], im.k[use], kC, kC * KP, 16 * nb, 16 * kt, lane);
-        mma_row<4>(x, fs, fk);
+        if (kt == 0)
+          mma_row<4, true>(x, fs, fk);
+        else
+          mma_row<4>(x, fs, fk);
       }
       if (lane == 0) pr.inv_s = inv_s;
       wkv7::fence_proxy_async_smem();
@@ -115,15 +117,17 @@ __global__ void __launch_bounds__((2 * kBwdChains<T, KP> + 1) * 32, 1) bwd_kerne
 
       // lam = T^T y
       float l[8][4];
-      zero(l);
       if (!has_t.wait(a.status)) return;
 #pragma unroll
-      for (int i = 0; i < 4; ++i) {
+      for (int i = 3; i >= 0; --i) {
         Frag<2> fy, ft[4];
         to_a(fy, x[2 * i], x[2 * i + 1], sY);
 #pragma unroll
         for (int j = 0; j <= i; ++j) b_tri_kn<2>(ft[j], im.t, i, j, lane);
-        mma_row<4>(l, fy, ft, 0, i + 1);
+        if (i == 3)
+          mma_row<4, true>(l, fy, ft);
+        else
+          mma_row<4>(l, fy, ft, 0, i + 1);
       }
       const Asked has_l(&pr.free_l, use ^ 1), has_g(&pr.full_g, use);
       const float fl = sc.inv_t * pow2_inverse(sY);
@@ -198,21 +202,23 @@ __global__ void __launch_bounds__((2 * kBwdChains<T, KP> + 1) * 32, 1) bwd_kerne
     fetch(s + 2);
     const float sD = pow2_scale(warp_max(d));
     inv_d = pow2_inverse(sD);
-    zero(x);
     if (!mbar_wait_bounded(a.status, &im.full_k[use], (s >> 1) & 1)) return false;
     if (!mbar_wait_bounded(a.status, &im.full_p, use)) return false;
     if (lane == 0) bulk_wait_read();  // the images of dS and do of the step before are out
     __syncwarp();
     if (s > 0) signal(&pr.free_s, lane);
 #pragma unroll
-    for (int i = 0; i < 4; ++i) {
+    for (int i = 3; i >= 0; --i) {
       Frag<P> fd;
       Frag<2> fp[4];
       to_a(fd, d[2 * i], d[2 * i + 1], sD);
       put_a(pr.d_img, kVt * kC, 16 * i, fd, lane);
 #pragma unroll
       for (int j = 0; j <= i; ++j) b_tri_kn<2>(fp[j], im.p, i, j, lane);
-      mma_row<4>(x, fd, fp, 0, i + 1);
+      if (i == 3)
+        mma_row<4, true>(x, fd, fp);
+      else
+        mma_row<4>(x, fd, fp, 0, i + 1);
     }
     signal(&im.free_p, lane);
     wkv7::fence_proxy_async_smem();
@@ -232,7 +238,6 @@ __global__ void __launch_bounds__((2 * kBwdChains<T, KP> + 1) * 32, 1) bwd_kerne
     }
     const float sW = pow2_scale(warp_max(d));
     float g[kNt][4];
-    zero(g);
     if (!mbar_wait_bounded(a.status, &im.full_q, use)) return false;
 #pragma unroll
     for (int j = 0; j < 4; ++j) {
@@ -241,7 +246,10 @@ __global__ void __launch_bounds__((2 * kBwdChains<T, KP> + 1) * 32, 1) bwd_kerne
       Frag<P> fq[KP / 16];
 #pragma unroll
       for (int nb = 0; nb < KP / 16; ++nb) b_kn<P>(fq[nb], im.q, kC, kC * KP, 16 * nb, 16 * j, lane);
-      mma_row<KP / 16>(g, fd, fq);
+      if (j == 0)
+        mma_row<KP / 16, true>(g, fd, fq);
+      else
+        mma_row<KP / 16>(g, fd, fq);
     }
     signal(&im.free_q, lane);
     signal(&im.free_k[use], lane);

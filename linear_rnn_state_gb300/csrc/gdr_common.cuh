@@ -149,6 +149,13 @@ __device__ __forceinline__ void mma16(float (&d)[4], const uint32_t (&a)[4], uin
       : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1));
 }
 
+// d = a b: adds to the zero register, which takes no instruction to clear d.
+__device__ __forceinline__ void mma16_first(float (&d)[4], const uint32_t (&a)[4], uint32_t b0, uint32_t b1) {
+  asm("mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, {%10,%10,%10,%10};\n"
+      : "=f"(d[0]), "=f"(d[1]), "=f"(d[2]), "=f"(d[3])
+      : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1), "f"(0.f));
+}
+
 // Fragments of m16n8k16 for one 16-deep block, from an image of `rows` rows
 // (lo part `part` halves after the hi part). With g = lane / 4, t = lane % 4
 // the accumulator holds C[g][2t, 2t+1] and C[g+8][2t, 2t+1].
@@ -217,9 +224,15 @@ __device__ __forceinline__ void put2_tri(__half* s, int row, int col, float x0, 
 }
 
 // Two n8 tiles += a b, the small terms first.
+template <bool kFirst = false>
 __device__ __forceinline__ void mma_pair(float (&d0)[4], float (&d1)[4], const uint32_t (&a)[4], const uint32_t (&b)[4]) {
-  mma16(d0, a, b[0], b[1]);
-  mma16(d1, a, b[2], b[3]);
+  if constexpr (kFirst) {
+    mma16_first(d0, a, b[0], b[1]);
+    mma16_first(d1, a, b[2], b[3]);
+  } else {
+    mma16(d0, a, b[0], b[1]);
+    mma16(d1, a, b[2], b[3]);
+  }
 }
 template <int kA, int kB>
 __device__ __forceinline__ void mma_parts(float (&d0)[4], float (&d1)[4], const Frag<kA>& a, const Frag<kB>& b) {
@@ -228,33 +241,30 @@ __device__ __forceinline__ void mma_parts(float (&d0)[4], float (&d1)[4], const 
   mma_pair(d0, d1, a.h, b.h);
 }
 
-// N pairs of n8 tiles += a b[n]: part by part over all of them, so that two mma
-// on one accumulator stand 2 N apart (a dependent mma waits about 33 cycles, an
-// independent one 8).
-template <int N, int kA, int kB, int kTilesOf>
+template <int kA, int kB>
+__device__ __forceinline__ void mma_parts_first(float (&d0)[4], float (&d1)[4], const Frag<kA>& a, const Frag<kB>& b) {
+  if constexpr (kA == 2) mma_pair<true>(d0, d1, a.l, b.h);
+  if constexpr (kB == 2) mma_pair<kA != 2>(d0, d1, a.h, b.l);
+  mma_pair<kA != 2 && kB != 2>(d0, d1, a.h, b.h);
+}
+
+// N pairs of n8 tiles += a b[n] (or, kFirst, = a b[n]): part by part over all of
+// them, so that two mma on one accumulator stand 2 N apart (a dependent mma waits
+// 38 cycles, an independent one 8 to 16). kHi: of a its hi part alone.
+template <int N, bool kFirst = false, bool kHi = false, int kA, int kB, int kTilesOf>
 __device__ __forceinline__ void mma_row(float (&d)[kTilesOf][4], const Frag<kA>& a, const Frag<kB> (&b)[N], int first = 0, int end = N) {
-  if constexpr (kA == 2)
+  constexpr bool lh = kA == 2 && !kHi, hl = kB == 2;
+  if constexpr (lh)
 #pragma unroll
     for (int n = 0; n < N; ++n)
-      if (n >= first && n < end) mma_pair(d[2 * n], d[2 * n + 1], a.l, b[n].h);
-  if constexpr (kB == 2)
+      if (n >= first && n < end) mma_pair<kFirst>(d[2 * n], d[2 * n + 1], a.l, b[n].h);
+  if constexpr (hl)
 #pragma unroll
     for (int n = 0; n < N; ++n)
-      if (n >= first && n < end) mma_pair(d[2 * n], d[2 * n + 1], a.h, b[n].l);
+      if (n >= first && n < end) mma_pair<kFirst && !lh>(d[2 * n], d[2 * n + 1], a.h, b[n].l);
 #pragma unroll
   for (int n = 0; n < N; ++n)
-    if (n >= first && n < end) mma_pair(d[2 * n], d[2 * n + 1], a.h, b[n].h);
-}
-// As mma_row, with the hi part of a alone where b has one part.
-template <int N, int kA, int kB, int kTilesOf>
-__device__ __forceinline__ void mma_row_out(float (&d)[kTilesOf][4], const Frag<kA>& a, const Frag<kB> (&b)[N], int first = 0) {
-  if constexpr (kB == 2) {
-    mma_row<N, kA, kB>(d, a, b, first);
-  } else {
-#pragma unroll
-    for (int n = 0; n < N; ++n)
-      if (n >= first) mma_pair(d[2 * n], d[2 * n + 1], a.h, b[n].h);
-  }
+    if (n >= first && n < end) mma_pair<kFirst && !lh && !hl>(d[2 * n], d[2 * n + 1], a.h, b[n].h);
 }
 
 // Two accumulator tiles (16 rows, columns k0 .. k0+7 and k0+8 .. k0+15) times s

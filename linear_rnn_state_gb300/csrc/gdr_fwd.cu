@@ -86,7 +86,6 @@ __global__ void __launch_bounds__((2 * kFwdChains<T, KP> + 1) * 32, 1) fwd_kerne
       const float sS = pow2_scale(s_max), inv_s = pow2_inverse(sS);
       // S0 k^T
       float x[8][4];
-      zero(x);
       const Asked has_s(&pr.free_s, use ^ 1), has_v(&pr.full_v[use], c >> 1), has_t(&im.full_t, use);
       if (!has_k.wait(a.status)) return;
       if (c > 0 && !has_s.wait(a.status)) return;
@@ -98,7 +97,10 @@ __global__ void __launch_bounds__((2 * kFwdChains<T, KP> + 1) * 32, 1) fwd_kerne
         Frag<P> fk[4];
 #pragma unroll
         for (int nb = 0; nb < 4; ++nb) b_nk<P>(fk[nb], im.k[use], kC, kC * KP, 16 * nb, 16 * kt, lane);
-        mma_row<4>(x, fs, fk);
+        if (kt == 0)
+          mma_row<4, true>(x, fs, fk);
+        else
+          mma_row<4>(x, fs, fk);
       }
       if (lane == 0) pr.inv_s = inv_s;
       if (kSave) wkv7::fence_proxy_async_smem();
@@ -123,7 +125,6 @@ __global__ void __launch_bounds__((2 * kFwdChains<T, KP> + 1) * 32, 1) fwd_kerne
 
       // u = T r
       float u[8][4];
-      zero(u);
       if (!has_t.wait(a.status)) return;
 #pragma unroll
       for (int j = 0; j < 4; ++j) {
@@ -131,7 +132,10 @@ __global__ void __launch_bounds__((2 * kFwdChains<T, KP> + 1) * 32, 1) fwd_kerne
         to_a(fr, x[2 * j], x[2 * j + 1], sR);
 #pragma unroll
         for (int i = j; i < 4; ++i) b_tri_nk<2>(ft[i], im.t, i, j, lane);
-        mma_row<4>(u, fr, ft, j);
+        if (j == 0)
+          mma_row<4, true>(u, fr, ft);
+        else
+          mma_row<4>(u, fr, ft, j);
       }
       const Asked has_u(&pr.free_u, use ^ 1);
       const float fu = sc.inv_t * pow2_inverse(sR);
@@ -195,7 +199,6 @@ __global__ void __launch_bounds__((2 * kFwdChains<T, KP> + 1) * 32, 1) fwd_kerne
     const Scal& sc = im.sc(use);
     // S0 q^T
     float o[8][4], x[8][4];
-    zero(o), zero(x);
     if (!mbar_wait_bounded(a.status, &im.full_k[use], (c >> 1) & 1)) return;
     if (!mbar_wait_bounded(a.status, &im.full_q, use)) return;
     if (!mbar_wait_bounded(a.status, &pr.full_s, use)) return;
@@ -209,7 +212,10 @@ __global__ void __launch_bounds__((2 * kFwdChains<T, KP> + 1) * 32, 1) fwd_kerne
       a_mk<P>(fs, pr.s, kVt, kVt * KP, 0, 16 * kt, lane);
 #pragma unroll
       for (int nb = 0; nb < 4; ++nb) b_nk<P>(fq[nb], im.q, kC, kC * KP, 16 * nb, 16 * kt, lane);
-      mma_row<4>(o, fs, fq);
+      if (kt == 0)
+        mma_row<4, true>(o, fs, fq);
+      else
+        mma_row<4>(o, fs, fq);
     }
     signal(&im.free_q, lane);
     const float inv_s = pr.inv_s, inv_p = sc.inv_p;
@@ -239,7 +245,11 @@ __global__ void __launch_bounds__((2 * kFwdChains<T, KP> + 1) * 32, 1) fwd_kerne
       if constexpr (kSave) put_a(pr.u_img, kVt * kC, 16 * j, fu, lane);
 #pragma unroll
       for (int i = j; i < 4; ++i) b_tri_nk<P>(fp[i], im.p, i, j, lane);
-      mma_row_out<4>(x, fu, fp, j);
+      constexpr bool kHi = P == 1;
+      if (j == 0)
+        mma_row<4, true, kHi>(x, fu, fp);
+      else
+        mma_row<4, false, kHi>(x, fu, fp, j);
     }
     signal(&im.free_p, lane);
     if (kSave) {
@@ -248,7 +258,7 @@ __global__ void __launch_bounds__((2 * kFwdChains<T, KP> + 1) * 32, 1) fwd_kerne
       if (lane == 0) {
         bulk_store(a.b.u_img + at_t * sizeof(pr.u_img), pr.u_img, sizeof(pr.u_img));
         bulk_commit();
-        a.b.su[at_t] = make_float2(inv_s, inv_u);
+        a.b.su[at_t] = make_float4(inv_s, inv_u, 0.f, 0.f);
       }
     }
     const float fo = inv_p * inv_u;

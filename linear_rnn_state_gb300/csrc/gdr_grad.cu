@@ -32,6 +32,8 @@ struct alignas(128) Tile {  // of 16 value columns
   __half s[2 * kVt * KP], ds[2 * kVt * KP];
   __half u[2 * kVt * kC], l[2 * kVt * kC];
   __half d[P * kVt * kC];
+  float4 su, dsl;  // their inverse scales: S0, u; dS1, lam, do
+  float4 pad[6];
 };
 constexpr int kStages = 4;
 struct alignas(128) Pairs {  // F and E as operands: columns times beta ks, and rows times qs or ks
@@ -50,7 +52,6 @@ struct alignas(128) GradSmem {
   float fd[kC];               // f_i
   float dot[4][KP / 32][kC];  // row sums of 32 keys each: q.dq, k.read, k.w, k.(e^(Gc - G) u dS1)
   float sdot[KP / 8];
-  float dG[kC];
   uint64_t bar[kStages + 1];
 };
 
@@ -89,7 +90,7 @@ __global__ void __launch_bounds__(kThreads<KP>, KP == 64 ? 2 : 1) grad_kernel(co
   const int vts = (a.s.V + kVt - 1) / kVt, K = a.s.K;
   const size_t at_k = (size_t)slot * a.s.Hk + hk, at_v = (size_t)slot * a.s.Hv + hv;
   constexpr int image = P * kC * KP * 2;
-  constexpr uint32_t kTileBytes = sizeof(Tile<P, KP>);
+  constexpr uint32_t kTileBytes = sizeof(Tile<P, KP>) - sizeof(Tile<P, KP>::pad);
 
   auto load = [&](int v) {
     Tile<P, KP>& t = sm.tile[v % kStages];
@@ -101,6 +102,8 @@ __global__ void __launch_bounds__(kThreads<KP>, KP == 64 ? 2 : 1) grad_kernel(co
     bulk_load(t.u, a.b.u_img + at * sizeof(t.u), sizeof(t.u), bar);
     bulk_load(t.l, a.b.l_img + at * sizeof(t.l), sizeof(t.l), bar);
     bulk_load(t.d, a.b.do_img + at * sizeof(t.d), sizeof(t.d), bar);
+    bulk_load(&t.su, a.b.su + at, sizeof(t.su), bar);
+    bulk_load(&t.dsl, a.b.dsl + at, sizeof(t.dsl), bar);
   };
   if (tid == 0) {
     for (int s = 0; s <= kStages; ++s) mbar_init(&sm.bar[s], 1);
@@ -120,10 +123,8 @@ __global__ void __launch_bounds__(kThreads<KP>, KP == 64 ? 2 : 1) grad_kernel(co
   float sdot = 0.f, du = 0.f, lu = 0.f;
   for (int v = 0; v < vts; ++v) {
     Tile<P, KP>& t = sm.tile[v % kStages];
-    const size_t at = at_v * vts + v;
-    const float2 su = a.b.su[at];
-    const float4 dsl = a.b.dsl[at];
     if (!mbar_wait_bounded(a.status, &sm.bar[v % kStages], (v / kStages) & 1)) return;
+    const float4 su = t.su, dsl = t.dsl;
     Frag<P> fd;
     Frag<2> fl, fu;
     a_km<P>(fd, t.d, kVt, kVt * kC, 16 * wr, 0, lane);
@@ -134,12 +135,11 @@ __global__ void __launch_bounds__(kThreads<KP>, KP == 64 ? 2 : 1) grad_kernel(co
     for (int nt = 0; nt < kNt; nt += 2) {
       Frag<2> fs, fds;
       float x[6][4];
-      zero(x);
       b_kn<2>(fs, t.s, kVt, kVt * KP, key0 + 8 * nt, 0, lane);
       b_kn<2>(fds, t.ds, kVt, kVt * KP, key0 + 8 * nt, 0, lane);
-      mma_parts<P, 2>(x[0], x[1], fd, fs);
-      mma_parts<2, 2>(x[2], x[3], fl, fs);
-      mma_parts<2, 2>(x[4], x[5], fu, fds);
+      mma_parts_first<P, 2>(x[0], x[1], fd, fs);
+      mma_parts_first<2, 2>(x[2], x[3], fl, fs);
+      mma_parts_first<2, 2>(x[4], x[5], fu, fds);
 #pragma unroll
       for (int h = 0; h < 2; ++h)
 #pragma unroll
@@ -154,11 +154,10 @@ __global__ void __launch_bounds__(kThreads<KP>, KP == 64 ? 2 : 1) grad_kernel(co
       const int jb = kNf * wc + b;
       if (jb <= wr) {
         float x[4][4];
-        zero(x);
         Frag<2> fj;
         b_kn<2>(fj, t.u, kVt, kVt * kC, 16 * jb, 0, lane);
-        mma_parts<P, 2>(x[0], x[1], fd, fj);
-        mma_parts<2, 2>(x[2], x[3], fl, fj);
+        mma_parts_first<P, 2>(x[0], x[1], fd, fj);
+        mma_parts_first<2, 2>(x[2], x[3], fl, fj);
 #pragma unroll
         for (int h = 0; h < 2; ++h)
 #pragma unroll
@@ -244,57 +243,81 @@ __global__ void __launch_bounds__(kThreads<KP>, KP == 64 ? 2 : 1) grad_kernel(co
     qs[h] = rows.qs[i], ks[h] = rows.ks[i];
   }
   const float inv[4] = {pow2_inverse(scale[0]), pow2_inverse(scale[1]), pow2_inverse(scale[2]), pow2_inverse(scale[3])};
-  float dot[4][2];
+  // (F beta) k and (E beta) k: the tokens up to the warp's rows
+  {
+    float x[kNt][4], y[kNt][4];
 #pragma unroll
-  for (int m = 0; m < 4; ++m) dot[m][0] = dot[m][1] = 0.f;
-#pragma unroll
-  for (int nt = 0; nt < kNt; nt += 2) {
-    float x[2][4], y[2][4], z[2][4], q[2][4];
-    zero(x), zero(y), zero(z), zero(q);
-#pragma unroll
-    for (int kt = 0; kt < 4; ++kt) {
-      Frag<P> fk;
-      b_kn<P>(fk, sm.k, kC, kC * KP, key0 + 8 * nt, 16 * kt, lane);
+    for (int kt = 0; kt < 4; ++kt)
       if (kt <= wr) {
         Frag<2> f, e;
         a_tri(f, sm.pairs.fb, wr, kt, lane);
         a_tri(e, sm.pairs.eb, wr, kt, lane);
-        mma_parts<2, P>(x[0], x[1], f, fk);
-        mma_parts<2, P>(y[0], y[1], e, fk);
-      }
-      if (kt >= wr) {
-        Frag<2> f, e;
-        Frag<P> fq;
-        b_kn<P>(fq, sm.q, kC, kC * KP, key0 + 8 * nt, 16 * kt, lane);
-        a_tri_t(f, sm.pairs.f, kt, wr, lane);
-        a_tri_t(e, sm.pairs.e, kt, wr, lane);
-        mma_parts<2, P>(q[0], q[1], f, fq);
-        mma_parts<2, P>(z[0], z[1], e, fk);
-      }
-    }
 #pragma unroll
-    for (int b = 0; b < 2; ++b)
-#pragma unroll
-      for (int h = 0; h < 2; ++h) {
-        const int i = i0 + 8 * h, col = key0 + 8 * (nt + b) + 2 * t4;
-        const float2 qh = pick2<P, KP>(sm.q, i, col), kh = pick2<P, KP>(sm.k, i, col);
-        const float qq[2] = {qh.x * qs[h], qh.y * qs[h]}, kk[2] = {kh.x * ks[h], kh.y * ks[h]};
-#pragma unroll
-        for (int e = 0; e < 2; ++e) {
-          const int at = 2 * h + e;
-          const float tail = ex[h] * w[nt + b][at];
-          const float d = fmaf(x[b][at], inv[0], sg[h] * dq[nt + b][at]);
-          const float r = fmaf(y[b][at], -inv[1], -eg[h] * rd[nt + b][at]);
-          const float ww = fmaf(q[b][at], inv[2], fmaf(z[b][at], -inv[3], tail));
-          dot[0][h] = fmaf(qq[e], d, dot[0][h]);
-          dot[1][h] = fmaf(kk[e], r, dot[1][h]);
-          dot[2][h] = fmaf(kk[e], ww, dot[2][h]);
-          dot[3][h] = fmaf(kk[e], tail, dot[3][h]);
-          dq[nt + b][at] = fmaf(fb[h], kk[e], d);
-          rd[nt + b][at] = fmaf(beta[h], fmaf(fdi[h], qq[e], ww), r);  // dk
+        for (int nt = 0; nt < kNt; nt += 2) {
+          Frag<P> fk;
+          b_kn<P>(fk, sm.k, kC, kC * KP, key0 + 8 * nt, 16 * kt, lane);
+          if (kt == 0) {
+            mma_parts_first<2, P>(x[nt], x[nt + 1], f, fk);
+            mma_parts_first<2, P>(y[nt], y[nt + 1], e, fk);
+          } else {
+            mma_parts<2, P>(x[nt], x[nt + 1], f, fk);
+            mma_parts<2, P>(y[nt], y[nt + 1], e, fk);
+          }
         }
       }
+#pragma unroll
+    for (int nt = 0; nt < kNt; ++nt)
+#pragma unroll
+      for (int e = 0; e < 4; ++e) {
+        dq[nt][e] = fmaf(x[nt][e], inv[0], sg[e >> 1] * dq[nt][e]);
+        rd[nt][e] = fmaf(y[nt][e], -inv[1], -eg[e >> 1] * rd[nt][e]);
+      }
   }
+  // F^T q and E^T k: the tokens from the warp's rows on
+  float q[kNt][4], z[kNt][4];
+#pragma unroll
+  for (int kt = 3; kt >= 0; --kt)
+    if (kt >= wr) {
+      Frag<2> f, e;
+      a_tri_t(f, sm.pairs.f, kt, wr, lane);
+      a_tri_t(e, sm.pairs.e, kt, wr, lane);
+#pragma unroll
+      for (int nt = 0; nt < kNt; nt += 2) {
+        Frag<P> fq, fk;
+        b_kn<P>(fq, sm.q, kC, kC * KP, key0 + 8 * nt, 16 * kt, lane);
+        b_kn<P>(fk, sm.k, kC, kC * KP, key0 + 8 * nt, 16 * kt, lane);
+        if (kt == 3) {
+          mma_parts_first<2, P>(q[nt], q[nt + 1], f, fq);
+          mma_parts_first<2, P>(z[nt], z[nt + 1], e, fk);
+        } else {
+          mma_parts<2, P>(q[nt], q[nt + 1], f, fq);
+          mma_parts<2, P>(z[nt], z[nt + 1], e, fk);
+        }
+      }
+    }
+  float dot[4][2];
+#pragma unroll
+  for (int m = 0; m < 4; ++m) dot[m][0] = dot[m][1] = 0.f;
+#pragma unroll
+  for (int nt = 0; nt < kNt; ++nt)
+#pragma unroll
+    for (int h = 0; h < 2; ++h) {
+      const int i = i0 + 8 * h, col = key0 + 8 * nt + 2 * t4;
+      const float2 qh = pick2<P, KP>(sm.q, i, col), kh = pick2<P, KP>(sm.k, i, col);
+      const float qq[2] = {qh.x * qs[h], qh.y * qs[h]}, kk[2] = {kh.x * ks[h], kh.y * ks[h]};
+#pragma unroll
+      for (int e = 0; e < 2; ++e) {
+        const int at = 2 * h + e;
+        const float tail = ex[h] * w[nt][at], d = dq[nt][at], r = rd[nt][at];
+        const float ww = fmaf(q[nt][at], inv[2], fmaf(z[nt][at], -inv[3], tail));
+        dot[0][h] = fmaf(qq[e], d, dot[0][h]);
+        dot[1][h] = fmaf(kk[e], r, dot[1][h]);
+        dot[2][h] = fmaf(kk[e], ww, dot[2][h]);
+        dot[3][h] = fmaf(kk[e], tail, dot[3][h]);
+        dq[nt][at] = fmaf(fb[h], kk[e], d);
+        rd[nt][at] = fmaf(beta[h], fmaf(fdi[h], qq[e], ww), r);  // dk
+      }
+    }
 #pragma unroll
   for (int m = 0; m < 4; ++m)
 #pragma unroll
@@ -304,20 +327,21 @@ __global__ void __launch_bounds__(kThreads<KP>, KP == 64 ? 2 : 1) grad_kernel(co
     }
   __syncthreads();
   const size_t tok = (size_t)c.b * a.s.T + c.t0;
-  if (tid < kC) {
-    const int i = tid;
-    const float b = sc.beta[i], qd = row_sum(sm.dot[0], i), kr = row_sum(sm.dot[1], i), kw = row_sum(sm.dot[2], i);
-    sm.dG[i] = qd + kr - b * kw;
-    if (i < c.len) a.dbeta[(tok + i) * a.s.Hv + hv] = fmaf(sm.fd[i], rows.qk[i], kw);
-  }
-  __syncthreads();
-  if (warp == 0) {  // dg: the suffix sums, two tokens a lane
-    float x = row_sum(sm.dot[3], 2 * lane) * sc.beta[2 * lane] + row_sum(sm.dot[3], 2 * lane + 1) * sc.beta[2 * lane + 1];
+  if (warp == 0) {  // dbeta, and dg as suffix sums, two tokens a lane
+    float dG[2], x = 0.f;
+#pragma unroll
+    for (int e = 0; e < 2; ++e) {
+      const int i = 2 * lane + e;
+      const float b = sc.beta[i], kw = row_sum(sm.dot[2], i);
+      dG[e] = row_sum(sm.dot[0], i) + row_sum(sm.dot[1], i) - b * kw;
+      x = fmaf(b, row_sum(sm.dot[3], i), x);
+      if (i < c.len) a.dbeta[(tok + i) * a.s.Hv + hv] = fmaf(sm.fd[i], rows.qk[i], kw);
+    }
     x = wkv7::group_allreduce<32>(x);
     float s0 = sm.sdot[0];
 #pragma unroll
     for (int i = 1; i < KP / 8; ++i) s0 += sm.sdot[i];
-    const float d0 = sm.dG[2 * lane], d1 = sm.dG[2 * lane + 1] + (lane == 31 ? fmaf(sc.egc, s0, x) : 0.f);
+    const float d0 = dG[0], d1 = dG[1] + (lane == 31 ? fmaf(sc.egc, s0, x) : 0.f);
     float s = d0 + d1;
 #pragma unroll
     for (int o = 1; o < 32; o <<= 1) {

@@ -91,7 +91,7 @@ struct Buffers {
   Rows* rows;
   Scal* scal;
   char *s_img, *u_img;  // the state before each chunk and the chunk's u, a tile of value columns each
-  float2* su;           // the inverse scales of those two images
+  float4* su;           // the inverse scales of those two images
   char *ds_img, *l_img, *do_img;  // the carried gradient after each chunk, lambda and do
   float4* dsl;                    // the inverse scales of those three
   float *dq_part, *dk_part;       // [B][T][Hv][K] terms of shared heads' gradients, or null
