@@ -75,9 +75,7 @@ size_t place_saved(Buffers& b, const Shape& s, bool bf16, bool for_backward, cha
   b.p_img = take(l.n_v * Layout::tp_img);
   b.scal = reinterpret_cast<Scal*>(take(l.n_v * sizeof(Scal)));
   if (for_backward) {
-    b.s_img = take(l.n_t * l.st_img);
-    b.u_img = take(l.n_t * l.u_img);
-    b.su = reinterpret_cast<float4*>(take(l.n_t * sizeof(float4)));
+    b.f_rec = take(l.n_t * l.f_rec);
   }
   return at - p;
 }
@@ -89,10 +87,7 @@ size_t place_workspace(Buffers& b, const Shape& s, bool bf16, char* p) {
     at += align128(bytes);
     return r;
   };
-  b.ds_img = take(l.n_t * l.st_img);
-  b.l_img = take(l.n_t * l.u_img);
-  b.do_img = take(l.n_t * l.do_img);
-  b.dsl = reinterpret_cast<float4*>(take(l.n_t * sizeof(float4)));
+  b.b_rec = take(l.n_t * l.b_rec);
   b.dq_part = b.dk_part = nullptr;
   if (s.Hv != s.Hk) {
     const size_t bytes = (size_t)s.B * s.T * s.Hv * s.K * 4;

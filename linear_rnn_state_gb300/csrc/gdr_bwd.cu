@@ -188,12 +188,14 @@ __global__ void __launch_bounds__((2 * kBwdChains<T, KP> + 1) * 32, 1) bwd_kerne
     copy_commit();
     if (c >= 2) rows_ask(do_at + (c - 2) * kC * row_t, row_t, kC, lane);
   };
+  constexpr Record rec = b_record(KP, P);
+  auto record_of = [&](int s) { return a.b.b_rec + (((sq.slot + n - 1 - s) * a.s.Hv + hv) * vts + vt) * rec.size; };
   float inv_d = 0.f;
   // What step s needs of do: its image, do^T P and (scale e^G do)^T q.
   auto ahead = [&](int s) {
     const int use = s & 1;
     const Scal& sc = im.sc(use);
-    const size_t at_t = ((sq.slot + n - 1 - s) * a.s.Hv + hv) * vts + vt;
+    char* record = record_of(s);
     copy_wait<1>();
     __syncwarp();
     float d[8][4], x[8][4];
@@ -224,7 +226,7 @@ __global__ void __launch_bounds__((2 * kBwdChains<T, KP> + 1) * 32, 1) bwd_kerne
     wkv7::fence_proxy_async_smem();
     __syncwarp();
     if (lane == 0) {
-      bulk_store(a.b.do_img + at_t * sizeof(pr.d_img), pr.d_img, sizeof(pr.d_img));
+      bulk_store(record + rec.d, pr.d_img, sizeof(pr.d_img));
       bulk_commit();
     }
     if (s > 0 && !mbar_wait_bounded(a.status, &pr.free_y, use ^ 1)) return false;
@@ -262,12 +264,12 @@ __global__ void __launch_bounds__((2 * kBwdChains<T, KP> + 1) * 32, 1) bwd_kerne
   if (n > 0 && !ahead(0)) return;
   for (int s = 0; s < n; ++s) {
     const int c = n - 1 - s, use = s & 1;
-    const size_t at_t = ((sq.slot + c) * a.s.Hv + hv) * vts + vt;
+    char* record = record_of(s);
     const float inv_do = inv_d;
     if (!mbar_wait_bounded(a.status, &pr.full_s, use)) return;
     const float inv_s = pr.inv_s;
     if (lane == 0) {
-      bulk_store(a.b.ds_img + at_t * sizeof(pr.s), pr.s, sizeof(pr.s));
+      bulk_store(record, pr.s, sizeof(pr.s));
       bulk_commit();
     }
     if (s + 1 < n && !ahead(s + 1)) return;
@@ -286,9 +288,9 @@ __global__ void __launch_bounds__((2 * kBwdChains<T, KP> + 1) * 32, 1) bwd_kerne
     wkv7::fence_proxy_async_smem();
     __syncwarp();
     if (lane == 0) {
-      bulk_store(a.b.l_img + at_t * sizeof(pr.l_img), pr.l_img, sizeof(pr.l_img));
+      bulk_store(record + rec.u, pr.l_img, sizeof(pr.l_img));
       bulk_commit();
-      a.b.dsl[at_t] = make_float4(inv_s, pow2_inverse(sL), inv_do, 0.f);
+      *reinterpret_cast<float4*>(record + rec.scales) = make_float4(inv_s, pow2_inverse(sL), inv_do, 0.f);
       bulk_wait_read();
     }
     __syncwarp();

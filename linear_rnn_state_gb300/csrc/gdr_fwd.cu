@@ -195,7 +195,8 @@ __global__ void __launch_bounds__((2 * kFwdChains<T, KP> + 1) * 32, 1) fwd_kerne
   fetch(0), fetch(1);
   for (int c = 0; c < n; ++c) {
     const int use = c & 1;
-    const size_t at_t = ((sq.slot + c) * a.s.Hv + hv) * vts + vt;
+    constexpr Record rec = f_record(KP, P);
+    char* record = a.b.f_rec + (((sq.slot + c) * a.s.Hv + hv) * vts + vt) * rec.size;
     const Scal& sc = im.sc(use);
     // S0 q^T
     float o[8][4], x[8][4];
@@ -203,7 +204,7 @@ __global__ void __launch_bounds__((2 * kFwdChains<T, KP> + 1) * 32, 1) fwd_kerne
     if (!mbar_wait_bounded(a.status, &im.full_q, use)) return;
     if (!mbar_wait_bounded(a.status, &pr.full_s, use)) return;
     if (kSave && lane == 0) {
-      bulk_store(a.b.s_img + at_t * sizeof(pr.s), pr.s, sizeof(pr.s));
+      bulk_store(record, pr.s, sizeof(pr.s));
       bulk_commit();
     }
 #pragma unroll
@@ -256,9 +257,9 @@ __global__ void __launch_bounds__((2 * kFwdChains<T, KP> + 1) * 32, 1) fwd_kerne
       wkv7::fence_proxy_async_smem();
       __syncwarp();
       if (lane == 0) {
-        bulk_store(a.b.u_img + at_t * sizeof(pr.u_img), pr.u_img, sizeof(pr.u_img));
+        bulk_store(record + rec.u, pr.u_img, sizeof(pr.u_img));
         bulk_commit();
-        a.b.su[at_t] = make_float4(inv_s, inv_u, 0.f, 0.f);
+        *reinterpret_cast<float4*>(record + rec.scales) = make_float4(inv_s, inv_u, 0.f, 0.f);
       }
     }
     const float fo = inv_p * inv_u;

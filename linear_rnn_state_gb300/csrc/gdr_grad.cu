@@ -28,12 +28,11 @@ template <int KP>
 constexpr int kThreads = KP / 32 * 128;
 
 template <int P, int KP>
-struct alignas(128) Tile {  // of 16 value columns
-  __half s[2 * kVt * KP], ds[2 * kVt * KP];
-  __half u[2 * kVt * kC], l[2 * kVt * kC];
-  __half d[P * kVt * kC];
-  float4 su, dsl;  // their inverse scales: S0, u; dS1, lam, do
-  float4 pad[6];
+struct alignas(128) Tile {  // of 16 value columns: the forward's record, the backward's
+  __half s[2 * kVt * KP], u[2 * kVt * kC];
+  float4 su, pad0[7];  // inverse scales: of S0, of u
+  __half ds[2 * kVt * KP], l[2 * kVt * kC], d[P * kVt * kC];
+  float4 dsl, pad1[7];  // of dS1, of lam, of do
 };
 constexpr int kStages = 4;
 struct alignas(128) Pairs {  // F and E as operands: columns times beta ks, and rows times qs or ks
@@ -90,32 +89,32 @@ __global__ void __launch_bounds__(kThreads<KP>, KP == 64 ? 2 : 1) grad_kernel(co
   const int vts = (a.s.V + kVt - 1) / kVt, K = a.s.K;
   const size_t at_k = (size_t)slot * a.s.Hk + hk, at_v = (size_t)slot * a.s.Hv + hv;
   constexpr int image = P * kC * KP * 2;
-  constexpr uint32_t kTileBytes = sizeof(Tile<P, KP>) - sizeof(Tile<P, KP>::pad);
 
   auto load = [&](int v) {
     Tile<P, KP>& t = sm.tile[v % kStages];
     uint64_t* bar = &sm.bar[v % kStages];
+    constexpr uint32_t f = f_record(KP, P).size, b = b_record(KP, P).size;
+    static_assert(sizeof(Tile<P, KP>) == f + b, "a tile is its two records");
     const size_t at = at_v * vts + v;
-    mbar_arrive_expect_tx(bar, kTileBytes);
-    bulk_load(t.s, a.b.s_img + at * sizeof(t.s), sizeof(t.s), bar);
-    bulk_load(t.ds, a.b.ds_img + at * sizeof(t.ds), sizeof(t.ds), bar);
-    bulk_load(t.u, a.b.u_img + at * sizeof(t.u), sizeof(t.u), bar);
-    bulk_load(t.l, a.b.l_img + at * sizeof(t.l), sizeof(t.l), bar);
-    bulk_load(t.d, a.b.do_img + at * sizeof(t.d), sizeof(t.d), bar);
-    bulk_load(&t.su, a.b.su + at, sizeof(t.su), bar);
-    bulk_load(&t.dsl, a.b.dsl + at, sizeof(t.dsl), bar);
+    mbar_arrive_expect_tx(bar, f + b);
+    bulk_load(t.s, a.b.f_rec + at * f, f, bar);
+    bulk_load(t.ds, a.b.b_rec + at * b, b, bar);
   };
   if (tid == 0) {
     for (int s = 0; s <= kStages; ++s) mbar_init(&sm.bar[s], 1);
     wkv7::fence_mbar_init();
-    for (int v = 0; v < kStages && v < vts; ++v) load(v);
+  }
+  __syncthreads();
+  // an issue of a bulk copy takes some 80 cycles of its thread: a warp a tile
+  if (lane == 0 && warp < kStages && warp < vts) load(warp);
+  if (lane == 0 && warp == kStages) {
     mbar_arrive_expect_tx(&sm.bar[kStages], 2 * image + sizeof(Scal) + sizeof(Rows));
     bulk_load(sm.q, a.b.q_img + at_k * image, image, &sm.bar[kStages]);
     bulk_load(sm.k, a.b.k_img + at_k * image, image, &sm.bar[kStages]);
     bulk_load(&sm.scal, a.b.scal + at_v, sizeof(Scal), &sm.bar[kStages]);
     bulk_load(&sm.rows, a.b.rows + at_k, sizeof(Rows), &sm.bar[kStages]);
   }
-  __syncthreads();
+  __syncwarp();
 
   const int key0 = wc * 32;
   float dq[kNt][4], rd[kNt][4], w[kNt][4], F[2 * kNf][4], E[2 * kNf][4];

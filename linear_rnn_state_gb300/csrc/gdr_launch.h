@@ -8,6 +8,12 @@
 #include <stddef.h>
 #include <stdint.h>
 
+#ifdef __CUDACC__
+#define GDR_BOTH __host__ __device__
+#else
+#define GDR_BOTH
+#endif
+
 namespace gdr {
 
 constexpr int kC = 64;        // tokens of a chunk
@@ -63,10 +69,25 @@ constexpr float kNear = 60.f;  // e^+-30 leaves the products of fa, fb and any f
 constexpr size_t kChainScal = 3 * kC * sizeof(float) + 128;
 static_assert(sizeof(Scal) % 128 == 0 && sizeof(Rows) % 128 == 0, "bulk copies");
 
+// Where a record holds its images (the state's or its gradient's first) and its
+// scales; pairs of fp16, do in `parts`.
+struct Record {
+  size_t u, d, scales, size;
+};
+GDR_BOTH constexpr Record f_record(int Kp, int) {
+  const size_t st = 2 * kVt * Kp * 2, u = 2 * kVt * kC * 2;
+  return {st, 0, st + u, st + u + 128};
+}
+GDR_BOTH constexpr Record b_record(int Kp, int parts) {
+  const size_t st = 2 * kVt * Kp * 2, u = 2 * kVt * kC * 2, d = (size_t)parts * kVt * kC * 2;
+  return {st, st + u, st + u + d, st + u + d + 128};
+}
+
 struct Layout {
   int Kp, vt, parts;
   size_t n_k, n_v, n_t;           // (slot, key head), (slot, value head), (slot, value head, tile) counts
-  size_t kq_img, st_img, u_img, do_img;  // bytes of one image
+  size_t kq_img;         // bytes of one image of q or k
+  size_t f_rec, b_rec;   // and of a tile's records
   static constexpr size_t tp_img = 2 * 10 * 16 * 16 * 2;  // T or P: the lower ten blocks of 16 x 16
 };
 inline Layout layout(const Shape& s, bool bf16) {
@@ -78,9 +99,8 @@ inline Layout layout(const Shape& s, bool bf16) {
   l.n_v = (size_t)s.slots * s.Hv;
   l.n_t = l.n_v * l.vt;
   l.kq_img = (size_t)l.parts * kC * l.Kp * 2;
-  l.st_img = (size_t)2 * kVt * l.Kp * 2;
-  l.u_img = (size_t)2 * kVt * kC * 2;
-  l.do_img = (size_t)l.parts * kVt * kC * 2;
+  l.f_rec = f_record(l.Kp, l.parts).size;
+  l.b_rec = b_record(l.Kp, l.parts).size;
   return l;
 }
 
@@ -90,10 +110,10 @@ struct Buffers {
   char *k_img, *q_img, *t_img, *p_img;
   Rows* rows;
   Scal* scal;
-  char *s_img, *u_img;  // the state before each chunk and the chunk's u, a tile of value columns each
-  float4* su;           // the inverse scales of those two images
-  char *ds_img, *l_img, *do_img;  // the carried gradient after each chunk, lambda and do
-  float4* dsl;                    // the inverse scales of those three
+  // A record a tile of value columns, which the gradients copy whole. Of the
+  // forward: the images of the state before the chunk and of u, their inverse
+  // scales; of the backward: of the carried gradient after it, lambda and do.
+  char *f_rec, *b_rec;
   float *dq_part, *dk_part;       // [B][T][Hv][K] terms of shared heads' gradients, or null
 };
 
