@@ -89,7 +89,7 @@ size_t place_workspace(Buffers& b, const Shape& s, bool bf16, char* p) {
   };
   b.b_rec = take(l.n_t * l.b_rec);
   b.dq_part = b.dk_part = nullptr;
-  if (s.Hv != s.Hk) {
+  if (needs_terms(s, l.parts)) {
     const size_t bytes = (size_t)s.B * s.T * s.Hv * s.K * 4;
     b.dq_part = reinterpret_cast<float*>(take(bytes));
     b.dk_part = reinterpret_cast<float*>(take(bytes));

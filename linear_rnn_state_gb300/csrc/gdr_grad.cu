@@ -15,9 +15,13 @@
 // because both sums are formed from the same images of F and E.
 // <S1, dS1> = e^Gc <S0, dS1> + sum_j beta_j k_j.(e^(Gc - G_j) u_j dS1).
 //
-// Value heads that share a key head write fp32 terms that a second kernel adds
-// in the order of the heads (no atomics), with the gradient of the
-// normalisation of q and k.
+// Value heads that share a key head: a block takes them one after the other and
+// adds their terms in shared memory where that has room (bfloat16, 128 keys, and
+// enough key heads to fill the SMs: 2 x 4095 tokens of 16 key and 32 value heads
+// 537 -> 461 us); otherwise each writes fp32 terms that a second kernel adds in the
+// order of the heads. No atomics.
+#include <type_traits>
+
 #include "gdr_common.cuh"
 
 namespace gdr {
@@ -34,24 +38,38 @@ struct alignas(128) Tile {  // of 16 value columns: the forward's record, the ba
   __half ds[2 * kVt * KP], l[2 * kVt * kC], d[P * kVt * kC];
   float4 dsl, pad1[7];  // of dS1, of lam, of do
 };
-constexpr int kStages = 4;
+// How the gradients of q and k leave a block: its one value head's, that head's
+// terms for the second kernel, or the sum over its key head's value heads.
+enum Out { kAlone, kTerms, kSum };
+constexpr int stages_of(Out out) { return out == kSum ? 3 : 4; }
+// Rows of fp32 gradients on their way out, 32 bytes apart from a multiple of 128,
+// so that the eight rows of an accumulator's store fall into different banks.
+template <int KP>
+constexpr int kRow = KP + 8;
 struct alignas(128) Pairs {  // F and E as operands: columns times beta ks, and rows times qs or ks
   __half fb[2 * kTriPart], eb[2 * kTriPart], f[2 * kTriPart], e[2 * kTriPart];
 };
-template <typename T, int KP>
+template <typename T, int KP, Out kOut>
 struct alignas(128) GradSmem {
-  static constexpr int P = In<T>::kParts;
+  static constexpr int P = In<T>::kParts, kStages = stages_of(kOut);
   __half q[P * kC * KP], k[P * kC * KP];
-  union {
+  struct Apart {  // the next head's tiles come in while this one's pairs are in use
+    Tile<P, KP> tile[kStages];
+    Pairs pairs;
+    float out[2][kC][kRow<KP>];
+  };
+  union Shared {
     Tile<P, KP> tile[kStages];
     Pairs pairs;  // once the tiles are used up
+    float out[2][kC][kRow<KP>];  // once the pairs are
   };
+  std::conditional_t<kOut == kSum, Apart, Shared> m;
   Scal scal;
   Rows rows;
   float fd[kC];               // f_i
   float dot[4][KP / 32][kC];  // row sums of 32 keys each: q.dq, k.read, k.w, k.(e^(Gc - G) u dS1)
   float sdot[KP / 8];
-  uint64_t bar[kStages + 1];
+  uint64_t bar[kStages], bar_k, bar_s;
 };
 
 template <int P, int KP>
@@ -73,56 +91,73 @@ __device__ __forceinline__ float row_sum(const float (&x)[N][kC], int i) {
   return s;
 }
 
-template <typename T, int KP, bool kShared>
+template <typename T, int KP, Out kOut>
 __global__ void __launch_bounds__(kThreads<KP>, KP == 64 ? 2 : 1) grad_kernel(const Args a) {
   extern __shared__ __align__(128) unsigned char raw[];
-  using Smem = GradSmem<T, KP>;
+  using Smem = GradSmem<T, KP, kOut>;
   constexpr int P = In<T>::kParts, kWc = KP / 32, kNt = 4, kNf = 4 / kWc;  // n8 tiles of keys, 16-blocks of F's columns
+  constexpr int kStages = Smem::kStages;
   Smem& sm = *reinterpret_cast<Smem*>(raw);
+  auto& tiles = sm.m.tile;
+  auto& pairs = sm.m.pairs;
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5, wc = warp >> 2, wr = wc & 1 ? 3 - (warp & 3) : warp & 3;
-  const int g4 = lane >> 2, t4 = lane & 3;
-  const int slot = blockIdx.x / a.s.Hv, hv = blockIdx.x % a.s.Hv, hk = hv / (a.s.Hv / a.s.Hk);
+  const int g4 = lane >> 2, t4 = lane & 3, group = a.s.Hv / a.s.Hk;
+  const int heads = kOut == kSum ? group : 1, per_slot = a.s.Hv / heads;
+  const int slot = blockIdx.x / per_slot, hv0 = blockIdx.x % per_slot * heads, hk = hv0 / group;
   ChunkAt c;
   if (a.small) grid_go();
   if (!chunk_at(a.s, slot, c)) return;
   grid_wait();
   const int vts = (a.s.V + kVt - 1) / kVt, K = a.s.K;
-  const size_t at_k = (size_t)slot * a.s.Hk + hk, at_v = (size_t)slot * a.s.Hv + hv;
+  const size_t at_k = (size_t)slot * a.s.Hk + hk, at_v0 = (size_t)slot * a.s.Hv + hv0;
   constexpr int image = P * kC * KP * 2;
 
-  auto load = [&](int v) {
-    Tile<P, KP>& t = sm.tile[v % kStages];
-    uint64_t* bar = &sm.bar[v % kStages];
+  // tile n of the block: of value head hv0 + n / vts; the heads' records follow one another
+  const int n_tiles = heads * vts;
+  auto load = [&](int n) {
+    Tile<P, KP>& t = tiles[n % kStages];
+    uint64_t* bar = &sm.bar[n % kStages];
     constexpr uint32_t f = f_record(KP, P).size, b = b_record(KP, P).size;
     static_assert(sizeof(Tile<P, KP>) == f + b, "a tile is its two records");
-    const size_t at = at_v * vts + v;
+    const size_t at = at_v0 * vts + n;
     mbar_arrive_expect_tx(bar, f + b);
     bulk_load(t.s, a.b.f_rec + at * f, f, bar);
     bulk_load(t.ds, a.b.b_rec + at * b, b, bar);
   };
+  auto load_scal = [&](int hg) {
+    mbar_arrive_expect_tx(&sm.bar_s, sizeof(Scal));
+    bulk_load(&sm.scal, a.b.scal + at_v0 + hg, sizeof(Scal), &sm.bar_s);
+  };
   if (tid == 0) {
-    for (int s = 0; s <= kStages; ++s) mbar_init(&sm.bar[s], 1);
+    for (int s = 0; s < kStages; ++s) mbar_init(&sm.bar[s], 1);
+    mbar_init(&sm.bar_k, 1), mbar_init(&sm.bar_s, 1);
     wkv7::fence_mbar_init();
   }
   __syncthreads();
   // an issue of a bulk copy takes some 80 cycles of its thread: a warp a tile
-  if (lane == 0 && warp < kStages && warp < vts) load(warp);
+  if (lane == 0 && warp < kStages && warp < n_tiles) load(warp);
   if (lane == 0 && warp == kStages) {
-    mbar_arrive_expect_tx(&sm.bar[kStages], 2 * image + sizeof(Scal) + sizeof(Rows));
-    bulk_load(sm.q, a.b.q_img + at_k * image, image, &sm.bar[kStages]);
-    bulk_load(sm.k, a.b.k_img + at_k * image, image, &sm.bar[kStages]);
-    bulk_load(&sm.scal, a.b.scal + at_v, sizeof(Scal), &sm.bar[kStages]);
-    bulk_load(&sm.rows, a.b.rows + at_k, sizeof(Rows), &sm.bar[kStages]);
+    load_scal(0);
+    mbar_arrive_expect_tx(&sm.bar_k, 2 * image + sizeof(Rows));
+    bulk_load(sm.q, a.b.q_img + at_k * image, image, &sm.bar_k);
+    bulk_load(sm.k, a.b.k_img + at_k * image, image, &sm.bar_k);
+    bulk_load(&sm.rows, a.b.rows + at_k, sizeof(Rows), &sm.bar_k);
   }
   __syncwarp();
+  const Scal& sc = sm.scal;
+  const Rows& rows = sm.rows;
+  const size_t tok = (size_t)c.b * a.s.T + c.t0;
 
+  for (int hg = 0; hg < heads; ++hg) {
+  const int hv = hv0 + hg;
   const int key0 = wc * 32;
   float dq[kNt][4], rd[kNt][4], w[kNt][4], F[2 * kNf][4], E[2 * kNf][4];
   zero(dq), zero(rd), zero(w), zero(F), zero(E);
   float sdot = 0.f, du = 0.f, lu = 0.f;
   for (int v = 0; v < vts; ++v) {
-    Tile<P, KP>& t = sm.tile[v % kStages];
-    if (!mbar_wait_bounded(a.status, &sm.bar[v % kStages], (v / kStages) & 1)) return;
+    const int n = hg * vts + v;
+    Tile<P, KP>& t = tiles[n % kStages];
+    if (!mbar_wait_bounded(a.status, &sm.bar[n % kStages], (n / kStages) & 1)) return;
     const float4 su = t.su, dsl = t.dsl;
     Frag<P> fd;
     Frag<2> fl, fu;
@@ -180,15 +215,14 @@ __global__ void __launch_bounds__(kThreads<KP>, KP == 64 ? 2 : 1) grad_kernel(co
       }
       sdot = fmaf(sd, su.x * dsl.x, sdot);
     }
-    if (v + kStages < vts) {
+    if (n + kStages < n_tiles) {
       __syncthreads();
-      if (tid == 0) load(v + kStages);
+      if (tid == 0) load(n + kStages);
     }
     du += dsl.z * su.y, lu += dsl.y * su.y;
   }
-  if (!mbar_wait_bounded(a.status, &sm.bar[kStages], 0)) return;
-  const Scal& sc = sm.scal;
-  const Rows& rows = sm.rows;
+  if (!mbar_wait_bounded(a.status, &sm.bar_k, 0)) return;
+  if (!mbar_wait_bounded(a.status, &sm.bar_s, hg & 1)) return;
 
   // F and E with their decays and factors; the diagonal of F apart. Images hold
   // magnitudes below 2^14, so |do.u| and |lam.u| are below 16 2^28 times the sum
@@ -224,10 +258,10 @@ __global__ void __launch_bounds__(kThreads<KP>, KP == 64 ? 2 : 1) grad_kernel(co
         x0 = j < i ? x0 : 0.f, x1 = j + 1 < i ? x1 : 0.f, y0 = j < i ? y0 : 0.f, y1 = j + 1 < i ? y1 : 0.f;
       }
       const float q = rows.qs[i] * scale[2], k = rows.ks[i] * scale[3];
-      put2_tri(sm.pairs.fb, i, j, x0 * (c0 * scale[0]), x1 * (c1 * scale[0]));
-      put2_tri(sm.pairs.eb, i, j, y0 * (c0 * scale[1]), y1 * (c1 * scale[1]));
-      put2_tri(sm.pairs.f, i, j, x0 * q, x1 * q);
-      put2_tri(sm.pairs.e, i, j, y0 * k, y1 * k);
+      put2_tri(pairs.fb, i, j, x0 * (c0 * scale[0]), x1 * (c1 * scale[0]));
+      put2_tri(pairs.eb, i, j, y0 * (c0 * scale[1]), y1 * (c1 * scale[1]));
+      put2_tri(pairs.f, i, j, x0 * q, x1 * q);
+      put2_tri(pairs.e, i, j, y0 * k, y1 * k);
     }
   }
   __syncthreads();
@@ -249,8 +283,8 @@ __global__ void __launch_bounds__(kThreads<KP>, KP == 64 ? 2 : 1) grad_kernel(co
     for (int kt = 0; kt < 4; ++kt)
       if (kt <= wr) {
         Frag<2> f, e;
-        a_tri(f, sm.pairs.fb, wr, kt, lane);
-        a_tri(e, sm.pairs.eb, wr, kt, lane);
+        a_tri(f, pairs.fb, wr, kt, lane);
+        a_tri(e, pairs.eb, wr, kt, lane);
 #pragma unroll
         for (int nt = 0; nt < kNt; nt += 2) {
           Frag<P> fk;
@@ -278,8 +312,8 @@ __global__ void __launch_bounds__(kThreads<KP>, KP == 64 ? 2 : 1) grad_kernel(co
   for (int kt = 3; kt >= 0; --kt)
     if (kt >= wr) {
       Frag<2> f, e;
-      a_tri_t(f, sm.pairs.f, kt, wr, lane);
-      a_tri_t(e, sm.pairs.e, kt, wr, lane);
+      a_tri_t(f, pairs.f, kt, wr, lane);
+      a_tri_t(e, pairs.e, kt, wr, lane);
 #pragma unroll
       for (int nt = 0; nt < kNt; nt += 2) {
         Frag<P> fq, fk;
@@ -325,7 +359,6 @@ __global__ void __launch_bounds__(kThreads<KP>, KP == 64 ? 2 : 1) grad_kernel(co
       if (t4 == 0) sm.dot[m][wc][i0 + 8 * h] = x;
     }
   __syncthreads();
-  const size_t tok = (size_t)c.b * a.s.T + c.t0;
   if (warp == 0) {  // dbeta, and dg as suffix sums, two tokens a lane
     float dG[2], x = 0.f;
 #pragma unroll
@@ -356,36 +389,54 @@ __global__ void __launch_bounds__(kThreads<KP>, KP == 64 ? 2 : 1) grad_kernel(co
     if (i < c.len) a.dg[(tok + i) * a.s.Hv + hv] = g0 < -150.f ? 0.f : s;
     if (i + 1 < c.len) a.dg[(tok + i + 1) * a.s.Hv + hv] = g1 < -150.f ? 0.f : s1;
   }
+  // the rows in fp32; the pairs are used up (the barrier above)
 #pragma unroll
-  for (int h = 0; h < 2; ++h) {
-    const int i = i0 + 8 * h;
-    if (i >= c.len) continue;
-    float nq = 0.f, nk = 0.f;  // q.dq and k.dk of the whole row
-    const bool norm = !kShared && a.s.l2norm;
-    if (norm) {
-      const float b = sc.beta[i], f = sm.fd[i], qk = rows.qk[i];
-      nq = fmaf(f * b, qk, row_sum(sm.dot[0], i));
-      nk = fmaf(b, fmaf(f, qk, row_sum(sm.dot[2], i)), row_sum(sm.dot[1], i));
+  for (int nt = 0; nt < kNt; ++nt)
+#pragma unroll
+    for (int h = 0; h < 2; ++h) {
+      const int i = i0 + 8 * h, col = key0 + 8 * nt + 2 * t4;
+      float2* x = reinterpret_cast<float2*>(&sm.m.out[0][i][col]);
+      float2* y = reinterpret_cast<float2*>(&sm.m.out[1][i][col]);
+      float2 p = make_float2(dq[nt][2 * h], dq[nt][2 * h + 1]), r = make_float2(rd[nt][2 * h], rd[nt][2 * h + 1]);
+      if (kOut == kSum && hg > 0) p.x += x->x, p.y += x->y, r.x += y->x, r.y += y->y;
+      *x = p, *y = r;
     }
+  if (kOut == kSum && hg + 1 < heads) {
+    __syncthreads();  // warp 0 is past the scalars
+    if (tid == 0) load_scal(hg + 1);
+  }
+  }
+  __syncthreads();
+
+  // eight keys a lane: the gradient of the normalisation, and out
+  constexpr int kLanes = KP / 8, kPass = kThreads<KP> / kLanes;
+  const int cl = tid % kLanes, col = 8 * cl;
 #pragma unroll
-    for (int nt = 0; nt < kNt; ++nt) {
-      const int col = key0 + 8 * nt + 2 * t4;
-      if (col >= K) continue;
-      float x0 = dq[nt][2 * h], x1 = dq[nt][2 * h + 1], y0 = rd[nt][2 * h], y1 = rd[nt][2 * h + 1];
-      if constexpr (kShared) {
-        const size_t at = ((tok + i) * a.s.Hv + hv) * K + col;
-        store2(a.b.dq_part + at, x0, x1);
-        store2(a.b.dk_part + at, y0, y1);
+  for (int id = tid / kLanes; id < 2 * kC; id += kPass) {
+    const bool is_k = id >= kC;
+    const int i = id % kC;
+    float d[8];
+    load8(d, &sm.m.out[is_k][i][col]);
+    if (kOut != kTerms && a.s.l2norm) {
+      const __half* im = is_k ? sm.k : sm.q;
+      float x[8], xd = 0.f;
+#pragma unroll
+      for (int e = 0; e < 4; ++e) {
+        const float2 y = pick2<P, KP>(im, i, col + 2 * e);
+        x[2 * e] = y.x, x[2 * e + 1] = y.y;
+      }
+#pragma unroll
+      for (int e = 0; e < 8; ++e) xd = fmaf(x[e], d[e], xd);
+      xd = wkv7::group_allreduce<kLanes>(xd);
+      const float s = is_k ? rows.ks[i] : rows.qs[i], r = is_k ? rows.rk[i] : rows.rq[i], f = -s * s * xd;
+#pragma unroll
+      for (int e = 0; e < 8; ++e) d[e] = r * fmaf(f, x[e], d[e]);
+    }
+    if (i < c.len && col < K) {
+      if constexpr (kOut == kTerms) {
+        store8((is_k ? a.b.dk_part : a.b.dq_part) + ((tok + i) * a.s.Hv + hv0) * K + col, d);
       } else {
-        if (norm) {
-          const float2 qh = pick2<P, KP>(sm.q, i, col), kh = pick2<P, KP>(sm.k, i, col);
-          const float rq = rows.rq[i], rk = rows.rk[i];
-          x0 = rq * fmaf(-qh.x * rows.qs[i], nq, x0), x1 = rq * fmaf(-qh.y * rows.qs[i], nq, x1);
-          y0 = rk * fmaf(-kh.x * rows.ks[i], nk, y0), y1 = rk * fmaf(-kh.y * rows.ks[i], nk, y1);
-        }
-        const size_t at = ((tok + i) * a.s.Hk + hk) * K + col;
-        store2(static_cast<T*>(a.dq) + at, x0, x1);
-        store2(static_cast<T*>(a.dk) + at, y0, y1);
+        store8(static_cast<T*>(is_k ? a.dk : a.dq) + ((tok + i) * a.s.Hk + hk) * K + col, d);
       }
     }
   }
@@ -426,29 +477,30 @@ __global__ void __launch_bounds__(256) join_kernel(const Args a) {
   }
   if (in) {
     T* out = static_cast<T*>(is_k ? a.dk : a.dq) + row * K + cl * 8;
-#pragma unroll
-    for (int e = 0; e < 4; ++e) store2(out + 2 * e, d[2 * e], d[2 * e + 1]);
+    store8(out, d);
   }
 }
 
-template <typename T, int KP, bool kShared>
+template <typename T, int KP, Out kOut>
 cudaError_t launch(const Args& a, cudaStream_t stream) {
-  constexpr size_t smem = sizeof(GradSmem<T, KP>);
-  auto kernel = grad_kernel<T, KP, kShared>;
+  constexpr size_t smem = sizeof(GradSmem<T, KP, kOut>);
+  static_assert(smem <= 227 * 1024, "shared memory of a block");
+  auto kernel = grad_kernel<T, KP, kOut>;
   static std::atomic<unsigned long long> done{0};
   cudaError_t e = allow_smem(reinterpret_cast<const void*>(kernel), smem, done);
   if (e != cudaSuccess) return e;
-  e = launch_after(a.small, kernel, (unsigned)((size_t)a.s.slots * a.s.Hv), kThreads<KP>, smem, stream, a);
-  if (e != cudaSuccess) return e;
-  if (kShared) {
-    const size_t rows = 2 * (size_t)a.s.B * a.s.T * a.s.Hk;
-    e = launch_after(a.small, join_kernel<T>, (unsigned)((rows * 16 + 255) / 256), 256, 0, stream, a);
-  }
-  return e;
+  const size_t blocks = (size_t)a.s.slots * (kOut == kSum ? a.s.Hk : a.s.Hv);
+  e = launch_after(a.small, kernel, (unsigned)blocks, kThreads<KP>, smem, stream, a);
+  if (e != cudaSuccess || kOut != kTerms) return e;
+  const size_t rows = 2 * (size_t)a.s.B * a.s.T * a.s.Hk;
+  return launch_after(a.small, join_kernel<T>, (unsigned)((rows * 16 + 255) / 256), 256, 0, stream, a);
 }
 template <typename T, int KP>
 cudaError_t pick(const Args& a, cudaStream_t s) {
-  return a.s.Hv == a.s.Hk ? launch<T, KP, false>(a, s) : launch<T, KP, true>(a, s);
+  if (a.s.Hv == a.s.Hk) return launch<T, KP, kAlone>(a, s);
+  if constexpr (sums_in_block(In<T>::kParts, KP))
+    if (!needs_terms(a.s, In<T>::kParts)) return launch<T, KP, kSum>(a, s);
+  return launch<T, KP, kTerms>(a, s);
 }
 
 }  // namespace

@@ -168,6 +168,13 @@ __device__ __forceinline__ void grid_wait() { asm volatile("griddepcontrol.wait;
 __device__ __forceinline__ void grid_go() { asm volatile("griddepcontrol.launch_dependents;" ::: "memory"); }
 #endif
 
+// The gradients of shared heads: summed in the block that makes them all, where
+// shared memory has room for the sums and the key heads fill the SMs, or terms.
+constexpr bool sums_in_block(int parts, int Kp) { return parts == 1 && Kp == 128; }
+inline bool needs_terms(const Shape& s, int parts) {
+  return s.Hv != s.Hk && !(sums_in_block(parts, padded_k(s.K)) && (long long)s.slots * s.Hk >= 152);
+}
+
 struct StepArgs {
   const void *q, *k, *v;
   const float *g, *beta;
