@@ -9,8 +9,9 @@
 // the chain kernels copy into shared memory, with their scales and the tokens'
 // factors (gdr_launch.h, Rows and Scal).
 //
-// The decay ratios. G is summed in double and kept as two floats, so that no
-// difference of it is rounded. g below -200 counts as -200 (e^-200 is 0 in fp32
+// The decay ratios. G is summed and kept as an unrounded sum of two floats, so
+// that no difference of it is rounded (doubles took 3600 of a chunk's 31000
+// cycles). g below -200 counts as -200 (e^-200 is 0 in fp32
 // either way), which makes -inf a reset of the state instead of inf - inf.
 // Where G spans at most 60 in the chunk, r_ij is the product of a row's and a
 // column's factor, two multiplications an element; elsewhere it is the
@@ -18,14 +19,14 @@
 //
 // T in fp32: the four diagonal 16 x 16 blocks by forward substitution, a column
 // a thread, then blocks joined two by two, [T1 0; -T2 L21 T1 T2], 16 and then
-// 32 wide.
+// 32 wide, the products of the joins on the tensor cores in fp16 pairs (as fp32
+// multiply-adds they took 7000 of a chunk's 31000 cycles).
 #include "gdr_common.cuh"
 
 namespace gdr {
 namespace {
 
 constexpr int kThreads = 128;
-constexpr int kLx = 36;
 constexpr int kLd = 68;  // row stride of the fp32 64 x 64 tiles: rows stay 16-byte aligned
 
 template <typename T, int KP>
@@ -33,7 +34,6 @@ struct alignas(128) PrepSmem {
   static constexpr int P = In<T>::kParts;
   __half q[P * kC * KP], k[P * kC * KP];
   float L[kC * kLd];            // L, and then T in its place
-  float x[32 * kLx];            // L21 T1 in between
   __half out[2 * kTriPart];     // the image of P, then of T
   Rows rows;
   Scal scal;
@@ -99,7 +99,9 @@ struct RowLoader {
         float s2 = 0.f;
 #pragma unroll
         for (int e = 0; e < 8; ++e) s2 = fmaf(x[e], x[e], s2);
-        r = 1.f / sqrtf(wkv7::group_allreduce<kLanes>(s2) + 1e-6f);
+        s2 = wkv7::group_allreduce<kLanes>(s2) + 1e-6f;
+        r = rsqrtf(s2);
+        r = fmaf(0.5f * r, fmaf(-s2 * r, r, 1.f), r);  // a Newton step: the last bits
       }
       uint32_t hi[4], lo[4];
 #pragma unroll
@@ -109,6 +111,47 @@ struct RowLoader {
       if constexpr (P == 2) *reinterpret_cast<uint4*>(image + kC * KP + at) = make_uint4(lo[0], lo[1], lo[2], lo[3]);
       if (cl == 0) inv[row] = pow2_inverse(sc) * r, rn[row] = r;
     }
+  }
+};
+
+// A number as the unrounded sum of two floats.
+struct Two {
+  float h, l;
+};
+__device__ __forceinline__ Two sum2(Two a, Two b) {
+  const float s = __fadd_rn(a.h, b.h), c = __fsub_rn(s, a.h);
+  const float e = __fadd_rn(__fadd_rn(__fsub_rn(a.h, __fsub_rn(s, c)), __fsub_rn(b.h, c)), __fadd_rn(a.l, b.l));
+  const float h = __fadd_rn(s, e);
+  return {h, __fsub_rn(e, __fsub_rn(h, s))};
+}
+
+// Operands of 16 x 16 pieces of fp32 tiles, as pairs at a common scale: load,
+// largest of the warp, split.
+struct Raw {
+  float v[8];
+  // A[m][k] = s[m0 + m][k0 + k]
+  __device__ __forceinline__ void a(const float* s, int m0, int k0, int lane) {
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+      const float2 x = *reinterpret_cast<const float2*>(s + (m0 + (lane >> 2) + 8 * (i & 1)) * kLd + k0 + 2 * (lane & 3) + 8 * (i >> 1));
+      v[2 * i] = x.x, v[2 * i + 1] = x.y;
+    }
+  }
+  // B[k][n] = s[k0 + k][n0 + n]
+  __device__ __forceinline__ void b(const float* s, int k0, int n0, int lane) {
+#pragma unroll
+    for (int i = 0; i < 8; ++i)
+      v[i] = s[(k0 + 2 * (lane & 3) + (i & 1) + 8 * ((i >> 1) & 1)) * kLd + n0 + (lane >> 2) + 8 * (i >> 2)];
+  }
+  __device__ __forceinline__ float largest() const {
+    float m = 0.f;
+#pragma unroll
+    for (int i = 0; i < 8; ++i) m = fmaxf(m, fabsf(v[i]));
+    return m;
+  }
+  __device__ __forceinline__ void split(Frag<2>& f, float s) const {
+#pragma unroll
+    for (int i = 0; i < 4; ++i) split2<2>(v[2 * i] * s, v[2 * i + 1] * s, f.h[i], f.l[i]);
   }
 };
 
@@ -125,41 +168,13 @@ __device__ __forceinline__ float block_max(float x, float* red, int tid) {
   return m;
 }
 
-// X[i][j] = sign sum_m A[i][m] B[m][j] for the thread's R rows from r and C
-// columns from c, m < N; rows of A and B 16-byte aligned.
-template <int R, int C, int N>
-__device__ __forceinline__ void small_product(float (&x)[R][C], const float* A, int lda, const float* B, int ldb, int r, int c) {
-#pragma unroll
-  for (int i = 0; i < R; ++i)
-#pragma unroll
-    for (int j = 0; j < C; ++j) x[i][j] = 0.f;
-#pragma unroll 4
-  for (int m = 0; m < N; m += 4) {
-    float4 a[R];
-#pragma unroll
-    for (int i = 0; i < R; ++i) a[i] = *reinterpret_cast<const float4*>(A + (r + i) * lda + m);
-#pragma unroll
-    for (int q = 0; q < 4; ++q) {
-      float b[C];
-      if constexpr (C == 4) {
-        const float4 v = *reinterpret_cast<const float4*>(B + (m + q) * ldb + c);
-        b[0] = v.x, b[1] = v.y, b[2] = v.z, b[3] = v.w;
-      } else {
-        const float2 v = *reinterpret_cast<const float2*>(B + (m + q) * ldb + c);
-        b[0] = v.x, b[1] = v.y;
-      }
-#pragma unroll
-      for (int i = 0; i < R; ++i) {
-        const float s = q == 0 ? a[i].x : q == 1 ? a[i].y : q == 2 ? a[i].z : a[i].w;
-#pragma unroll
-        for (int j = 0; j < C; ++j) x[i][j] = fmaf(s, b[j], x[i][j]);
-      }
-    }
-  }
-}
-
+// Blocks that an SM's shared memory takes; registers are shared out for as many.
 template <typename T, int KP>
-__global__ void __launch_bounds__(kThreads, 4) prep_kernel(const Args a) {
+constexpr int kBlocks = 227 * 1024 / (sizeof(PrepSmem<T, KP>) + 1024) < 4 ? 227 * 1024 / (sizeof(PrepSmem<T, KP>) + 1024) : 4;
+
+// kOne: each key head has one value head, and the grams end with its P and L.
+template <typename T, int KP, bool kOne>
+__global__ void __launch_bounds__(kThreads, kBlocks<T, KP>) prep_kernel(const Args a) {
   extern __shared__ __align__(128) unsigned char raw[];
   PrepSmem<T, KP>& sm = *reinterpret_cast<PrepSmem<T, KP>*>(raw);
   constexpr int P = In<T>::kParts;
@@ -169,7 +184,7 @@ __global__ void __launch_bounds__(kThreads, 4) prep_kernel(const Args a) {
   ChunkAt c;
   if (!chunk_at(a.s, slot, c)) return;
   const size_t at_k = (size_t)slot * a.s.Hk + hk;
-  const int g4 = lane >> 2, t4 = lane & 3, group = a.s.Hv / a.s.Hk;
+  const int g4 = lane >> 2, t4 = lane & 3, group = kOne ? 1 : a.s.Hv / a.s.Hk;
   float gin[2] = {0.f, 0.f}, bin[2] = {0.f, 0.f};  // warp 0: g and beta of tokens 2 lane, 2 lane + 1
   auto load_gates = [&](int hv) {
     if (warp == 0)
@@ -232,15 +247,15 @@ __global__ void __launch_bounds__(kThreads, 4) prep_kernel(const Args a) {
     const int hv = hk * group + hg;
     const size_t at_v = (size_t)slot * a.s.Hv + hv;
     if (warp == 0) {  // the running sum of g, two tokens a lane
-      const double x[2] = {gin[0] < -200.f ? -200.f : gin[0], gin[1] < -200.f ? -200.f : gin[1]};
-      double s = x[0] + x[1];
+      const float x[2] = {gin[0] < -200.f ? -200.f : gin[0], gin[1] < -200.f ? -200.f : gin[1]};
+      Two s = sum2({x[0], 0.f}, {x[1], 0.f});
 #pragma unroll
       for (int o = 1; o < 32; o <<= 1) {
-        const double y = __shfl_up_sync(0xffffffffu, s, o);
-        if (lane >= o) s += y;
+        const Two y = {__shfl_up_sync(0xffffffffu, s.h, o), __shfl_up_sync(0xffffffffu, s.l, o)};
+        if (lane >= o) s = sum2(s, y);
       }
-      const double G[2] = {s - x[1], s}, Gc = __shfl_sync(0xffffffffu, s, 31);
-      float top = fmaxf((float)G[0], (float)G[1]), low = fminf((float)G[0], (float)G[1]);
+      const Two G[2] = {sum2(s, {-x[1], 0.f}), s}, Gc = {__shfl_sync(0xffffffffu, s.h, 31), __shfl_sync(0xffffffffu, s.l, 31)};
+      float top = fmaxf(G[0].h, G[1].h), low = fminf(G[0].h, G[1].h);
 #pragma unroll
       for (int o = 1; o < 32; o <<= 1) {
         top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, o));
@@ -251,12 +266,12 @@ __global__ void __launch_bounds__(kThreads, 4) prep_kernel(const Args a) {
 #pragma unroll
       for (int e = 0; e < 2; ++e) {
         const int i = 2 * lane + e;
-        const float b = bin[e], hi = (float)G[e], lo = (float)(G[e] - hi), th = (float)(Gc - G[e]), tl = (float)(Gc - G[e] - th);
-        const float mh = (float)(G[e] - mid), ml = (float)(G[e] - mid - mh);
-        const float eg = expf(hi) * (1.f + lo), w = expf(th) * (1.f + tl) * b, fa = expf(mh) * (1.f + ml), fb = expf(-mh) * (1.f - ml);
+        const Two tail = sum2(Gc, {-G[e].h, -G[e].l}), m = sum2(G[e], {-mid, 0.f});
+        const float b = bin[e], eg = expf(G[e].h) * (1.f + G[e].l), w = expf(tail.h) * (1.f + tail.l) * b;
+        const float fa = expf(m.h) * (1.f + m.l), fb = expf(-m.h) * (1.f - m.l);
         const float qs = sm.rows.qs[i], ks = sm.rows.ks[i];
         Scal& o = sm.scal;
-        o.beta[i] = b, o.gh[i] = hi, o.gl[i] = lo, o.eg[i] = eg, o.fa[i] = fa, o.fb[i] = fb;
+        o.beta[i] = b, o.gh[i] = G[e].h, o.gl[i] = G[e].l, o.eg[i] = eg, o.fa[i] = fa, o.fb[i] = fb;
         o.ek[i] = eg * ks, o.wk[i] = w * ks, o.eq[i] = a.s.scale * eg * qs;
         sm.pa[i] = a.s.scale * qs * fa, sm.la[i] = ks * fa, sm.cb[i] = b * ks * fb;
         bk = abs_max(bk, b * ks), qm = abs_max(qm, qs), km = abs_max(km, ks);
@@ -265,9 +280,9 @@ __global__ void __launch_bounds__(kThreads, 4) prep_kernel(const Args a) {
       // the largest e^(G_i - G_j), j <= i, is 1 unless some g is positive
       const bool grows = __any_sync(0xffffffffu, x[0] > 0 || x[1] > 0);
       if (lane == 31) {
-        const float ch = (float)Gc, cl = (float)(Gc - ch), r = grows ? expf(top - low) : 1.f, sr = fabsf(a.s.scale) * r;
+        const float r = grows ? expf(top - low) : 1.f, sr = fabsf(a.s.scale) * r;
         Scal& o = sm.scal;
-        o.egc = expf(ch) * (1.f + cl);
+        o.egc = expf(Gc.h) * (1.f + Gc.l);
         o.near = top - low <= kNear ? 1.f : 0.f;
         o.fb_max = sr * bk, o.eb_max = r * bk, o.f_max = sr * qm, o.e_max = r * km;
       }
@@ -347,34 +362,85 @@ __global__ void __launch_bounds__(kThreads, 4) prep_kernel(const Args a) {
       for (int i = 0; i < 16; ++i) D[i * kLd + j] = col[i];
     }
     __syncthreads();
-    {
-      const int pair = tid >> 6, r = ((tid >> 3) & 7) * 2, cc = (tid & 7) * 2;
-      float* T1 = sm.L + 32 * pair * (kLd + 1);
-      float *L21 = T1 + 16 * kLd, *X = sm.x + 16 * pair * kLx;
-      float x[2][2];
-      small_product<2, 2, 16>(x, L21, kLd, T1, kLd, r, cc);
+    if (warp < 2) {  // 16 wide: T21 = -(T2 L21) T1 of rows and columns 32 warp ..
+      float* T1 = sm.L + 32 * warp * (kLd + 1);
+      Raw ra, rb, rc;
+      ra.a(T1, 16, 16, lane), rb.b(T1, 16, 0, lane), rc.b(T1, 0, 0, lane);
+      const float sa = pow2_scale(warp_max_abs(ra.largest())), sb = pow2_scale(warp_max_abs(rb.largest())),
+                  sc = pow2_scale(warp_max_abs(rc.largest()));
+      Frag<2> fa, fb, fc;
+      ra.split(fa, sa), rb.split(fb, sb), rc.split(fc, sc);
+      float x[2][4], y[2][4];
+      mma_parts_first<2, 2>(x[0], x[1], fa, fb);
+      const float sx = pow2_scale(warp_max(x));
+      to_a(fa, x[0], x[1], sx);
+      mma_parts_first<2, 2>(y[0], y[1], fa, fc);
+      const float f = -pow2_inverse(sa) * pow2_inverse(sb) * pow2_inverse(sx) * pow2_inverse(sc);
 #pragma unroll
-      for (int i = 0; i < 2; ++i) *reinterpret_cast<float2*>(X + (r + i) * kLx + cc) = make_float2(x[i][0], x[i][1]);
-      __syncthreads();
-      small_product<2, 2, 16>(x, L21 + 16, kLd, X, kLx, r, cc);
+      for (int n = 0; n < 2; ++n)
 #pragma unroll
-      for (int i = 0; i < 2; ++i) *reinterpret_cast<float2*>(L21 + (r + i) * kLd + cc) = make_float2(-x[i][0], -x[i][1]);
+        for (int h = 0; h < 2; ++h)
+          *reinterpret_cast<float2*>(T1 + (16 + g4 + 8 * h) * kLd + 8 * n + 2 * t4) = make_float2(f * y[n][2 * h], f * y[n][2 * h + 1]);
     }
     __syncthreads();
-    {
-      const int r = (tid >> 3) * 2, cc = (tid & 7) * 4;
-      float *L21 = sm.L + 32 * kLd, x[2][4];
-      // the 16 x 16 block above the diagonal of T1 and of T2 still holds what L's buffer held
-      *reinterpret_cast<float4*>(sm.L + 32 * (tid >> 6) * (kLd + 1) + ((tid >> 2) & 15) * kLd + 16 + (tid & 3) * 4) =
-          make_float4(0.f, 0.f, 0.f, 0.f);
-      __syncthreads();
-      small_product<2, 4, 32>(x, L21, kLd, sm.L, kLd, r, cc);
+    {  // 32 wide: a warp has 16 rows (block mb) of T2 L21, and 16 columns (nh) of its product with T1
+      const int mb = warp >> 1, nh = warp & 1;
+      float* L21 = sm.L + 32 * kLd;
+      float x[4][4], y[2][4];
+      float inv_x;
+      {
+        Raw ra[2], rb[2][2];
+        float ma = 0.f, mx = 0.f;
 #pragma unroll
-      for (int i = 0; i < 2; ++i) *reinterpret_cast<float4*>(sm.x + (r + i) * kLx + cc) = make_float4(x[i][0], x[i][1], x[i][2], x[i][3]);
-      __syncthreads();
-      small_product<2, 4, 32>(x, L21 + 32, kLd, sm.x, kLx, r, cc);
+        for (int k = 0; k < 2; ++k)
+          if (k <= mb) {
+            ra[k].a(L21, 16 * mb, 32 + 16 * k, lane);
+            ma = fmaxf(ma, ra[k].largest());
 #pragma unroll
-      for (int i = 0; i < 2; ++i) *reinterpret_cast<float4*>(L21 + (r + i) * kLd + cc) = make_float4(-x[i][0], -x[i][1], -x[i][2], -x[i][3]);
+            for (int n = 0; n < 2; ++n) {
+              rb[k][n].b(L21, 16 * k, 16 * n, lane);
+              mx = fmaxf(mx, rb[k][n].largest());
+            }
+          }
+        const float sa = pow2_scale(warp_max_abs(ma)), sb = pow2_scale(warp_max_abs(mx));
+        inv_x = pow2_inverse(sa) * pow2_inverse(sb);
+#pragma unroll
+        for (int k = 0; k < 2; ++k)
+          if (k <= mb) {
+            Frag<2> fa, fb[2];
+            ra[k].split(fa, sa);
+#pragma unroll
+            for (int n = 0; n < 2; ++n) rb[k][n].split(fb[n], sb);
+            if (k == 0)
+              mma_row<2, true>(x, fa, fb);
+            else
+              mma_row<2>(x, fa, fb);
+          }
+      }
+      const float sx = pow2_scale(warp_max(x));
+      Raw rc[2];
+      float mc = 0.f;
+#pragma unroll
+      for (int k = 1; k >= 0; --k)
+        if (k >= nh) rc[k].b(sm.L, 16 * k, 16 * nh, lane), mc = fmaxf(mc, rc[k].largest());
+      const float sc = pow2_scale(warp_max_abs(mc)), f = -inv_x * pow2_inverse(sx) * pow2_inverse(sc);
+#pragma unroll
+      for (int k = 1; k >= 0; --k)
+        if (k >= nh) {
+          Frag<2> fx, fc;
+          to_a(fx, x[2 * k], x[2 * k + 1], sx);
+          rc[k].split(fc, sc);
+          if (k == 1)
+            mma_parts_first<2, 2>(y[0], y[1], fx, fc);
+          else
+            mma_parts<2, 2>(y[0], y[1], fx, fc);
+        }
+      __syncthreads();  // every warp has read L21
+#pragma unroll
+      for (int n = 0; n < 2; ++n)
+#pragma unroll
+        for (int h = 0; h < 2; ++h)
+          *reinterpret_cast<float2*>(L21 + (16 * mb + g4 + 8 * h) * kLd + 16 * nh + 8 * n + 2 * t4) = make_float2(f * y[n][2 * h], f * y[n][2 * h + 1]);
     }
     __syncthreads();
     // two neighbours of a row at a time: ten blocks of 128 pairs
@@ -411,14 +477,19 @@ __global__ void __launch_bounds__(kThreads, 4) prep_kernel(const Args a) {
   if (tid == 0) bulk_wait_all();
 }
 
-template <typename T, int KP>
+template <typename T, int KP, bool kOne>
 cudaError_t launch(const Args& a, cudaStream_t stream) {
   constexpr size_t smem = sizeof(PrepSmem<T, KP>);
   static std::atomic<unsigned long long> done{0};
-  cudaError_t e = allow_smem(reinterpret_cast<const void*>(prep_kernel<T, KP>), smem, done);
+  cudaError_t e = allow_smem(reinterpret_cast<const void*>(prep_kernel<T, KP, kOne>), smem, done);
   if (e != cudaSuccess) return e;
-  prep_kernel<T, KP><<<(unsigned)((size_t)a.s.slots * a.s.Hk), kThreads, smem, stream>>>(a);
+  prep_kernel<T, KP, kOne><<<(unsigned)((size_t)a.s.slots * a.s.Hk), kThreads, smem, stream>>>(a);
   return cudaGetLastError();
+}
+
+template <typename T, int KP>
+cudaError_t launch(const Args& a, cudaStream_t stream) {
+  return a.s.Hv == a.s.Hk ? launch<T, KP, true>(a, stream) : launch<T, KP, false>(a, stream);
 }
 
 }  // namespace
