@@ -131,9 +131,10 @@ __device__ __forceinline__ int img(int rows, int row, int col) {
   return (col >> 6) * rows * 64 + row * 64 + ((((col >> 3) & 7) ^ (row & 7)) << 3) + (col & 7);
 }
 
-// Lower triangular images: the block (i, j), j <= i < 4, and a place in it.
+// Lower triangular images: the block (i, j), j <= i < 4, and a place in it. The
+// blocks of a column follow one another.
 constexpr int kTriPart = 10 * 256;
-__device__ __forceinline__ int tri_block(int i, int j) { return (i * (i + 1) / 2 + j) * 256; }
+__host__ __device__ constexpr int tri_block(int i, int j) { return (j * (7 - j) / 2 + i) * 256; }
 __device__ __forceinline__ int tri_at(int row, int col) { return row * 16 + (((col >> 3) ^ ((row >> 2) & 1)) << 3) + (col & 7); }
 
 __device__ __forceinline__ void ldsm4(uint32_t (&r)[4], const __half* p) {

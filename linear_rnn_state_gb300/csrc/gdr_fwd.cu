@@ -1,291 +1,434 @@
 // The gated delta rule's forward chain: the states from chunk to chunk, and o.
 //
 // With T, P, the decays and the images of q and k from the parallel pass
-// (gdr_prep.cu), for the 16 rows of the state that a warp owns (gdr_chain.cuh),
-// all transposed (rows: value columns):
+// (gdr_prep.cu), for 64 rows of the state (value columns) a block, all
+// transposed (rows: value columns):
 //   r^T = v^T - e^G (S0 k^T)                    chain
 //   u^T = r^T T^T                               chain
 //   S1  = e^Gc S0 + (wk u)^T k                  chain
-//   o^T = scale e^G (S0 q^T) + u^T P^T          helper
-// T and P have their lower blocks only: a block (i, j) meets only the tokens j
-// of r and the tokens i of the result.
+//   o^T = scale e^G (S0 q^T) + u^T P^T          helpers
+// Every product has the 64 rows as its m and goes to the tensor cores as one
+// batch of tcgen05 instructions (gdr_tc.cuh). Between two batches a warp has 16
+// of the rows in registers: it reads its accumulator tiles from tensor memory,
+// scales them, splits them to fp16 pairs at the exact maximum of its own values,
+// and writes them back as rows of the next batch's operand.
+//
+// What bounds it is the latency of a step: three batches that wait for one
+// another, each some 700 cycles of products, hand-over and conversion. So the
+// chain's four warps make only what the next state waits for, and four helper
+// warps beside them (which reach the same rows) make o and move the rows and
+// images to and from memory. Two warps wait for operands and issue the products,
+// one fills the chunk's images.
+// kSave: the images of S0 and u go to memory for the backward.
 //
 // Arithmetic: fp16 pairs in everything that the states depend on. o of
 // bfloat16 calls takes S0, u and P with their hi part alone (11 bits against
-// the 8 that o is rounded to: 0.0003 of o's error of 0.0017), which saves 72 of
-// 312 mma a step at 64 keys.
+// the 8 that o is rounded to: 0.0003 of o's error of 0.0017).
 #include "gdr_chain.cuh"
+#include "gdr_tc.cuh"
 
 namespace gdr {
 namespace {
 
-// What a chain and its helper share.
-template <typename T, int KP>
-struct alignas(128) FwdPair {
-  unsigned char v[2][kRowsBytes<T>];
-  union {  // the helper's ways to memory
+constexpr int kWarps = 4;  // of 16 rows each: chain warps, and as many helpers
+constexpr int kFiller = 2 * kWarps, kIssuer = kFiller + 1, kHelpersIssuer = kIssuer + 1, kThreads = (kHelpersIssuer + 1) * 32;
+
+template <typename T, int KP, bool kSave>
+struct alignas(1024) FwdSmem {
+  static constexpr int P = In<T>::kParts, kPlaces = P * KP >= 256 ? 1 : 2;  // of v: what fits
+  __half k[2][P * kC * KP], q[P * kC * KP];
+  __half s[kSave ? kWarps : 1][2 * kVt * KP];  // images of S0 on their way to memory
+  union {
+    __half u[2 * kVt * kC];  // and of u
     unsigned char o[kRowsBytes<T>];
-    __half u_img[2 * kVt * kC];
-  };
-  __half s[2 * kVt * KP];  // the image of S0
-  float4 u[8 * 32];        // u as accumulator tiles
-  float inv_s;
-  uint64_t full_s, full_u, full_v[2], free_s, free_u;
+  } out[kWarps];
+  __half t[2 * kTriPart], p[P * kTriPart];
+  unsigned char v[kWarps][kPlaces][kRowsBytes<T>];
+  unsigned char scal[2][kChainScal];
+  float inv_s[kWarps], inv_r[kWarps];  // inverse scales of the warps' rows
+  uint64_t full_k[2], full_q, full_t, full_p, free_k[2], free_q, free_t, free_p;
+  uint64_t done_x, done_q, done_u, done_w, done_o, end[2];  // products
+  uint64_t ready_s, ready_r, ready_w, ready_u;  // operands in tensor memory
+  uint64_t full_s[kWarps], full_u[kWarps], full_v[kWarps][2], free_v[kWarps], free_s, free_u;
+  uint32_t tmem;
+  __device__ __forceinline__ const Scal& sc(int place) const { return *reinterpret_cast<const Scal*>(scal[place]); }
 };
-template <typename T, int KP>
-constexpr int kFwdChains = 4;
-template <typename T, int KP>
-struct FwdSmem {
-  Images<In<T>::kParts, KP, In<T>::kParts> im;
-  FwdPair<T, KP> pair[kFwdChains<T, KP>];
+
+// Tensor memory, columns: the products x (and then the state's), S0 q^T, u and
+// u P^T (which for 128 keys takes u's place); the operands S0, r (and then wk u)
+// and u, hi and lo.
+template <int KP>
+struct Columns {
+  static constexpr uint32_t x = 0, q = KP, u = KP + 64, o = KP == 64 ? u + 64 : u;
+  static constexpr uint32_t s_in = 256, r_in = s_in + KP, u_in = r_in + 64, all = 512;
+};
+
+// The warp that fills the chunk's images; lane 0 of it.
+template <typename T, int KP, bool kSave>
+__device__ __forceinline__ void fill(FwdSmem<T, KP, kSave>& m, const Args& a, long long slot, int n, int hk, int hv) {
+  constexpr int P = In<T>::kParts, image = P * kC * KP * 2, tri = kTriPart * 2;
+  auto at_k = [&](int c) { return (size_t)(slot + c) * a.s.Hk + hk; };
+  auto at_v = [&](int c) { return (size_t)(slot + c) * a.s.Hv + hv; };
+  auto k = [&](int c) {
+    uint64_t* bar = &m.full_k[c & 1];
+    mbar_arrive_expect_tx(bar, image + kChainScal);
+    bulk_load(m.k[c & 1], a.b.k_img + at_k(c) * image, image, bar);
+    bulk_load(m.scal[c & 1], a.b.scal + at_v(c), kChainScal, bar);
+  };
+  auto one = [&](void* to, const char* from, uint32_t bytes, uint64_t* bar) {
+    mbar_arrive_expect_tx(bar, bytes);
+    bulk_load(to, from, bytes, bar);
+  };
+  auto q = [&](int c) { one(m.q, a.b.q_img + at_k(c) * image, image, &m.full_q); };
+  auto t = [&](int c) { one(m.t, a.b.t_img + at_v(c) * Layout::tp_img, 2 * tri, &m.full_t); };
+  auto p = [&](int c) { one(m.p, a.b.p_img + at_v(c) * Layout::tp_img, P * tri, &m.full_p); };
+  auto ask = [&](int c) {  // into L2
+    if (c >= n) return;
+    bulk_prefetch(a.b.k_img + at_k(c) * image, image);
+    bulk_prefetch(a.b.q_img + at_k(c) * image, image);
+    bulk_prefetch(a.b.t_img + at_v(c) * Layout::tp_img, 2 * tri);
+    bulk_prefetch(a.b.p_img + at_v(c) * Layout::tp_img, P * tri);
+    bulk_prefetch(a.b.scal + at_v(c), kChainScal);
+  };
+  k(0), t(0), q(0), p(0);
+  if (n > 1) k(1);
+  ask(2);
+  int c = 1;
+  for (; c < n; ++c) {  // in the order in which step c - 1 gives the places up
+    if (!mbar_wait_bounded(a.status, &m.free_q, (c - 1) & 1)) break;
+    q(c);
+    if (!mbar_wait_bounded(a.status, &m.free_t, (c - 1) & 1)) break;
+    t(c);
+    if (!mbar_wait_bounded(a.status, &m.free_k[(c - 1) & 1], ((c - 1) >> 1) & 1)) break;
+    if (c + 1 < n) k(c + 1);
+    if (!mbar_wait_bounded(a.status, &m.free_p, (c - 1) & 1)) break;
+    p(c);
+    ask(c + 2);
+  }
+  if (c < n) {  // given up: no copy is left in flight
+    for (uint64_t* b : {&m.full_k[0], &m.full_k[1], &m.full_q, &m.full_t, &m.full_p}) {
+      mbar_wait_bounded(nullptr, b, 0, 1000000);
+      mbar_wait_bounded(nullptr, b, 1, 1000000);
+    }
+  }
+}
+
+// A wait that a warp gives up on once: from then on it goes through its steps
+// without waiting (all accesses are in bounds whatever the data), so that the
+// block's barriers and its tensor memory are left in order.
+struct Patience {
+  unsigned* status;
+  bool ok = true;
+  __device__ __forceinline__ void operator()(const Asked& b) {
+    if (ok) ok = b.wait(status);
+  }
+  __device__ __forceinline__ void operator()(uint64_t* bar, uint32_t parity) {
+    if (ok) ok = mbar_wait_bounded(status, bar, parity & 1);
+  }
 };
 
 template <typename T, int KP, bool kSave>
-__global__ void __launch_bounds__((2 * kFwdChains<T, KP> + 1) * 32, 1) fwd_kernel(const Args a) {
-  extern __shared__ __align__(128) unsigned char raw[];
-  constexpr int P = In<T>::kParts, kNt = KP / 8;
-  FwdSmem<T, KP>& sm = *reinterpret_cast<FwdSmem<T, KP>*>(raw);
-  const int chains = blockDim.x / 64, warp = threadIdx.x >> 5, lane = threadIdx.x & 31, t4 = lane & 3;
-  const int vts = (a.s.V + kVt - 1) / kVt, sets = (vts + chains - 1) / chains;
+__global__ void __launch_bounds__(kThreads, 1) fwd_kernel(const Args a) {
+  extern __shared__ __align__(1024) unsigned char raw[];
+  constexpr int P = In<T>::kParts, kNt = KP / 8, kPlaces = FwdSmem<T, KP, kSave>::kPlaces;
+  using Col = Columns<KP>;
+  using Smem = FwdSmem<T, KP, kSave>;
+  Smem& sm = *reinterpret_cast<Smem*>(raw + (-smem_addr(raw) & 1023u));
+  const int warp = __shfl_sync(0xffffffffu, threadIdx.x >> 5, 0), lane = threadIdx.x & 31, t4 = lane & 3, own = warp & 3;
+  const int vts = (a.s.V + kVt - 1) / kVt, sets = (vts + kWarps - 1) / kWarps;
   const int set = blockIdx.x % sets, hv = blockIdx.x / sets % a.s.Hv, seq = blockIdx.x / (sets * a.s.Hv);
   const int hk = hv / (a.s.Hv / a.s.Hk);
-  const SeqRange sq = seq_range(a.s, seq);
-  const int n = (sq.t1 - sq.t0 + kC - 1) / kC;
-  const int K = a.s.K, V = a.s.V;
-  auto& im = sm.im;
   if (threadIdx.x == 0) {
-    init_images(im, min(chains, vts - set * chains));
-    for (int i = 0; i < chains; ++i) {
-      FwdPair<T, KP>& p = sm.pair[i];
-      for (uint64_t* b : {&p.full_s, &p.full_u, &p.free_s, &p.free_u}) mbar_init(b, 1);
-      mbar_init(&p.full_v[0], 32), mbar_init(&p.full_v[1], 32);
+    for (uint64_t* b : {&sm.full_k[0], &sm.full_k[1], &sm.full_q, &sm.full_t, &sm.full_p, &sm.free_q, &sm.free_t, &sm.free_p,
+                        &sm.done_x, &sm.done_q, &sm.done_u, &sm.done_w, &sm.done_o, &sm.end[0], &sm.end[1]})
+      mbar_init(b, 1);
+    for (uint64_t* b : {&sm.free_k[0], &sm.free_k[1]}) mbar_init(b, 2 * kWarps + 1);
+    for (uint64_t* b : {&sm.free_s, &sm.free_u, &sm.ready_s, &sm.ready_r, &sm.ready_w, &sm.ready_u}) mbar_init(b, kWarps);
+    for (int i = 0; i < kWarps; ++i) {
+      for (uint64_t* b : {&sm.full_s[i], &sm.full_u[i], &sm.free_v[i]}) mbar_init(b, 1);
+      mbar_init(&sm.full_v[i][0], 32), mbar_init(&sm.full_v[i][1], 32);
     }
     wkv7::fence_mbar_init();
   }
+  if (warp == kFiller) wkv7::tmem_alloc(&sm.tmem, Col::all);
   grid_wait();
+  tmem_fence_before_sync();
   __syncthreads();
-  if (warp == 2 * chains) {
-    if (lane == 0) fill_images(im, a, sq.slot, 1, n, hk, hv);
-    return;
-  }
-  const int own = warp % chains, vt = set * chains + own;
-  if (vt >= vts) return;
-  FwdPair<T, KP>& pr = sm.pair[own];
-  const int cols = V - vt * kVt, tokens = sq.t1 - sq.t0;
-  const T* v_at = static_cast<const T*>(a.v) + sq.b * a.s.v_b + sq.t0 * a.s.v_t + (size_t)hv * V + vt * kVt;
+  tmem_fence_after_sync();
+  const SeqRange sq = seq_range(a.s, seq);
+  const int n = (sq.t1 - sq.t0 + kC - 1) / kC;
+  const int K = a.s.K, V = a.s.V, vt = set * kWarps + own;
+  const int cols = V - vt * kVt, tokens = sq.t1 - sq.t0;  // cols <= 0: this warp's rows are zeros
+  const uint32_t tmem = sm.tmem, mine = tmem + ((uint32_t)own << 21);  // this warp's lanes
+  const T* v_at = static_cast<const T*>(a.v) + sq.b * a.s.v_b + sq.t0 * a.s.v_t + (size_t)hv * V + (cols > 0 ? vt * kVt : 0);
+  Patience wait{a.status};
+  constexpr int kPartK = kC * KP;  // halves from an image's hi part to its lo part
 
-  if (warp < chains) {  // ------------------------------------------------ chain
+  if (warp == kFiller) {
+    if (lane == 0 && n > 0) fill(sm, a, sq.slot, n, hk, hv);
+  } else if (warp == kIssuer) {
+    for (int c = 0; c < n; ++c) {
+      const int use = c & 1;
+      const uint32_t k_at = smem_addr(sm.k[use]), q_at = smem_addr(sm.q);
+      wait(&sm.full_k[use], c >> 1);
+      wait(&sm.ready_s, use);
+      tmem_fence_after_sync();
+      if (elected()) {
+        tc_product<2, P>(tmem + Col::x, product_of(64, false), KP / 16, tmem + Col::s_in,
+                         [&](int part, int ks) { return desc_k(k_at + part * kPartK * 2, ks); });
+        tc_commit(&sm.done_x);
+      }
+      wait(&sm.full_q, use);
+      if (elected()) {
+        tc_product<P, P>(tmem + Col::q, product_of(64, false), KP / 16, tmem + Col::s_in,
+                         [&](int part, int ks) { return desc_k(q_at + part * kPartK * 2, ks); });
+        tc_commit(&sm.done_q);
+        tc_commit(&sm.free_q);
+      }
+      wait(&sm.full_t, use);
+      if (c > 0) wait(&sm.free_u, use ^ 1);
+      wait(&sm.ready_r, use);
+      tmem_fence_after_sync();
+      if (elected()) {
+        tc_product_tri<2, 2>(tmem + Col::u, tmem + Col::r_in, smem_addr(sm.t));
+        tc_commit(&sm.done_u);
+        tc_commit(&sm.free_t);
+      }
+      wait(&sm.ready_w, use);
+      tmem_fence_after_sync();
+      if (elected()) {
+        tc_product<2, P>(tmem + Col::x, product_of(KP, true), 4, tmem + Col::r_in,
+                         [&](int part, int ks) { return desc_mn(k_at + part * kPartK * 2, ks); });
+        tc_commit(&sm.done_w);
+        tc_commit(&sm.free_k[use]);
+      }
+    }
+    if (elected()) tc_commit(&sm.end[0]);
+    mbar_wait_bounded(a.status, &sm.end[0], 0);
+  } else if (warp == kHelpersIssuer) {
+    for (int c = 0; c < n; ++c) {
+      const int use = c & 1;
+      wait(&sm.full_p, use);
+      wait(&sm.ready_u, use);
+      tmem_fence_after_sync();
+      if (elected()) {
+        tc_product_tri<P, P>(tmem + Col::o, tmem + Col::u_in, smem_addr(sm.p));
+        tc_commit(&sm.done_o);
+        tc_commit(&sm.free_p);
+      }
+    }
+    if (elected()) tc_commit(&sm.end[1]);
+    mbar_wait_bounded(a.status, &sm.end[1], 0);
+  } else if (warp < kWarps) {  // ------------------------------------------ chain
     const size_t state_at = (((size_t)seq * a.s.Hv + hv) * V + vt * kVt) * K;
     float S[kNt][4];
     load_state(S, a.s_init ? a.s_init + state_at : nullptr, cols, K, lane);
     float s_max = warp_max(S);
-    Asked has_k(&im.full_k[0], 0);
+    Asked has_s(&sm.free_s, 1);
+    auto ready = [&](uint64_t* bar) {  // what was stored to tensor memory is there
+      tc_stored();
+      tmem_fence_before_sync();
+      signal(bar, lane);
+    };
     for (int c = 0; c < n; ++c) {
-      const int use = c & 1;
-      const Scal& sc = im.sc(use);
+      const int use = c & 1, place = kPlaces == 2 ? use : 0;
+      const Scal& sc = sm.sc(use);
+      // S0 k^T and S0 q^T
       const float sS = pow2_scale(s_max), inv_s = pow2_inverse(sS);
-      // S0 k^T
-      float x[8][4];
-      const Asked has_s(&pr.free_s, use ^ 1), has_v(&pr.full_v[use], c >> 1), has_t(&im.full_t, use);
-      if (!has_k.wait(a.status)) return;
-      if (c > 0 && !has_s.wait(a.status)) return;
+      Operand64<2> f[KP / 64];
 #pragma unroll
-      for (int kt = 0; kt < KP / 16; ++kt) {
-        Frag<2> fs;
-        to_a(fs, S[2 * kt], S[2 * kt + 1], sS);
-        put_a(pr.s, kVt * KP, 16 * kt, fs, lane);
-        Frag<P> fk[4];
+      for (int i = 0; i < KP / 64; ++i) f[i].split(S + 8 * i, sS);
+      if (c > 0) wait(has_s);
 #pragma unroll
-        for (int nb = 0; nb < 4; ++nb) b_nk<P>(fk[nb], im.k[use], kC, kC * KP, 16 * nb, 16 * kt, lane);
-        if (kt == 0)
-          mma_row<4, true>(x, fs, fk);
-        else
-          mma_row<4>(x, fs, fk);
+      for (int i = 0; i < KP / 64; ++i) f[i].store(mine + Col::s_in + 32 * i, KP / 2);
+      ready(&sm.ready_s);
+      const Asked has_k(&sm.full_k[use], c >> 1), has_v(&sm.full_v[own][place], kPlaces == 2 ? c >> 1 : c);
+      if (lane == 0) sm.inv_s[own] = inv_s;
+      if constexpr (kSave) {
+#pragma unroll
+        for (int i = 0; i < KP / 64; ++i) f[i].put(sm.s[own], kVt * KP, 64 * i, lane);
+        wkv7::fence_proxy_async_smem();
       }
-      if (lane == 0) pr.inv_s = inv_s;
-      if (kSave) wkv7::fence_proxy_async_smem();
-      signal(&pr.full_s, lane);
+      signal(&sm.full_s[own], lane);
 
       // r
-      if (!has_v.wait(a.status)) return;
+      float x[8][4];
       {
+        wait(has_k);
+        float2 ek[8];
+#pragma unroll
+        for (int nt = 0; nt < 8; ++nt)
+          ek[nt] = mul2(*reinterpret_cast<const float2*>(sc.ek + 8 * nt + 2 * t4), make_float2(-inv_s, -inv_s));
+        wait(has_v);
         float v[8][4];
-        rows_get(v, pr.v[use], lane, v_at);
+        rows_get(v, sm.v[own][place], lane, v_at);
+        if (kPlaces == 1) signal(&sm.free_v[own], lane);
+        wait(&sm.done_x, use);
+        tmem_fence_after_sync();
+        tc_load(x, mine + Col::x);
+        tc_loaded(x);
 #pragma unroll
-        for (int nt = 0; nt < 8; ++nt) {
-          const float2 f = *reinterpret_cast<const float2*>(sc.ek + 8 * nt + 2 * t4);
-          const float f0 = -f.x * inv_s, f1 = -f.y * inv_s;
+        for (int nt = 0; nt < 8; ++nt)
 #pragma unroll
-          for (int h = 0; h < 4; h += 2) {
-            x[nt][h] = fmaf(f0, x[nt][h], v[nt][h]), x[nt][h + 1] = fmaf(f1, x[nt][h + 1], v[nt][h + 1]);
-          }
-        }
+          for (int h = 0; h < 2; ++h) set_pair(x[nt], h, fma2(ek[nt], pair_of(x[nt], h), pair_of(v[nt], h)));
       }
       const float sR = pow2_scale(warp_max(x));
+      const float fu = sc.inv_t * pow2_inverse(sR);
+      {
+        Operand64<2> fr;
+        fr.split(x, sR), fr.store(mine + Col::r_in, 32);
+      }
+      ready(&sm.ready_r);
 
       // u = T r
-      float u[8][4];
-      if (!has_t.wait(a.status)) return;
+      float2 wk[8];
 #pragma unroll
-      for (int j = 0; j < 4; ++j) {
-        Frag<2> fr, ft[4];
-        to_a(fr, x[2 * j], x[2 * j + 1], sR);
-#pragma unroll
-        for (int i = j; i < 4; ++i) b_tri_nk<2>(ft[i], im.t, i, j, lane);
-        if (j == 0)
-          mma_row<4, true>(u, fr, ft);
-        else
-          mma_row<4>(u, fr, ft, j);
-      }
-      const Asked has_u(&pr.free_u, use ^ 1);
-      const float fu = sc.inv_t * pow2_inverse(sR);
+      for (int nt = 0; nt < 8; ++nt)
+        wk[nt] = mul2(*reinterpret_cast<const float2*>(sc.wk + 8 * nt + 2 * t4), make_float2(fu, fu));
+      const float egc = sc.egc;
+      wait(&sm.done_u, use);
+      tmem_fence_after_sync();
+      if (lane == 0) sm.inv_r[own] = fu;  // the helpers are past the one before
+      tc_load(x, mine + Col::u);
+      tc_loaded(x);
+
+      // wk u, and the state
 #pragma unroll
       for (int nt = 0; nt < 8; ++nt)
 #pragma unroll
-        for (int e = 0; e < 4; ++e) u[nt][e] *= fu;
-      if (c > 0 && !has_u.wait(a.status)) return;
-      tiles_put(pr.u, u, 1.f, lane);
-      signal(&pr.full_u, lane);
-
-      // S1: the products are added to S0 at their own scale, which is kept
-      // below 2^60 of S0's so that S0 stays finite in it
-#pragma unroll
-      for (int nt = 0; nt < 8; ++nt) {
-        const float2 f = *reinterpret_cast<const float2*>(sc.wk + 8 * nt + 2 * t4);
-#pragma unroll
-        for (int h = 0; h < 4; h += 2) u[nt][h] *= f.x, u[nt][h + 1] *= f.y;
+        for (int h = 0; h < 2; ++h) set_pair(x[nt], h, mul2(pair_of(x[nt], h), wk[nt]));
+      const float sW = pow2_scale(warp_max(x)), inv_w = pow2_inverse(sW);
+      {
+        Operand64<2> fw;
+        fw.split(x, sW), fw.store(mine + Col::r_in, 32);
       }
-      const float sW = fminf(pow2_scale(warp_max(u)), sS * 0x1p60f), egc = sc.egc * sW;
+      ready(&sm.ready_w);
+      signal(&sm.full_u[own], lane);  // only now: the helper beside has its work while this warp waits
+      signal(&sm.free_k[use], lane);
+      has_s = Asked(&sm.free_s, use);
 #pragma unroll
       for (int nt = 0; nt < kNt; ++nt)
 #pragma unroll
-        for (int e = 0; e < 4; ++e) S[nt][e] *= egc;
+        for (int h = 0; h < 2; ++h) set_pair(S[nt], h, mul2(pair_of(S[nt], h), make_float2(egc, egc)));
+      wait(&sm.done_w, use);
+      tmem_fence_after_sync();
 #pragma unroll
-      for (int j = 0; j < 4; ++j) {
-        Frag<2> fw;
-        to_a(fw, u[2 * j], u[2 * j + 1], sW);
-        Frag<P> fk[KP / 16];
+      for (int half = 0; half < KP / 64; ++half) {
+        tc_load(x, mine + Col::x + 64 * half);
+        tc_loaded(x);
 #pragma unroll
-        for (int nb = 0; nb < KP / 16; ++nb) b_kn<P>(fk[nb], im.k[use], kC, kC * KP, 16 * nb, 16 * j, lane);
-        mma_row<KP / 16>(S, fw, fk);
+        for (int nt = 0; nt < 8; ++nt)
+#pragma unroll
+          for (int h = 0; h < 2; ++h) {
+            float(&s)[4] = S[8 * half + nt];
+            set_pair(s, h, fma2(make_float2(inv_w, inv_w), pair_of(x[nt], h), pair_of(s, h)));
+          }
       }
-      has_k = Asked(&im.full_k[use ^ 1], (c + 1) >> 1);
-      signal(&im.free_k[use], lane);
-      const float inv_w = pow2_inverse(sW);
-#pragma unroll
-      for (int nt = 0; nt < kNt; ++nt)
-#pragma unroll
-        for (int e = 0; e < 4; ++e) S[nt][e] *= inv_w;
       s_max = warp_max(S);
     }
-    if (a.s_final) store_state(S, a.s_final + state_at, cols, K, lane);
-    return;
-  }
-
-  // ------------------------------------------------------------------- helper
-  T* o_at = static_cast<T*>(a.o) + (((size_t)sq.b * a.s.T + sq.t0) * a.s.Hv + hv) * V + vt * kVt;
-  const long long o_t = (long long)a.s.Hv * V;
-  auto fetch = [&](int c) {  // v of chunk c, and a request for a later one
-    if (c < n) {
-      rows_in(pr.v[c & 1], v_at + c * kC * a.s.v_t, a.s.v_t, tokens - c * kC, cols, lane);
-      copy_arrive(&pr.full_v[c & 1]);
-    }
-    if (c + 2 < n) rows_ask(v_at + (c + 2) * kC * a.s.v_t, a.s.v_t, tokens - (c + 2) * kC, lane);
-  };
-  fetch(0), fetch(1);
-  for (int c = 0; c < n; ++c) {
-    const int use = c & 1;
-    constexpr Record rec = f_record(KP, P);
-    char* record = a.b.f_rec + (((sq.slot + c) * a.s.Hv + hv) * vts + vt) * rec.size;
-    const Scal& sc = im.sc(use);
-    // S0 q^T
-    float o[8][4], x[8][4];
-    if (!mbar_wait_bounded(a.status, &im.full_k[use], (c >> 1) & 1)) return;
-    if (!mbar_wait_bounded(a.status, &im.full_q, use)) return;
-    if (!mbar_wait_bounded(a.status, &pr.full_s, use)) return;
-    if (kSave && lane == 0) {
-      bulk_store(record, pr.s, sizeof(pr.s));
-      bulk_commit();
-    }
-#pragma unroll
-    for (int kt = 0; kt < KP / 16; ++kt) {
-      Frag<P> fs, fq[4];
-      a_mk<P>(fs, pr.s, kVt, kVt * KP, 0, 16 * kt, lane);
-#pragma unroll
-      for (int nb = 0; nb < 4; ++nb) b_nk<P>(fq[nb], im.q, kC, kC * KP, 16 * nb, 16 * kt, lane);
-      if (kt == 0)
-        mma_row<4, true>(o, fs, fq);
-      else
-        mma_row<4>(o, fs, fq);
-    }
-    signal(&im.free_q, lane);
-    const float inv_s = pr.inv_s, inv_p = sc.inv_p;
-#pragma unroll
-    for (int nt = 0; nt < 8; ++nt) {
-      const float2 f = *reinterpret_cast<const float2*>(sc.eq + 8 * nt + 2 * t4);
-#pragma unroll
-      for (int h = 0; h < 4; h += 2) o[nt][h] *= f.x * inv_s, o[nt][h + 1] *= f.y * inv_s;
-    }
-    signal(&im.free_k[use], lane);
-    if (kSave && lane == 0) bulk_wait_read();
-    signal(&pr.free_s, lane);
-
-    // P u
-    if (!mbar_wait_bounded(a.status, &pr.full_u, use)) return;
-    float u[8][4];
-    tiles_get(u, pr.u, lane);
-    signal(&pr.free_u, lane);
-    fetch(c + 2);  // the chain is past v of this step
-    const float sU = pow2_scale(warp_max(u)), inv_u = pow2_inverse(sU);
-    if (!mbar_wait_bounded(a.status, &im.full_p, use)) return;
-#pragma unroll
-    for (int j = 0; j < 4; ++j) {
-      Frag<kSave ? 2 : P> fu;
-      Frag<P> fp[4];
-      to_a(fu, u[2 * j], u[2 * j + 1], sU);
-      if constexpr (kSave) put_a(pr.u_img, kVt * kC, 16 * j, fu, lane);
-#pragma unroll
-      for (int i = j; i < 4; ++i) b_tri_nk<P>(fp[i], im.p, i, j, lane);
-      constexpr bool kHi = P == 1;
-      if (j == 0)
-        mma_row<4, true, kHi>(x, fu, fp);
-      else
-        mma_row<4, false, kHi>(x, fu, fp, j);
-    }
-    signal(&im.free_p, lane);
-    if (kSave) {
-      wkv7::fence_proxy_async_smem();
-      __syncwarp();
-      if (lane == 0) {
-        bulk_store(record + rec.u, pr.u_img, sizeof(pr.u_img));
-        bulk_commit();
-        *reinterpret_cast<float4*>(record + rec.scales) = make_float4(inv_s, inv_u, 0.f, 0.f);
+    if (a.s_final && cols > 0) store_state(S, a.s_final + state_at, cols, K, lane);
+  } else {  // -------------------------------------------------------------- helper
+    T* o_at = static_cast<T*>(a.o) + (((size_t)sq.b * a.s.T + sq.t0) * a.s.Hv + hv) * V + vt * kVt;
+    const long long o_t = (long long)a.s.Hv * V;
+    auto fetch = [&](int c) {  // v of chunk c, and a request for a later one
+      const int place = kPlaces == 2 ? c & 1 : 0;
+      if (c < n) {
+        rows_in(sm.v[own][place], v_at + c * kC * a.s.v_t, a.s.v_t, cols > 0 ? tokens - c * kC : 0, cols, lane);
+        copy_arrive(&sm.full_v[own][place]);
       }
+      if (c + 2 < n && cols > 0) rows_ask(v_at + (c + 2) * kC * a.s.v_t, a.s.v_t, tokens - (c + 2) * kC, lane);
+    };
+    fetch(0);
+    if (kPlaces == 2) fetch(1);
+    for (int c = 0; c < n; ++c) {
+      const int use = c & 1;
+      constexpr Record rec = f_record(KP, P);
+      char* record = a.b.f_rec + (((sq.slot + c) * a.s.Hv + hv) * vts + vt) * rec.size;
+      const Scal& sc = sm.sc(use);
+      if (kPlaces == 1 && c + 1 < n) {
+        wait(&sm.free_v[own], c);
+        fetch(c + 1);
+      }
+      // S0 q^T
+      float o[8][4], x[8][4];
+      wait(&sm.full_s[own], use);
+      if (kSave && lane == 0 && cols > 0) {
+        bulk_store(record, sm.s[own], sizeof(sm.s[own]));
+        bulk_commit();
+      }
+      const float inv_s = sm.inv_s[own];
+      wait(&sm.done_q, use);
+      tmem_fence_after_sync();
+      tc_load(o, mine + Col::q);
+      tc_loaded(o);
+      if (kSave && lane == 0) bulk_wait_read();
+      tmem_fence_before_sync();
+      signal(&sm.free_s, lane);
+
+      // u P^T
+      wait(&sm.full_u[own], use);
+      tmem_fence_after_sync();
+      tc_load(x, mine + Col::u);
+      tc_loaded(x);
+      const float fu = sm.inv_r[own];
+      const float sU = pow2_scale(warp_max(x)), inv_u = pow2_inverse(sU) * fu;
+      Operand64<kSave ? 2 : P> f;
+      f.split(x, sU), f.store(mine + Col::u_in, 32);
+      tc_stored();
+      tmem_fence_before_sync();
+      signal(&sm.ready_u, lane);
+      if (kPlaces == 2) fetch(c + 2);  // the chain is past v of this step
+      if constexpr (kSave) {
+        f.put(sm.out[own].u, kVt * kC, 0, lane);
+        wkv7::fence_proxy_async_smem();
+        __syncwarp();
+        if (lane == 0 && cols > 0) {
+          bulk_store(record + rec.u, sm.out[own].u, sizeof(sm.out[own].u));
+          bulk_commit();
+          *reinterpret_cast<float4*>(record + rec.scales) = make_float4(inv_s, inv_u, 0.f, 0.f);
+        }
+      }
+      wait(&sm.full_k[use], c >> 1);
+      const float fo = sc.inv_p * inv_u;
+#pragma unroll
+      for (int nt = 0; nt < 8; ++nt) {
+        const float2 eq = mul2(*reinterpret_cast<const float2*>(sc.eq + 8 * nt + 2 * t4), make_float2(inv_s, inv_s));
+#pragma unroll
+        for (int h = 0; h < 2; ++h) set_pair(o[nt], h, mul2(pair_of(o[nt], h), eq));
+      }
+      signal(&sm.free_k[use], lane);
+      wait(&sm.done_o, use);
+      tmem_fence_after_sync();
+      tc_load(x, mine + Col::o);
+      tc_loaded(x);
+      tmem_fence_before_sync();
+      signal(&sm.free_u, lane);
+#pragma unroll
+      for (int nt = 0; nt < 8; ++nt)
+#pragma unroll
+        for (int h = 0; h < 2; ++h) set_pair(o[nt], h, fma2(make_float2(fo, fo), pair_of(x[nt], h), pair_of(o[nt], h)));
+      if (kSave && lane == 0) bulk_wait_read();
+      __syncwarp();
+      rows_out(o, sm.out[own].o, o_at + (size_t)c * kC * o_t, o_t, tokens - c * kC, cols, lane);
     }
-    const float fo = inv_p * inv_u;
-#pragma unroll
-    for (int nt = 0; nt < 8; ++nt)
-#pragma unroll
-      for (int e = 0; e < 4; ++e) o[nt][e] = fmaf(fo, x[nt][e], o[nt][e]);
-    if (kSave && lane == 0) bulk_wait_read();
-    __syncwarp();
-    rows_out(o, pr.o, o_at + (size_t)c * kC * o_t, o_t, tokens - c * kC, cols, lane);
+    if (kSave && lane == 0) bulk_wait_all();
   }
-  if (kSave && lane == 0) bulk_wait_all();
+  tmem_fence_before_sync();
+  __syncthreads();
+  tmem_fence_after_sync();
+  if (warp == kFiller) wkv7::tmem_dealloc(tmem, Col::all);
 }
 
 template <typename T, int KP, bool kSave>
 cudaError_t launch(const Args& a, cudaStream_t stream) {
-  constexpr int most = kFwdChains<T, KP>;
-  constexpr size_t all = sizeof(FwdSmem<T, KP>);
-  static_assert(all <= 227 * 1024, "shared memory of a block");
+  constexpr size_t smem = sizeof(FwdSmem<T, KP, kSave>) + 1024;
+  static_assert(smem <= 227 * 1024, "shared memory of a block");
   auto kernel = fwd_kernel<T, KP, kSave>;
   static std::atomic<unsigned long long> done{0};
-  cudaError_t e = allow_smem(reinterpret_cast<const void*>(kernel), all, done);
+  cudaError_t e = allow_smem(reinterpret_cast<const void*>(kernel), smem, done);
   if (e != cudaSuccess) return e;
-  const int chains = chain_warps(a.s, most), sets = (v_tiles(a.s.V) + chains - 1) / chains;
-  const size_t smem = all - (most - chains) * sizeof(FwdPair<T, KP>);
-  return launch_after(a.small, kernel, (unsigned)((size_t)a.s.nseq * a.s.Hv * sets), (2 * chains + 1) * 32, smem, stream, a);
+  const int sets = (v_tiles(a.s.V) + kWarps - 1) / kWarps;
+  return launch_after(a.small, kernel, (unsigned)((size_t)a.s.nseq * a.s.Hv * sets), kThreads, smem, stream, a);
 }
 template <typename T>
 cudaError_t pick(const Args& a, bool save, cudaStream_t s) {

@@ -1,0 +1,182 @@
+// The fifth-generation tensor cores (tcgen05) as the gated delta rule's chains
+// use them: products with 64 rows, the left operand (what a warp computed) and the
+// accumulator in tensor memory, the right one an image in shared memory. (With the
+// left operand in shared memory too, an mma of 64 x 64 x 16 took the 37 cycles in
+// which 4 KB come out of it, and everybody else's accesses waited.)
+//
+// An image (gdr_common.cuh) is an operand as it lies: its rows of 128 bytes with
+// permuted pieces are the 128-byte swizzle, read along the row (K-major: desc_k)
+// or across it (MN-major: desc_mn); the 32-byte rows of the triangular images'
+// blocks are the 32-byte swizzle.
+//
+// With 64 rows an accumulator's row i lies in lane 32 (i / 16) + i % 16: warp w
+// of four reads rows 16 w .., and by 16 x 256 bits it gets them as mma.sync's
+// accumulator tiles, so that the code around the products is the same for both.
+#pragma once
+
+#include "gdr_common.cuh"
+#include "wkv7_tmem.cuh"
+
+namespace gdr {
+
+using wkv7::tmem_fence_after_sync;
+using wkv7::tmem_fence_before_sync;
+
+// Descriptor of an operand: start, leading and stride byte offsets, version 1,
+// layout (2: 128-byte swizzle, 6: 32-byte).
+__device__ __forceinline__ uint64_t operand(uint32_t addr, uint32_t lbo, uint32_t sbo, uint32_t layout) {
+  return (uint64_t)((addr >> 4) & 0x3FFFu) | ((uint64_t)((lbo >> 4) & 0x3FFFu) << 16) |
+         ((uint64_t)((sbo >> 4) & 0x3FFFu) << 32) | ((uint64_t)1 << 46) | ((uint64_t)layout << 61);
+}
+constexpr uint32_t kPanel = kC * 128;  // bytes of a panel: 64 rows
+// Rows of an image as the operand's rows, its columns 16 ks .. as k.
+__device__ __forceinline__ uint64_t desc_k(uint32_t image, int ks) {
+  return operand(image + (ks >> 2) * kPanel + 32 * (ks & 3), 16, 1024, 2);
+}
+// Columns as the operand's rows (panels of 64 follow one another), rows 16 ks .. as k.
+__device__ __forceinline__ uint64_t desc_mn(uint32_t image, int ks) { return operand(image + 2048 * ks, kPanel, 1024, 2); }
+// The blocks (j .., j) of a triangular image: rows as the operand's rows, columns as k.
+__device__ __forceinline__ uint64_t desc_tri_k(uint32_t image, int j) { return operand(image + 2 * tri_block(j, j), 16, 256, 6); }
+
+// fp16 operands, fp32 accumulator, 64 x n.
+__host__ __device__ constexpr uint32_t product_of(int n, bool b_mn) {
+  return (1u << 4) | ((uint32_t)b_mn << 16) | ((uint32_t)(n >> 3) << 17) | ((uint32_t)(64 >> 4) << 24);
+}
+// The left operand lies in tensor memory.
+__device__ __forceinline__ void tc_mma(uint32_t d, uint32_t a, uint64_t b, uint32_t what, bool add) {
+  asm volatile(
+      "{\n .reg .pred p;\n setp.ne.b32 p, %4, 0;\n tcgen05.mma.cta_group::1.kind::f16 [%0], [%1], %2, %3, p;\n}" ::"r"(d),
+      "r"(a), "l"(b), "r"(what), "r"((uint32_t)add)
+      : "memory");
+}
+// The barrier gets an arrival when this thread's products so far are done.
+__device__ __forceinline__ void tc_commit(uint64_t* bar) {
+  asm volatile("tcgen05.commit.cta_group::1.mbarrier::arrive::one.shared::cluster.b64 [%0];" ::"r"(smem_addr(bar)) : "memory");
+}
+
+// d = a b over `steps` 16-deep steps, a and b in parts: the small terms first, lo
+// lo left out. a's lo part lies behind its hi part; b_of(part, step) gives b's descriptors.
+template <int kA, int kB, typename FB>
+__device__ __forceinline__ void tc_product(uint32_t d, uint32_t what, int steps, uint32_t a, FB b_of) {
+  bool add = false;
+  auto term = [&](int pa, int pb) {
+#pragma unroll
+    for (int ks = 0; ks < steps; ++ks) tc_mma(d, a + 8 * (pa * steps + ks), b_of(pb, ks), what, add || ks > 0);
+    add = true;
+  };
+  if constexpr (kA == 2) term(1, 0);
+  if constexpr (kB == 2) term(0, 1);
+  term(0, 0);
+}
+// d = a X^T with X a triangular image: columns of X 16 j .. meet the rows from 16 j on.
+template <int kA, int kB>
+__device__ __forceinline__ void tc_product_tri(uint32_t d, uint32_t a, uint32_t tri) {
+  bool add = false;
+  auto term = [&](int pa, int pb) {
+#pragma unroll
+    for (int j = 0; j < 4; ++j)
+      tc_mma(d + 16 * j, a + 8 * (4 * pa + j), desc_tri_k(tri + pb * kTriPart * 2, j), product_of(64 - 16 * j, false), add || j > 0);
+    add = true;
+  };
+  if constexpr (kA == 2) term(1, 0);
+  if constexpr (kB == 2) term(0, 1);
+  term(0, 0);
+}
+
+// 64 columns of a warp's 16 rows as accumulator tiles; complete after tc_loaded.
+__device__ __forceinline__ void tc_load(float (*x)[4], uint32_t taddr) {
+  asm volatile(
+      "tcgen05.ld.sync.aligned.16x256b.x8.b32 {%0, %1, %2, %3, %4, %5, %6, %7, %8, %9, %10, %11, %12, %13, %14, "
+      "%15, %16, %17, %18, %19, %20, %21, %22, %23, %24, %25, %26, %27, %28, %29, %30, %31}, [%32];"
+      : "=f"(x[0][0]), "=f"(x[0][1]), "=f"(x[0][2]), "=f"(x[0][3]), "=f"(x[1][0]), "=f"(x[1][1]), "=f"(x[1][2]),
+        "=f"(x[1][3]), "=f"(x[2][0]), "=f"(x[2][1]), "=f"(x[2][2]), "=f"(x[2][3]), "=f"(x[3][0]), "=f"(x[3][1]),
+        "=f"(x[3][2]), "=f"(x[3][3]), "=f"(x[4][0]), "=f"(x[4][1]), "=f"(x[4][2]), "=f"(x[4][3]), "=f"(x[5][0]),
+        "=f"(x[5][1]), "=f"(x[5][2]), "=f"(x[5][3]), "=f"(x[6][0]), "=f"(x[6][1]), "=f"(x[6][2]), "=f"(x[6][3]),
+        "=f"(x[7][0]), "=f"(x[7][1]), "=f"(x[7][2]), "=f"(x[7][3])
+      : "r"(taddr)
+      : "memory");
+}
+
+// The loads so far are in their registers; x depends on it, so that no use moves before.
+__device__ __forceinline__ void tc_loaded(float (*x)[4]) {
+  asm volatile("tcgen05.wait::ld.sync.aligned;"
+               : "+f"(x[0][0]), "+f"(x[0][1]), "+f"(x[0][2]), "+f"(x[0][3]), "+f"(x[1][0]), "+f"(x[1][1]),
+                 "+f"(x[1][2]), "+f"(x[1][3]), "+f"(x[2][0]), "+f"(x[2][1]), "+f"(x[2][2]), "+f"(x[2][3]),
+                 "+f"(x[3][0]), "+f"(x[3][1]), "+f"(x[3][2]), "+f"(x[3][3]), "+f"(x[4][0]), "+f"(x[4][1]),
+                 "+f"(x[4][2]), "+f"(x[4][3]), "+f"(x[5][0]), "+f"(x[5][1]), "+f"(x[5][2]), "+f"(x[5][3]),
+                 "+f"(x[6][0]), "+f"(x[6][1]), "+f"(x[6][2]), "+f"(x[6][3]), "+f"(x[7][0]), "+f"(x[7][1]),
+                 "+f"(x[7][2]), "+f"(x[7][3])
+               :
+               : "memory");
+}
+
+// True in one lane of a whole warp. (Under a branch on the thread's number the
+// compiler cannot tell that descriptors are uniform, and an mma took 60 cycles to issue.)
+__device__ __forceinline__ bool elected() {
+  uint32_t p;
+  asm volatile("{\n .reg .pred p;\n elect.sync _|p, 0xffffffff;\n selp.u32 %0, 1, 0, p;\n}" : "=r"(p));
+  return p != 0;
+}
+
+// Two floats at once.
+__device__ __forceinline__ float2 mul2(float2 a, float2 b) {
+  float2 d;
+  asm("{\n .reg .b64 x, y;\n mov.b64 x, {%2, %3};\n mov.b64 y, {%4, %5};\n mul.rn.f32x2 x, x, y;\n mov.b64 {%0, %1}, x;\n}"
+      : "=f"(d.x), "=f"(d.y)
+      : "f"(a.x), "f"(a.y), "f"(b.x), "f"(b.y));
+  return d;
+}
+__device__ __forceinline__ float2 fma2(float2 a, float2 b, float2 c) {
+  float2 d;
+  asm("{\n .reg .b64 x, y, z;\n mov.b64 x, {%2, %3};\n mov.b64 y, {%4, %5};\n mov.b64 z, {%6, %7};\n"
+      " fma.rn.f32x2 x, x, y, z;\n mov.b64 {%0, %1}, x;\n}"
+      : "=f"(d.x), "=f"(d.y)
+      : "f"(a.x), "f"(a.y), "f"(b.x), "f"(b.y), "f"(c.x), "f"(c.y));
+  return d;
+}
+__device__ __forceinline__ float2 pair_of(const float (&x)[4], int h) { return make_float2(x[2 * h], x[2 * h + 1]); }
+__device__ __forceinline__ void set_pair(float (&x)[4], int h, float2 y) { x[2 * h] = y.x, x[2 * h + 1] = y.y; }
+
+// 64 columns of a left operand (one part), as A fragments, into tensor memory;
+// complete after tc_stored.
+__device__ __forceinline__ void tc_store(uint32_t taddr, const uint32_t (&f)[4][4]) {
+  asm volatile(
+      "tcgen05.st.sync.aligned.16x128b.x8.b32 [%0], {%1, %2, %3, %4, %5, %6, %7, %8, %9, %10, %11, %12, %13, %14, %15, %16};" ::"r"(taddr),
+      "r"(f[0][0]), "r"(f[0][1]), "r"(f[0][2]), "r"(f[0][3]), "r"(f[1][0]), "r"(f[1][1]), "r"(f[1][2]), "r"(f[1][3]),
+      "r"(f[2][0]), "r"(f[2][1]), "r"(f[2][2]), "r"(f[2][3]), "r"(f[3][0]), "r"(f[3][1]), "r"(f[3][2]), "r"(f[3][3])
+      : "memory");
+}
+__device__ __forceinline__ void tc_stored() { asm volatile("tcgen05.wait::st.sync.aligned;" ::: "memory"); }
+// x times s as 64 columns of a left operand, hi and lo `part` columns behind.
+template <int kP>
+struct Operand64 {
+  uint32_t h[4][4], l[kP == 2 ? 4 : 1][4];
+  __device__ __forceinline__ void split(const float (*x)[4], float s) {
+#pragma unroll
+    for (int j = 0; j < 4; ++j)
+#pragma unroll
+      for (int e = 0; e < 4; ++e) {
+        const float2 y = mul2(pair_of(x[2 * j + (e >> 1)], e & 1), make_float2(s, s));
+        h[j][e] = pack_f16(y.x, y.y);
+        if constexpr (kP == 2) {
+          const float2 z = fma2(unpack_f16(h[j][e]), make_float2(-1.f, -1.f), y);
+          l[j][e] = pack_f16(z.x, z.y);
+        }
+      }
+  }
+  __device__ __forceinline__ void store(uint32_t taddr, int part) const {
+    tc_store(taddr, h);
+    if constexpr (kP == 2) tc_store(taddr + part, l);
+  }
+  // rows of 16 of an image, from column k0 on
+  __device__ __forceinline__ void put(__half* image, int part, int k0, int lane) const {
+#pragma unroll
+    for (int j = 0; j < 4; ++j) {
+      __half* p = image + img(16, lane & 15, k0 + 16 * j + (lane >> 4) * 8);
+      stsm4(p, h[j]);
+      if constexpr (kP == 2) stsm4(p + part, l[j]);
+    }
+  }
+};
+
+}  // namespace gdr
