@@ -1,316 +1,434 @@
 // The gated delta rule's backward chain: the carried gradient dS of the state,
 // from the last chunk to the first, and dv.
 //
-// For the 16 rows of the state that a warp owns (gdr_chain.cuh), with the
-// images of q, k, T and P that the forward used, all transposed:
-//   y^T   = do^T P (helper) + wk (dS1 k^T)          the gradient of u
+// For 64 rows of the state a block, with the images of q, k, T and P that the
+// forward used, all transposed:
+//   y^T   = do^T P (helpers) + wk (dS1 k^T)          the gradient of u
 //   lam^T = y^T T = dv^T
-//   dS0   = e^Gc dS1 + (scale e^G do)^T q (helper) - (e^G lam)^T k
-// The helper's two products do not wait for the chain: it makes them a step
-// ahead. It leaves the images of dS1, lam and do for the gradients of q, k, g
-// and beta (gdr_grad.cu). fp16 pairs throughout: dS, lam and do enter fp32
-// results.
+//   dS0   = e^Gc dS1 + (scale e^G do)^T q (helpers) - (e^G lam)^T k
+// Built as the forward chain (gdr_fwd.cu): three batches of tcgen05 products a
+// step that wait for one another, the rows in registers between them. The
+// helpers' two products do not wait for the chain: they are a step ahead. The
+// helpers leave the images of dS1, lam and do for the gradients of q, k, g and
+// beta (gdr_grad.cu). fp16 pairs throughout: dS, lam and do enter fp32 results.
 #include "gdr_chain.cuh"
+#include "gdr_tc.cuh"
 
 namespace gdr {
 namespace {
 
-// What a chain and its helper share.
 template <typename T, int KP>
-struct alignas(128) BwdPair {
-  unsigned char d[2][kRowsBytes<T>];
-  union {  // the helper's ways to memory
+struct alignas(1024) BwdSmem {
+  static constexpr int P = In<T>::kParts, kPlaces = P * KP >= 256 ? 1 : 2;  // of do: what fits
+  __half k[2][P * kC * KP], q[P * kC * KP];
+  __half t[2 * kSpreadPart], p[2 * kSpreadPart];
+  __half s[kWarps][2 * kVt * KP];  // images of dS1 on their way to memory
+  float4 l[kWarps][8 * 32];        // lam as accumulator tiles
+  union {                          // the helpers' ways to memory
+    __half image[2 * kVt * kC];
     unsigned char dv[kRowsBytes<T>];
-    __half l_img[2 * kVt * kC];
-  };
-  __half s[2 * kVt * KP], d_img[In<T>::kParts * kVt * kC];  // images of dS1 and do
-  float4 l[8 * 32], y[8 * 32], g[KP / 8 * 32];  // lam, do^T P and (scale e^G do)^T q, as accumulator tiles
-  float inv_s;
-  uint64_t full_s, full_l, full_y, full_g, free_s, free_l, free_y, free_g;
-};
-// fp32 images of 128 keys leave room for two
-template <typename T, int KP>
-constexpr int kBwdChains = sizeof(T) * KP <= 256 ? 4 : 2;
-template <typename T, int KP>
-struct BwdSmem {
-  Images<In<T>::kParts, KP, 2> im;
-  BwdPair<T, KP> pair[kBwdChains<T, KP>];
+  } out[kWarps];
+  unsigned char d[kWarps][kPlaces][kRowsBytes<T>];
+  unsigned char scal[2][kChainScal];
+  float inv_s[kWarps], inv_d[2][kWarps], inv_g[2][kWarps];  // inverse scales of the warps' rows
+  uint64_t full_k[2], full_q, full_t, full_p, free_k[2], free_q, free_t, free_p;
+  uint64_t done_x, done_y, done_l, done_w, done_g, end[2];    // products
+  uint64_t ready_s, ready_y, ready_w, ready_d, ready_e;       // operands in tensor memory
+  uint64_t full_s[kWarps], free_s[kWarps], full_l[kWarps], free_l[kWarps], full_d[kWarps], free_y, free_g;
+  uint32_t tmem;
+  __device__ __forceinline__ const Scal& sc(int place) const { return *reinterpret_cast<const Scal*>(scal[place]); }
 };
 
+// Tensor memory, columns: the products x (and then the state's), do P, lam (which
+// for 128 keys lies behind x, where the state's product comes later) and
+// (scale e^G do) q; the operands dS1 (and then y, and then e^G lam) and do (and
+// then scale e^G do), hi and lo.
+template <int KP>
+struct Columns {
+  static constexpr uint32_t x = 0, y = KP, g = KP + 64, l = KP == 64 ? 2 * KP + 64 : 64;
+  static constexpr uint32_t s_in = KP == 64 ? 256 : 320, d_in = s_in + KP, all = 512;
+};
+
+// The warp that fills the chunk's images; lane 0 of it. Step s is chunk slot - s.
 template <typename T, int KP>
-__global__ void __launch_bounds__((2 * kBwdChains<T, KP> + 1) * 32, 1) bwd_kernel(const Args a) {
-  extern __shared__ __align__(128) unsigned char raw[];
-  constexpr int P = In<T>::kParts, kNt = KP / 8;
-  BwdSmem<T, KP>& sm = *reinterpret_cast<BwdSmem<T, KP>*>(raw);
-  const int chains = blockDim.x / 64, warp = threadIdx.x >> 5, lane = threadIdx.x & 31, t4 = lane & 3;
-  const int vts = (a.s.V + kVt - 1) / kVt, sets = (vts + chains - 1) / chains;
+__device__ __forceinline__ void fill(BwdSmem<T, KP>& m, const Args& a, long long slot, int n, int hk, int hv) {
+  constexpr int P = In<T>::kParts, image = P * kC * KP * 2, tri = kTriPart * 2;
+  auto at_k = [&](int s) { return (size_t)(slot - s) * a.s.Hk + hk; };
+  auto at_v = [&](int s) { return (size_t)(slot - s) * a.s.Hv + hv; };
+  auto k = [&](int s) {
+    uint64_t* bar = &m.full_k[s & 1];
+    mbar_arrive_expect_tx(bar, image + kChainScal);
+    bulk_load(m.k[s & 1], a.b.k_img + at_k(s) * image, image, bar);
+    bulk_load(m.scal[s & 1], a.b.scal + at_v(s), kChainScal, bar);
+  };
+  auto spread = [&](__half* to, const char* from, uint64_t* bar) {
+    mbar_arrive_expect_tx(bar, 2 * tri);
+#pragma unroll
+    for (int part = 0; part < 2; ++part)
+#pragma unroll
+      for (int j = 0; j < 4; ++j)
+        bulk_load(to + part * kSpreadPart + 5 * j * 256, from + 2 * (part * kTriPart + tri_block(j, j)), (4 - j) * 512, bar);
+  };
+  auto q = [&](int s) {
+    mbar_arrive_expect_tx(&m.full_q, image);
+    bulk_load(m.q, a.b.q_img + at_k(s) * image, image, &m.full_q);
+  };
+  auto t = [&](int s) { spread(m.t, a.b.t_img + at_v(s) * Layout::tp_img, &m.full_t); };
+  auto p = [&](int s) { spread(m.p, a.b.p_img + at_v(s) * Layout::tp_img, &m.full_p); };
+  auto ask = [&](int s) {  // into L2
+    if (s >= n) return;
+    bulk_prefetch(a.b.k_img + at_k(s) * image, image);
+    bulk_prefetch(a.b.q_img + at_k(s) * image, image);
+    bulk_prefetch(a.b.t_img + at_v(s) * Layout::tp_img, 2 * tri);
+    bulk_prefetch(a.b.p_img + at_v(s) * Layout::tp_img, 2 * tri);
+    bulk_prefetch(a.b.scal + at_v(s), kChainScal);
+  };
+  k(0), p(0), q(0), t(0);
+  if (n > 1) k(1);
+  ask(2);
+  int s = 1;
+  for (; s < n; ++s) {  // in the order in which step s - 1 gives the places up
+    if (!mbar_wait_bounded(a.status, &m.free_p, (s - 1) & 1)) break;
+    p(s);
+    if (!mbar_wait_bounded(a.status, &m.free_q, (s - 1) & 1)) break;
+    q(s);
+    if (!mbar_wait_bounded(a.status, &m.free_t, (s - 1) & 1)) break;
+    t(s);
+    if (!mbar_wait_bounded(a.status, &m.free_k[(s - 1) & 1], ((s - 1) >> 1) & 1)) break;
+    if (s + 1 < n) k(s + 1);
+    ask(s + 2);
+  }
+  if (s < n) {  // given up: no copy is left in flight
+    for (uint64_t* b : {&m.full_k[0], &m.full_k[1], &m.full_q, &m.full_t, &m.full_p}) {
+      mbar_wait_bounded(nullptr, b, 0, 1000000);
+      mbar_wait_bounded(nullptr, b, 1, 1000000);
+    }
+  }
+}
+
+// A warp's image to memory, `kHalves` of it. (By loads and stores: the proxy fence
+// that a bulk copy wants before it took 400 to 1400 cycles beside running products.)
+template <int kHalves>
+__device__ __forceinline__ void image_out(char* to, const __half* image, int lane) {
+#pragma unroll
+  for (int i = 0; i < kHalves / 256; ++i)
+    reinterpret_cast<uint4*>(to)[i * 32 + lane] = reinterpret_cast<const uint4*>(image)[i * 32 + lane];
+}
+
+template <typename T, int KP>
+__global__ void __launch_bounds__(kThreads, 1) bwd_kernel(const Args a) {
+  extern __shared__ __align__(1024) unsigned char raw[];
+  using Smem = BwdSmem<T, KP>;
+  using Col = Columns<KP>;
+  constexpr int P = In<T>::kParts, kNt = KP / 8, kPlaces = Smem::kPlaces;
+  Smem& sm = *reinterpret_cast<Smem*>(raw + (-smem_addr(raw) & 1023u));
+  const int warp = __shfl_sync(0xffffffffu, threadIdx.x >> 5, 0), lane = threadIdx.x & 31, t4 = lane & 3, own = warp & 3;
+  const int vts = (a.s.V + kVt - 1) / kVt, sets = (vts + kWarps - 1) / kWarps;
   const int set = blockIdx.x % sets, hv = blockIdx.x / sets % a.s.Hv, seq = blockIdx.x / (sets * a.s.Hv);
   const int hk = hv / (a.s.Hv / a.s.Hk);
-  const SeqRange sq = seq_range(a.s, seq);
-  const int n = (sq.t1 - sq.t0 + kC - 1) / kC;
-  const int K = a.s.K, V = a.s.V;
-  auto& im = sm.im;
   if (threadIdx.x == 0) {
-    init_images(im, min(chains, vts - set * chains));
-    for (int i = 0; i < chains; ++i) {
-      BwdPair<T, KP>& p = sm.pair[i];
-      for (uint64_t* b : {&p.full_s, &p.full_l, &p.full_y, &p.full_g, &p.free_s, &p.free_l, &p.free_y, &p.free_g}) mbar_init(b, 1);
-    }
+    for (uint64_t* b : {&sm.full_k[0], &sm.full_k[1], &sm.full_q, &sm.full_t, &sm.full_p, &sm.free_q, &sm.free_t, &sm.free_p,
+                        &sm.done_x, &sm.done_y, &sm.done_l, &sm.done_w, &sm.done_g, &sm.end[0], &sm.end[1]})
+      mbar_init(b, 1);
+    for (uint64_t* b : {&sm.free_k[0], &sm.free_k[1]}) mbar_init(b, 2 * kWarps + 1);
+    for (uint64_t* b : {&sm.free_y, &sm.free_g, &sm.ready_s, &sm.ready_y, &sm.ready_w, &sm.ready_d, &sm.ready_e}) mbar_init(b, kWarps);
+    for (int i = 0; i < kWarps; ++i)
+      for (uint64_t* b : {&sm.full_s[i], &sm.free_s[i], &sm.full_l[i], &sm.free_l[i], &sm.full_d[i]}) mbar_init(b, 1);
     wkv7::fence_mbar_init();
   }
+  if (warp == kFiller) wkv7::tmem_alloc(&sm.tmem, Col::all);
+  tmem_fence_before_sync();
   __syncthreads();
+  tmem_fence_after_sync();
   if (a.small) grid_go();
-  if (warp == 2 * chains) {
-    if (lane == 0) fill_images(im, a, sq.slot + n - 1, -1, n, hk, hv);
-    return;
-  }
-  const int own = warp % chains, vt = set * chains + own;
-  if (vt >= vts) return;
-  BwdPair<T, KP>& pr = sm.pair[own];
-  const int cols = V - vt * kVt, tokens = sq.t1 - sq.t0;
+  const SeqRange sq = seq_range(a.s, seq);
+  const int n = (sq.t1 - sq.t0 + kC - 1) / kC;
+  const int K = a.s.K, V = a.s.V, vt = set * kWarps + own;
+  const int cols = V - vt * kVt, tokens = sq.t1 - sq.t0;  // cols <= 0: this warp's rows are zeros
+  const uint32_t tmem = sm.tmem, mine = tmem + ((uint32_t)own << 21);  // this warp's lanes
+  Patience wait{a.status};
+  constexpr int kPartK = kC * KP;  // halves from an image's hi part to its lo part
+  auto ready = [&](uint64_t* bar) {  // what was stored to tensor memory is there
+    tc_stored();
+    tmem_fence_before_sync();
+    signal(bar, lane);
+  };
 
   // step s works on chunk n - 1 - s
-  if (warp < chains) {  // ------------------------------------------------ chain
+  if (warp == kFiller) {
+    if (lane == 0 && n > 0) fill(sm, a, sq.slot + n - 1, n, hk, hv);
+  } else if (warp == kIssuer) {
+    for (int s = 0; s < n; ++s) {
+      const int use = s & 1;
+      const uint32_t k_at = smem_addr(sm.k[use]);
+      wait(&sm.full_k[use], s >> 1);
+      wait(&sm.ready_s, use);
+      tmem_fence_after_sync();
+      if (elected()) {
+        tc_product<2, P>(tmem + Col::x, product_of(64, false), KP / 16, tmem + Col::s_in,
+                         [&](int part, int ks) { return desc_k(k_at + part * kPartK * 2, ks); });
+        tc_commit(&sm.done_x);
+      }
+      wait(&sm.full_t, use);
+      wait(&sm.ready_y, use);
+      tmem_fence_after_sync();
+      if (elected()) {
+        tc_product_tri_mn<2, 2>(tmem + Col::l, tmem + Col::s_in, smem_addr(sm.t));
+        tc_commit(&sm.done_l);
+        tc_commit(&sm.free_t);
+      }
+      wait(&sm.ready_w, use);
+      tmem_fence_after_sync();
+      if (elected()) {
+        tc_product<2, P>(tmem + Col::x, product_of(KP, true), 4, tmem + Col::s_in,
+                         [&](int part, int ks) { return desc_mn(k_at + part * kPartK * 2, ks); });
+        tc_commit(&sm.done_w);
+        tc_commit(&sm.free_k[use]);
+      }
+    }
+    if (elected()) tc_commit(&sm.end[0]);
+    mbar_wait_bounded(a.status, &sm.end[0], 0);
+  } else if (warp == kHelpersIssuer) {
+    const uint32_t q_at = smem_addr(sm.q);
+    for (int s = 0; s < n; ++s) {
+      const int use = s & 1;
+      wait(&sm.full_p, use);
+      if (s > 0) wait(&sm.free_y, use ^ 1);
+      wait(&sm.ready_d, use);
+      tmem_fence_after_sync();
+      if (elected()) {
+        tc_product_tri_mn<P, 2>(tmem + Col::y, tmem + Col::d_in, smem_addr(sm.p));
+        tc_commit(&sm.done_y);
+        tc_commit(&sm.free_p);
+      }
+      wait(&sm.full_q, use);
+      if (s > 0) wait(&sm.free_g, use ^ 1);
+      wait(&sm.ready_e, use);
+      tmem_fence_after_sync();
+      if (elected()) {
+        tc_product<2, P>(tmem + Col::g, product_of(KP, true), 4, tmem + Col::d_in,
+                         [&](int part, int ks) { return desc_mn(q_at + part * kPartK * 2, ks); });
+        tc_commit(&sm.done_g);
+        tc_commit(&sm.free_q);
+      }
+    }
+    if (elected()) tc_commit(&sm.end[1]);
+    mbar_wait_bounded(a.status, &sm.end[1], 0);
+  } else if (warp < kWarps) {  // ------------------------------------------ chain
     const size_t state_at = (((size_t)seq * a.s.Hv + hv) * V + vt * kVt) * K;
     float S[kNt][4];
     load_state(S, a.dS_final ? a.dS_final + state_at : nullptr, cols, K, lane);
     float s_max = warp_max(S);
-    Asked has_k(&im.full_k[0], 0);
     for (int s = 0; s < n; ++s) {
       const int use = s & 1;
-      const Scal& sc = im.sc(use);
-      const float sS = pow2_scale(s_max), inv_s = pow2_inverse(sS);
+      const Scal& sc = sm.sc(use);
       // dS1 k^T
-      float x[8][4];
-      const Asked has_s(&pr.free_s, use ^ 1), has_y(&pr.full_y, use), has_t(&im.full_t, use);
-      if (!has_k.wait(a.status)) return;
-      if (s > 0 && !has_s.wait(a.status)) return;
+      const float sS = pow2_scale(s_max), inv_s = pow2_inverse(sS);
+      const Asked has_s(&sm.free_s[own], use ^ 1);
+      Operand64<2> f[KP / 64];
 #pragma unroll
-      for (int kt = 0; kt < KP / 16; ++kt) {
-        Frag<2> fs;
-        to_a(fs, S[2 * kt], S[2 * kt + 1], sS);
-        put_a(pr.s, kVt * KP, 16 * kt, fs, lane);
-        Frag<P> fk[4];
+      for (int i = 0; i < KP / 64; ++i) f[i].split(S + 8 * i, sS), f[i].store(mine + Col::s_in + 32 * i, KP / 2);
+      ready(&sm.ready_s);
+      const Asked has_k(&sm.full_k[use], s >> 1), has_d(&sm.full_d[own], use);
+      if (s > 0) wait(has_s);
+      if (lane == 0) sm.inv_s[own] = inv_s;
 #pragma unroll
-        for (int nb = 0; nb < 4; ++nb) b_nk<P>(fk[nb], im.k[use], kC, kC * KP, 16 * nb, 16 * kt, lane);
-        if (kt == 0)
-          mma_row<4, true>(x, fs, fk);
-        else
-          mma_row<4>(x, fs, fk);
-      }
-      if (lane == 0) pr.inv_s = inv_s;
-      wkv7::fence_proxy_async_smem();
-      signal(&pr.full_s, lane);
+      for (int i = 0; i < KP / 64; ++i) f[i].put(sm.s[own], kVt * KP, 64 * i, lane);
+      signal(&sm.full_s[own], lane);
 
       // y
-      if (!has_y.wait(a.status)) return;
+      float x[8][4], y[8][4];
+      wait(has_k);
+      wait(has_d);
+      const float fy = sc.inv_p * sm.inv_d[use][own], inv_g = sm.inv_g[use][own];
+      float2 wk[8];
 #pragma unroll
-      for (int nt = 0; nt < 8; ++nt) {
-        const float2 f = *reinterpret_cast<const float2*>(sc.wk + 8 * nt + 2 * t4);
-        const float4 y = pr.y[nt * 32 + lane];
-        const float f0 = f.x * inv_s, f1 = f.y * inv_s;
-        x[nt][0] = fmaf(f0, x[nt][0], y.x), x[nt][1] = fmaf(f1, x[nt][1], y.y);
-        x[nt][2] = fmaf(f0, x[nt][2], y.z), x[nt][3] = fmaf(f1, x[nt][3], y.w);
-      }
-      signal(&pr.free_y, lane);
-      const float sY = pow2_scale(warp_max(x));
-
-      // lam = T^T y
-      float l[8][4];
-      if (!has_t.wait(a.status)) return;
-#pragma unroll
-      for (int i = 3; i >= 0; --i) {
-        Frag<2> fy, ft[4];
-        to_a(fy, x[2 * i], x[2 * i + 1], sY);
-#pragma unroll
-        for (int j = 0; j <= i; ++j) b_tri_kn<2>(ft[j], im.t, i, j, lane);
-        if (i == 3)
-          mma_row<4, true>(l, fy, ft);
-        else
-          mma_row<4>(l, fy, ft, 0, i + 1);
-      }
-      const Asked has_l(&pr.free_l, use ^ 1), has_g(&pr.full_g, use);
-      const float fl = sc.inv_t * pow2_inverse(sY);
+      for (int nt = 0; nt < 8; ++nt)
+        wk[nt] = mul2(*reinterpret_cast<const float2*>(sc.wk + 8 * nt + 2 * t4), make_float2(inv_s, inv_s));
+      wait(&sm.done_y, use);
+      tmem_fence_after_sync();
+      tc_load(y, mine + Col::y);
+      tc_loaded(y);
 #pragma unroll
       for (int nt = 0; nt < 8; ++nt)
 #pragma unroll
-        for (int e = 0; e < 4; ++e) l[nt][e] *= fl;
-      if (s > 0 && !has_l.wait(a.status)) return;
-      tiles_put(pr.l, l, 1.f, lane);
-      signal(&pr.full_l, lane);
-
-      // dS0, the product at its own scale, kept below 2^60 of dS1's
+        for (int h = 0; h < 2; ++h) set_pair(y[nt], h, mul2(pair_of(y[nt], h), make_float2(fy, fy)));
+      wait(&sm.done_x, use);
+      tmem_fence_after_sync();
+      tc_load(x, mine + Col::x);
+      tc_loaded(x);
 #pragma unroll
-      for (int nt = 0; nt < 8; ++nt) {
-        const float2 f = *reinterpret_cast<const float2*>(sc.ek + 8 * nt + 2 * t4);
+      for (int nt = 0; nt < 8; ++nt)
 #pragma unroll
-        for (int h = 0; h < 4; h += 2) l[nt][h] *= -f.x, l[nt][h + 1] *= -f.y;
+        for (int h = 0; h < 2; ++h) set_pair(y[nt], h, fma2(wk[nt], pair_of(x[nt], h), pair_of(y[nt], h)));
+      const float sY = pow2_scale(warp_max(y)), fl = sc.inv_t * pow2_inverse(sY);
+      {
+        Operand64<2> fy_in;
+        fy_in.split(y, sY), fy_in.store(mine + Col::s_in, 32);
       }
-      const float sW = fminf(pow2_scale(warp_max(l)), sS * 0x1p60f), egc = sc.egc * sW;
+      ready(&sm.ready_y);
+      signal(&sm.free_y, lane);
+
+      // lam = T^T y
+      const Asked has_l(&sm.free_l[own], use ^ 1);
+      float2 ek[8];
+#pragma unroll
+      for (int nt = 0; nt < 8; ++nt)
+        ek[nt] = mul2(*reinterpret_cast<const float2*>(sc.ek + 8 * nt + 2 * t4), make_float2(-fl, -fl));
+      const float egc = sc.egc;
+      wait(&sm.done_l, use);
+      tmem_fence_after_sync();
+      tc_load(x, mine + Col::l);
+      tc_loaded(x);
+
+      // e^G lam, and the state's gradient
+#pragma unroll
+      for (int nt = 0; nt < 8; ++nt)
+#pragma unroll
+        for (int h = 0; h < 2; ++h) set_pair(y[nt], h, mul2(pair_of(x[nt], h), ek[nt]));
+      const float sW = pow2_scale(warp_max(y)), inv_w = pow2_inverse(sW);
+      {
+        Operand64<2> fw;
+        fw.split(y, sW), fw.store(mine + Col::s_in, 32);
+      }
+      ready(&sm.ready_w);
+      if (s > 0) wait(has_l);
+      tiles_put(sm.l[own], x, fl, lane);
+      signal(&sm.full_l[own], lane);
+      signal(&sm.free_k[use], lane);
 #pragma unroll
       for (int nt = 0; nt < kNt; ++nt)
 #pragma unroll
-        for (int e = 0; e < 4; ++e) S[nt][e] *= egc;
+        for (int h = 0; h < 2; ++h) set_pair(S[nt], h, mul2(pair_of(S[nt], h), make_float2(egc, egc)));
+      wait(&sm.done_g, use);
+      tmem_fence_after_sync();
+      auto add = [&](uint32_t at, float f) {
 #pragma unroll
-      for (int j = 0; j < 4; ++j) {
-        Frag<2> fw;
-        to_a(fw, l[2 * j], l[2 * j + 1], sW);
-        Frag<P> fk[KP / 16];
+        for (int half = 0; half < KP / 64; ++half) {
+          tc_load(x, at + 64 * half);
+          tc_loaded(x);
 #pragma unroll
-        for (int nb = 0; nb < KP / 16; ++nb) b_kn<P>(fk[nb], im.k[use], kC, kC * KP, 16 * nb, 16 * j, lane);
-        mma_row<KP / 16>(S, fw, fk);
-      }
-      has_k = Asked(&im.full_k[use ^ 1], (s + 1) >> 1);
-      signal(&im.free_k[use], lane);
-      const float inv_w = pow2_inverse(sW);
-      if (!has_g.wait(a.status)) return;
+          for (int nt = 0; nt < 8; ++nt)
 #pragma unroll
-      for (int nt = 0; nt < kNt; ++nt) {
-        const float4 g = pr.g[nt * 32 + lane];
-        S[nt][0] = fmaf(S[nt][0], inv_w, g.x), S[nt][1] = fmaf(S[nt][1], inv_w, g.y);
-        S[nt][2] = fmaf(S[nt][2], inv_w, g.z), S[nt][3] = fmaf(S[nt][3], inv_w, g.w);
-      }
-      signal(&pr.free_g, lane);
+            for (int h = 0; h < 2; ++h) {
+              float(&to)[4] = S[8 * half + nt];
+              set_pair(to, h, fma2(make_float2(f, f), pair_of(x[nt], h), pair_of(to, h)));
+            }
+        }
+      };
+      add(mine + Col::g, inv_g);
+      tmem_fence_before_sync();
+      signal(&sm.free_g, lane);
+      wait(&sm.done_w, use);
+      tmem_fence_after_sync();
+      add(mine + Col::x, inv_w);
       s_max = warp_max(S);
     }
-    if (a.dS_init) store_state(S, a.dS_init + state_at, cols, K, lane);
-    return;
-  }
+    if (a.dS_init && cols > 0) store_state(S, a.dS_init + state_at, cols, K, lane);
+  } else {  // -------------------------------------------------------------- helper
+    const size_t first = (((size_t)sq.b * a.s.T + sq.t0) * a.s.Hv + hv) * V + (cols > 0 ? vt * kVt : 0);
+    const T* do_at = static_cast<const T*>(a.d_o) + first;
+    T* dv_at = static_cast<T*>(a.dv) + first;
+    const long long row_t = (long long)a.s.Hv * V;
+    auto fetch = [&](int s) {  // do of step s, and a request for a later one
+      const int c = n - 1 - s;
+      if (c >= 0) rows_in(sm.d[own][s % kPlaces], do_at + c * kC * row_t, row_t, cols > 0 ? tokens - c * kC : 0, cols, lane);
+      copy_commit();
+      if (c >= 2 && cols > 0) rows_ask(do_at + (c - 2) * kC * row_t, row_t, kC, lane);
+    };
+    constexpr Record rec = b_record(KP, P);
+    auto record_of = [&](int s) { return a.b.b_rec + (((sq.slot + n - 1 - s) * a.s.Hv + hv) * vts + vt) * rec.size; };
+    float inv_d = 0.f;
+    // What step s needs of do: its image, do^T P and (scale e^G do)^T q.
+    auto ahead = [&](int s) {
+      const int use = s & 1;
+      const Scal& sc = sm.sc(use);
+      float d[8][4];
+      copy_wait<kPlaces - 1>();
+      __syncwarp();
+      rows_get(d, sm.d[own][s % kPlaces], lane, do_at);
+      __syncwarp();
+      const float sD = pow2_scale(warp_max(d));
+      inv_d = pow2_inverse(sD);
+      if (s > 0) wait(&sm.done_g, use ^ 1);
+      tmem_fence_after_sync();
+      {
+        Operand64<P> f;
+        f.split(d, sD), f.store(mine + Col::d_in, 32);
+        ready(&sm.ready_d);
+        f.put(sm.out[own].image, kVt * kC, 0, lane);
+      }
+      __syncwarp();
+      if (cols > 0) image_out<P * kVt * kC>(record_of(s) + rec.d, sm.out[own].image, lane);
+      __syncwarp();
+      wait(&sm.full_k[use], s >> 1);
+#pragma unroll
+      for (int nt = 0; nt < 8; ++nt) {
+        const float2 eq = *reinterpret_cast<const float2*>(sc.eq + 8 * nt + 2 * t4);
+#pragma unroll
+        for (int h = 0; h < 2; ++h) set_pair(d[nt], h, mul2(pair_of(d[nt], h), eq));
+      }
+      signal(&sm.free_k[use], lane);
+      const float sE = pow2_scale(warp_max(d));
+      Operand64<2> f;
+      f.split(d, sE);
+      wait(&sm.done_y, use);  // do's place is free
+      tmem_fence_after_sync();
+      f.store(mine + Col::d_in, 32);
+      ready(&sm.ready_e);
+      // the chain has taken do P of the step before, and with it these of that step
+      if (lane == 0) sm.inv_d[use][own] = inv_d, sm.inv_g[use][own] = pow2_inverse(sE);
+      signal(&sm.full_d[own], lane);
+      fetch(s + kPlaces);
+    };
+    fetch(0);
+    if (kPlaces == 2) fetch(1);
+    if (n > 0) ahead(0);
+    for (int s = 0; s < n; ++s) {
+      const int c = n - 1 - s, use = s & 1;
+      char* record = record_of(s);
+      const float inv_do = inv_d;
+      wait(&sm.full_s[own], use);
+      const float inv_s = sm.inv_s[own];
+      if (cols > 0) image_out<2 * kVt * KP>(record, sm.s[own], lane);
+      signal(&sm.free_s[own], lane);
+      if (s + 1 < n) ahead(s + 1);
 
-  // ------------------------------------------------------------------- helper
-  const size_t first = (((size_t)sq.b * a.s.T + sq.t0) * a.s.Hv + hv) * V + vt * kVt;
-  const T* do_at = static_cast<const T*>(a.d_o) + first;
-  T* dv_at = static_cast<T*>(a.dv) + first;
-  const long long row_t = (long long)a.s.Hv * V;
-  auto fetch = [&](int s) {  // do of step s, and a request for a later one
-    const int c = n - 1 - s;
-    if (c >= 0) rows_in(pr.d[s & 1], do_at + c * kC * row_t, row_t, tokens - c * kC, cols, lane);
-    copy_commit();
-    if (c >= 2) rows_ask(do_at + (c - 2) * kC * row_t, row_t, kC, lane);
-  };
-  constexpr Record rec = b_record(KP, P);
-  auto record_of = [&](int s) { return a.b.b_rec + (((sq.slot + n - 1 - s) * a.s.Hv + hv) * vts + vt) * rec.size; };
-  float inv_d = 0.f;
-  // What step s needs of do: its image, do^T P and (scale e^G do)^T q.
-  auto ahead = [&](int s) {
-    const int use = s & 1;
-    const Scal& sc = im.sc(use);
-    char* record = record_of(s);
-    copy_wait<1>();
-    __syncwarp();
-    float d[8][4], x[8][4];
-    rows_get(d, pr.d[use], lane, do_at);
-    __syncwarp();
-    fetch(s + 2);
-    const float sD = pow2_scale(warp_max(d));
-    inv_d = pow2_inverse(sD);
-    if (!mbar_wait_bounded(a.status, &im.full_k[use], (s >> 1) & 1)) return false;
-    if (!mbar_wait_bounded(a.status, &im.full_p, use)) return false;
-    if (lane == 0) bulk_wait_read();  // the images of dS and do of the step before are out
-    __syncwarp();
-    if (s > 0) signal(&pr.free_s, lane);
-#pragma unroll
-    for (int i = 3; i >= 0; --i) {
-      Frag<P> fd;
-      Frag<2> fp[4];
-      to_a(fd, d[2 * i], d[2 * i + 1], sD);
-      put_a(pr.d_img, kVt * kC, 16 * i, fd, lane);
-#pragma unroll
-      for (int j = 0; j <= i; ++j) b_tri_kn<2>(fp[j], im.p, i, j, lane);
-      if (i == 3)
-        mma_row<4, true>(x, fd, fp);
-      else
-        mma_row<4>(x, fd, fp, 0, i + 1);
+      wait(&sm.full_l[own], use);
+      float x[8][4];
+      tiles_get(x, sm.l[own], lane);
+      signal(&sm.free_l[own], lane);
+      const float sL = pow2_scale(warp_max(x));
+      {
+        Operand64<2> f;
+        f.split(x, sL), f.put(sm.out[own].image, kVt * kC, 0, lane);
+      }
+      __syncwarp();
+      if (cols > 0) {
+        image_out<2 * kVt * kC>(record + rec.u, sm.out[own].image, lane);
+        if (lane == 0) *reinterpret_cast<float4*>(record + rec.scales) = make_float4(inv_s, pow2_inverse(sL), inv_do, 0.f);
+      }
+      __syncwarp();
+      rows_out(x, sm.out[own].dv, dv_at + (size_t)c * kC * row_t, row_t, tokens - c * kC, cols, lane);
     }
-    signal(&im.free_p, lane);
-    wkv7::fence_proxy_async_smem();
-    __syncwarp();
-    if (lane == 0) {
-      bulk_store(record + rec.d, pr.d_img, sizeof(pr.d_img));
-      bulk_commit();
-    }
-    if (s > 0 && !mbar_wait_bounded(a.status, &pr.free_y, use ^ 1)) return false;
-    tiles_put(pr.y, x, sc.inv_p * inv_d, lane);
-    signal(&pr.full_y, lane);
-#pragma unroll
-    for (int nt = 0; nt < 8; ++nt) {
-      const float2 f = *reinterpret_cast<const float2*>(sc.eq + 8 * nt + 2 * t4);
-#pragma unroll
-      for (int h = 0; h < 4; h += 2) d[nt][h] *= f.x, d[nt][h + 1] *= f.y;
-    }
-    const float sW = pow2_scale(warp_max(d));
-    float g[kNt][4];
-    if (!mbar_wait_bounded(a.status, &im.full_q, use)) return false;
-#pragma unroll
-    for (int j = 0; j < 4; ++j) {
-      Frag<2> fd;
-      to_a(fd, d[2 * j], d[2 * j + 1], sW);
-      Frag<P> fq[KP / 16];
-#pragma unroll
-      for (int nb = 0; nb < KP / 16; ++nb) b_kn<P>(fq[nb], im.q, kC, kC * KP, 16 * nb, 16 * j, lane);
-      if (j == 0)
-        mma_row<KP / 16, true>(g, fd, fq);
-      else
-        mma_row<KP / 16>(g, fd, fq);
-    }
-    signal(&im.free_q, lane);
-    signal(&im.free_k[use], lane);
-    if (s > 0 && !mbar_wait_bounded(a.status, &pr.free_g, use ^ 1)) return false;
-    tiles_put(pr.g, g, pow2_inverse(sW), lane);
-    signal(&pr.full_g, lane);
-    return true;
-  };
-  fetch(0), fetch(1);
-  if (n > 0 && !ahead(0)) return;
-  for (int s = 0; s < n; ++s) {
-    const int c = n - 1 - s, use = s & 1;
-    char* record = record_of(s);
-    const float inv_do = inv_d;
-    if (!mbar_wait_bounded(a.status, &pr.full_s, use)) return;
-    const float inv_s = pr.inv_s;
-    if (lane == 0) {
-      bulk_store(record, pr.s, sizeof(pr.s));
-      bulk_commit();
-    }
-    if (s + 1 < n && !ahead(s + 1)) return;
-
-    if (!mbar_wait_bounded(a.status, &pr.full_l, use)) return;
-    float x[8][4];
-    tiles_get(x, pr.l, lane);
-    signal(&pr.free_l, lane);
-    const float sL = pow2_scale(warp_max(x));
-#pragma unroll
-    for (int j = 0; j < 4; ++j) {
-      Frag<2> f;
-      to_a(f, x[2 * j], x[2 * j + 1], sL);
-      put_a(pr.l_img, kVt * kC, 16 * j, f, lane);
-    }
-    wkv7::fence_proxy_async_smem();
-    __syncwarp();
-    if (lane == 0) {
-      bulk_store(record + rec.u, pr.l_img, sizeof(pr.l_img));
-      bulk_commit();
-      *reinterpret_cast<float4*>(record + rec.scales) = make_float4(inv_s, pow2_inverse(sL), inv_do, 0.f);
-      bulk_wait_read();
-    }
-    __syncwarp();
-    rows_out(x, pr.dv, dv_at + (size_t)c * kC * row_t, row_t, tokens - c * kC, cols, lane);
+    copy_wait<0>();
   }
-  if (lane == 0) bulk_wait_all();
+  tmem_fence_before_sync();
+  __syncthreads();
+  tmem_fence_after_sync();
+  if (warp == kFiller) wkv7::tmem_dealloc(tmem, Col::all);
 }
 
 template <typename T, int KP>
 cudaError_t launch(const Args& a, cudaStream_t stream) {
-  constexpr int most = kBwdChains<T, KP>;
-  constexpr size_t all = sizeof(BwdSmem<T, KP>);
-  static_assert(all <= 227 * 1024, "shared memory of a block");
+  constexpr size_t smem = sizeof(BwdSmem<T, KP>) + 1024;
+  static_assert(smem <= 227 * 1024, "shared memory of a block");
   auto kernel = bwd_kernel<T, KP>;
   static std::atomic<unsigned long long> done{0};
-  cudaError_t e = allow_smem(reinterpret_cast<const void*>(kernel), all, done);
+  cudaError_t e = allow_smem(reinterpret_cast<const void*>(kernel), smem, done);
   if (e != cudaSuccess) return e;
-  const int chains = chain_warps(a.s, most), sets = (v_tiles(a.s.V) + chains - 1) / chains;
-  const size_t smem = all - (most - chains) * sizeof(BwdPair<T, KP>);
-  kernel<<<(unsigned)((size_t)a.s.nseq * a.s.Hv * sets), (2 * chains + 1) * 32, smem, stream>>>(a);
+  const int sets = (v_tiles(a.s.V) + kWarps - 1) / kWarps;
+  kernel<<<(unsigned)((size_t)a.s.nseq * a.s.Hv * sets), kThreads, smem, stream>>>(a);
   return cudaGetLastError();
 }
 template <typename T>

@@ -30,9 +30,6 @@
 namespace gdr {
 namespace {
 
-constexpr int kWarps = 4;  // of 16 rows each: chain warps, and as many helpers
-constexpr int kFiller = 2 * kWarps, kIssuer = kFiller + 1, kHelpersIssuer = kIssuer + 1, kThreads = (kHelpersIssuer + 1) * 32;
-
 template <typename T, int KP, bool kSave>
 struct alignas(1024) FwdSmem {
   static constexpr int P = In<T>::kParts, kPlaces = P * KP >= 256 ? 1 : 2;  // of v: what fits
@@ -112,20 +109,6 @@ __device__ __forceinline__ void fill(FwdSmem<T, KP, kSave>& m, const Args& a, lo
     }
   }
 }
-
-// A wait that a warp gives up on once: from then on it goes through its steps
-// without waiting (all accesses are in bounds whatever the data), so that the
-// block's barriers and its tensor memory are left in order.
-struct Patience {
-  unsigned* status;
-  bool ok = true;
-  __device__ __forceinline__ void operator()(const Asked& b) {
-    if (ok) ok = b.wait(status);
-  }
-  __device__ __forceinline__ void operator()(uint64_t* bar, uint32_t parity) {
-    if (ok) ok = mbar_wait_bounded(status, bar, parity & 1);
-  }
-};
 
 template <typename T, int KP, bool kSave>
 __global__ void __launch_bounds__(kThreads, 1) fwd_kernel(const Args a) {

@@ -35,6 +35,10 @@ __device__ __forceinline__ uint64_t desc_k(uint32_t image, int ks) {
 }
 // Columns as the operand's rows (panels of 64 follow one another), rows 16 ks .. as k.
 __device__ __forceinline__ uint64_t desc_mn(uint32_t image, int ks) { return operand(image + 2048 * ks, kPanel, 1024, 2); }
+// A triangular image spread out to whole columns: its block (i, j) is block 4 j + i.
+constexpr int kSpreadPart = 16 * 256;
+// Its blocks (i, 0 ..): columns as the operand's rows, rows as k.
+__device__ __forceinline__ uint64_t desc_tri_mn(uint32_t image, int i) { return operand(image + 512 * i, 2048, 256, 6); }
 // The blocks (j .., j) of a triangular image: rows as the operand's rows, columns as k.
 __device__ __forceinline__ uint64_t desc_tri_k(uint32_t image, int j) { return operand(image + 2 * tri_block(j, j), 16, 256, 6); }
 
@@ -76,6 +80,21 @@ __device__ __forceinline__ void tc_product_tri(uint32_t d, uint32_t a, uint32_t 
 #pragma unroll
     for (int j = 0; j < 4; ++j)
       tc_mma(d + 16 * j, a + 8 * (4 * pa + j), desc_tri_k(tri + pb * kTriPart * 2, j), product_of(64 - 16 * j, false), add || j > 0);
+    add = true;
+  };
+  if constexpr (kA == 2) term(1, 0);
+  if constexpr (kB == 2) term(0, 1);
+  term(0, 0);
+}
+
+// d = a X with X spread out: rows of X 16 i .. meet the columns up to them.
+template <int kA, int kB>
+__device__ __forceinline__ void tc_product_tri_mn(uint32_t d, uint32_t a, uint32_t tri) {
+  bool add = false;
+  auto term = [&](int pa, int pb) {
+#pragma unroll
+    for (int i = 3; i >= 0; --i)
+      tc_mma(d, a + 8 * (4 * pa + i), desc_tri_mn(tri + pb * kSpreadPart * 2, i), product_of(16 * i + 16, true), add || i < 3);
     add = true;
   };
   if constexpr (kA == 2) term(1, 0);
@@ -176,6 +195,23 @@ struct Operand64 {
       stsm4(p, h[j]);
       if constexpr (kP == 2) stsm4(p + part, l[j]);
     }
+  }
+};
+
+constexpr int kWarps = 4;  // of 16 rows each: a block's chain warps, and as many helpers
+constexpr int kFiller = 2 * kWarps, kIssuer = kFiller + 1, kHelpersIssuer = kIssuer + 1, kThreads = (kHelpersIssuer + 1) * 32;
+
+// A wait that a warp gives up on once: from then on it goes through its steps
+// without waiting (all accesses are in bounds whatever the data), so that the
+// block's barriers and its tensor memory are left in order.
+struct Patience {
+  unsigned* status;
+  bool ok = true;
+  __device__ __forceinline__ void operator()(const Asked& b) {
+    if (ok) ok = b.wait(status);
+  }
+  __device__ __forceinline__ void operator()(uint64_t* bar, uint32_t parity) {
+    if (ok) ok = mbar_wait_bounded(status, bar, parity & 1);
   }
 };
 
