@@ -408,21 +408,26 @@ __global__ void __launch_bounds__(kThreads<KP>, KP == 64 ? 2 : 1) grad_kernel(co
   }
   __syncthreads();
 
-  // eight keys a lane: the gradient of the normalisation, and out
+  // eight keys a lane: the gradient of the normalisation, and out. fp32 rows by
+  // halves, four keys of each, so that a store writes whole sectors (8 x 4096
+  // tokens of 12 heads of 64: 430 -> 409 us).
+  using Stored = std::conditional_t<kOut == kTerms, float, T>;
   constexpr int kLanes = KP / 8, kPass = kThreads<KP> / kLanes;
-  const int cl = tid % kLanes, col = 8 * cl;
+  constexpr bool kHalves = sizeof(Stored) == 4;
+  const int cl = tid % kLanes, c0 = kHalves ? 4 * cl : 8 * cl, c1 = kHalves ? KP / 2 + 4 * cl : 8 * cl + 4;
 #pragma unroll
   for (int id = tid / kLanes; id < 2 * kC; id += kPass) {
     const bool is_k = id >= kC;
     const int i = id % kC;
     float d[8];
-    load8(d, &sm.m.out[is_k][i][col]);
+    const float4 lo = *reinterpret_cast<const float4*>(&sm.m.out[is_k][i][c0]), hi = *reinterpret_cast<const float4*>(&sm.m.out[is_k][i][c1]);
+    d[0] = lo.x, d[1] = lo.y, d[2] = lo.z, d[3] = lo.w, d[4] = hi.x, d[5] = hi.y, d[6] = hi.z, d[7] = hi.w;
     if (kOut != kTerms && a.s.l2norm) {
       const __half* im = is_k ? sm.k : sm.q;
       float x[8], xd = 0.f;
 #pragma unroll
       for (int e = 0; e < 4; ++e) {
-        const float2 y = pick2<P, KP>(im, i, col + 2 * e);
+        const float2 y = pick2<P, KP>(im, i, (e < 2 ? c0 : c1) + 2 * (e & 1));
         x[2 * e] = y.x, x[2 * e + 1] = y.y;
       }
 #pragma unroll
@@ -432,11 +437,14 @@ __global__ void __launch_bounds__(kThreads<KP>, KP == 64 ? 2 : 1) grad_kernel(co
 #pragma unroll
       for (int e = 0; e < 8; ++e) d[e] = r * fmaf(f, x[e], d[e]);
     }
-    if (i < c.len && col < K) {
-      if constexpr (kOut == kTerms) {
-        store8((is_k ? a.b.dk_part : a.b.dq_part) + ((tok + i) * a.s.Hv + hv0) * K + col, d);
-      } else {
-        store8(static_cast<T*>(is_k ? a.dk : a.dq) + ((tok + i) * a.s.Hk + hk) * K + col, d);
+    if (i < c.len) {
+      Stored* out = kOut == kTerms ? reinterpret_cast<Stored*>(is_k ? a.b.dk_part : a.b.dq_part) + ((tok + i) * a.s.Hv + hv0) * K
+                                   : static_cast<Stored*>(is_k ? a.dk : a.dq) + ((tok + i) * a.s.Hk + hk) * K;
+      if constexpr (kHalves) {
+        if (c0 < K) *reinterpret_cast<float4*>(out + c0) = make_float4(d[0], d[1], d[2], d[3]);
+        if (c1 < K) *reinterpret_cast<float4*>(out + c1) = make_float4(d[4], d[5], d[6], d[7]);
+      } else if (c0 < K) {
+        store8(out + c0, d);
       }
     }
   }
