@@ -98,12 +98,8 @@ __device__ __forceinline__ void fill(BwdSmem<T, KP>& m, const Args& a, long long
     if (s + 1 < n) k(s + 1);
     ask(s + 2);
   }
-  if (s < n) {  // given up: no copy is left in flight
-    for (uint64_t* b : {&m.full_k[0], &m.full_k[1], &m.full_q, &m.full_t, &m.full_p}) {
-      mbar_wait_bounded(nullptr, b, 0, 1000000);
-      mbar_wait_bounded(nullptr, b, 1, 1000000);
-    }
-  }
+  if (s < n)
+    for (uint64_t* b : {&m.full_k[0], &m.full_k[1], &m.full_q, &m.full_t, &m.full_p}) drain(b);
 }
 
 // A warp's image to memory, `kHalves` of it. (By loads and stores: the proxy fence

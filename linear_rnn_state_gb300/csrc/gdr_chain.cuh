@@ -1,113 +1,31 @@
-// What the forward and the backward chain of the gated delta rule share.
+// What the forward and the backward chain of the gated delta rule share, beside
+// the tensor cores' part (gdr_tc.cuh): barriers, the rows of v, o, do and dv, the
+// state.
 //
-// A warp owns 16 rows of the state (value columns) and all keys, and keeps them
-// as the accumulator of its products. With the rows as the m of every product
-// (S k^T, r T^T, u P^T, w^T k are 16 x 64 or 16 x keys) the result of one is,
-// packed to fp16 pairs, the A operand of the next (to_a): the whole step runs
-// in registers, warps never wait for one another, and every scale is the exact
-// maximum of the warp's own values. Only the chunk's images of q, k, T and P
-// come from shared memory, read by all warps of the block, which take the same
-// head's rows. (Measured before: tiles of 16 tokens by 16 columns a warp, with
-// each intermediate in shared memory, spent 42 % of a step on shared-memory
-// reads and another 25 % at three barriers.)
+// A warp has 16 rows of the state (value columns) and all keys. With the rows as
+// the m of every product (S k^T, r T^T, u P^T, w^T k are 16 x 64 or 16 x keys) the
+// result of one is, scaled and packed to fp16 pairs, the left operand of the next,
+// warps never exchange values, and every scale is the exact maximum of the warp's
+// own. Between two products all is in registers, laid out as mma.sync's
+// accumulator tiles.
 //
-// A warp alone on its scheduler pays every latency of its step, so the step is
-// cut in two: the chain's warp makes only what the next state waits for, and a
-// helper warp beside it (on the same scheduler) makes the rest, o in the forward
-// and the products with do in the backward, and moves the rows and images to and
-// from memory. They meet through the images in shared memory, with a barrier for
-// each one full and one free again.
+// The chain's warps make only what the next state waits for; helper warps beside
+// them make the rest, o in the forward and the products with do in the backward,
+// and move the rows and images to and from memory. They meet at a barrier for
+// each thing full and one for it free again.
 //
-// One more warp fills the chunk's images by bulk copies: q, T and P have one
-// place each and k two, each filled again as soon as its readers are past their
-// last use in the step.
+// History of a step at 64 keys, bfloat16, forward: tiles of 16 tokens by 16
+// columns a warp with intermediates in shared memory, 411 us for 64 steps (42 % of
+// it shared-memory reads, 25 % three barriers); 16 rows a warp by mma.sync, in
+// registers, 254; helper warps, 194; barriers asked early, 178; tcgen05 with left
+// operands in shared memory, 183 to 210; in tensor memory, 189; products issued by
+// warps of their own, 138.
 #pragma once
 
 #include "gdr_common.cuh"
 
 namespace gdr {
 
-
-// pT: parts of the P image that the chain reads.
-template <int P, int KP, int pT>
-struct alignas(128) Images {
-  __half k[2][P * kC * KP];
-  __half q[P * kC * KP];
-  __half t[2 * kTriPart], p[pT * kTriPart];
-  unsigned char scal[2][kChainScal];
-  uint64_t full_k[2], full_q, full_t, full_p;
-  uint64_t free_k[2], free_q, free_p;
-  __device__ __forceinline__ const Scal& sc(int place) const { return *reinterpret_cast<const Scal*>(scal[place]); }
-};
-
-// Chains and helpers read k's place (it has the scalars too), helpers q and P,
-// chains T, which goes free with k.
-template <int P, int KP, int pT>
-__device__ __forceinline__ void init_images(Images<P, KP, pT>& m, int chains) {
-  for (uint64_t* b : {&m.full_k[0], &m.full_k[1], &m.full_q, &m.full_t, &m.full_p}) mbar_init(b, 1);
-  for (uint64_t* b : {&m.free_q, &m.free_p}) mbar_init(b, chains);
-  for (uint64_t* b : {&m.free_k[0], &m.free_k[1]}) mbar_init(b, 2 * chains);
-}
-
-// The filling thread: images of steps 0 .. n - 1, whose chunk slots are slot0 +
-// s or, backwards, slot0 - s. Later steps are asked into L2 two steps ahead.
-template <int P, int KP, int pT>
-__device__ __forceinline__ void fill_images(Images<P, KP, pT>& m, const Args& a, long long slot0, int direction, int n, int hk,
-                                            int hv) {
-  constexpr int image = P * kC * KP * 2, tri = kTriPart * 2;
-  auto at_k = [&](int s) { return (size_t)(slot0 + (long long)direction * s) * a.s.Hk + hk; };
-  auto at_v = [&](int s) { return (size_t)(slot0 + (long long)direction * s) * a.s.Hv + hv; };
-  auto k = [&](int s) {
-    uint64_t* bar = &m.full_k[s & 1];
-    mbar_arrive_expect_tx(bar, image + kChainScal);
-    bulk_load(m.k[s & 1], a.b.k_img + at_k(s) * image, image, bar);
-    bulk_load(m.scal[s & 1], a.b.scal + at_v(s), kChainScal, bar);
-  };
-  auto q = [&](int s) {
-    mbar_arrive_expect_tx(&m.full_q, image);
-    bulk_load(m.q, a.b.q_img + at_k(s) * image, image, &m.full_q);
-  };
-  auto t = [&](int s) {
-    mbar_arrive_expect_tx(&m.full_t, 2 * tri);
-    bulk_load(m.t, a.b.t_img + at_v(s) * Layout::tp_img, 2 * tri, &m.full_t);
-  };
-  auto p = [&](int s) {
-    mbar_arrive_expect_tx(&m.full_p, pT * tri);
-    bulk_load(m.p, a.b.p_img + at_v(s) * Layout::tp_img, pT * tri, &m.full_p);
-  };
-  auto ask = [&](int s) {
-    if (s >= n) return;
-    bulk_prefetch(a.b.k_img + at_k(s) * image, image);
-    bulk_prefetch(a.b.q_img + at_k(s) * image, image);
-    bulk_prefetch(a.b.t_img + at_v(s) * Layout::tp_img, 2 * tri);
-    bulk_prefetch(a.b.p_img + at_v(s) * Layout::tp_img, pT * tri);
-    bulk_prefetch(a.b.scal + at_v(s), kChainScal);
-  };
-  auto given_up = [&](uint64_t* bar, int use) { return mbar_wait_bounded(a.status, bar, use & 1); };
-  if (n <= 0) return;
-  k(0), q(0), t(0), p(0);
-  if (n > 1) k(1);
-  ask(2);
-  for (int s = 1; s < n; ++s) {  // in the order in which step s - 1 gives the places up
-    if (direction > 0) {
-      if (!given_up(&m.free_q, s - 1)) return;
-      q(s);
-    } else {
-      if (!given_up(&m.free_p, s - 1)) return;
-      p(s);
-      if (!given_up(&m.free_q, s - 1)) return;
-      q(s);
-    }
-    if (!given_up(&m.free_k[(s - 1) & 1], (s - 1) >> 1)) return;
-    t(s);
-    if (s + 1 < n) k(s + 1);
-    if (direction > 0) {
-      if (!given_up(&m.free_p, s - 1)) return;
-      p(s);
-    }
-    ask(s + 2);
-  }
-}
 // A barrier asked early (a try_wait takes some 85 cycles to answer) and waited
 // for only where the answer was no.
 struct Asked {
@@ -259,14 +177,6 @@ __device__ __forceinline__ void store_state(const float (&S)[N][4], float* dst, 
 
 __device__ __forceinline__ void copy_arrive(uint64_t* bar) {  // once this lane's copies so far have landed
   asm volatile("cp.async.mbarrier.arrive.noinc.shared::cta.b64 [%0];" ::"r"(smem_addr(bar)) : "memory");
-}
-
-// Chains of a block: as many as `most`, one a scheduler, unless that leaves half
-// the SMs without a block; then two.
-inline int chain_warps(const Shape& s, int most) {
-  const long long tiles = v_tiles(s.V);
-  const int w = tiles < most ? (int)tiles : most;
-  return w > 2 && (long long)s.nseq * s.Hv * ((tiles + w - 1) / w) <= 152 / 2 ? 2 : w;
 }
 
 }  // namespace gdr

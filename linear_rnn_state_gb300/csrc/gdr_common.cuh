@@ -75,16 +75,6 @@ __device__ __forceinline__ void store8(float* p, const float (&x)[8]) {
   *reinterpret_cast<float4*>(p) = make_float4(x[0], x[1], x[2], x[3]);
   *reinterpret_cast<float4*>(p + 4) = make_float4(x[4], x[5], x[6], x[7]);
 }
-__device__ __forceinline__ float2 load2(const __nv_bfloat16* p) {
-  const uint32_t u = *reinterpret_cast<const uint32_t*>(p);
-  return make_float2(__uint_as_float(u << 16), __uint_as_float(u & 0xFFFF0000u));
-}
-__device__ __forceinline__ float2 load2(const float* p) { return *reinterpret_cast<const float2*>(p); }
-__device__ __forceinline__ void store2(__nv_bfloat16* p, float a, float b) {
-  *reinterpret_cast<__nv_bfloat162*>(p) = __floats2bfloat162_rn(a, b);
-}
-__device__ __forceinline__ void store2(float* p, float a, float b) { *reinterpret_cast<float2*>(p) = make_float2(a, b); }
-
 // ---------------------------------------------------------- fp16 pairs ---
 
 __device__ __forceinline__ uint32_t pack_f16(float lo, float hi) {
@@ -217,19 +207,6 @@ __device__ __forceinline__ void a_tri_t(Frag<2>& f, const __half* s, int i, int 
   ldsm4t(f.h, p);
   ldsm4t(f.l, p + kTriPart);
 }
-// B fragments of the block (i, j): B[k][n] = X[16 i + n][16 j + k], or X[16 i + k][16 j + n].
-template <int kP>
-__device__ __forceinline__ void b_tri_nk(Frag<kP>& f, const __half* s, int i, int j, int lane) {
-  const __half* p = s + tri_block(i, j) + tri_at((lane & 7) + (lane >> 4) * 8, ((lane >> 3) & 1) * 8);
-  ldsm4(f.h, p);
-  if constexpr (kP == 2) ldsm4(f.l, p + kTriPart);
-}
-template <int kP>
-__device__ __forceinline__ void b_tri_kn(Frag<kP>& f, const __half* s, int i, int j, int lane) {
-  const __half* p = s + tri_block(i, j) + tri_at(lane & 15, (lane >> 4) * 8);
-  ldsm4t(f.h, p);
-  if constexpr (kP == 2) ldsm4t(f.l, p + kTriPart);
-}
 __device__ __forceinline__ void put2_tri(__half* s, int row, int col, float x0, float x1) {
   uint32_t hi, lo;
   split2<2>(x0, x1, hi, lo);
@@ -265,21 +242,17 @@ __device__ __forceinline__ void mma_parts_first(float (&d0)[4], float (&d1)[4], 
 
 // N pairs of n8 tiles += a b[n] (or, kFirst, = a b[n]): part by part over all of
 // them, so that two mma on one accumulator stand 2 N apart (a dependent mma waits
-// 38 cycles, an independent one 8 to 16). kHi: of a its hi part alone.
-template <int N, bool kFirst = false, bool kHi = false, int kA, int kB, int kTilesOf>
-__device__ __forceinline__ void mma_row(float (&d)[kTilesOf][4], const Frag<kA>& a, const Frag<kB> (&b)[N], int first = 0, int end = N) {
-  constexpr bool lh = kA == 2 && !kHi, hl = kB == 2;
-  if constexpr (lh)
+// 38 cycles, an independent one 8 to 16).
+template <int N, bool kFirst = false, int kA, int kB, int kTilesOf>
+__device__ __forceinline__ void mma_row(float (&d)[kTilesOf][4], const Frag<kA>& a, const Frag<kB> (&b)[N]) {
+  if constexpr (kA == 2)
 #pragma unroll
-    for (int n = 0; n < N; ++n)
-      if (n >= first && n < end) mma_pair<kFirst>(d[2 * n], d[2 * n + 1], a.l, b[n].h);
-  if constexpr (hl)
+    for (int n = 0; n < N; ++n) mma_pair<kFirst>(d[2 * n], d[2 * n + 1], a.l, b[n].h);
+  if constexpr (kB == 2)
 #pragma unroll
-    for (int n = 0; n < N; ++n)
-      if (n >= first && n < end) mma_pair<kFirst && !lh>(d[2 * n], d[2 * n + 1], a.h, b[n].l);
+    for (int n = 0; n < N; ++n) mma_pair<kFirst && kA != 2>(d[2 * n], d[2 * n + 1], a.h, b[n].l);
 #pragma unroll
-  for (int n = 0; n < N; ++n)
-    if (n >= first && n < end) mma_pair<kFirst && !lh && !hl>(d[2 * n], d[2 * n + 1], a.h, b[n].h);
+  for (int n = 0; n < N; ++n) mma_pair<kFirst && kA != 2 && kB != 2>(d[2 * n], d[2 * n + 1], a.h, b[n].h);
 }
 
 // Two accumulator tiles (16 rows, columns k0 .. k0+7 and k0+8 .. k0+15) times s
@@ -295,14 +268,6 @@ __device__ __forceinline__ void to_a(Frag<kP>& f, const float (&x)[4], const flo
 #pragma unroll
     for (int i = 0; i < 4; ++i) f.l[i] = l[i];
 }
-// An A fragment into an image of 16 rows, where a_mk would read it.
-template <int kP>
-__device__ __forceinline__ void put_a(__half* s, int part, int k0, const Frag<kP>& f, int lane) {
-  __half* p = s + img(16, lane & 15, k0 + (lane >> 4) * 8);
-  stsm4(p, f.h);
-  if constexpr (kP == 2) stsm4(p + part, f.l);
-}
-
 // ---------------------------------------------------------- bulk copies ---
 
 __device__ __forceinline__ void bulk_load(void* dst, const void* src, uint32_t bytes, uint64_t* bar) {

@@ -102,12 +102,8 @@ __device__ __forceinline__ void fill(FwdSmem<T, KP, kSave>& m, const Args& a, lo
     p(c);
     ask(c + 2);
   }
-  if (c < n) {  // given up: no copy is left in flight
-    for (uint64_t* b : {&m.full_k[0], &m.full_k[1], &m.full_q, &m.full_t, &m.full_p}) {
-      mbar_wait_bounded(nullptr, b, 0, 1000000);
-      mbar_wait_bounded(nullptr, b, 1, 1000000);
-    }
-  }
+  if (c < n)
+    for (uint64_t* b : {&m.full_k[0], &m.full_k[1], &m.full_q, &m.full_t, &m.full_p}) drain(b);
 }
 
 template <typename T, int KP, bool kSave>
