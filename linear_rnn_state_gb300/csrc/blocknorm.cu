@@ -17,6 +17,13 @@
 // sums over rows: a block walks rows a grid apart, keeps its columns' sums in
 // registers and writes them as one partial row; a last kernel adds the
 // partial rows in order (no atomics, the same bits every time).
+//
+// Measured: add, 16384 x 2048, x bfloat16 and residual fp32, 60 us forward (6.7
+// TB/s, a copy's rate) and 107 backward (5.6 TB/s, the two sums kept beside the
+// rows); gated, 16384 x 32 rows of 64, bfloat16, 40 us forward (5.0 TB/s) and 58
+// backward (5.8 TB/s): a row of 64 leaves a thread eight values between its loads
+// and its store, two rows a thread gave 38 us and took the add norm to 62. The
+// sums' kernel adds 5 us. One row: 2.1 us on the device, the rest is the call.
 #include <cuda_bf16.h>
 
 #include "blocknorm_launch.h"
