@@ -1,5 +1,7 @@
 // C ABI of the gated delta rule (gdr.h): argument checks, the regions of the
 // caller's buffers, and the launches.
+#include <algorithm>
+
 #include "api_check.h"
 #include "gdr.h"
 #include "gdr_launch.h"
@@ -50,6 +52,7 @@ int set_shape(Shape& s, int B, int T, int Hk, int Hv, int K, int V, int nseq) {
   s = Shape{};
   s.B = B, s.T = T, s.Hk = Hk, s.Hv = Hv, s.K = K, s.V = V;
   s.nseq = nseq >= 0 ? nseq : B;
+  s.packed = nseq >= 0;
   const unsigned long long slots = slot_count(B, T, s.nseq, nseq >= 0);
   if (slots * (Hv ? Hv : 1) * v_tiles(V) >= kMaxBlocks || (unsigned long long)s.nseq * Hv * v_tiles(V) >= kMaxBlocks)
     return fail(WKV7_ERR_INVALID, "too many chunks");
@@ -74,9 +77,8 @@ size_t place_saved(Buffers& b, const Shape& s, bool bf16, bool for_backward, cha
   b.t_img = take(l.n_v * Layout::tp_img);
   b.p_img = take(l.n_v * Layout::tp_img);
   b.scal = reinterpret_cast<Scal*>(take(l.n_v * sizeof(Scal)));
-  if (for_backward) {
-    b.f_rec = take(l.n_t * l.f_rec);
-  }
+  if (for_backward) b.f_rec = take(l.n_t * l.f_rec);
+  b.carry = segments_of(s) > 1 ? reinterpret_cast<float*>(take((size_t)s.nseq * s.Hv * s.V * s.K * 4)) : nullptr;
   return at - p;
 }
 size_t place_workspace(Buffers& b, const Shape& s, bool bf16, char* p) {
@@ -135,8 +137,18 @@ int forward_impl(bool bf16, const void* q, const void* k, const void* v, const f
   a.s.q_b = st[0], a.s.q_t = st[1], a.s.k_b = st[2], a.s.k_t = st[3], a.s.v_b = st[4], a.s.v_t = st[5];
   a.q = q, a.k = k, a.v = v, a.g = g, a.beta = beta, a.s_init = s_init, a.o = o, a.s_final = s_final;
   if ((rc = wkv7::api_status_word(&a.status))) return rc;
-  if ((rc = launched(launch_prep(a, bf16, stream), "chunk preparation"))) return rc;
-  return launched(launch_fwd(a, bf16, for_backward, stream), "forward");
+  const int parts = segments_of(a.s), chunks = (T + kC - 1) / kC, each = (chunks + parts - 1) / parts;
+  for (int at = 0; at < chunks || at == 0; at += each) {
+    if (parts > 1) {
+      a.seg0 = at, a.segn = std::min(each, chunks - at);
+      if (at) a.s_init = a.s_final;
+      if (!s_final) a.s_final = a.b.carry;
+    }
+    if ((rc = launched(launch_prep(a, bf16, stream), "chunk preparation"))) return rc;
+    if ((rc = launched(launch_fwd(a, bf16, for_backward, stream), "forward"))) return rc;
+    if (parts == 1) break;
+  }
+  return WKV7_OK;
 }
 
 int backward_impl(bool bf16, const void* q, const void* k, const void* v, const float* g, const float* beta,

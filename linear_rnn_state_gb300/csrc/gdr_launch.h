@@ -26,6 +26,7 @@ struct Shape {
   int nseq;             // sequences: B, or those packed in the one batch row
   const int* starts;    // device [nseq + 1], or null
   int slots;            // chunk slots: an upper bound of the chunks, see slot_count
+  int packed;           // nseq sequences in one batch row
   int l2norm;
   float scale;
   long long q_b, q_t, k_b, k_t, v_b, v_t;  // element strides of a batch row and of a token
@@ -114,6 +115,7 @@ struct Buffers {
   // forward: the images of the state before the chunk and of u, their inverse
   // scales; of the backward: of the carried gradient after it, lambda and do.
   char *f_rec, *b_rec;
+  float* carry;                   // states from segment to segment, where the caller wants none
   float *dq_part, *dk_part;       // [B][T][Hv][K] terms of shared heads' gradients, or null
 };
 
@@ -125,10 +127,21 @@ struct Args {
   float *s_final, *dg, *dbeta, *dS_init;
   Buffers b;
   unsigned* status;
+  int seg0, segn;  // the chunks of a sequence that this launch is about (segments_of), segn 0: all
   int small;  // few chunks: a call's kernels may begin while the one before still runs (launch_after).
               // Saves 4 of 31 us for one chunk; 40 heads of 1024 chunks lost 650 of 3900 us to blocks
               // that waited where others could have run.
 };
+// A forward in segments, the preparation of one beside the chain of the one
+// before: where the chains leave half of the SMs free or more, and segments have
+// 64 chunks or more. 40 heads of 1024 chunks 2985 us in one, 2467 in four, 2399 in
+// eight, 2384 in sixteen; 96 heads of 64 chunks, forward and backward, 960 in one,
+// 944 in two and 971 in four.
+inline int segments_of(const Shape& s) {
+  const int n = (s.T + kC - 1) / kC, most = n / 64;
+  const long long chains = (long long)s.nseq * s.Hv * ((v_tiles(s.V) + 3) / 4);
+  return s.packed || chains > 152 / 2 || most < 2 ? 1 : most < 16 ? most : 16;
+}
 inline int is_small(const Shape& s) { return (long long)s.slots * s.Hv <= 152; }
 
 cudaError_t launch_prep(const Args& a, bool bf16, cudaStream_t stream);

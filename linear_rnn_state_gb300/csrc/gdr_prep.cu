@@ -187,7 +187,9 @@ __global__ void __launch_bounds__(kThreads, kBlocks<T, KP>) prep_kernel(const Ar
   PrepSmem<T, KP>& sm = *reinterpret_cast<PrepSmem<T, KP>*>(raw);
   constexpr int P = In<T>::kParts;
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
-  const int slot = blockIdx.x / a.s.Hk, hk = blockIdx.x % a.s.Hk;
+  const int hk = blockIdx.x % a.s.Hk;
+  int slot = blockIdx.x / a.s.Hk;
+  if (a.segn) slot = slot / a.segn * ((a.s.T + kC - 1) / kC) + a.seg0 + slot % a.segn;
   if (a.small) grid_go();
   ChunkAt c;
   if (!chunk_at(a.s, slot, c)) return;
@@ -483,6 +485,8 @@ __global__ void __launch_bounds__(kThreads, kBlocks<T, KP>) prep_kernel(const Ar
     if (hg + 1 < group) __syncthreads();
   }
   if (tid == 0) bulk_wait_all();
+  // begun beside the chain of the segment before: over only when that is, for the next chain
+  if (a.seg0 && blockIdx.x == 0) grid_wait();
 }
 
 template <typename T, int KP, bool kOne>
@@ -491,8 +495,8 @@ cudaError_t launch(const Args& a, cudaStream_t stream) {
   static std::atomic<unsigned long long> done{0};
   cudaError_t e = allow_smem(reinterpret_cast<const void*>(prep_kernel<T, KP, kOne>), smem, done);
   if (e != cudaSuccess) return e;
-  prep_kernel<T, KP, kOne><<<(unsigned)((size_t)a.s.slots * a.s.Hk), kThreads, smem, stream>>>(a);
-  return cudaGetLastError();
+  const size_t slots = a.segn ? (size_t)a.s.B * a.segn : a.s.slots;
+  return launch_after(a.seg0 > 0, prep_kernel<T, KP, kOne>, (unsigned)(slots * a.s.Hk), kThreads, smem, stream, a);
 }
 
 template <typename T, int KP>

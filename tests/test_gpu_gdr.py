@@ -131,6 +131,25 @@ def test_more_and_fewer_heads_than_sms(env, B, Hv):
     _check(env, _make(B, 70, Hv, Hv, 16, 64, F32, B), carry=False)
 
 
+@pytest.mark.parametrize("dtype", [BF16, F32], ids=["bf16", "f32"])
+@pytest.mark.parametrize("B,T", [(2, 8191), (1, 8193), (1, 12345)])
+def test_long_sequences_of_few_heads(env, B, T, dtype):
+    # 128 chunks, 129 and 193: the forward goes in segments of its own accord
+    orc, gdr = env
+    d = _make(B, T, 1, 2, 16, 24, dtype, T, rate=0.1)
+    o, s, _ = _check(env, d)
+    o2, none, _ = gdr.forward(*(d[n] for n in INS), d["s_init"], want_s_final=False)
+    assert none is None and torch.equal(o2, o)
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        o3, s3, _ = gdr.forward(*(d[n] for n in INS), d["s_init"], want_saved=False)
+    o3.zero_()
+    graph.replay()
+    torch.cuda.synchronize()
+    assert torch.equal(s3, s)
+    _close("o", o3, o.double().cpu().numpy())
+
+
 def test_one_token_from_nothing_has_no_decay_gradient(env):
     _, _, g = _check(env, _make(3, 1, 2, 2, 64, 64, BF16), carry=False)
     assert torch.count_nonzero(g["dg"]) == 0
