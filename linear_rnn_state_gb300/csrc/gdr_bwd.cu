@@ -38,6 +38,7 @@ struct alignas(1024) BwdSmem {
   } out[kWarps];
   unsigned char d[kWarps][kPlaces][kRowsBytes<T>];
   unsigned char scal[2][kChainScal];
+  float most[3][kWarps][2];  // of the chain warps' dS, y and e^G lam
   float inv_s[kWarps], inv_d[2][kWarps], inv_g[2][kWarps];  // inverse scales of the warps' rows
   uint64_t full_k[2], full_q, full_t, full_p, free_k[2], free_q, free_t, free_p;
   uint64_t done_x, done_y, done_l, done_w, done_g, end[2];    // products
@@ -124,7 +125,7 @@ __global__ void __launch_bounds__(kThreads, 1) bwd_kernel(const Args a) {
   extern __shared__ __align__(1024) unsigned char raw[];
   using Smem = BwdSmem<T, KP>;
   using Col = Columns<KP>;
-  constexpr int P = In<T>::kParts, kNt = KP / 8, kPlaces = Smem::kPlaces;
+  constexpr int P = In<T>::kParts, kPlaces = Smem::kPlaces;
   Smem& sm = *reinterpret_cast<Smem*>(raw + (-smem_addr(raw) & 1023u));
   const int warp = __shfl_sync(0xffffffffu, threadIdx.x >> 5, 0), lane = threadIdx.x & 31, t4 = lane & 3, own = warp & 3;
   const int vts = (a.s.V + kVt - 1) / kVt, sets = (vts + kWarps - 1) / kWarps;
@@ -134,10 +135,13 @@ __global__ void __launch_bounds__(kThreads, 1) bwd_kernel(const Args a) {
     for (uint64_t* b : {&sm.full_k[0], &sm.full_k[1], &sm.full_q, &sm.full_t, &sm.full_p, &sm.free_q, &sm.free_t, &sm.free_p,
                         &sm.done_x, &sm.done_y, &sm.done_l, &sm.done_w, &sm.done_g, &sm.end[0], &sm.end[1]})
       mbar_init(b, 1);
-    for (uint64_t* b : {&sm.free_k[0], &sm.free_k[1]}) mbar_init(b, 2 * kWarps + 1);
-    for (uint64_t* b : {&sm.free_y, &sm.free_g, &sm.ready_s, &sm.ready_y, &sm.ready_w, &sm.ready_d, &sm.ready_e}) mbar_init(b, kWarps);
-    for (int i = 0; i < kWarps; ++i)
-      for (uint64_t* b : {&sm.full_s[i], &sm.free_s[i], &sm.full_l[i], &sm.free_l[i], &sm.full_d[i]}) mbar_init(b, 1);
+    for (uint64_t* b : {&sm.free_k[0], &sm.free_k[1]}) mbar_init(b, kChains + kWarps + 1);
+    for (uint64_t* b : {&sm.free_y, &sm.free_g, &sm.ready_s, &sm.ready_y, &sm.ready_w}) mbar_init(b, kChains);
+    for (uint64_t* b : {&sm.ready_d, &sm.ready_e}) mbar_init(b, kWarps);
+    for (int i = 0; i < kWarps; ++i) {
+      for (uint64_t* b : {&sm.full_s[i], &sm.full_l[i]}) mbar_init(b, 2);
+      for (uint64_t* b : {&sm.free_s[i], &sm.free_l[i], &sm.full_d[i]}) mbar_init(b, 1);
+    }
     wkv7::fence_mbar_init();
   }
   if (warp == kFiller) wkv7::tmem_alloc(&sm.tmem, Col::all);
@@ -218,117 +222,114 @@ __global__ void __launch_bounds__(kThreads, 1) bwd_kernel(const Args a) {
     }
     if (elected()) tc_commit(&sm.end[1]);
     mbar_wait_bounded(a.status, &sm.end[1], 0);
-  } else if (warp < kWarps) {  // ------------------------------------------ chain
+  } else if (warp < kChains) {  // ----------------------------------------- chain
+    constexpr int kS = KP / 16;                // n8 tiles of the warp's half of the keys
+    const int half = warp / kWarps, key0 = half * (KP / 2), token0 = half * (kC / 2);
+    const uint32_t s_in = mine + Col::s_in + half * (KP / 4), y_in = mine + Col::s_in + half * (kC / 4);
     const size_t state_at = (((size_t)seq * a.s.Hv + hv) * V + vt * kVt) * K;
-    float S[kNt][4];
-    load_state(S, a.dS_final ? a.dS_final + state_at : nullptr, cols, K, lane);
-    float s_max = warp_max(S);
+    auto both = [&](float m, int which) { return both_max(m, sm.most[which][own], half, 1 + own, lane); };
+    float S[kS][4];
+    load_state(S, a.dS_final ? a.dS_final + state_at : nullptr, cols, key0, K, lane);
+    float s_max = both(warp_max(S), 0);
     for (int s = 0; s < n; ++s) {
       const int use = s & 1;
       const Scal& sc = sm.sc(use);
       // dS1 k^T
       const float sS = pow2_scale(s_max), inv_s = pow2_inverse(sS);
       const Asked has_s(&sm.free_s[own], use ^ 1);
-      Operand64<2> f[KP / 64];
-#pragma unroll
-      for (int i = 0; i < KP / 64; ++i) f[i].split(S + 8 * i, sS), f[i].store(mine + Col::s_in + 32 * i, KP / 2);
+      Operand<2, kS / 2> f;
+      f.split(S, sS), f.store(s_in, KP / 2);
       ready(&sm.ready_s);
       const Asked has_k(&sm.full_k[use], s >> 1), has_d(&sm.full_d[own], use);
       if (s > 0) wait(has_s);
-      if (lane == 0) sm.inv_s[own] = inv_s;
-#pragma unroll
-      for (int i = 0; i < KP / 64; ++i) f[i].put(sm.s[own], kVt * KP, 64 * i, lane);
+      if (lane == 0 && half == 0) sm.inv_s[own] = inv_s;
+      f.put(sm.s[own], kVt * KP, key0, lane);
       signal(&sm.full_s[own], lane);
 
       // y
-      float x[8][4], y[8][4];
+      float x[4][4], y[4][4];
       wait(has_k);
       wait(has_d);
       const float fy = sc.inv_p * sm.inv_d[use][own], inv_g = sm.inv_g[use][own];
-      float2 wk[8];
+      float2 wk[4];
 #pragma unroll
-      for (int nt = 0; nt < 8; ++nt)
-        wk[nt] = mul2(*reinterpret_cast<const float2*>(sc.wk + 8 * nt + 2 * t4), make_float2(inv_s, inv_s));
+      for (int nt = 0; nt < 4; ++nt)
+        wk[nt] = mul2(*reinterpret_cast<const float2*>(sc.wk + token0 + 8 * nt + 2 * t4), make_float2(inv_s, inv_s));
       wait(&sm.done_y, use);
       tmem_fence_after_sync();
-      tc_load(y, mine + Col::y);
+      tc_load(y, mine + Col::y + token0);
       tc_loaded(y);
 #pragma unroll
-      for (int nt = 0; nt < 8; ++nt)
+      for (int nt = 0; nt < 4; ++nt)
 #pragma unroll
         for (int h = 0; h < 2; ++h) set_pair(y[nt], h, mul2(pair_of(y[nt], h), make_float2(fy, fy)));
       wait(&sm.done_x, use);
       tmem_fence_after_sync();
-      tc_load(x, mine + Col::x);
+      tc_load(x, mine + Col::x + token0);
       tc_loaded(x);
 #pragma unroll
-      for (int nt = 0; nt < 8; ++nt)
+      for (int nt = 0; nt < 4; ++nt)
 #pragma unroll
         for (int h = 0; h < 2; ++h) set_pair(y[nt], h, fma2(wk[nt], pair_of(x[nt], h), pair_of(y[nt], h)));
-      const float sY = pow2_scale(warp_max(y)), fl = sc.inv_t * pow2_inverse(sY);
+      const float sY = pow2_scale(both(warp_max(y), 1)), fl = sc.inv_t * pow2_inverse(sY);
       {
-        Operand64<2> fy_in;
-        fy_in.split(y, sY), fy_in.store(mine + Col::s_in, 32);
+        Operand<2, 2> f2;
+        f2.split(y, sY), f2.store(y_in, 32);
       }
       ready(&sm.ready_y);
       signal(&sm.free_y, lane);
 
       // lam = T^T y
       const Asked has_l(&sm.free_l[own], use ^ 1);
-      float2 ek[8];
+      float2 ek[4];
 #pragma unroll
-      for (int nt = 0; nt < 8; ++nt)
-        ek[nt] = mul2(*reinterpret_cast<const float2*>(sc.ek + 8 * nt + 2 * t4), make_float2(-fl, -fl));
+      for (int nt = 0; nt < 4; ++nt)
+        ek[nt] = mul2(*reinterpret_cast<const float2*>(sc.ek + token0 + 8 * nt + 2 * t4), make_float2(-fl, -fl));
       const float egc = sc.egc;
       wait(&sm.done_l, use);
       tmem_fence_after_sync();
-      tc_load(x, mine + Col::l);
+      tc_load(x, mine + Col::l + token0);
       tc_loaded(x);
 
       // e^G lam, and the state's gradient
 #pragma unroll
-      for (int nt = 0; nt < 8; ++nt)
+      for (int nt = 0; nt < 4; ++nt)
 #pragma unroll
         for (int h = 0; h < 2; ++h) set_pair(y[nt], h, mul2(pair_of(x[nt], h), ek[nt]));
-      const float sW = pow2_scale(warp_max(y)), inv_w = pow2_inverse(sW);
+      const float sW = pow2_scale(both(warp_max(y), 2)), inv_w = pow2_inverse(sW);
       {
-        Operand64<2> fw;
-        fw.split(y, sW), fw.store(mine + Col::s_in, 32);
+        Operand<2, 2> fw;
+        fw.split(y, sW), fw.store(y_in, 32);
       }
       ready(&sm.ready_w);
       if (s > 0) wait(has_l);
-      tiles_put(sm.l[own], x, fl, lane);
+      tiles_put(sm.l[own] + token0 / 8 * 32, x, fl, lane);
       signal(&sm.full_l[own], lane);
       signal(&sm.free_k[use], lane);
 #pragma unroll
-      for (int nt = 0; nt < kNt; ++nt)
+      for (int nt = 0; nt < kS; ++nt)
 #pragma unroll
         for (int h = 0; h < 2; ++h) set_pair(S[nt], h, mul2(pair_of(S[nt], h), make_float2(egc, egc)));
+      auto add = [&](uint32_t at, float f) {
+        float z[kS][4];
+        tc_load(z, at);
+        tc_loaded(z);
+#pragma unroll
+        for (int nt = 0; nt < kS; ++nt)
+#pragma unroll
+          for (int h = 0; h < 2; ++h) set_pair(S[nt], h, fma2(make_float2(f, f), pair_of(z[nt], h), pair_of(S[nt], h)));
+      };
       wait(&sm.done_g, use);
       tmem_fence_after_sync();
-      auto add = [&](uint32_t at, float f) {
-#pragma unroll
-        for (int half = 0; half < KP / 64; ++half) {
-          tc_load(x, at + 64 * half);
-          tc_loaded(x);
-#pragma unroll
-          for (int nt = 0; nt < 8; ++nt)
-#pragma unroll
-            for (int h = 0; h < 2; ++h) {
-              float(&to)[4] = S[8 * half + nt];
-              set_pair(to, h, fma2(make_float2(f, f), pair_of(x[nt], h), pair_of(to, h)));
-            }
-        }
-      };
-      add(mine + Col::g, inv_g);
+      add(mine + Col::g + key0, inv_g);
       tmem_fence_before_sync();
       signal(&sm.free_g, lane);
       wait(&sm.done_w, use);
       tmem_fence_after_sync();
-      add(mine + Col::x, inv_w);
-      s_max = warp_max(S);
+      add(mine + Col::x + key0, inv_w);
+      s_max = both(warp_max(S), 0);
     }
-    if (a.dS_init && cols > 0) store_state(S, a.dS_init + state_at, cols, K, lane);
+    if (a.dS_init && cols > 0) store_state(S, a.dS_init + state_at, cols, key0, K, lane);
   } else {  // -------------------------------------------------------------- helper
     const size_t first = (((size_t)sq.b * a.s.T + sq.t0) * a.s.Hv + hv) * V + (cols > 0 ? vt * kVt : 0);
     const T* do_at = static_cast<const T*>(a.d_o) + first;
@@ -350,14 +351,14 @@ __global__ void __launch_bounds__(kThreads, 1) bwd_kernel(const Args a) {
       float d[8][4];
       copy_wait<kPlaces - 1>();
       __syncwarp();
-      rows_get(d, sm.d[own][s % kPlaces], lane, do_at);
+      rows_get(d, sm.d[own][s % kPlaces], 0, lane, do_at);
       __syncwarp();
       const float sD = pow2_scale(warp_max(d));
       inv_d = pow2_inverse(sD);
       if (s > 0) wait(&sm.done_g, use ^ 1);
       tmem_fence_after_sync();
       {
-        Operand64<P> f;
+        Operand<P, 4> f;
         f.split(d, sD), f.store(mine + Col::d_in, 32);
         ready(&sm.ready_d);
         f.put(sm.out[own].image, kVt * kC, 0, lane);
@@ -374,7 +375,7 @@ __global__ void __launch_bounds__(kThreads, 1) bwd_kernel(const Args a) {
       }
       signal(&sm.free_k[use], lane);
       const float sE = pow2_scale(warp_max(d));
-      Operand64<2> f;
+      Operand<2, 4> f;
       f.split(d, sE);
       wait(&sm.done_y, use);  // do's place is free
       tmem_fence_after_sync();
@@ -404,7 +405,7 @@ __global__ void __launch_bounds__(kThreads, 1) bwd_kernel(const Args a) {
       signal(&sm.free_l[own], lane);
       const float sL = pow2_scale(warp_max(x));
       {
-        Operand64<2> f;
+        Operand<2, 4> f;
         f.split(x, sL), f.put(sm.out[own].image, kVt * kC, 0, lane);
       }
       __syncwarp();

@@ -89,11 +89,13 @@ __device__ __forceinline__ void rows_in(unsigned char* buf, const T* rows, long 
     copy_async16(dst, there ? rows + row * stride_t + c * kPer : rows, there);
   }
 }
-__device__ __forceinline__ void rows_get(float (&x)[8][4], const unsigned char* buf, int lane, const __nv_bfloat16*) {
+// Tokens 8 n0 .. 8 (n0 + N) - 1 of a warp's rows (n0 even).
+template <int N>
+__device__ __forceinline__ void rows_get(float (&x)[N][4], const unsigned char* buf, int n0, int lane, const __nv_bfloat16*) {
 #pragma unroll
-  for (int q = 0; q < 4; ++q) {
+  for (int q = 0; q < N / 2; ++q) {
     uint32_t r[4];
-    ldsm4t(r, reinterpret_cast<const __half*>(buf) + tri_at(16 * q + (lane & 15), (lane >> 4) * 8));
+    ldsm4t(r, reinterpret_cast<const __half*>(buf) + tri_at(8 * n0 + 16 * q + (lane & 15), (lane >> 4) * 8));
 #pragma unroll
     for (int i = 0; i < 4; ++i) {
       float* y = &x[2 * q + (i & 1)][i & 2];
@@ -101,12 +103,13 @@ __device__ __forceinline__ void rows_get(float (&x)[8][4], const unsigned char* 
     }
   }
 }
-__device__ __forceinline__ void rows_get(float (&x)[8][4], const unsigned char* buf, int lane, const float*) {
+template <int N>
+__device__ __forceinline__ void rows_get(float (&x)[N][4], const unsigned char* buf, int n0, int lane, const float*) {
   const float* s = reinterpret_cast<const float*>(buf);
 #pragma unroll
-  for (int nt = 0; nt < 8; ++nt)
+  for (int nt = 0; nt < N; ++nt)
 #pragma unroll
-    for (int e = 0; e < 4; ++e) x[nt][e] = s[(8 * nt + 2 * (lane & 3) + (e & 1)) * 20 + (lane >> 2) + 8 * (e >> 1)];
+    for (int e = 0; e < 4; ++e) x[nt][e] = s[(8 * (n0 + nt) + 2 * (lane & 3) + (e & 1)) * 20 + (lane >> 2) + 8 * (e >> 1)];
 }
 __device__ __forceinline__ void rows_put(const float (&x)[8][4], unsigned char* buf, int lane, const __nv_bfloat16*) {
 #pragma unroll
@@ -151,26 +154,26 @@ __device__ __forceinline__ void rows_ask(const T* rows, long long stride_t, int 
     if (i * 32 + lane < len) prefetch_l2(rows + (i * 32 + lane) * stride_t);
 }
 
-// The state of a warp: rows row0 + g4 (+ 8), keys 8 nt + 2 t4 (+ 1).
+// The state of a warp: rows g4 (+ 8), keys key0 + 8 nt + 2 t4 (+ 1).
 template <int N>
-__device__ __forceinline__ void load_state(float (&S)[N][4], const float* src, int rows, int K, int lane) {
+__device__ __forceinline__ void load_state(float (&S)[N][4], const float* src, int rows, int key0, int K, int lane) {
 #pragma unroll
   for (int nt = 0; nt < N; ++nt)
 #pragma unroll
     for (int h = 0; h < 2; ++h) {
-      const int row = (lane >> 2) + 8 * h, key = 8 * nt + 2 * (lane & 3);
+      const int row = (lane >> 2) + 8 * h, key = key0 + 8 * nt + 2 * (lane & 3);
       float2 x = make_float2(0.f, 0.f);
       if (src && row < rows && key < K) x = *reinterpret_cast<const float2*>(src + (size_t)row * K + key);
       S[nt][2 * h] = x.x, S[nt][2 * h + 1] = x.y;
     }
 }
 template <int N>
-__device__ __forceinline__ void store_state(const float (&S)[N][4], float* dst, int rows, int K, int lane) {
+__device__ __forceinline__ void store_state(const float (&S)[N][4], float* dst, int rows, int key0, int K, int lane) {
 #pragma unroll
   for (int nt = 0; nt < N; ++nt)
 #pragma unroll
     for (int h = 0; h < 2; ++h) {
-      const int row = (lane >> 2) + 8 * h, key = 8 * nt + 2 * (lane & 3);
+      const int row = (lane >> 2) + 8 * h, key = key0 + 8 * nt + 2 * (lane & 3);
       if (row < rows && key < K) *reinterpret_cast<float2*>(dst + (size_t)row * K + key) = make_float2(S[nt][2 * h], S[nt][2 * h + 1]);
     }
 }

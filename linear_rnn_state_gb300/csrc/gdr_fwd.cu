@@ -51,6 +51,7 @@ struct alignas(1024) FwdSmem {
   __half t[2 * kTriPart], p[P * kTriPart];
   unsigned char v[kWarps][kPlaces][kRowsBytes<T>];
   unsigned char scal[2][kChainScal];
+  float most[3][kWarps][2];  // of the chain warps' S, r and u
   float inv_s[kWarps], inv_r[kWarps];  // inverse scales of the warps' rows
   uint64_t full_k[2], full_q, full_t, full_p, free_k[2], free_q, free_t, free_p;
   uint64_t done_x, done_q, done_u, done_w, done_o, end[2];  // products
@@ -118,7 +119,7 @@ __device__ __forceinline__ void fill(FwdSmem<T, KP, kSave>& m, const Args& a, lo
 template <typename T, int KP, bool kSave>
 __global__ void __launch_bounds__(kThreads, 1) fwd_kernel(const Args a) {
   extern __shared__ __align__(1024) unsigned char raw[];
-  constexpr int P = In<T>::kParts, kNt = KP / 8, kPlaces = FwdSmem<T, KP, kSave>::kPlaces;
+  constexpr int P = In<T>::kParts, kPlaces = FwdSmem<T, KP, kSave>::kPlaces;
   using Col = Columns<KP>;
   using Smem = FwdSmem<T, KP, kSave>;
   Smem& sm = *reinterpret_cast<Smem*>(raw + (-smem_addr(raw) & 1023u));
@@ -130,10 +131,11 @@ __global__ void __launch_bounds__(kThreads, 1) fwd_kernel(const Args a) {
     for (uint64_t* b : {&sm.full_k[0], &sm.full_k[1], &sm.full_q, &sm.full_t, &sm.full_p, &sm.free_q, &sm.free_t, &sm.free_p,
                         &sm.done_x, &sm.done_q, &sm.done_u, &sm.done_w, &sm.done_o, &sm.end[0], &sm.end[1]})
       mbar_init(b, 1);
-    for (uint64_t* b : {&sm.free_k[0], &sm.free_k[1]}) mbar_init(b, 2 * kWarps + 1);
-    for (uint64_t* b : {&sm.free_s, &sm.free_u, &sm.ready_s, &sm.ready_r, &sm.ready_w, &sm.ready_u}) mbar_init(b, kWarps);
+    for (uint64_t* b : {&sm.free_k[0], &sm.free_k[1]}) mbar_init(b, kChains + kWarps + 1);
+    for (uint64_t* b : {&sm.ready_s, &sm.ready_r, &sm.ready_w}) mbar_init(b, kChains);
+    for (uint64_t* b : {&sm.free_s, &sm.free_u, &sm.ready_u}) mbar_init(b, kWarps);
     for (int i = 0; i < kWarps; ++i) {
-      for (uint64_t* b : {&sm.full_s[i], &sm.full_u[i], &sm.free_v[i]}) mbar_init(b, 1);
+      for (uint64_t* b : {&sm.full_s[i], &sm.full_u[i], &sm.free_v[i]}) mbar_init(b, 2);
       mbar_init(&sm.full_v[i][0], 32), mbar_init(&sm.full_v[i][1], 32);
     }
     wkv7::fence_mbar_init();
@@ -209,11 +211,15 @@ __global__ void __launch_bounds__(kThreads, 1) fwd_kernel(const Args a) {
     }
     if (elected()) tc_commit(&sm.end[1]);
     mbar_wait_bounded(a.status, &sm.end[1], 0);
-  } else if (warp < kWarps) {  // ------------------------------------------ chain
+  } else if (warp < kChains) {  // ----------------------------------------- chain
+    constexpr int kS = KP / 16;                // n8 tiles of the warp's half of the keys
+    const int half = warp / kWarps, key0 = half * (KP / 2), token0 = half * (kC / 2);
+    const uint32_t s_in = mine + Col::s_in + half * (KP / 4), r_in = mine + Col::r_in + half * (kC / 4);
     const size_t state_at = (((size_t)seq * a.s.Hv + hv) * V + vt * kVt) * K;
-    float S[kNt][4];
-    load_state(S, a.s_init ? a.s_init + state_at : nullptr, cols, K, lane);
-    float s_max = warp_max(S);
+    auto both = [&](float m, int which) { return both_max(m, sm.most[which][own], half, 1 + own, lane); };
+    float S[kS][4];
+    load_state(S, a.s_init ? a.s_init + state_at : nullptr, cols, key0, K, lane);
+    float s_max = both(warp_max(S), 0);
     Asked has_s(&sm.free_s, 1);
     auto ready = [&](uint64_t* bar) {  // what was stored to tensor memory is there
       tc_stored();
@@ -225,98 +231,90 @@ __global__ void __launch_bounds__(kThreads, 1) fwd_kernel(const Args a) {
       const Scal& sc = sm.sc(use);
       // S0 k^T and S0 q^T
       const float sS = pow2_scale(s_max), inv_s = pow2_inverse(sS);
-      Operand64<2> f[KP / 64];
-#pragma unroll
-      for (int i = 0; i < KP / 64; ++i) f[i].split(S + 8 * i, sS);
+      Operand<2, kS / 2> f;
+      f.split(S, sS);
       if (c > 0) wait(has_s);
-#pragma unroll
-      for (int i = 0; i < KP / 64; ++i) f[i].store(mine + Col::s_in + 32 * i, KP / 2);
+      f.store(s_in, KP / 2);
       ready(&sm.ready_s);
       const Asked has_k(&sm.full_k[use], c >> 1), has_v(&sm.full_v[own][place], kPlaces == 2 ? c >> 1 : c);
-      if (lane == 0) sm.inv_s[own] = inv_s;
+      if (lane == 0 && half == 0) sm.inv_s[own] = inv_s;
       if constexpr (kSave) {
-#pragma unroll
-        for (int i = 0; i < KP / 64; ++i) f[i].put(sm.s[own], kVt * KP, 64 * i, lane);
+        f.put(sm.s[own], kVt * KP, key0, lane);
         wkv7::fence_proxy_async_smem();
       }
       signal(&sm.full_s[own], lane);
 
       // r
-      float x[8][4];
+      float x[4][4];
       {
         wait(has_k);
-        float2 ek[8];
+        float2 ek[4];
 #pragma unroll
-        for (int nt = 0; nt < 8; ++nt)
-          ek[nt] = mul2(*reinterpret_cast<const float2*>(sc.ek + 8 * nt + 2 * t4), make_float2(-inv_s, -inv_s));
+        for (int nt = 0; nt < 4; ++nt)
+          ek[nt] = mul2(*reinterpret_cast<const float2*>(sc.ek + token0 + 8 * nt + 2 * t4), make_float2(-inv_s, -inv_s));
         wait(has_v);
-        float v[8][4];
-        rows_get(v, sm.v[own][place], lane, v_at);
+        float v[4][4];
+        rows_get(v, sm.v[own][place], token0 / 8, lane, v_at);
         if (kPlaces == 1) signal(&sm.free_v[own], lane);
         wait(&sm.done_x, use);
         tmem_fence_after_sync();
-        tc_load(x, mine + Col::x);
+        tc_load(x, mine + Col::x + token0);
         tc_loaded(x);
 #pragma unroll
-        for (int nt = 0; nt < 8; ++nt)
+        for (int nt = 0; nt < 4; ++nt)
 #pragma unroll
           for (int h = 0; h < 2; ++h) set_pair(x[nt], h, fma2(ek[nt], pair_of(x[nt], h), pair_of(v[nt], h)));
       }
-      const float sR = pow2_scale(warp_max(x));
+      const float sR = pow2_scale(both(warp_max(x), 1));
       const float fu = sc.inv_t * pow2_inverse(sR);
       {
-        Operand64<2> fr;
-        fr.split(x, sR), fr.store(mine + Col::r_in, 32);
+        Operand<2, 2> fr;
+        fr.split(x, sR), fr.store(r_in, 32);
       }
       ready(&sm.ready_r);
 
       // u = T r
-      float2 wk[8];
+      float2 wk[4];
 #pragma unroll
-      for (int nt = 0; nt < 8; ++nt)
-        wk[nt] = mul2(*reinterpret_cast<const float2*>(sc.wk + 8 * nt + 2 * t4), make_float2(fu, fu));
+      for (int nt = 0; nt < 4; ++nt)
+        wk[nt] = mul2(*reinterpret_cast<const float2*>(sc.wk + token0 + 8 * nt + 2 * t4), make_float2(fu, fu));
       const float egc = sc.egc;
       wait(&sm.done_u, use);
       tmem_fence_after_sync();
-      if (lane == 0) sm.inv_r[own] = fu;  // the helpers are past the one before
-      tc_load(x, mine + Col::u);
+      if (lane == 0 && half == 0) sm.inv_r[own] = fu;  // the helpers are past the one before
+      tc_load(x, mine + Col::u + token0);
       tc_loaded(x);
 
       // wk u, and the state
 #pragma unroll
-      for (int nt = 0; nt < 8; ++nt)
+      for (int nt = 0; nt < 4; ++nt)
 #pragma unroll
         for (int h = 0; h < 2; ++h) set_pair(x[nt], h, mul2(pair_of(x[nt], h), wk[nt]));
-      const float sW = pow2_scale(warp_max(x)), inv_w = pow2_inverse(sW);
+      const float sW = pow2_scale(both(warp_max(x), 2)), inv_w = pow2_inverse(sW);
       {
-        Operand64<2> fw;
-        fw.split(x, sW), fw.store(mine + Col::r_in, 32);
+        Operand<2, 2> fw;
+        fw.split(x, sW), fw.store(r_in, 32);
       }
       ready(&sm.ready_w);
       signal(&sm.full_u[own], lane);  // only now: the helper beside has its work while this warp waits
       signal(&sm.free_k[use], lane);
       has_s = Asked(&sm.free_s, use);
 #pragma unroll
-      for (int nt = 0; nt < kNt; ++nt)
+      for (int nt = 0; nt < kS; ++nt)
 #pragma unroll
         for (int h = 0; h < 2; ++h) set_pair(S[nt], h, mul2(pair_of(S[nt], h), make_float2(egc, egc)));
       wait(&sm.done_w, use);
       tmem_fence_after_sync();
+      float y[kS][4];
+      tc_load(y, mine + Col::x + key0);
+      tc_loaded(y);
 #pragma unroll
-      for (int half = 0; half < KP / 64; ++half) {
-        tc_load(x, mine + Col::x + 64 * half);
-        tc_loaded(x);
+      for (int nt = 0; nt < kS; ++nt)
 #pragma unroll
-        for (int nt = 0; nt < 8; ++nt)
-#pragma unroll
-          for (int h = 0; h < 2; ++h) {
-            float(&s)[4] = S[8 * half + nt];
-            set_pair(s, h, fma2(make_float2(inv_w, inv_w), pair_of(x[nt], h), pair_of(s, h)));
-          }
-      }
-      s_max = warp_max(S);
+        for (int h = 0; h < 2; ++h) set_pair(S[nt], h, fma2(make_float2(inv_w, inv_w), pair_of(y[nt], h), pair_of(S[nt], h)));
+      s_max = both(warp_max(S), 0);
     }
-    if (a.s_final && cols > 0) store_state(S, a.s_final + state_at, cols, K, lane);
+    if (a.s_final && cols > 0) store_state(S, a.s_final + state_at, cols, key0, K, lane);
   } else {  // -------------------------------------------------------------- helper
     T* o_at = static_cast<T*>(a.o) + (((size_t)sq.b * a.s.T + sq.t0) * a.s.Hv + hv) * V + vt * kVt;
     const long long o_t = (long long)a.s.Hv * V;
@@ -362,7 +360,7 @@ __global__ void __launch_bounds__(kThreads, 1) fwd_kernel(const Args a) {
       tc_loaded(x);
       const float fu = sm.inv_r[own];
       const float sU = pow2_scale(warp_max(x)), inv_u = pow2_inverse(sU) * fu;
-      Operand64<kSave ? 2 : P> f;
+      Operand<kSave ? 2 : P, 4> f;
       f.split(x, sU), f.store(mine + Col::u_in, 32);
       tc_stored();
       tmem_fence_before_sync();

@@ -102,22 +102,22 @@ __device__ __forceinline__ void tc_product_tri_mn(uint32_t d, uint32_t a, uint32
   term(0, 0);
 }
 
-// 64 columns of a warp's 16 rows as accumulator tiles; complete after tc_loaded.
-__device__ __forceinline__ void tc_load(float (*x)[4], uint32_t taddr) {
-  asm volatile(
-      "tcgen05.ld.sync.aligned.16x256b.x8.b32 {%0, %1, %2, %3, %4, %5, %6, %7, %8, %9, %10, %11, %12, %13, %14, "
-      "%15, %16, %17, %18, %19, %20, %21, %22, %23, %24, %25, %26, %27, %28, %29, %30, %31}, [%32];"
-      : "=f"(x[0][0]), "=f"(x[0][1]), "=f"(x[0][2]), "=f"(x[0][3]), "=f"(x[1][0]), "=f"(x[1][1]), "=f"(x[1][2]),
-        "=f"(x[1][3]), "=f"(x[2][0]), "=f"(x[2][1]), "=f"(x[2][2]), "=f"(x[2][3]), "=f"(x[3][0]), "=f"(x[3][1]),
-        "=f"(x[3][2]), "=f"(x[3][3]), "=f"(x[4][0]), "=f"(x[4][1]), "=f"(x[4][2]), "=f"(x[4][3]), "=f"(x[5][0]),
-        "=f"(x[5][1]), "=f"(x[5][2]), "=f"(x[5][3]), "=f"(x[6][0]), "=f"(x[6][1]), "=f"(x[6][2]), "=f"(x[6][3]),
-        "=f"(x[7][0]), "=f"(x[7][1]), "=f"(x[7][2]), "=f"(x[7][3])
-      : "r"(taddr)
-      : "memory");
+// Columns of a warp's 16 rows as accumulator tiles, and the wait for the loads so
+// far (x depends on it, so that no use moves before).
+__device__ __forceinline__ void tc_load(float (&x)[8][4], uint32_t taddr) {
+  asm volatile("tcgen05.ld.sync.aligned.16x256b.x8.b32 {"
+               "%0, %1, %2, %3, %4, %5, %6, %7, %8, %9, %10, %11, %12, %13, %14, %15, %16, %17, %18, %19, %20, "
+               "%21, %22, %23, %24, %25, %26, %27, %28, %29, %30, %31}, [%32];"
+               : "=f"(x[0][0]), "=f"(x[0][1]), "=f"(x[0][2]), "=f"(x[0][3]), "=f"(x[1][0]), "=f"(x[1][1]),
+                 "=f"(x[1][2]), "=f"(x[1][3]), "=f"(x[2][0]), "=f"(x[2][1]), "=f"(x[2][2]), "=f"(x[2][3]),
+                 "=f"(x[3][0]), "=f"(x[3][1]), "=f"(x[3][2]), "=f"(x[3][3]), "=f"(x[4][0]), "=f"(x[4][1]),
+                 "=f"(x[4][2]), "=f"(x[4][3]), "=f"(x[5][0]), "=f"(x[5][1]), "=f"(x[5][2]), "=f"(x[5][3]),
+                 "=f"(x[6][0]), "=f"(x[6][1]), "=f"(x[6][2]), "=f"(x[6][3]), "=f"(x[7][0]), "=f"(x[7][1]),
+                 "=f"(x[7][2]), "=f"(x[7][3])
+               : "r"(taddr)
+               : "memory");
 }
-
-// The loads so far are in their registers; x depends on it, so that no use moves before.
-__device__ __forceinline__ void tc_loaded(float (*x)[4]) {
+__device__ __forceinline__ void tc_loaded(float (&x)[8][4]) {
   asm volatile("tcgen05.wait::ld.sync.aligned;"
                : "+f"(x[0][0]), "+f"(x[0][1]), "+f"(x[0][2]), "+f"(x[0][3]), "+f"(x[1][0]), "+f"(x[1][1]),
                  "+f"(x[1][2]), "+f"(x[1][3]), "+f"(x[2][0]), "+f"(x[2][1]), "+f"(x[2][2]), "+f"(x[2][3]),
@@ -125,6 +125,23 @@ __device__ __forceinline__ void tc_loaded(float (*x)[4]) {
                  "+f"(x[4][2]), "+f"(x[4][3]), "+f"(x[5][0]), "+f"(x[5][1]), "+f"(x[5][2]), "+f"(x[5][3]),
                  "+f"(x[6][0]), "+f"(x[6][1]), "+f"(x[6][2]), "+f"(x[6][3]), "+f"(x[7][0]), "+f"(x[7][1]),
                  "+f"(x[7][2]), "+f"(x[7][3])
+               :
+               : "memory");
+}
+__device__ __forceinline__ void tc_load(float (&x)[4][4], uint32_t taddr) {
+  asm volatile("tcgen05.ld.sync.aligned.16x256b.x4.b32 {"
+               "%0, %1, %2, %3, %4, %5, %6, %7, %8, %9, %10, %11, %12, %13, %14, %15}, [%16];"
+               : "=f"(x[0][0]), "=f"(x[0][1]), "=f"(x[0][2]), "=f"(x[0][3]), "=f"(x[1][0]), "=f"(x[1][1]),
+                 "=f"(x[1][2]), "=f"(x[1][3]), "=f"(x[2][0]), "=f"(x[2][1]), "=f"(x[2][2]), "=f"(x[2][3]),
+                 "=f"(x[3][0]), "=f"(x[3][1]), "=f"(x[3][2]), "=f"(x[3][3])
+               : "r"(taddr)
+               : "memory");
+}
+__device__ __forceinline__ void tc_loaded(float (&x)[4][4]) {
+  asm volatile("tcgen05.wait::ld.sync.aligned;"
+               : "+f"(x[0][0]), "+f"(x[0][1]), "+f"(x[0][2]), "+f"(x[0][3]), "+f"(x[1][0]), "+f"(x[1][1]),
+                 "+f"(x[1][2]), "+f"(x[1][3]), "+f"(x[2][0]), "+f"(x[2][1]), "+f"(x[2][2]), "+f"(x[2][3]),
+                 "+f"(x[3][0]), "+f"(x[3][1]), "+f"(x[3][2]), "+f"(x[3][3])
                :
                : "memory");
 }
@@ -156,23 +173,29 @@ __device__ __forceinline__ float2 fma2(float2 a, float2 b, float2 c) {
 __device__ __forceinline__ float2 pair_of(const float (&x)[4], int h) { return make_float2(x[2 * h], x[2 * h + 1]); }
 __device__ __forceinline__ void set_pair(float (&x)[4], int h, float2 y) { x[2 * h] = y.x, x[2 * h + 1] = y.y; }
 
-// 64 columns of a left operand (one part), as A fragments, into tensor memory;
+// 16-deep blocks of a left operand (one part), as A fragments, into tensor memory;
 // complete after tc_stored.
 __device__ __forceinline__ void tc_store(uint32_t taddr, const uint32_t (&f)[4][4]) {
-  asm volatile(
-      "tcgen05.st.sync.aligned.16x128b.x8.b32 [%0], {%1, %2, %3, %4, %5, %6, %7, %8, %9, %10, %11, %12, %13, %14, %15, %16};" ::"r"(taddr),
-      "r"(f[0][0]), "r"(f[0][1]), "r"(f[0][2]), "r"(f[0][3]), "r"(f[1][0]), "r"(f[1][1]), "r"(f[1][2]), "r"(f[1][3]),
-      "r"(f[2][0]), "r"(f[2][1]), "r"(f[2][2]), "r"(f[2][3]), "r"(f[3][0]), "r"(f[3][1]), "r"(f[3][2]), "r"(f[3][3])
-      : "memory");
+  asm volatile("tcgen05.st.sync.aligned.16x128b.x8.b32 [%0], {%1, %2, %3, %4, %5, %6, %7, %8, %9, %10, %11, %12, %13, %14, %15, %16};" ::"r"(taddr),
+               "r"(f[0][0]), "r"(f[0][1]), "r"(f[0][2]), "r"(f[0][3]), "r"(f[1][0]), "r"(f[1][1]), "r"(f[1][2]),
+               "r"(f[1][3]), "r"(f[2][0]), "r"(f[2][1]), "r"(f[2][2]), "r"(f[2][3]), "r"(f[3][0]), "r"(f[3][1]),
+               "r"(f[3][2]), "r"(f[3][3])
+               : "memory");
+}
+__device__ __forceinline__ void tc_store(uint32_t taddr, const uint32_t (&f)[2][4]) {
+  asm volatile("tcgen05.st.sync.aligned.16x128b.x4.b32 [%0], {%1, %2, %3, %4, %5, %6, %7, %8};" ::"r"(taddr),
+               "r"(f[0][0]), "r"(f[0][1]), "r"(f[0][2]), "r"(f[0][3]), "r"(f[1][0]), "r"(f[1][1]), "r"(f[1][2]),
+               "r"(f[1][3])
+               : "memory");
 }
 __device__ __forceinline__ void tc_stored() { asm volatile("tcgen05.wait::st.sync.aligned;" ::: "memory"); }
-// x times s as 64 columns of a left operand, hi and lo `part` columns behind.
-template <int kP>
-struct Operand64 {
-  uint32_t h[4][4], l[kP == 2 ? 4 : 1][4];
-  __device__ __forceinline__ void split(const float (*x)[4], float s) {
+// Accumulator tiles times s as N such blocks, hi and lo `part` columns behind.
+template <int kP, int N>
+struct Operand {
+  uint32_t h[N][4], l[kP == 2 ? N : 1][4];
+  __device__ __forceinline__ void split(const float (&x)[2 * N][4], float s) {
 #pragma unroll
-    for (int j = 0; j < 4; ++j)
+    for (int j = 0; j < N; ++j)
 #pragma unroll
       for (int e = 0; e < 4; ++e) {
         const float2 y = mul2(pair_of(x[2 * j + (e >> 1)], e & 1), make_float2(s, s));
@@ -190,7 +213,7 @@ struct Operand64 {
   // rows of 16 of an image, from column k0 on
   __device__ __forceinline__ void put(__half* image, int part, int k0, int lane) const {
 #pragma unroll
-    for (int j = 0; j < 4; ++j) {
+    for (int j = 0; j < N; ++j) {
       __half* p = image + img(16, lane & 15, k0 + 16 * j + (lane >> 4) * 8);
       stsm4(p, h[j]);
       if constexpr (kP == 2) stsm4(p + part, l[j]);
@@ -198,8 +221,16 @@ struct Operand64 {
   }
 };
 
-constexpr int kWarps = 4;  // of 16 rows each: a block's chain warps, and as many helpers
-constexpr int kFiller = 2 * kWarps, kIssuer = kFiller + 1, kHelpersIssuer = kIssuer + 1, kThreads = (kHelpersIssuer + 1) * 32;
+constexpr int kWarps = 4;  // times 16 rows a block: two chain warps each, and a helper
+constexpr int kChains = 2 * kWarps, kFiller = kChains + kWarps, kIssuer = kFiller + 1, kHelpersIssuer = kIssuer + 1, kThreads = (kHelpersIssuer + 1) * 32;
+
+// The larger of two warps' values: of the two chain warps of 16 rows, each with
+// half of the columns, which meet at barrier `id`.
+__device__ __forceinline__ float both_max(float m, float* slot, int half, int id, int lane) {
+  if (lane == 0) slot[half] = m;
+  asm volatile("bar.sync %0, 64;" ::"r"(id) : "memory");
+  return fmaxf(m, slot[half ^ 1]);
+}
 
 // A wait that a warp gives up on once: from then on it goes through its steps
 // without waiting (all accesses are in bounds whatever the data), so that the
