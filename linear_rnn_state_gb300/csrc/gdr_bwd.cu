@@ -155,7 +155,6 @@ __global__ void __launch_bounds__(kThreads, 1) bwd_kernel(const Args a) {
   const int cols = V - vt * kVt, tokens = sq.t1 - sq.t0;  // cols <= 0: this warp's rows are zeros
   const uint32_t tmem = sm.tmem, mine = tmem + ((uint32_t)own << 21);  // this warp's lanes
   Patience wait{a.status};
-  constexpr int kPartK = kC * KP;  // halves from an image's hi part to its lo part
   auto ready = [&](uint64_t* bar) {  // what was stored to tensor memory is there
     tc_stored();
     tmem_fence_before_sync();
@@ -168,28 +167,25 @@ __global__ void __launch_bounds__(kThreads, 1) bwd_kernel(const Args a) {
   } else if (warp == kIssuer) {
     for (int s = 0; s < n; ++s) {
       const int use = s & 1;
-      const uint32_t k_at = smem_addr(sm.k[use]);
       wait(&sm.full_k[use], s >> 1);
       wait(&sm.ready_s, use);
       tmem_fence_after_sync();
       if (elected()) {
-        tc_product<2, P>(tmem + Col::x, product_of(64, false), KP / 16, tmem + Col::s_in,
-                         [&](int part, int ks) { return desc_k(k_at + part * kPartK * 2, ks); });
+        tc_rows<2, P, KP>(tmem + Col::x, tmem + Col::s_in, sm.k[use]);
         tc_commit(&sm.done_x);
       }
       wait(&sm.full_t, use);
       wait(&sm.ready_y, use);
       tmem_fence_after_sync();
       if (elected()) {
-        tc_product_tri_mn<2, 2>(tmem + Col::l, tmem + Col::s_in, smem_addr(sm.t));
+        tc_tri_columns<2, 2>(tmem + Col::l, tmem + Col::s_in, sm.t);
         tc_commit(&sm.done_l);
         tc_commit(&sm.free_t);
       }
       wait(&sm.ready_w, use);
       tmem_fence_after_sync();
       if (elected()) {
-        tc_product<2, P>(tmem + Col::x, product_of(KP, true), 4, tmem + Col::s_in,
-                         [&](int part, int ks) { return desc_mn(k_at + part * kPartK * 2, ks); });
+        tc_columns<2, P, KP>(tmem + Col::x, tmem + Col::s_in, sm.k[use]);
         tc_commit(&sm.done_w);
         tc_commit(&sm.free_k[use]);
       }
@@ -197,7 +193,6 @@ __global__ void __launch_bounds__(kThreads, 1) bwd_kernel(const Args a) {
     if (elected()) tc_commit(&sm.end[0]);
     mbar_wait_bounded(a.status, &sm.end[0], 0);
   } else if (warp == kHelpersIssuer) {
-    const uint32_t q_at = smem_addr(sm.q);
     for (int s = 0; s < n; ++s) {
       const int use = s & 1;
       wait(&sm.full_p, use);
@@ -205,7 +200,7 @@ __global__ void __launch_bounds__(kThreads, 1) bwd_kernel(const Args a) {
       wait(&sm.ready_d, use);
       tmem_fence_after_sync();
       if (elected()) {
-        tc_product_tri_mn<P, 2>(tmem + Col::y, tmem + Col::d_in, smem_addr(sm.p));
+        tc_tri_columns<P, 2>(tmem + Col::y, tmem + Col::d_in, sm.p);
         tc_commit(&sm.done_y);
         tc_commit(&sm.free_p);
       }
@@ -214,8 +209,7 @@ __global__ void __launch_bounds__(kThreads, 1) bwd_kernel(const Args a) {
       wait(&sm.ready_e, use);
       tmem_fence_after_sync();
       if (elected()) {
-        tc_product<2, P>(tmem + Col::g, product_of(KP, true), 4, tmem + Col::d_in,
-                         [&](int part, int ks) { return desc_mn(q_at + part * kPartK * 2, ks); });
+        tc_columns<2, P, KP>(tmem + Col::g, tmem + Col::d_in, sm.q);
         tc_commit(&sm.done_g);
         tc_commit(&sm.free_q);
       }

@@ -154,26 +154,22 @@ __global__ void __launch_bounds__(kThreads, 1) fwd_kernel(const Args a) {
   const uint32_t tmem = sm.tmem, mine = tmem + ((uint32_t)own << 21);  // this warp's lanes
   const T* v_at = static_cast<const T*>(a.v) + sq.b * a.s.v_b + sq.t0 * a.s.v_t + (size_t)hv * V + (cols > 0 ? vt * kVt : 0);
   Patience wait{a.status};
-  constexpr int kPartK = kC * KP;  // halves from an image's hi part to its lo part
 
   if (warp == kFiller) {
     if (lane == 0 && n > 0) fill(sm, a, sq.slot, n, hk, hv);
   } else if (warp == kIssuer) {
     for (int c = 0; c < n; ++c) {
       const int use = c & 1;
-      const uint32_t k_at = smem_addr(sm.k[use]), q_at = smem_addr(sm.q);
       wait(&sm.full_k[use], c >> 1);
       wait(&sm.ready_s, use);
       tmem_fence_after_sync();
       if (elected()) {
-        tc_product<2, P>(tmem + Col::x, product_of(64, false), KP / 16, tmem + Col::s_in,
-                         [&](int part, int ks) { return desc_k(k_at + part * kPartK * 2, ks); });
+        tc_rows<2, P, KP>(tmem + Col::x, tmem + Col::s_in, sm.k[use]);
         tc_commit(&sm.done_x);
       }
       wait(&sm.full_q, use);
       if (elected()) {
-        tc_product<P, P>(tmem + Col::q, product_of(64, false), KP / 16, tmem + Col::s_in,
-                         [&](int part, int ks) { return desc_k(q_at + part * kPartK * 2, ks); });
+        tc_rows<P, P, KP>(tmem + Col::q, tmem + Col::s_in, sm.q);
         tc_commit(&sm.done_q);
         tc_commit(&sm.free_q);
       }
@@ -182,15 +178,14 @@ __global__ void __launch_bounds__(kThreads, 1) fwd_kernel(const Args a) {
       wait(&sm.ready_r, use);
       tmem_fence_after_sync();
       if (elected()) {
-        tc_product_tri<2, 2>(tmem + Col::u, tmem + Col::r_in, smem_addr(sm.t));
+        tc_tri_rows<2, 2>(tmem + Col::u, tmem + Col::r_in, sm.t);
         tc_commit(&sm.done_u);
         tc_commit(&sm.free_t);
       }
       wait(&sm.ready_w, use);
       tmem_fence_after_sync();
       if (elected()) {
-        tc_product<2, P>(tmem + Col::x, product_of(KP, true), 4, tmem + Col::r_in,
-                         [&](int part, int ks) { return desc_mn(k_at + part * kPartK * 2, ks); });
+        tc_columns<2, P, KP>(tmem + Col::x, tmem + Col::r_in, sm.k[use]);
         tc_commit(&sm.done_w);
         tc_commit(&sm.free_k[use]);
       }
@@ -204,7 +199,7 @@ __global__ void __launch_bounds__(kThreads, 1) fwd_kernel(const Args a) {
       wait(&sm.ready_u, use);
       tmem_fence_after_sync();
       if (elected()) {
-        tc_product_tri<P, P>(tmem + Col::o, tmem + Col::u_in, smem_addr(sm.p));
+        tc_tri_rows<P, P>(tmem + Col::o, tmem + Col::u_in, sm.p);
         tc_commit(&sm.done_o);
         tc_commit(&sm.free_p);
       }

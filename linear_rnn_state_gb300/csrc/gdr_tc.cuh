@@ -5,8 +5,8 @@
 // which 4 KB come out of it, and everybody else's accesses waited.)
 //
 // An image (gdr_common.cuh) is an operand as it lies: its rows of 128 bytes with
-// permuted pieces are the 128-byte swizzle, read along the row (K-major: desc_k)
-// or across it (MN-major: desc_mn); the 32-byte rows of the triangular images'
+// permuted pieces are the 128-byte swizzle, read along the row (K-major: tc_rows)
+// or across it (MN-major: tc_columns); the 32-byte rows of the triangular images'
 // blocks are the 32-byte swizzle.
 //
 // With 64 rows an accumulator's row i lies in lane 32 (i / 16) + i % 16: warp w
@@ -22,25 +22,23 @@ namespace gdr {
 using wkv7::tmem_fence_after_sync;
 using wkv7::tmem_fence_before_sync;
 
-// Descriptor of an operand: start, leading and stride byte offsets, version 1,
-// layout (2: 128-byte swizzle, 6: 32-byte).
-__device__ __forceinline__ uint64_t operand(uint32_t addr, uint32_t lbo, uint32_t sbo, uint32_t layout) {
-  return (uint64_t)((addr >> 4) & 0x3FFFu) | ((uint64_t)((lbo >> 4) & 0x3FFFu) << 16) |
-         ((uint64_t)((sbo >> 4) & 0x3FFFu) << 32) | ((uint64_t)1 << 46) | ((uint64_t)layout << 61);
-}
-constexpr uint32_t kPanel = kC * 128;  // bytes of a panel: 64 rows
-// Rows of an image as the operand's rows, its columns 16 ks .. as k.
-__device__ __forceinline__ uint64_t desc_k(uint32_t image, int ks) {
-  return operand(image + (ks >> 2) * kPanel + 32 * (ks & 3), 16, 1024, 2);
-}
-// Columns as the operand's rows (panels of 64 follow one another), rows 16 ks .. as k.
-__device__ __forceinline__ uint64_t desc_mn(uint32_t image, int ks) { return operand(image + 2048 * ks, kPanel, 1024, 2); }
+// Descriptor of a right operand: start, leading and stride byte offsets, version 1,
+// layout (2: 128-byte swizzle, 6: 32-byte). Made once a product; the parts and
+// steps in it lie at offsets that are constants (addresses stay below 2^18, so
+// adding to the low word is enough).
+struct Right {
+  uint32_t lo, hi;
+  __device__ __forceinline__ Right(const void* image, uint32_t lbo, uint32_t sbo, uint32_t layout)
+      : lo((smem_addr(image) >> 4) | (lbo >> 4) << 16), hi((sbo >> 4) | 1u << 14 | layout << 29) {}
+  __device__ __forceinline__ uint64_t at(int bytes) const {
+    uint64_t d;
+    asm("mov.b64 %0, {%1, %2};" : "=l"(d) : "r"(lo + (bytes >> 4)), "r"(hi));
+    return d;
+  }
+};
+constexpr int kPanel = kC * 128;  // bytes of a panel: 64 rows
 // A triangular image spread out to whole columns: its block (i, j) is block 4 j + i.
 constexpr int kSpreadPart = 16 * 256;
-// Its blocks (i, 0 ..): columns as the operand's rows, rows as k.
-__device__ __forceinline__ uint64_t desc_tri_mn(uint32_t image, int i) { return operand(image + 512 * i, 2048, 256, 6); }
-// The blocks (j .., j) of a triangular image: rows as the operand's rows, columns as k.
-__device__ __forceinline__ uint64_t desc_tri_k(uint32_t image, int j) { return operand(image + 2 * tri_block(j, j), 16, 256, 6); }
 
 // fp16 operands, fp32 accumulator, 64 x n.
 __host__ __device__ constexpr uint32_t product_of(int n, bool b_mn) {
@@ -58,48 +56,54 @@ __device__ __forceinline__ void tc_commit(uint64_t* bar) {
   asm volatile("tcgen05.commit.cta_group::1.mbarrier::arrive::one.shared::cluster.b64 [%0];" ::"r"(smem_addr(bar)) : "memory");
 }
 
-// d = a b over `steps` 16-deep steps, a and b in parts: the small terms first, lo
-// lo left out. a's lo part lies behind its hi part; b_of(part, step) gives b's descriptors.
-template <int kA, int kB, typename FB>
-__device__ __forceinline__ void tc_product(uint32_t d, uint32_t what, int steps, uint32_t a, FB b_of) {
-  bool add = false;
-  auto term = [&](int pa, int pb) {
+// The terms of a product in parts: the small ones first, lo lo left out.
+template <int kA, int kB, typename F>
+__device__ __forceinline__ void tc_terms(F term) {
+  if constexpr (kA == 2) term(1, 0, true);
+  if constexpr (kB == 2) term(0, 1, kA != 2);
+  term(0, 0, kA != 2 && kB != 2);
+}
+// d = a b^T: b's rows (64) are the columns of d, its KP columns the sum's.
+template <int kA, int kB, int KP>
+__device__ __forceinline__ void tc_rows(uint32_t d, uint32_t a, const __half* b) {
+  const Right r(b, 16, 1024, 2);
+  tc_terms<kA, kB>([&](int pa, int pb, bool first) {
 #pragma unroll
-    for (int ks = 0; ks < steps; ++ks) tc_mma(d, a + 8 * (pa * steps + ks), b_of(pb, ks), what, add || ks > 0);
-    add = true;
-  };
-  if constexpr (kA == 2) term(1, 0);
-  if constexpr (kB == 2) term(0, 1);
-  term(0, 0);
+    for (int ks = 0; ks < KP / 16; ++ks)
+      tc_mma(d, a + 8 * (pa * (KP / 16) + ks), r.at(pb * kC * KP * 2 + (ks >> 2) * kPanel + 32 * (ks & 3)), product_of(64, false),
+             !first || ks > 0);
+  });
+}
+// d = a b: b's KP columns are those of d, its rows (64) the sum's.
+template <int kA, int kB, int KP>
+__device__ __forceinline__ void tc_columns(uint32_t d, uint32_t a, const __half* b) {
+  const Right r(b, kPanel, 1024, 2);
+  tc_terms<kA, kB>([&](int pa, int pb, bool first) {
+#pragma unroll
+    for (int ks = 0; ks < 4; ++ks)
+      tc_mma(d, a + 8 * (4 * pa + ks), r.at(pb * kC * KP * 2 + 2048 * ks), product_of(KP, true), !first || ks > 0);
+  });
 }
 // d = a X^T with X a triangular image: columns of X 16 j .. meet the rows from 16 j on.
 template <int kA, int kB>
-__device__ __forceinline__ void tc_product_tri(uint32_t d, uint32_t a, uint32_t tri) {
-  bool add = false;
-  auto term = [&](int pa, int pb) {
+__device__ __forceinline__ void tc_tri_rows(uint32_t d, uint32_t a, const __half* tri) {
+  const Right r(tri, 16, 256, 6);
+  tc_terms<kA, kB>([&](int pa, int pb, bool first) {
 #pragma unroll
     for (int j = 0; j < 4; ++j)
-      tc_mma(d + 16 * j, a + 8 * (4 * pa + j), desc_tri_k(tri + pb * kTriPart * 2, j), product_of(64 - 16 * j, false), add || j > 0);
-    add = true;
-  };
-  if constexpr (kA == 2) term(1, 0);
-  if constexpr (kB == 2) term(0, 1);
-  term(0, 0);
+      tc_mma(d + 16 * j, a + 8 * (4 * pa + j), r.at(2 * (pb * kTriPart + tri_block(j, j))), product_of(64 - 16 * j, false),
+             !first || j > 0);
+  });
 }
-
 // d = a X with X spread out: rows of X 16 i .. meet the columns up to them.
 template <int kA, int kB>
-__device__ __forceinline__ void tc_product_tri_mn(uint32_t d, uint32_t a, uint32_t tri) {
-  bool add = false;
-  auto term = [&](int pa, int pb) {
+__device__ __forceinline__ void tc_tri_columns(uint32_t d, uint32_t a, const __half* tri) {
+  const Right r(tri, 2048, 256, 6);
+  tc_terms<kA, kB>([&](int pa, int pb, bool first) {
 #pragma unroll
     for (int i = 3; i >= 0; --i)
-      tc_mma(d, a + 8 * (4 * pa + i), desc_tri_mn(tri + pb * kSpreadPart * 2, i), product_of(16 * i + 16, true), add || i < 3);
-    add = true;
-  };
-  if constexpr (kA == 2) term(1, 0);
-  if constexpr (kB == 2) term(0, 1);
-  term(0, 0);
+      tc_mma(d, a + 8 * (4 * pa + i), r.at(2 * pb * kSpreadPart + 512 * i), product_of(16 * i + 16, true), !first || i < 3);
+  });
 }
 
 // Columns of a warp's 16 rows as accumulator tiles, and the wait for the loads so
