@@ -25,6 +25,13 @@
 namespace gdr {
 namespace {
 
+// Warps: the chain's eight, eight helpers, and those without rows and one more to
+// make them four. Registers of a thread of each, and what it is launched with.
+constexpr int kHelpers = 2 * kWarps, kFiller = kChains + kHelpers, kThreads = (kFiller + 4) * 32;
+enum { kIssuer = kFiller + 1, kHelpersIssuer };
+constexpr int kRegChain = 120, kRegHelper = 96, kRegRest = 48, kRegLaunch = 96;
+static_assert(2 * kRegChain + 2 * kRegHelper + kRegRest <= 5 * kRegLaunch, "a request for more would wait forever");
+
 template <typename T, int KP>
 struct alignas(1024) BwdSmem {
   static constexpr int P = In<T>::kParts, kPlaces = P * KP >= 256 ? 1 : 2;  // of do: what fits
@@ -38,7 +45,7 @@ struct alignas(1024) BwdSmem {
   } out[kWarps];
   unsigned char d[kWarps][kPlaces][kRowsBytes<T>];
   unsigned char scal[2][kChainScal];
-  float most[3][kWarps][2];  // of the chain warps' dS, y and e^G lam
+  float most[6][kWarps][2];  // of the chain warps' dS, y and e^G lam, of the helpers' do, scale e^G do and lam
   float inv_s[kWarps], inv_d[2][kWarps], inv_g[2][kWarps];  // inverse scales of the warps' rows
   uint64_t full_k[2], full_q, full_t, full_p, free_k[2], free_q, free_t, free_p;
   uint64_t done_x, done_y, done_l, done_w, done_g, end[2];    // products
@@ -111,13 +118,26 @@ __device__ __forceinline__ void fill(BwdSmem<T, KP>& m, const Args& a, long long
     for (uint64_t* b : {&m.full_k[0], &m.full_k[1], &m.full_q, &m.full_t, &m.full_p}) drain(b);
 }
 
-// A warp's image to memory, `kHalves` of it. (By loads and stores: the proxy fence
-// that a bulk copy wants before it took 400 to 1400 cycles beside running products.)
+// An image to memory, half of it by each of two warps. (By loads and stores: the
+// proxy fence that a bulk copy wants before it took 400 to 1400 cycles beside
+// running products.)
 template <int kHalves>
-__device__ __forceinline__ void image_out(char* to, const __half* image, int lane) {
+__device__ __forceinline__ void image_out(char* to, const __half* image, int half, int lane) {
+  constexpr int kEach = kHalves / 512;
 #pragma unroll
-  for (int i = 0; i < kHalves / 256; ++i)
-    reinterpret_cast<uint4*>(to)[i * 32 + lane] = reinterpret_cast<const uint4*>(image)[i * 32 + lane];
+  for (int i = 0; i < kEach; ++i) {
+    const int at = (half * kEach + i) * 32 + lane;
+    reinterpret_cast<uint4*>(to)[at] = reinterpret_cast<const uint4*>(image)[at];
+  }
+}
+// The columns 32 half .. of an image of 16 rows of 64, which the warp itself wrote.
+template <int kParts>
+__device__ __forceinline__ void columns_out(char* to, const __half* image, int half, int lane) {
+#pragma unroll
+  for (int i = 0; i < 2 * kParts; ++i) {
+    const int row = (i & 1) * 8 + (lane >> 2), at = (i >> 1) * kVt * kC + img(16, row, 32 * half + 8 * (lane & 3));
+    *reinterpret_cast<uint4*>(to + 2 * at) = *reinterpret_cast<const uint4*>(image + at);
+  }
 }
 
 template <typename T, int KP>
@@ -135,13 +155,11 @@ __global__ void __launch_bounds__(kThreads, 1) bwd_kernel(const Args a) {
     for (uint64_t* b : {&sm.full_k[0], &sm.full_k[1], &sm.full_q, &sm.full_t, &sm.full_p, &sm.free_q, &sm.free_t, &sm.free_p,
                         &sm.done_x, &sm.done_y, &sm.done_l, &sm.done_w, &sm.done_g, &sm.end[0], &sm.end[1]})
       mbar_init(b, 1);
-    for (uint64_t* b : {&sm.free_k[0], &sm.free_k[1]}) mbar_init(b, kChains + kWarps + 1);
+    for (uint64_t* b : {&sm.free_k[0], &sm.free_k[1]}) mbar_init(b, kChains + kHelpers + 1);
     for (uint64_t* b : {&sm.free_y, &sm.free_g, &sm.ready_s, &sm.ready_y, &sm.ready_w}) mbar_init(b, kChains);
-    for (uint64_t* b : {&sm.ready_d, &sm.ready_e}) mbar_init(b, kWarps);
-    for (int i = 0; i < kWarps; ++i) {
-      for (uint64_t* b : {&sm.full_s[i], &sm.full_l[i]}) mbar_init(b, 2);
-      for (uint64_t* b : {&sm.free_s[i], &sm.free_l[i], &sm.full_d[i]}) mbar_init(b, 1);
-    }
+    for (uint64_t* b : {&sm.ready_d, &sm.ready_e}) mbar_init(b, kHelpers);
+    for (int i = 0; i < kWarps; ++i)
+      for (uint64_t* b : {&sm.full_s[i], &sm.full_l[i], &sm.free_s[i], &sm.free_l[i], &sm.full_d[i]}) mbar_init(b, 2);
     wkv7::fence_mbar_init();
   }
   if (warp == kFiller) wkv7::tmem_alloc(&sm.tmem, Col::all);
@@ -154,6 +172,7 @@ __global__ void __launch_bounds__(kThreads, 1) bwd_kernel(const Args a) {
   const int K = a.s.K, V = a.s.V, vt = set * kWarps + own;
   const int cols = V - vt * kVt, tokens = sq.t1 - sq.t0;  // cols <= 0: this warp's rows are zeros
   const uint32_t tmem = sm.tmem, mine = tmem + ((uint32_t)own << 21);  // this warp's lanes
+  const int half = warp / kWarps & 1, token0 = half * (kC / 2);  // of the two warps of the same rows
   Patience wait{a.status};
   auto ready = [&](uint64_t* bar) {  // what was stored to tensor memory is there
     tc_stored();
@@ -162,63 +181,67 @@ __global__ void __launch_bounds__(kThreads, 1) bwd_kernel(const Args a) {
   };
 
   // step s works on chunk n - 1 - s
-  if (warp == kFiller) {
-    if (lane == 0 && n > 0) fill(sm, a, sq.slot + n - 1, n, hk, hv);
-  } else if (warp == kIssuer) {
-    for (int s = 0; s < n; ++s) {
-      const int use = s & 1;
-      wait(&sm.full_k[use], s >> 1);
-      wait(&sm.ready_s, use);
-      tmem_fence_after_sync();
-      if (elected()) {
-        tc_rows<2, P, KP>(tmem + Col::x, tmem + Col::s_in, sm.k[use]);
-        tc_commit(&sm.done_x);
+  if (warp >= kFiller) {
+    fewer_registers<kRegRest>();
+    if (warp == kFiller) {
+      if (lane == 0 && n > 0) fill(sm, a, sq.slot + n - 1, n, hk, hv);
+    } else if (warp == kIssuer) {
+      for (int s = 0; s < n; ++s) {
+        const int use = s & 1;
+        wait(&sm.full_k[use], s >> 1);
+        wait(&sm.ready_s, use);
+        tmem_fence_after_sync();
+        if (elected()) {
+          tc_rows<2, P, KP>(tmem + Col::x, tmem + Col::s_in, sm.k[use]);
+          tc_commit(&sm.done_x);
+        }
+        wait(&sm.full_t, use);
+        wait(&sm.ready_y, use);
+        tmem_fence_after_sync();
+        if (elected()) {
+          tc_tri_columns<2, 2>(tmem + Col::l, tmem + Col::s_in, sm.t);
+          tc_commit(&sm.done_l);
+          tc_commit(&sm.free_t);
+        }
+        wait(&sm.ready_w, use);
+        tmem_fence_after_sync();
+        if (elected()) {
+          tc_columns<2, P, KP>(tmem + Col::x, tmem + Col::s_in, sm.k[use]);
+          tc_commit(&sm.done_w);
+          tc_commit(&sm.free_k[use]);
+        }
       }
-      wait(&sm.full_t, use);
-      wait(&sm.ready_y, use);
-      tmem_fence_after_sync();
-      if (elected()) {
-        tc_tri_columns<2, 2>(tmem + Col::l, tmem + Col::s_in, sm.t);
-        tc_commit(&sm.done_l);
-        tc_commit(&sm.free_t);
+      if (elected()) tc_commit(&sm.end[0]);
+      mbar_wait_bounded(a.status, &sm.end[0], 0);
+    } else if (warp == kHelpersIssuer) {
+      for (int s = 0; s < n; ++s) {
+        const int use = s & 1;
+        wait(&sm.full_p, use);
+        if (s > 0) wait(&sm.free_y, use ^ 1);
+        wait(&sm.ready_d, use);
+        tmem_fence_after_sync();
+        if (elected()) {
+          tc_tri_columns<P, 2>(tmem + Col::y, tmem + Col::d_in, sm.p);
+          tc_commit(&sm.done_y);
+          tc_commit(&sm.free_p);
+        }
+        wait(&sm.full_q, use);
+        if (s > 0) wait(&sm.free_g, use ^ 1);
+        wait(&sm.ready_e, use);
+        tmem_fence_after_sync();
+        if (elected()) {
+          tc_columns<2, P, KP>(tmem + Col::g, tmem + Col::d_in, sm.q);
+          tc_commit(&sm.done_g);
+          tc_commit(&sm.free_q);
+        }
       }
-      wait(&sm.ready_w, use);
-      tmem_fence_after_sync();
-      if (elected()) {
-        tc_columns<2, P, KP>(tmem + Col::x, tmem + Col::s_in, sm.k[use]);
-        tc_commit(&sm.done_w);
-        tc_commit(&sm.free_k[use]);
-      }
+      if (elected()) tc_commit(&sm.end[1]);
+      mbar_wait_bounded(a.status, &sm.end[1], 0);
     }
-    if (elected()) tc_commit(&sm.end[0]);
-    mbar_wait_bounded(a.status, &sm.end[0], 0);
-  } else if (warp == kHelpersIssuer) {
-    for (int s = 0; s < n; ++s) {
-      const int use = s & 1;
-      wait(&sm.full_p, use);
-      if (s > 0) wait(&sm.free_y, use ^ 1);
-      wait(&sm.ready_d, use);
-      tmem_fence_after_sync();
-      if (elected()) {
-        tc_tri_columns<P, 2>(tmem + Col::y, tmem + Col::d_in, sm.p);
-        tc_commit(&sm.done_y);
-        tc_commit(&sm.free_p);
-      }
-      wait(&sm.full_q, use);
-      if (s > 0) wait(&sm.free_g, use ^ 1);
-      wait(&sm.ready_e, use);
-      tmem_fence_after_sync();
-      if (elected()) {
-        tc_columns<2, P, KP>(tmem + Col::g, tmem + Col::d_in, sm.q);
-        tc_commit(&sm.done_g);
-        tc_commit(&sm.free_q);
-      }
-    }
-    if (elected()) tc_commit(&sm.end[1]);
-    mbar_wait_bounded(a.status, &sm.end[1], 0);
   } else if (warp < kChains) {  // ----------------------------------------- chain
+    more_registers<kRegChain>();
     constexpr int kS = KP / 16;                // n8 tiles of the warp's half of the keys
-    const int half = warp / kWarps, key0 = half * (KP / 2), token0 = half * (kC / 2);
+    const int key0 = half * (KP / 2);
     const uint32_t s_in = mine + Col::s_in + half * (KP / 4), y_in = mine + Col::s_in + half * (kC / 4);
     const size_t state_at = (((size_t)seq * a.s.Hv + hv) * V + vt * kVt) * K;
     auto both = [&](float m, int which) { return both_max(m, sm.most[which][own], half, 1 + own, lane); };
@@ -329,11 +352,15 @@ __global__ void __launch_bounds__(kThreads, 1) bwd_kernel(const Args a) {
     const T* do_at = static_cast<const T*>(a.d_o) + first;
     T* dv_at = static_cast<T*>(a.dv) + first;
     const long long row_t = (long long)a.s.Hv * V;
+    const uint32_t d_in = mine + Col::d_in + half * (kC / 4);
+    const int meet = 1 + kWarps + own;
+    auto both = [&](float m, int which) { return both_max(m, sm.most[which][own], half, meet, lane); };
     auto fetch = [&](int s) {  // do of step s, and a request for a later one
       const int c = n - 1 - s;
-      if (c >= 0) rows_in(sm.d[own][s % kPlaces], do_at + c * kC * row_t, row_t, cols > 0 ? tokens - c * kC : 0, cols, lane);
+      if (c >= 0)
+        rows_in<4>(sm.d[own][s % kPlaces], do_at + c * kC * row_t, row_t, cols > 0 ? tokens - c * kC : 0, cols, token0 / 8, lane);
       copy_commit();
-      if (c >= 2 && cols > 0) rows_ask(do_at + (c - 2) * kC * row_t, row_t, kC, lane);
+      if (c >= 2 && cols > 0) rows_ask<4>(do_at + (c - 2) * kC * row_t, row_t, kC, token0 / 8, lane);
     };
     constexpr Record rec = b_record(KP, P);
     auto record_of = [&](int s) { return a.b.b_rec + (((sq.slot + n - 1 - s) * a.s.Hv + hv) * vts + vt) * rec.size; };
@@ -342,41 +369,41 @@ __global__ void __launch_bounds__(kThreads, 1) bwd_kernel(const Args a) {
     auto ahead = [&](int s) {
       const int use = s & 1;
       const Scal& sc = sm.sc(use);
-      float d[8][4];
+      float d[4][4];
       copy_wait<kPlaces - 1>();
       __syncwarp();
-      rows_get(d, sm.d[own][s % kPlaces], 0, lane, do_at);
+      rows_get(d, sm.d[own][s % kPlaces], token0 / 8, lane, do_at);
       __syncwarp();
-      const float sD = pow2_scale(warp_max(d));
+      const float sD = pow2_scale(both(warp_max(d), 3));
       inv_d = pow2_inverse(sD);
       if (s > 0) wait(&sm.done_g, use ^ 1);
       tmem_fence_after_sync();
       {
-        Operand<P, 4> f;
-        f.split(d, sD), f.store(mine + Col::d_in, 32);
+        Operand<P, 2> f;
+        f.split(d, sD), f.store(d_in, 32);
         ready(&sm.ready_d);
-        f.put(sm.out[own].image, kVt * kC, 0, lane);
+        f.put(sm.out[own].image, kVt * kC, token0, lane);
       }
       __syncwarp();
-      if (cols > 0) image_out<P * kVt * kC>(record_of(s) + rec.d, sm.out[own].image, lane);
+      if (cols > 0) columns_out<P>(record_of(s) + rec.d, sm.out[own].image, half, lane);
       __syncwarp();
       wait(&sm.full_k[use], s >> 1);
 #pragma unroll
-      for (int nt = 0; nt < 8; ++nt) {
-        const float2 eq = *reinterpret_cast<const float2*>(sc.eq + 8 * nt + 2 * t4);
+      for (int nt = 0; nt < 4; ++nt) {
+        const float2 eq = *reinterpret_cast<const float2*>(sc.eq + token0 + 8 * nt + 2 * t4);
 #pragma unroll
         for (int h = 0; h < 2; ++h) set_pair(d[nt], h, mul2(pair_of(d[nt], h), eq));
       }
       signal(&sm.free_k[use], lane);
-      const float sE = pow2_scale(warp_max(d));
-      Operand<2, 4> f;
+      const float sE = pow2_scale(both(warp_max(d), 4));
+      Operand<2, 2> f;
       f.split(d, sE);
       wait(&sm.done_y, use);  // do's place is free
       tmem_fence_after_sync();
-      f.store(mine + Col::d_in, 32);
+      f.store(d_in, 32);
       ready(&sm.ready_e);
       // the chain has taken do P of the step before, and with it these of that step
-      if (lane == 0) sm.inv_d[use][own] = inv_d, sm.inv_g[use][own] = pow2_inverse(sE);
+      if (lane == 0 && half == 0) sm.inv_d[use][own] = inv_d, sm.inv_g[use][own] = pow2_inverse(sE);
       signal(&sm.full_d[own], lane);
       fetch(s + kPlaces);
     };
@@ -389,26 +416,26 @@ __global__ void __launch_bounds__(kThreads, 1) bwd_kernel(const Args a) {
       const float inv_do = inv_d;
       wait(&sm.full_s[own], use);
       const float inv_s = sm.inv_s[own];
-      if (cols > 0) image_out<2 * kVt * KP>(record, sm.s[own], lane);
+      if (cols > 0) image_out<2 * kVt * KP>(record, sm.s[own], half, lane);
       signal(&sm.free_s[own], lane);
       if (s + 1 < n) ahead(s + 1);
 
       wait(&sm.full_l[own], use);
-      float x[8][4];
-      tiles_get(x, sm.l[own], lane);
+      float x[4][4];
+      tiles_get(x, sm.l[own] + token0 / 8 * 32, lane);
       signal(&sm.free_l[own], lane);
-      const float sL = pow2_scale(warp_max(x));
+      const float sL = pow2_scale(both(warp_max(x), 5));
       {
-        Operand<2, 4> f;
-        f.split(x, sL), f.put(sm.out[own].image, kVt * kC, 0, lane);
+        Operand<2, 2> f;
+        f.split(x, sL), f.put(sm.out[own].image, kVt * kC, token0, lane);
       }
       __syncwarp();
       if (cols > 0) {
-        image_out<2 * kVt * kC>(record + rec.u, sm.out[own].image, lane);
-        if (lane == 0) *reinterpret_cast<float4*>(record + rec.scales) = make_float4(inv_s, pow2_inverse(sL), inv_do, 0.f);
+        columns_out<2>(record + rec.u, sm.out[own].image, half, lane);
+        if (lane == 0 && half == 0) *reinterpret_cast<float4*>(record + rec.scales) = make_float4(inv_s, pow2_inverse(sL), inv_do, 0.f);
       }
-      __syncwarp();
-      rows_out(x, sm.out[own].dv, dv_at + (size_t)c * kC * row_t, row_t, tokens - c * kC, cols, lane);
+      both_sync(meet);  // dv takes the place of the image
+      rows_out(x, sm.out[own].dv, dv_at + (size_t)c * kC * row_t, row_t, tokens - c * kC, cols, token0 / 8, lane);
     }
     copy_wait<0>();
   }
@@ -426,6 +453,11 @@ cudaError_t launch(const Args& a, cudaStream_t stream) {
   static std::atomic<unsigned long long> done{0};
   cudaError_t e = allow_smem(reinterpret_cast<const void*>(kernel), smem, done);
   if (e != cudaSuccess) return e;
+  static const bool enough = [kernel] {
+    cudaFuncAttributes f;
+    return cudaFuncGetAttributes(&f, reinterpret_cast<const void*>(kernel)) == cudaSuccess && f.numRegs >= kRegLaunch;
+  }();
+  if (!enough) return cudaErrorInvalidConfiguration;
   const int sets = (v_tiles(a.s.V) + kWarps - 1) / kWarps;
   kernel<<<(unsigned)((size_t)a.s.nseq * a.s.Hv * sets), kThreads, smem, stream>>>(a);
   return cudaGetLastError();

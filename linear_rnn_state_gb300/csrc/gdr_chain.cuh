@@ -77,19 +77,19 @@ __device__ __forceinline__ void copy_wait() {
   asm volatile("cp.async.wait_group %0;" ::"n"(kLeft) : "memory");
 }
 
-// rows points at token 0 of the chunk; len of its tokens and cols of the 16 columns exist.
-template <typename T>
-__device__ __forceinline__ void rows_in(unsigned char* buf, const T* rows, long long stride_t, int len, int cols, int lane) {
+// rows points at token 0 of the chunk; len of its tokens and cols of the 16 columns
+// exist. All for tokens 8 n0 .. 8 (n0 + N) - 1 (n0 even).
+template <int N, typename T>
+__device__ __forceinline__ void rows_in(unsigned char* buf, const T* rows, long long stride_t, int len, int cols, int n0, int lane) {
   constexpr int kPer = 16 / sizeof(T), kPieces = 16 / kPer;  // values and pieces of 16 bytes
 #pragma unroll
-  for (int i = 0; i < kC * kPieces / 32; ++i) {
-    const int id = i * 32 + lane, row = id / kPieces, c = id % kPieces;
+  for (int i = 0; i < N * 8 * kPieces / 32; ++i) {
+    const int id = i * 32 + lane, row = 8 * n0 + id / kPieces, c = id % kPieces;
     const bool there = row < len && c * kPer < cols;
     unsigned char* dst = sizeof(T) == 2 ? buf + 2 * tri_at(row, c * 8) : buf + row * 80 + c * 16;
     copy_async16(dst, there ? rows + row * stride_t + c * kPer : rows, there);
   }
 }
-// Tokens 8 n0 .. 8 (n0 + N) - 1 of a warp's rows (n0 even).
 template <int N>
 __device__ __forceinline__ void rows_get(float (&x)[N][4], const unsigned char* buf, int n0, int lane, const __nv_bfloat16*) {
 #pragma unroll
@@ -111,9 +111,10 @@ __device__ __forceinline__ void rows_get(float (&x)[N][4], const unsigned char* 
 #pragma unroll
     for (int e = 0; e < 4; ++e) x[nt][e] = s[(8 * (n0 + nt) + 2 * (lane & 3) + (e & 1)) * 20 + (lane >> 2) + 8 * (e >> 1)];
 }
-__device__ __forceinline__ void rows_put(const float (&x)[8][4], unsigned char* buf, int lane, const __nv_bfloat16*) {
+template <int N>
+__device__ __forceinline__ void rows_put(const float (&x)[N][4], unsigned char* buf, int n0, int lane, const __nv_bfloat16*) {
 #pragma unroll
-  for (int q = 0; q < 4; ++q) {
+  for (int q = 0; q < N / 2; ++q) {
     uint32_t r[4];
 #pragma unroll
     for (int i = 0; i < 4; ++i) {
@@ -121,37 +122,40 @@ __device__ __forceinline__ void rows_put(const float (&x)[8][4], unsigned char* 
       const __nv_bfloat162 v = __floats2bfloat162_rn(y[0], y[1]);
       r[i] = *reinterpret_cast<const uint32_t*>(&v);
     }
-    stsm4t(reinterpret_cast<__half*>(buf) + tri_at(16 * q + (lane & 15), (lane >> 4) * 8), r);
+    stsm4t(reinterpret_cast<__half*>(buf) + tri_at(8 * n0 + 16 * q + (lane & 15), (lane >> 4) * 8), r);
   }
 }
-__device__ __forceinline__ void rows_put(const float (&x)[8][4], unsigned char* buf, int lane, const float*) {
+template <int N>
+__device__ __forceinline__ void rows_put(const float (&x)[N][4], unsigned char* buf, int n0, int lane, const float*) {
   float* s = reinterpret_cast<float*>(buf);
 #pragma unroll
-  for (int nt = 0; nt < 8; ++nt)
+  for (int nt = 0; nt < N; ++nt)
 #pragma unroll
-    for (int e = 0; e < 4; ++e) s[(8 * nt + 2 * (lane & 3) + (e & 1)) * 20 + (lane >> 2) + 8 * (e >> 1)] = x[nt][e];
+    for (int e = 0; e < 4; ++e) s[(8 * (n0 + nt) + 2 * (lane & 3) + (e & 1)) * 20 + (lane >> 2) + 8 * (e >> 1)] = x[nt][e];
 }
 // x to memory by way of buf.
-template <typename T>
-__device__ __forceinline__ void rows_out(const float (&x)[8][4], unsigned char* buf, T* rows, long long stride_t, int len,
-                                         int cols, int lane) {
+template <int N, typename T>
+__device__ __forceinline__ void rows_out(const float (&x)[N][4], unsigned char* buf, T* rows, long long stride_t, int len, int cols,
+                                         int n0, int lane) {
   constexpr int kPer = 16 / sizeof(T), kPieces = 16 / kPer;
-  rows_put(x, buf, lane, rows);
+  rows_put(x, buf, n0, lane, rows);
   __syncwarp();
 #pragma unroll
-  for (int i = 0; i < kC * kPieces / 32; ++i) {
-    const int id = i * 32 + lane, row = id / kPieces, c = id % kPieces;
+  for (int i = 0; i < N * 8 * kPieces / 32; ++i) {
+    const int id = i * 32 + lane, row = 8 * n0 + id / kPieces, c = id % kPieces;
     const unsigned char* src = sizeof(T) == 2 ? buf + 2 * tri_at(row, c * 8) : buf + row * 80 + c * 16;
     if (row < len && c * kPer < cols) *reinterpret_cast<uint4*>(rows + row * stride_t + c * kPer) = *reinterpret_cast<const uint4*>(src);
   }
   __syncwarp();
 }
-// Asks for a chunk's rows into L2.
-template <typename T>
-__device__ __forceinline__ void rows_ask(const T* rows, long long stride_t, int len, int lane) {
+// Asks for rows into L2 (N a multiple of 4).
+template <int N, typename T>
+__device__ __forceinline__ void rows_ask(const T* rows, long long stride_t, int len, int n0, int lane) {
 #pragma unroll
-  for (int i = 0; i < kC / 32; ++i)
-    if (i * 32 + lane < len) prefetch_l2(rows + (i * 32 + lane) * stride_t);
+  for (int i = 0; i < N * 8; i += 32) {
+    const int row = 8 * n0 + i + lane;
+    if (row < len) prefetch_l2(rows + row * stride_t);
+  }
 }
 
 // The state of a warp: rows g4 (+ 8), keys key0 + 8 nt + 2 t4 (+ 1).

@@ -39,6 +39,9 @@
 namespace gdr {
 namespace {
 
+// Warps: the chain's eight, four helpers, and those without rows.
+constexpr int kFiller = kChains + kWarps, kIssuer = kFiller + 1, kHelpersIssuer = kIssuer + 1, kThreads = (kHelpersIssuer + 1) * 32;
+
 template <typename T, int KP, bool kSave>
 struct alignas(1024) FwdSmem {
   static constexpr int P = In<T>::kParts, kPlaces = P * KP >= 256 ? 1 : 2;  // of v: what fits
@@ -316,10 +319,10 @@ __global__ void __launch_bounds__(kThreads, 1) fwd_kernel(const Args a) {
     auto fetch = [&](int c) {  // v of chunk c, and a request for a later one
       const int place = kPlaces == 2 ? c & 1 : 0;
       if (c < n) {
-        rows_in(sm.v[own][place], v_at + c * kC * a.s.v_t, a.s.v_t, cols > 0 ? tokens - c * kC : 0, cols, lane);
+        rows_in<8>(sm.v[own][place], v_at + c * kC * a.s.v_t, a.s.v_t, cols > 0 ? tokens - c * kC : 0, cols, 0, lane);
         copy_arrive(&sm.full_v[own][place]);
       }
-      if (c + 2 < n && cols > 0) rows_ask(v_at + (c + 2) * kC * a.s.v_t, a.s.v_t, tokens - (c + 2) * kC, lane);
+      if (c + 2 < n && cols > 0) rows_ask<8>(v_at + (c + 2) * kC * a.s.v_t, a.s.v_t, tokens - (c + 2) * kC, 0, lane);
     };
     fetch(0);
     if (kPlaces == 2) fetch(1);
@@ -392,7 +395,7 @@ __global__ void __launch_bounds__(kThreads, 1) fwd_kernel(const Args a) {
         for (int h = 0; h < 2; ++h) set_pair(o[nt], h, fma2(make_float2(fo, fo), pair_of(x[nt], h), pair_of(o[nt], h)));
       if (kSave && lane == 0) bulk_wait_read();
       __syncwarp();
-      rows_out(o, sm.out[own].o, o_at + (size_t)c * kC * o_t, o_t, tokens - c * kC, cols, lane);
+      rows_out(o, sm.out[own].o, o_at + (size_t)c * kC * o_t, o_t, tokens - c * kC, cols, 0, lane);
     }
     if (kSave && lane == 0) bulk_wait_all();
   }

@@ -225,14 +225,20 @@ struct Operand {
   }
 };
 
-constexpr int kWarps = 4;  // times 16 rows a block: two chain warps each, and a helper
-constexpr int kChains = 2 * kWarps, kFiller = kChains + kWarps, kIssuer = kFiller + 1, kHelpersIssuer = kIssuer + 1, kThreads = (kHelpersIssuer + 1) * 32;
+constexpr int kWarps = 4, kChains = 2 * kWarps;  // of 16 rows each: two chain warps, half of the columns each
 
-// The larger of two warps' values: of the two chain warps of 16 rows, each with
-// half of the columns, which meet at barrier `id`.
+// Registers of a thread of the calling four warps, of those the block was launched with.
+template <int N>
+__device__ __forceinline__ void more_registers() { asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(N)); }
+template <int N>
+__device__ __forceinline__ void fewer_registers() { asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(N)); }
+
+// The two warps of 16 rows, each with half of the columns, meet at barrier `id`;
+// the larger of their values.
+__device__ __forceinline__ void both_sync(int id) { asm volatile("bar.sync %0, 64;" ::"r"(id) : "memory"); }
 __device__ __forceinline__ float both_max(float m, float* slot, int half, int id, int lane) {
   if (lane == 0) slot[half] = m;
-  asm volatile("bar.sync %0, 64;" ::"r"(id) : "memory");
+  both_sync(id);
   return fmaxf(m, slot[half ^ 1]);
 }
 
