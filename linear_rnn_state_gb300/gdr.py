@@ -15,6 +15,7 @@ and states [n][Hv][V][K] float32. q, k, v may be slices of a wider tensor.
 from __future__ import annotations
 
 import ctypes
+import functools
 
 from . import wkv7
 
@@ -158,8 +159,20 @@ def _sequences(seq_starts, B, dev):
     return n, n
 
 
+# The buffers' sizes depend on the arguments alone (a C call takes 1.1 us, the lookup 0.2).
+@functools.lru_cache(maxsize=256)
+def _saved_bytes(*args):
+    return load().gdr_saved_bytes(*args)
+
+
+@functools.lru_cache(maxsize=256)
+def _backward_bytes(*args):
+    return load().gdr_backward_bytes(*args)
+
+
 def saved_bytes(B, T, Hk, Hv, K, V, nseq=-1, *, bf16, for_backward) -> int:
-    return load().gdr_saved_bytes(B, T, Hk, Hv, K, V, nseq, int(bf16), int(for_backward))
+    """Bytes of what ``forward`` keeps for itself and, with for_backward, for ``backward``."""
+    return _saved_bytes(B, T, Hk, Hv, K, V, nseq, int(bf16), int(for_backward))
 
 
 def forward(q, k, v, g, beta, s_init=None, *, scale: float | None = None, qk_l2norm: bool = False, seq_starts=None,
@@ -180,7 +193,7 @@ def forward(q, k, v, g, beta, s_init=None, *, scale: float | None = None, qk_l2n
         _check_tensor("s_init", s_init, (n, Hv, V, K), _torch.float32, dev)
     o = _torch.empty((B, T, Hv, V), dtype=q.dtype, device=dev)
     s_final = _torch.empty((n, Hv, V, K), dtype=_torch.float32, device=dev) if want_s_final else None
-    saved = _torch.empty(lib.gdr_saved_bytes(B, T, Hk, Hv, K, V, nseq, bf16, want_saved), dtype=_torch.uint8, device=dev)
+    saved = _torch.empty(_saved_bytes(B, T, Hk, Hv, K, V, nseq, bf16, want_saved), dtype=_torch.uint8, device=dev)
     rc = (lib.gdr_forward_bf16 if bf16 else lib.gdr_forward)(
         q.data_ptr(), k.data_ptr(), v.data_ptr(), g.data_ptr(), beta.data_ptr(), _addr(s_init), _addr(seq_starts), o.data_ptr(),
         _addr(s_final), saved.data_ptr(), _strides(q, k, v), K ** -0.5 if scale is None else scale, qk_l2norm, want_saved, B, T,
@@ -206,7 +219,7 @@ def backward(q, k, v, g, beta, do, saved, *, dS_final=None, want_dS_init: bool =
     _check_tensor("do", do, (B, T, Hv, V), q.dtype, dev)
     if dS_final is not None:
         _check_tensor("dS_final", dS_final, (n, Hv, V, K), _torch.float32, dev)
-    need = lib.gdr_saved_bytes(*dims, nseq, bf16, 1)
+    need = _saved_bytes(*dims, nseq, bf16, 1)
     if saved is None:
         raise ValueError("saved must be what forward(..., want_saved=True) returned")
     _check_tensor("saved", saved, (need,), _torch.uint8, dev)
@@ -215,7 +228,7 @@ def backward(q, k, v, g, beta, do, saved, *, dS_final=None, want_dS_init: bool =
 
     grads = {"dq": empty(q.shape, q.dtype), "dk": empty(q.shape, q.dtype), "dv": empty(v.shape, q.dtype), "dg": empty(g.shape),
              "dbeta": empty(g.shape), "dS_init": empty((n, Hv, V, K)) if want_dS_init else None}
-    work = empty(lib.gdr_backward_bytes(*dims, nseq, bf16), _torch.uint8)
+    work = empty(_backward_bytes(*dims, nseq, bf16), _torch.uint8)
     fn = lib.gdr_backward_bf16 if bf16 else lib.gdr_backward
     wkv7._check(fn(*(_addr(x) for x in (q, k, v, g, beta, do, dS_final, seq_starts, saved, work)),
                    *(_addr(x) for x in grads.values()), _strides(q, k, v), K ** -0.5 if scale is None else scale, qk_l2norm, *dims,
