@@ -12,13 +12,15 @@
 // helpers leave the images of dS1, lam and do for the gradients of q, k, g and
 // beta (gdr_grad.cu). fp16 pairs throughout: dS, lam and do enter fp32 results.
 //
-// Bound by a step's latency, some 6200 cycles: the three warps that share a
-// scheduler run three long straight pieces of code, and waiting for instructions
-// (3.8 of 10 cycles between issues) is the largest part of it. Measured (64
-// steps): 4 x 4096 x 32 heads of 64 bfloat16 210 us, 3.6 TB/s; 8 x 4096 x 12 x 64
-// fp32 238 us, 3.4 TB/s; 2 x 4095 x 32 x 128 bfloat16 233 us, 4.0 TB/s.
-// Measured and dropped: four more warps for dv and the images of dS1 and lam
-// (214 us); products issued in rolled loops, for less code (218 us).
+// Two helper warps for each 16 rows, as the chain has: one took 5800 cycles over
+// its step, and the chain waited for 1100 to 2200 of them (200 to 162 us).
+//
+// Bound by a step's latency, some 4700 cycles, and at 4.7 TB/s by memory in part
+// (stores wait). Measured (64 steps): 4 x 4096 x 32 heads of 64 bfloat16 162 us, 4.7
+// TB/s; 8 x 4096 x 12 x 64 fp32 210 us, 3.9 TB/s; 2 x 4095 x 32 x 128 bfloat16 192
+// us, 4.8 TB/s. Measured and dropped, at the first size: four warps apart for dv and
+// the images of dS1 and lam (201 to 193 us, at 128 keys 201 to 220); products issued
+// in rolled loops, for less code (210 to 218).
 #include "gdr_chain.cuh"
 #include "gdr_tc.cuh"
 

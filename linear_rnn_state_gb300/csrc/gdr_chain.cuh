@@ -2,12 +2,12 @@
 // the tensor cores' part (gdr_tc.cuh): barriers, the rows of v, o, do and dv, the
 // state.
 //
-// A warp has 16 rows of the state (value columns) and all keys. With the rows as
-// the m of every product (S k^T, r T^T, u P^T, w^T k are 16 x 64 or 16 x keys) the
-// result of one is, scaled and packed to fp16 pairs, the left operand of the next,
-// warps never exchange values, and every scale is the exact maximum of the warp's
-// own. Between two products all is in registers, laid out as mma.sync's
-// accumulator tiles.
+// Two warps have 16 rows of the state (value columns), half of the keys and half of
+// the tokens each. With the rows as the m of every product (S k^T, r T^T, u P^T,
+// w^T k are 16 x 64 or 16 x keys) the result of one is, scaled and packed to fp16
+// pairs, the left operand of the next, the two exchange nothing but a maximum, and
+// every scale is the exact maximum of the 16 rows. Between two products all is in
+// registers, laid out as mma.sync's accumulator tiles.
 //
 // The chain's warps make only what the next state waits for; helper warps beside
 // them make the rest, o in the forward and the products with do in the backward,
@@ -19,7 +19,7 @@
 // it shared-memory reads, 25 % three barriers); 16 rows a warp by mma.sync, in
 // registers, 254; helper warps, 194; barriers asked early, 178; tcgen05 with left
 // operands in shared memory, 183 to 210; in tensor memory, 189; products issued by
-// warps of their own, 138.
+// warps of their own, 138; two warps for the 16 rows, 127.
 #pragma once
 
 #include "gdr_common.cuh"

@@ -13,26 +13,27 @@
 // scales them, splits them to fp16 pairs at the exact maximum of its own values,
 // and writes them back as rows of the next batch's operand.
 //
-// What bounds it is the latency of a step, some 4000 cycles: three batches that
+// What bounds it is the latency of a step, some 3700 cycles: three batches that
 // wait for one another, each 300 to 450 cycles until its products are back and
-// 500 to 700 to scale, split and store the next operand. So the chain's four
-// warps make only what the next state waits for, and four helper
-// warps beside them (which reach the same rows) make o and move the rows and
-// images to and from memory. Two warps wait for operands and issue the products,
-// one fills the chunk's images.
+// some 500 to scale, split and store the next operand. So the chain's warps, two
+// for each 16 rows with half of the columns each, make only what the next state
+// waits for; four helper warps beside them (which reach the same rows) make o and
+// move the rows and images to and from memory. Two warps wait for operands and
+// issue the products, one fills the chunk's images.
 // kSave: the images of S0 and u go to memory for the backward.
 //
 // Arithmetic: fp16 pairs in everything that the states depend on. o of
 // bfloat16 calls takes S0, u and P with their hi part alone (11 bits against
 // the 8 that o is rounded to: 0.0003 of o's error of 0.0017).
 //
-// Measured (64 steps; time, traffic): 4 x 4096 x 32 heads of 64 bfloat16 139 us,
-// 3.8 TB/s; 8 x 4096 x 12 x 64 fp32 170 us, 3.4 TB/s; 2 x 4095 x 32 x 128 bfloat16
-// 174 us, 3.9 TB/s. 65536 tokens of 40 heads (1024 steps on 40 of 152 SMs) 2.04 ms.
-// Measured and dropped: 128 rows, the hi and lo parts as one operand (twice the
-// tensor-memory reads, 200 us); v by a warp of its own (156 us, it comes later);
-// v and o by whole rows of 64 columns instead of 16 a warp (144 us); the operands'
-// images to memory by loads and stores instead of bulk copies (145 us).
+// Measured (64 steps; time, traffic): 4 x 4096 x 32 heads of 64 bfloat16 127 us,
+// 4.2 TB/s; 8 x 4096 x 12 x 64 fp32 160 us, 3.6 TB/s; 2 x 4095 x 32 x 128 bfloat16
+// 155 us, 4.4 TB/s. 65536 tokens of 40 heads (1024 steps on 40 of 152 SMs) 2.04 ms.
+// Measured and dropped, at the first size: 128 rows, the hi and lo parts as one
+// operand (twice the reads of tensor memory; 183 to 202 us); v by a warp of its own
+// (145 to 156, it comes later); v and o by whole rows of 64 columns instead of 16 a
+// warp (139 to 144); the images to memory by loads and stores instead of bulk copies
+// (137 to 145); two helper warps for each 16 rows (128 to 133).
 #include "gdr_chain.cuh"
 #include "gdr_tc.cuh"
 
