@@ -90,6 +90,7 @@ size_t place_workspace(Buffers& b, const Shape& s, bool bf16, char* p) {
     return r;
   };
   b.b_rec = take(l.n_t * l.b_rec);
+  b.carry_back = segments_of(s) > 1 ? reinterpret_cast<float*>(take((size_t)s.nseq * s.Hv * s.V * s.K * 4)) : nullptr;
   b.dq_part = b.dk_part = nullptr;
   if (needs_terms(s, l.parts)) {
     const size_t bytes = (size_t)s.B * s.T * s.Hv * s.K * 4;
@@ -138,6 +139,7 @@ int forward_impl(bool bf16, const void* q, const void* k, const void* v, const f
   a.q = q, a.k = k, a.v = v, a.g = g, a.beta = beta, a.s_init = s_init, a.o = o, a.s_final = s_final;
   if ((rc = wkv7::api_status_word(&a.status))) return rc;
   const int parts = segments_of(a.s), chunks = (T + kC - 1) / kC, each = (chunks + parts - 1) / parts;
+  if (parts > 1) a.small = 0;
   for (int at = 0; at < chunks || at == 0; at += each) {
     if (parts > 1) {
       a.seg0 = at, a.segn = std::min(each, chunks - at);
@@ -186,8 +188,24 @@ int backward_impl(bool bf16, const void* q, const void* k, const void* v, const 
   a.q = q, a.k = k, a.v = v, a.g = g, a.beta = beta, a.d_o = d_o, a.dS_final = dS_final;
   a.dq = dq, a.dk = dk, a.dv = dv, a.dg = dg, a.dbeta = dbeta, a.dS_init = dS_init;
   if ((rc = wkv7::api_status_word(&a.status))) return rc;
-  if ((rc = launched(launch_bwd(a, bf16, stream), "backward"))) return rc;
-  return launched(launch_grad(a, bf16, stream), "gradients");
+  const int parts = segments_of(a.s), chunks = (T + kC - 1) / kC, each = (chunks + parts - 1) / parts;
+  if (parts > 1) a.small = 0;
+  if (parts == 1) {
+    if ((rc = launched(launch_bwd(a, bf16, stream), "backward"))) return rc;
+    return launched(launch_grad(a, bf16, stream), "gradients");
+  }
+  // from the last segment to the first: the chain of one, then the gradients of the one after it beside that chain
+  if (!dS_init) a.dS_init = a.b.carry_back;
+  const int last = (chunks - 1) / each * each;
+  Args after{};
+  for (int at = last; at >= 0; at -= each) {
+    a.seg0 = at, a.segn = std::min(each, chunks - at);
+    if ((rc = launched(launch_bwd(a, bf16, stream), "backward"))) return rc;
+    if (at < last && (rc = launched(launch_grad(after, bf16, stream), "gradients"))) return rc;
+    after = a;
+    a.dS_final = a.dS_init;
+  }
+  return launched(launch_grad(after, bf16, stream), "gradients");
 }
 
 int step_impl(bool bf16, const void* q, const void* k, const void* v, const float* g, const float* beta, float* state,

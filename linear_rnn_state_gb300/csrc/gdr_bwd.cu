@@ -168,8 +168,9 @@ __global__ void __launch_bounds__(kThreads, 1) bwd_kernel(const Args a) {
   tmem_fence_before_sync();
   __syncthreads();
   tmem_fence_after_sync();
-  if (a.small) grid_go();
-  const SeqRange sq = seq_range(a.s, seq);
+  if (a.small || a.segn) grid_go();  // the gradients, of the segment before
+  SeqRange sq = seq_range(a.s, seq);
+  if (a.segn) sq.t0 += a.seg0 * kC, sq.t1 = min(sq.t1, sq.t0 + a.segn * kC), sq.slot += a.seg0;
   const int n = (sq.t1 - sq.t0 + kC - 1) / kC;
   const int K = a.s.K, V = a.s.V, vt = set * kWarps + own;
   const int cols = V - vt * kVt, tokens = sq.t1 - sq.t0;  // cols <= 0: this warp's rows are zeros

@@ -110,11 +110,13 @@ __global__ void __launch_bounds__(kThreads<KP>, KP == 64 ? 2 : 1) grad_kernel(co
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5, wc = warp >> 2, wr = wc & 1 ? 3 - (warp & 3) : warp & 3;
   const int g4 = lane >> 2, t4 = lane & 3, group = a.s.Hv / a.s.Hk;
   const int heads = kOut == kSum ? group : 1, per_slot = a.s.Hv / heads;
-  const int slot = blockIdx.x / per_slot, hv0 = blockIdx.x % per_slot * heads, hk = hv0 / group;
+  int slot = blockIdx.x / per_slot;
+  if (a.segn) slot = slot / a.segn * ((a.s.T + kC - 1) / kC) + a.seg0 + slot % a.segn;
+  const int hv0 = blockIdx.x % per_slot * heads, hk = hv0 / group;
   ChunkAt c;
   if (a.small) grid_go();
   if (!chunk_at(a.s, slot, c)) return;
-  grid_wait();
+  if (!a.segn) grid_wait();  // else begun beside the chain of the segment before, of which nothing is read
   const int vts = (a.s.V + kVt - 1) / kVt, K = a.s.K;
   const size_t at_k = (size_t)slot * a.s.Hk + hk, at_v0 = (size_t)slot * a.s.Hv + hv0;
   constexpr int image = P * kC * KP * 2;
@@ -455,6 +457,7 @@ __global__ void __launch_bounds__(kThreads<KP>, KP == 64 ? 2 : 1) grad_kernel(co
       }
     }
   }
+  if (a.segn && blockIdx.x == 0) grid_wait();  // over only when that chain is, for what comes next
 }
 
 // dq and dk of a key head: its value heads' terms in order, then the gradient
@@ -504,9 +507,10 @@ cudaError_t launch(const Args& a, cudaStream_t stream) {
   static std::atomic<unsigned long long> done{0};
   cudaError_t e = allow_smem(reinterpret_cast<const void*>(kernel), smem, done);
   if (e != cudaSuccess) return e;
-  const size_t blocks = (size_t)a.s.slots * (kOut == kSum ? a.s.Hk : a.s.Hv);
-  e = launch_after(a.small, kernel, (unsigned)blocks, kThreads<KP>, smem, stream, a);
-  if (e != cudaSuccess || kOut != kTerms) return e;
+  const size_t blocks = (a.segn ? (size_t)a.s.B * a.segn : a.s.slots) * (kOut == kSum ? a.s.Hk : a.s.Hv);
+  const bool more = a.segn && a.seg0 > 0;  // segments
+  e = launch_after(a.small || more, kernel, (unsigned)blocks, kThreads<KP>, smem, stream, a);
+  if (e != cudaSuccess || kOut != kTerms || more) return e;
   const size_t rows = 2 * (size_t)a.s.B * a.s.T * a.s.Hk;
   return launch_after(a.small, join_kernel<T>, (unsigned)((rows * 16 + 255) / 256), 256, 0, stream, a);
 }

@@ -115,7 +115,7 @@ struct Buffers {
   // forward: the images of the state before the chunk and of u, their inverse
   // scales; of the backward: of the carried gradient after it, lambda and do.
   char *f_rec, *b_rec;
-  float* carry;                   // states from segment to segment, where the caller wants none
+  float *carry, *carry_back;      // states and their gradients from segment to segment, where the caller wants none
   float *dq_part, *dk_part;       // [B][T][Hv][K] terms of shared heads' gradients, or null
 };
 
@@ -132,15 +132,17 @@ struct Args {
               // Saves 4 of 31 us for one chunk; 40 heads of 1024 chunks lost 650 of 3900 us to blocks
               // that waited where others could have run.
 };
-// A forward in segments, the preparation of one beside the chain of the one
-// before: where the chains leave half of the SMs free or more, and segments have
-// 64 chunks or more. 40 heads of 1024 chunks 2985 us in one, 2467 in four, 2399 in
-// eight, 2384 in sixteen; 96 heads of 64 chunks, forward and backward, 960 in one,
-// 944 in two and 971 in four.
+// A forward in segments, the preparation of one beside the chain of the one before,
+// and a backward, the gradients of one beside the chain of the next: where the
+// chains leave SMs free. us in one segment and in as many as here: 40 heads of 1024
+// chunks, fp32, forward 2985 and 2174 (4: 2467, 8: 2399); forward and backward,
+// bfloat16, 32 heads of 256 chunks 1580 and 1306, 100 of 256 2568 and 2388, 8 of 256
+// 1242 and 1208 (8: 1248), 8 of 64 348 (2: 355), fp32 96 of 64 957 and 925.
 inline int segments_of(const Shape& s) {
-  const int n = (s.T + kC - 1) / kC, most = n / 64;
+  const int n = (s.T + kC - 1) / kC;
   const long long chains = (long long)s.nseq * s.Hv * ((v_tiles(s.V) + 3) / 4);
-  return s.packed || chains > 152 / 2 || most < 2 ? 1 : most < 16 ? most : 16;
+  const int most = n >= 128 ? n / 64 : n >= 64 && chains >= 16 ? 2 : 1;
+  return s.packed || chains > 104 ? 1 : most < 16 ? most : 16;
 }
 inline int is_small(const Shape& s) { return (long long)s.slots * s.Hv <= 152; }
 

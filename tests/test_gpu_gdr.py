@@ -150,6 +150,26 @@ def test_long_sequences_of_few_heads(env, B, T, dtype):
     _close("o", o3, o.double().cpu().numpy())
 
 
+@pytest.mark.parametrize("Hk,Hv,K,dtype", [(2, 2, 64, F32), (1, 3, 128, BF16), (3, 3, 72, BF16)])
+def test_long_sequences_backward_in_segments(env, Hk, Hv, K, dtype):
+    orc, gdr = env
+    d = _make(1, 8300, Hk, Hv, K, 16, dtype, K, rate=0.1)
+    _check(env, d)
+    o, s, saved = gdr.forward(*(d[n] for n in INS))
+    first = gdr.backward(*(d[n] for n in INS), d["do"], saved, dS_final=d["dS_final"])
+    again = gdr.backward(*(d[n] for n in INS), d["do"], saved, dS_final=d["dS_final"], want_dS_init=False)
+    assert again["dS_init"] is None
+    assert all(torch.equal(first[n], again[n]) for n in ("dq", "dk", "dv", "dg", "dbeta"))
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        third = gdr.backward(*(d[n] for n in INS), d["do"], saved, dS_final=d["dS_final"])
+    for x in third.values():
+        x.zero_()
+    graph.replay()
+    torch.cuda.synchronize()
+    assert all(torch.equal(first[n], third[n]) for n in third)
+
+
 def test_one_token_from_nothing_has_no_decay_gradient(env):
     _, _, g = _check(env, _make(3, 1, 2, 2, 64, 64, BF16), carry=False)
     assert torch.count_nonzero(g["dg"]) == 0
