@@ -12,9 +12,9 @@
 // its rounding to the residual's type.
 //
 // A row belongs to a group of kGroup threads with kVec pieces of eight values
-// each; a block holds 256 / kGroup rows. All are bound by memory: the pieces
-// are 16-byte loads, and 2048 threads an SM keep some 64 KB in flight. The
-// sums over rows: a block walks rows a grid apart, keeps its columns' sums in
+// each; a block of 256 threads holds 256 / kGroup rows. All are bound by memory:
+// the pieces are 16-byte loads where rows allow them, and 2048 threads an SM keep
+// some 64 KB in flight. The sums over rows: a block walks rows a grid apart, keeps its columns' sums in
 // registers and writes them as one partial row; a last kernel adds the
 // partial rows in order (no atomics, the same bits every time).
 //
@@ -32,7 +32,10 @@
 namespace blocknorm {
 namespace {
 
-constexpr int kThreads = 256;
+// Threads of a block whose rows have groups of kGroup.
+template <int kGroup>
+constexpr int kThreads = kGroup > 256 ? kGroup : 256;
+constexpr int kSumThreads = 256;
 
 __device__ __forceinline__ void unpack(float (&x)[8], uint4 u) {
   const uint32_t w[4] = {u.x, u.y, u.z, u.w};
@@ -137,9 +140,9 @@ __device__ __forceinline__ long long row_at(const Args& p, long long row, long l
 
 // kGate: the gated norm (a = o, b = z); otherwise the add norm (a = x, b = residual).
 template <typename TA, typename TB, bool kGate, int kGroup, int kVec, bool kWhole>
-__global__ void __launch_bounds__(kThreads) forward_kernel(const Args p) {
-  __shared__ float red[kThreads / 32];
-  constexpr int kRows = kThreads / kGroup, kStep = kWhole ? 1 : kGroup;
+__global__ void __launch_bounds__(kThreads<kGroup>) forward_kernel(const Args p) {
+  __shared__ float red[kThreads<kGroup> / 32];
+  constexpr int kRows = kThreads<kGroup> / kGroup, kStep = kWhole ? 1 : kGroup;
   const int tg = threadIdx.x % kGroup;
   const long long row = (long long)blockIdx.x * kRows + threadIdx.x / kGroup;
   const bool in = row < p.rows;
@@ -192,10 +195,10 @@ __global__ void __launch_bounds__(kThreads) forward_kernel(const Args p) {
 }
 
 template <typename TA, typename TB, bool kGate, int kGroup, int kVec, bool kWhole>
-__global__ void __launch_bounds__(kThreads) backward_kernel(const Args p) {
-  __shared__ float red[kThreads / 32];
-  constexpr int kRows = kThreads / kGroup, kSums = kGate ? 1 : 2, kStep = kWhole ? 1 : kGroup;
-  __shared__ float join[kRows > 1 ? kSums * kThreads * 8 : 1];
+__global__ void __launch_bounds__(kThreads<kGroup>) backward_kernel(const Args p) {
+  __shared__ float red[kThreads<kGroup> / 32];
+  constexpr int kRows = kThreads<kGroup> / kGroup, kSums = kGate ? 1 : 2, kStep = kWhole ? 1 : kGroup;
+  __shared__ float join[kRows > 1 ? kSums * kThreads<kGroup> * 8 : 1];
   const int tg = threadIdx.x % kGroup, sub = threadIdx.x / kGroup, D = p.D;
   gdr::grid_go();
   float dw[kVec][8], ds[kGate ? 1 : kVec][8];
@@ -296,13 +299,13 @@ __global__ void __launch_bounds__(kThreads) backward_kernel(const Args p) {
     for (int e = 0; e < 8; ++e) {
       const int at = sub * kGroup * 8 + column<kStep, kGroup>(0, tg) + e * kStep;
       join[at] = dw[0][e];
-      if constexpr (!kGate) join[kThreads * 8 + at] = ds[0][e];
+      if constexpr (!kGate) join[kThreads<kGroup> * 8 + at] = ds[0][e];
     }
     __syncthreads();
-    for (int i = threadIdx.x; i < kSums * kGroup * 8; i += kThreads) {
+    for (int i = threadIdx.x; i < kSums * kGroup * 8; i += kThreads<kGroup>) {
       const int sum = i / (kGroup * 8), c = i % (kGroup * 8);
       float s = 0.f;
-      for (int q = 0; q < kRows; ++q) s += join[(sum * kThreads + q * kGroup) * 8 + c];
+      for (int q = 0; q < kRows; ++q) s += join[(sum * kThreads<kGroup> + q * kGroup) * 8 + c];
       if (c < D) part[sum * D + c] = s;
     }
   } else {
@@ -320,7 +323,7 @@ __global__ void __launch_bounds__(kThreads) backward_kernel(const Args p) {
 }
 
 // The partial rows' sums, column by column: 32 columns a block, eight threads each.
-__global__ void __launch_bounds__(kThreads) sums_kernel(const float* part, int parts, int sums, int D, float* dw, float* ds) {
+__global__ void __launch_bounds__(kSumThreads) sums_kernel(const float* part, int parts, int sums, int D, float* dw, float* ds) {
   __shared__ float red[8][33];
   gdr::grid_wait();
   const int x = threadIdx.x & 31, y = threadIdx.x >> 5, c = blockIdx.x * 32 + x, n = sums * D;
@@ -340,23 +343,30 @@ __global__ void __launch_bounds__(kThreads) sums_kernel(const float* part, int p
 }
 
 template <typename TA, typename TB, bool kGate, int kGroup, int kVec, bool kWhole>
-cudaError_t launch(const Args& p, bool backward, cudaStream_t s) {
-  constexpr int rows = kThreads / kGroup;
-  const long long blocks = (p.rows + rows - 1) / rows;
-  if (!backward) {
-    forward_kernel<TA, TB, kGate, kGroup, kVec, kWhole><<<(unsigned)blocks, kThreads, 0, s>>>(p);
-    return cudaGetLastError();
-  }
+cudaError_t forward(const Args& p, cudaStream_t s) {
+  constexpr int rows = kThreads<kGroup> / kGroup;
+  forward_kernel<TA, TB, kGate, kGroup, kVec, kWhole><<<(unsigned)((p.rows + rows - 1) / rows), kThreads<kGroup>, 0, s>>>(p);
+  return cudaGetLastError();
+}
+template <typename TA, typename TB, bool kGate, int kGroup, int kVec, bool kWhole>
+cudaError_t backward(const Args& p, cudaStream_t s) {
   const int parts = part_rows(p.rows, p.D);
-  backward_kernel<TA, TB, kGate, kGroup, kVec, kWhole><<<parts, kThreads, 0, s>>>(p);
+  backward_kernel<TA, TB, kGate, kGroup, kVec, kWhole><<<parts, kThreads<kGroup>, 0, s>>>(p);
   cudaError_t e = cudaGetLastError();
   if (e != cudaSuccess) return e;
   const int sums = kGate ? 1 : 2;
-  return gdr::launch_after(true, sums_kernel, (unsigned)((sums * p.D + 31) / 32), (unsigned)kThreads, 0, s, (const float*)p.part, parts, sums, p.D,
+  return gdr::launch_after(true, sums_kernel, (unsigned)((sums * p.D + 31) / 32), (unsigned)kSumThreads, 0, s, (const float*)p.part, parts, sums, p.D,
                            p.dw, p.dscale);
 }
+template <typename TA, typename TB, bool kGate, int kGroup, int kVec, bool kWhole>
+cudaError_t launch(const Args& p, bool bw, cudaStream_t s) {
+  return bw ? backward<TA, TB, kGate, kGroup, kVec, kWhole>(p, s) : forward<TA, TB, kGate, kGroup, kVec, kWhole>(p, s);
+}
 // A group of threads is the least power of two with eight values each; rows
-// wider than 2048 take more pieces a thread.
+// wider than 2048 take more pieces a thread, but past 4096 the backward's sums would
+// leave a block an SM: there a thread has one (8192, 16 M values of bfloat16 and
+// fp32 residual: 165 -> 117 us; to 4096 it loses, 105 -> 109, and so does the
+// forward, 44 -> 50).
 template <typename TA, typename TB, bool kGate, bool kWhole>
 cudaError_t pick(const Args& p, bool bw, cudaStream_t s) {
   const int need = (p.D + 7) / 8;
@@ -367,7 +377,7 @@ cudaError_t pick(const Args& p, bool bw, cudaStream_t s) {
   if (need <= 128) return launch<TA, TB, kGate, 128, 1, kWhole>(p, bw, s);
   if (need <= 256) return launch<TA, TB, kGate, 256, 1, kWhole>(p, bw, s);
   if (need <= 512) return launch<TA, TB, kGate, 256, 2, kWhole>(p, bw, s);
-  return launch<TA, TB, kGate, 256, 4, kWhole>(p, bw, s);
+  return bw ? backward<TA, TB, kGate, 1024, 1, kWhole>(p, s) : forward<TA, TB, kGate, 256, 4, kWhole>(p, s);
 }
 template <typename TA, typename TB, bool kGate>
 cudaError_t whole(const Args& p, bool bw, cudaStream_t s) {
