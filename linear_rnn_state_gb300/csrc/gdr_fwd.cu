@@ -22,9 +22,8 @@
 // issue the products, one fills the chunk's images.
 // kSave: the images of S0 and u go to memory for the backward.
 //
-// Arithmetic: fp16 pairs in everything that the states depend on. o of
-// bfloat16 calls takes S0, u and P with their hi part alone (11 bits against
-// the 8 that o is rounded to: 0.0003 of o's error of 0.0017).
+// Arithmetic: fp16 pairs in every product, those of o too: a bfloat16 o is an
+// fp32 result rounded once.
 //
 // Measured (64 steps; time, traffic): 4 x 4096 x 32 heads of 64 bfloat16 127 us,
 // 4.2 TB/s; 8 x 4096 x 12 x 64 fp32 160 us, 3.6 TB/s; 2 x 4095 x 32 x 128 bfloat16
@@ -52,7 +51,7 @@ struct alignas(1024) FwdSmem {
     __half u[2 * kVt * kC];  // and of u
     unsigned char o[kRowsBytes<T>];
   } out[kWarps];
-  __half t[2 * kTriPart], p[P * kTriPart];
+  __half t[2 * kTriPart], p[2 * kTriPart];
   unsigned char v[kWarps][kPlaces][kRowsBytes<T>];
   unsigned char scal[2][kChainScal];
   float most[3][kWarps][2];  // of the chain warps' S, r and u
@@ -92,13 +91,13 @@ __device__ __forceinline__ void fill(FwdSmem<T, KP, kSave>& m, const Args& a, lo
   };
   auto q = [&](int c) { one(m.q, a.b.q_img + at_k(c) * image, image, &m.full_q); };
   auto t = [&](int c) { one(m.t, a.b.t_img + at_v(c) * Layout::tp_img, 2 * tri, &m.full_t); };
-  auto p = [&](int c) { one(m.p, a.b.p_img + at_v(c) * Layout::tp_img, P * tri, &m.full_p); };
+  auto p = [&](int c) { one(m.p, a.b.p_img + at_v(c) * Layout::tp_img, 2 * tri, &m.full_p); };
   auto ask = [&](int c) {  // into L2
     if (c >= n) return;
     bulk_prefetch(a.b.k_img + at_k(c) * image, image);
     bulk_prefetch(a.b.q_img + at_k(c) * image, image);
     bulk_prefetch(a.b.t_img + at_v(c) * Layout::tp_img, 2 * tri);
-    bulk_prefetch(a.b.p_img + at_v(c) * Layout::tp_img, P * tri);
+    bulk_prefetch(a.b.p_img + at_v(c) * Layout::tp_img, 2 * tri);
     bulk_prefetch(a.b.scal + at_v(c), kChainScal);
   };
   k(0), t(0), q(0), p(0);
@@ -173,7 +172,7 @@ __global__ void __launch_bounds__(kThreads, 1) fwd_kernel(const Args a) {
       }
       wait(&sm.full_q, use);
       if (elected()) {
-        tc_rows<P, P, KP>(tmem + Col::q, tmem + Col::s_in, sm.q);
+        tc_rows<2, P, KP>(tmem + Col::q, tmem + Col::s_in, sm.q);
         tc_commit(&sm.done_q);
         tc_commit(&sm.free_q);
       }
@@ -203,7 +202,7 @@ __global__ void __launch_bounds__(kThreads, 1) fwd_kernel(const Args a) {
       wait(&sm.ready_u, use);
       tmem_fence_after_sync();
       if (elected()) {
-        tc_tri_rows<P, P>(tmem + Col::o, tmem + Col::u_in, sm.p);
+        tc_tri_rows<2, 2>(tmem + Col::o, tmem + Col::u_in, sm.p);
         tc_commit(&sm.done_o);
         tc_commit(&sm.free_p);
       }
@@ -359,7 +358,7 @@ __global__ void __launch_bounds__(kThreads, 1) fwd_kernel(const Args a) {
       tc_loaded(x);
       const float fu = sm.inv_r[own];
       const float sU = pow2_scale(warp_max(x)), inv_u = pow2_inverse(sU) * fu;
-      Operand<kSave ? 2 : P, 4> f;
+      Operand<2, 4> f;
       f.split(x, sU), f.store(mine + Col::u_in, 32);
       tc_stored();
       tmem_fence_before_sync();

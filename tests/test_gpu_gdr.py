@@ -387,6 +387,34 @@ def test_a_sequence_cut_in_two(env):
         _close(name, x, y.double().cpu().numpy())
 
 
+# ------------------------------------------------ roundings, gates, magnitudes ---
+
+
+def _close_rounded(name, got, ref):
+    """A bfloat16 output against its reference rounded to bfloat16. An fp32 result
+    that is off by e is rounded to another neighbour with a probability of 2 |e| / ulp
+    and then differs by one ulp, at most 2^-7 |x|: the squares sum up to 2^-6 sum |e x|,
+    at most 2^-6 |e| |x| in 2-norms. With fp32's bar, 4e-6: 2.5e-4 of the norm."""
+    want = torch.from_numpy(ref).to(BF16).double().numpy()
+    off = np.linalg.norm(got.double().cpu().numpy() - want) / np.linalg.norm(want)
+    assert off <= 2.5e-4, f"{name}: {off:.2e} from the rounded reference"
+
+
+@pytest.mark.parametrize("K,V", [(64, 64), (128, 128), (40, 24)])
+def test_bfloat16_outputs_are_fp32_results_rounded_once(env, K, V):
+    orc, gdr = env
+    d = _make(2, 300, 2, 4, K, V, BF16, 30, l2norm=True, rate=0.3)
+    o, s, saved = gdr.forward(*(d[n] for n in INS), d["s_init"], qk_l2norm=True)
+    o2, _, _ = gdr.forward(*(d[n] for n in INS), d["s_init"], qk_l2norm=True, want_saved=False)
+    g = gdr.backward(*(d[n] for n in INS), d["do"], saved, dS_final=d["dS_final"], qk_l2norm=True)
+    h = _np(d)
+    o_ref, _ = orc.forward(*(h[n] for n in INS), h["s_init"], l2norm=True)
+    ref = orc.backward(*(h[n] for n in INS), h["do"], h["s_init"], h["dS_final"], l2norm=True)
+    _close_rounded("o", o, o_ref), _close_rounded("o without saved", o2, o_ref)
+    for n in ("dq", "dk", "dv"):
+        _close_rounded(n, g[n], ref[n])
+
+
 # ------------------------------------------------------------------------- step ---
 
 
