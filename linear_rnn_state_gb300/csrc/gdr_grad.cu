@@ -236,9 +236,10 @@ __global__ void __launch_bounds__(kThreads<KP>, KP == 64 ? 2 : 1) grad_kernel(co
   // F and E with their decays and factors; the diagonal of F apart. Images hold
   // magnitudes below 2^14, so |do.u| and |lam.u| are below 16 2^28 times the sum
   // of their tiles' inverse scales: a bound for the scales, with no maximum to
-  // wait for (loose by some 2^6).
-  const float scale[4] = {pow2_scale(sc.fb_max * (du * 0x1p32f)), pow2_scale(sc.eb_max * (lu * 0x1p32f)),
-                          pow2_scale(sc.f_max * (du * 0x1p32f)), pow2_scale(sc.e_max * (lu * 0x1p32f))};
+  // wait for (loose by some 2^6). Not below 2^-100, so that a factor times its scale
+  // stays finite where F or E is 0.
+  const float fm = fmaxf(sc.sr_max * (du * 0x1p32f), 0x1p-100f), em = fmaxf(sc.r_max * (lu * 0x1p32f), 0x1p-100f);
+  const float scale[4] = {pow2_scale(sc.bk_max * fm), pow2_scale(sc.bk_max * em), pow2_scale(sc.q_max * fm), pow2_scale(sc.k_max * em)};
   const int i0 = 16 * wr + g4;
   sdot = wkv7::group_allreduce<32>(sdot);
   if (lane == 0) sm.sdot[warp] = sdot;

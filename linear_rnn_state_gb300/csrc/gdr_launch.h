@@ -57,9 +57,10 @@ struct Scal {
   float inv_t, inv_p;  // the inverse scales of the T and P images
   float egc;           // e^Gc
   float near;          // 1: G spans at most kNear in the chunk, and fa, fb hold
-  float f_max, e_max;  // bounds of |F|, |E| and their factors over |do.u|, |lam.u| (gdr_grad.cu)
-  float fb_max, eb_max;
-  float pad[24];
+  // bounds for the gradients' operands (gdr_grad.cu): of r_ij, j <= i, and |scale|
+  // times it; of |beta ks|, qs and ks
+  float r_max, sr_max, bk_max, q_max, k_max;
+  float pad[23];
   // up to here for the chains, from here on for the gradients
   float eg[kC];          // e^G
   float gh[kC], gl[kC];  // G as an unrounded sum of two floats

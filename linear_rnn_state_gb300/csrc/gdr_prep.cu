@@ -290,11 +290,11 @@ __global__ void __launch_bounds__(kThreads, kBlocks<T, KP>) prep_kernel(const Ar
       // the largest e^(G_i - G_j), j <= i, is 1 unless some g is positive
       const bool grows = __any_sync(0xffffffffu, x[0] > 0 || x[1] > 0);
       if (lane == 31) {
-        const float r = grows ? expf(top - low) : 1.f, sr = fabsf(a.s.scale) * r;
+        const float r = grows ? expf(top - low) : 1.f;
         Scal& o = sm.scal;
         o.egc = expf(Gc.h) * (1.f + Gc.l);
         o.near = top - low <= kNear ? 1.f : 0.f;
-        o.fb_max = sr * bk, o.eb_max = r * bk, o.f_max = sr * qm, o.e_max = r * km;
+        o.r_max = r, o.sr_max = fabsf(a.s.scale) * r, o.bk_max = bk, o.q_max = qm, o.k_max = km;
       }
     }
     __syncthreads();

@@ -415,6 +415,19 @@ def test_bfloat16_outputs_are_fp32_results_rounded_once(env, K, V):
         _close_rounded(n, g[n], ref[n])
 
 
+@pytest.mark.parametrize("T", [1, 90])
+def test_nothing_to_learn_from_large_queries(env, T):
+    """No values, no state and no gradient beside queries of 1e9: all gradients are 0."""
+    orc, gdr = env
+    d = _make(1, T, 1, 2, 64, 64, F32, 34)
+    d["q"] *= 1e9
+    d["v"][:], d["do"][:] = 0, 0
+    o, s, saved = gdr.forward(*(d[n] for n in INS))
+    grads = gdr.backward(*(d[n] for n in INS), d["do"], saved)
+    assert torch.count_nonzero(o) == 0 and torch.count_nonzero(s) == 0
+    assert all(torch.count_nonzero(x) == 0 for x in grads.values())
+
+
 # ------------------------------------------------------------------------- step ---
 
 
