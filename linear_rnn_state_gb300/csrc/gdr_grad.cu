@@ -76,6 +76,7 @@ struct alignas(128) GradSmem {
   float fd[kC];               // f_i
   float dot[4][KP / 32][kC];  // row sums of 32 keys each: q.dq, k.read, k.w, k.(e^(Gc - G) u dS1)
   float sdot[KP / 8];
+  float4 most[KP / 8];        // the warps' largest values of the four pairs
   uint64_t bar[kStages], bar_k, bar_s;
 };
 
@@ -162,7 +163,7 @@ __global__ void __launch_bounds__(kThreads<KP>, KP == 64 ? 2 : 1) grad_kernel(co
   const int key0 = wc * 32;
   float dq[kNt][4], rd[kNt][4], w[kNt][4], F[2 * kNf][4], E[2 * kNf][4];
   zero(dq), zero(rd), zero(w), zero(F), zero(E);
-  float sdot = 0.f, du = 0.f, lu = 0.f;
+  float sdot = 0.f;
   for (int v = 0; v < vts; ++v) {
     const int n = hg * vts + v;
     Tile<P, KP>& t = tiles[n % kStages];
@@ -228,23 +229,19 @@ __global__ void __launch_bounds__(kThreads<KP>, KP == 64 ? 2 : 1) grad_kernel(co
       __syncthreads();
       if (tid == 0) load(n + kStages);
     }
-    du += dsl.z * su.y, lu += dsl.y * su.y;
   }
   if (!mbar_wait_bounded(a.status, &sm.bar_k, 0)) return;
   if (!mbar_wait_bounded(a.status, &sm.bar_s, hg & 1)) return;
 
-  // F and E with their decays and factors; the diagonal of F apart. Images hold
-  // magnitudes below 2^14, so |do.u| and |lam.u| are below 16 2^28 times the sum
-  // of their tiles' inverse scales: a bound for the scales, with no maximum to
-  // wait for (loose by some 2^6). Not below 2^-100, so that a factor times its scale
-  // stays finite where F or E is 0.
-  const float fm = fmaxf(sc.sr_max * (du * 0x1p32f), 0x1p-100f), em = fmaxf(sc.r_max * (lu * 0x1p32f), 0x1p-100f);
-  const float scale[4] = {pow2_scale(sc.bk_max * fm), pow2_scale(sc.bk_max * em), pow2_scale(sc.q_max * fm), pow2_scale(sc.k_max * em)};
+  // F and E with their decays, the diagonal of F apart, and the largest value of
+  // each of the four operands that they become. (A bound by the largest decay ratio,
+  // do, lam and u has no maximum to wait for and saved 4 to 6 % of a backward. But
+  // these may belong to different tokens; then it is loose without limit, and pairs
+  // at its scale lose bits, or all.)
   const int i0 = 16 * wr + g4;
   sdot = wkv7::group_allreduce<32>(sdot);
-  if (lane == 0) sm.sdot[warp] = sdot;
-  __syncthreads();  // the tiles are used up
   const bool near = sc.near != 0.f;
+  float m[4] = {0.f, 0.f, 0.f, 0.f};
 #pragma unroll
   for (int n = 0; n < 2 * kNf; ++n) {
     const int jb = kNf * wc + n / 2;
@@ -267,11 +264,35 @@ __global__ void __launch_bounds__(kThreads<KP>, KP == 64 ? 2 : 1) grad_kernel(co
         if (j + 1 == i) sm.fd[i] = a.s.scale * F[n][2 * h + 1];
         x0 = j < i ? x0 : 0.f, x1 = j + 1 < i ? x1 : 0.f, y0 = j < i ? y0 : 0.f, y1 = j + 1 < i ? y1 : 0.f;
       }
-      const float q = rows.qs[i] * scale[2], k = rows.ks[i] * scale[3];
-      put2_tri(pairs.fb, i, j, x0 * (c0 * scale[0]), x1 * (c1 * scale[0]));
-      put2_tri(pairs.eb, i, j, y0 * (c0 * scale[1]), y1 * (c1 * scale[1]));
-      put2_tri(pairs.f, i, j, x0 * q, x1 * q);
-      put2_tri(pairs.e, i, j, y0 * k, y1 * k);
+      F[n][2 * h] = x0, F[n][2 * h + 1] = x1, E[n][2 * h] = y0, E[n][2 * h + 1] = y1;
+      m[0] = fmaxf(m[0], fmaxf(fabsf(x0 * c0), fabsf(x1 * c1))), m[1] = fmaxf(m[1], fmaxf(fabsf(y0 * c0), fabsf(y1 * c1)));
+      m[2] = fmaxf(m[2], fmaxf(fabsf(x0), fabsf(x1)) * rows.qs[i]), m[3] = fmaxf(m[3], fmaxf(fabsf(y0), fabsf(y1)) * rows.ks[i]);
+    }
+  }
+#pragma unroll
+  for (int p = 0; p < 4; ++p) m[p] = warp_max_abs(m[p]);
+  if (lane == 0) sm.sdot[warp] = sdot, sm.most[warp] = make_float4(m[0], m[1], m[2], m[3]);
+  __syncthreads();  // and the tiles are used up
+#pragma unroll
+  for (int w = 0; w < KP / 8; ++w) {
+    const float4 x = sm.most[w];
+    m[0] = fmaxf(m[0], x.x), m[1] = fmaxf(m[1], x.y), m[2] = fmaxf(m[2], x.z), m[3] = fmaxf(m[3], x.w);
+  }
+  const float scale[4] = {pow2_scale(m[0]), pow2_scale(m[1]), pow2_scale(m[2]), pow2_scale(m[3])};
+#pragma unroll
+  for (int n = 0; n < 2 * kNf; ++n) {
+    if (kNf * wc + n / 2 > wr) continue;
+    const int j = 16 * kNf * wc + 8 * n + 2 * t4;
+    const float c0 = sc.beta[j] * rows.ks[j], c1 = sc.beta[j + 1] * rows.ks[j + 1];
+#pragma unroll
+    for (int h = 0; h < 2; ++h) {
+      const int i = i0 + 8 * h;
+      const float q = rows.qs[i], k = rows.ks[i], x0 = F[n][2 * h], x1 = F[n][2 * h + 1], y0 = E[n][2 * h], y1 = E[n][2 * h + 1];
+      // the factor first: with its scale it may pass fp32
+      put2_tri(pairs.fb, i, j, x0 * c0 * scale[0], x1 * c1 * scale[0]);
+      put2_tri(pairs.eb, i, j, y0 * c0 * scale[1], y1 * c1 * scale[1]);
+      put2_tri(pairs.f, i, j, x0 * q * scale[2], x1 * q * scale[2]);
+      put2_tri(pairs.e, i, j, y0 * k * scale[3], y1 * k * scale[3]);
     }
   }
   __syncthreads();

@@ -57,10 +57,7 @@ struct Scal {
   float inv_t, inv_p;  // the inverse scales of the T and P images
   float egc;           // e^Gc
   float near;          // 1: G spans at most kNear in the chunk, and fa, fb hold
-  // bounds for the gradients' operands (gdr_grad.cu): of r_ij, j <= i, and |scale|
-  // times it; of |beta ks|, qs and ks
-  float r_max, sr_max, bk_max, q_max, k_max;
-  float pad[23];
+  float pad[28];
   // up to here for the chains, from here on for the gradients
   float eg[kC];          // e^G
   float gh[kC], gl[kC];  // G as an unrounded sum of two floats

@@ -272,7 +272,6 @@ __global__ void __launch_bounds__(kThreads, kBlocks<T, KP>) prep_kernel(const Ar
         low = fminf(low, __shfl_xor_sync(0xffffffffu, low, o));
       }
       const float mid = 0.5f * (top + low);
-      float bk = 0.f, qm = 0.f, km = 0.f;
 #pragma unroll
       for (int e = 0; e < 2; ++e) {
         const int i = 2 * lane + e;
@@ -284,17 +283,10 @@ __global__ void __launch_bounds__(kThreads, kBlocks<T, KP>) prep_kernel(const Ar
         o.beta[i] = b, o.gh[i] = G[e].h, o.gl[i] = G[e].l, o.eg[i] = eg, o.fa[i] = fa, o.fb[i] = fb;
         o.ek[i] = eg * ks, o.wk[i] = w * ks, o.eq[i] = a.s.scale * eg * qs;
         sm.pa[i] = a.s.scale * qs * fa, sm.la[i] = ks * fa, sm.cb[i] = b * ks * fb;
-        bk = abs_max(bk, b * ks), qm = abs_max(qm, qs), km = abs_max(km, ks);
       }
-      bk = warp_max_abs(bk), qm = warp_max_abs(qm), km = warp_max_abs(km);
-      // the largest e^(G_i - G_j), j <= i, is 1 unless some g is positive
-      const bool grows = __any_sync(0xffffffffu, x[0] > 0 || x[1] > 0);
       if (lane == 31) {
-        const float r = grows ? expf(top - low) : 1.f;
-        Scal& o = sm.scal;
-        o.egc = expf(Gc.h) * (1.f + Gc.l);
-        o.near = top - low <= kNear ? 1.f : 0.f;
-        o.r_max = r, o.sr_max = fabsf(a.s.scale) * r, o.bk_max = bk, o.q_max = qm, o.k_max = km;
+        sm.scal.egc = expf(Gc.h) * (1.f + Gc.l);
+        sm.scal.near = top - low <= kNear ? 1.f : 0.f;
       }
     }
     __syncthreads();

@@ -415,6 +415,49 @@ def test_bfloat16_outputs_are_fp32_results_rounded_once(env, K, V):
         _close_rounded(n, g[n], ref[n])
 
 
+@pytest.mark.parametrize("dtype", [BF16, F32], ids=["bf16", "f32"])
+@pytest.mark.parametrize("up", [1e-3, 0.5])
+@pytest.mark.parametrize("rate", [0.3, 0.5, 3.0])
+def test_growth_among_decays(env, rate, up, dtype):
+    """Single tokens with g > 0: what grows from a token to a later one, not the
+    chunk's whole span of decays, bounds the gradients' factors."""
+    d = _make(1, 150, 1, 2, 64, 64, dtype, 31, rate=rate)
+    d["g"][:, ::13] = up
+    _check(env, d)
+
+
+@pytest.mark.parametrize("size", [0.5, 1.0])
+@pytest.mark.parametrize("Hk,Hv,K,dtype", [(1, 2, 64, BF16), (2, 2, 128, F32)])
+def test_gates_of_both_signs(env, Hk, Hv, K, dtype, size):
+    d = _make(1, 150, Hk, Hv, K, 64, dtype, 32)
+    d["g"] = size * torch.randn(d["g"].shape, device="cuda", generator=torch.Generator("cuda").manual_seed(32))
+    _check(env, d)
+
+
+@pytest.mark.parametrize("dtype", [BF16, F32], ids=["bf16", "f32"])
+def test_large_gradients_before_large_values(env, dtype):
+    """Of a chunk's tokens the first have large gradients and the last large values, which never meet."""
+    d = _make(1, 128, 1, 2, 64, 64, dtype, 40, rate=0.1)
+    d["do"][:, :32] *= 1e4
+    d["v"][:, 32:64] *= 1e4
+    _check(env, d)
+
+
+def test_a_reset_beside_growth(env):
+    orc, gdr = env
+    d = _make(1, 100, 1, 2, 64, 64, F32, 33, rate=0.1)
+    d["g"][:, 20], d["g"][:, 30], d["g"][:, 70] = -torch.inf, 0.01, 0.01
+    o, s, saved = gdr.forward(*(d[n] for n in INS), d["s_init"])
+    grads = gdr.backward(*(d[n] for n in INS), d["do"], saved, dS_final=d["dS_final"])
+    h = _np(d)
+    h["g"][np.isinf(h["g"])] = -1e3
+    o_ref, s_ref = orc.forward(*(h[n] for n in INS), h["s_init"])
+    _close("o", o, o_ref), _close("s_final", s, s_ref)
+    ref = orc.backward(*(h[n] for n in INS), h["do"], h["s_init"], h["dS_final"])
+    for n in ("dq", "dk", "dv", "dg", "dbeta", "dS_init"):
+        _close(n, grads[n], ref[n])
+
+
 @pytest.mark.parametrize("T", [1, 90])
 def test_nothing_to_learn_from_large_queries(env, T):
     """No values, no state and no gradient beside queries of 1e9: all gradients are 0."""
