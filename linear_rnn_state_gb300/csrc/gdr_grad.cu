@@ -116,8 +116,10 @@ __global__ void __launch_bounds__(kThreads<KP>, KP == 64 ? 2 : 1) grad_kernel(co
   const int hv0 = blockIdx.x % per_slot * heads, hk = hv0 / group;
   ChunkAt c;
   if (a.small) grid_go();
+  // in segments begun beside the chain of the segment before, of which nothing is read; elsewhere
+  // every block waits for the chain, those without a chunk too: this kernel's end is the chain's
+  if (!a.segn) grid_wait();
   if (!chunk_at(a.s, slot, c)) return;
-  if (!a.segn) grid_wait();  // else begun beside the chain of the segment before, of which nothing is read
   const int vts = (a.s.V + kVt - 1) / kVt, K = a.s.K;
   const size_t at_k = (size_t)slot * a.s.Hk + hk, at_v0 = (size_t)slot * a.s.Hv + hv0;
   constexpr int image = P * kC * KP * 2;

@@ -471,6 +471,25 @@ def test_nothing_to_learn_from_large_queries(env, T):
     assert all(torch.count_nonzero(x) == 0 for x in grads.values())
 
 
+# ---------------------------------------------- shared heads, segments, starts ---
+
+
+@pytest.mark.parametrize("starts", [[0, 0], [30, 30, 30], [100, 100, 100, 100]])
+def test_packed_sequences_without_a_token(env, starts):
+    """Tokens there are, but the sequences have none: states and their gradients pass through,
+    and are there for what follows on the stream."""
+    _, gdr = env
+    n = len(starts) - 1
+    d = _make(1, 100, 1, 2, 64, 64, BF16, 41, states=n)
+    st = torch.tensor(starts, dtype=torch.int32, device="cuda")
+    for _ in range(5):
+        o, s, saved = gdr.forward(*(d[m] for m in INS), d["s_init"], seq_starts=st)
+        grads = gdr.backward(*(d[m] for m in INS), d["do"], saved, dS_final=d["dS_final"], seq_starts=st)
+        after = s + 1, grads["dS_init"] + 1
+        assert torch.equal(after[0], d["s_init"] + 1) and torch.equal(after[1], d["dS_final"] + 1)
+    gdr.wkv7.status()
+
+
 # ------------------------------------------------------------------------- step ---
 
 
