@@ -27,8 +27,9 @@
  * Packed sequences: with seq_starts (device int32 [nseq + 1]) B is 1 and
  * sequence s has the tokens seq_starts[s] .. seq_starts[s+1] - 1 of the one
  * batch row, from its own state; it may be empty. The numbers must not
- * decrease and should run from 0 to T (they are clamped into [0, T]; a token
- * that belongs to no sequence gets no output). Without it nseq is not read.
+ * decrease (they are clamped into [0, T]); where they do not run from 0 to T, o
+ * and the gradients of the tokens before and behind are 0, so that a batch may be
+ * padded to a fixed size. Without it nseq is not read.
  *
  * Chunks. The forward and backward work on chunks of 64 tokens: what a chunk
  * needs beyond the state (the inverse of its key Gram matrix, its decays) for

@@ -1,6 +1,7 @@
 // C ABI of the gated delta rule (gdr.h): argument checks, the regions of the
 // caller's buffers, and the launches.
 #include <algorithm>
+#include <initializer_list>
 
 #include "api_check.h"
 #include "gdr.h"
@@ -61,6 +62,15 @@ int set_shape(Shape& s, int B, int T, int Hk, int Hv, int K, int V, int nseq) {
 }
 
 size_t align128(size_t x) { return (x + 127) & ~(size_t)127; }
+
+// Packed, but no sequence at all: outputs of tokens are 0.
+int zero_tokens(std::initializer_list<Span> outs, cudaStream_t stream) {
+  for (const Span& x : outs) {
+    const cudaError_t e = x.bytes ? cudaMemsetAsync(const_cast<void*>(x.p), 0, x.bytes, stream) : cudaSuccess;
+    if (e != cudaSuccess) return fail(WKV7_ERR_CUDA, "%s: %s", x.name, cudaGetErrorString(e));
+  }
+  return WKV7_OK;
+}
 
 // The regions of `saved` from p on; returns the bytes.
 size_t place_saved(Buffers& b, const Shape& s, bool bf16, bool for_backward, char* p) {
@@ -130,7 +140,8 @@ int forward_impl(bool bf16, const void* q, const void* k, const void* v, const f
                        {starts, starts ? ((unsigned long long)nseq + 1) * 4 : 0, "seq_starts", false, 4}};
   const Span outs[3] = {{o, rows * V * es, "o", true}, {s_final, state, "s_final", false}, {saved, rows ? need : 0, "saved", true}};
   if ((rc = api::check_spans(ins, outs))) return rc;
-  if (!Hv || !a.s.nseq) return WKV7_OK;
+  if (!Hv) return WKV7_OK;
+  if (!a.s.nseq) return zero_tokens({outs[0]}, stream);
   if (!rows) return copy_state(s_final, s_init, state, stream);
   a.s.starts = starts;
   a.s.l2norm = l2norm, a.s.scale = scale;
@@ -149,6 +160,10 @@ int forward_impl(bool bf16, const void* q, const void* k, const void* v, const f
     if ((rc = launched(launch_prep(a, bf16, stream), "chunk preparation"))) return rc;
     if ((rc = launched(launch_fwd(a, bf16, for_backward, stream), "forward"))) return rc;
     if (parts == 1) break;
+  }
+  if (a.s.packed) {
+    const Gaps gaps{{static_cast<uint32_t*>(o)}, {(long long)Hv * V * es / 4}};
+    return launched(launch_gaps(a, gaps, stream), "gaps");
   }
   return WKV7_OK;
 }
@@ -179,7 +194,8 @@ int backward_impl(bool bf16, const void* q, const void* k, const void* v, const 
                         {dg, rows * 4, "dg", true, 4}, {dbeta, rows * 4, "dbeta", true, 4}, {dS_init, state, "dS_init", false},
                         {workspace, rows ? need : 0, "workspace", true}};
   if ((rc = api::check_spans(ins, outs))) return rc;
-  if (!Hv || !a.s.nseq) return WKV7_OK;
+  if (!Hv) return WKV7_OK;
+  if (!a.s.nseq) return zero_tokens({outs[0], outs[1], outs[2], outs[3], outs[4]}, stream);
   if (!rows) return copy_state(dS_init, dS_final, state, stream);
   a.s.starts = starts;
   a.s.l2norm = l2norm, a.s.scale = scale;
@@ -192,7 +208,11 @@ int backward_impl(bool bf16, const void* q, const void* k, const void* v, const 
   if (parts > 1) a.small = 0;
   if (parts == 1) {
     if ((rc = launched(launch_bwd(a, bf16, stream), "backward"))) return rc;
-    return launched(launch_grad(a, bf16, stream), "gradients");
+    if ((rc = launched(launch_grad(a, bf16, stream), "gradients")) || !a.s.packed) return rc;
+    auto words = [](void* p) { return static_cast<uint32_t*>(p); };
+    const long long wk = (long long)Hk * K * es / 4, wv = (long long)Hv * V * es / 4;
+    const Gaps gaps{{words(dq), words(dk), words(dv), words(dg), words(dbeta)}, {wk, wk, wv, Hv, Hv}};
+    return launched(launch_gaps(a, gaps, stream), "gaps");
   }
   // from the last segment to the first: the chain of one, then the gradients of the one after it beside that chain
   if (!dS_init) a.dS_init = a.b.carry_back;

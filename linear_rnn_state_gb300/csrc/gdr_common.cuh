@@ -328,6 +328,11 @@ __device__ __forceinline__ SeqRange seq_range(const Shape& a, int s) {
   }
   return r;
 }
+// Of a packed call: the tokens that sequences cover, of the first's start to the
+// last's end; those before and behind lie in none.
+__device__ __forceinline__ int2 covered(const Shape& a) {
+  return make_int2(seq_range(a, 0).t0, seq_range(a, a.nseq - 1).t1);
+}
 struct ChunkAt {
   int b, t0, len;
   bool last;  // the sequence's last chunk

@@ -494,8 +494,15 @@ __global__ void __launch_bounds__(256) join_kernel(const Args a) {
   const int cl = threadIdx.x & 15, group = a.s.Hv / a.s.Hk, K = a.s.K;
   const bool is_k = id >= rows, in = id < 2 * rows && cl * 8 < K;
   const size_t row = is_k ? id - rows : id;
+  // tokens in no sequence have no terms
+  bool none = false;
+  if (a.s.packed && in) {
+    const int2 some = covered(a.s);
+    const int t = (int)(row / a.s.Hk);
+    none = t < some.x || t >= some.y;
+  }
   float d[8] = {0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f}, x[8] = {0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f};
-  if (in) {
+  if (in && !none) {
     const float* part = (is_k ? a.b.dk_part : a.b.dq_part) + row * group * K + cl * 8;
     for (int g = 0; g < group; ++g) {
       float y[8];
@@ -517,7 +524,7 @@ __global__ void __launch_bounds__(256) join_kernel(const Args a) {
 #pragma unroll
     for (int e = 0; e < 8; ++e) d[e] = r * fmaf(-f, x[e], d[e]);
   }
-  if (in) {
+  if (in && !none) {
     T* out = static_cast<T*>(is_k ? a.dk : a.dq) + row * K + cl * 8;
     store8(out, d);
   }

@@ -148,6 +148,13 @@ cudaError_t launch_prep(const Args& a, bool bf16, cudaStream_t stream);
 cudaError_t launch_fwd(const Args& a, bool bf16, bool save, cudaStream_t stream);
 cudaError_t launch_bwd(const Args& a, bool bf16, cudaStream_t stream);
 cudaError_t launch_grad(const Args& a, bool bf16, cudaStream_t stream);
+// Zeros in up to five outputs of a packed call at the tokens of no sequence; after
+// its other kernels.
+struct Gaps {
+  uint32_t* at[5];
+  long long words[5];  // of a token
+};
+cudaError_t launch_gaps(const Args& a, const Gaps& g, cudaStream_t stream);
 
 // Allows a kernel its dynamic shared memory, once a device; `done` belongs to the kernel.
 inline cudaError_t allow_smem(const void* kernel, size_t bytes, std::atomic<unsigned long long>& done) {

@@ -481,6 +481,21 @@ __global__ void __launch_bounds__(kThreads, kBlocks<T, KP>) prep_kernel(const Ar
   if (a.seg0 && blockIdx.x == 0) grid_wait();
 }
 
+// Zeros where no sequence is, contiguous in each output: before the first and behind
+// the last. (In warps of the chains that have nothing else to do it took no launch,
+// 2 us of a packed call, but code between theirs: 5 % of every backward chain.)
+__global__ void __launch_bounds__(256) gaps_kernel(const Args a, const Gaps g) {
+  const int2 in = covered(a.s);
+  const long long first = (long long)blockIdx.x * 256 + threadIdx.x, step = (long long)gridDim.x * 256;
+#pragma unroll
+  for (int b = 0; b < 5; ++b) {
+    const long long w = g.words[b];
+    for (long long i = first; i < in.x * w; i += step) g.at[b][i] = 0;
+    for (long long i = in.y * w + first; i < a.s.T * w; i += step) g.at[b][i] = 0;
+  }
+  grid_wait();  // over only when the kernel before is
+}
+
 template <typename T, int KP, bool kOne>
 cudaError_t launch(const Args& a, cudaStream_t stream) {
   constexpr size_t smem = sizeof(PrepSmem<T, KP>);
@@ -497,6 +512,10 @@ cudaError_t launch(const Args& a, cudaStream_t stream) {
 }
 
 }  // namespace
+
+cudaError_t launch_gaps(const Args& a, const Gaps& g, cudaStream_t stream) {
+  return launch_after(true, gaps_kernel, 152u, 256u, 0, stream, a, g);
+}
 
 cudaError_t launch_prep(const Args& a, bool bf16, cudaStream_t stream) {
   const bool wide = padded_k(a.s.K) == 128;

@@ -179,7 +179,8 @@ def forward(q, k, v, g, beta, s_init=None, *, scale: float | None = None, qk_l2n
             want_saved: bool = True, want_s_final: bool = True, stream=None):
     """The recurrence over whole sequences, in chunks. scale: K ** -0.5 unless
     given. qk_l2norm divides q and k by their lengths. seq_starts (int32,
-    one more than the sequences; B = 1) gives packed sequences' starts.
+    one more than the sequences; B = 1) gives packed sequences' starts; tokens
+    before the first and from the last on have outputs and gradients of 0.
     Returns (o, s_final, saved); saved is what ``backward`` needs (None
     without want_saved)."""
     if stream is not None:

@@ -490,6 +490,60 @@ def test_packed_sequences_without_a_token(env, starts):
     gdr.wkv7.status()
 
 
+@pytest.mark.parametrize("dtype,Hk,Hv,K,T,starts", [
+    (BF16, 1, 2, 64, 100, [0, 40, 70]),
+    (F32, 2, 2, 72, 333, [10, 40, 40, 70]),
+    (BF16, 2, 4, 128, 6000, [70, 5100]),  # 80 chunks of two key heads: summed in the block
+    (F32, 2, 4, 64, 200, [3, 3, 130, 199]),
+    (BF16, 1, 2, 64, 90, [50]),  # no sequence at all
+    (BF16, 1, 3, 64, 90, [50, 50]),
+])
+def test_tokens_of_no_sequence(env, dtype, Hk, Hv, K, T, starts):
+    """Before the first start and from the last on: o and the gradients are 0 there,
+    whatever the buffers held, and the others' are those of the tokens alone."""
+    _, gdr = env
+    n, V = len(starts) - 1, 80
+    d = _make(1, T, Hk, Hv, K, V, dtype, 39, states=n, l2norm=True)
+    out = _raw(gdr, d, starts)
+    a, b = starts[0], starts[-1]
+    cut = {m: x if m in ("s_init", "dS_final") else x[:, a:b].contiguous() for m, x in d.items()}
+    want = _raw(gdr, cut, [x - a for x in starts])
+    for m, x in out.items():
+        if m in ("s_final", "dS_init"):
+            assert torch.equal(x, want[m]), m
+        else:
+            assert torch.equal(x[:, a:b], want[m]), m
+            assert torch.count_nonzero(x[:, :a]) == 0 and torch.count_nonzero(x[:, b:]) == 0, m
+
+
+def _raw(gdr, d, starts):
+    """Forward and backward by the C functions, into buffers that hold NaN before."""
+    lib = gdr.load()
+    q, v = d["q"], d["v"]
+    (B, T, Hk, K), (Hv, V), n, bf16 = q.shape, v.shape[2:], len(starts) - 1, q.dtype == BF16
+    st = torch.tensor(starts, dtype=torch.int32, device="cuda")
+
+    def nan(*shape, dtype=F32):
+        return torch.full(shape, float("nan"), dtype=dtype, device="cuda")
+
+    def junk(size):
+        return torch.full((size,), 255, dtype=torch.uint8, device="cuda")
+
+    dims = (B, T, Hk, Hv, K, V, n)
+    saved, work = junk(gdr.saved_bytes(*dims, bf16=bf16, for_backward=True)), junk(lib.gdr_backward_bytes(*dims, bf16))
+    out = {"o": nan(B, T, Hv, V, dtype=q.dtype), "s_final": nan(n, Hv, V, K)}
+    stream, tail = torch.cuda.current_stream().cuda_stream, (None, 0.25, 1)
+    p = lambda *xs: [x.data_ptr() for x in xs]
+    fn, back = (lib.gdr_forward_bf16, lib.gdr_backward_bf16) if bf16 else (lib.gdr_forward, lib.gdr_backward)
+    ins = p(*(d[m] for m in INS))
+    assert fn(*ins, *p(d["s_init"], st, out["o"], out["s_final"], saved), *tail, 1, *dims, stream) == 0
+    g = {"dq": nan(*q.shape, dtype=q.dtype), "dk": nan(*q.shape, dtype=q.dtype), "dv": nan(*v.shape, dtype=q.dtype),
+         "dg": nan(B, T, Hv), "dbeta": nan(B, T, Hv), "dS_init": nan(n, Hv, V, K)}
+    assert back(*ins, *p(d["do"], d["dS_final"], st, saved, work, *g.values()), *tail, *dims, stream) == 0
+    gdr.wkv7.status()
+    return {**out, **g}
+
+
 # ------------------------------------------------------------------------- step ---
 
 
