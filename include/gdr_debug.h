@@ -1,0 +1,26 @@
+/*
+ * gdr_debug.h - an extra entry point of the debug build (libwkv7_debug.so,
+ * compiled with WKV7_DEBUG) for the gated delta rule. The product library does
+ * not export it. It exists to test WKV7_ERR_TIMEOUT of the gradients' kernel,
+ * whose waits in the debug build end after 1 ms instead of about 2 s.
+ */
+#ifndef GDR_DEBUG_H
+#define GDR_DEBUG_H
+
+#ifdef __cplusplus
+extern "C" {
+#endif
+
+/* tile > 0: from now on the gradients' kernel of gdr_backward issues no copy, and
+ * no expected byte count, for this one (counted from 1) of every block's tiles of
+ * 16 value columns, so that the wait for it runs out; the call returns WKV7_OK, its
+ * gradients of q, k, g and beta are without meaning and the next wkv7_status()
+ * returns WKV7_ERR_TIMEOUT. tile = 0 restores normal operation. Process-wide;
+ * returns WKV7_OK. */
+int gdr_debug_skip_tile(int tile);
+
+#ifdef __cplusplus
+}
+#endif
+
+#endif /* GDR_DEBUG_H */

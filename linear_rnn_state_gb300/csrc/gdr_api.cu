@@ -3,6 +3,11 @@
 #include <algorithm>
 #include <initializer_list>
 
+#ifdef WKV7_DEBUG
+#include <atomic>
+#include "gdr_debug.h"
+#endif
+
 #include "api_check.h"
 #include "gdr.h"
 #include "gdr_launch.h"
@@ -14,6 +19,10 @@ using api::fail;
 using api::Span;
 
 constexpr unsigned long long kMaxBytes = 1ull << 46, kMaxBlocks = 1ull << 31;
+
+#ifdef WKV7_DEBUG
+std::atomic<int> g_debug_skip_tile{0};  // gdr_debug.h
+#endif
 
 int check_dims(int B, int T, int Hk, int Hv, int K, int V, const char* rows) {
   if (B < 0 || T < 0 || Hk < 0 || Hv < 0) return fail(WKV7_ERR_INVALID, "%s, T, Hk and Hv must be >= 0 (got %d, %d, %d, %d)", rows, B, T, Hk, Hv);
@@ -203,6 +212,9 @@ int backward_impl(bool bf16, const void* q, const void* k, const void* v, const 
   a.s.q_b = st[0], a.s.q_t = st[1], a.s.k_b = st[2], a.s.k_t = st[3], a.s.v_b = st[4], a.s.v_t = st[5];
   a.q = q, a.k = k, a.v = v, a.g = g, a.beta = beta, a.d_o = d_o, a.dS_final = dS_final;
   a.dq = dq, a.dk = dk, a.dv = dv, a.dg = dg, a.dbeta = dbeta, a.dS_init = dS_init;
+#ifdef WKV7_DEBUG
+  a.skip_tile = g_debug_skip_tile.load();
+#endif
   if ((rc = wkv7::api_status_word(&a.status))) return rc;
   const int parts = segments_of(a.s), chunks = (T + kC - 1) / kC, each = (chunks + parts - 1) / parts;
   if (parts > 1) a.small = 0;
@@ -256,6 +268,13 @@ int step_impl(bool bf16, const void* q, const void* k, const void* v, const floa
 }  // namespace gdr
 
 extern "C" {
+
+#ifdef WKV7_DEBUG
+int gdr_debug_skip_tile(int tile) {
+  gdr::g_debug_skip_tile.store(tile > 0 ? tile : 0);
+  return WKV7_OK;
+}
+#endif
 
 size_t gdr_saved_bytes(int B, int T, int Hk, int Hv, int K, int V, int nseq, int bf16, int for_backward) {
   gdr::Shape s;

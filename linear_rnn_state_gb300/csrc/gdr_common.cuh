@@ -290,6 +290,12 @@ __device__ __forceinline__ void bulk_prefetch(const void* src, uint32_t bytes) {
 __device__ __forceinline__ void mbar_arrive(uint64_t* bar) {
   asm volatile("mbarrier.arrive.shared::cta.b64 _, [%0];" ::"r"(smem_addr(bar)) : "memory");
 }
+// A thread that started copies, after it gave up: no copy is left in flight, either
+// phase of each barrier is waited for, for a millisecond at most.
+__device__ __forceinline__ void drain(uint64_t* bar) {
+  mbar_wait_bounded(nullptr, bar, 0, 1000000);
+  mbar_wait_bounded(nullptr, bar, 1, 1000000);
+}
 __device__ __forceinline__ void prefetch_l2(const void* p) { asm volatile("prefetch.global.L2 [%0];" ::"l"(p)); }
 template <int N>
 __device__ __forceinline__ float warp_max(const float (&x)[N][4]) {

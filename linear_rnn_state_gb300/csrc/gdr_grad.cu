@@ -127,6 +127,9 @@ __global__ void __launch_bounds__(kThreads<KP>, KP == 64 ? 2 : 1) grad_kernel(co
   // tile n of the block: of value head hv0 + n / vts; the heads' records follow one another
   const int n_tiles = heads * vts;
   auto load = [&](int n) {
+#ifdef WKV7_DEBUG
+    if (n + 1 == a.skip_tile) return;
+#endif
     Tile<P, KP>& t = tiles[n % kStages];
     uint64_t* bar = &sm.bar[n % kStages];
     constexpr uint32_t f = f_record(KP, P).size, b = b_record(KP, P).size;
@@ -159,6 +162,13 @@ __global__ void __launch_bounds__(kThreads<KP>, KP == 64 ? 2 : 1) grad_kernel(co
   const Scal& sc = sm.scal;
   const Rows& rows = sm.rows;
   const size_t tok = (size_t)c.b * a.s.T + c.t0;
+  // A wait that this thread gives up on once: from then on it goes on without waiting
+  // (all accesses are in bounds whatever the data), so that the block's barriers are
+  // kept and nobody leaves while copies are in flight.
+  bool ok = true;
+  auto wait = [&](uint64_t* bar, int parity) {
+    if (ok) ok = mbar_wait_bounded(a.status, bar, parity);
+  };
 
   for (int hg = 0; hg < heads; ++hg) {
   const int hv = hv0 + hg;
@@ -169,7 +179,7 @@ __global__ void __launch_bounds__(kThreads<KP>, KP == 64 ? 2 : 1) grad_kernel(co
   for (int v = 0; v < vts; ++v) {
     const int n = hg * vts + v;
     Tile<P, KP>& t = tiles[n % kStages];
-    if (!mbar_wait_bounded(a.status, &sm.bar[n % kStages], (n / kStages) & 1)) return;
+    wait(&sm.bar[n % kStages], (n / kStages) & 1);
     const float4 su = t.su, dsl = t.dsl;
     Frag<P> fd;
     Frag<2> fl, fu;
@@ -229,11 +239,11 @@ __global__ void __launch_bounds__(kThreads<KP>, KP == 64 ? 2 : 1) grad_kernel(co
     }
     if (n + kStages < n_tiles) {
       __syncthreads();
-      if (tid == 0) load(n + kStages);
+      if (tid == 0 && ok) load(n + kStages);
     }
   }
-  if (!mbar_wait_bounded(a.status, &sm.bar_k, 0)) return;
-  if (!mbar_wait_bounded(a.status, &sm.bar_s, hg & 1)) return;
+  wait(&sm.bar_k, 0);
+  wait(&sm.bar_s, hg & 1);
 
   // F and E with their decays, the diagonal of F apart, and the largest value of
   // each of the four operands that they become. (A bound by the largest decay ratio,
@@ -436,10 +446,14 @@ __global__ void __launch_bounds__(kThreads<KP>, KP == 64 ? 2 : 1) grad_kernel(co
     }
   if (kOut == kSum && hg + 1 < heads) {
     __syncthreads();  // warp 0 is past the scalars
-    if (tid == 0) load_scal(hg + 1);
+    if (tid == 0 && ok) load_scal(hg + 1);
   }
   }
   __syncthreads();
+  if (tid == 0 && !ok) {  // the thread that waits for every copy
+    for (uint64_t& b : sm.bar) drain(&b);
+    drain(&sm.bar_k), drain(&sm.bar_s);
+  }
 
   // eight keys a lane: the gradient of the normalisation, and out. fp32 rows by
   // halves, four keys of each, so that a store writes whole sectors (8 x 4096

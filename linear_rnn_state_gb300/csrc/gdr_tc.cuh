@@ -256,11 +256,4 @@ struct Patience {
   }
 };
 
-// The filling thread after it gave up: no copy is left in flight, either phase of
-// each barrier is waited for, for a millisecond at most.
-__device__ __forceinline__ void drain(uint64_t* bar) {
-  mbar_wait_bounded(nullptr, bar, 0, 1000000);
-  mbar_wait_bounded(nullptr, bar, 1, 1000000);
-}
-
 }  // namespace gdr
