@@ -1,8 +1,9 @@
 /*
- * gdr_debug.h - an extra entry point of the debug build (libwkv7_debug.so,
+ * gdr_debug.h - extra entry points of the debug build (libwkv7_debug.so,
  * compiled with WKV7_DEBUG) for the gated delta rule. The product library does
- * not export it. It exists to test WKV7_ERR_TIMEOUT of the gradients' kernel,
- * whose waits in the debug build end after 1 ms instead of about 2 s.
+ * not export them. They exist to test WKV7_ERR_TIMEOUT of the chains and of the
+ * gradients' kernel, whose waits in the debug build end after 1 ms instead of
+ * about 2 s.
  */
 #ifndef GDR_DEBUG_H
 #define GDR_DEBUG_H
@@ -18,6 +19,12 @@ extern "C" {
  * returns WKV7_ERR_TIMEOUT. tile = 0 restores normal operation. Process-wide;
  * returns WKV7_OK. */
 int gdr_debug_skip_tile(int tile);
+
+/* step > 0: from now on the chains of gdr_forward and gdr_backward issue no copy,
+ * and no expected byte count, of the image of T in this one (counted from 1) of
+ * their steps, a chunk each, of every sequence (or segment) that has it; otherwise as
+ * above. step = 0 restores normal operation. */
+int gdr_debug_skip_t(int step);
 
 #ifdef __cplusplus
 }

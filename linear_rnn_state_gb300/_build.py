@@ -7,8 +7,8 @@ both see the same current device).
 It also links the debug build, libwkv7_debug.so: the same objects, the C ABI
 and the WKV7 scan kernels recompiled with WKV7_DEBUG (every plain global load
 and store checked against its buffer, 1 ms mbarrier wait limit, and the hooks
-of include/wkv7_debug.h), and with it the gated delta rule's C ABI and gradients
-(1 ms and include/gdr_debug.h). Only the tests of those checks and of the timeout
+of include/wkv7_debug.h), and with it the gated delta rule's C ABI, chains and
+gradients (1 ms and include/gdr_debug.h). Only the tests of those checks and of the timeout
 paths load it.
 """
 from __future__ import annotations
@@ -26,7 +26,8 @@ BUILD_DIR = os.path.join(PKG, "_build")
 LIB = os.path.join(PKG, "libwkv7.so")
 DEBUG_LIB = os.path.join(PKG, "libwkv7_debug.so")
 DEBUG_SOURCES = ["wkv7_api.cu", "wkv7_fwd2.cu", "wkv7_fwd3.cu", "wkv7_bwd2.cu", "wkv7_bwd3.cu",
-                 "wkv7_bwd4.cu", "wkv7_bwd4_f32.cu", "gdr_api.cu", "gdr_grad.cu"]  # recompiled with -DWKV7_DEBUG for the debug build
+                 "wkv7_bwd4.cu", "wkv7_bwd4_f32.cu", "gdr_api.cu", "gdr_fwd.cu", "gdr_bwd.cu",
+                 "gdr_grad.cu"]  # recompiled with -DWKV7_DEBUG for the debug build
 
 SOURCES = ["wkv7_api.cu", "wkv7_fwd2.cu", "wkv7_fwd3.cu", "wkv7_bwd2.cu", "wkv7_bwd3.cu", "wkv7_bwd4.cu",
            "wkv7_bwd4_f32.cu", "rwkv8_api.cu",

@@ -21,7 +21,7 @@ using api::Span;
 constexpr unsigned long long kMaxBytes = 1ull << 46, kMaxBlocks = 1ull << 31;
 
 #ifdef WKV7_DEBUG
-std::atomic<int> g_debug_skip_tile{0};  // gdr_debug.h
+std::atomic<int> g_debug_skip_tile{0}, g_debug_skip_t{0};  // gdr_debug.h
 #endif
 
 int check_dims(int B, int T, int Hk, int Hv, int K, int V, const char* rows) {
@@ -157,6 +157,9 @@ int forward_impl(bool bf16, const void* q, const void* k, const void* v, const f
   a.small = is_small(a.s);
   a.s.q_b = st[0], a.s.q_t = st[1], a.s.k_b = st[2], a.s.k_t = st[3], a.s.v_b = st[4], a.s.v_t = st[5];
   a.q = q, a.k = k, a.v = v, a.g = g, a.beta = beta, a.s_init = s_init, a.o = o, a.s_final = s_final;
+#ifdef WKV7_DEBUG
+  a.skip_t = g_debug_skip_t.load();
+#endif
   if ((rc = wkv7::api_status_word(&a.status))) return rc;
   const int parts = segments_of(a.s), chunks = (T + kC - 1) / kC, each = (chunks + parts - 1) / parts;
   if (parts > 1) a.small = 0;
@@ -213,7 +216,7 @@ int backward_impl(bool bf16, const void* q, const void* k, const void* v, const 
   a.q = q, a.k = k, a.v = v, a.g = g, a.beta = beta, a.d_o = d_o, a.dS_final = dS_final;
   a.dq = dq, a.dk = dk, a.dv = dv, a.dg = dg, a.dbeta = dbeta, a.dS_init = dS_init;
 #ifdef WKV7_DEBUG
-  a.skip_tile = g_debug_skip_tile.load();
+  a.skip_tile = g_debug_skip_tile.load(), a.skip_t = g_debug_skip_t.load();
 #endif
   if ((rc = wkv7::api_status_word(&a.status))) return rc;
   const int parts = segments_of(a.s), chunks = (T + kC - 1) / kC, each = (chunks + parts - 1) / parts;
@@ -272,6 +275,10 @@ extern "C" {
 #ifdef WKV7_DEBUG
 int gdr_debug_skip_tile(int tile) {
   gdr::g_debug_skip_tile.store(tile > 0 ? tile : 0);
+  return WKV7_OK;
+}
+int gdr_debug_skip_t(int step) {
+  gdr::g_debug_skip_t.store(step > 0 ? step : 0);
   return WKV7_OK;
 }
 #endif

@@ -49,7 +49,7 @@ struct alignas(1024) BwdSmem {
   unsigned char scal[2][kChainScal];
   float most[6][kWarps][2];  // of the chain warps' dS, y and e^G lam, of the helpers' do, scale e^G do and lam
   float inv_s[kWarps], inv_d[2][kWarps], inv_g[2][kWarps];  // inverse scales of the warps' rows
-  uint64_t full_k[2], full_q, full_t, full_p, free_k[2], free_q, free_t, free_p;
+  uint64_t full[5], free_k[2], free_q, free_t, free_p;
   uint64_t done_x, done_y, done_l, done_w, done_g, end[2];    // products
   uint64_t ready_s, ready_y, ready_w, ready_d, ready_e;       // operands in tensor memory
   uint64_t full_s[kWarps], free_s[kWarps], full_l[kWarps], free_l[kWarps], full_d[kWarps], free_y, free_g;
@@ -74,7 +74,7 @@ __device__ __forceinline__ void fill(BwdSmem<T, KP>& m, const Args& a, long long
   auto at_k = [&](int s) { return (size_t)(slot - s) * a.s.Hk + hk; };
   auto at_v = [&](int s) { return (size_t)(slot - s) * a.s.Hv + hv; };
   auto k = [&](int s) {
-    uint64_t* bar = &m.full_k[s & 1];
+    uint64_t* bar = &m.full[s & 1];
     mbar_arrive_expect_tx(bar, image + kChainScal);
     bulk_load(m.k[s & 1], a.b.k_img + at_k(s) * image, image, bar);
     bulk_load(m.scal[s & 1], a.b.scal + at_v(s), kChainScal, bar);
@@ -88,11 +88,16 @@ __device__ __forceinline__ void fill(BwdSmem<T, KP>& m, const Args& a, long long
         bulk_load(to + part * kSpreadPart + 5 * j * 256, from + 2 * (part * kTriPart + tri_block(j, j)), (4 - j) * 512, bar);
   };
   auto q = [&](int s) {
-    mbar_arrive_expect_tx(&m.full_q, image);
-    bulk_load(m.q, a.b.q_img + at_k(s) * image, image, &m.full_q);
+    mbar_arrive_expect_tx(&m.full[kQ], image);
+    bulk_load(m.q, a.b.q_img + at_k(s) * image, image, &m.full[kQ]);
   };
-  auto t = [&](int s) { spread(m.t, a.b.t_img + at_v(s) * Layout::tp_img, &m.full_t); };
-  auto p = [&](int s) { spread(m.p, a.b.p_img + at_v(s) * Layout::tp_img, &m.full_p); };
+  auto t = [&](int s) {
+#ifdef WKV7_DEBUG
+    if (s + 1 == a.skip_t) return;
+#endif
+    spread(m.t, a.b.t_img + at_v(s) * Layout::tp_img, &m.full[kT]);
+  };
+  auto p = [&](int s) { spread(m.p, a.b.p_img + at_v(s) * Layout::tp_img, &m.full[kP]); };
   auto ask = [&](int s) {  // into L2
     if (s >= n) return;
     bulk_prefetch(a.b.k_img + at_k(s) * image, image);
@@ -117,7 +122,9 @@ __device__ __forceinline__ void fill(BwdSmem<T, KP>& m, const Args& a, long long
     ask(s + 2);
   }
   if (s < n)
-    for (uint64_t* b : {&m.full_k[0], &m.full_k[1], &m.full_q, &m.full_t, &m.full_p}) drain(b);
+    for (uint64_t& b : m.full) drain(&b);
+  else
+    drain_last(m.full, n);
 }
 
 // An image to memory, half of it by each of two warps. (By loads and stores: the
@@ -154,7 +161,7 @@ __global__ void __launch_bounds__(kThreads, 1) bwd_kernel(const Args a) {
   const int set = blockIdx.x % sets, hv = blockIdx.x / sets % a.s.Hv, seq = blockIdx.x / (sets * a.s.Hv);
   const int hk = hv / (a.s.Hv / a.s.Hk);
   if (threadIdx.x == 0) {
-    for (uint64_t* b : {&sm.full_k[0], &sm.full_k[1], &sm.full_q, &sm.full_t, &sm.full_p, &sm.free_q, &sm.free_t, &sm.free_p,
+    for (uint64_t* b : {&sm.full[0], &sm.full[1], &sm.full[kQ], &sm.full[kT], &sm.full[kP], &sm.free_q, &sm.free_t, &sm.free_p,
                         &sm.done_x, &sm.done_y, &sm.done_l, &sm.done_w, &sm.done_g, &sm.end[0], &sm.end[1]})
       mbar_init(b, 1);
     for (uint64_t* b : {&sm.free_k[0], &sm.free_k[1]}) mbar_init(b, kChains + kHelpers + 1);
@@ -191,14 +198,14 @@ __global__ void __launch_bounds__(kThreads, 1) bwd_kernel(const Args a) {
     } else if (warp == kIssuer) {
       for (int s = 0; s < n; ++s) {
         const int use = s & 1;
-        wait(&sm.full_k[use], s >> 1);
+        wait(&sm.full[use], s >> 1);
         wait(&sm.ready_s, use);
         tmem_fence_after_sync();
         if (elected()) {
           tc_rows<2, P, KP>(tmem + Col::x, tmem + Col::s_in, sm.k[use]);
           tc_commit(&sm.done_x);
         }
-        wait(&sm.full_t, use);
+        wait(&sm.full[kT], use);
         wait(&sm.ready_y, use);
         tmem_fence_after_sync();
         if (elected()) {
@@ -219,7 +226,7 @@ __global__ void __launch_bounds__(kThreads, 1) bwd_kernel(const Args a) {
     } else if (warp == kHelpersIssuer) {
       for (int s = 0; s < n; ++s) {
         const int use = s & 1;
-        wait(&sm.full_p, use);
+        wait(&sm.full[kP], use);
         if (s > 0) wait(&sm.free_y, use ^ 1);
         wait(&sm.ready_d, use);
         tmem_fence_after_sync();
@@ -228,7 +235,7 @@ __global__ void __launch_bounds__(kThreads, 1) bwd_kernel(const Args a) {
           tc_commit(&sm.done_y);
           tc_commit(&sm.free_p);
         }
-        wait(&sm.full_q, use);
+        wait(&sm.full[kQ], use);
         if (s > 0) wait(&sm.free_g, use ^ 1);
         wait(&sm.ready_e, use);
         tmem_fence_after_sync();
@@ -260,7 +267,7 @@ __global__ void __launch_bounds__(kThreads, 1) bwd_kernel(const Args a) {
       Operand<2, kS / 2> f;
       f.split(S, sS), f.store(s_in, KP / 2);
       ready(&sm.ready_s);
-      const Asked has_k(&sm.full_k[use], s >> 1), has_d(&sm.full_d[own], use);
+      const Asked has_k(&sm.full[use], s >> 1), has_d(&sm.full_d[own], use);
       if (s > 0) wait(has_s);
       if (lane == 0 && half == 0) sm.inv_s[own] = inv_s;
       f.put(sm.s[own], kVt * KP, key0, lane);
@@ -390,7 +397,7 @@ __global__ void __launch_bounds__(kThreads, 1) bwd_kernel(const Args a) {
       __syncwarp();
       if (cols > 0) columns_out<P>(record_of(s) + rec.d, sm.out[own].image, half, lane);
       __syncwarp();
-      wait(&sm.full_k[use], s >> 1);
+      wait(&sm.full[use], s >> 1);
 #pragma unroll
       for (int nt = 0; nt < 4; ++nt) {
         const float2 eq = *reinterpret_cast<const float2*>(sc.eq + token0 + 8 * nt + 2 * t4);
@@ -440,7 +447,7 @@ __global__ void __launch_bounds__(kThreads, 1) bwd_kernel(const Args a) {
       both_sync(meet);  // dv takes the place of the image
       rows_out(x, sm.out[own].dv, dv_at + (size_t)c * kC * row_t, row_t, tokens - c * kC, cols, token0 / 8, lane);
     }
-    copy_wait<0>();
+    copy_wait_all();
   }
   tmem_fence_before_sync();
   __syncthreads();

@@ -76,6 +76,7 @@ template <int kLeft>
 __device__ __forceinline__ void copy_wait() {
   asm volatile("cp.async.wait_group %0;" ::"n"(kLeft) : "memory");
 }
+__device__ __forceinline__ void copy_wait_all() { asm volatile("cp.async.wait_all;" ::: "memory"); }
 
 // rows points at token 0 of the chunk; len of its tokens and cols of the 16 columns
 // exist. All for tokens 8 n0 .. 8 (n0 + N) - 1 (n0 even).

@@ -56,7 +56,7 @@ struct alignas(1024) FwdSmem {
   unsigned char scal[2][kChainScal];
   float most[3][kWarps][2];  // of the chain warps' S, r and u
   float inv_s[kWarps], inv_r[kWarps];  // inverse scales of the warps' rows
-  uint64_t full_k[2], full_q, full_t, full_p, free_k[2], free_q, free_t, free_p;
+  uint64_t full[5], free_k[2], free_q, free_t, free_p;
   uint64_t done_x, done_q, done_u, done_w, done_o, end[2];  // products
   uint64_t ready_s, ready_r, ready_w, ready_u;  // operands in tensor memory
   uint64_t full_s[kWarps], full_u[kWarps], full_v[kWarps][2], free_v[kWarps], free_s, free_u;
@@ -80,7 +80,7 @@ __device__ __forceinline__ void fill(FwdSmem<T, KP, kSave>& m, const Args& a, lo
   auto at_k = [&](int c) { return (size_t)(slot + c) * a.s.Hk + hk; };
   auto at_v = [&](int c) { return (size_t)(slot + c) * a.s.Hv + hv; };
   auto k = [&](int c) {
-    uint64_t* bar = &m.full_k[c & 1];
+    uint64_t* bar = &m.full[c & 1];
     mbar_arrive_expect_tx(bar, image + kChainScal);
     bulk_load(m.k[c & 1], a.b.k_img + at_k(c) * image, image, bar);
     bulk_load(m.scal[c & 1], a.b.scal + at_v(c), kChainScal, bar);
@@ -89,9 +89,14 @@ __device__ __forceinline__ void fill(FwdSmem<T, KP, kSave>& m, const Args& a, lo
     mbar_arrive_expect_tx(bar, bytes);
     bulk_load(to, from, bytes, bar);
   };
-  auto q = [&](int c) { one(m.q, a.b.q_img + at_k(c) * image, image, &m.full_q); };
-  auto t = [&](int c) { one(m.t, a.b.t_img + at_v(c) * Layout::tp_img, 2 * tri, &m.full_t); };
-  auto p = [&](int c) { one(m.p, a.b.p_img + at_v(c) * Layout::tp_img, 2 * tri, &m.full_p); };
+  auto q = [&](int c) { one(m.q, a.b.q_img + at_k(c) * image, image, &m.full[kQ]); };
+  auto t = [&](int c) {
+#ifdef WKV7_DEBUG
+    if (c + 1 == a.skip_t) return;
+#endif
+    one(m.t, a.b.t_img + at_v(c) * Layout::tp_img, 2 * tri, &m.full[kT]);
+  };
+  auto p = [&](int c) { one(m.p, a.b.p_img + at_v(c) * Layout::tp_img, 2 * tri, &m.full[kP]); };
   auto ask = [&](int c) {  // into L2
     if (c >= n) return;
     bulk_prefetch(a.b.k_img + at_k(c) * image, image);
@@ -116,7 +121,9 @@ __device__ __forceinline__ void fill(FwdSmem<T, KP, kSave>& m, const Args& a, lo
     ask(c + 2);
   }
   if (c < n)
-    for (uint64_t* b : {&m.full_k[0], &m.full_k[1], &m.full_q, &m.full_t, &m.full_p}) drain(b);
+    for (uint64_t& b : m.full) drain(&b);
+  else
+    drain_last(m.full, n);
 }
 
 template <typename T, int KP, bool kSave>
@@ -131,7 +138,7 @@ __global__ void __launch_bounds__(kThreads, 1) fwd_kernel(const Args a) {
   const int set = blockIdx.x % sets, hv = blockIdx.x / sets % a.s.Hv, seq = blockIdx.x / (sets * a.s.Hv);
   const int hk = hv / (a.s.Hv / a.s.Hk);
   if (threadIdx.x == 0) {
-    for (uint64_t* b : {&sm.full_k[0], &sm.full_k[1], &sm.full_q, &sm.full_t, &sm.full_p, &sm.free_q, &sm.free_t, &sm.free_p,
+    for (uint64_t* b : {&sm.full[0], &sm.full[1], &sm.full[kQ], &sm.full[kT], &sm.full[kP], &sm.free_q, &sm.free_t, &sm.free_p,
                         &sm.done_x, &sm.done_q, &sm.done_u, &sm.done_w, &sm.done_o, &sm.end[0], &sm.end[1]})
       mbar_init(b, 1);
     for (uint64_t* b : {&sm.free_k[0], &sm.free_k[1]}) mbar_init(b, kChains + kWarps + 1);
@@ -163,20 +170,20 @@ __global__ void __launch_bounds__(kThreads, 1) fwd_kernel(const Args a) {
   } else if (warp == kIssuer) {
     for (int c = 0; c < n; ++c) {
       const int use = c & 1;
-      wait(&sm.full_k[use], c >> 1);
+      wait(&sm.full[use], c >> 1);
       wait(&sm.ready_s, use);
       tmem_fence_after_sync();
       if (elected()) {
         tc_rows<2, P, KP>(tmem + Col::x, tmem + Col::s_in, sm.k[use]);
         tc_commit(&sm.done_x);
       }
-      wait(&sm.full_q, use);
+      wait(&sm.full[kQ], use);
       if (elected()) {
         tc_rows<2, P, KP>(tmem + Col::q, tmem + Col::s_in, sm.q);
         tc_commit(&sm.done_q);
         tc_commit(&sm.free_q);
       }
-      wait(&sm.full_t, use);
+      wait(&sm.full[kT], use);
       if (c > 0) wait(&sm.free_u, use ^ 1);
       wait(&sm.ready_r, use);
       tmem_fence_after_sync();
@@ -198,7 +205,7 @@ __global__ void __launch_bounds__(kThreads, 1) fwd_kernel(const Args a) {
   } else if (warp == kHelpersIssuer) {
     for (int c = 0; c < n; ++c) {
       const int use = c & 1;
-      wait(&sm.full_p, use);
+      wait(&sm.full[kP], use);
       wait(&sm.ready_u, use);
       tmem_fence_after_sync();
       if (elected()) {
@@ -234,7 +241,7 @@ __global__ void __launch_bounds__(kThreads, 1) fwd_kernel(const Args a) {
       if (c > 0) wait(has_s);
       f.store(s_in, KP / 2);
       ready(&sm.ready_s);
-      const Asked has_k(&sm.full_k[use], c >> 1), has_v(&sm.full_v[own][place], kPlaces == 2 ? c >> 1 : c);
+      const Asked has_k(&sm.full[use], c >> 1), has_v(&sm.full_v[own][place], kPlaces == 2 ? c >> 1 : c);
       if (lane == 0 && half == 0) sm.inv_s[own] = inv_s;
       if constexpr (kSave) {
         f.put(sm.s[own], kVt * KP, key0, lane);
@@ -374,7 +381,7 @@ __global__ void __launch_bounds__(kThreads, 1) fwd_kernel(const Args a) {
           *reinterpret_cast<float4*>(record + rec.scales) = make_float4(inv_s, inv_u, 0.f, 0.f);
         }
       }
-      wait(&sm.full_k[use], c >> 1);
+      wait(&sm.full[use], c >> 1);
       const float fo = sc.inv_p * inv_u;
 #pragma unroll
       for (int nt = 0; nt < 8; ++nt) {
@@ -398,6 +405,7 @@ __global__ void __launch_bounds__(kThreads, 1) fwd_kernel(const Args a) {
       rows_out(o, sm.out[own].o, o_at + (size_t)c * kC * o_t, o_t, tokens - c * kC, cols, 0, lane);
     }
     if (kSave && lane == 0) bulk_wait_all();
+    copy_wait_all();
   }
   tmem_fence_before_sync();
   __syncthreads();

@@ -129,7 +129,9 @@ struct Args {
   int small;  // few chunks: a call's kernels may begin while the one before still runs (launch_after).
               // Saves 4 of 31 us for one chunk; 40 heads of 1024 chunks lost 650 of 3900 us to blocks
               // that waited where others could have run.
-  int skip_tile;  // the debug build's: this one (from 1) of the gradients' tiles is not copied, and its wait runs out
+  // The debug build's: this one (from 1) of the gradients' tiles, or of the chains' images of T, is not
+  // copied, and its wait runs out.
+  int skip_tile, skip_t;
 };
 // A forward in segments, the preparation of one beside the chain of the one before,
 // and a backward, the gradients of one beside the chain of the next: where the

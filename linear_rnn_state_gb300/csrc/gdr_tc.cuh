@@ -256,4 +256,16 @@ struct Patience {
   }
 };
 
+enum { kQ = 2, kT, kP };  // barriers of full places: two of k, q, t, p
+// The filling thread at its end: the last of n copies into each place (k by turns)
+// has landed, also where the warps that would wait for it gave up before. A
+// millisecond at most each.
+__device__ __forceinline__ void drain_last(uint64_t* full, int n) {
+#pragma unroll 1
+  for (int b = 0; b < 5; ++b) {
+    const int copies = b < 2 ? (n + 1 - b) / 2 : n;
+    mbar_wait_bounded(nullptr, full + b, (copies - 1) & 1, 1000000);
+  }
+}
+
 }  // namespace gdr

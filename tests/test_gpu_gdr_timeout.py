@@ -28,9 +28,10 @@ def env():
     torch.cuda.set_device(0)
     gdr.load()
     dbg = gdr.load(_build.DEBUG_LIB)
-    dbg.gdr_debug_skip_tile.argtypes, dbg.gdr_debug_skip_tile.restype = [ctypes.c_int], ctypes.c_int
+    for hook in (dbg.gdr_debug_skip_tile, dbg.gdr_debug_skip_t):
+        hook.argtypes, hook.restype = [ctypes.c_int], ctypes.c_int
     yield gdr, dbg
-    dbg.gdr_debug_skip_tile(0)
+    dbg.gdr_debug_skip_tile(0), dbg.gdr_debug_skip_t(0)
 
 
 # a head's own gradients, the terms of shared heads, their sum in the block (tiles of two heads), segments
@@ -75,3 +76,43 @@ def test_a_wait_that_runs_out_is_reported(env, B, T, Hk, Hv, K, V, dtype, tile):
 def test_the_hook_is_the_debug_build_alone_s(env):
     gdr, dbg = env
     assert hasattr(dbg, "gdr_debug_skip_tile") and not hasattr(gdr.load(), "gdr_debug_skip_tile")
+
+
+@pytest.mark.parametrize("step", [1, 3, 5])
+@pytest.mark.parametrize("B,T,Hk,Hv,K,V,dtype", [(2, 300, 1, 2, 64, 64, F32), (1, 300, 1, 2, 128, 80, BF16)], ids=["64", "128"])
+def test_a_chain_s_wait_that_runs_out_is_reported(env, B, T, Hk, Hv, K, V, dtype, step):
+    """The chains' image of T in one of five steps: their warps go on without it."""
+    gdr, dbg = env
+    gen = torch.Generator("cuda").manual_seed(step)
+    n = lambda *s: torch.randn(s, device="cuda", generator=gen)
+    unit = lambda x: (x / x.norm(dim=-1, keepdim=True)).to(dtype)
+    q, k, v, do = unit(n(B, T, Hk, K)), unit(n(B, T, Hk, K)), n(B, T, Hv, V).to(dtype), n(B, T, Hv, V).to(dtype)
+    g, beta = -0.1 * n(B, T, Hv).abs(), torch.sigmoid(n(B, T, Hv))
+    o, s, saved = gdr.forward(q, k, v, g, beta)
+    want = {"o": o, "s": s, **gdr.backward(q, k, v, g, beta, do, saved)}
+    gdr.wkv7.status()
+    stream, bf16, dims = torch.cuda.current_stream().cuda_stream, dtype is BF16, (B, T, Hk, Hv, K, V, -1)
+    work = torch.empty(dbg.gdr_backward_bytes(*dims, bf16), dtype=torch.uint8, device="cuda")
+    kept, got = torch.empty_like(saved), {m: torch.empty_like(x) for m, x in want.items()}
+    suffix = "_bf16" if bf16 else ""
+    p = lambda *xs: [x.data_ptr() for x in xs]
+    tail = (None, K ** -0.5, 0)
+
+    def forward():
+        return getattr(dbg, "gdr_forward" + suffix)(*p(q, k, v, g, beta), None, None, *p(got["o"], got["s"], kept), *tail, 1, *dims, stream)
+
+    def backward():
+        return getattr(dbg, "gdr_backward" + suffix)(*p(q, k, v, g, beta, do), None, None, *p(saved, work),
+                                                     *p(*list(got.values())[2:]), *tail, *dims, stream)
+
+    for call in (forward, backward):
+        assert dbg.wkv7_status(stream) == 0, dbg.wkv7_last_error().decode()
+        assert dbg.gdr_debug_skip_t(step) == 0
+        try:
+            assert call() == 0
+            assert dbg.wkv7_status(stream) == -4  # WKV7_ERR_TIMEOUT
+            assert dbg.wkv7_status(stream) == 0
+        finally:
+            dbg.gdr_debug_skip_t(0)
+    assert forward() == 0 and backward() == 0 and dbg.wkv7_status(stream) == 0
+    assert all(torch.equal(got[m], want[m]) for m in want)
