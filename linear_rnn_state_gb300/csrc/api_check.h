@@ -9,6 +9,11 @@
 #include "wkv7.h"
 #include "wkv7_launch.h"
 
+namespace wkv7 {
+// The current device's status word, which kernels report a timeout through (wkv7_api.cu).
+int api_status_word(unsigned** out);
+}  // namespace wkv7
+
 namespace api {
 
 inline int fail(int code, const char* fmt, ...) {

@@ -9,8 +9,6 @@ namespace wkv7 {
 
 // Records `msg` as the calling thread's last error and returns `code`.
 int api_fail(int code, const char* msg);
-// The current device's status word, which kernels report a timeout through.
-int api_status_word(unsigned** out);
 
 // A buffer that a kernel reads or writes with plain (non-TMA) loads and
 // stores: its first byte and its size. The debug build (WKV7_DEBUG) checks
