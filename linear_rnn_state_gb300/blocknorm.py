@@ -24,7 +24,6 @@ EXPORTS = {
     "blocknorm_part_bytes": 3,
 }
 
-_typed = set()
 _lib = None
 
 
@@ -36,7 +35,7 @@ def load(path: str | None = None):
         _lib = lib
     if gdr._torch is None:
         gdr._setup()
-    if id(lib) not in _typed:
+    if not hasattr(lib, "_blocknorm_typed"):
         vp, i, n, f = ctypes.c_void_p, ctypes.c_int, ctypes.c_longlong, ctypes.c_float
         lib.blocknorm_add_forward.argtypes = [vp] * 7 + [n] * 3 + [i, f, i, i, vp]
         lib.blocknorm_add_backward.argtypes = [vp] * 12 + [n] * 3 + [i, i, i, vp]
@@ -46,7 +45,7 @@ def load(path: str | None = None):
         lib.blocknorm_part_bytes.restype = ctypes.c_size_t
         for name in ("add_forward", "add_backward", "gated_forward", "gated_backward"):
             getattr(lib, "blocknorm_" + name).restype = i
-        _typed.add(id(lib))
+        lib._blocknorm_typed = True
     return lib
 
 

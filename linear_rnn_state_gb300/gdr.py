@@ -33,7 +33,6 @@ EXPORTS = {
     "gdr_step_bf16": 18,
 }
 
-_typed = set()
 _lib = None
 
 
@@ -43,7 +42,7 @@ def load(path: str | None = None):
     lib = wkv7.load(path)
     if path is None:
         _lib = lib
-    if id(lib) not in _typed:
+    if not hasattr(lib, "_gdr_typed"):
         vp, i, f = ctypes.c_void_p, ctypes.c_int, ctypes.c_float
         lib.gdr_saved_bytes.argtypes = [i] * 9
         lib.gdr_backward_bytes.argtypes = [i] * 8
@@ -55,7 +54,7 @@ def load(path: str | None = None):
             getattr(lib, "gdr_step" + suffix).argtypes = [vp] * 9 + [f] + [i] * 7 + [vp]
             for name in ("gdr_forward", "gdr_backward", "gdr_step"):
                 getattr(lib, name + suffix).restype = i
-        _typed.add(id(lib))
+        lib._gdr_typed = True
     return lib
 
 

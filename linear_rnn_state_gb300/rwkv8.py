@@ -21,13 +21,11 @@ EXPORTS = {
     "rwkv8_backward": 21,
 }
 
-_typed = set()
-
 
 def load(path: str | None = None):
     """The loaded library with the rwkv8_* signatures set."""
     lib = wkv7.load(path)
-    if id(lib) not in _typed:
+    if not hasattr(lib, "_rwkv8_typed"):
         vp, i = ctypes.c_void_p, ctypes.c_int
         lib.rwkv8_ckpt_bytes.argtypes = [i] * 5
         lib.rwkv8_ckpt_bytes.restype = ctypes.c_size_t
@@ -35,7 +33,7 @@ def load(path: str | None = None):
         lib.rwkv8_forward.restype = i
         lib.rwkv8_backward.argtypes = [vp] * 14 + [i] * 6 + [vp]
         lib.rwkv8_backward.restype = i
-        _typed.add(id(lib))
+        lib._rwkv8_typed = True
     return lib
 
 
