@@ -9,7 +9,9 @@
  * is the norm of residual itself and h is not written.
  * After it, for every row of D values (a head):
  *     r = 1 / sqrt(mean(o^2) + eps),   y = o r weight z sigmoid(z)
- * All arithmetic is fp32; h enters n before it is rounded to its type.
+ * All arithmetic is fp32; h enters n before it is rounded to its type. The sigmoid
+ * of bfloat16 calls comes from the fast exponential: within (2 + |z|) 2^-24 of
+ * itself, and 0 for z below -87.3.
  *
  * Sizes: D from 1 to 8192. x, n and their gradients have one type, residual, h
  * and their gradients another (bfloat16 or fp32; fp32 where x is fp32); weight,

@@ -145,6 +145,19 @@ def test_gated(env, tokens, H, D, dt):
         _close(name, g[name], want)
 
 
+def test_gated_fp32_gates_to_the_last_bits(env):
+    """Every element of y, where the sigmoid runs from 1 down to fp32's smallest normal
+    numbers: an exponential (2 ulp), a sum, a quotient, the row's sum (16 values: 4 and
+    the root's 3) and five products, some sixteen roundings of 2^-24: 1e-6 of the element."""
+    orc, bn = env
+    z = torch.linspace(-87.0, 30.0, 16 * 400, device="cuda").view(400, 1, 16)
+    o = 1 + torch.rand(400, 1, 16, device="cuda", generator=torch.Generator("cuda").manual_seed(7))
+    w = torch.ones(16, device="cuda")
+    y, _ = bn.gated_forward(o, z, w)
+    ref = orc.gated(_n(o), _n(z), _n(w))
+    assert np.max(np.abs(_n(y) - ref) / np.maximum(np.abs(ref), 1e-37)) <= 1e-6
+
+
 def test_gated_gates_far_out(env):
     """z of -200 (its sigmoid is 0 in fp32) and 200."""
     orc, bn = env
