@@ -145,6 +145,43 @@ def test_gated(env, tokens, H, D, dt):
         _close(name, g[name], want)
 
 
+PAIRS = pytest.mark.parametrize("dt,rt", [(BF16, BF16), (BF16, F32), (F32, F32)], ids=["bf16", "bf16_f32", "f32"])
+
+
+@PAIRS
+@pytest.mark.parametrize("rows,D", [(37, 513), (37, 1023), (37, 2047), (37, 2049), (37, 4095), (700, 4097), (700, 8191)])
+def test_add_wide_odd_widths(env, rows, D, dt, rt):
+    """Rows of single values: groups of 128 threads and more, several pieces a thread, more rows than blocks."""
+    _add(env, rows, D, dt, rt, seed=D)
+
+
+@pytest.mark.parametrize("dt", [BF16, F32], ids=["bf16", "f32"])
+@pytest.mark.parametrize("tokens,H,D", [(50, 3, 515), (20, 2, 1027), (700, 1, 2047), (9, 2, 4099), (700, 1, 8191)])
+def test_gated_wide_odd_widths(env, tokens, H, D, dt):
+    test_gated(env, tokens, H, D, dt)
+
+
+@pytest.mark.parametrize("D", [96, 520, 2048, 5000])
+def test_rows_at_odd_strides(env, D):
+    """Widths of whole pieces of eight whose rows are not whole pieces apart: by single values."""
+    orc, bn = env
+    gen = torch.Generator("cuda").manual_seed(D)
+    n = lambda *s: torch.randn(s, device="cuda", generator=gen)
+    x, r, w, a, dn, dh = n(40, D + 5).bfloat16()[:, :D], n(40, D + 3)[:, :D], n(D), n(D), n(40, D).bfloat16(), n(40, D)
+    h, y, rstd = bn.add_forward(x, r, w, a)
+    h_ref, n_ref = orc.add(*(_n(t) for t in (x, r, w, a)))
+    _close("h", h, h_ref), _close("n", y, n_ref)
+    g = bn.add_backward(x, r, w, rstd, dn, dh, a)
+    for name, want in orc.add_grad(_n(x), _n(r), _n(w), _n(dn), _n(dh), _n(a)).items():
+        _close(name, g[name], want)
+    o, z, dy = n(40, 2 * D + 1)[:, :2 * D].unflatten(-1, (2, D)), n(40, 2 * D + 7)[:, :2 * D].unflatten(-1, (2, D)), n(40, 2, D)
+    y, rstd = bn.gated_forward(o, z, w)
+    _close("y", y, orc.gated(_n(o), _n(z), _n(w)))
+    g = bn.gated_backward(o, z, w, rstd, dy)
+    for name, want in orc.gated_grad(_n(o), _n(z), _n(w), _n(dy)).items():
+        _close(name, g[name], want)
+
+
 def test_gated_fp32_gates_to_the_last_bits(env):
     """Every element of y, where the sigmoid runs from 1 down to fp32's smallest normal
     numbers: an exponential (2 ulp), a sum, a quotient, the row's sum (16 values: 4 and
