@@ -474,6 +474,53 @@ def test_nothing_to_learn_from_large_queries(env, T):
 # ---------------------------------------------- shared heads, segments, starts ---
 
 
+@pytest.mark.parametrize("Hk,Hv,K,V,T,l2norm,starts", [
+    (16, 32, 128, 128, 640, True, None),
+    (16, 48, 96, 16, 640, False, None),
+    (20, 40, 128, 24, 500, True, [0, 1, 1, 130, 300, 500]),
+], ids=["128", "96", "packed"])
+def test_shared_heads_summed_in_the_block(env, Hk, Hv, K, V, T, l2norm, starts):
+    """bfloat16, keys wider than 64 and at least 152 chunks of key heads."""
+    orc, gdr = env
+    n = len(starts) - 1 if starts else 1
+    d = _make(1, T, Hk, Hv, K, V, BF16, 36, states=n, l2norm=l2norm, rate=0.3)
+    if not starts:
+        _check(env, d, qk_l2norm=l2norm)
+    kw = {"qk_l2norm": l2norm, "seq_starts": torch.tensor(starts, dtype=torch.int32, device="cuda") if starts else None}
+
+    def run():
+        o, s, saved = gdr.forward(*(d[m] for m in INS), d["s_init"], **kw)
+        return o, s, gdr.backward(*(d[m] for m in INS), d["do"], saved, dS_final=d["dS_final"], **kw)
+
+    o, s, g = run()
+    if starts:
+        h = _np(d)
+        fwd = orc.packed(orc.forward, starts, [h[m] for m in INS], {"s_init": h["s_init"]}, l2norm=l2norm)
+        _close("o", o, np.concatenate([x[0] for x in fwd], 1)), _close("s_final", s, np.concatenate([x[1] for x in fwd]))
+        bwd = orc.packed(orc.backward, starts, [h[m] for m in INS + ("do",)], {"s_init": h["s_init"], "dS_final": h["dS_final"]}, l2norm=l2norm)
+        for m in ("dq", "dk", "dv", "dg", "dbeta"):
+            _close(m, g[m], np.concatenate([x[m] for x in bwd], 1))
+        _close("dS_init", g["dS_init"], np.concatenate([x["dS_init"] for x in bwd]))
+    for _ in range(3):
+        again = run()
+        assert torch.equal(o, again[0]) and all(torch.equal(g[m], again[2][m]) for m in g)
+
+
+def test_shared_heads_summed_in_the_block_by_segments(env):
+    _check(env, _make(1, 8300, 2, 4, 128, 16, BF16, 37, rate=0.1, l2norm=True), qk_l2norm=True)
+
+
+@pytest.mark.parametrize("T,Hk,Hv,dtype", [(4096, 16, 16, F32), (4159, 9, 18, BF16), (8191, 8, 16, F32)])
+def test_two_segments_of_many_heads(env, T, Hk, Hv, dtype):
+    """64 to 128 chunks and at least 16 chains: two segments, forwards and backwards."""
+    _check(env, _make(1, T, Hk, Hv, 16, 16, dtype, 38, rate=0.1))
+
+
+@pytest.mark.parametrize("B,Hv,V", [(1, 40, 16), (1, 40, 64), (1, 40, 80), (2, 80, 128)])
+def test_fewer_and_more_chains_than_sms(env, B, Hv, V):
+    """A chain's block has 64 value columns: 40, 40, 80 and 320 of them, whole ones and with columns left over."""
+    _check(env, _make(B, 70, Hv, Hv, 16, V, F32, B), carry=False)
+
 @pytest.mark.parametrize("starts", [[0, 0], [30, 30, 30], [100, 100, 100, 100]])
 def test_packed_sequences_without_a_token(env, starts):
     """Tokens there are, but the sequences have none: states and their gradients pass through,
