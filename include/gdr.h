@@ -10,8 +10,8 @@
  *     u_t = v_t - e^{g_t} S k_t          (the value less what S holds for k)
  *     S  <- e^{g_t} S + beta_t u_t k_t^T
  *     o_t = scale S q_t
- * With l2norm != 0, q_t and k_t are first divided by sqrt(|.|^2 + 1e-6), and
- * the gradients are those of the vectors given. g = -inf empties the state.
+ * With l2norm != 0, q_t and k_t (of lengths up to 2^115) are first divided by
+ * sqrt(|.|^2 + 1e-6), and the gradients are those of the vectors given. g = -inf empties the state.
  * The rule is stable for |k| <= 1, 0 <= beta <= 1 (up to 2), g <= 0; the
  * kernels compute any finite values.
  *

@@ -75,6 +75,9 @@ __device__ __forceinline__ void store8(float* p, const float (&x)[8]) {
   *reinterpret_cast<float4*>(p) = make_float4(x[0], x[1], x[2], x[3]);
   *reinterpret_cast<float4*>(p + 4) = make_float4(x[4], x[5], x[6], x[7]);
 }
+// The squares of vectors that are normalised are formed of the vector times kSmall,
+// the epsilon's part with them: in fp32's range up to a length of 2^115.
+constexpr float kSmall = 0x1p-52f, kSmallEps = 1e-6f * 0x1p-104f;
 // ---------------------------------------------------------- fp16 pairs ---
 
 __device__ __forceinline__ uint32_t pack_f16(float lo, float hi) {

@@ -532,11 +532,11 @@ __global__ void __launch_bounds__(256) join_kernel(const Args a) {
     }
     float s2 = 0.f, xd = 0.f;
 #pragma unroll
-    for (int e = 0; e < 8; ++e) s2 = fmaf(x[e], x[e], s2), xd = fmaf(x[e], d[e], xd);
+    for (int e = 0; e < 8; ++e) x[e] *= kSmall, s2 = fmaf(x[e], x[e], s2), xd = fmaf(x[e], d[e], xd);
     s2 = wkv7::group_allreduce<16>(s2), xd = wkv7::group_allreduce<16>(xd);
-    const float r = 1.f / sqrtf(s2 + 1e-6f), f = r * r * xd;
+    const float r = 1.f / sqrtf(s2 + kSmallEps), f = r * (r * xd);
 #pragma unroll
-    for (int e = 0; e < 8; ++e) d[e] = r * fmaf(-f, x[e], d[e]);
+    for (int e = 0; e < 8; ++e) d[e] = r * kSmall * fmaf(-f, x[e], d[e]);
   }
   if (in && !none) {
     T* out = static_cast<T*>(is_k ? a.dk : a.dq) + row * K + cl * 8;

@@ -106,10 +106,10 @@ struct RowLoader {
       if (l2norm) {
         float s2 = 0.f;
 #pragma unroll
-        for (int e = 0; e < 8; ++e) s2 = fmaf(x[e], x[e], s2);
-        s2 = wkv7::group_allreduce<kLanes>(s2) + 1e-6f;
+        for (int e = 0; e < 8; ++e) s2 = fmaf(x[e] * kSmall, x[e] * kSmall, s2);
+        s2 = wkv7::group_allreduce<kLanes>(s2) + kSmallEps;
         r = rsqrtf(s2);
-        r = fmaf(0.5f * r, fmaf(-s2 * r, r, 1.f), r);  // a Newton step: the last bits
+        r = kSmall * fmaf(0.5f * r, fmaf(-s2 * r, r, 1.f), r);  // a Newton step: the last bits
       }
       uint32_t hi[4], lo[4];
 #pragma unroll

@@ -63,11 +63,14 @@ __global__ void __launch_bounds__(kThreads) step_kernel(const StepArgs a) {
     const int mine = cl / kStep % kRows, row = row0 + mine * kSub;
     const T* v = static_cast<const T*>(a.v) + r * a.v_b + t * a.v_t + (size_t)hv * a.V;
     const float vr = row < a.V ? load1(v + row) : 0.f;
+    const float small = a.l2norm ? kSmall : 1.f;
+    q.x *= small, q.y *= small, q.z *= small, q.w *= small;
+    k.x *= small, k.y *= small, k.z *= small, k.w *= small;
     float kq = wkv7::group_allreduce<kLanes>(dot4(q, k, 0.f));
     float rq = a.scale, rk = 1.f;
     if (a.l2norm) {
-      rq *= 1.f / sqrtf(wkv7::group_allreduce<kLanes>(dot4(q, q, 0.f)) + 1e-6f);
-      rk = 1.f / sqrtf(wkv7::group_allreduce<kLanes>(dot4(k, k, 0.f)) + 1e-6f);
+      rq *= 1.f / sqrtf(wkv7::group_allreduce<kLanes>(dot4(q, q, 0.f)) + kSmallEps);
+      rk = 1.f / sqrtf(wkv7::group_allreduce<kLanes>(dot4(k, k, 0.f)) + kSmallEps);
     }
     kq *= rk * rq;
     const bool second = cl >= kLanes / 2;  // S q rather than S k

@@ -471,6 +471,33 @@ def test_nothing_to_learn_from_large_queries(env, T):
     assert all(torch.count_nonzero(x) == 0 for x in grads.values())
 
 
+@pytest.mark.parametrize("Hk", [1, 2])
+@pytest.mark.parametrize("K", [24, 64, 128])
+def test_normalised_vectors_whose_squares_pass_fp32(env, K, Hk):
+    """Queries and keys of length 1e21, some of their rows: divided by their lengths all the same."""
+    orc, gdr = env
+    d = _make(2, 130, Hk, 2, K, 64, F32, 35, l2norm=True)
+    d["q"][:, ::3] *= 1e20
+    d["k"][:, ::5] *= 1e20
+    o, s, saved = gdr.forward(*(d[n] for n in INS), d["s_init"], qk_l2norm=True)
+    g = gdr.backward(*(d[n] for n in INS), d["do"], saved, dS_final=d["dS_final"], qk_l2norm=True)
+    h = _np(d)
+    o_ref, s_ref = orc.forward(*(h[n] for n in INS), h["s_init"], l2norm=True)
+    ref = orc.backward(*(h[n] for n in INS), h["do"], h["s_init"], h["dS_final"], l2norm=True)
+    _close("o", o, o_ref), _close("s_final", s, s_ref)
+    for n in ("dv", "dg", "dbeta", "dS_init"):
+        _close(n, g[n], ref[n])
+    for n, x, step in (("dq", "q", 3), ("dk", "k", 5)):  # a row's gradient is 1e20 smaller where the row is larger
+        far = np.zeros(130, bool)
+        far[::step] = True
+        for rows in (far, ~far):
+            _close(n, g[n][:, torch.from_numpy(rows).cuda()], ref[n][:, rows])
+    pool = d["s_init"].clone()
+    o1 = gdr.step(*(d[n][:, :1].contiguous() for n in INS), pool, qk_l2norm=True)
+    o_ref, s_ref = orc.forward(*(h[n][:, :1] for n in INS), h["s_init"], l2norm=True)
+    _close("o", o1, o_ref), _close("s_final", pool, s_ref)
+
+
 # ---------------------------------------------- shared heads, segments, starts ---
 
 
