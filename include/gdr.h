@@ -36,7 +36,12 @@
  * all chunks at once, then the states from chunk to chunk, then (backward) the
  * gradients of all chunks at once. Products run on the tensor cores with
  * operands of two fp16 values (22 bits; bfloat16 inputs are exact in one) and
- * fp32 accumulation; states, sums and decays are fp32. A value of infinity or
+ * fp32 accumulation; states, sums and decays are fp32. Each operand tile (a chunk's
+ * 64 tokens by 16 value columns, 16 rows of a state, a chunk's T, P, F or E, a
+ * token's q or k) has a scale from its largest value: a value 2^-17 of that has 22
+ * bits, smaller ones have fewer, and below 2^-39 it counts as 0. So a state that only
+ * decays within a chunk is right to 2^-36 of the chunk's largest input and state, not
+ * of itself. (gdr_step computes in fp32 throughout.) A value of infinity or
  * NaN makes its chunk and those after it (before it, for gradients)
  * non-finite in its head.
  *

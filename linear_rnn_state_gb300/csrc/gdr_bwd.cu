@@ -16,8 +16,8 @@
 // its step, and the chain waited for 1100 to 2200 of them (200 to 162 us).
 //
 // Bound by a step's latency, some 4700 cycles, and at 4.7 TB/s by memory in part
-// (stores wait). Measured (64 steps): 4 x 4096 x 32 heads of 64 bfloat16 162 us, 4.7
-// TB/s; 8 x 4096 x 12 x 64 fp32 210 us, 3.9 TB/s; 2 x 4095 x 32 x 128 bfloat16 192
+// (stores wait). Measured (64 steps): 4 x 4096 x 32 heads of 64 bfloat16 160 us, 4.7
+// TB/s; 8 x 4032 x 12 x 64 fp32 207 us, 3.9 TB/s; 2 x 4095 x 32 x 128 bfloat16 189
 // us, 4.8 TB/s. Measured and dropped, at the first size: four warps apart for dv and
 // the images of dS1 and lam (201 to 193 us, at 128 keys 201 to 220); products issued
 // in rolled loops, for less code (210 to 218).

@@ -10,10 +10,10 @@
 // scale by a power of two, so a product with them takes two mma (a b_hi +
 // a b_lo) and a product of two pairs three (the lo lo term is 2^-22 of it).
 // fp16 has 5 exponent bits: every tile carries a power-of-two scale that puts
-// a bound of its largest magnitude just below 2^14 (pow2_scale). A value 2^-39
-// of that bound or smaller is lost, which costs nothing in a sum that holds
-// the larger ones; bounds may be loose by 2^10 or so before the pair has fewer
-// bits than fp32.
+// its largest magnitude just below 2^14 (pow2_scale). A value keeps the 22 bits
+// down to 2^-17 of that, fewer below, and is lost at 2^-39, which costs nothing in
+// a sum that holds the larger ones. So a scale comes from the values themselves: a
+// bound that is loose by more than 2^10 or so costs bits of all of them.
 //
 // Images. A tile lives in global memory exactly as in shared memory: rows of
 // 128 bytes (64 fp16 values; wider tiles are several such panels one after the
@@ -100,7 +100,7 @@ __device__ __forceinline__ void split2(float a, float b, uint32_t& hi, uint32_t&
 
 // The power of two s with largest * s in [2^13, 2^14), its exponent held to
 // +-120 so that s and 1/s are normal floats (0 gives 2^120; infinity and NaN
-// give 2^-114, and the values themselves carry them into the products).
+// give 2^-115, and the values themselves carry them into the products).
 __device__ __forceinline__ float pow2_scale(float largest) {
   int e = (int)((__float_as_uint(largest) >> 23) & 255u) - 127;
   e = 13 - e;

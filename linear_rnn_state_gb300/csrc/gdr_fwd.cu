@@ -25,9 +25,11 @@
 // Arithmetic: fp16 pairs in every product, those of o too: a bfloat16 o is an
 // fp32 result rounded once.
 //
-// Measured (64 steps; time, traffic): 4 x 4096 x 32 heads of 64 bfloat16 127 us,
-// 4.2 TB/s; 8 x 4096 x 12 x 64 fp32 160 us, 3.6 TB/s; 2 x 4095 x 32 x 128 bfloat16
-// 155 us, 4.4 TB/s. 65536 tokens of 40 heads (1024 steps on 40 of 152 SMs) 2.04 ms.
+// Measured (64 steps; time, traffic): 4 x 4096 x 32 heads of 64 bfloat16 133 us,
+// 4.5 TB/s; 8 x 4032 x 12 x 64 fp32 160 us, 3.6 TB/s; 2 x 4095 x 32 x 128 bfloat16
+// 159 us, 4.3 TB/s. 65536 tokens of 40 heads (1024 steps on 40 of 152 SMs) 2.09 ms.
+// (bfloat16 with 11 bits of S0, u and P in o: 127 and 155 us, and o 1.1e-3 from the
+// rounded fp32 result.)
 // Measured and dropped, at the first size: 128 rows, the hi and lo parts as one
 // operand (twice the reads of tensor memory; 183 to 202 us); v by a warp of its own
 // (145 to 156, it comes later); v and o by whole rows of 64 columns instead of 16 a

@@ -21,11 +21,11 @@
 // 537 -> 461 us); otherwise each writes fp32 terms that a second kernel adds in the
 // order of the heads. No atomics.
 //
-// Bound by the SM's shared-memory pipe and issue (57 % and 46 % at two blocks of
-// eight warps, the tensor pipe 34 %): fragments by ldmatrix, four warps of a block
+// Bound by the SM's shared-memory pipe and issue (57 % and 47 % at two blocks of
+// eight warps, the tensor pipe 35 %): fragments by ldmatrix, four warps of a block
 // reading the same columns. Measured: 4 x 4096 tokens x 32 heads of 64 bfloat16
-// 312 us, 2.9 TB/s; 8 x 4096 x 12 x 64 fp32 410 us, 2.4 TB/s; 2 x 4095 x 16 and 32
-// x 128 bfloat16 460 us. mma.sync and not tcgen05: every tile of 16 value columns
+// 329 us, 2.7 TB/s; 8 x 4032 x 12 x 64 fp32 415 us, 2.4 TB/s; 2 x 4095 x 16 and 32
+// x 128 bfloat16 495 us. mma.sync and not tcgen05: every tile of 16 value columns
 // has scales of its own, which products over several tiles would have to share.
 #include <type_traits>
 
