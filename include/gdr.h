@@ -41,7 +41,9 @@
  * token's q or k) has a scale from its largest value: a value 2^-17 of that has 22
  * bits, smaller ones have fewer, and below 2^-39 it counts as 0. So a state that only
  * decays within a chunk is right to 2^-36 of the chunk's largest input and state, not
- * of itself. (gdr_step computes in fp32 throughout.) A value of infinity or
+ * of itself, and results have fewer bits where g > 0 lets a chunk grow by more than
+ * 2^17 from one token to another (1e-4 at e^17). (gdr_step computes in fp32
+ * throughout.) A value of infinity or
  * NaN makes its chunk and those after it (before it, for gradients)
  * non-finite in its head.
  *
