@@ -1,0 +1,235 @@
+// C ABI of linear attention with a decay (linattn.h): argument checks, the
+// regions of the caller's buffers, and the launches.
+#include <initializer_list>
+
+#include "api_check.h"
+#include "linattn.h"
+#include "linattn_launch.h"
+
+namespace linattn {
+namespace {
+
+using api::fail;
+using api::Span;
+
+constexpr unsigned long long kMaxBytes = 1ull << 46, kMaxBlocks = 1ull << 31;
+
+int check_dims(int B, int T, int Hk, int Hv, int K, int V, const char* rows) {
+  if (B < 0 || T < 0 || Hk < 0 || Hv < 0) return fail(WKV7_ERR_INVALID, "%s, T, Hk and Hv must be >= 0 (got %d, %d, %d, %d)", rows, B, T, Hk, Hv);
+  if (Hk > Hv || (Hk ? Hv % Hk : Hv)) return fail(WKV7_ERR_INVALID, "Hv must be a multiple of Hk (got %d, %d)", Hv, Hk);
+  if (K < 8 || K > kMaxDim || K % 8 || V < 8 || V > kMaxDim || V % 8)
+    return fail(WKV7_ERR_INVALID, "K and V must be multiples of 8 from 8 to %d (got %d, %d)", kMaxDim, K, V);
+  if ((unsigned long long)B * T >= 1ull << 40 || (unsigned long long)B * T * Hv >= kMaxBytes / (4 * kMaxDim))
+    return fail(WKV7_ERR_INVALID, "%s * T * Hv too large", rows);
+  return WKV7_OK;
+}
+
+// Strides of q, k, v: the given ones, checked, or the dense ones. bytes: what
+// each tensor spans.
+int set_strides(long long (&out)[6], unsigned long long (&bytes)[3], const long long* given, int B, int T, int Hk, int Hv,
+                int K, int V, int es) {
+  const long long row[3] = {(long long)Hk * K, (long long)Hk * K, (long long)Hv * V};
+  const char* const names[3] = {"q", "k", "v"};
+  for (int i = 0; i < 3; ++i) {
+    long long b = row[i] * T, t = row[i];
+    if (given) b = given[2 * i], t = given[2 * i + 1];
+    if (given && ((T > 1 && (t < row[i] || t % 8 || t > 1ll << 40)) || (B > 1 && (b < 0 || b % 8 || b > 1ll << 45))))
+      return fail(WKV7_ERR_INVALID, "%s: strides must be multiples of 8, a token's at least its heads (got %lld, %lld)", names[i], b, t);
+    if (B <= 1) b = 0;
+    if (T <= 1) t = 0;
+    out[2 * i] = b, out[2 * i + 1] = t;
+    bytes[i] = B && T && Hv ? ((unsigned long long)(B - 1) * b + (unsigned long long)(T - 1) * t + row[i]) * es : 0;
+    if (bytes[i] >= kMaxBytes) return fail(WKV7_ERR_INVALID, "%s too large", names[i]);
+  }
+  return WKV7_OK;
+}
+
+// Fills a shape; nseq < 0 for dense batches.
+int set_shape(Shape& s, int B, int T, int Hk, int Hv, int K, int V, int nseq) {
+  int rc = check_dims(B, T, Hk, Hv, K, V, "B");
+  if (rc) return rc;
+  if (nseq >= 0 && B != 1) return fail(WKV7_ERR_INVALID, "packed sequences lie in one batch row (got B = %d)", B);
+  s = Shape{};
+  s.B = B, s.T = T, s.Hk = Hk, s.Hv = Hv, s.K = K, s.V = V;
+  s.nseq = nseq >= 0 ? nseq : B;
+  s.packed = nseq >= 0;
+  const unsigned long long slots = slot_count(B, T, s.nseq, s.packed), heads = Hv ? Hv : 1;
+  if (slots * heads * 2 >= kMaxBlocks || (unsigned long long)s.nseq * heads * 16 >= kMaxBlocks)
+    return fail(WKV7_ERR_INVALID, "too many chunks");
+  s.slots = (int)slots;
+  return WKV7_OK;
+}
+
+struct Place {
+  char* at;
+  char* const start;
+  template <typename T>
+  void take(T*& p, size_t count) {
+    p = reinterpret_cast<T*>(at);
+    at += (count * sizeof(T) + 127) & ~(size_t)127;
+  }
+};
+// The regions of `saved`, and of the backward's workspace, from p on; returns the bytes.
+size_t place_saved(Args& a, char* p) {
+  const Shape& s = a.s;
+  Place x{p, p};
+  x.take(a.states, (size_t)s.slots * s.Hv * s.V * s.K);
+  x.take(a.decay, (size_t)s.slots * s.Hv);
+  return x.at - x.start;
+}
+size_t place_workspace(Args& a, char* p) {
+  const Shape& s = a.s;
+  Place x{p, p};
+  x.take(a.dstates, (size_t)s.slots * s.Hv * s.V * s.K);
+  x.take(a.decay, (size_t)s.slots * s.Hv);
+  if (s.fixed) {
+    x.take(a.dg, (size_t)s.B * s.T * s.Hv);
+    x.take(a.part, (size_t)kParts * s.Hv);
+  }
+  return x.at - x.start;
+}
+
+int zero_all(std::initializer_list<Span> outs, cudaStream_t stream) {
+  for (const Span& x : outs) {
+    const cudaError_t e = x.p && x.bytes ? cudaMemsetAsync(const_cast<void*>(x.p), 0, x.bytes, stream) : cudaSuccess;
+    if (e != cudaSuccess) return fail(WKV7_ERR_CUDA, "%s: %s", x.name, cudaGetErrorString(e));
+  }
+  return WKV7_OK;
+}
+int copy_state(float* dst, const float* src, size_t bytes, cudaStream_t stream) {
+  if (!dst || !bytes) return WKV7_OK;
+  const cudaError_t e = src ? cudaMemcpyAsync(dst, src, bytes, cudaMemcpyDeviceToDevice, stream) : cudaMemsetAsync(dst, 0, bytes, stream);
+  return e == cudaSuccess ? WKV7_OK : fail(WKV7_ERR_CUDA, "state copy: %s", cudaGetErrorString(e));
+}
+int launched(cudaError_t e, const char* what) {
+  return e == cudaSuccess ? WKV7_OK : fail(WKV7_ERR_CUDA, "%s launch: %s", what, cudaGetErrorString(e));
+}
+uint32_t* words(void* p) { return static_cast<uint32_t*>(p); }
+
+}  // namespace
+}  // namespace linattn
+
+using namespace linattn;
+
+extern "C" {
+
+size_t linattn_saved_bytes(int B, int T, int Hk, int Hv, int K, int V, int nseq, int, int) {
+  Args a{};
+  if (set_shape(a.s, B, T, Hk, Hv, K, V, nseq)) return 0;
+  return place_saved(a, nullptr);
+}
+size_t linattn_backward_bytes(int B, int T, int Hk, int Hv, int K, int V, int nseq, int g_fixed, int) {
+  Args a{};
+  if (set_shape(a.s, B, T, Hk, Hv, K, V, nseq)) return 0;
+  a.s.fixed = g_fixed;
+  return place_workspace(a, nullptr);
+}
+
+int linattn_forward(const void* q, const void* k, const void* v, const float* g, const float* s_init,
+                    const int* seq_starts, void* o, float* s_final, void* saved, const long long* strides, float scale,
+                    int g_fixed, int, int B, int T, int Hk, int Hv, int K, int V, int nseq, int bf16, void* stream_) {
+  const cudaStream_t stream = static_cast<cudaStream_t>(stream_);
+  if (!seq_starts) nseq = -1;
+  if (seq_starts && nseq < 0) return fail(WKV7_ERR_INVALID, "nseq must be >= 0 with seq_starts (got %d)", nseq);
+  Args a{};
+  int rc = set_shape(a.s, B, T, Hk, Hv, K, V, nseq);
+  if (rc) return rc;
+  const int es = bf16 ? 2 : 4;
+  long long st[6];
+  unsigned long long in_bytes[3];
+  if ((rc = set_strides(st, in_bytes, strides, B, T, Hk, Hv, K, V, es))) return rc;
+  const unsigned long long rows = (unsigned long long)B * T * Hv, state = (unsigned long long)a.s.nseq * Hv * V * K * 4;
+  const size_t need = place_saved(a, static_cast<char*>(saved));
+  const Span ins[6] = {{q, in_bytes[0], "q", true}, {k, in_bytes[1], "k", true}, {v, in_bytes[2], "v", true},
+                       {g, rows ? (g_fixed ? Hv : rows) * 4 : 0, "g", true, 4}, {s_init, state, "s_init", false},
+                       {seq_starts, seq_starts ? ((unsigned long long)nseq + 1) * 4 : 0, "seq_starts", false, 4}};
+  const Span outs[3] = {{o, rows * V * es, "o", true}, {s_final, state, "s_final", false}, {saved, rows ? need : 0, "saved", true}};
+  if ((rc = api::check_spans(ins, outs))) return rc;
+  if (!Hv) return WKV7_OK;
+  if (!a.s.nseq) return zero_all({outs[0]}, stream);
+  if (!rows) return copy_state(s_final, s_init, state, stream);
+  a.s.starts = seq_starts, a.s.scale = scale, a.s.fixed = g_fixed;
+  a.s.q_b = st[0], a.s.q_t = st[1], a.s.k_b = st[2], a.s.k_t = st[3], a.s.v_b = st[4], a.s.v_t = st[5];
+  a.q = q, a.k = k, a.v = v, a.g = g, a.s_init = s_init, a.o = o, a.s_final = s_final;
+  if ((rc = launched(launch_states(a, bf16, false, stream), "states"))) return rc;
+  if ((rc = launched(launch_o(a, bf16, stream), "forward")) || !a.s.packed) return rc;
+  return launched(launch_gaps(a, Gaps{{words(o)}, {(long long)Hv * V * es / 4}}, stream), "gaps");
+}
+
+int linattn_backward(const void* q, const void* k, const void* v, const float* g, const void* d_o,
+                     const float* dS_final, const int* seq_starts, const void* saved, void* workspace, void* dq,
+                     void* dk, void* dv, float* dg, float* dS_init, const long long* strides, float scale, int g_fixed,
+                     int B, int T, int Hk, int Hv, int K, int V, int nseq, int bf16, void* stream_) {
+  const cudaStream_t stream = static_cast<cudaStream_t>(stream_);
+  if (!seq_starts) nseq = -1;
+  if (seq_starts && nseq < 0) return fail(WKV7_ERR_INVALID, "nseq must be >= 0 with seq_starts (got %d)", nseq);
+  Args a{};
+  int rc = set_shape(a.s, B, T, Hk, Hv, K, V, nseq);
+  if (rc) return rc;
+  a.s.fixed = g_fixed;
+  const int es = bf16 ? 2 : 4;
+  long long st[6];
+  unsigned long long in_bytes[3];
+  if ((rc = set_strides(st, in_bytes, strides, B, T, Hk, Hv, K, V, es))) return rc;
+  const unsigned long long rows = (unsigned long long)B * T * Hv, keys = (unsigned long long)B * T * Hk * K * es,
+                           state = (unsigned long long)a.s.nseq * Hv * V * K * 4,
+                           gs = (g_fixed ? Hv : rows) * 4;
+  const size_t have = place_saved(a, const_cast<char*>(static_cast<const char*>(saved)));
+  const size_t need = place_workspace(a, static_cast<char*>(workspace));
+  const Span ins[8] = {{q, in_bytes[0], "q", true}, {k, in_bytes[1], "k", true}, {v, in_bytes[2], "v", true},
+                       {g, rows ? gs : 0, "g", true, 4}, {d_o, rows * V * es, "d_o", true}, {dS_final, state, "dS_final", false},
+                       {seq_starts, seq_starts ? ((unsigned long long)nseq + 1) * 4 : 0, "seq_starts", false, 4},
+                       {saved, rows ? have : 0, "saved", true}};
+  const Span outs[6] = {{dq, keys, "dq", true}, {dk, keys, "dk", true}, {dv, rows * V * es, "dv", true},
+                        {dg, gs, "dg", false, 4}, {dS_init, state, "dS_init", false}, {workspace, rows ? need : 0, "workspace", true}};
+  if ((rc = api::check_spans(ins, outs))) return rc;
+  if (!Hv) return WKV7_OK;
+  if (!a.s.nseq) return zero_all({outs[0], outs[1], outs[2], outs[3]}, stream);
+  if (!rows) {
+    if (g_fixed && (rc = zero_all({outs[3]}, stream))) return rc;
+    return copy_state(dS_init, dS_final, state, stream);
+  }
+  a.s.starts = seq_starts, a.s.scale = scale;
+  a.s.q_b = st[0], a.s.q_t = st[1], a.s.k_b = st[2], a.s.k_t = st[3], a.s.v_b = st[4], a.s.v_t = st[5];
+  a.q = q, a.k = k, a.v = v, a.g = g, a.d_o = d_o, a.dS_final = dS_final;
+  a.dq = dq, a.dk = dk, a.dv = dv, a.dS_init = dS_init;
+  if (g_fixed)
+    a.dg_fixed = dg;
+  else
+    a.dg = dg;
+  if (!dg) a.dg = nullptr;
+  if ((rc = launched(launch_states(a, bf16, true, stream), "states"))) return rc;
+  if ((rc = launched(launch_grad(a, bf16, stream), "gradients"))) return rc;
+  if (a.s.packed) {
+    const long long wk = (long long)Hk * K * es / 4, wv = (long long)Hv * V * es / 4;
+    const Gaps gaps{{words(dq), words(dk), words(dv), words(a.dg)}, {wk, wk, wv, Hv}};
+    if ((rc = launched(launch_gaps(a, gaps, stream), "gaps"))) return rc;
+  }
+  return a.dg_fixed ? launched(launch_dg_sums(a, stream), "sums of dg") : WKV7_OK;
+}
+
+int linattn_step(const void* q, const void* k, const void* v, const float* g, float* state, const int* slots, void* o,
+                 const long long* strides, float scale, int g_fixed, int R, int T, int Hk, int Hv, int K, int V,
+                 int n_slots, int bf16, void* stream) {
+  int rc = check_dims(R, T, Hk, Hv, K, V, "R");
+  if (rc) return rc;
+  if (n_slots < 0 || (!slots && R > n_slots)) return fail(WKV7_ERR_INVALID, "%d states for %d requests", n_slots, R);
+  const int es = bf16 ? 2 : 4;
+  long long st[6];
+  unsigned long long in_bytes[3];
+  if ((rc = set_strides(st, in_bytes, strides, R, T, Hk, Hv, K, V, es))) return rc;
+  const unsigned long long rows = (unsigned long long)R * T * Hv, pool = (unsigned long long)n_slots * Hv * V * K * 4;
+  if (pool >= kMaxBytes || (unsigned long long)R * Hv * 16 >= kMaxBlocks) return fail(WKV7_ERR_INVALID, "too many states");
+  const Span ins[5] = {{q, in_bytes[0], "q", true}, {k, in_bytes[1], "k", true}, {v, in_bytes[2], "v", true},
+                       {g, rows ? (g_fixed ? Hv : rows) * 4 : 0, "g", true, 4}, {slots, (unsigned long long)R * 4, "slots", false, 4}};
+  const Span outs[2] = {{state, pool, "state", rows != 0}, {o, rows * V * es, "o", true}};
+  if ((rc = api::check_spans(ins, outs))) return rc;
+  if (!rows) return WKV7_OK;
+  StepArgs a{};
+  a.q = q, a.k = k, a.v = v, a.g = g, a.state = state, a.slots = slots, a.o = o;
+  a.R = R, a.T = T, a.Hk = Hk, a.Hv = Hv, a.K = K, a.V = V, a.n_slots = n_slots, a.fixed = g_fixed, a.scale = scale;
+  a.q_b = st[0], a.q_t = st[1], a.k_b = st[2], a.k_t = st[3], a.v_b = st[4], a.v_t = st[5];
+  return launched(launch_step(a, bf16, static_cast<cudaStream_t>(stream)), "step");
+}
+
+}  // extern "C"

@@ -1,0 +1,87 @@
+// Internal launch interface of linear attention with a decay between the C ABI
+// (linattn_api.cu) and its kernels.
+#pragma once
+
+#include <atomic>
+
+#include <cuda_runtime.h>
+#include <stddef.h>
+#include <stdint.h>
+
+namespace linattn {
+
+constexpr int kC = 64;        // tokens of a chunk
+constexpr int kMaxDim = 128;  // largest head size
+
+// What a call's sequences and heads look like.
+struct Shape {
+  int B, T, Hk, Hv, K, V;
+  int nseq;           // sequences: B, or those packed in the one batch row
+  const int* starts;  // device [nseq + 1], or null
+  int slots;          // chunk slots: an upper bound of the chunks, see slot_count
+  int packed;         // nseq sequences in one batch row
+  int fixed;          // g is [Hv], one number a head
+  float scale;
+  long long q_b, q_t, k_b, k_t, v_b, v_t;  // element strides of a batch row and of a token
+};
+
+// Every sequence's chunks get slots of their own. Dense: batch * ceil(T / kC).
+// Packed: a sequence that starts at token x is given the slots from x / kC + s
+// on (s its number): x / kC + ceil(len / kC) <= (x + len) / kC + 1, so the next
+// sequence's slots start after them, and T / kC + nseq are enough.
+inline long long slot_count(int B, int T, int nseq, bool packed) {
+  return packed ? (long long)T / kC + nseq : (long long)B * ((T + kC - 1) / kC);
+}
+
+struct Args {
+  Shape s;
+  const void *q, *k, *v, *d_o;
+  const float *g, *s_init, *dS_final;
+  void *o, *dq, *dk, *dv;
+  float *s_final, *dS_init;
+  float *dg;           // [B][T][Hv] (a workspace where g is fixed)
+  float *dg_fixed;     // [Hv], where g is fixed
+  float *states;       // [slots][Hv][V][K]: the state before each chunk
+  float *dstates;      // the gradient of the state after each chunk
+  float *decay;        // [slots][Hv]: the whole decay of each chunk
+  double *part;        // [kParts][Hv]: sums of dg over tokens
+};
+constexpr int kParts = 256;
+
+cudaError_t launch_states(const Args& a, bool bf16, bool backward, cudaStream_t stream);  // states or dstates; s_final or dS_init
+cudaError_t launch_o(const Args& a, bool bf16, cudaStream_t stream);
+cudaError_t launch_grad(const Args& a, bool bf16, cudaStream_t stream);  // dv, dq, dk, dg
+cudaError_t launch_dg_sums(const Args& a, cudaStream_t stream);          // dg_fixed from dg
+
+// Zeros in up to five outputs of a packed call at the tokens of no sequence.
+struct Gaps {
+  uint32_t* at[5];
+  long long words[5];  // of a token
+};
+cudaError_t launch_gaps(const Args& a, const Gaps& g, cudaStream_t stream);
+
+struct StepArgs {
+  const void *q, *k, *v;
+  const float* g;
+  float* state;
+  const int* slots;
+  void* o;
+  int R, T, Hk, Hv, K, V, n_slots, fixed;
+  float scale;
+  long long q_b, q_t, k_b, k_t, v_b, v_t;
+};
+cudaError_t launch_step(const StepArgs& a, bool bf16, cudaStream_t stream);
+
+// Allows a kernel its dynamic shared memory, once a device; `done` belongs to the kernel.
+inline cudaError_t allow_smem(const void* kernel, size_t bytes, std::atomic<unsigned long long>& done) {
+  int dev = 0;
+  cudaError_t e = cudaGetDevice(&dev);
+  if (e != cudaSuccess) return e;
+  const unsigned long long bit = 1ull << (dev & 63);
+  if (done.load(std::memory_order_acquire) & bit) return cudaSuccess;
+  e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)bytes);
+  if (e == cudaSuccess) done.fetch_or(bit, std::memory_order_release);
+  return e;
+}
+
+}  // namespace linattn

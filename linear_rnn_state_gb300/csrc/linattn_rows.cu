@@ -1,0 +1,353 @@
+// Linear attention with a decay: the rows of o, dq, dk and dv of every chunk, all chunks at once.
+//
+// Each is a masked product of the chunk's own tokens and one with a state. With G the running sum of the
+// chunk's log decays, Gc the whole sum, S the state before the chunk and D the gradient of the state after it:
+//   o_i  = sum_{j<=i} scale e^{G_i - G_j} (q_i.k_j) v_j   + scale e^{G_i} S q_i
+//   dq_i = sum_{j<=i} scale e^{G_i - G_j} (do_i.v_j) k_j  + scale e^{G_i} S^T do_i
+//   dv_j = sum_{i>=j} scale e^{G_i - G_j} (k_j.q_i) do_i  + e^{Gc - G_j} D k_j
+//   dk_j = sum_{i>=j} scale e^{G_i - G_j} (v_j.do_i) q_i  + e^{Gc - G_j} D^T v_j
+// A log decay g_t moves whatever passes it: pairs j < t <= i of the chunk, the state's part that is read
+// from t on, what is written before t and read after the chunk, and what passes the whole chunk,
+//   dg_t = sum_{j<t<=i} X_ij + sum_{i>=t} q_i.(scale e^{G_i} S^T do_i) + sum_{j<t} k_j.(e^{Gc - G_j} D^T v_j)
+//          + e^{Gc} <S, D>,   X_ij = scale e^{G_i - G_j} (q_i.k_j)(do_i.v_j),
+// all of them sums: no differences of large ones.
+#include "linattn_common.cuh"
+
+namespace linattn {
+namespace {
+
+constexpr int kThreads = 128;
+enum Mode { kO, kDv, kDq, kDk };
+
+template <typename T>
+__device__ __forceinline__ void store2(T* p, float x, float y);
+template <>
+__device__ __forceinline__ void store2<bf16_t>(bf16_t* p, float x, float y) {
+  *reinterpret_cast<uint32_t*>(p) = pack2(x, y);
+}
+template <>
+__device__ __forceinline__ void store2<float>(float* p, float x, float y) {
+  *reinterpret_cast<float2*>(p) = make_float2(x, y);
+}
+__device__ __forceinline__ float2 load2(const bf16_t* p) { return unpack2(*reinterpret_cast<const uint32_t*>(p)); }
+__device__ __forceinline__ float2 load2(const float* p) { return *reinterpret_cast<const float2*>(p); }
+
+template <typename T>
+struct Tokens {  // a chunk's rows of one head
+  const T* p;
+  long long stride;
+  int cols;
+};
+
+// What a block keeps in shared memory; D: the (padded) size of the products' inner dimension.
+template <typename T, int kStateParts>
+struct Layout {
+  static constexpr int kP = In<T>::kParts;
+  __host__ __device__ static constexpr size_t a(int) { return 0; }
+  __host__ __device__ static constexpr size_t b(int D) { return (size_t)kP * kC * D * 2; }
+  __host__ __device__ static constexpr size_t x(int D) { return 2 * b(D); }
+  __host__ __device__ static constexpr size_t s(int D) { return x(D) + (size_t)kP * kC * 64 * 2; }
+  __host__ __device__ static constexpr size_t g(int D) { return s(D) + (size_t)kStateParts * 64 * D * 2; }
+  __host__ __device__ static constexpr size_t size(int D) { return g(D) + kC * 8 + kC * 4 + 6 * kC * 4; }
+};
+
+// rows += a b^T of the warp's 16 rows and the columns that the mask leaves it.
+template <int kP, bool kUpper>
+__device__ __forceinline__ void scores(float (&x)[8][4], const bf16_t* as, const bf16_t* bs, int D, int Dp, int warp, int lane) {
+  zero(x);
+  for (int k0 = 0; k0 < D; k0 += 16) {
+    Frag<kP> fa;
+    a_mk(fa, as, kC, kC * Dp, 16 * warp, k0, lane);
+#pragma unroll
+    for (int n = 0; n < 4; ++n)
+      if (kUpper ? n >= warp : n <= warp) {
+        Frag<kP> fb;
+        b_nk(fb, bs, kC, kC * Dp, 16 * n, k0, lane);
+        mma_parts(x[2 * n], x[2 * n + 1], fa, fb);
+      }
+  }
+}
+
+// A block: a chunk and a value head (o, dv), or a key head with all its value heads (dq, dk). 16 tokens a
+// warp; kSlices x 64 columns of the output.
+template <typename T, int kMode, int kSlices>
+__global__ void __launch_bounds__(kThreads) rows_kernel(const Args a) {
+  constexpr bool kUpper = kMode == kDv || kMode == kDk, kKeys = kMode == kDq || kMode == kDk;  // kKeys: the output is a key's
+  constexpr int kP = In<T>::kParts, kPc = kP == 1 ? 2 : 3, kPs = kKeys ? 3 : kPc;
+  using L = Layout<T, kPs>;
+  extern __shared__ __align__(128) unsigned char smem[];
+  const Shape& s = a.s;
+  const int D = kKeys ? s.V : s.K, Dx = kKeys ? s.K : s.V, Dp = (D + 63) & ~63;
+  bf16_t* as = reinterpret_cast<bf16_t*>(smem);
+  bf16_t* bs = reinterpret_cast<bf16_t*>(smem + L::b(Dp));
+  bf16_t* xs = reinterpret_cast<bf16_t*>(smem + L::x(Dp));
+  bf16_t* ss = reinterpret_cast<bf16_t*>(smem + L::s(Dp));
+  float2* G = reinterpret_cast<float2*>(smem + L::g(Dp));
+  float* w = reinterpret_cast<float*>(G + kC);
+  float* red = w + kC;  // [6][kC]: dg of the warps' rows, the rows' terms, the state's
+  const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5, gr = lane >> 2, tq = lane & 3;
+  const int heads = kKeys ? s.Hk : s.Hv, head = blockIdx.x % heads, slot = blockIdx.x / heads, group = s.Hv / s.Hk;
+  ChunkAt c;
+  if (!chunk_at(s, slot, c)) return;
+  const size_t tok = (size_t)c.b * s.T + c.t0;
+  float acc[kSlices][8][4];
+#pragma unroll
+  for (int i = 0; i < kSlices; ++i) zero(acc[i]);
+  const int hk = kKeys ? head : head / group;
+  const Tokens<T> q{static_cast<const T*>(a.q) + c.b * s.q_b + c.t0 * s.q_t + (size_t)hk * s.K, s.q_t, s.K};
+  const Tokens<T> k{static_cast<const T*>(a.k) + c.b * s.k_b + c.t0 * s.k_t + (size_t)hk * s.K, s.k_t, s.K};
+  for (int hv = kKeys ? hk * group : head; hv < (kKeys ? (hk + 1) * group : head + 1); ++hv) {
+    const Tokens<T> v{static_cast<const T*>(a.v) + c.b * s.v_b + c.t0 * s.v_t + (size_t)hv * s.V, s.v_t, s.V};
+    const Tokens<T> d{static_cast<const T*>(a.d_o) + (tok * s.Hv + hv) * s.V, (long long)s.Hv * s.V, s.V};
+    const Tokens<T>&ta = kMode == kO ? q : kMode == kDv ? k : kMode == kDq ? d : v;
+    const Tokens<T>&tb = kMode == kO ? k : kMode == kDv ? q : kMode == kDq ? v : d;
+    const Tokens<T>&tx = kMode == kO ? v : kMode == kDv ? d : kMode == kDq ? k : q;
+    const float* state = (kUpper ? a.dstates : a.states) + ((size_t)slot * s.Hv + hv) * s.V * s.K;
+    const bool dg = kKeys && a.dg;
+    __syncthreads();  // the head before is done with shared memory
+    if (warp == 0) {
+      running_sums(G, s.fixed ? a.g + hv : a.g + tok * s.Hv + hv, s.fixed ? 0 : s.Hv, c.len, lane);
+      __syncwarp();
+#pragma unroll
+      for (int j = lane; j < kC; j += 32) w[j] = kUpper ? expf(minus(G[kC - 1], G[j])) : s.scale * expf(G[j].x + G[j].y);
+    }
+    float qk[8][4];
+    if (kMode == kDq && dg) {
+      const int Kp = (s.K + 63) & ~63;
+      if (Kp <= Dp) {
+        fill_tile<kP>(as, q.p, q.stride, c.len, s.K, nullptr, tid, kThreads);
+        fill_tile<kP>(bs, k.p, k.stride, c.len, s.K, nullptr, tid, kThreads);
+        __syncthreads();
+        scores<kP, false>(qk, as, bs, s.K, Kp, warp, lane);
+      } else {  // in two halves
+        for (int h = 0; h < 2; ++h) {
+          fill_tile<kP>(as, q.p + 64 * h, q.stride, c.len, h ? s.K - 64 : 64, nullptr, tid, kThreads);
+          fill_tile<kP>(bs, k.p + 64 * h, k.stride, c.len, h ? s.K - 64 : 64, nullptr, tid, kThreads);
+          __syncthreads();
+          float half[8][4];
+          scores<kP, false>(half, as, bs, h ? s.K - 64 : 64, 64, warp, lane);
+#pragma unroll
+          for (int n = 0; n < 8; ++n)
+#pragma unroll
+            for (int e = 0; e < 4; ++e) qk[n][e] = h ? qk[n][e] + half[n][e] : half[n][e];
+          __syncthreads();
+        }
+      }
+      __syncthreads();
+    }
+    fill_tile<kP>(as, ta.p, ta.stride, c.len, D, nullptr, tid, kThreads);
+    fill_tile<kP>(bs, tb.p, tb.stride, c.len, D, nullptr, tid, kThreads);
+    __syncthreads();
+    Frag<kPc> pf[4];
+    {
+      float x[8][4];
+      scores<kP, kUpper>(x, as, bs, D, Dp, warp, lane);
+#pragma unroll
+      for (int h = 0; h < 2; ++h) {
+        const int i = 16 * warp + gr + 8 * h;
+        const float2 Gi = G[i];
+        const float sc = s.scale;
+        float run = 0.f;  // of the row's X so far
+#pragma unroll
+        for (int n = 0; n < 8; ++n) {
+          float y[2];
+#pragma unroll
+          for (int e = 0; e < 2; ++e) {
+            const int j = 8 * n + 2 * tq + e;
+            const bool keep = kUpper ? j >= i : j <= i;
+            y[e] = keep ? x[n][2 * h + e] * sc * expf(kUpper ? minus(G[j], Gi) : minus(Gi, G[j])) : 0.f;
+            x[n][2 * h + e] = y[e];
+          }
+          if (kMode == kDq && dg) {  // qk: the sums over j' < j of X_ij', where j <= i
+            const int j = 8 * n + 2 * tq;
+            const float z0 = j < i ? y[0] * qk[n][2 * h] : 0.f, z1 = j + 1 < i ? y[1] * qk[n][2 * h + 1] : 0.f;
+            float p = z0 + z1, up = __shfl_up_sync(0xffffffffu, p, 1, 4);
+            if (tq >= 1) p += up;
+            up = __shfl_up_sync(0xffffffffu, p, 2, 4);
+            if (tq >= 2) p += up;
+            up = __shfl_up_sync(0xffffffffu, p, 1, 4);
+            const float before = run + (tq ? up : 0.f);
+            qk[n][2 * h] = j <= i ? before : 0.f;
+            qk[n][2 * h + 1] = j + 1 <= i ? before + z0 : 0.f;
+            run += __shfl_sync(0xffffffffu, p, 3, 4);
+          }
+        }
+      }
+#pragma unroll
+      for (int n = 0; n < 4; ++n) to_a(pf[n], x[2 * n], x[2 * n + 1]);
+    }
+    if (kMode == kDq && dg) {  // over the warp's rows
+#pragma unroll
+      for (int n = 0; n < 8; ++n)
+#pragma unroll
+        for (int e = 0; e < 2; ++e) {
+          float x = qk[n][e] + qk[n][2 + e];
+          x += __shfl_xor_sync(0xffffffffu, x, 4);
+          x += __shfl_xor_sync(0xffffffffu, x, 8);
+          x += __shfl_xor_sync(0xffffffffu, x, 16);
+          if (gr == 0) red[warp * kC + 8 * n + 2 * tq + e] = x;
+        }
+    }
+    float dots[2] = {0.f, 0.f}, whole = 0.f;
+#pragma unroll
+    for (int sl = 0; sl < kSlices; ++sl) {
+      const int x0 = 64 * sl, xn = min(64, Dx - x0);
+      __syncthreads();
+      fill_tile<kP>(xs, tx.p + x0, tx.stride, c.len, xn, nullptr, tid, kThreads);
+      // the state's slice: rows of values and 64 keys (kKeys), or 64 rows and all keys
+      const int rows = kKeys ? Dp : 64, pieces = kKeys ? 8 : Dp / 8;
+      for (int i = tid; i < rows * pieces; i += kThreads) {
+        const int r = i / pieces, col = (i - r * pieces) * 8;
+        const int sr = kKeys ? r : x0 + r, scol = kKeys ? x0 + col : col;
+        float f[8] = {0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f};
+        if (sr < s.V && scol < s.K) {
+          load8(f, state + (size_t)sr * s.K + scol);
+          if (kMode == kDq && dg) {
+            float f2[8];
+            load8(f2, a.dstates + ((size_t)slot * s.Hv + hv) * s.V * s.K + (size_t)sr * s.K + scol);
+#pragma unroll
+            for (int e = 0; e < 8; ++e) whole = fmaf(f[e], f2[e], whole);
+          }
+        }
+        put8<kPs>(ss + at(rows, r, col), 64 * Dp, f);
+      }
+      __syncthreads();
+#pragma unroll
+      for (int n = 0; n < 4; ++n)
+        if (16 * n < xn) {
+          float y0[4] = {0.f, 0.f, 0.f, 0.f}, y1[4] = {0.f, 0.f, 0.f, 0.f};
+          for (int k0 = 0; k0 < D; k0 += 16) {
+            Frag<kP> fa;
+            Frag<kPs> fb;
+            a_mk(fa, as, kC, kC * Dp, 16 * warp, k0, lane);
+            if (kKeys)
+              b_kn(fb, ss, Dp, 64 * Dp, 16 * n, k0, lane);
+            else
+              b_nk(fb, ss, 64, 64 * Dp, 16 * n, k0, lane);
+            mma_parts(y0, y1, fa, fb);
+          }
+          const float w0 = w[16 * warp + gr], w1 = w[16 * warp + gr + 8];
+#pragma unroll
+          for (int e = 0; e < 4; ++e) {
+            y0[e] *= e < 2 ? w0 : w1, y1[e] *= e < 2 ? w0 : w1;
+            acc[sl][2 * n][e] += y0[e], acc[sl][2 * n + 1][e] += y1[e];
+          }
+          if (dg) {  // q.(the state's part of dq), or k.(that of dk)
+            const Tokens<T>& t = kMode == kDq ? q : k;
+#pragma unroll
+            for (int h = 0; h < 2; ++h) {
+              const int row = 16 * warp + gr + 8 * h, col = x0 + 16 * n + 2 * tq;
+              if (row < c.len) {
+                const T* p = t.p + row * t.stride + col;
+                if (col < Dx) {
+                  const float2 z = load2(p);
+                  dots[h] = fmaf(z.x, y0[2 * h], fmaf(z.y, y0[2 * h + 1], dots[h]));
+                }
+                if (col + 8 < Dx) {
+                  const float2 z = load2(p + 8);
+                  dots[h] = fmaf(z.x, y1[2 * h], fmaf(z.y, y1[2 * h + 1], dots[h]));
+                }
+              }
+            }
+          }
+#pragma unroll
+          for (int j = 0; j < 4; ++j)
+            if (kUpper ? j >= warp : j <= warp) {
+              Frag<kP> fx;
+              b_kn(fx, xs, kC, kC * 64, 16 * n, 16 * j, lane);
+              mma_parts(acc[sl][2 * n], acc[sl][2 * n + 1], pf[j], fx);
+            }
+        }
+    }
+    if (dg) {
+#pragma unroll
+      for (int h = 0; h < 2; ++h) {
+        float x = dots[h];
+        x += __shfl_xor_sync(0xffffffffu, x, 1);
+        x += __shfl_xor_sync(0xffffffffu, x, 2);
+        if (tq == 0) red[4 * kC + 16 * warp + gr + 8 * h] = x;
+      }
+      if (kMode == kDq) {
+#pragma unroll
+        for (int o = 16; o >= 1; o >>= 1) whole += __shfl_xor_sync(0xffffffffu, whole, o);
+        if (lane == 0) red[5 * kC + warp] = whole;
+      }
+      __syncthreads();
+      if (warp == 0) {  // two tokens a lane
+        float* out = a.dg + tok * s.Hv + hv;
+        const float x0 = red[4 * kC + 2 * lane], x1 = red[4 * kC + 2 * lane + 1];
+        float run = x0 + x1;
+#pragma unroll
+        for (int o = 1; o < 32; o <<= 1) {
+          const float y = kMode == kDq ? __shfl_down_sync(0xffffffffu, run, o) : __shfl_up_sync(0xffffffffu, run, o);
+          if (kMode == kDq ? lane + o < 32 : lane >= o) run += y;
+        }
+        float other = kMode == kDq ? __shfl_down_sync(0xffffffffu, run, 1) : __shfl_up_sync(0xffffffffu, run, 1);
+        if (lane == (kMode == kDq ? 31 : 0)) other = 0.f;
+        const float y0 = kMode == kDq ? run : other, y1 = kMode == kDq ? other + x1 : other + x0;
+        const float pass = kMode == kDq ? expf(G[kC - 1].x + G[kC - 1].y) * ((red[5 * kC] + red[5 * kC + 1]) + (red[5 * kC + 2] + red[5 * kC + 3])) : 0.f;
+#pragma unroll
+        for (int e = 0; e < 2; ++e) {
+          const int t = 2 * lane + e;
+          if (t < c.len) {
+            float x = (e ? y1 : y0) + pass;
+            if (kMode == kDq)
+              x += (red[t] + red[kC + t]) + (red[2 * kC + t] + red[3 * kC + t]);
+            else
+              x += out[(size_t)t * s.Hv];
+            out[(size_t)t * s.Hv] = x;
+          }
+        }
+      }
+    }
+  }
+  T* out = kMode == kO   ? static_cast<T*>(a.o)
+           : kMode == kDv ? static_cast<T*>(a.dv)
+           : kMode == kDq ? static_cast<T*>(a.dq)
+                          : static_cast<T*>(a.dk);
+  out += (tok * heads + head) * Dx;
+#pragma unroll
+  for (int sl = 0; sl < kSlices; ++sl)
+#pragma unroll
+    for (int n = 0; n < 8; ++n)
+#pragma unroll
+      for (int h = 0; h < 2; ++h) {
+        const int row = 16 * warp + gr + 8 * h, col = 64 * sl + 8 * n + 2 * tq;
+        if (row < c.len && col < Dx) store2(out + (size_t)row * heads * Dx + col, acc[sl][n][2 * h], acc[sl][n][2 * h + 1]);
+      }
+}
+
+template <typename T, int kMode, int kSlices>
+cudaError_t launch(const Args& a, cudaStream_t stream) {
+  constexpr bool kKeys = kMode == kDq || kMode == kDk;
+  using L = Layout<T, kKeys ? 3 : In<T>::kParts == 1 ? 2 : 3>;
+  const int D = kKeys ? a.s.V : a.s.K;
+  static std::atomic<unsigned long long> done{0};
+  const cudaError_t e = allow_smem(reinterpret_cast<const void*>(rows_kernel<T, kMode, kSlices>), L::size(kMaxDim), done);
+  if (e != cudaSuccess) return e;
+  rows_kernel<T, kMode, kSlices><<<(unsigned)((size_t)a.s.slots * (kKeys ? a.s.Hk : a.s.Hv)), kThreads, L::size((D + 63) & ~63), stream>>>(a);
+  return cudaGetLastError();
+}
+template <typename T, int kMode>
+cudaError_t pick(const Args& a, cudaStream_t stream) {
+  const int Dx = kMode == kDq || kMode == kDk ? a.s.K : a.s.V;
+  return Dx <= 64 ? launch<T, kMode, 1>(a, stream) : launch<T, kMode, 2>(a, stream);
+}
+template <typename T>
+cudaError_t grad(const Args& a, cudaStream_t stream) {
+  cudaError_t e = pick<T, kDv>(a, stream);
+  if (e == cudaSuccess) e = pick<T, kDq>(a, stream);
+  if (e == cudaSuccess) e = pick<T, kDk>(a, stream);
+  return e;
+}
+
+}  // namespace
+
+cudaError_t launch_o(const Args& a, bool bf16, cudaStream_t stream) {
+  return bf16 ? pick<bf16_t, kO>(a, stream) : pick<float, kO>(a, stream);
+}
+cudaError_t launch_grad(const Args& a, bool bf16, cudaStream_t stream) {
+  return bf16 ? grad<bf16_t>(a, stream) : grad<float>(a, stream);
+}
+
+}  // namespace linattn
