@@ -33,11 +33,12 @@ SOURCES = ["wkv7_api.cu", "wkv7_fwd2.cu", "wkv7_fwd3.cu", "wkv7_bwd2.cu", "wkv7_
            "wkv7_bwd4_f32.cu", "rwkv8_api.cu",
            "rwkv8_fwd.cu", "rwkv8_bwd.cu", "rwkv8_bwd_split.cu", "rwkv8_state.cu", "rwkv8_chunk.cu", "wkv7_epilogue.cu",
            "gdr_api.cu", "gdr_prep.cu", "gdr_fwd.cu", "gdr_bwd.cu", "gdr_grad.cu", "gdr_step.cu", "blocknorm_api.cu",
-           "blocknorm.cu", "linattn_api.cu", "linattn_states.cu", "linattn_rows.cu", "linattn_step.cu",
+           "blocknorm.cu", "linattn_api.cu", "linattn_states.cu", "linattn_rows.cu", "linattn_chain.cu", "linattn_grad.cu",
+           "linattn_step.cu",
            "qkrope_api.cu", "qkrope.cu"]
 HEADERS = ["wkv7_common.cuh", "wkv7_launch.h", "wkv7_mma.cuh", "wkv7_scaled.cuh", "wkv7_tmem.cuh", "wkv7_decay.cuh",
            "rwkv8_launch.h", "rwkv8_split.cuh", "api_check.h", "gdr_launch.h", "gdr_common.cuh", "gdr_chain.cuh", "gdr_tc.cuh", "blocknorm_launch.h",
-           "linattn_launch.h", "linattn_common.cuh", "qkrope_launch.h"]
+           "linattn_launch.h", "linattn_common.cuh", "linattn_tc.cuh", "qkrope_launch.h"]
 
 ARCH = ["-gencode", "arch=compute_103a,code=sm_103a"]
 NVCC_FLAGS = ARCH + ["-O3", "-lineinfo", "-std=c++17", "-Xcompiler", "-fPIC", "-cudart", "shared",

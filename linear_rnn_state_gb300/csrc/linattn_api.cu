@@ -19,7 +19,7 @@ int check_dims(int B, int T, int Hk, int Hv, int K, int V, const char* rows) {
   if (Hk > Hv || (Hk ? Hv % Hk : Hv)) return fail(WKV7_ERR_INVALID, "Hv must be a multiple of Hk (got %d, %d)", Hv, Hk);
   if (K < 8 || K > kMaxDim || K % 8 || V < 8 || V > kMaxDim || V % 8)
     return fail(WKV7_ERR_INVALID, "K and V must be multiples of 8 from 8 to %d (got %d, %d)", kMaxDim, K, V);
-  if ((unsigned long long)B * T >= 1ull << 40 || (unsigned long long)B * T * Hv >= kMaxBytes / (4 * kMaxDim))
+  if (T > 1 << 30 || (unsigned long long)B * T >= 1ull << 40 || (unsigned long long)B * T * Hv >= kMaxBytes / (4 * kMaxDim))
     return fail(WKV7_ERR_INVALID, "%s * T * Hv too large", rows);
   return WKV7_OK;
 }
@@ -45,7 +45,7 @@ int set_strides(long long (&out)[6], unsigned long long (&bytes)[3], const long 
 }
 
 // Fills a shape; nseq < 0 for dense batches.
-int set_shape(Shape& s, int B, int T, int Hk, int Hv, int K, int V, int nseq) {
+int set_shape(Shape& s, int B, int T, int Hk, int Hv, int K, int V, int nseq, int bf16) {
   int rc = check_dims(B, T, Hk, Hv, K, V, "B");
   if (rc) return rc;
   if (nseq >= 0 && B != 1) return fail(WKV7_ERR_INVALID, "packed sequences lie in one batch row (got B = %d)", B);
@@ -53,7 +53,8 @@ int set_shape(Shape& s, int B, int T, int Hk, int Hv, int K, int V, int nseq) {
   s.B = B, s.T = T, s.Hk = Hk, s.Hv = Hv, s.K = K, s.V = V;
   s.nseq = nseq >= 0 ? nseq : B;
   s.packed = nseq >= 0;
-  const unsigned long long slots = slot_count(B, T, s.nseq, s.packed), heads = Hv ? Hv : 1;
+  s.C = bf16 ? kCBf16 : kCF32;
+  const unsigned long long slots = slot_count(B, T, s.nseq, s.packed, s.C), heads = Hv ? Hv : 1;
   if (slots * heads * 2 >= kMaxBlocks || (unsigned long long)s.nseq * heads * 16 >= kMaxBlocks)
     return fail(WKV7_ERR_INVALID, "too many chunks");
   s.slots = (int)slots;
@@ -104,6 +105,16 @@ int copy_state(float* dst, const float* src, size_t bytes, cudaStream_t stream) 
 int launched(cudaError_t e, const char* what) {
   return e == cudaSuccess ? WKV7_OK : fail(WKV7_ERR_CUDA, "%s launch: %s", what, cudaGetErrorString(e));
 }
+// bfloat16: the chains of all sequences, heads and slices of 64 values, whole where they fill the GPU, else in segments
+// that begin from states made before.
+int chains(const Args& a, bool backward, bool keep, cudaStream_t stream) {
+  const Shape& s = a.s;
+  const int chunks = (s.T + s.C - 1) / s.C;
+  const long long lines = (long long)s.nseq * s.Hv * ((s.V + 63) / 64);
+  if (lines >= 76 || chunks <= 4) return launched(launch_chain(a, backward, chunks, false, keep, stream), "chain");
+  const int rc = launched(launch_states(a, true, backward, stream), "states");
+  return rc ? rc : launched(launch_chain(a, backward, 2, true, false, stream), "chain");
+}
 uint32_t* words(void* p) { return static_cast<uint32_t*>(p); }
 
 }  // namespace
@@ -113,26 +124,26 @@ using namespace linattn;
 
 extern "C" {
 
-size_t linattn_saved_bytes(int B, int T, int Hk, int Hv, int K, int V, int nseq, int, int) {
+size_t linattn_saved_bytes(int B, int T, int Hk, int Hv, int K, int V, int nseq, int bf16, int) {
   Args a{};
-  if (set_shape(a.s, B, T, Hk, Hv, K, V, nseq)) return 0;
+  if (set_shape(a.s, B, T, Hk, Hv, K, V, nseq, bf16)) return 0;
   return place_saved(a, nullptr);
 }
-size_t linattn_backward_bytes(int B, int T, int Hk, int Hv, int K, int V, int nseq, int g_fixed, int) {
+size_t linattn_backward_bytes(int B, int T, int Hk, int Hv, int K, int V, int nseq, int g_fixed, int bf16) {
   Args a{};
-  if (set_shape(a.s, B, T, Hk, Hv, K, V, nseq)) return 0;
+  if (set_shape(a.s, B, T, Hk, Hv, K, V, nseq, bf16)) return 0;
   a.s.fixed = g_fixed;
   return place_workspace(a, nullptr);
 }
 
 int linattn_forward(const void* q, const void* k, const void* v, const float* g, const float* s_init,
                     const int* seq_starts, void* o, float* s_final, void* saved, const long long* strides, float scale,
-                    int g_fixed, int, int B, int T, int Hk, int Hv, int K, int V, int nseq, int bf16, void* stream_) {
+                    int g_fixed, int for_backward, int B, int T, int Hk, int Hv, int K, int V, int nseq, int bf16, void* stream_) {
   const cudaStream_t stream = static_cast<cudaStream_t>(stream_);
   if (!seq_starts) nseq = -1;
   if (seq_starts && nseq < 0) return fail(WKV7_ERR_INVALID, "nseq must be >= 0 with seq_starts (got %d)", nseq);
   Args a{};
-  int rc = set_shape(a.s, B, T, Hk, Hv, K, V, nseq);
+  int rc = set_shape(a.s, B, T, Hk, Hv, K, V, nseq, bf16);
   if (rc) return rc;
   const int es = bf16 ? 2 : 4;
   long long st[6];
@@ -151,8 +162,13 @@ int linattn_forward(const void* q, const void* k, const void* v, const float* g,
   a.s.starts = seq_starts, a.s.scale = scale, a.s.fixed = g_fixed;
   a.s.q_b = st[0], a.s.q_t = st[1], a.s.k_b = st[2], a.s.k_t = st[3], a.s.v_b = st[4], a.s.v_t = st[5];
   a.q = q, a.k = k, a.v = v, a.g = g, a.s_init = s_init, a.o = o, a.s_final = s_final;
-  if ((rc = launched(launch_states(a, bf16, false, stream), "states"))) return rc;
-  if ((rc = launched(launch_o(a, bf16, stream), "forward")) || !a.s.packed) return rc;
+  if (bf16) {
+    if ((rc = wkv7::api_status_word(&a.status)) || (rc = chains(a, false, for_backward, stream))) return rc;
+  } else {
+    if ((rc = launched(launch_states(a, false, false, stream), "states"))) return rc;
+    if ((rc = launched(launch_rows_o(a, stream), "forward"))) return rc;
+  }
+  if (!a.s.packed) return WKV7_OK;
   return launched(launch_gaps(a, Gaps{{words(o)}, {(long long)Hv * V * es / 4}}, stream), "gaps");
 }
 
@@ -164,7 +180,7 @@ int linattn_backward(const void* q, const void* k, const void* v, const float* g
   if (!seq_starts) nseq = -1;
   if (seq_starts && nseq < 0) return fail(WKV7_ERR_INVALID, "nseq must be >= 0 with seq_starts (got %d)", nseq);
   Args a{};
-  int rc = set_shape(a.s, B, T, Hk, Hv, K, V, nseq);
+  int rc = set_shape(a.s, B, T, Hk, Hv, K, V, nseq, bf16);
   if (rc) return rc;
   a.s.fixed = g_fixed;
   const int es = bf16 ? 2 : 4;
@@ -198,8 +214,13 @@ int linattn_backward(const void* q, const void* k, const void* v, const float* g
   else
     a.dg = dg;
   if (!dg) a.dg = nullptr;
-  if ((rc = launched(launch_states(a, bf16, true, stream), "states"))) return rc;
-  if ((rc = launched(launch_grad(a, bf16, stream), "gradients"))) return rc;
+  if (bf16) {
+    if ((rc = wkv7::api_status_word(&a.status)) || (rc = chains(a, true, true, stream))) return rc;
+    if ((rc = launched(launch_grad(a, stream), "gradients"))) return rc;
+  } else {
+    if ((rc = launched(launch_states(a, false, true, stream), "states"))) return rc;
+    if ((rc = launched(launch_rows_grad(a, stream), "gradients"))) return rc;
+  }
   if (a.s.packed) {
     const long long wk = (long long)Hk * K * es / 4, wv = (long long)Hv * V * es / 4;
     const Gaps gaps{{words(dq), words(dk), words(dv), words(a.dg)}, {wk, wk, wv, Hv}};

@@ -1,0 +1,280 @@
+// Linear attention with a decay, bfloat16: o, and backward dv, from chunk to chunk on tcgen05.
+//
+// A block takes a sequence (or a segment of one), a value head and 64 of its values, and goes through
+// its chunks of 128 tokens with the state in registers. With a, b, x = q, k, v forward and k, q, do
+// backward (there in reverse, the state being the gradient D of the state after the chunk):
+//   P = mask . decay . (a b^T),  out = P x + w . (a S^T),  S <- e^{Gc} S + (u . x)^T b
+// P x and a S^T end as bfloat16 values, so P and S enter them as pairs of bfloat16 (16 bits); u . x enters
+// the state, an fp32 result, in three parts (24 bits).
+//
+// Tensor memory: the scores and then P in their place (128 columns), a S^T (64), P x (64), the state's
+// sum (64 or 128, 64 rows). Products of a chunk that do not wait for P run while it is made.
+#include "linattn_tc.cuh"
+
+namespace linattn {
+namespace {
+
+constexpr int kThreads = 256;
+
+template <int KP>
+struct Smem {
+  static constexpr int kStages = KP == 64 ? 2 : 1;
+  struct Stage {
+    bf16_t a[kCT * KP], b[kCT * KP], x[kCT * 64];
+  };
+  Stage stage[kStages];
+  bf16_t xt[3 * kCT * 64];  // u . x; then the rows on their way out
+  bf16_t s[2 * 64 * KP];    // the state's pair
+  Decays d[2];
+  uint64_t done[3];  // scores; a S^T and the state's sum; P x
+  uint32_t tmem;
+};
+
+struct Plan {
+  int chunks;  // of a segment
+  int resume, keep;
+};
+
+template <int KP, bool kUpper>
+__global__ void __launch_bounds__(kThreads, 1) chain_kernel(const Args a, const Plan plan) {
+  extern __shared__ __align__(1024) unsigned char raw[];
+  Smem<KP>& sm = *reinterpret_cast<Smem<KP>*>(raw);
+  constexpr int kTiles = KP / 16;  // n8 tiles of a warp's half of the keys
+  constexpr int kSt = Smem<KP>::kStages;
+  enum { kP = 0, kIn = 128, kO = 192, kU = 256, kCols = 512 };
+  const Shape& s = a.s;
+  const int tid = threadIdx.x, lane = tid & 31, warp = __shfl_sync(0xffffffffu, tid >> 5, 0), sub = warp & 3, half = warp >> 2;
+  const int slices = (s.V + 63) >> 6, slice = blockIdx.x % slices, hv = blockIdx.x / slices % s.Hv, slot = blockIdx.x / slices / s.Hv;
+  const int hk = hv / (s.Hv / s.Hk), v0 = slice * 64, vn = min(64, s.V - v0);
+  ChunkAt seg;
+  if (plan.resume) {
+    if (!chunk_at(s, slot, kCT * plan.chunks, seg)) return;
+  } else {  // a whole sequence, which may be empty: its state passes through
+    const SeqRange r = seq_range(s, slot, kCT);
+    seg.b = r.b, seg.t0 = seg.first = r.t0, seg.len = r.t1 - r.t0, seg.seq = slot;
+  }
+  if (warp == 0) wkv7::tmem_alloc(&sm.tmem, kCols);
+  if (tid == 0) {
+    for (int i = 0; i < 3; ++i) mbar_init(&sm.done[i], 1);
+    wkv7::fence_mbar_init();
+  }
+  const int n = (seg.len + kCT - 1) / kCT, row = sub * 32 + lane;
+  const long long st_a = kUpper ? s.k_t : s.q_t, st_b = kUpper ? s.q_t : s.k_t, st_x = kUpper ? (long long)s.Hv * s.V : s.v_t;
+  const bf16_t* q = static_cast<const bf16_t*>(a.q) + seg.b * s.q_b + seg.t0 * s.q_t + (size_t)hk * s.K;
+  const bf16_t* k = static_cast<const bf16_t*>(a.k) + seg.b * s.k_b + seg.t0 * s.k_t + (size_t)hk * s.K;
+  const size_t tok = (size_t)seg.b * s.T + seg.t0;
+  const bf16_t* pa = kUpper ? k : q;
+  const bf16_t* pb = kUpper ? q : k;
+  const bf16_t* px = kUpper ? static_cast<const bf16_t*>(a.d_o) + (tok * s.Hv + hv) * s.V + v0
+                            : static_cast<const bf16_t*>(a.v) + seg.b * s.v_b + seg.t0 * s.v_t + (size_t)hv * s.V + v0;
+  bf16_t* out = static_cast<bf16_t*>(kUpper ? a.dv : a.o) + (tok * s.Hv + hv) * s.V + v0;
+  const float* g = s.fixed ? a.g + hv : a.g + tok * s.Hv + hv;
+  float* states = kUpper ? a.dstates : a.states;
+  auto begin = [&](int i) { return (kUpper ? n - 1 - i : i) * kCT; };  // first token of the i-th chunk, from the segment's
+  auto length = [&](int i) { return min(kCT, seg.len - begin(i)); };
+  auto copy_ab = [&](int i) {
+    auto& st = sm.stage[i % kSt];
+    copy_tile<KP>(st.a, pa + begin(i) * st_a, st_a, length(i), s.K, tid, kThreads);
+    copy_tile<KP>(st.b, pb + begin(i) * st_b, st_b, length(i), s.K, tid, kThreads);
+  };
+  auto copy_x = [&](int i) { copy_tile<64>(sm.stage[i % kSt].x, px + begin(i) * st_x, st_x, length(i), vn, tid, kThreads); };
+  auto decays = [&](int i) {
+    make_decays<!kUpper, kUpper>(sm.d[i & 1], s.fixed ? g : g + (size_t)begin(i) * s.Hv, s.fixed ? 0 : s.Hv, length(i), s.scale, lane);
+  };
+  if (n) copy_ab(0), copy_x(0), copies_committed();
+  // The state: rows 16 sub .., keys KP / 2 half .. in accumulator tiles.
+  float S[kTiles][4];
+  auto each = [&](float* m, auto f) {  // pairs of the state's numbers that exist
+#pragma unroll
+    for (int t = 0; t < kTiles; ++t)
+#pragma unroll
+      for (int h = 0; h < 2; ++h) {
+        const int r = v0 + 16 * sub + (lane >> 2) + 8 * h, c = half * (KP / 2) + 8 * t + 2 * (lane & 3);
+        if (r < s.V && c < s.K) f(m + (size_t)r * s.K + c, S[t][2 * h], S[t][2 * h + 1]);
+      }
+  };
+  auto load = [](float* p, float& x, float& y) {
+    const float2 v = *reinterpret_cast<const float2*>(p);
+    x = v.x, y = v.y;
+  };
+  auto store = [](float* p, float& x, float& y) { *reinterpret_cast<float2*>(p) = make_float2(x, y); };
+  auto planes = [&] {
+#pragma unroll
+    for (int t = 0; t < kTiles; t += 2) {
+      Frag<2> f;
+      to_a(f, S[t], S[t + 1]);
+      bf16_t* p = sm.s + at(64, 16 * sub + (lane & 15), half * (KP / 2) + 8 * t + (lane >> 4) * 8);
+      stsm4(p, f.p[0]);
+      stsm4(p + 64 * KP, f.p[1]);
+    }
+  };
+#pragma unroll
+  for (int t = 0; t < kTiles; ++t)
+#pragma unroll
+    for (int e = 0; e < 4; ++e) S[t][e] = 0.f;
+  const size_t state = (size_t)s.V * s.K;
+  auto state_of = [&](int i) { return states + (chunk_slot(s, seg, seg.t0 + begin(i)) * s.Hv + hv) * state; };
+  float* init = const_cast<float*>(kUpper ? a.dS_final : a.s_init);
+  if (plan.resume)
+    each(state_of(0), load);
+  else if (init)
+    each(init + ((size_t)seg.seq * s.Hv + hv) * state, load);
+  planes();
+  if (warp == 7 && n) decays(0);
+  copies_landed();
+  fence_proxy_async_smem();
+  tmem_fence_before_sync();
+  __syncthreads();
+  tmem_fence_after_sync();
+  const uint32_t tm = sm.tmem, mine = tm + ((uint32_t)(sub * 32) << 16);
+  Patience wait{a.status};
+  for (int i = 0; i < n; ++i) {
+    auto& st = sm.stage[i % kSt];
+    const Decays& d = sm.d[i & 1];
+    if (kSt == 2 && i + 1 < n) copy_ab(i + 1), copy_x(i + 1), copies_committed();
+    if (warp == 0) {
+      if (elected()) {
+        const uint64_t da = desc(st.a), db = desc(st.b), ds = desc(sm.s);
+#pragma unroll
+        for (int ks = 0; ks < KP / 16; ++ks) tc_mma(tm + kP, da + along<kCT>(ks), db + along<kCT>(ks), product_of(128, 128, false, false), ks > 0);
+        tc_commit(&sm.done[0]);
+#pragma unroll
+        for (int part = 1; part >= 0; --part)
+#pragma unroll
+          for (int ks = 0; ks < KP / 16; ++ks)
+            tc_mma(tm + kIn, da + along<kCT>(ks), ds + along<64>(ks) + part * (64 * KP * 2 >> 4), product_of(128, 64, false, false), part == 0 || ks > 0);
+      }
+      __syncwarp();
+    }
+    // u . x
+#pragma unroll 2
+    for (int e = tid; e < kCT * 8; e += kThreads) {
+      const int r = e >> 3, o = at(kCT, r, (e & 7) * 8);
+      float x[8];
+      load8(x, st.x + o);
+      const float f = d.u[kUpper][r];
+#pragma unroll
+      for (int j = 0; j < 8; ++j) x[j] *= f;
+      put8<3>(sm.xt + o, kCT * 64, x);
+    }
+    fence_proxy_async_smem();
+    __syncthreads();
+    if (warp == 0) {
+      if (elected()) {
+        const uint64_t dx = desc(sm.xt), db = desc(st.b, kRowPanel);
+#pragma unroll
+        for (int part = 2; part >= 0; --part)
+#pragma unroll
+          for (int ks = 0; ks < kCT / 16; ++ks)
+            tc_mma(tm + kU, dx + across(ks) + part * (kRowPanel >> 4), db + across(ks), product_of(64, KP, true, true), part < 2 || ks > 0);
+        tc_commit(&sm.done[1]);
+      }
+      __syncwarp();
+    }
+    if (plan.keep) each(state_of(i), store);
+    if (warp == 7 && i + 1 < n) decays(i + 1);
+    wait(&sm.done[0], i);
+    tmem_fence_after_sync();
+#pragma unroll
+    for (int b = 0; b < 2; ++b) {
+      const int blk = half + 2 * b;
+      if (kUpper ? blk >= sub : blk <= sub) {
+        float x[32];
+        tc_load32(x, mine + kP + 32 * blk);
+        tc_loaded32(x);
+        decayed<kUpper>(x, d, row, blk, s.scale);
+        store_pairs(mine + kP + 32 * blk, x);
+      } else {
+        store_zeros(mine + kP + 32 * blk);
+      }
+    }
+    wkv7::tmem_wait_st();
+    tmem_fence_before_sync();
+    __syncthreads();
+    if (warp == 0) {
+      tmem_fence_after_sync();
+      if (elected()) {
+        const uint64_t dx = desc(st.x, kRowPanel);
+#pragma unroll
+        for (int part = 1; part >= 0; --part)
+#pragma unroll
+          for (int ks = 0; ks < kCT / 16; ++ks)
+            tc_mma_t(tm + kO, tm + kP + pair_at(ks, part), dx + across(ks), product_of(128, 64, false, true), part == 0 || ks > 0);
+        tc_commit(&sm.done[2]);
+      }
+      __syncwarp();
+    }
+    wait(&sm.done[1], i);
+    tmem_fence_after_sync();
+    if (kSt == 1 && i + 1 < n) copy_ab(i + 1), copies_committed();
+#pragma unroll
+    for (int t = 0; t < kTiles; t += 4) {
+      float x[4][4];
+      tc_load_tiles(x, mine + kU + half * (KP / 2) + 8 * t);
+#pragma unroll
+      for (int j = 0; j < 4; ++j)
+#pragma unroll
+        for (int e = 0; e < 4; ++e) S[t + j][e] = fmaf(d.whole, S[t + j][e], x[j][e]);
+    }
+    planes();
+    wait(&sm.done[2], i);
+    tmem_fence_after_sync();
+    {
+      float x[32], y[32];
+      tc_load32(x, mine + kIn + 32 * half);
+      tc_load32(y, mine + kO + 32 * half);
+      tc_loaded32(x);
+      tc_loaded32(y);
+      const float w = d.w[kUpper][row];
+#pragma unroll
+      for (int p = 0; p < 4; ++p) {
+        uint32_t o[4];
+#pragma unroll
+        for (int j = 0; j < 4; ++j) o[j] = pack2(fmaf(w, x[8 * p + 2 * j], y[8 * p + 2 * j]), fmaf(w, x[8 * p + 2 * j + 1], y[8 * p + 2 * j + 1]));
+        *reinterpret_cast<uint4*>(sm.xt + at(kCT, row, 32 * half + 8 * p)) = make_uint4(o[0], o[1], o[2], o[3]);
+      }
+    }
+    tmem_fence_before_sync();
+    __syncthreads();
+    if (kSt == 1 && i + 1 < n) copy_x(i + 1), copies_committed();
+    {
+      const int len = length(i);
+      bf16_t* p = out + (size_t)begin(i) * s.Hv * s.V;
+#pragma unroll
+      for (int e = 0; e < 4; ++e) {
+        const int r = (e * kThreads + tid) >> 3, c = (tid & 7) * 8;
+        const uint4 v = *reinterpret_cast<const uint4*>(sm.xt + at(kCT, r, c));
+        if (r < len && c < vn) *reinterpret_cast<uint4*>(p + (size_t)r * s.Hv * s.V + c) = v;
+      }
+    }
+    copies_landed();
+    fence_proxy_async_smem();
+    __syncthreads();
+    tmem_fence_after_sync();
+  }
+  float* last = kUpper ? a.dS_init : a.s_final;
+  if (!plan.resume && last) each(last + ((size_t)seg.seq * s.Hv + hv) * state, store);
+  if (warp == 0) wkv7::tmem_dealloc(tm, kCols);
+}
+
+template <int KP, bool kUpper>
+cudaError_t launch(const Args& a, const Plan& plan, cudaStream_t stream) {
+  const size_t smem = sizeof(Smem<KP>);
+  static std::atomic<unsigned long long> done{0};
+  const cudaError_t e = allow_smem(reinterpret_cast<const void*>(chain_kernel<KP, kUpper>), smem, done);
+  if (e != cudaSuccess) return e;
+  const Shape& s = a.s;
+  const long long segs = plan.resume ? slot_count(s.B, s.T, s.nseq, s.packed, kCT * plan.chunks) : s.nseq;
+  chain_kernel<KP, kUpper><<<(unsigned)(segs * s.Hv * ((s.V + 63) / 64)), kThreads, smem, stream>>>(a, plan);
+  return cudaGetLastError();
+}
+
+}  // namespace
+
+cudaError_t launch_chain(const Args& a, bool backward, int chunks, bool resume, bool keep, cudaStream_t stream) {
+  const Plan plan{chunks, resume, keep};
+  if (a.s.K <= 64) return backward ? launch<64, true>(a, plan, stream) : launch<64, false>(a, plan, stream);
+  return backward ? launch<128, true>(a, plan, stream) : launch<128, false>(a, plan, stream);
+}
+
+}  // namespace linattn

@@ -159,13 +159,13 @@ __device__ __forceinline__ void zero(float (&x)[N][4]) {
 #pragma unroll
     for (int e = 0; e < 4; ++e) x[n][e] = 0.f;
 }
-// Rows 0 .. kC-1 (zeros from `len` on) and columns 0 .. ceil(cols / 64) 64 - 1 (zeros from `cols`
+// Rows 0 .. kRows-1 (zeros from `len` on) and columns 0 .. ceil(cols / 64) 64 - 1 (zeros from `cols`
 // on) of a tile, times w[row] where w is given; src is row 0, `stride` elements from row to row.
-template <int kP, typename T>
+template <int kP, int kRows, typename T>
 __device__ __forceinline__ void fill_tile(bf16_t* dst, const T* src, long long stride, int len, int cols, const float* w,
                                           int tid, int threads) {
-  const int pieces = ((cols + 63) >> 6) * 8, part = pieces * 8 * kC;
-  for (int i = tid; i < kC * pieces; i += threads) {
+  const int pieces = ((cols + 63) >> 6) * 8, part = pieces * 8 * kRows;
+  for (int i = tid; i < kRows * pieces; i += threads) {
     const int row = i / pieces, col = (i - row * pieces) * 8;
     float x[8] = {0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f};
     if (row < len && col < cols) {
@@ -176,7 +176,7 @@ __device__ __forceinline__ void fill_tile(bf16_t* dst, const T* src, long long s
         for (int e = 0; e < 8; ++e) x[e] *= f;
       }
     }
-    put8<kP>(dst + at(kC, row, col), part, x);
+    put8<kP>(dst + at(kRows, row, col), part, x);
   }
 }
 
@@ -193,21 +193,31 @@ __device__ __forceinline__ float2 two_sum(float2 a, float2 b) {
   return make_float2(h, e - (h - s));
 }
 __device__ __forceinline__ float minus(float2 a, float2 b) { return (a.x - b.x) + (a.y - b.y); }
-// G[0 .. kC-1] of a warp's lanes from g at `g` (`stride` floats from token to token; 0 from `len` on).
-__device__ __forceinline__ void running_sums(float2* G, const float* g, long long stride, int len, int lane) {
-  static_assert(kC == 64, "two tokens a lane");
-  float a = 2 * lane < len ? g[2 * lane * stride] : 0.f, b = 2 * lane + 1 < len ? g[(2 * lane + 1) * stride] : 0.f;
-  a = a < kReset ? kReset : a, b = b < kReset ? kReset : b;  // (a NaN stays)
-  float2 s = two_sum(make_float2(a, 0.f), make_float2(b, 0.f));
+// G[0 .. 32 kPer - 1] by a warp's lanes from g at `g` (`stride` floats from token to token; 0 from `len`
+// on). Whether a log decay is above 0 (or NaN) comes back.
+template <int kPer>
+__device__ __forceinline__ bool running_sums(float2* G, const float* g, long long stride, int len, int lane) {
+  float2 x[kPer];
+  bool up = false;
+#pragma unroll
+  for (int i = 0; i < kPer; ++i) {
+    float a = kPer * lane + i < len ? g[(kPer * lane + i) * stride] : 0.f;
+    up |= !(a <= 0.f);
+    a = a < kReset ? kReset : a;  // (a NaN stays)
+    x[i] = make_float2(a, 0.f);
+    if (i) x[i] = two_sum(x[i - 1], x[i]);
+  }
+  float2 s = x[kPer - 1];
 #pragma unroll
   for (int o = 1; o < 32; o <<= 1) {
-    const float2 x = make_float2(__shfl_up_sync(0xffffffffu, s.x, o), __shfl_up_sync(0xffffffffu, s.y, o));
-    if (lane >= o) s = two_sum(s, x);
+    const float2 y = make_float2(__shfl_up_sync(0xffffffffu, s.x, o), __shfl_up_sync(0xffffffffu, s.y, o));
+    if (lane >= o) s = two_sum(s, y);
   }
-  G[2 * lane + 1] = s;
   float2 e = make_float2(__shfl_up_sync(0xffffffffu, s.x, 1), __shfl_up_sync(0xffffffffu, s.y, 1));
   if (lane == 0) e = make_float2(0.f, 0.f);
-  G[2 * lane] = two_sum(e, make_float2(a, 0.f));
+#pragma unroll
+  for (int i = 0; i < kPer; ++i) G[kPer * lane + i] = two_sum(e, x[i]);
+  return __any_sync(0xffffffffu, up);
 }
 
 // --------------------------------------------------- sequences and chunks ---
@@ -215,44 +225,50 @@ __device__ __forceinline__ void running_sums(float2* G, const float* g, long lon
 struct SeqRange {
   int b;           // batch row the sequence lies in
   int t0, t1;      // its tokens there
-  long long slot;  // its first chunk slot
+  long long slot;  // its first slot
 };
 // Packed starts are clamped into [0, T] and to non-negative lengths, so that
 // no value in them can take an access out of a buffer.
-__device__ __forceinline__ SeqRange seq_range(const Shape& a, int s) {
+__device__ __forceinline__ SeqRange seq_range(const Shape& a, int s, int tokens) {
   SeqRange r;
   if (a.starts) {
     const int x0 = min(max(a.starts[s], 0), a.T), x1 = min(max(a.starts[s + 1], 0), a.T);
-    r.b = 0, r.t0 = x0, r.t1 = max(x0, x1), r.slot = x0 / kC + s;
+    r.b = 0, r.t0 = x0, r.t1 = max(x0, x1), r.slot = x0 / tokens + s;
   } else {
-    r.b = s, r.t0 = 0, r.t1 = a.T, r.slot = (long long)s * ((a.T + kC - 1) / kC);
+    r.b = s, r.t0 = 0, r.t1 = a.T, r.slot = (long long)s * ((a.T + tokens - 1) / tokens);
   }
   return r;
 }
 struct ChunkAt {
-  int b, t0, len;
+  int b, t0, len;  // batch row, first token, tokens
+  int seq, first;  // its sequence, and that one's first token
 };
-__device__ __forceinline__ bool chunk_at(const Shape& a, int slot, ChunkAt& c) {
+// The stretch of `tokens` tokens (a chunk, or a segment of chunks) that has the slot; false: none.
+__device__ __forceinline__ bool chunk_at(const Shape& a, int slot, int tokens, ChunkAt& c) {
+  int n;
   if (a.starts) {
     int lo = 0, hi = a.nseq - 1;  // the last sequence whose first slot is <= slot
     while (lo < hi) {
       const int mid = (lo + hi + 1) / 2;
-      if (min(max(a.starts[mid], 0), a.T) / kC + mid <= slot)
+      if (min(max(a.starts[mid], 0), a.T) / tokens + mid <= slot)
         lo = mid;
       else
         hi = mid - 1;
     }
-    const SeqRange r = seq_range(a, lo);
-    const int n = slot - (int)r.slot;
-    if (n < 0 || r.t0 + (long long)n * kC >= r.t1) return false;
-    c.b = 0, c.t0 = r.t0 + n * kC, c.len = min(kC, r.t1 - c.t0);
-    return true;
+    c.seq = lo;
+  } else {
+    c.seq = slot / ((a.T + tokens - 1) / tokens);
   }
-  const int nc = (a.T + kC - 1) / kC;
-  c.b = slot / nc;
-  c.t0 = (slot - c.b * nc) * kC;
-  c.len = min(kC, a.T - c.t0);
+  const SeqRange r = seq_range(a, c.seq, tokens);
+  n = slot - (int)r.slot;
+  if (n < 0 || r.t0 + (long long)n * tokens >= r.t1) return false;
+  c.b = r.b, c.first = r.t0, c.t0 = r.t0 + n * tokens, c.len = min(tokens, r.t1 - c.t0);
   return true;
+}
+// The slot of the chunk that begins at token t0 of a sequence.
+__device__ __forceinline__ long long chunk_slot(const Shape& a, const ChunkAt& c, int t0) {
+  const int n = (t0 - c.first) / a.C;
+  return (a.starts ? (long long)c.first / a.C + c.seq : (long long)c.seq * ((a.T + a.C - 1) / a.C)) + n;
 }
 
 }  // namespace linattn

@@ -10,7 +10,8 @@
 
 namespace linattn {
 
-constexpr int kC = 64;        // tokens of a chunk
+// Tokens of a chunk: those that fill the rows of a tcgen05 product, or (fp32, mma.sync) 64.
+constexpr int kCBf16 = 128, kCF32 = 64;
 constexpr int kMaxDim = 128;  // largest head size
 
 // What a call's sequences and heads look like.
@@ -18,6 +19,7 @@ struct Shape {
   int B, T, Hk, Hv, K, V;
   int nseq;           // sequences: B, or those packed in the one batch row
   const int* starts;  // device [nseq + 1], or null
+  int C;              // tokens of a chunk
   int slots;          // chunk slots: an upper bound of the chunks, see slot_count
   int packed;         // nseq sequences in one batch row
   int fixed;          // g is [Hv], one number a head
@@ -25,12 +27,12 @@ struct Shape {
   long long q_b, q_t, k_b, k_t, v_b, v_t;  // element strides of a batch row and of a token
 };
 
-// Every sequence's chunks get slots of their own. Dense: batch * ceil(T / kC).
-// Packed: a sequence that starts at token x is given the slots from x / kC + s
-// on (s its number): x / kC + ceil(len / kC) <= (x + len) / kC + 1, so the next
-// sequence's slots start after them, and T / kC + nseq are enough.
-inline long long slot_count(int B, int T, int nseq, bool packed) {
-  return packed ? (long long)T / kC + nseq : (long long)B * ((T + kC - 1) / kC);
+// Every sequence's chunks get slots of their own, and so do segments of several chunks. Dense: batch *
+// ceil(T / tokens). Packed: a sequence that starts at token x is given the slots from x / tokens + s
+// on (s its number): x / tokens + ceil(len / tokens) <= (x + len) / tokens + 1, so the next
+// sequence's slots start after them, and T / tokens + nseq are enough.
+inline long long slot_count(int B, int T, int nseq, bool packed, int tokens) {
+  return packed ? (long long)T / tokens + nseq : (long long)B * ((T + tokens - 1) / tokens);
 }
 
 struct Args {
@@ -45,12 +47,20 @@ struct Args {
   float *dstates;      // the gradient of the state after each chunk
   float *decay;        // [slots][Hv]: the whole decay of each chunk
   double *part;        // [kParts][Hv]: sums of dg over tokens
+  unsigned* status;    // the device's status word
 };
 constexpr int kParts = 256;
 
-cudaError_t launch_states(const Args& a, bool bf16, bool backward, cudaStream_t stream);  // states or dstates; s_final or dS_init
-cudaError_t launch_o(const Args& a, bool bf16, cudaStream_t stream);
-cudaError_t launch_grad(const Args& a, bool bf16, cudaStream_t stream);  // dv, dq, dk, dg
+// The states before all chunks, or the gradients of those after them, and the last one (s_final, dS_init).
+cudaError_t launch_states(const Args& a, bool bf16, bool backward, cudaStream_t stream);
+// fp32: o; dv, dq, dk and dg of all chunks at once.
+cudaError_t launch_rows_o(const Args& a, cudaStream_t stream);
+cudaError_t launch_rows_grad(const Args& a, cudaStream_t stream);
+// bfloat16: o (backward: dv), segments of `chunks` chunks one after the other in a block. resume: from `states` (or
+// dstates); else these are written on the way where keep, as is the last one.
+cudaError_t launch_chain(const Args& a, bool backward, int chunks, bool resume, bool keep, cudaStream_t stream);
+// bfloat16: dq, dk and dg of all chunks at once.
+cudaError_t launch_grad(const Args& a, cudaStream_t stream);
 cudaError_t launch_dg_sums(const Args& a, cudaStream_t stream);          // dg_fixed from dg
 
 // Zeros in up to five outputs of a packed call at the tokens of no sequence.

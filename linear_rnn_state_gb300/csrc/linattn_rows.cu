@@ -16,20 +16,15 @@
 namespace linattn {
 namespace {
 
-constexpr int kThreads = 128;
+constexpr int kThreads = 128, kC = kCF32;
 enum Mode { kO, kDv, kDq, kDk };
 
 template <typename T>
 __device__ __forceinline__ void store2(T* p, float x, float y);
 template <>
-__device__ __forceinline__ void store2<bf16_t>(bf16_t* p, float x, float y) {
-  *reinterpret_cast<uint32_t*>(p) = pack2(x, y);
-}
-template <>
 __device__ __forceinline__ void store2<float>(float* p, float x, float y) {
   *reinterpret_cast<float2*>(p) = make_float2(x, y);
 }
-__device__ __forceinline__ float2 load2(const bf16_t* p) { return unpack2(*reinterpret_cast<const uint32_t*>(p)); }
 __device__ __forceinline__ float2 load2(const float* p) { return *reinterpret_cast<const float2*>(p); }
 
 template <typename T>
@@ -88,7 +83,7 @@ __global__ void __launch_bounds__(kThreads) rows_kernel(const Args a) {
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5, gr = lane >> 2, tq = lane & 3;
   const int heads = kKeys ? s.Hk : s.Hv, head = blockIdx.x % heads, slot = blockIdx.x / heads, group = s.Hv / s.Hk;
   ChunkAt c;
-  if (!chunk_at(s, slot, c)) return;
+  if (!chunk_at(s, slot, kC, c)) return;
   const size_t tok = (size_t)c.b * s.T + c.t0;
   float acc[kSlices][8][4];
 #pragma unroll
@@ -106,7 +101,7 @@ __global__ void __launch_bounds__(kThreads) rows_kernel(const Args a) {
     const bool dg = kKeys && a.dg;
     __syncthreads();  // the head before is done with shared memory
     if (warp == 0) {
-      running_sums(G, s.fixed ? a.g + hv : a.g + tok * s.Hv + hv, s.fixed ? 0 : s.Hv, c.len, lane);
+      running_sums<2>(G, s.fixed ? a.g + hv : a.g + tok * s.Hv + hv, s.fixed ? 0 : s.Hv, c.len, lane);
       __syncwarp();
 #pragma unroll
       for (int j = lane; j < kC; j += 32) w[j] = kUpper ? expf(minus(G[kC - 1], G[j])) : s.scale * expf(G[j].x + G[j].y);
@@ -115,14 +110,14 @@ __global__ void __launch_bounds__(kThreads) rows_kernel(const Args a) {
     if (kMode == kDq && dg) {
       const int Kp = (s.K + 63) & ~63;
       if (Kp <= Dp) {
-        fill_tile<kP>(as, q.p, q.stride, c.len, s.K, nullptr, tid, kThreads);
-        fill_tile<kP>(bs, k.p, k.stride, c.len, s.K, nullptr, tid, kThreads);
+        fill_tile<kP, kC>(as, q.p, q.stride, c.len, s.K, nullptr, tid, kThreads);
+        fill_tile<kP, kC>(bs, k.p, k.stride, c.len, s.K, nullptr, tid, kThreads);
         __syncthreads();
         scores<kP, false>(qk, as, bs, s.K, Kp, warp, lane);
       } else {  // in two halves
         for (int h = 0; h < 2; ++h) {
-          fill_tile<kP>(as, q.p + 64 * h, q.stride, c.len, h ? s.K - 64 : 64, nullptr, tid, kThreads);
-          fill_tile<kP>(bs, k.p + 64 * h, k.stride, c.len, h ? s.K - 64 : 64, nullptr, tid, kThreads);
+          fill_tile<kP, kC>(as, q.p + 64 * h, q.stride, c.len, h ? s.K - 64 : 64, nullptr, tid, kThreads);
+          fill_tile<kP, kC>(bs, k.p + 64 * h, k.stride, c.len, h ? s.K - 64 : 64, nullptr, tid, kThreads);
           __syncthreads();
           float half[8][4];
           scores<kP, false>(half, as, bs, h ? s.K - 64 : 64, 64, warp, lane);
@@ -135,8 +130,8 @@ __global__ void __launch_bounds__(kThreads) rows_kernel(const Args a) {
       }
       __syncthreads();
     }
-    fill_tile<kP>(as, ta.p, ta.stride, c.len, D, nullptr, tid, kThreads);
-    fill_tile<kP>(bs, tb.p, tb.stride, c.len, D, nullptr, tid, kThreads);
+    fill_tile<kP, kC>(as, ta.p, ta.stride, c.len, D, nullptr, tid, kThreads);
+    fill_tile<kP, kC>(bs, tb.p, tb.stride, c.len, D, nullptr, tid, kThreads);
     __syncthreads();
     Frag<kPc> pf[4];
     {
@@ -193,7 +188,7 @@ __global__ void __launch_bounds__(kThreads) rows_kernel(const Args a) {
     for (int sl = 0; sl < kSlices; ++sl) {
       const int x0 = 64 * sl, xn = min(64, Dx - x0);
       __syncthreads();
-      fill_tile<kP>(xs, tx.p + x0, tx.stride, c.len, xn, nullptr, tid, kThreads);
+      fill_tile<kP, kC>(xs, tx.p + x0, tx.stride, c.len, xn, nullptr, tid, kThreads);
       // the state's slice: rows of values and 64 keys (kKeys), or 64 rows and all keys
       const int rows = kKeys ? Dp : 64, pieces = kKeys ? 8 : Dp / 8;
       for (int i = tid; i < rows * pieces; i += kThreads) {
@@ -343,11 +338,7 @@ cudaError_t grad(const Args& a, cudaStream_t stream) {
 
 }  // namespace
 
-cudaError_t launch_o(const Args& a, bool bf16, cudaStream_t stream) {
-  return bf16 ? pick<bf16_t, kO>(a, stream) : pick<float, kO>(a, stream);
-}
-cudaError_t launch_grad(const Args& a, bool bf16, cudaStream_t stream) {
-  return bf16 ? grad<bf16_t>(a, stream) : grad<float>(a, stream);
-}
+cudaError_t launch_rows_o(const Args& a, cudaStream_t stream) { return pick<float, kO>(a, stream); }
+cudaError_t launch_rows_grad(const Args& a, cudaStream_t stream) { return grad<float>(a, stream); }
 
 }  // namespace linattn

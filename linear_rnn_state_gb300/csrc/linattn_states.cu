@@ -4,7 +4,7 @@
 // Within a chunk, with G the running sum of its log decays and Gc the whole sum:
 //   forward   S' = e^{Gc} S + sum_j e^{Gc - G_j} v_j k_j^T
 //   backward  D  = e^{Gc} D' + sum_i scale e^{G_i} do_i q_i^T
-// The sums of all chunks come first, all at once, as products of 64 tokens on the tensor cores (the
+// The sums of all chunks come first, all at once, as products of a chunk's tokens on the tensor cores (the
 // scaled values in three bfloat16 parts, 24 bits: states are fp32 results); a second kernel
 // runs over the chunks of each sequence, every number of a state on its own, and puts the state
 // before each chunk in the place of its sum.
@@ -14,11 +14,13 @@ namespace linattn {
 namespace {
 
 constexpr int kThreads = 128;
+template <typename T>
+constexpr int kChunk = sizeof(T) == 2 ? kCBf16 : kCF32;
 
 // A block: a chunk, a value head, 64 values (16 a warp) by all keys.
 template <typename T, bool kBack, int kTiles>
 __global__ void __launch_bounds__(kThreads) sums_kernel(const Args a, float* out) {
-  constexpr int kP = In<T>::kParts, kKp = kTiles * 8;
+  constexpr int kP = In<T>::kParts, kKp = kTiles * 8, kC = kChunk<T>;
   extern __shared__ __align__(128) unsigned char smem[];
   bf16_t* xs = reinterpret_cast<bf16_t*>(smem);  // [64 tokens][64 values], 3 parts
   bf16_t* bs = xs + 3 * kC * 64;                 // [64 tokens][keys]
@@ -29,10 +31,10 @@ __global__ void __launch_bounds__(kThreads) sums_kernel(const Args a, float* out
   const int slices = (s.V + 63) >> 6, slice = blockIdx.x % slices, hv = blockIdx.x / slices % s.Hv, slot = blockIdx.x / slices / s.Hv;
   const int hk = hv / (s.Hv / s.Hk), v0 = slice * 64;
   ChunkAt c;
-  if (!chunk_at(s, slot, c)) return;
+  if (!chunk_at(s, slot, kC, c)) return;
   const size_t tok = (size_t)c.b * s.T + c.t0;
   if (warp == 0) {
-    running_sums(G, s.fixed ? a.g + hv : a.g + tok * s.Hv + hv, s.fixed ? 0 : s.Hv, c.len, lane);
+    running_sums<kC / 32>(G, s.fixed ? a.g + hv : a.g + tok * s.Hv + hv, s.fixed ? 0 : s.Hv, c.len, lane);
     __syncwarp();
 #pragma unroll
     for (int j = lane; j < kC; j += 32) u[j] = kBack ? s.scale * expf(G[j].x + G[j].y) : expf(minus(G[kC - 1], G[j]));
@@ -43,8 +45,8 @@ __global__ void __launch_bounds__(kThreads) sums_kernel(const Args a, float* out
                      : static_cast<const T*>(a.v) + c.b * s.v_b + c.t0 * s.v_t + (size_t)hv * s.V + v0;
   const T* b = kBack ? static_cast<const T*>(a.q) + c.b * s.q_b + c.t0 * s.q_t + (size_t)hk * s.K
                      : static_cast<const T*>(a.k) + c.b * s.k_b + c.t0 * s.k_t + (size_t)hk * s.K;
-  fill_tile<3>(xs, x, kBack ? (long long)s.Hv * s.V : s.v_t, c.len, min(64, s.V - v0), u, tid, kThreads);
-  fill_tile<kP>(bs, b, kBack ? s.q_t : s.k_t, c.len, s.K, nullptr, tid, kThreads);
+  fill_tile<3, kC>(xs, x, kBack ? (long long)s.Hv * s.V : s.v_t, c.len, min(64, s.V - v0), u, tid, kThreads);
+  fill_tile<kP, kC>(bs, b, kBack ? s.q_t : s.k_t, c.len, s.K, nullptr, tid, kThreads);
   __syncthreads();
   float acc[kTiles][4];
   zero(acc);
@@ -77,8 +79,8 @@ __global__ void __launch_bounds__(256) join_kernel(const Args a, float* states) 
   const int quads = s.V * s.K / 4, per = (quads + 255) / 256, piece = (blockIdx.x % per) * 256 + threadIdx.x;
   const int hv = blockIdx.x / per % s.Hv, seq = blockIdx.x / per / s.Hv;
   if (piece >= quads) return;
-  const SeqRange r = seq_range(s, seq);
-  const int n = (r.t1 - r.t0 + kC - 1) / kC;
+  const SeqRange r = seq_range(s, seq, s.C);
+  const int n = (r.t1 - r.t0 + s.C - 1) / s.C;
   const size_t mine = ((size_t)seq * s.Hv + hv) * quads + piece;
   const float* init = kBack ? a.dS_final : a.s_init;
   float4 S = init ? reinterpret_cast<const float4*>(init)[mine] : make_float4(0.f, 0.f, 0.f, 0.f);
@@ -108,6 +110,7 @@ __global__ void __launch_bounds__(256) join_kernel(const Args a, float* states) 
 
 template <typename T, bool kBack, int kTiles>
 cudaError_t sums(const Args& a, float* out, cudaStream_t stream) {
+  constexpr int kC = kChunk<T>;
   constexpr size_t smem = (3 * kC * 64 + In<T>::kParts * kC * kTiles * 8) * sizeof(bf16_t) + kC * 12;
   static std::atomic<unsigned long long> done{0};
   const cudaError_t e = allow_smem(reinterpret_cast<const void*>(sums_kernel<T, kBack, kTiles>), smem, done);
@@ -127,7 +130,7 @@ cudaError_t states(const Args& a, cudaStream_t stream) {
 
 // Tokens in front of the first packed sequence and behind the last.
 __global__ void gaps_kernel(const Args a, const Gaps g) {
-  const int t0 = seq_range(a.s, 0).t0, t1 = seq_range(a.s, a.s.nseq - 1).t1, none = a.s.T - max(t1 - t0, 0);
+  const int t0 = seq_range(a.s, 0, a.s.C).t0, t1 = seq_range(a.s, a.s.nseq - 1, a.s.C).t1, none = a.s.T - max(t1 - t0, 0);
   for (int i = 0; i < 5; ++i) {
     if (!g.at[i]) continue;
     for (int n = blockIdx.x; n < none; n += gridDim.x) {

@@ -1,0 +1,198 @@
+// The fifth-generation tensor cores (tcgen05) as linear attention's bfloat16 kernels use them: chunks of 128
+// tokens, which are the 128 rows (lanes of tensor memory) of a product's accumulator.
+//
+// A tile (linattn_common.cuh) is an operand as it lies: rows of 128 bytes with permuted pieces are
+// the 128-byte swizzle, read along the row (K-major) or across it (MN-major), so that one copy of q,
+// k, v and do in shared memory serves every product they stand in.
+#pragma once
+
+#include "linattn_common.cuh"
+#include "wkv7_tmem.cuh"
+
+namespace linattn {
+
+using wkv7::fence_proxy_async_smem;
+using wkv7::mbar_init;
+using wkv7::mbar_wait_bounded;
+using wkv7::tmem_fence_after_sync;
+using wkv7::tmem_fence_before_sync;
+using wkv7::tmem_st;
+
+constexpr int kCT = kCBf16;
+constexpr int kRowPanel = kCT * 128;  // bytes of a panel of 128 rows
+
+// Descriptor of an operand in shared memory: start, leading and stride byte offsets, version 1, 128-byte
+// swizzle. `lead`: MN-major, from one 64-wide panel to the next.
+__device__ __forceinline__ uint64_t desc(const void* tile, uint32_t lead = 16) {
+  const uint32_t lo = (smem_addr(tile) >> 4) | (lead >> 4) << 16, hi = (1024u >> 4) | 1u << 14 | 2u << 29;
+  return (uint64_t)hi << 32 | lo;
+}
+// bfloat16 operands, fp32 accumulator, m x n.
+__host__ __device__ constexpr uint32_t product_of(int m, int n, bool a_mn, bool b_mn) {
+  return (1u << 4) | (1u << 7) | (1u << 10) | ((uint32_t)a_mn << 15) | ((uint32_t)b_mn << 16) | ((uint32_t)(n >> 3) << 17) |
+         ((uint32_t)(m >> 4) << 24);
+}
+// d += a b, or = where !add; a in shared memory, or (tc_mma_t) in tensor memory.
+__device__ __forceinline__ void tc_mma(uint32_t d, uint64_t a, uint64_t b, uint32_t what, bool add) {
+  asm volatile("{\n .reg .pred p;\n setp.ne.b32 p, %4, 0;\n tcgen05.mma.cta_group::1.kind::f16 [%0], %1, %2, %3, p;\n}" ::"r"(d),
+               "l"(a), "l"(b), "r"(what), "r"((uint32_t)add)
+               : "memory");
+}
+__device__ __forceinline__ void tc_mma_t(uint32_t d, uint32_t a, uint64_t b, uint32_t what, bool add) {
+  asm volatile("{\n .reg .pred p;\n setp.ne.b32 p, %4, 0;\n tcgen05.mma.cta_group::1.kind::f16 [%0], [%1], %2, %3, p;\n}" ::"r"(d),
+               "r"(a), "l"(b), "r"(what), "r"((uint32_t)add)
+               : "memory");
+}
+// The barrier gets an arrival when this thread's products so far are done.
+__device__ __forceinline__ void tc_commit(uint64_t* bar) {
+  asm volatile("tcgen05.commit.cta_group::1.mbarrier::arrive::one.shared::cluster.b64 [%0];" ::"r"(smem_addr(bar)) : "memory");
+}
+// True in one lane of a whole warp (an election, so that the compiler sees that descriptors are uniform).
+__device__ __forceinline__ bool elected() {
+  uint32_t p;
+  asm volatile("{\n .reg .pred p;\n elect.sync _|p, 0xffffffff;\n selp.u32 %0, 1, 0, p;\n}" : "=r"(p));
+  return p != 0;
+}
+
+// Products. `step` and `panel` are 16-byte units from one 16-deep block to the next.
+// K-major operand of `rows` rows: block ks of its columns.
+template <int kRows>
+__device__ __forceinline__ constexpr uint32_t along(int ks) {
+  return ((ks >> 2) * kRows * 128 + (ks & 3) * 32) >> 4;
+}
+// MN-major: block ks of its rows.
+__device__ __forceinline__ constexpr uint32_t across(int ks) { return ks * 2048 >> 4; }
+
+// The pair of a 128 x 128 operand in tensor memory, in the place of the fp32 values it was made of: of each 32
+// columns 16 hold the high parts, 16 the low.
+__device__ __forceinline__ constexpr uint32_t pair_at(int ks, int part) { return (ks >> 1) * 32 + part * 16 + (ks & 1) * 8; }
+
+// 32 columns of a thread's lane, complete.
+__device__ __forceinline__ void tc_load32(float (&v)[32], uint32_t taddr) { wkv7::tmem_ld<32>(taddr, v); }
+__device__ __forceinline__ void tc_loaded32(float (&v)[32]) {
+  asm volatile("tcgen05.wait::ld.sync.aligned;"
+               : "+f"(v[0]), "+f"(v[1]), "+f"(v[2]), "+f"(v[3]), "+f"(v[4]), "+f"(v[5]), "+f"(v[6]), "+f"(v[7]), "+f"(v[8]), "+f"(v[9]),
+                 "+f"(v[10]), "+f"(v[11]), "+f"(v[12]), "+f"(v[13]), "+f"(v[14]), "+f"(v[15]), "+f"(v[16]), "+f"(v[17]), "+f"(v[18]),
+                 "+f"(v[19]), "+f"(v[20]), "+f"(v[21]), "+f"(v[22]), "+f"(v[23]), "+f"(v[24]), "+f"(v[25]), "+f"(v[26]), "+f"(v[27]),
+                 "+f"(v[28]), "+f"(v[29]), "+f"(v[30]), "+f"(v[31])
+               :
+               : "memory");
+}
+// 32 columns of 16 rows (those of a 64-row accumulator) as mma.sync's accumulator tiles.
+__device__ __forceinline__ void tc_load_tiles(float (&x)[4][4], uint32_t taddr) {
+  asm volatile("tcgen05.ld.sync.aligned.16x256b.x4.b32 {"
+               "%0, %1, %2, %3, %4, %5, %6, %7, %8, %9, %10, %11, %12, %13, %14, %15}, [%16];"
+               : "=f"(x[0][0]), "=f"(x[0][1]), "=f"(x[0][2]), "=f"(x[0][3]), "=f"(x[1][0]), "=f"(x[1][1]), "=f"(x[1][2]), "=f"(x[1][3]),
+                 "=f"(x[2][0]), "=f"(x[2][1]), "=f"(x[2][2]), "=f"(x[2][3]), "=f"(x[3][0]), "=f"(x[3][1]), "=f"(x[3][2]), "=f"(x[3][3])
+               : "r"(taddr)
+               : "memory");
+  asm volatile("tcgen05.wait::ld.sync.aligned;"
+               : "+f"(x[0][0]), "+f"(x[0][1]), "+f"(x[0][2]), "+f"(x[0][3]), "+f"(x[1][0]), "+f"(x[1][1]), "+f"(x[1][2]), "+f"(x[1][3]),
+                 "+f"(x[2][0]), "+f"(x[2][1]), "+f"(x[2][2]), "+f"(x[2][3]), "+f"(x[3][0]), "+f"(x[3][1]), "+f"(x[3][2]), "+f"(x[3][3])
+               :
+               : "memory");
+}
+__device__ __forceinline__ void stsm4(bf16_t* p, const uint32_t (&r)[4]) {
+  asm volatile("stmatrix.sync.aligned.m8n8.x4.shared.b16 [%0], {%1,%2,%3,%4};" ::"r"(smem_addr(p)), "r"(r[0]), "r"(r[1]), "r"(r[2]),
+               "r"(r[3])
+               : "memory");
+}
+
+// A wait that a warp gives up on once: from then on it goes through its steps without waiting (all accesses
+// are in bounds whatever the data), so that barriers and tensor memory are left in order.
+struct Patience {
+  unsigned* status;
+  bool ok = true;
+  __device__ __forceinline__ void operator()(uint64_t* bar, uint32_t parity) {
+    if (ok) ok = mbar_wait_bounded(status, bar, parity & 1);
+  }
+};
+
+// ---------------------------------------------------------------- copies ---
+
+__device__ __forceinline__ void copy16(void* dst, const void* src, bool in) {
+  asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(smem_addr(dst)), "l"(src), "r"(in ? 16 : 0) : "memory");
+}
+__device__ __forceinline__ void copies_committed() { asm volatile("cp.async.commit_group;" ::: "memory"); }
+__device__ __forceinline__ void copies_landed() { asm volatile("cp.async.wait_group 0;" ::: "memory"); }
+// Rows 0 .. 127 (zeros from `len` on) and kCols columns (zeros from `cols` on) of a tile.
+template <int kCols>
+__device__ __forceinline__ void copy_tile(bf16_t* dst, const bf16_t* src, long long stride, int len, int cols, int tid, int threads) {
+  constexpr int kPieces = kCols / 8;
+#pragma unroll 4
+  for (int i = tid; i < kCT * kPieces; i += threads) {
+    const int row = i / kPieces, col = i % kPieces * 8;
+    const bool in = row < len && col < cols;
+    copy16(dst + at(kCT, row, col), in ? src + row * stride + col : src, in);
+  }
+}
+
+// ---------------------------------------------------------------- decays ---
+
+// A chunk's factors, by one warp. Lower (o, dq: row i, columns j <= i) and upper (dv, dk: row j, columns i >= j):
+//   w: of the state's part of a row; u: of a token in the next state
+//   c: of a column in 32-column blocks away from the diagonal, where e^{G_i - G_j} = e^{G_i - G_r} e^{G_r - G_j} with
+//      r between the two: both at most 1 where no log decay is above 0.
+struct alignas(16) Decays {
+  float2 G[kCT];
+  float w[2][kCT], u[2][kCT], c[2][kCT];  // lower, upper
+  float whole;                            // e^{Gc}
+  int up;                                 // a log decay is above 0
+};
+template <bool kLower, bool kUpper>
+__device__ __forceinline__ void make_decays(Decays& d, const float* g, long long stride, int len, float scale, int lane) {
+  const bool up = running_sums<kCT / 32>(d.G, g, stride, len, lane);
+  __syncwarp();
+  const float2 last = d.G[kCT - 1];
+#pragma unroll
+  for (int i = 0; i < kCT / 32; ++i) {
+    const int j = 32 * i + lane;
+    const float2 G = d.G[j];
+    const float head = scale * expf(G.x + G.y), tail = expf(minus(last, G));
+    if (kLower) d.w[0][j] = head, d.u[0][j] = tail, d.c[0][j] = expf(minus(d.G[32 * i + 31], G));
+    if (kUpper) d.w[1][j] = tail, d.u[1][j] = head, d.c[1][j] = i ? expf(minus(G, d.G[32 * i - 1])) : 1.f;
+  }
+  if (lane == 0) d.whole = expf(last.x + last.y), d.up = up;
+}
+
+// 32 columns (block `blk`) of a row's products times scale e^{G_i - G_j}, 0 outside the mask.
+template <bool kUpper>
+__device__ __forceinline__ void decayed(float (&x)[32], const Decays& d, int row, int blk, float scale) {
+  const float2 Gr = d.G[row];
+  if (blk == row >> 5 || d.up) {
+#pragma unroll
+    for (int j = 0; j < 32; ++j) {
+      const int col = 32 * blk + j;
+      const float2 Gc = d.G[col];
+      const bool keep = kUpper ? col >= row : col <= row;
+      x[j] = keep ? x[j] * (scale * __expf(kUpper ? minus(Gc, Gr) : minus(Gr, Gc))) : 0.f;
+    }
+  } else {
+    const float r = scale * __expf(kUpper ? minus(d.G[32 * blk - 1], Gr) : minus(Gr, d.G[32 * blk + 31]));
+    const float4* c = reinterpret_cast<const float4*>(d.c[kUpper] + 32 * blk);
+#pragma unroll
+    for (int j = 0; j < 32; j += 4) {
+      const float4 f = c[j / 4];
+      x[j] *= f.x * r, x[j + 1] *= f.y * r, x[j + 2] *= f.z * r, x[j + 3] *= f.w * r;
+    }
+  }
+}
+// 32 values as pairs into their place in tensor memory.
+__device__ __forceinline__ void store_pairs(uint32_t taddr, const float (&x)[32]) {
+  float v[32];
+#pragma unroll
+  for (int j = 0; j < 16; ++j) {
+    uint32_t p[2];
+    split2<2>(x[2 * j], x[2 * j + 1], p);
+    v[j] = __uint_as_float(p[0]), v[16 + j] = __uint_as_float(p[1]);
+  }
+  tmem_st<32>(taddr, v);
+}
+__device__ __forceinline__ void store_zeros(uint32_t taddr) {
+  float v[32];
+#pragma unroll
+  for (int j = 0; j < 32; ++j) v[j] = 0.f;
+  tmem_st<32>(taddr, v);
+}
+
+}  // namespace linattn
