@@ -7,26 +7,30 @@
 // P x and a S^T end as bfloat16 values, so P and S enter them as pairs of bfloat16 (16 bits); u . x enters
 // the state, an fp32 result, in three parts (24 bits).
 //
-// Tensor memory: the scores and then P in their place (128 columns), a S^T (64), P x (64), the state's
-// sum (64 or 128, 64 rows). Products of a chunk that do not wait for P run while it is made.
+// Eight warps work on rows; one forms the decays of a chunk to come, one issues the products. With up to 64 keys
+// the scores of chunk i + 1 are made and decayed while the other products of chunk i run (three stages of
+// tiles, two places for the scores); wider keys leave room for two stages, and u . x goes by halves of the tokens.
 #include "linattn_tc.cuh"
 
 namespace linattn {
 namespace {
 
-constexpr int kThreads = 256;
+constexpr int kWorkers = 256, kThreads = kWorkers + 64;
+constexpr int kDecayWarp = 8, kIssueWarp = 9;
 
-template <int KP>
+template <int KP, bool kUpper>
 struct Smem {
-  static constexpr int kStages = KP == 64 ? 2 : 1;
+  using Dec = Decays<!kUpper, kUpper>;
+  static constexpr bool kEarly = KP == 64;
+  static constexpr int kStages = kEarly ? 3 : 2, kHalves = kEarly ? 1 : 2, kXt = kCT / kHalves;
   struct Stage {
     bf16_t a[kCT * KP], b[kCT * KP], x[kCT * 64];
   };
   Stage stage[kStages];
-  bf16_t xt[3 * kCT * 64];  // u . x; then the rows on their way out
+  bf16_t xt[3 * kXt * 64];  // u . x; then the rows on their way out
   bf16_t s[2 * 64 * KP];    // the state's pair
-  Decays d[2];
-  uint64_t done[3];  // scores; a S^T and the state's sum; P x
+  Dec d[3];
+  uint64_t scored, first, summed, out;  // the scores; the first half of the state's sum, all of it; the rows
   uint32_t tmem;
 };
 
@@ -38,10 +42,14 @@ struct Plan {
 template <int KP, bool kUpper>
 __global__ void __launch_bounds__(kThreads, 1) chain_kernel(const Args a, const Plan plan) {
   extern __shared__ __align__(1024) unsigned char raw[];
-  Smem<KP>& sm = *reinterpret_cast<Smem<KP>*>(raw);
+  using M = Smem<KP, kUpper>;
+  M& sm = *reinterpret_cast<M*>(raw);
   constexpr int kTiles = KP / 16;  // n8 tiles of a warp's half of the keys
-  constexpr int kSt = Smem<KP>::kStages;
-  enum { kP = 0, kIn = 128, kO = 192, kU = 256, kCols = 512 };
+  constexpr bool kEarly = M::kEarly;
+  constexpr int kSt = M::kStages, kXt = M::kXt;
+  enum { kP = 0, kIn = kEarly ? 256 : 128, kO = kIn + 64, kU = kO + 64, kCols = 512 };
+  enum { kBarX = 1, kBarP, kBarX2, kBarOut };
+  constexpr int kPair = kWorkers + 32;
   const Shape& s = a.s;
   const int tid = threadIdx.x, lane = tid & 31, warp = __shfl_sync(0xffffffffu, tid >> 5, 0), sub = warp & 3, half = warp >> 2;
   const int slices = (s.V + 63) >> 6, slice = blockIdx.x % slices, hv = blockIdx.x / slices % s.Hv, slot = blockIdx.x / slices / s.Hv;
@@ -55,49 +63,148 @@ __global__ void __launch_bounds__(kThreads, 1) chain_kernel(const Args a, const 
   }
   if (warp == 0) wkv7::tmem_alloc(&sm.tmem, kCols);
   if (tid == 0) {
-    for (int i = 0; i < 3; ++i) mbar_init(&sm.done[i], 1);
+    for (uint64_t* b : {&sm.scored, &sm.first, &sm.summed, &sm.out}) mbar_init(b, 1);
     wkv7::fence_mbar_init();
   }
-  const int n = (seg.len + kCT - 1) / kCT, row = sub * 32 + lane;
+  const int n = (seg.len + kCT - 1) / kCT;
+  const size_t tok = (size_t)seg.b * s.T + seg.t0;
+  auto begin = [&](int i) { return (kUpper ? n - 1 - i : i) * kCT; };  // first token of the i-th chunk, from the segment's
+  auto length = [&](int i) { return min(kCT, seg.len - begin(i)); };
+
+  if (warp == kDecayWarp || warp == kIssueWarp) {
+    const float* g = s.fixed ? a.g + hv : a.g + tok * s.Hv + hv;
+    auto decays = [&](int i) {
+      make_decays(sm.d[i % 3], s.fixed ? g : g + (size_t)begin(i) * s.Hv, s.fixed ? 0 : s.Hv, length(i), s.scale, lane);
+    };
+    const int mine = warp - kDecayWarp;
+    if (mine < n) decays(mine);
+    __syncthreads();
+    tmem_fence_after_sync();
+    if (warp == kDecayWarp) {
+      if (kEarly) __syncthreads();
+      for (int i = 0; i < n; ++i) {
+        if (i + 2 < n) decays(i + 2);
+        __syncthreads();
+      }
+      __syncthreads();
+      return;
+    }
+    const uint32_t tm = sm.tmem;
+    auto scores = [&](int i) {
+      const uint64_t da = desc(sm.stage[i % kSt].a), db = desc(sm.stage[i % kSt].b);
+#pragma unroll
+      for (int ks = 0; ks < KP / 16; ++ks)
+        tc_mma(tm + kP + (kEarly ? i % 2 * 128 : 0), da + along<kCT>(ks), db + along<kCT>(ks), product_of(128, 128, false, false), ks > 0);
+      tc_commit(&sm.scored);
+    };
+    auto from_state = [&](int i) {
+      const uint64_t da = desc(sm.stage[i % kSt].a), ds = desc(sm.s);
+#pragma unroll
+      for (int part = 1; part >= 0; --part)
+#pragma unroll
+        for (int ks = 0; ks < KP / 16; ++ks)
+          tc_mma(tm + kIn, da + along<kCT>(ks), ds + along<64>(ks) + part * (64 * KP * 2 >> 4), product_of(128, 64, false, false), part == 0 || ks > 0);
+    };
+    auto from_chunk = [&](int i) {
+      const uint64_t dx = desc(sm.stage[i % kSt].x);
+#pragma unroll
+      for (int part = 1; part >= 0; --part)
+#pragma unroll
+        for (int ks = 0; ks < kCT / 16; ++ks)
+          tc_mma_t(tm + kO, tm + kP + (kEarly ? i % 2 * 128 : 0) + pair_at(ks, part), dx + across(ks), product_of(128, 64, false, true), part == 0 || ks > 0);
+    };
+    auto sum = [&](int i, int h) {  // of half h of the tokens
+      const uint64_t dx = desc(sm.xt), db = desc(sm.stage[i % kSt].b, kRowPanel) + across(h * (kXt / 16));
+#pragma unroll
+      for (int part = 2; part >= 0; --part)
+#pragma unroll
+        for (int ks = 0; ks < kXt / 16; ++ks)
+          tc_mma(tm + kU, dx + across(ks) + part * (kXt * 128 >> 4), db + across(ks), product_of(64, KP, true, true), h > 0 || part < 2 || ks > 0);
+    };
+    if (kEarly) {
+      if (n && elected()) scores(0);
+      __syncwarp();
+      __syncthreads();
+      tmem_fence_after_sync();
+    }
+    for (int i = 0; i < n; ++i) {
+      if (elected()) {
+        if (!kEarly) scores(i);
+        if (kEarly && i + 1 < n) scores(i + 1);
+        from_state(i);
+        if (kEarly) {
+          from_chunk(i);
+          tc_commit(&sm.out);
+        }
+      }
+      __syncwarp();
+      meet(kBarX, kPair);
+      if (elected()) {
+        sum(i, 0);
+        tc_commit(kEarly ? &sm.summed : &sm.first);
+      }
+      __syncwarp();
+      if (!kEarly) {
+        meet(kBarP, kPair);
+        tmem_fence_after_sync();
+        if (elected()) {
+          from_chunk(i);
+          tc_commit(&sm.out);
+        }
+        __syncwarp();
+        meet(kBarX2, kPair);
+        if (elected()) {
+          sum(i, 1);
+          tc_commit(&sm.summed);
+        }
+        __syncwarp();
+      }
+      __syncthreads();
+      tmem_fence_after_sync();
+    }
+    __syncthreads();
+    return;
+  }
+
+  // ------------------------------------------------------------------ rows ---
+  const int row = sub * 32 + lane;
   const long long st_a = kUpper ? s.k_t : s.q_t, st_b = kUpper ? s.q_t : s.k_t, st_x = kUpper ? (long long)s.Hv * s.V : s.v_t;
   const bf16_t* q = static_cast<const bf16_t*>(a.q) + seg.b * s.q_b + seg.t0 * s.q_t + (size_t)hk * s.K;
   const bf16_t* k = static_cast<const bf16_t*>(a.k) + seg.b * s.k_b + seg.t0 * s.k_t + (size_t)hk * s.K;
-  const size_t tok = (size_t)seg.b * s.T + seg.t0;
   const bf16_t* pa = kUpper ? k : q;
   const bf16_t* pb = kUpper ? q : k;
   const bf16_t* px = kUpper ? static_cast<const bf16_t*>(a.d_o) + (tok * s.Hv + hv) * s.V + v0
                             : static_cast<const bf16_t*>(a.v) + seg.b * s.v_b + seg.t0 * s.v_t + (size_t)hv * s.V + v0;
   bf16_t* out = static_cast<bf16_t*>(kUpper ? a.dv : a.o) + (tok * s.Hv + hv) * s.V + v0;
-  const float* g = s.fixed ? a.g + hv : a.g + tok * s.Hv + hv;
-  float* states = kUpper ? a.dstates : a.states;
-  auto begin = [&](int i) { return (kUpper ? n - 1 - i : i) * kCT; };  // first token of the i-th chunk, from the segment's
-  auto length = [&](int i) { return min(kCT, seg.len - begin(i)); };
-  auto copy_ab = [&](int i) {
-    auto& st = sm.stage[i % kSt];
-    copy_tile<KP>(st.a, pa + begin(i) * st_a, st_a, length(i), s.K, tid, kThreads);
-    copy_tile<KP>(st.b, pb + begin(i) * st_b, st_b, length(i), s.K, tid, kThreads);
+  auto copy = [&](int i) {
+    if (i < n) {
+      auto& st = sm.stage[i % kSt];
+      const int t0 = begin(i), len = length(i);
+      copy_tile<KP>(st.a, pa + t0 * st_a, st_a, len, s.K, tid, kWorkers);
+      copy_tile<KP>(st.b, pb + t0 * st_b, st_b, len, s.K, tid, kWorkers);
+      copy_tile<64>(st.x, px + t0 * st_x, st_x, len, vn, tid, kWorkers);
+    }
+    copies_committed();
   };
-  auto copy_x = [&](int i) { copy_tile<64>(sm.stage[i % kSt].x, px + begin(i) * st_x, st_x, length(i), vn, tid, kThreads); };
-  auto decays = [&](int i) {
-    make_decays<!kUpper, kUpper>(sm.d[i & 1], s.fixed ? g : g + (size_t)begin(i) * s.Hv, s.fixed ? 0 : s.Hv, length(i), s.scale, lane);
-  };
-  if (n) copy_ab(0), copy_x(0), copies_committed();
+  copy(0);
+  if (kEarly) copy(1);
   // The state: rows 16 sub .., keys KP / 2 half .. in accumulator tiles.
   float S[kTiles][4];
-  auto each = [&](float* m, auto f) {  // pairs of the state's numbers that exist
+  const int s_row = v0 + 16 * sub + (lane >> 2), s_col = half * (KP / 2) + 2 * (lane & 3);
+  float* const states = (kUpper ? a.dstates : a.states) + ((size_t)s_row * s.K + s_col);
+  const size_t state = (size_t)s.V * s.K;
+  auto each = [&](float* m, auto f) {  // pairs of the state's numbers that exist; m is where its first is
 #pragma unroll
     for (int t = 0; t < kTiles; ++t)
 #pragma unroll
-      for (int h = 0; h < 2; ++h) {
-        const int r = v0 + 16 * sub + (lane >> 2) + 8 * h, c = half * (KP / 2) + 8 * t + 2 * (lane & 3);
-        if (r < s.V && c < s.K) f(m + (size_t)r * s.K + c, S[t][2 * h], S[t][2 * h + 1]);
-      }
+      for (int h = 0; h < 2; ++h)
+        if (s_row + 8 * h < s.V && s_col + 8 * t < s.K) f(reinterpret_cast<float2*>(m + (h ? 8 * s.K : 0) + 8 * t), S[t][2 * h], S[t][2 * h + 1]);
   };
-  auto load = [](float* p, float& x, float& y) {
-    const float2 v = *reinterpret_cast<const float2*>(p);
+  auto load = [](float2* p, float& x, float& y) {
+    const float2 v = *p;
     x = v.x, y = v.y;
   };
-  auto store = [](float* p, float& x, float& y) { *reinterpret_cast<float2*>(p) = make_float2(x, y); };
+  auto store = [](float2* p, float& x, float& y) { *p = make_float2(x, y); };
   auto planes = [&] {
 #pragma unroll
     for (int t = 0; t < kTiles; t += 2) {
@@ -112,15 +219,14 @@ __global__ void __launch_bounds__(kThreads, 1) chain_kernel(const Args a, const 
   for (int t = 0; t < kTiles; ++t)
 #pragma unroll
     for (int e = 0; e < 4; ++e) S[t][e] = 0.f;
-  const size_t state = (size_t)s.V * s.K;
   auto state_of = [&](int i) { return states + (chunk_slot(s, seg, seg.t0 + begin(i)) * s.Hv + hv) * state; };
+  const size_t ends = ((size_t)seg.seq * s.Hv + hv) * state + (size_t)s_row * s.K + s_col;
   float* init = const_cast<float*>(kUpper ? a.dS_final : a.s_init);
   if (plan.resume)
     each(state_of(0), load);
   else if (init)
-    each(init + ((size_t)seg.seq * s.Hv + hv) * state, load);
+    each(init + ends, load);
   planes();
-  if (warp == 7 && n) decays(0);
   copies_landed();
   fence_proxy_async_smem();
   tmem_fence_before_sync();
@@ -128,85 +234,64 @@ __global__ void __launch_bounds__(kThreads, 1) chain_kernel(const Args a, const 
   tmem_fence_after_sync();
   const uint32_t tm = sm.tmem, mine = tm + ((uint32_t)(sub * 32) << 16);
   Patience wait{a.status};
-  for (int i = 0; i < n; ++i) {
-    auto& st = sm.stage[i % kSt];
-    const Decays& d = sm.d[i & 1];
-    if (kSt == 2 && i + 1 < n) copy_ab(i + 1), copy_x(i + 1), copies_committed();
-    if (warp == 0) {
-      if (elected()) {
-        const uint64_t da = desc(st.a), db = desc(st.b), ds = desc(sm.s);
-#pragma unroll
-        for (int ks = 0; ks < KP / 16; ++ks) tc_mma(tm + kP, da + along<kCT>(ks), db + along<kCT>(ks), product_of(128, 128, false, false), ks > 0);
-        tc_commit(&sm.done[0]);
-#pragma unroll
-        for (int part = 1; part >= 0; --part)
-#pragma unroll
-          for (int ks = 0; ks < KP / 16; ++ks)
-            tc_mma(tm + kIn, da + along<kCT>(ks), ds + along<64>(ks) + part * (64 * KP * 2 >> 4), product_of(128, 64, false, false), part == 0 || ks > 0);
-      }
-      __syncwarp();
-    }
-    // u . x
-#pragma unroll 2
-    for (int e = tid; e < kCT * 8; e += kThreads) {
-      const int r = e >> 3, o = at(kCT, r, (e & 7) * 8);
-      float x[8];
-      load8(x, st.x + o);
-      const float f = d.u[kUpper][r];
-#pragma unroll
-      for (int j = 0; j < 8; ++j) x[j] *= f;
-      put8<3>(sm.xt + o, kCT * 64, x);
-    }
-    fence_proxy_async_smem();
-    __syncthreads();
-    if (warp == 0) {
-      if (elected()) {
-        const uint64_t dx = desc(sm.xt), db = desc(st.b, kRowPanel);
-#pragma unroll
-        for (int part = 2; part >= 0; --part)
-#pragma unroll
-          for (int ks = 0; ks < kCT / 16; ++ks)
-            tc_mma(tm + kU, dx + across(ks) + part * (kRowPanel >> 4), db + across(ks), product_of(64, KP, true, true), part < 2 || ks > 0);
-        tc_commit(&sm.done[1]);
-      }
-      __syncwarp();
-    }
-    if (plan.keep) each(state_of(i), store);
-    if (warp == 7 && i + 1 < n) decays(i + 1);
-    wait(&sm.done[0], i);
+  // The scores of chunk i, decayed, as pairs.
+  auto score = [&](int i) {
+    const uint32_t at_p = mine + kP + (kEarly ? i % 2 * 128 : 0);
+    wait(&sm.scored, i);
     tmem_fence_after_sync();
 #pragma unroll
     for (int b = 0; b < 2; ++b) {
       const int blk = half + 2 * b;
       if (kUpper ? blk >= sub : blk <= sub) {
         float x[32];
-        tc_load32(x, mine + kP + 32 * blk);
+        tc_load32(x, at_p + 32 * blk);
         tc_loaded32(x);
-        decayed<kUpper>(x, d, row, blk, s.scale);
-        store_pairs(mine + kP + 32 * blk, x);
+        decayed<kUpper>(x, sm.d[i % 3], row, blk, s.scale);
+        store_pairs(at_p + 32 * blk, x);
       } else {
-        store_zeros(mine + kP + 32 * blk);
+        store_zeros(at_p + 32 * blk);
       }
     }
     wkv7::tmem_wait_st();
     tmem_fence_before_sync();
-    __syncthreads();
-    if (warp == 0) {
-      tmem_fence_after_sync();
-      if (elected()) {
-        const uint64_t dx = desc(st.x, kRowPanel);
+  };
+  // u . x of half h of the tokens
+  auto scaled = [&](int i, int h) {
+    const bf16_t* x0 = sm.stage[i % kSt].x;
+    const float* u = sm.d[i % 3].u[0];
+#pragma unroll 2
+    for (int e = tid; e < kXt * 8; e += kWorkers) {
+      const int r = e >> 3;
+      float x[8];
+      load8(x, x0 + at(kCT, h * kXt + r, (e & 7) * 8));
+      const float f = u[h * kXt + r];
 #pragma unroll
-        for (int part = 1; part >= 0; --part)
-#pragma unroll
-          for (int ks = 0; ks < kCT / 16; ++ks)
-            tc_mma_t(tm + kO, tm + kP + pair_at(ks, part), dx + across(ks), product_of(128, 64, false, true), part == 0 || ks > 0);
-        tc_commit(&sm.done[2]);
-      }
-      __syncwarp();
+      for (int j = 0; j < 8; ++j) x[j] *= f;
+      put8<3>(sm.xt + at(kXt, r, (e & 7) * 8), kXt * 64, x);
     }
-    wait(&sm.done[1], i);
+    fence_proxy_async_smem();
+  };
+  if (kEarly) {
+    if (n) score(0);
+    __syncthreads();
+  }
+  for (int i = 0; i < n; ++i) {
+    const auto& d = sm.d[i % 3];
+    copy(kEarly ? i + 2 : i + 1);
+    if (plan.keep) each(state_of(i), store);
+    scaled(i, 0);
+    announce(kBarX, kPair);
+    if (kEarly) {
+      if (i + 1 < n) score(i + 1);
+    } else {
+      score(i);
+      announce(kBarP, kPair);
+      wait(&sm.first, i);
+      scaled(i, 1);
+      announce(kBarX2, kPair);
+    }
+    wait(&sm.summed, i);
     tmem_fence_after_sync();
-    if (kSt == 1 && i + 1 < n) copy_ab(i + 1), copies_committed();
 #pragma unroll
     for (int t = 0; t < kTiles; t += 4) {
       float x[4][4];
@@ -217,7 +302,7 @@ __global__ void __launch_bounds__(kThreads, 1) chain_kernel(const Args a, const 
         for (int e = 0; e < 4; ++e) S[t + j][e] = fmaf(d.whole, S[t + j][e], x[j][e]);
     }
     planes();
-    wait(&sm.done[2], i);
+    wait(&sm.out, i);
     tmem_fence_after_sync();
     {
       float x[32], y[32];
@@ -225,7 +310,7 @@ __global__ void __launch_bounds__(kThreads, 1) chain_kernel(const Args a, const 
       tc_load32(y, mine + kO + 32 * half);
       tc_loaded32(x);
       tc_loaded32(y);
-      const float w = d.w[kUpper][row];
+      const float w = d.w[0][row];
 #pragma unroll
       for (int p = 0; p < 4; ++p) {
         uint32_t o[4];
@@ -234,32 +319,33 @@ __global__ void __launch_bounds__(kThreads, 1) chain_kernel(const Args a, const 
         *reinterpret_cast<uint4*>(sm.xt + at(kCT, row, 32 * half + 8 * p)) = make_uint4(o[0], o[1], o[2], o[3]);
       }
     }
-    tmem_fence_before_sync();
-    __syncthreads();
-    if (kSt == 1 && i + 1 < n) copy_x(i + 1), copies_committed();
+    meet(kBarOut, kWorkers);
     {
       const int len = length(i);
       bf16_t* p = out + (size_t)begin(i) * s.Hv * s.V;
 #pragma unroll
       for (int e = 0; e < 4; ++e) {
-        const int r = (e * kThreads + tid) >> 3, c = (tid & 7) * 8;
+        const int r = (e * kWorkers + tid) >> 3, c = (tid & 7) * 8;
         const uint4 v = *reinterpret_cast<const uint4*>(sm.xt + at(kCT, r, c));
         if (r < len && c < vn) *reinterpret_cast<uint4*>(p + (size_t)r * s.Hv * s.V + c) = v;
       }
     }
     copies_landed();
     fence_proxy_async_smem();
+    tmem_fence_before_sync();
     __syncthreads();
     tmem_fence_after_sync();
   }
   float* last = kUpper ? a.dS_init : a.s_final;
-  if (!plan.resume && last) each(last + ((size_t)seg.seq * s.Hv + hv) * state, store);
+  if (!plan.resume && last) each(last + ends, store);
+  __syncthreads();
   if (warp == 0) wkv7::tmem_dealloc(tm, kCols);
 }
 
 template <int KP, bool kUpper>
 cudaError_t launch(const Args& a, const Plan& plan, cudaStream_t stream) {
-  const size_t smem = sizeof(Smem<KP>);
+  const size_t smem = sizeof(Smem<KP, kUpper>);
+  static_assert(sizeof(Smem<KP, kUpper>) <= 232448, "shared memory of a block");
   static std::atomic<unsigned long long> done{0};
   const cudaError_t e = allow_smem(reinterpret_cast<const void*>(chain_kernel<KP, kUpper>), smem, done);
   if (e != cudaSuccess) return e;

@@ -26,7 +26,7 @@ template <int KP, int VP>
 struct Smem {
   bf16_t q[kCT * KP], k[kCT * KP], v[kCT * VP], d[kCT * VP];
   bf16_t s[3 * VP * 64];  // 64 keys of S or D; then rows on their way out
-  Decays dec;
+  Decays<true, true> dec;
   float total[4][kCT];    // of a row's A_ij (q_i.k_j), by blocks of 32 columns
   float pairs[4][kCT];    // of a block of 32 rows: the sums over j < t
   float dots[2][2][kCT];  // q.(S's part of dq), k.(D's part of dk), by halves of the columns
@@ -101,7 +101,7 @@ __global__ void __launch_bounds__(kThreads, KP == 64 && VP == 64 && !kShared ? 2
     copy_tile<VP>(sm.v, static_cast<const bf16_t*>(a.v) + c.b * s.v_b + c.t0 * s.v_t + (size_t)hv * s.V, s.v_t, c.len, s.V, tid, kThreads);
     copy_tile<VP>(sm.d, static_cast<const bf16_t*>(a.d_o) + (tok * s.Hv + hv) * s.V, (long long)s.Hv * s.V, c.len, s.V, tid, kThreads);
     copies_committed();
-    if (warp == 7) make_decays<true, true>(sm.dec, s.fixed ? a.g + hv : a.g + tok * s.Hv + hv, s.fixed ? 0 : s.Hv, c.len, s.scale, lane);
+    if (warp == 7) make_decays(sm.dec, s.fixed ? a.g + hv : a.g + tok * s.Hv + hv, s.fixed ? 0 : s.Hv, c.len, s.scale, lane);
     const float* S = a.states + ((size_t)slot * s.Hv + hv) * s.V * s.K;
     const float* D = a.dstates + ((size_t)slot * s.Hv + hv) * s.V * s.K;
     copies_landed();

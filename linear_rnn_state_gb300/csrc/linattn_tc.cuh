@@ -98,6 +98,10 @@ __device__ __forceinline__ void stsm4(bf16_t* p, const uint32_t (&r)[4]) {
                : "memory");
 }
 
+// Barrier `id` of some of a block's warps: `n` threads in all meet there, or announce themselves and go on.
+__device__ __forceinline__ void meet(int id, int n) { asm volatile("bar.sync %0, %1;" ::"r"(id), "r"(n) : "memory"); }
+__device__ __forceinline__ void announce(int id, int n) { asm volatile("bar.arrive %0, %1;" ::"r"(id), "r"(n) : "memory"); }
+
 // A wait that a warp gives up on once: from then on it goes through its steps without waiting (all accesses
 // are in bounds whatever the data), so that barriers and tensor memory are left in order.
 struct Patience {
@@ -133,14 +137,17 @@ __device__ __forceinline__ void copy_tile(bf16_t* dst, const bf16_t* src, long l
 //   w: of the state's part of a row; u: of a token in the next state
 //   c: of a column in 32-column blocks away from the diagonal, where e^{G_i - G_j} = e^{G_i - G_r} e^{G_r - G_j} with
 //      r between the two: both at most 1 where no log decay is above 0.
+template <bool kLower, bool kUpper>
 struct alignas(16) Decays {
+  static constexpr int kSets = kLower + kUpper;
   float2 G[kCT];
-  float w[2][kCT], u[2][kCT], c[2][kCT];  // lower, upper
-  float whole;                            // e^{Gc}
-  int up;                                 // a log decay is above 0
+  float w[kSets][kCT], u[kSets][kCT], c[kSets][kCT];
+  float whole;  // e^{Gc}
+  int up;       // a log decay is above 0
+  static __device__ constexpr int set(bool upper) { return kSets == 2 ? upper : 0; }
 };
 template <bool kLower, bool kUpper>
-__device__ __forceinline__ void make_decays(Decays& d, const float* g, long long stride, int len, float scale, int lane) {
+__device__ __forceinline__ void make_decays(Decays<kLower, kUpper>& d, const float* g, long long stride, int len, float scale, int lane) {
   const bool up = running_sums<kCT / 32>(d.G, g, stride, len, lane);
   __syncwarp();
   const float2 last = d.G[kCT - 1];
@@ -150,26 +157,33 @@ __device__ __forceinline__ void make_decays(Decays& d, const float* g, long long
     const float2 G = d.G[j];
     const float head = scale * expf(G.x + G.y), tail = expf(minus(last, G));
     if (kLower) d.w[0][j] = head, d.u[0][j] = tail, d.c[0][j] = expf(minus(d.G[32 * i + 31], G));
-    if (kUpper) d.w[1][j] = tail, d.u[1][j] = head, d.c[1][j] = i ? expf(minus(G, d.G[32 * i - 1])) : 1.f;
+    if (kUpper) {
+      constexpr int k = Decays<kLower, kUpper>::kSets - 1;
+      d.w[k][j] = tail, d.u[k][j] = head, d.c[k][j] = i ? expf(minus(G, d.G[32 * i - 1])) : 1.f;
+    }
   }
   if (lane == 0) d.whole = expf(last.x + last.y), d.up = up;
 }
 
 // 32 columns (block `blk`) of a row's products times scale e^{G_i - G_j}, 0 outside the mask.
-template <bool kUpper>
-__device__ __forceinline__ void decayed(float (&x)[32], const Decays& d, int row, int blk, float scale) {
+template <bool kUpper, typename D>
+__device__ __forceinline__ void decayed(float (&x)[32], const D& d, int row, int blk, float scale) {
   const float2 Gr = d.G[row];
   if (blk == row >> 5 || d.up) {
+    const float4* G = reinterpret_cast<const float4*>(d.G + 32 * blk);  // two tokens
+    const int at = row - 32 * blk;                                      // the diagonal's column
 #pragma unroll
-    for (int j = 0; j < 32; ++j) {
-      const int col = 32 * blk + j;
-      const float2 Gc = d.G[col];
-      const bool keep = kUpper ? col >= row : col <= row;
-      x[j] = keep ? x[j] * (scale * __expf(kUpper ? minus(Gc, Gr) : minus(Gr, Gc))) : 0.f;
+    for (int j = 0; j < 32; j += 2) {
+      const float4 g = G[j / 2];
+      const float d0 = minus(Gr, make_float2(g.x, g.y)), d1 = minus(Gr, make_float2(g.z, g.w));
+      // (selects, no branches: a masked place takes the exponent 0)
+      const bool k0 = kUpper ? j >= at : j <= at, k1 = kUpper ? j + 1 >= at : j + 1 <= at;
+      const float e0 = scale * __expf(k0 ? (kUpper ? -d0 : d0) : 0.f), e1 = scale * __expf(k1 ? (kUpper ? -d1 : d1) : 0.f);
+      x[j] = k0 ? x[j] * e0 : 0.f, x[j + 1] = k1 ? x[j + 1] * e1 : 0.f;
     }
   } else {
     const float r = scale * __expf(kUpper ? minus(d.G[32 * blk - 1], Gr) : minus(Gr, d.G[32 * blk + 31]));
-    const float4* c = reinterpret_cast<const float4*>(d.c[kUpper] + 32 * blk);
+    const float4* c = reinterpret_cast<const float4*>(d.c[D::set(kUpper)] + 32 * blk);
 #pragma unroll
     for (int j = 0; j < 32; j += 4) {
       const float4 f = c[j / 4];
