@@ -5,6 +5,7 @@
 #include "api_check.h"
 #include "linattn.h"
 #include "linattn_launch.h"
+#include "linattn_maps.h"
 
 namespace linattn {
 namespace {
@@ -69,20 +70,38 @@ struct Place {
     p = reinterpret_cast<T*>(at);
     at += (count * sizeof(T) + 127) & ~(size_t)127;
   }
+  void* bytes(size_t n) {
+    char* p;
+    take(p, n);
+    return p;
+  }
 };
+// bfloat16: whether the chains of all sequences, heads and slices of 64 values would leave most of the GPU idle, so
+// that they go in segments, from states made before.
+bool resumes(const Shape& s) {
+  return (long long)s.nseq * s.Hv * ((s.V + 63) / 64) < 76 && (s.T + s.C - 1) / s.C > 4;
+}
 // The regions of `saved`, and of the backward's workspace, from p on; returns the bytes.
-size_t place_saved(Args& a, char* p) {
+size_t place_saved(Args& a, bool bf16, bool for_backward, char* p) {
   const Shape& s = a.s;
+  const size_t n = (size_t)s.slots * s.Hv;
   Place x{p, p};
-  x.take(a.states, (size_t)s.slots * s.Hv * s.V * s.K);
-  x.take(a.decay, (size_t)s.slots * s.Hv);
+  if (bf16 && for_backward) a.images = x.bytes(n * image_bytes(s.K, s.V));
+  if (!bf16 || resumes(s)) {
+    x.take(a.states, n * s.V * s.K);
+    x.take(a.decay, n);
+  }
   return x.at - x.start;
 }
-size_t place_workspace(Args& a, char* p) {
+size_t place_workspace(Args& a, bool bf16, char* p) {
   const Shape& s = a.s;
+  const size_t n = (size_t)s.slots * s.Hv;
   Place x{p, p};
-  x.take(a.dstates, (size_t)s.slots * s.Hv * s.V * s.K);
-  x.take(a.decay, (size_t)s.slots * s.Hv);
+  if (bf16) a.dimages = x.bytes(n * image_bytes(s.K, s.V));
+  if (!bf16 || resumes(s)) {
+    x.take(a.dstates, n * s.V * s.K);
+    x.take(a.decay, n);
+  }
   if (s.fixed) {
     x.take(a.dg, (size_t)s.B * s.T * s.Hv);
     x.take(a.part, (size_t)kParts * s.Hv);
@@ -105,35 +124,58 @@ int copy_state(float* dst, const float* src, size_t bytes, cudaStream_t stream) 
 int launched(cudaError_t e, const char* what) {
   return e == cudaSuccess ? WKV7_OK : fail(WKV7_ERR_CUDA, "%s launch: %s", what, cudaGetErrorString(e));
 }
-// bfloat16: the chains of all sequences, heads and slices of 64 values, whole where they fill the GPU, else in segments
-// that begin from states made before.
-int chains(const Args& a, bool backward, bool keep, cudaStream_t stream) {
-  const Shape& s = a.s;
-  const int chunks = (s.T + s.C - 1) / s.C;
-  const long long lines = (long long)s.nseq * s.Hv * ((s.V + 63) / 64);
-  if (lines >= 76 || chunks <= 4) return launched(launch_chain(a, backward, chunks, false, keep, stream), "chain");
-  const int rc = launched(launch_states(a, true, backward, stream), "states");
-  return rc ? rc : launched(launch_chain(a, backward, 2, true, false, stream), "chain");
+// bfloat16: o, or dv.
+int chains(const Maps& maps, const Args& a, bool backward, bool keep, cudaStream_t stream) {
+  const bool resume = resumes(a.s);
+  const int rc = resume ? launched(launch_states(a, true, backward, stream), "states") : WKV7_OK;
+  return rc ? rc : launched(launch_chain(maps, a, backward, resume ? 2 : 0, resume, keep, stream), "chain");
 }
 uint32_t* words(void* p) { return static_cast<uint32_t*>(p); }
 
+PFN_cuTensorMapEncodeTiled_v12000 encoder() {
+  static PFN_cuTensorMapEncodeTiled_v12000 fn = [] {
+    void* p = nullptr;
+    cudaDriverEntryPointQueryResult q;
+    const cudaError_t e = cudaGetDriverEntryPointByVersion("cuTensorMapEncodeTiled", &p, 12000, cudaEnableDefault, &q);
+    return e == cudaSuccess && q == cudaDriverEntryPointSuccess ? reinterpret_cast<PFN_cuTensorMapEncodeTiled_v12000>(p) : nullptr;
+  }();
+  return fn;
+}
+// [B][T][H][D] with token and batch strides. A batch row that is every batch row's (stride 0) is one.
+bool make_map(CUtensorMap& map, const void* p, int B, int T, int H, int D, long long t, long long b) {
+  const cuuint64_t row = (cuuint64_t)H * D * 2, ts = t ? (cuuint64_t)t * 2 : row, bs = b ? (cuuint64_t)b * 2 : ts * T;
+  const cuuint64_t dims[4] = {(cuuint64_t)D, (cuuint64_t)H, (cuuint64_t)T, (cuuint64_t)(b ? B : 1)}, strides[3] = {(cuuint64_t)D * 2, ts, bs};
+  const cuuint32_t box[4] = {64, 1, (cuuint32_t)kCBf16, 1}, one[4] = {1, 1, 1, 1};
+  return encoder()(&map, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 4, const_cast<void*>(p), dims, strides, box, one, CU_TENSOR_MAP_INTERLEAVE_NONE,
+                   CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
+}
+
 }  // namespace
+
+bool make_maps(Maps& m, const Args& a) {
+  const Shape& s = a.s;
+  if (!encoder()) return false;
+  return make_map(m.q, a.q, s.B, s.T, s.Hk, s.K, s.q_t, s.q_b) && make_map(m.k, a.k, s.B, s.T, s.Hk, s.K, s.k_t, s.k_b) &&
+         make_map(m.v, a.v, s.B, s.T, s.Hv, s.V, s.v_t, s.v_b) &&
+         (!a.d_o || make_map(m.d, a.d_o, s.B, s.T, s.Hv, s.V, 0, s.B > 1 ? (long long)s.T * s.Hv * s.V : 0));
+}
+
 }  // namespace linattn
 
 using namespace linattn;
 
 extern "C" {
 
-size_t linattn_saved_bytes(int B, int T, int Hk, int Hv, int K, int V, int nseq, int bf16, int) {
+size_t linattn_saved_bytes(int B, int T, int Hk, int Hv, int K, int V, int nseq, int bf16, int for_backward) {
   Args a{};
   if (set_shape(a.s, B, T, Hk, Hv, K, V, nseq, bf16)) return 0;
-  return place_saved(a, nullptr);
+  return place_saved(a, bf16, for_backward, nullptr);
 }
 size_t linattn_backward_bytes(int B, int T, int Hk, int Hv, int K, int V, int nseq, int g_fixed, int bf16) {
   Args a{};
   if (set_shape(a.s, B, T, Hk, Hv, K, V, nseq, bf16)) return 0;
   a.s.fixed = g_fixed;
-  return place_workspace(a, nullptr);
+  return place_workspace(a, bf16, nullptr);
 }
 
 int linattn_forward(const void* q, const void* k, const void* v, const float* g, const float* s_init,
@@ -150,7 +192,7 @@ int linattn_forward(const void* q, const void* k, const void* v, const float* g,
   unsigned long long in_bytes[3];
   if ((rc = set_strides(st, in_bytes, strides, B, T, Hk, Hv, K, V, es))) return rc;
   const unsigned long long rows = (unsigned long long)B * T * Hv, state = (unsigned long long)a.s.nseq * Hv * V * K * 4;
-  const size_t need = place_saved(a, static_cast<char*>(saved));
+  const size_t need = place_saved(a, bf16, for_backward, static_cast<char*>(saved));
   const Span ins[6] = {{q, in_bytes[0], "q", true}, {k, in_bytes[1], "k", true}, {v, in_bytes[2], "v", true},
                        {g, rows ? (g_fixed ? Hv : rows) * 4 : 0, "g", true, 4}, {s_init, state, "s_init", false},
                        {seq_starts, seq_starts ? ((unsigned long long)nseq + 1) * 4 : 0, "seq_starts", false, 4}};
@@ -163,7 +205,9 @@ int linattn_forward(const void* q, const void* k, const void* v, const float* g,
   a.s.q_b = st[0], a.s.q_t = st[1], a.s.k_b = st[2], a.s.k_t = st[3], a.s.v_b = st[4], a.s.v_t = st[5];
   a.q = q, a.k = k, a.v = v, a.g = g, a.s_init = s_init, a.o = o, a.s_final = s_final;
   if (bf16) {
-    if ((rc = wkv7::api_status_word(&a.status)) || (rc = chains(a, false, for_backward, stream))) return rc;
+    Maps maps;
+    if (!make_maps(maps, a)) return fail(WKV7_ERR_CUDA, "no tensor maps of q, k and v");
+    if ((rc = wkv7::api_status_word(&a.status)) || (rc = chains(maps, a, false, for_backward, stream))) return rc;
   } else {
     if ((rc = launched(launch_states(a, false, false, stream), "states"))) return rc;
     if ((rc = launched(launch_rows_o(a, stream), "forward"))) return rc;
@@ -190,8 +234,8 @@ int linattn_backward(const void* q, const void* k, const void* v, const float* g
   const unsigned long long rows = (unsigned long long)B * T * Hv, keys = (unsigned long long)B * T * Hk * K * es,
                            state = (unsigned long long)a.s.nseq * Hv * V * K * 4,
                            gs = (g_fixed ? Hv : rows) * 4;
-  const size_t have = place_saved(a, const_cast<char*>(static_cast<const char*>(saved)));
-  const size_t need = place_workspace(a, static_cast<char*>(workspace));
+  const size_t have = place_saved(a, bf16, true, const_cast<char*>(static_cast<const char*>(saved)));
+  const size_t need = place_workspace(a, bf16, static_cast<char*>(workspace));
   const Span ins[8] = {{q, in_bytes[0], "q", true}, {k, in_bytes[1], "k", true}, {v, in_bytes[2], "v", true},
                        {g, rows ? gs : 0, "g", true, 4}, {d_o, rows * V * es, "d_o", true}, {dS_final, state, "dS_final", false},
                        {seq_starts, seq_starts ? ((unsigned long long)nseq + 1) * 4 : 0, "seq_starts", false, 4},
@@ -215,8 +259,10 @@ int linattn_backward(const void* q, const void* k, const void* v, const float* g
     a.dg = dg;
   if (!dg) a.dg = nullptr;
   if (bf16) {
-    if ((rc = wkv7::api_status_word(&a.status)) || (rc = chains(a, true, true, stream))) return rc;
-    if ((rc = launched(launch_grad(a, stream), "gradients"))) return rc;
+    Maps maps;
+    if (!make_maps(maps, a)) return fail(WKV7_ERR_CUDA, "no tensor maps of q, k, v and d_o");
+    if ((rc = wkv7::api_status_word(&a.status)) || (rc = chains(maps, a, true, true, stream))) return rc;
+    if ((rc = launched(launch_grad(maps, a, stream), "gradients"))) return rc;
   } else {
     if ((rc = launched(launch_states(a, false, true, stream), "states"))) return rc;
     if ((rc = launched(launch_rows_grad(a, stream), "gradients"))) return rc;

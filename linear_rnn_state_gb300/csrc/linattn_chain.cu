@@ -7,7 +7,9 @@
 // P x and a S^T end as bfloat16 values, so P and S enter them as pairs of bfloat16 (16 bits); u . x enters
 // the state, an fp32 result, in three parts (24 bits).
 //
-// Eight warps work on rows; one forms the decays of a chunk to come, one issues the products. With up to 64 keys
+// Eight warps work on rows; one brings the tiles of a chunk to come (TMA) and forms its decays, one issues the products.
+// For the gradients (linattn_grad.cu) the state before each chunk leaves as the tiles that products read, its pair
+// and a third part, by bulk copies. With up to 64 keys
 // the scores of chunk i + 1 are made and decayed while the other products of chunk i run (three stages of
 // tiles, two places for the scores); wider keys leave room for two stages, and u . x goes by halves of the tokens.
 #include "linattn_tc.cuh"
@@ -16,7 +18,7 @@ namespace linattn {
 namespace {
 
 constexpr int kWorkers = 256, kThreads = kWorkers + 64;
-constexpr int kDecayWarp = 8, kIssueWarp = 9;
+constexpr int kBringWarp = 8, kIssueWarp = 9;
 
 template <int KP, bool kUpper>
 struct Smem {
@@ -27,9 +29,10 @@ struct Smem {
     bf16_t a[kCT * KP], b[kCT * KP], x[kCT * 64];
   };
   Stage stage[kStages];
-  bf16_t xt[3 * kXt * 64];  // u . x; then the rows on their way out
+  bf16_t xt[3 * kXt * 64];  // u . x
   bf16_t s[2 * 64 * KP];    // the state's pair
   Dec d[3];
+  uint64_t full[kStages];               // the tiles are there
   uint64_t scored, first, summed, out;  // the scores; the first half of the state's sum, all of it; the rows
   uint32_t tmem;
 };
@@ -40,7 +43,7 @@ struct Plan {
 };
 
 template <int KP, bool kUpper>
-__global__ void __launch_bounds__(kThreads, 1) chain_kernel(const Args a, const Plan plan) {
+__global__ void __launch_bounds__(kThreads, 1) chain_kernel(const __grid_constant__ Maps maps, const Args a, const Plan plan) {
   extern __shared__ __align__(1024) unsigned char raw[];
   using M = Smem<KP, kUpper>;
   M& sm = *reinterpret_cast<M*>(raw);
@@ -48,7 +51,7 @@ __global__ void __launch_bounds__(kThreads, 1) chain_kernel(const Args a, const 
   constexpr bool kEarly = M::kEarly;
   constexpr int kSt = M::kStages, kXt = M::kXt;
   enum { kP = 0, kIn = kEarly ? 256 : 128, kO = kIn + 64, kU = kO + 64, kCols = 512 };
-  enum { kBarX = 1, kBarP, kBarX2, kBarOut };
+  enum { kBarX = 1, kBarP, kBarX2, kBarOut, kBarFree };
   constexpr int kPair = kWorkers + 32;
   const Shape& s = a.s;
   const int tid = threadIdx.x, lane = tid & 31, warp = __shfl_sync(0xffffffffu, tid >> 5, 0), sub = warp & 3, half = warp >> 2;
@@ -64,31 +67,87 @@ __global__ void __launch_bounds__(kThreads, 1) chain_kernel(const Args a, const 
   if (warp == 0) wkv7::tmem_alloc(&sm.tmem, kCols);
   if (tid == 0) {
     for (uint64_t* b : {&sm.scored, &sm.first, &sm.summed, &sm.out}) mbar_init(b, 1);
+    for (uint64_t& b : sm.full) mbar_init(&b, 1);
     wkv7::fence_mbar_init();
   }
+  __syncthreads();
   const int n = (seg.len + kCT - 1) / kCT;
   const size_t tok = (size_t)seg.b * s.T + seg.t0;
   auto begin = [&](int i) { return (kUpper ? n - 1 - i : i) * kCT; };  // first token of the i-th chunk, from the segment's
   auto length = [&](int i) { return min(kCT, seg.len - begin(i)); };
 
-  if (warp == kDecayWarp || warp == kIssueWarp) {
+  if (warp == kBringWarp || warp == kIssueWarp) {
     const float* g = s.fixed ? a.g + hv : a.g + tok * s.Hv + hv;
     auto decays = [&](int i) {
       make_decays(sm.d[i % 3], s.fixed ? g : g + (size_t)begin(i) * s.Hv, s.fixed ? 0 : s.Hv, length(i), s.scale, lane);
     };
-    const int mine = warp - kDecayWarp;
-    if (mine < n) decays(mine);
-    __syncthreads();
-    tmem_fence_after_sync();
-    if (warp == kDecayWarp) {
+    Patience wait{a.status};
+    if (warp == kBringWarp) {
+      constexpr int kLead = kEarly ? 2 : 1;  // chunks ahead
+      const CUtensorMap *ma = kUpper ? &maps.k : &maps.q, *mb = kUpper ? &maps.q : &maps.k, *mx = kUpper ? &maps.d : &maps.v;
+      const int b_a = kUpper ? s.k_b != 0 : s.q_b != 0, b_b = kUpper ? s.q_b != 0 : s.k_b != 0, b_x = kUpper || s.v_b != 0;
+      auto bring = [&](int i) {
+        if (i < n && lane == 0) {
+          auto& st = sm.stage[i % kSt];
+          uint64_t* bar = &sm.full[i % kSt];
+          wkv7::mbar_arrive_expect_tx(bar, sizeof st);
+          const int t = seg.t0 + begin(i);
+          load_tile<KP>(st.a, ma, bar, 0, hk, t, seg.b * b_a);
+          load_tile<KP>(st.b, mb, bar, 0, hk, t, seg.b * b_b);
+          load_tile<64>(st.x, mx, bar, v0, hv, t, seg.b * b_x);
+        }
+      };
+      auto brought = [&](int i) {
+        if (i >= n) return;
+        wait(&sm.full[i % kSt], i / kSt);
+        if (s.packed && length(i) < kCT) {
+          auto& st = sm.stage[i % kSt];
+          clear_rows<KP>(st.a, length(i), lane, 32);
+          clear_rows<KP>(st.b, length(i), lane, 32);
+          clear_rows<64>(st.x, length(i), lane, 32);
+          fence_proxy_async_smem();
+        }
+      };
+      // the state before chunk i: its pair, and the third part in the place of the keys of the chunk before
+      char* const images = static_cast<char*>(kUpper ? a.dimages : a.images);
+      auto leave = [&](int i) {
+        if (plan.keep && i < n && lane == 0) {
+          char* to = images + ((size_t)chunk_slot(s, seg, seg.t0 + begin(i)) * s.Hv + hv) * image_bytes(s.K, s.V) + slice * kImagePiece;
+#pragma unroll
+          for (int part = 0; part < 3; ++part)
+#pragma unroll
+            for (int c = 0; c < KP / 64; ++c)
+              bulk_store(to + (size_t)(part * (KP / 64) + c) * slices * kImagePiece,
+                         (part < 2 ? sm.s + part * 64 * KP : sm.stage[(i + kSt - 1) % kSt].b) + c * 64 * 64, kImagePiece);
+          bulk_commit();
+        }
+      };
+      bring(0);
+      if (kEarly) bring(1);
+      if (n) decays(0);
+      brought(0);
+      if (kEarly) brought(1);
+      __syncthreads();
+      leave(0);
       if (kEarly) __syncthreads();
       for (int i = 0; i < n; ++i) {
+        if (lane == 0) bulk_wait_read();
+        __syncwarp();
+        announce(kBarFree, kPair);
+        bring(i + kLead);
         if (i + 2 < n) decays(i + 2);
+        brought(i + kLead);
+        meet(kBarOut, kPair);
+        leave(i + 1);
         __syncthreads();
       }
+      if (lane == 0) bulk_wait_all();
       __syncthreads();
       return;
     }
+    if (n > 1) decays(1);
+    __syncthreads();
+    tmem_fence_after_sync();
     const uint32_t tm = sm.tmem;
     auto scores = [&](int i) {
       const uint64_t da = desc(sm.stage[i % kSt].a), db = desc(sm.stage[i % kSt].b);
@@ -168,26 +227,7 @@ __global__ void __launch_bounds__(kThreads, 1) chain_kernel(const Args a, const 
 
   // ------------------------------------------------------------------ rows ---
   const int row = sub * 32 + lane;
-  const long long st_a = kUpper ? s.k_t : s.q_t, st_b = kUpper ? s.q_t : s.k_t, st_x = kUpper ? (long long)s.Hv * s.V : s.v_t;
-  const bf16_t* q = static_cast<const bf16_t*>(a.q) + seg.b * s.q_b + seg.t0 * s.q_t + (size_t)hk * s.K;
-  const bf16_t* k = static_cast<const bf16_t*>(a.k) + seg.b * s.k_b + seg.t0 * s.k_t + (size_t)hk * s.K;
-  const bf16_t* pa = kUpper ? k : q;
-  const bf16_t* pb = kUpper ? q : k;
-  const bf16_t* px = kUpper ? static_cast<const bf16_t*>(a.d_o) + (tok * s.Hv + hv) * s.V + v0
-                            : static_cast<const bf16_t*>(a.v) + seg.b * s.v_b + seg.t0 * s.v_t + (size_t)hv * s.V + v0;
   bf16_t* out = static_cast<bf16_t*>(kUpper ? a.dv : a.o) + (tok * s.Hv + hv) * s.V + v0;
-  auto copy = [&](int i) {
-    if (i < n) {
-      auto& st = sm.stage[i % kSt];
-      const int t0 = begin(i), len = length(i);
-      copy_tile<KP>(st.a, pa + t0 * st_a, st_a, len, s.K, tid, kWorkers);
-      copy_tile<KP>(st.b, pb + t0 * st_b, st_b, len, s.K, tid, kWorkers);
-      copy_tile<64>(st.x, px + t0 * st_x, st_x, len, vn, tid, kWorkers);
-    }
-    copies_committed();
-  };
-  copy(0);
-  if (kEarly) copy(1);
   // The state: rows 16 sub .., keys KP / 2 half .. in accumulator tiles.
   float S[kTiles][4];
   const int s_row = v0 + 16 * sub + (lane >> 2), s_col = half * (KP / 2) + 2 * (lane & 3);
@@ -205,29 +245,28 @@ __global__ void __launch_bounds__(kThreads, 1) chain_kernel(const Args a, const 
     x = v.x, y = v.y;
   };
   auto store = [](float2* p, float& x, float& y) { *p = make_float2(x, y); };
-  auto planes = [&] {
+  auto planes = [&](bf16_t* third) {
 #pragma unroll
     for (int t = 0; t < kTiles; t += 2) {
-      Frag<2> f;
+      Frag<3> f;
       to_a(f, S[t], S[t + 1]);
-      bf16_t* p = sm.s + at(64, 16 * sub + (lane & 15), half * (KP / 2) + 8 * t + (lane >> 4) * 8);
-      stsm4(p, f.p[0]);
-      stsm4(p + 64 * KP, f.p[1]);
+      const int o = at(64, 16 * sub + (lane & 15), half * (KP / 2) + 8 * t + (lane >> 4) * 8);
+      stsm4(sm.s + o, f.p[0]);
+      stsm4(sm.s + 64 * KP + o, f.p[1]);
+      if (plan.keep) stsm4(third + o, f.p[2]);
     }
   };
 #pragma unroll
   for (int t = 0; t < kTiles; ++t)
 #pragma unroll
     for (int e = 0; e < 4; ++e) S[t][e] = 0.f;
-  auto state_of = [&](int i) { return states + (chunk_slot(s, seg, seg.t0 + begin(i)) * s.Hv + hv) * state; };
   const size_t ends = ((size_t)seg.seq * s.Hv + hv) * state + (size_t)s_row * s.K + s_col;
   float* init = const_cast<float*>(kUpper ? a.dS_final : a.s_init);
   if (plan.resume)
-    each(state_of(0), load);
+    each(states + (chunk_slot(s, seg, seg.t0 + begin(0)) * s.Hv + hv) * state, load);
   else if (init)
     each(init + ends, load);
-  planes();
-  copies_landed();
+  planes(sm.stage[kSt - 1].b);
   fence_proxy_async_smem();
   tmem_fence_before_sync();
   __syncthreads();
@@ -266,7 +305,10 @@ __global__ void __launch_bounds__(kThreads, 1) chain_kernel(const Args a, const 
       load8(x, x0 + at(kCT, h * kXt + r, (e & 7) * 8));
       const float f = u[h * kXt + r];
 #pragma unroll
-      for (int j = 0; j < 8; ++j) x[j] *= f;
+      for (int j = 0; j < 8; j += 2) {
+        const float2 y = times2(make_float2(x[j], x[j + 1]), make_float2(f, f));
+        x[j] = y.x, x[j + 1] = y.y;
+      }
       put8<3>(sm.xt + at(kXt, r, (e & 7) * 8), kXt * 64, x);
     }
     fence_proxy_async_smem();
@@ -277,8 +319,8 @@ __global__ void __launch_bounds__(kThreads, 1) chain_kernel(const Args a, const 
   }
   for (int i = 0; i < n; ++i) {
     const auto& d = sm.d[i % 3];
-    copy(kEarly ? i + 2 : i + 1);
-    if (plan.keep) each(state_of(i), store);
+    auto& st = sm.stage[i % kSt];
+    wait(&sm.full[i % kSt], i / kSt);
     scaled(i, 0);
     announce(kBarX, kPair);
     if (kEarly) {
@@ -301,7 +343,8 @@ __global__ void __launch_bounds__(kThreads, 1) chain_kernel(const Args a, const 
 #pragma unroll
         for (int e = 0; e < 4; ++e) S[t + j][e] = fmaf(d.whole, S[t + j][e], x[j][e]);
     }
-    planes();
+    meet(kBarFree, kPair);
+    planes(st.b);
     wait(&sm.out, i);
     tmem_fence_after_sync();
     {
@@ -316,21 +359,21 @@ __global__ void __launch_bounds__(kThreads, 1) chain_kernel(const Args a, const 
         uint32_t o[4];
 #pragma unroll
         for (int j = 0; j < 4; ++j) o[j] = pack2(fmaf(w, x[8 * p + 2 * j], y[8 * p + 2 * j]), fmaf(w, x[8 * p + 2 * j + 1], y[8 * p + 2 * j + 1]));
-        *reinterpret_cast<uint4*>(sm.xt + at(kCT, row, 32 * half + 8 * p)) = make_uint4(o[0], o[1], o[2], o[3]);
+        *reinterpret_cast<uint4*>(st.a + at(kCT, row, 32 * half + 8 * p)) = make_uint4(o[0], o[1], o[2], o[3]);
       }
     }
-    meet(kBarOut, kWorkers);
+    fence_proxy_async_smem();
+    meet(kBarOut, kPair);
     {
       const int len = length(i);
       bf16_t* p = out + (size_t)begin(i) * s.Hv * s.V;
 #pragma unroll
       for (int e = 0; e < 4; ++e) {
         const int r = (e * kWorkers + tid) >> 3, c = (tid & 7) * 8;
-        const uint4 v = *reinterpret_cast<const uint4*>(sm.xt + at(kCT, r, c));
+        const uint4 v = *reinterpret_cast<const uint4*>(st.a + at(kCT, r, c));
         if (r < len && c < vn) *reinterpret_cast<uint4*>(p + (size_t)r * s.Hv * s.V + c) = v;
       }
     }
-    copies_landed();
     fence_proxy_async_smem();
     tmem_fence_before_sync();
     __syncthreads();
@@ -343,7 +386,7 @@ __global__ void __launch_bounds__(kThreads, 1) chain_kernel(const Args a, const 
 }
 
 template <int KP, bool kUpper>
-cudaError_t launch(const Args& a, const Plan& plan, cudaStream_t stream) {
+cudaError_t launch(const Maps& maps, const Args& a, const Plan& plan, cudaStream_t stream) {
   const size_t smem = sizeof(Smem<KP, kUpper>);
   static_assert(sizeof(Smem<KP, kUpper>) <= 232448, "shared memory of a block");
   static std::atomic<unsigned long long> done{0};
@@ -351,16 +394,16 @@ cudaError_t launch(const Args& a, const Plan& plan, cudaStream_t stream) {
   if (e != cudaSuccess) return e;
   const Shape& s = a.s;
   const long long segs = plan.resume ? slot_count(s.B, s.T, s.nseq, s.packed, kCT * plan.chunks) : s.nseq;
-  chain_kernel<KP, kUpper><<<(unsigned)(segs * s.Hv * ((s.V + 63) / 64)), kThreads, smem, stream>>>(a, plan);
+  chain_kernel<KP, kUpper><<<(unsigned)(segs * s.Hv * ((s.V + 63) / 64)), kThreads, smem, stream>>>(maps, a, plan);
   return cudaGetLastError();
 }
 
 }  // namespace
 
-cudaError_t launch_chain(const Args& a, bool backward, int chunks, bool resume, bool keep, cudaStream_t stream) {
+cudaError_t launch_chain(const Maps& maps, const Args& a, bool backward, int chunks, bool resume, bool keep, cudaStream_t stream) {
   const Plan plan{chunks, resume, keep};
-  if (a.s.K <= 64) return backward ? launch<64, true>(a, plan, stream) : launch<64, false>(a, plan, stream);
-  return backward ? launch<128, true>(a, plan, stream) : launch<128, false>(a, plan, stream);
+  if (a.s.K <= 64) return backward ? launch<64, true>(maps, a, plan, stream) : launch<64, false>(maps, a, plan, stream);
+  return backward ? launch<128, true>(maps, a, plan, stream) : launch<128, false>(maps, a, plan, stream);
 }
 
 }  // namespace linattn

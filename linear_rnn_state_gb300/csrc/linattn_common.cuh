@@ -44,6 +44,21 @@ __device__ __forceinline__ uint32_t pack2(float lo, float hi) {
   return r;
 }
 __device__ __forceinline__ float2 unpack2(uint32_t u) { return make_float2(__uint_as_float(u << 16), __uint_as_float(u & 0xFFFF0000u)); }
+// Two floats at once: a - b (exact where b is a's rounding), a b.
+__device__ __forceinline__ float2 minus2(float2 a, float2 b) {
+  float2 d;
+  asm("{\n .reg .b64 x, y;\n mov.b64 x, {%2, %3};\n mov.b64 y, {%4, %5};\n sub.rn.f32x2 x, x, y;\n mov.b64 {%0, %1}, x;\n}"
+      : "=f"(d.x), "=f"(d.y)
+      : "f"(a.x), "f"(a.y), "f"(b.x), "f"(b.y));
+  return d;
+}
+__device__ __forceinline__ float2 times2(float2 a, float2 b) {
+  float2 d;
+  asm("{\n .reg .b64 x, y;\n mov.b64 x, {%2, %3};\n mov.b64 y, {%4, %5};\n mul.rn.f32x2 x, x, y;\n mov.b64 {%0, %1}, x;\n}"
+      : "=f"(d.x), "=f"(d.y)
+      : "f"(a.x), "f"(a.y), "f"(b.x), "f"(b.y));
+  return d;
+}
 // (a, b) as kP packed parts, each the rounding of what the ones before leave. (An infinity
 // leaves NaN; the products that meet it are non-finite anyway.)
 template <int kP>
@@ -52,8 +67,8 @@ __device__ __forceinline__ void split2(float a, float b, uint32_t (&p)[kP]) {
   for (int i = 0; i < kP; ++i) {
     p[i] = pack2(a, b);
     if (i + 1 < kP) {
-      const float2 f = unpack2(p[i]);
-      a -= f.x, b -= f.y;
+      const float2 f = unpack2(p[i]), r = minus2(make_float2(a, b), f);
+      a = r.x, b = r.y;
     }
   }
 }

@@ -31,7 +31,7 @@ struct Smem {
   float pairs[4][kCT];    // of a block of 32 rows: the sums over j < t
   float dots[2][2][kCT];  // q.(S's part of dq), k.(D's part of dk), by halves of the columns
   float whole[8];
-  uint64_t done[2];
+  uint64_t done[2], full[2];  // products; tiles of q and k or of v and do, the state
   uint32_t tmem;
 };
 
@@ -52,7 +52,7 @@ __device__ __forceinline__ float warp_sum(float x) {
 }
 
 template <int KP, int VP, bool kShared>
-__global__ void __launch_bounds__(kThreads, KP == 64 && VP == 64 && !kShared ? 2 : 1) grad_kernel(const Args a) {
+__global__ void __launch_bounds__(kThreads, KP == 64 && VP == 64 && !kShared ? 2 : 1) grad_kernel(const __grid_constant__ Maps maps, const Args a) {
   extern __shared__ __align__(1024) unsigned char raw[];
   Smem<KP, VP>& sm = *reinterpret_cast<Smem<KP, VP>*>(raw);
   constexpr int kSlices = KP / 64, kCols = KP == 64 ? 256 : 512;
@@ -66,18 +66,17 @@ __global__ void __launch_bounds__(kThreads, KP == 64 && VP == 64 && !kShared ? 2
   const bool dg = a.dg != nullptr;
   if (warp == 0) wkv7::tmem_alloc(&sm.tmem, kCols);
   if (tid == 0) {
-    mbar_init(&sm.done[0], 1), mbar_init(&sm.done[1], 1);
+    mbar_init(&sm.done[0], 1), mbar_init(&sm.done[1], 1), mbar_init(&sm.full[0], 1), mbar_init(&sm.full[1], 1);
     wkv7::fence_mbar_init();
   }
-  copy_tile<KP>(sm.q, static_cast<const bf16_t*>(a.q) + c.b * s.q_b + c.t0 * s.q_t + (size_t)hk * s.K, s.q_t, c.len, s.K, tid, kThreads);
-  copy_tile<KP>(sm.k, static_cast<const bf16_t*>(a.k) + c.b * s.k_b + c.t0 * s.k_t + (size_t)hk * s.K, s.k_t, c.len, s.K, tid, kThreads);
   float acc[2][kShared ? 32 * kSlices : 1];
 #pragma unroll
   for (int i = 0; i < 2; ++i)
 #pragma unroll
     for (int j = 0; j < (kShared ? 32 * kSlices : 1); ++j) acc[i][j] = 0.f;
   Patience wait{a.status};
-  uint32_t turn0 = 0, turn1 = 0, tm = 0;
+  uint32_t turn0 = 0, turn1 = 0, turn2 = 0, turn3 = 0, tm = 0;
+  __syncthreads();
   // 64 columns of rows from shared memory to dq or dk
   auto leave = [&](bf16_t* to, int sl) {
     __syncthreads();
@@ -88,6 +87,7 @@ __global__ void __launch_bounds__(kThreads, KP == 64 && VP == 64 && !kShared ? 2
       if (r < c.len && 64 * sl + col < s.K)
         *reinterpret_cast<uint4*>(p + (size_t)r * s.Hk * s.K + col) = *reinterpret_cast<const uint4*>(sm.s + at(kCT, r, col));
     }
+    fence_proxy_async_smem();
     __syncthreads();
   };
   auto put_row = [&](const float* x) {  // the thread's 32 columns
@@ -98,13 +98,25 @@ __global__ void __launch_bounds__(kThreads, KP == 64 && VP == 64 && !kShared ? 2
                      pack2(x[8 * p + 6], x[8 * p + 7]));
   };
   for (int hv = hk * group; hv < hk * group + group; ++hv) {
-    copy_tile<VP>(sm.v, static_cast<const bf16_t*>(a.v) + c.b * s.v_b + c.t0 * s.v_t + (size_t)hv * s.V, s.v_t, c.len, s.V, tid, kThreads);
-    copy_tile<VP>(sm.d, static_cast<const bf16_t*>(a.d_o) + (tok * s.Hv + hv) * s.V, (long long)s.Hv * s.V, c.len, s.V, tid, kThreads);
-    copies_committed();
+    if (tid == 0) {
+      const bool all = hv == hk * group;
+      wkv7::mbar_arrive_expect_tx(&sm.full[0], (all ? sizeof sm.q + sizeof sm.k : 0) + sizeof sm.v + sizeof sm.d);
+      if (all) {
+        load_tile<KP>(sm.q, &maps.q, &sm.full[0], 0, hk, c.t0, s.q_b ? c.b : 0);
+        load_tile<KP>(sm.k, &maps.k, &sm.full[0], 0, hk, c.t0, s.k_b ? c.b : 0);
+      }
+      load_tile<VP>(sm.v, &maps.v, &sm.full[0], 0, hv, c.t0, s.v_b ? c.b : 0);
+      load_tile<VP>(sm.d, &maps.d, &sm.full[0], 0, hv, c.t0, c.b);
+    }
     if (warp == 7) make_decays(sm.dec, s.fixed ? a.g + hv : a.g + tok * s.Hv + hv, s.fixed ? 0 : s.Hv, c.len, s.scale, lane);
-    const float* S = a.states + ((size_t)slot * s.Hv + hv) * s.V * s.K;
-    const float* D = a.dstates + ((size_t)slot * s.Hv + hv) * s.V * s.K;
-    copies_landed();
+    const size_t image = ((size_t)slot * s.Hv + hv) * image_bytes(s.K, s.V);
+    const char *S = static_cast<const char*>(a.images) + image, *D = static_cast<const char*>(a.dimages) + image;
+    wait(&sm.full[0], turn2++);
+    if (s.packed && c.len < kCT) {
+      if (hv == hk * group) clear_rows<KP>(sm.q, c.len, tid, kThreads), clear_rows<KP>(sm.k, c.len, tid, kThreads);
+      clear_rows<VP>(sm.v, c.len, tid, kThreads);
+      clear_rows<VP>(sm.d, c.len, tid, kThreads);
+    }
     fence_proxy_async_smem();
     tmem_fence_before_sync();
     __syncthreads();
@@ -129,23 +141,38 @@ __global__ void __launch_bounds__(kThreads, KP == 64 && VP == 64 && !kShared ? 2
         }
         __syncwarp();
       }
-      auto planes = [&](int sl) {
-#pragma unroll 2
-        for (int i = tid; i < VP * 8; i += kThreads) {
-          const int r = i >> 3, col = 64 * sl + (i & 7) * 8;
-          float x[8] = {0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f};
-          if (r < s.V && col < s.K) {
-            load8(x, (kUpper ? D : S) + (size_t)r * s.K + col);
-            if (!kUpper && dg) {
-              float y[8];
-              load8(y, D + (size_t)r * s.K + col);
+      // 64 keys of the state. (What was there has been read: the products that did are waited for.)
+      auto fetch = [&](int sl) {
+        if (tid == 0) {
+          wkv7::mbar_arrive_expect_tx(&sm.full[1], sizeof sm.s);
 #pragma unroll
-              for (int e = 0; e < 8; ++e) whole = fmaf(x[e], y[e], whole);
-            }
-          }
-          put8<3>(sm.s + at(VP, r, (i & 7) * 8), VP * 64, x);
+          for (int part = 0; part < 3; ++part)
+            bulk_load(sm.s + part * VP * 64, (kUpper ? D : S) + (size_t)(part * kSlices + sl) * VP * 128, VP * 128, &sm.full[1]);
         }
-        fence_proxy_async_smem();
+      };
+      // and their part of <S, D>
+      auto fetched = [&](int sl) {
+        wait(&sm.full[1], turn3++);
+        if (!kUpper && dg) {
+          const bf16_t* other = reinterpret_cast<const bf16_t*>(D + (size_t)sl * VP * 128);
+#pragma unroll 2
+          for (int i = tid; i < VP * 8; i += kThreads) {
+            float x[8], y[8], t[8];
+            load8(x, sm.s + 8 * i), load8(y, other + 8 * i);
+#pragma unroll
+            for (int part = 1; part < 3; ++part) {
+              load8(t, sm.s + part * VP * 64 + 8 * i);
+#pragma unroll
+              for (int e = 0; e < 8; ++e) x[e] += t[e];
+              load8(t, other + part * kSlices * VP * 64 + 8 * i);
+#pragma unroll
+              for (int e = 0; e < 8; ++e) y[e] += t[e];
+            }
+#pragma unroll
+            for (int e = 0; e < 8; ++e) whole = fmaf(x[e], y[e], whole);
+          }
+          fence_proxy_async_smem();
+        }
       };
       auto inter = [&](int sl) {
         const uint64_t da = desc(ta), ds = desc(sm.s);
@@ -155,7 +182,7 @@ __global__ void __launch_bounds__(kThreads, KP == 64 && VP == 64 && !kShared ? 2
           for (int ks = 0; ks < VP / 16; ++ks)
             tc_mma(tm + kIn + 64 * sl, da + along<kCT>(ks), ds + across(ks) + part * (VP * 128 >> 4), product_of(128, 64, false, true), part < 2 || ks > 0);
       };
-      planes(0);
+      fetch(0);
       wait(&sm.done[0], turn0++);
       tmem_fence_after_sync();
 #pragma unroll 1
@@ -184,6 +211,7 @@ __global__ void __launch_bounds__(kThreads, KP == 64 && VP == 64 && !kShared ? 2
           store_zeros(mine + kE + 32 * blk);
         }
       }
+      fetched(0);
       wkv7::tmem_wait_st();
       tmem_fence_before_sync();
       __syncthreads();
@@ -206,7 +234,9 @@ __global__ void __launch_bounds__(kThreads, KP == 64 && VP == 64 && !kShared ? 2
       }
       wait(&sm.done[1], turn1++);
       if (kSlices == 2) {
-        planes(1);
+        __syncthreads();  // <S, D> has been read
+        fetch(1);
+        fetched(1);
         tmem_fence_before_sync();
         __syncthreads();
         if (warp == 0) {
@@ -307,24 +337,24 @@ __global__ void __launch_bounds__(kThreads, KP == 64 && VP == 64 && !kShared ? 2
 }
 
 template <int KP, int VP, bool kShared>
-cudaError_t launch(const Args& a, cudaStream_t stream) {
+cudaError_t launch(const Maps& maps, const Args& a, cudaStream_t stream) {
   const size_t smem = sizeof(Smem<KP, VP>);
   static std::atomic<unsigned long long> done{0};
   const cudaError_t e = allow_smem(reinterpret_cast<const void*>(grad_kernel<KP, VP, kShared>), smem, done);
   if (e != cudaSuccess) return e;
-  grad_kernel<KP, VP, kShared><<<(unsigned)((size_t)a.s.slots * a.s.Hk), kThreads, smem, stream>>>(a);
+  grad_kernel<KP, VP, kShared><<<(unsigned)((size_t)a.s.slots * a.s.Hk), kThreads, smem, stream>>>(maps, a);
   return cudaGetLastError();
 }
 template <int KP, int VP>
-cudaError_t shared(const Args& a, cudaStream_t stream) {
-  return a.s.Hv > a.s.Hk ? launch<KP, VP, true>(a, stream) : launch<KP, VP, false>(a, stream);
+cudaError_t shared(const Maps& maps, const Args& a, cudaStream_t stream) {
+  return a.s.Hv > a.s.Hk ? launch<KP, VP, true>(maps, a, stream) : launch<KP, VP, false>(maps, a, stream);
 }
 
 }  // namespace
 
-cudaError_t launch_grad(const Args& a, cudaStream_t stream) {
-  if (a.s.K <= 64) return a.s.V <= 64 ? shared<64, 64>(a, stream) : shared<64, 128>(a, stream);
-  return a.s.V <= 64 ? shared<128, 64>(a, stream) : shared<128, 128>(a, stream);
+cudaError_t launch_grad(const Maps& maps, const Args& a, cudaStream_t stream) {
+  if (a.s.K <= 64) return a.s.V <= 64 ? shared<64, 64>(maps, a, stream) : shared<64, 128>(maps, a, stream);
+  return a.s.V <= 64 ? shared<128, 64>(maps, a, stream) : shared<128, 128>(maps, a, stream);
 }
 
 }  // namespace linattn

@@ -46,6 +46,7 @@ struct Args {
   float *states;       // [slots][Hv][V][K]: the state before each chunk
   float *dstates;      // the gradient of the state after each chunk
   float *decay;        // [slots][Hv]: the whole decay of each chunk
+  void *images, *dimages;  // bfloat16: states and dstates as the gradients' products read them (linattn_tc.cuh)
   double *part;        // [kParts][Hv]: sums of dg over tokens
   unsigned* status;    // the device's status word
 };
@@ -57,10 +58,13 @@ cudaError_t launch_states(const Args& a, bool bf16, bool backward, cudaStream_t 
 cudaError_t launch_rows_o(const Args& a, cudaStream_t stream);
 cudaError_t launch_rows_grad(const Args& a, cudaStream_t stream);
 // bfloat16: o (backward: dv), segments of `chunks` chunks one after the other in a block. resume: from `states` (or
-// dstates); else these are written on the way where keep, as is the last one.
-cudaError_t launch_chain(const Args& a, bool backward, int chunks, bool resume, bool keep, cudaStream_t stream);
+// dstates); else whole sequences, and the last state is written. keep: images (or dimages) too.
+struct Maps;
+cudaError_t launch_chain(const Maps& maps, const Args& a, bool backward, int chunks, bool resume, bool keep, cudaStream_t stream);
 // bfloat16: dq, dk and dg of all chunks at once.
-cudaError_t launch_grad(const Args& a, cudaStream_t stream);
+cudaError_t launch_grad(const Maps& maps, const Args& a, cudaStream_t stream);
+// The tensor maps of q, k, v and (where not null) do; false: the driver has no encoder or refuses.
+bool make_maps(Maps& maps, const Args& a);
 cudaError_t launch_dg_sums(const Args& a, cudaStream_t stream);          // dg_fixed from dg
 
 // Zeros in up to five outputs of a packed call at the tokens of no sequence.

@@ -7,6 +7,7 @@
 #pragma once
 
 #include "linattn_common.cuh"
+#include "linattn_maps.h"
 #include "wkv7_tmem.cuh"
 
 namespace linattn {
@@ -114,36 +115,48 @@ struct Patience {
 
 // ---------------------------------------------------------------- copies ---
 
-__device__ __forceinline__ void copy16(void* dst, const void* src, bool in) {
-  asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(smem_addr(dst)), "l"(src), "r"(in ? 16 : 0) : "memory");
-}
-__device__ __forceinline__ void copies_committed() { asm volatile("cp.async.commit_group;" ::: "memory"); }
-__device__ __forceinline__ void copies_landed() { asm volatile("cp.async.wait_group 0;" ::: "memory"); }
-// Rows 0 .. 127 (zeros from `len` on) and kCols columns (zeros from `cols` on) of a tile.
+// kCols columns of a tile from token t on; the bytes that will arrive.
 template <int kCols>
-__device__ __forceinline__ void copy_tile(bf16_t* dst, const bf16_t* src, long long stride, int len, int cols, int tid, int threads) {
-  constexpr int kPieces = kCols / 8;
-#pragma unroll 4
-  for (int i = tid; i < kCT * kPieces; i += threads) {
-    const int row = i / kPieces, col = i % kPieces * 8;
-    const bool in = row < len && col < cols;
-    copy16(dst + at(kCT, row, col), in ? src + row * stride + col : src, in);
-  }
+__device__ __forceinline__ void load_tile(bf16_t* dst, const CUtensorMap* map, uint64_t* bar, int col, int head, int t, int b) {
+#pragma unroll
+  for (int c = 0; c < kCols; c += 64) wkv7::tma_load_4d(dst + c * kCT, map, bar, col + c, head, t, b);
 }
+// The rows of a packed chunk from `len` on, which belong to another sequence (whose values may be anything).
+template <int kCols>
+__device__ __forceinline__ void clear_rows(bf16_t* tile, int len, int tid, int threads) {
+  for (int i = tid; i < (kCT - len) * (kCols / 8); i += threads)
+    *reinterpret_cast<uint4*>(tile + at(kCT, len + i / (kCols / 8), i % (kCols / 8) * 8)) = make_uint4(0, 0, 0, 0);
+}
+__device__ __forceinline__ void bulk_load(void* dst, const void* src, uint32_t bytes, uint64_t* bar) {
+  asm volatile("cp.async.bulk.shared::cluster.global.mbarrier::complete_tx::bytes [%0], [%1], %2, [%3];" ::"r"(smem_addr(dst)), "l"(src),
+               "r"(bytes), "r"(smem_addr(bar))
+               : "memory");
+}
+__device__ __forceinline__ void bulk_store(void* dst, const void* src, uint32_t bytes) {
+  asm volatile("cp.async.bulk.global.shared::cta.bulk_group [%0], [%1], %2;" ::"l"(dst), "r"(smem_addr(src)), "r"(bytes) : "memory");
+}
+__device__ __forceinline__ void bulk_commit() { asm volatile("cp.async.bulk.commit_group;" ::: "memory"); }
+__device__ __forceinline__ void bulk_wait_read() { asm volatile("cp.async.bulk.wait_group.read 0;" ::: "memory"); }
+__device__ __forceinline__ void bulk_wait_all() { asm volatile("cp.async.bulk.wait_group 0;" ::: "memory"); }
 
 // ---------------------------------------------------------------- decays ---
 
 // A chunk's factors, by one warp. Lower (o, dq: row i, columns j <= i) and upper (dv, dk: row j, columns i >= j):
 //   w: of the state's part of a row; u: of a token in the next state
-//   c: of a column in 32-column blocks away from the diagonal, where e^{G_i - G_j} = e^{G_i - G_r} e^{G_r - G_j} with
-//      r between the two: both at most 1 where no log decay is above 0.
+//   c: of a column in blocks of 32 columns off the diagonal, where e^{G_i - G_j} = e^{G_i - G_r} e^{G_r - G_j} with
+//      r between the two: both at most 1 where no log decay is above 0
+//   to, from: e^{G - m} and e^{m - G} with m the middle of the range of G in a block of 32 tokens, whose products are
+//      the decays of the diagonal's blocks where the range is at most kNear
+constexpr float kNear = 60.f;  // e^+-30 leaves the products far from overflow
 template <bool kLower, bool kUpper>
 struct alignas(16) Decays {
   static constexpr int kSets = kLower + kUpper;
   float2 G[kCT];
   float w[kSets][kCT], u[kSets][kCT], c[kSets][kCT];
+  float to[kCT], from[kCT];
   float whole;  // e^{Gc}
   int up;       // a log decay is above 0
+  int near;     // bit b: block b's range is small
   static __device__ constexpr int set(bool upper) { return kSets == 2 ? upper : 0; }
 };
 template <bool kLower, bool kUpper>
@@ -151,6 +164,7 @@ __device__ __forceinline__ void make_decays(Decays<kLower, kUpper>& d, const flo
   const bool up = running_sums<kCT / 32>(d.G, g, stride, len, lane);
   __syncwarp();
   const float2 last = d.G[kCT - 1];
+  int near = 0;
 #pragma unroll
   for (int i = 0; i < kCT / 32; ++i) {
     const int j = 32 * i + lane;
@@ -161,17 +175,24 @@ __device__ __forceinline__ void make_decays(Decays<kLower, kUpper>& d, const flo
       constexpr int k = Decays<kLower, kUpper>::kSets - 1;
       d.w[k][j] = tail, d.u[k][j] = head, d.c[k][j] = i ? expf(minus(G, d.G[32 * i - 1])) : 1.f;
     }
+    float hi = G.x, lo = G.x;
+#pragma unroll
+    for (int o = 16; o >= 1; o >>= 1) hi = fmaxf(hi, __shfl_xor_sync(0xffffffffu, hi, o)), lo = fminf(lo, __shfl_xor_sync(0xffffffffu, lo, o));
+    const float m = 0.5f * (hi + lo), x = (G.x - m) + G.y;
+    if (__all_sync(0xffffffffu, hi - lo <= kNear && G.x == G.x)) near |= 1 << i;
+    d.to[j] = expf(x), d.from[j] = expf(-x);
   }
-  if (lane == 0) d.whole = expf(last.x + last.y), d.up = up;
+  if (lane == 0) d.whole = expf(last.x + last.y), d.up = up, d.near = near;
 }
 
 // 32 columns (block `blk`) of a row's products times scale e^{G_i - G_j}, 0 outside the mask.
 template <bool kUpper, typename D>
 __device__ __forceinline__ void decayed(float (&x)[32], const D& d, int row, int blk, float scale) {
-  const float2 Gr = d.G[row];
-  if (blk == row >> 5 || d.up) {
+  const bool diagonal = blk == row >> 5;
+  const int at = row - 32 * blk;  // the diagonal's column
+  if (diagonal ? !(d.near >> blk & 1) : d.up) {
+    const float2 Gr = d.G[row];
     const float4* G = reinterpret_cast<const float4*>(d.G + 32 * blk);  // two tokens
-    const int at = row - 32 * blk;                                      // the diagonal's column
 #pragma unroll
     for (int j = 0; j < 32; j += 2) {
       const float4 g = G[j / 2];
@@ -181,14 +202,29 @@ __device__ __forceinline__ void decayed(float (&x)[32], const D& d, int row, int
       const float e0 = scale * __expf(k0 ? (kUpper ? -d0 : d0) : 0.f), e1 = scale * __expf(k1 ? (kUpper ? -d1 : d1) : 0.f);
       x[j] = k0 ? x[j] * e0 : 0.f, x[j + 1] = k1 ? x[j + 1] * e1 : 0.f;
     }
+    return;
+  }
+  float r;
+  const float4* c;
+  if (diagonal) {
+    r = scale * (kUpper ? d.from : d.to)[row];
+    c = reinterpret_cast<const float4*>((kUpper ? d.to : d.from) + 32 * blk);
   } else {
-    const float r = scale * __expf(kUpper ? minus(d.G[32 * blk - 1], Gr) : minus(Gr, d.G[32 * blk + 31]));
-    const float4* c = reinterpret_cast<const float4*>(d.c[D::set(kUpper)] + 32 * blk);
+    r = scale * __expf(kUpper ? minus(d.G[32 * blk - 1], d.G[row]) : minus(d.G[row], d.G[32 * blk + 31]));
+    c = reinterpret_cast<const float4*>(d.c[D::set(kUpper)] + 32 * blk);
+  }
+  const float2 rr = make_float2(r, r);
 #pragma unroll
-    for (int j = 0; j < 32; j += 4) {
-      const float4 f = c[j / 4];
-      x[j] *= f.x * r, x[j + 1] *= f.y * r, x[j + 2] *= f.z * r, x[j + 3] *= f.w * r;
-    }
+  for (int j = 0; j < 32; j += 4) {
+    const float4 f = c[j / 4];
+    const float2 a = times2(make_float2(x[j], x[j + 1]), times2(make_float2(f.x, f.y), rr));
+    const float2 b = times2(make_float2(x[j + 2], x[j + 3]), times2(make_float2(f.z, f.w), rr));
+    x[j] = a.x, x[j + 1] = a.y, x[j + 2] = b.x, x[j + 3] = b.y;
+  }
+  if (diagonal) {
+#pragma unroll
+    for (int j = 0; j < 32; ++j)
+      if (kUpper ? j < at : j > at) x[j] = 0.f;
   }
 }
 // 32 values as pairs into their place in tensor memory.
