@@ -7,7 +7,7 @@
 // P x and a S^T end as bfloat16 values, so P and S enter them as pairs of bfloat16 (16 bits); u . x enters
 // the state, an fp32 result, in three parts (24 bits).
 //
-// Eight warps work on rows; one brings the tiles of a chunk to come (TMA) and forms its decays, one issues the products.
+// Sixteen warps work on rows; one brings the tiles of a chunk to come (TMA), one forms its decays, one issues the products.
 // For the gradients (linattn_grad.cu) the state before each chunk leaves as the tiles that products read, its pair
 // and a third part, by bulk copies. With up to 64 keys
 // the scores of chunk i + 1 are made and decayed while the other products of chunk i run (three stages of
@@ -17,12 +17,11 @@
 namespace linattn {
 namespace {
 
-constexpr int kWorkers = 256, kThreads = kWorkers + 64;
-constexpr int kBringWarp = 8, kIssueWarp = 9;
+constexpr int kWorkers = 512, kThreads = kWorkers + 96;
+constexpr int kBringWarp = 16, kDecayWarp = 17;  // and 18 issues
 
-template <int KP, bool kUpper>
+template <int KP>
 struct Smem {
-  using Dec = Decays<!kUpper, kUpper>;
   static constexpr bool kEarly = KP == 64;
   static constexpr int kStages = kEarly ? 3 : 2, kHalves = kEarly ? 1 : 2, kXt = kCT / kHalves;
   struct Stage {
@@ -31,7 +30,7 @@ struct Smem {
   Stage stage[kStages];
   bf16_t xt[3 * kXt * 64];  // u . x
   bf16_t s[2 * 64 * KP];    // the state's pair
-  Dec d[3];
+  Decays d[3];
   uint64_t full[kStages];               // the tiles are there
   uint64_t scored, first, summed, out;  // the scores; the first half of the state's sum, all of it; the rows
   uint32_t tmem;
@@ -45,16 +44,16 @@ struct Plan {
 template <int KP, bool kUpper>
 __global__ void __launch_bounds__(kThreads, 1) chain_kernel(const __grid_constant__ Maps maps, const Args a, const Plan plan) {
   extern __shared__ __align__(1024) unsigned char raw[];
-  using M = Smem<KP, kUpper>;
+  using M = Smem<KP>;
   M& sm = *reinterpret_cast<M*>(raw);
-  constexpr int kTiles = KP / 16;  // n8 tiles of a warp's half of the keys
+  constexpr int kTiles = KP / 32;  // n8 tiles of a warp's quarter of the keys
   constexpr bool kEarly = M::kEarly;
   constexpr int kSt = M::kStages, kXt = M::kXt;
   enum { kP = 0, kIn = kEarly ? 256 : 128, kO = kIn + 64, kU = kO + 64, kCols = 512 };
   enum { kBarX = 1, kBarP, kBarX2, kBarOut, kBarFree };
   constexpr int kPair = kWorkers + 32;
   const Shape& s = a.s;
-  const int tid = threadIdx.x, lane = tid & 31, warp = __shfl_sync(0xffffffffu, tid >> 5, 0), sub = warp & 3, half = warp >> 2;
+  const int tid = threadIdx.x, lane = tid & 31, warp = __shfl_sync(0xffffffffu, tid >> 5, 0), sub = warp & 3, quarter = warp >> 2;
   const int slices = (s.V + 63) >> 6, slice = blockIdx.x % slices, hv = blockIdx.x / slices % s.Hv, slot = blockIdx.x / slices / s.Hv;
   const int hk = hv / (s.Hv / s.Hk), v0 = slice * 64, vn = min(64, s.V - v0);
   ChunkAt seg;
@@ -76,12 +75,31 @@ __global__ void __launch_bounds__(kThreads, 1) chain_kernel(const __grid_constan
   auto begin = [&](int i) { return (kUpper ? n - 1 - i : i) * kCT; };  // first token of the i-th chunk, from the segment's
   auto length = [&](int i) { return min(kCT, seg.len - begin(i)); };
 
-  if (warp == kBringWarp || warp == kIssueWarp) {
-    const float* g = s.fixed ? a.g + hv : a.g + tok * s.Hv + hv;
-    auto decays = [&](int i) {
-      make_decays(sm.d[i % 3], s.fixed ? g : g + (size_t)begin(i) * s.Hv, s.fixed ? 0 : s.Hv, length(i), s.scale, lane);
-    };
+  if (warp >= kWorkers / 32) {
     Patience wait{a.status};
+    if (warp == kDecayWarp) {
+      const float* g = s.fixed ? a.g + hv : a.g + tok * s.Hv + hv;
+      float r[4];
+      auto ask = [&](int i) {
+        if (i < n) load_decays(r, s.fixed ? g : g + (size_t)begin(i) * s.Hv, s.fixed ? 0 : s.Hv, length(i), lane);
+      };
+      auto make = [&](int i) {  // and the next chunk's are asked for
+        if (i < n) {
+          float x[4] = {r[0], r[1], r[2], r[3]};
+          ask(i + 1);
+          make_decays(sm.d[i % 3], x, s.scale, lane);
+        }
+      };
+      ask(0), make(0), make(1);
+      __syncthreads();
+      if (kEarly) __syncthreads();
+      for (int i = 0; i < n; ++i) {
+        make(i + 2);
+        __syncthreads();
+      }
+      __syncthreads();
+      return;
+    }
     if (warp == kBringWarp) {
       constexpr int kLead = kEarly ? 2 : 1;  // chunks ahead
       const CUtensorMap *ma = kUpper ? &maps.k : &maps.q, *mb = kUpper ? &maps.q : &maps.k, *mx = kUpper ? &maps.d : &maps.v;
@@ -110,9 +128,10 @@ __global__ void __launch_bounds__(kThreads, 1) chain_kernel(const __grid_constan
       };
       // the state before chunk i: its pair, and the third part in the place of the keys of the chunk before
       char* const images = static_cast<char*>(kUpper ? a.dimages : a.images);
+      char* to = images + ((size_t)(n ? chunk_slot(s, seg, seg.t0 + begin(0)) : 0) * s.Hv + hv) * image_bytes(s.K, s.V) + slice * kImagePiece;
+      const long long next = (kUpper ? -1 : 1) * (long long)(s.Hv * image_bytes(s.K, s.V));
       auto leave = [&](int i) {
         if (plan.keep && i < n && lane == 0) {
-          char* to = images + ((size_t)chunk_slot(s, seg, seg.t0 + begin(i)) * s.Hv + hv) * image_bytes(s.K, s.V) + slice * kImagePiece;
 #pragma unroll
           for (int part = 0; part < 3; ++part)
 #pragma unroll
@@ -120,11 +139,11 @@ __global__ void __launch_bounds__(kThreads, 1) chain_kernel(const __grid_constan
               bulk_store(to + (size_t)(part * (KP / 64) + c) * slices * kImagePiece,
                          (part < 2 ? sm.s + part * 64 * KP : sm.stage[(i + kSt - 1) % kSt].b) + c * 64 * 64, kImagePiece);
           bulk_commit();
+          to += next;
         }
       };
       bring(0);
       if (kEarly) bring(1);
-      if (n) decays(0);
       brought(0);
       if (kEarly) brought(1);
       __syncthreads();
@@ -135,7 +154,6 @@ __global__ void __launch_bounds__(kThreads, 1) chain_kernel(const __grid_constan
         __syncwarp();
         announce(kBarFree, kPair);
         bring(i + kLead);
-        if (i + 2 < n) decays(i + 2);
         brought(i + kLead);
         meet(kBarOut, kPair);
         leave(i + 1);
@@ -145,7 +163,6 @@ __global__ void __launch_bounds__(kThreads, 1) chain_kernel(const __grid_constan
       __syncthreads();
       return;
     }
-    if (n > 1) decays(1);
     __syncthreads();
     tmem_fence_after_sync();
     const uint32_t tm = sm.tmem;
@@ -228,9 +245,9 @@ __global__ void __launch_bounds__(kThreads, 1) chain_kernel(const __grid_constan
   // ------------------------------------------------------------------ rows ---
   const int row = sub * 32 + lane;
   bf16_t* out = static_cast<bf16_t*>(kUpper ? a.dv : a.o) + (tok * s.Hv + hv) * s.V + v0;
-  // The state: rows 16 sub .., keys KP / 2 half .. in accumulator tiles.
+  // The state: rows 16 sub .., keys KP / 4 quarter .. in accumulator tiles.
   float S[kTiles][4];
-  const int s_row = v0 + 16 * sub + (lane >> 2), s_col = half * (KP / 2) + 2 * (lane & 3);
+  const int s_row = v0 + 16 * sub + (lane >> 2), s_col = quarter * (KP / 4) + 2 * (lane & 3);
   float* const states = (kUpper ? a.dstates : a.states) + ((size_t)s_row * s.K + s_col);
   const size_t state = (size_t)s.V * s.K;
   auto each = [&](float* m, auto f) {  // pairs of the state's numbers that exist; m is where its first is
@@ -250,7 +267,7 @@ __global__ void __launch_bounds__(kThreads, 1) chain_kernel(const __grid_constan
     for (int t = 0; t < kTiles; t += 2) {
       Frag<3> f;
       to_a(f, S[t], S[t + 1]);
-      const int o = at(64, 16 * sub + (lane & 15), half * (KP / 2) + 8 * t + (lane >> 4) * 8);
+      const int o = at(64, 16 * sub + (lane & 15), quarter * (KP / 4) + 8 * t + (lane >> 4) * 8);
       stsm4(sm.s + o, f.p[0]);
       stsm4(sm.s + 64 * KP + o, f.p[1]);
       if (plan.keep) stsm4(third + o, f.p[2]);
@@ -278,18 +295,15 @@ __global__ void __launch_bounds__(kThreads, 1) chain_kernel(const __grid_constan
     const uint32_t at_p = mine + kP + (kEarly ? i % 2 * 128 : 0);
     wait(&sm.scored, i);
     tmem_fence_after_sync();
-#pragma unroll
-    for (int b = 0; b < 2; ++b) {
-      const int blk = half + 2 * b;
-      if (kUpper ? blk >= sub : blk <= sub) {
-        float x[32];
-        tc_load32(x, at_p + 32 * blk);
-        tc_loaded32(x);
-        decayed<kUpper>(x, sm.d[i % 3], row, blk, s.scale);
-        store_pairs(at_p + 32 * blk, x);
-      } else {
-        store_zeros(at_p + 32 * blk);
-      }
+    const int blk = quarter;
+    if (kUpper ? blk >= sub : blk <= sub) {
+      float x[32];
+      tc_load32(x, at_p + 32 * blk);
+      tc_loaded32(x);
+      decayed<kUpper>(x, sm.d[i % 3], row, blk, s.scale);
+      store_pairs(at_p + 32 * blk, x);
+    } else {
+      store_zeros(at_p + 32 * blk);
     }
     wkv7::tmem_wait_st();
     tmem_fence_before_sync();
@@ -297,7 +311,7 @@ __global__ void __launch_bounds__(kThreads, 1) chain_kernel(const __grid_constan
   // u . x of half h of the tokens
   auto scaled = [&](int i, int h) {
     const bf16_t* x0 = sm.stage[i % kSt].x;
-    const float* u = sm.d[i % 3].u[0];
+    const float* u = kUpper ? sm.d[i % 3].head : sm.d[i % 3].tail;
 #pragma unroll 2
     for (int e = tid; e < kXt * 8; e += kWorkers) {
       const int r = e >> 3;
@@ -335,11 +349,11 @@ __global__ void __launch_bounds__(kThreads, 1) chain_kernel(const __grid_constan
     wait(&sm.summed, i);
     tmem_fence_after_sync();
 #pragma unroll
-    for (int t = 0; t < kTiles; t += 4) {
-      float x[4][4];
-      tc_load_tiles(x, mine + kU + half * (KP / 2) + 8 * t);
+    for (int t = 0; t < kTiles; t += 2) {
+      float x[2][4];
+      tc_load_tiles(x, mine + kU + quarter * (KP / 4) + 8 * t);
 #pragma unroll
-      for (int j = 0; j < 4; ++j)
+      for (int j = 0; j < 2; ++j)
 #pragma unroll
         for (int e = 0; e < 4; ++e) S[t + j][e] = fmaf(d.whole, S[t + j][e], x[j][e]);
     }
@@ -348,18 +362,18 @@ __global__ void __launch_bounds__(kThreads, 1) chain_kernel(const __grid_constan
     wait(&sm.out, i);
     tmem_fence_after_sync();
     {
-      float x[32], y[32];
-      tc_load32(x, mine + kIn + 32 * half);
-      tc_load32(y, mine + kO + 32 * half);
-      tc_loaded32(x);
-      tc_loaded32(y);
-      const float w = d.w[0][row];
+      float x[16], y[16];
+      tc_load16(x, mine + kIn + 16 * quarter);
+      tc_load16(y, mine + kO + 16 * quarter);
+      tc_loaded16(x);
+      tc_loaded16(y);
+      const float w = (kUpper ? d.tail : d.head)[row];
 #pragma unroll
-      for (int p = 0; p < 4; ++p) {
+      for (int p = 0; p < 2; ++p) {
         uint32_t o[4];
 #pragma unroll
         for (int j = 0; j < 4; ++j) o[j] = pack2(fmaf(w, x[8 * p + 2 * j], y[8 * p + 2 * j]), fmaf(w, x[8 * p + 2 * j + 1], y[8 * p + 2 * j + 1]));
-        *reinterpret_cast<uint4*>(st.a + at(kCT, row, 32 * half + 8 * p)) = make_uint4(o[0], o[1], o[2], o[3]);
+        *reinterpret_cast<uint4*>(st.a + at(kCT, row, 16 * quarter + 8 * p)) = make_uint4(o[0], o[1], o[2], o[3]);
       }
     }
     fence_proxy_async_smem();
@@ -368,7 +382,7 @@ __global__ void __launch_bounds__(kThreads, 1) chain_kernel(const __grid_constan
       const int len = length(i);
       bf16_t* p = out + (size_t)begin(i) * s.Hv * s.V;
 #pragma unroll
-      for (int e = 0; e < 4; ++e) {
+      for (int e = 0; e < 2; ++e) {
         const int r = (e * kWorkers + tid) >> 3, c = (tid & 7) * 8;
         const uint4 v = *reinterpret_cast<const uint4*>(st.a + at(kCT, r, c));
         if (r < len && c < vn) *reinterpret_cast<uint4*>(p + (size_t)r * s.Hv * s.V + c) = v;
@@ -387,8 +401,8 @@ __global__ void __launch_bounds__(kThreads, 1) chain_kernel(const __grid_constan
 
 template <int KP, bool kUpper>
 cudaError_t launch(const Maps& maps, const Args& a, const Plan& plan, cudaStream_t stream) {
-  const size_t smem = sizeof(Smem<KP, kUpper>);
-  static_assert(sizeof(Smem<KP, kUpper>) <= 232448, "shared memory of a block");
+  const size_t smem = sizeof(Smem<KP>);
+  static_assert(sizeof(Smem<KP>) <= 232448, "shared memory of a block");
   static std::atomic<unsigned long long> done{0};
   const cudaError_t e = allow_smem(reinterpret_cast<const void*>(chain_kernel<KP, kUpper>), smem, done);
   if (e != cudaSuccess) return e;

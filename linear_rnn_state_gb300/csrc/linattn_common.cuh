@@ -208,21 +208,15 @@ __device__ __forceinline__ float2 two_sum(float2 a, float2 b) {
   return make_float2(h, e - (h - s));
 }
 __device__ __forceinline__ float minus(float2 a, float2 b) { return (a.x - b.x) + (a.y - b.y); }
-// G[0 .. 32 kPer - 1] by a warp's lanes from g at `g` (`stride` floats from token to token; 0 from `len`
-// on). Whether a log decay is above 0 (or NaN) comes back.
+// The running sums of 32 kPer tokens by a warp, kPer a lane: of r, log decays.
 template <int kPer>
-__device__ __forceinline__ bool running_sums(float2* G, const float* g, long long stride, int len, int lane) {
-  float2 x[kPer];
-  bool up = false;
+__device__ __forceinline__ void running_sums(float2 (&G)[kPer], const float (&r)[kPer], int lane) {
 #pragma unroll
   for (int i = 0; i < kPer; ++i) {
-    float a = kPer * lane + i < len ? g[(kPer * lane + i) * stride] : 0.f;
-    up |= !(a <= 0.f);
-    a = a < kReset ? kReset : a;  // (a NaN stays)
-    x[i] = make_float2(a, 0.f);
-    if (i) x[i] = two_sum(x[i - 1], x[i]);
+    G[i] = make_float2(r[i] < kReset ? kReset : r[i], 0.f);  // (a NaN stays)
+    if (i) G[i] = two_sum(G[i - 1], G[i]);
   }
-  float2 s = x[kPer - 1];
+  float2 s = G[kPer - 1];
 #pragma unroll
   for (int o = 1; o < 32; o <<= 1) {
     const float2 y = make_float2(__shfl_up_sync(0xffffffffu, s.x, o), __shfl_up_sync(0xffffffffu, s.y, o));
@@ -231,8 +225,22 @@ __device__ __forceinline__ bool running_sums(float2* G, const float* g, long lon
   float2 e = make_float2(__shfl_up_sync(0xffffffffu, s.x, 1), __shfl_up_sync(0xffffffffu, s.y, 1));
   if (lane == 0) e = make_float2(0.f, 0.f);
 #pragma unroll
-  for (int i = 0; i < kPer; ++i) G[kPer * lane + i] = two_sum(e, x[i]);
-  return __any_sync(0xffffffffu, up);
+  for (int i = 0; i < kPer; ++i) G[i] = two_sum(e, G[i]);
+}
+// A lane's log decays, `stride` floats from token to token; 0 from token `len` on.
+template <int kPer>
+__device__ __forceinline__ void load_decays(float (&r)[kPer], const float* g, long long stride, int len, int lane) {
+#pragma unroll
+  for (int i = 0; i < kPer; ++i) r[i] = kPer * lane + i < len ? g[(kPer * lane + i) * stride] : 0.f;
+}
+template <int kPer>
+__device__ __forceinline__ void running_sums(float2* G, const float* g, long long stride, int len, int lane) {
+  float r[kPer];
+  float2 x[kPer];
+  load_decays(r, g, stride, len, lane);
+  running_sums(x, r, lane);
+#pragma unroll
+  for (int i = 0; i < kPer; ++i) G[kPer * lane + i] = x[i];
 }
 
 // --------------------------------------------------- sequences and chunks ---

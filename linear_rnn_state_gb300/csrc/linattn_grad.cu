@@ -26,7 +26,7 @@ template <int KP, int VP>
 struct Smem {
   bf16_t q[kCT * KP], k[kCT * KP], v[kCT * VP], d[kCT * VP];
   bf16_t s[3 * VP * 64];  // 64 keys of S or D; then rows on their way out
-  Decays<true, true> dec;
+  Decays dec;
   float total[4][kCT];    // of a row's A_ij (q_i.k_j), by blocks of 32 columns
   float pairs[4][kCT];    // of a block of 32 rows: the sums over j < t
   float dots[2][2][kCT];  // q.(S's part of dq), k.(D's part of dk), by halves of the columns
@@ -108,7 +108,11 @@ __global__ void __launch_bounds__(kThreads, KP == 64 && VP == 64 && !kShared ? 2
       load_tile<VP>(sm.v, &maps.v, &sm.full[0], 0, hv, c.t0, s.v_b ? c.b : 0);
       load_tile<VP>(sm.d, &maps.d, &sm.full[0], 0, hv, c.t0, c.b);
     }
-    if (warp == 7) make_decays(sm.dec, s.fixed ? a.g + hv : a.g + tok * s.Hv + hv, s.fixed ? 0 : s.Hv, c.len, s.scale, lane);
+    if (warp == 7) {
+      float r[4];
+      load_decays(r, s.fixed ? a.g + hv : a.g + tok * s.Hv + hv, s.fixed ? 0 : s.Hv, c.len, lane);
+      make_decays(sm.dec, r, s.scale, lane);
+    }
     const size_t image = ((size_t)slot * s.Hv + hv) * image_bytes(s.K, s.V);
     const char *S = static_cast<const char*>(a.images) + image, *D = static_cast<const char*>(a.dimages) + image;
     wait(&sm.full[0], turn2++);
@@ -250,7 +254,7 @@ __global__ void __launch_bounds__(kThreads, KP == 64 && VP == 64 && !kShared ? 2
         wait(&sm.done[1], turn1++);
       }
       tmem_fence_after_sync();
-      const float w = sm.dec.w[kUpper][row];
+      const float w = (kUpper ? sm.dec.tail : sm.dec.head)[row];
       float dot = 0.f;
 #pragma unroll
       for (int sl = 0; sl < kSlices; ++sl) {

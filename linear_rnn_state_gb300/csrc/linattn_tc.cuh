@@ -79,7 +79,31 @@ __device__ __forceinline__ void tc_loaded32(float (&v)[32]) {
                :
                : "memory");
 }
-// 32 columns of 16 rows (those of a 64-row accumulator) as mma.sync's accumulator tiles.
+__device__ __forceinline__ void tc_load16(float (&v)[16], uint32_t taddr) {
+  asm volatile("tcgen05.ld.sync.aligned.32x32b.x16.b32 {%0, %1, %2, %3, %4, %5, %6, %7, %8, %9, %10, %11, %12, %13, %14, %15}, [%16];"
+               : "=f"(v[0]), "=f"(v[1]), "=f"(v[2]), "=f"(v[3]), "=f"(v[4]), "=f"(v[5]), "=f"(v[6]), "=f"(v[7]), "=f"(v[8]), "=f"(v[9]),
+                 "=f"(v[10]), "=f"(v[11]), "=f"(v[12]), "=f"(v[13]), "=f"(v[14]), "=f"(v[15])
+               : "r"(taddr)
+               : "memory");
+}
+__device__ __forceinline__ void tc_loaded16(float (&v)[16]) {
+  asm volatile("tcgen05.wait::ld.sync.aligned;"
+               : "+f"(v[0]), "+f"(v[1]), "+f"(v[2]), "+f"(v[3]), "+f"(v[4]), "+f"(v[5]), "+f"(v[6]), "+f"(v[7]), "+f"(v[8]), "+f"(v[9]),
+                 "+f"(v[10]), "+f"(v[11]), "+f"(v[12]), "+f"(v[13]), "+f"(v[14]), "+f"(v[15])
+               :
+               : "memory");
+}
+// 16 or 32 columns of 16 rows (those of a 64-row accumulator) as mma.sync's accumulator tiles.
+__device__ __forceinline__ void tc_load_tiles(float (&x)[2][4], uint32_t taddr) {
+  asm volatile("tcgen05.ld.sync.aligned.16x256b.x2.b32 {%0, %1, %2, %3, %4, %5, %6, %7}, [%8];"
+               : "=f"(x[0][0]), "=f"(x[0][1]), "=f"(x[0][2]), "=f"(x[0][3]), "=f"(x[1][0]), "=f"(x[1][1]), "=f"(x[1][2]), "=f"(x[1][3])
+               : "r"(taddr)
+               : "memory");
+  asm volatile("tcgen05.wait::ld.sync.aligned;"
+               : "+f"(x[0][0]), "+f"(x[0][1]), "+f"(x[0][2]), "+f"(x[0][3]), "+f"(x[1][0]), "+f"(x[1][1]), "+f"(x[1][2]), "+f"(x[1][3])
+               :
+               : "memory");
+}
 __device__ __forceinline__ void tc_load_tiles(float (&x)[4][4], uint32_t taddr) {
   asm volatile("tcgen05.ld.sync.aligned.16x256b.x4.b32 {"
                "%0, %1, %2, %3, %4, %5, %6, %7, %8, %9, %10, %11, %12, %13, %14, %15}, [%16];"
@@ -141,56 +165,58 @@ __device__ __forceinline__ void bulk_wait_all() { asm volatile("cp.async.bulk.wa
 
 // ---------------------------------------------------------------- decays ---
 
-// A chunk's factors, by one warp. Lower (o, dq: row i, columns j <= i) and upper (dv, dk: row j, columns i >= j):
-//   w: of the state's part of a row; u: of a token in the next state
-//   c: of a column in blocks of 32 columns off the diagonal, where e^{G_i - G_j} = e^{G_i - G_r} e^{G_r - G_j} with
-//      r between the two: both at most 1 where no log decay is above 0
-//   to, from: e^{G - m} and e^{m - G} with m the middle of the range of G in a block of 32 tokens, whose products are
-//      the decays of the diagonal's blocks where the range is at most kNear
-constexpr float kNear = 60.f;  // e^+-30 leaves the products far from overflow
-template <bool kLower, bool kUpper>
+// A chunk's factors, by one warp:
+//   head: scale e^G and tail: e^{Gc - G}. Of the state's part of a row, and of a token in the next state (forward),
+//     or the other way round (backward)
+//   to, from: e^{G - m} and e^{m - G} with m the middle of the range of G in a token's block of 32. Where that range is
+//     at most kNear, products of them are the decays of the diagonal's blocks, and with e^{G_i - m} those of the others
+//     (at most 1 times e^30 where no log decay is above 0)
+constexpr float kNear = 60.f;
 struct alignas(16) Decays {
-  static constexpr int kSets = kLower + kUpper;
   float2 G[kCT];
-  float w[kSets][kCT], u[kSets][kCT], c[kSets][kCT];
-  float to[kCT], from[kCT];
-  float whole;  // e^{Gc}
-  int up;       // a log decay is above 0
-  int near;     // bit b: block b's range is small
-  static __device__ constexpr int set(bool upper) { return kSets == 2 ? upper : 0; }
+  float head[kCT], tail[kCT], to[kCT], from[kCT];
+  float middle[4];  // m
+  float whole;      // e^{Gc}
+  int up;           // a log decay is above 0 (or NaN)
+  int near;         // bit b: block b's range is at most kNear
 };
-template <bool kLower, bool kUpper>
-__device__ __forceinline__ void make_decays(Decays<kLower, kUpper>& d, const float* g, long long stride, int len, float scale, int lane) {
-  const bool up = running_sums<kCT / 32>(d.G, g, stride, len, lane);
-  __syncwarp();
-  const float2 last = d.G[kCT - 1];
-  int near = 0;
+__device__ __forceinline__ void make_decays(Decays& d, const float (&r)[4], float scale, int lane) {
+  float2 G[4];
+  running_sums(G, r, lane);
+  const float2 last = make_float2(__shfl_sync(0xffffffffu, G[3].x, 31), __shfl_sync(0xffffffffu, G[3].y, 31));
+  float hi = fmaxf(fmaxf(G[0].x, G[1].x), fmaxf(G[2].x, G[3].x)), lo = fminf(fminf(G[0].x, G[1].x), fminf(G[2].x, G[3].x));
 #pragma unroll
-  for (int i = 0; i < kCT / 32; ++i) {
-    const int j = 32 * i + lane;
-    const float2 G = d.G[j];
-    const float head = scale * expf(G.x + G.y), tail = expf(minus(last, G));
-    if (kLower) d.w[0][j] = head, d.u[0][j] = tail, d.c[0][j] = expf(minus(d.G[32 * i + 31], G));
-    if (kUpper) {
-      constexpr int k = Decays<kLower, kUpper>::kSets - 1;
-      d.w[k][j] = tail, d.u[k][j] = head, d.c[k][j] = i ? expf(minus(G, d.G[32 * i - 1])) : 1.f;
-    }
-    float hi = G.x, lo = G.x;
+  for (int o = 1; o < 8; o <<= 1) hi = fmaxf(hi, __shfl_xor_sync(0xffffffffu, hi, o)), lo = fminf(lo, __shfl_xor_sync(0xffffffffu, lo, o));
+  const float m = 0.5f * (hi + lo);
+  const bool sound = G[0].x == G[0].x && G[1].x == G[1].x && G[2].x == G[2].x && G[3].x == G[3].x;
+  const unsigned near = __ballot_sync(0xffffffffu, hi - lo <= kNear && sound);
+  const bool up = __any_sync(0xffffffffu, !(r[0] <= 0.f && r[1] <= 0.f && r[2] <= 0.f && r[3] <= 0.f));
+  float4 head, tail, to, from;
 #pragma unroll
-    for (int o = 16; o >= 1; o >>= 1) hi = fmaxf(hi, __shfl_xor_sync(0xffffffffu, hi, o)), lo = fminf(lo, __shfl_xor_sync(0xffffffffu, lo, o));
-    const float m = 0.5f * (hi + lo), x = (G.x - m) + G.y;
-    if (__all_sync(0xffffffffu, hi - lo <= kNear && G.x == G.x)) near |= 1 << i;
-    d.to[j] = expf(x), d.from[j] = expf(-x);
+  for (int i = 0; i < 4; ++i) {
+    const float x = (G[i].x - m) + G[i].y;
+    (&head.x)[i] = scale * expf(G[i].x + G[i].y), (&tail.x)[i] = expf(minus(last, G[i]));
+    (&to.x)[i] = expf(x), (&from.x)[i] = expf(-x);
   }
-  if (lane == 0) d.whole = expf(last.x + last.y), d.up = up, d.near = near;
+  reinterpret_cast<float4*>(d.G)[2 * lane] = make_float4(G[0].x, G[0].y, G[1].x, G[1].y);
+  reinterpret_cast<float4*>(d.G)[2 * lane + 1] = make_float4(G[2].x, G[2].y, G[3].x, G[3].y);
+  reinterpret_cast<float4*>(d.head)[lane] = head, reinterpret_cast<float4*>(d.tail)[lane] = tail;
+  reinterpret_cast<float4*>(d.to)[lane] = to, reinterpret_cast<float4*>(d.from)[lane] = from;
+  if ((lane & 7) == 0) d.middle[lane >> 3] = m;
+  if (lane == 0) {
+    d.whole = expf(last.x + last.y), d.up = up;
+    d.near = 0;
+#pragma unroll
+    for (int b = 0; b < 4; ++b) d.near |= ((near >> 8 * b & 255u) == 255u) << b;
+  }
 }
 
 // 32 columns (block `blk`) of a row's products times scale e^{G_i - G_j}, 0 outside the mask.
-template <bool kUpper, typename D>
-__device__ __forceinline__ void decayed(float (&x)[32], const D& d, int row, int blk, float scale) {
+template <bool kUpper>
+__device__ __forceinline__ void decayed(float (&x)[32], const Decays& d, int row, int blk, float scale) {
   const bool diagonal = blk == row >> 5;
   const int at = row - 32 * blk;  // the diagonal's column
-  if (diagonal ? !(d.near >> blk & 1) : d.up) {
+  if (!(d.near >> blk & 1) || (!diagonal && d.up)) {
     const float2 Gr = d.G[row];
     const float4* G = reinterpret_cast<const float4*>(d.G + 32 * blk);  // two tokens
 #pragma unroll
@@ -204,15 +230,10 @@ __device__ __forceinline__ void decayed(float (&x)[32], const D& d, int row, int
     }
     return;
   }
-  float r;
-  const float4* c;
-  if (diagonal) {
-    r = scale * (kUpper ? d.from : d.to)[row];
-    c = reinterpret_cast<const float4*>((kUpper ? d.to : d.from) + 32 * blk);
-  } else {
-    r = scale * __expf(kUpper ? minus(d.G[32 * blk - 1], d.G[row]) : minus(d.G[row], d.G[32 * blk + 31]));
-    c = reinterpret_cast<const float4*>(d.c[D::set(kUpper)] + 32 * blk);
-  }
+  const float2 Gr = d.G[row];
+  const float y = (Gr.x - d.middle[blk]) + Gr.y;
+  const float r = scale * (diagonal ? (kUpper ? d.from : d.to)[row] : __expf(kUpper ? -y : y));
+  const float4* c = reinterpret_cast<const float4*>((kUpper ? d.to : d.from) + 32 * blk);
   const float2 rr = make_float2(r, r);
 #pragma unroll
   for (int j = 0; j < 32; j += 4) {
