@@ -33,7 +33,7 @@ SOURCES = ["wkv7_api.cu", "wkv7_fwd2.cu", "wkv7_fwd3.cu", "wkv7_bwd2.cu", "wkv7_
            "wkv7_bwd4_f32.cu", "rwkv8_api.cu",
            "rwkv8_fwd.cu", "rwkv8_bwd.cu", "rwkv8_bwd_split.cu", "rwkv8_state.cu", "rwkv8_chunk.cu", "wkv7_epilogue.cu",
            "gdr_api.cu", "gdr_prep.cu", "gdr_fwd.cu", "gdr_bwd.cu", "gdr_grad.cu", "gdr_step.cu", "blocknorm_api.cu",
-           "blocknorm.cu", "linattn_api.cu", "linattn_states.cu", "linattn_rows.cu", "linattn_chain.cu", "linattn_grad.cu",
+           "blocknorm.cu", "linattn_api.cu", "linattn_states.cu", "linattn_rows.cu", "linattn_chain.cu", "linattn_chain32.cu", "linattn_grad.cu",
            "linattn_step.cu",
            "qkrope_api.cu", "qkrope.cu"]
 HEADERS = ["wkv7_common.cuh", "wkv7_launch.h", "wkv7_mma.cuh", "wkv7_scaled.cuh", "wkv7_tmem.cuh", "wkv7_decay.cuh",

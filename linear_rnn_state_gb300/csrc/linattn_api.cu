@@ -54,7 +54,7 @@ int set_shape(Shape& s, int B, int T, int Hk, int Hv, int K, int V, int nseq, in
   s.B = B, s.T = T, s.Hk = Hk, s.Hv = Hv, s.K = K, s.V = V;
   s.nseq = nseq >= 0 ? nseq : B;
   s.packed = nseq >= 0;
-  s.C = bf16 ? kCBf16 : kCF32;
+  s.C = on_tcgen05(K, V, bf16) ? kCBf16 : kCF32;
   const unsigned long long slots = slot_count(B, T, s.nseq, s.packed, s.C), heads = Hv ? Hv : 1;
   if (slots * heads * 2 >= kMaxBlocks || (unsigned long long)s.nseq * heads * 16 >= kMaxBlocks)
     return fail(WKV7_ERR_INVALID, "too many chunks");
@@ -76,7 +76,7 @@ struct Place {
     return p;
   }
 };
-// bfloat16: whether the chains of all sequences, heads and slices of 64 values would leave most of the GPU idle, so
+// On tcgen05: whether the chains of all sequences, heads and slices of 64 values would leave most of the GPU idle, so
 // that they go in segments, from states made before.
 bool resumes(const Shape& s) {
   return (long long)s.nseq * s.Hv * ((s.V + 63) / 64) < 76 && (s.T + s.C - 1) / s.C > 4;
@@ -86,8 +86,9 @@ size_t place_saved(Args& a, bool bf16, bool for_backward, char* p) {
   const Shape& s = a.s;
   const size_t n = (size_t)s.slots * s.Hv;
   Place x{p, p};
-  if (bf16 && for_backward) a.images = x.bytes(n * image_bytes(s.K, s.V));
-  if (!bf16 || resumes(s)) {
+  const bool tc = on_tcgen05(s.K, s.V, bf16);
+  if (tc && for_backward) a.images = x.bytes(n * image_bytes(s.K, s.V));
+  if (!tc || resumes(s)) {
     x.take(a.states, n * s.V * s.K);
     x.take(a.decay, n);
   }
@@ -97,8 +98,9 @@ size_t place_workspace(Args& a, bool bf16, char* p) {
   const Shape& s = a.s;
   const size_t n = (size_t)s.slots * s.Hv;
   Place x{p, p};
-  if (bf16) a.dimages = x.bytes(n * image_bytes(s.K, s.V));
-  if (!bf16 || resumes(s)) {
+  const bool tc = on_tcgen05(s.K, s.V, bf16);
+  if (tc) a.dimages = x.bytes(n * image_bytes(s.K, s.V));
+  if (!tc || resumes(s)) {
     x.take(a.dstates, n * s.V * s.K);
     x.take(a.decay, n);
   }
@@ -124,11 +126,13 @@ int copy_state(float* dst, const float* src, size_t bytes, cudaStream_t stream) 
 int launched(cudaError_t e, const char* what) {
   return e == cudaSuccess ? WKV7_OK : fail(WKV7_ERR_CUDA, "%s launch: %s", what, cudaGetErrorString(e));
 }
-// bfloat16: o, or dv.
-int chains(const Maps& maps, const Args& a, bool backward, bool keep, cudaStream_t stream) {
+// On tcgen05: o, or dv.
+int chains(const Maps& maps, const Args& a, bool bf16, bool backward, bool keep, cudaStream_t stream) {
   const bool resume = resumes(a.s);
-  const int rc = resume ? launched(launch_states(a, true, backward, stream), "states") : WKV7_OK;
-  return rc ? rc : launched(launch_chain(maps, a, backward, resume ? 2 : 0, resume, keep, stream), "chain");
+  const int chunks = resume ? 2 : 0;
+  const int rc = resume ? launched(launch_states(a, bf16, backward, stream), "states") : WKV7_OK;
+  if (rc) return rc;
+  return launched(bf16 ? launch_chain(maps, a, backward, chunks, resume, keep, stream) : launch_chain32(a, backward, chunks, resume, keep, stream), "chain");
 }
 uint32_t* words(void* p) { return static_cast<uint32_t*>(p); }
 
@@ -204,10 +208,10 @@ int linattn_forward(const void* q, const void* k, const void* v, const float* g,
   a.s.starts = seq_starts, a.s.scale = scale, a.s.fixed = g_fixed;
   a.s.q_b = st[0], a.s.q_t = st[1], a.s.k_b = st[2], a.s.k_t = st[3], a.s.v_b = st[4], a.s.v_t = st[5];
   a.q = q, a.k = k, a.v = v, a.g = g, a.s_init = s_init, a.o = o, a.s_final = s_final;
-  if (bf16) {
+  if (on_tcgen05(K, V, bf16)) {
     Maps maps;
-    if (!make_maps(maps, a)) return fail(WKV7_ERR_CUDA, "no tensor maps of q, k and v");
-    if ((rc = wkv7::api_status_word(&a.status)) || (rc = chains(maps, a, false, for_backward, stream))) return rc;
+    if (bf16 && !make_maps(maps, a)) return fail(WKV7_ERR_CUDA, "no tensor maps of q, k and v");
+    if ((rc = wkv7::api_status_word(&a.status)) || (rc = chains(maps, a, bf16, false, for_backward, stream))) return rc;
   } else {
     if ((rc = launched(launch_states(a, false, false, stream), "states"))) return rc;
     if ((rc = launched(launch_rows_o(a, stream), "forward"))) return rc;
@@ -258,11 +262,11 @@ int linattn_backward(const void* q, const void* k, const void* v, const float* g
   else
     a.dg = dg;
   if (!dg) a.dg = nullptr;
-  if (bf16) {
+  if (on_tcgen05(K, V, bf16)) {
     Maps maps;
-    if (!make_maps(maps, a)) return fail(WKV7_ERR_CUDA, "no tensor maps of q, k, v and d_o");
-    if ((rc = wkv7::api_status_word(&a.status)) || (rc = chains(maps, a, true, true, stream))) return rc;
-    if ((rc = launched(launch_grad(maps, a, stream), "gradients"))) return rc;
+    if (bf16 && !make_maps(maps, a)) return fail(WKV7_ERR_CUDA, "no tensor maps of q, k, v and d_o");
+    if ((rc = wkv7::api_status_word(&a.status)) || (rc = chains(maps, a, bf16, true, true, stream))) return rc;
+    if ((rc = launched(launch_grad(maps, a, bf16, stream), "gradients"))) return rc;
   } else {
     if ((rc = launched(launch_states(a, false, true, stream), "states"))) return rc;
     if ((rc = launched(launch_rows_grad(a, stream), "gradients"))) return rc;

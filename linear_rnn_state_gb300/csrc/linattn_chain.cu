@@ -187,7 +187,7 @@ __global__ void __launch_bounds__(kThreads, 1) chain_kernel(const __grid_constan
       for (int part = 1; part >= 0; --part)
 #pragma unroll
         for (int ks = 0; ks < kCT / 16; ++ks)
-          tc_mma_t(tm + kO, tm + kP + (kEarly ? i % 2 * 128 : 0) + pair_at(ks, part), dx + across(ks), product_of(128, 64, false, true), part == 0 || ks > 0);
+          tc_mma_t(tm + kO, tm + kP + (kEarly ? i % 2 * 128 : 0) + part_at<2>(ks, part), dx + across(ks), product_of(128, 64, false, true), part == 0 || ks > 0);
     };
     auto sum = [&](int i, int h) {  // of half h of the tokens
       const uint64_t dx = desc(sm.xt), db = desc(sm.stage[i % kSt].b, kRowPanel) + across(h * (kXt / 16));
@@ -301,9 +301,9 @@ __global__ void __launch_bounds__(kThreads, 1) chain_kernel(const __grid_constan
       tc_load32(x, at_p + 32 * blk);
       tc_loaded32(x);
       decayed<kUpper>(x, sm.d[i % 3], row, blk, s.scale);
-      store_pairs(at_p + 32 * blk, x);
+      store_parts<2>(at_p + 32 * blk, x);
     } else {
-      store_zeros(at_p + 32 * blk);
+      store_zeros<2>(at_p + 32 * blk);
     }
     wkv7::tmem_wait_st();
     tmem_fence_before_sync();

@@ -1,0 +1,331 @@
+// Linear attention with a decay, fp32 with heads of up to 64: o, and backward dv, from chunk to chunk on tcgen05.
+//
+// As linattn_chain.cu, with every operand in three bfloat16 parts (24 bits) and six products of parts for each
+// product. The tiles of a chunk (a, b, x and u . x, 192 KB) leave room for one stage: threads split the values of
+// the next chunk when the products of this one are done; a warp has brought them to L2 by then.
+//
+// Tensor memory: the scores (128 columns, later the rows' P x), P (192), a S^T (64), the state's sum (64).
+#include "linattn_tc.cuh"
+
+namespace linattn {
+namespace {
+
+constexpr int kWorkers = 512, kThreads = kWorkers + 64;
+constexpr int kHelpWarp = 16;  // and 17 issues
+
+struct Smem {
+  bf16_t a[3 * kCT * 64], b[3 * kCT * 64], x[3 * kCT * 64], xt[3 * kCT * 64];
+  bf16_t s[3 * 64 * 64];
+  Decays d[2];
+  uint64_t scored, summed, out;
+  uint32_t tmem;
+};
+static_assert(sizeof(Smem) <= 232448, "shared memory of a block");
+
+struct Plan {
+  int chunks;  // of a segment
+  int resume, keep;
+};
+
+template <bool kUpper>
+__global__ void __launch_bounds__(kThreads, 1) chain32_kernel(const Args a, const Plan plan) {
+  extern __shared__ __align__(1024) unsigned char raw[];
+  Smem& sm = *reinterpret_cast<Smem*>(raw);
+  enum { kScore = 0, kP = 128, kIn = 320, kU = 384, kO = 0, kCols = 512 };
+  enum { kBarP = 1, kBarOut, kBarFree, kBarRows };
+  constexpr int kPair = kWorkers + 32, kPart = kCT * 64;
+  const Shape& s = a.s;
+  const int tid = threadIdx.x, lane = tid & 31, warp = __shfl_sync(0xffffffffu, tid >> 5, 0), sub = warp & 3, quarter = warp >> 2;
+  const int slices = (s.V + 63) >> 6, slice = blockIdx.x % slices, hv = blockIdx.x / slices % s.Hv, slot = blockIdx.x / slices / s.Hv;
+  const int hk = hv / (s.Hv / s.Hk), v0 = slice * 64, vn = min(64, s.V - v0);
+  ChunkAt seg;
+  if (plan.resume) {
+    if (!chunk_at(s, slot, kCT * plan.chunks, seg)) return;
+  } else {  // a whole sequence, which may be empty: its state passes through
+    const SeqRange r = seq_range(s, slot, kCT);
+    seg.b = r.b, seg.t0 = seg.first = r.t0, seg.len = r.t1 - r.t0, seg.seq = slot;
+  }
+  if (warp == 0) wkv7::tmem_alloc(&sm.tmem, kCols);
+  if (tid == 0) {
+    for (uint64_t* b : {&sm.scored, &sm.summed, &sm.out}) mbar_init(b, 1);
+    wkv7::fence_mbar_init();
+  }
+  const int n = (seg.len + kCT - 1) / kCT;
+  const size_t tok = (size_t)seg.b * s.T + seg.t0;
+  auto begin = [&](int i) { return (kUpper ? n - 1 - i : i) * kCT; };  // first token of the i-th chunk, from the segment's
+  auto length = [&](int i) { return min(kCT, seg.len - begin(i)); };
+  const long long st_a = kUpper ? s.k_t : s.q_t, st_b = kUpper ? s.q_t : s.k_t, st_x = kUpper ? (long long)s.Hv * s.V : s.v_t;
+  const float* q = static_cast<const float*>(a.q) + seg.b * s.q_b + seg.t0 * s.q_t + (size_t)hk * s.K;
+  const float* k = static_cast<const float*>(a.k) + seg.b * s.k_b + seg.t0 * s.k_t + (size_t)hk * s.K;
+  const float* pa = kUpper ? k : q;
+  const float* pb = kUpper ? q : k;
+  const float* px = kUpper ? static_cast<const float*>(a.d_o) + (tok * s.Hv + hv) * s.V + v0
+                           : static_cast<const float*>(a.v) + seg.b * s.v_b + seg.t0 * s.v_t + (size_t)hv * s.V + v0;
+
+  if (warp == kHelpWarp) {
+    const float* g = s.fixed ? a.g + hv : a.g + tok * s.Hv + hv;
+    float r[4];
+    auto ask = [&](int i) {
+      if (i < n) load_decays(r, s.fixed ? g : g + (size_t)begin(i) * s.Hv, s.fixed ? 0 : s.Hv, length(i), lane);
+    };
+    auto make = [&](int i) {  // and the next chunk's are asked for
+      if (i < n) {
+        float x[4] = {r[0], r[1], r[2], r[3]};
+        ask(i + 1);
+        make_decays(sm.d[i & 1], x, s.scale, lane);
+      }
+    };
+    auto prefetch = [&](const float* p, long long stride, int cols, int len) {
+      for (int r = lane; r < len; r += 32)
+        for (int c = 0; c < cols; c += 32) asm volatile("prefetch.global.L2 [%0];" ::"l"(p + r * stride + c));
+    };
+    char* to = static_cast<char*>(kUpper ? a.dimages : a.images) +
+               ((size_t)(n ? chunk_slot(s, seg, seg.t0 + begin(0)) : 0) * s.Hv + hv) * image_bytes(s.K, s.V) + slice * kImagePiece;
+    const long long next = (kUpper ? -1 : 1) * (long long)(s.Hv * image_bytes(s.K, s.V));
+    auto leave = [&](int i) {  // the state before chunk i
+      if (plan.keep && i < n && lane == 0) {
+#pragma unroll
+        for (int part = 0; part < 3; ++part) bulk_store(to + (size_t)part * slices * kImagePiece, sm.s + part * 64 * 64, kImagePiece);
+        bulk_commit();
+        to += next;
+      }
+    };
+    ask(0), make(0);
+    __syncthreads();
+    __syncthreads();
+    leave(0);
+    for (int i = 0; i < n; ++i) {
+      if (lane == 0) bulk_wait_read();
+      __syncwarp();
+      announce(kBarFree, kPair);
+      make(i + 1);
+      if (i + 1 < n) {
+        const int t = begin(i + 1), len = length(i + 1);
+        prefetch(pa + t * st_a, st_a, s.K, len), prefetch(pb + t * st_b, st_b, s.K, len), prefetch(px + t * st_x, st_x, vn, len);
+      }
+      meet(kBarOut, kPair);
+      leave(i + 1);
+      __syncthreads();
+    }
+    if (lane == 0) bulk_wait_all();
+    __syncthreads();
+    return;
+  }
+  if (warp > kHelpWarp) {
+    __syncthreads();
+    __syncthreads();
+    tmem_fence_after_sync();
+    const uint32_t tm = sm.tmem;
+    for (int i = 0; i < n; ++i) {
+      if (elected()) {
+        const uint64_t da = desc(sm.a), db = desc(sm.b), ds = desc(sm.s), du = desc(sm.xt);
+        terms<3, 3>([&](int p, int r, bool first) {
+#pragma unroll
+          for (int ks = 0; ks < 4; ++ks)
+            tc_mma(tm + kScore, da + along<kCT>(ks) + p * (kRowPanel >> 4), db + along<kCT>(ks) + r * (kRowPanel >> 4),
+                   product_of(128, 128, false, false), !first || ks > 0);
+        });
+        tc_commit(&sm.scored);
+        terms<3, 3>([&](int p, int r, bool first) {
+#pragma unroll
+          for (int ks = 0; ks < 4; ++ks)
+            tc_mma(tm + kIn, da + along<kCT>(ks) + p * (kRowPanel >> 4), ds + along<64>(ks) + r * (64 * 128 >> 4),
+                   product_of(128, 64, false, false), !first || ks > 0);
+        });
+        terms<3, 3>([&](int p, int r, bool first) {
+#pragma unroll
+          for (int ks = 0; ks < kCT / 16; ++ks)
+            tc_mma(tm + kU, du + across(ks) + p * (kRowPanel >> 4), db + across(ks) + r * (kRowPanel >> 4), product_of(64, 64, true, true),
+                   !first || ks > 0);
+        });
+        tc_commit(&sm.summed);
+      }
+      __syncwarp();
+      meet(kBarP, kPair);
+      tmem_fence_after_sync();
+      if (elected()) {
+        const uint64_t dx = desc(sm.x);
+        terms<3, 3>([&](int p, int r, bool first) {
+#pragma unroll
+          for (int ks = 0; ks < kCT / 16; ++ks)
+            tc_mma_t(tm + kO, tm + kP + part_at<3>(ks, p), dx + across(ks) + r * (kRowPanel >> 4), product_of(128, 64, false, true), !first || ks > 0);
+        });
+        tc_commit(&sm.out);
+      }
+      __syncwarp();
+      __syncthreads();
+      tmem_fence_after_sync();
+    }
+    __syncthreads();
+    return;
+  }
+
+  // ------------------------------------------------------------------ rows ---
+  const int row = sub * 32 + lane;
+  float* out = static_cast<float*>(kUpper ? a.dv : a.o) + (tok * s.Hv + hv) * s.V + v0;
+  // A chunk's values: two pieces of eight of each of a, b and x a thread, the first two asked for early.
+  float va[2][8], vb[2][8];
+  const int piece = (tid & 7) * 8;
+  auto ask = [&](int i) {
+    const int t0 = begin(i), len = length(i);
+#pragma unroll
+    for (int e = 0; e < 2; ++e) {
+      const int r = (e * kWorkers + tid) >> 3;
+#pragma unroll
+      for (int j = 0; j < 8; ++j) va[e][j] = vb[e][j] = 0.f;
+      if (r < len && piece < s.K) load8(va[e], pa + (t0 + r) * st_a + piece), load8(vb[e], pb + (t0 + r) * st_b + piece);
+    }
+  };
+  auto fill = [&](int i) {
+    const float* u = kUpper ? sm.d[i & 1].head : sm.d[i & 1].tail;
+    const int t0 = begin(i), len = length(i);
+    float vx[2][8];
+#pragma unroll
+    for (int e = 0; e < 2; ++e) {
+      const int r = (e * kWorkers + tid) >> 3;
+#pragma unroll
+      for (int j = 0; j < 8; ++j) vx[e][j] = 0.f;
+      if (r < len && piece < vn) load8(vx[e], px + (t0 + r) * st_x + piece);
+    }
+#pragma unroll
+    for (int e = 0; e < 2; ++e) {
+      const int r = (e * kWorkers + tid) >> 3, o = at(kCT, r, piece);
+      put8<3>(sm.a + o, kPart, va[e]);
+      put8<3>(sm.b + o, kPart, vb[e]);
+      put8<3>(sm.x + o, kPart, vx[e]);
+      const float f = u[r];
+#pragma unroll
+      for (int j = 0; j < 8; ++j) vx[e][j] *= f;
+      put8<3>(sm.xt + o, kPart, vx[e]);
+    }
+    fence_proxy_async_smem();
+  };
+  if (n) ask(0);
+  // The state: rows 16 sub .., keys 16 quarter .. in accumulator tiles.
+  float S[2][4];
+  const int s_row = v0 + 16 * sub + (lane >> 2), s_col = quarter * 16 + 2 * (lane & 3);
+  float* const states = (kUpper ? a.dstates : a.states) + ((size_t)s_row * s.K + s_col);
+  const size_t state = (size_t)s.V * s.K;
+  auto each = [&](float* m, auto f) {  // pairs of the state's numbers that exist; m is where its first is
+#pragma unroll
+    for (int t = 0; t < 2; ++t)
+#pragma unroll
+      for (int h = 0; h < 2; ++h)
+        if (s_row + 8 * h < s.V && s_col + 8 * t < s.K) f(reinterpret_cast<float2*>(m + (h ? 8 * s.K : 0) + 8 * t), S[t][2 * h], S[t][2 * h + 1]);
+  };
+  auto load = [](float2* p, float& x, float& y) {
+    const float2 v = *p;
+    x = v.x, y = v.y;
+  };
+  auto store = [](float2* p, float& x, float& y) { *p = make_float2(x, y); };
+  auto planes = [&] {
+    Frag<3> f;
+    to_a(f, S[0], S[1]);
+    const int o = at(64, 16 * sub + (lane & 15), quarter * 16 + (lane >> 4) * 8);
+#pragma unroll
+    for (int p = 0; p < 3; ++p) stsm4(sm.s + p * 64 * 64 + o, f.p[p]);
+  };
+#pragma unroll
+  for (int t = 0; t < 2; ++t)
+#pragma unroll
+    for (int e = 0; e < 4; ++e) S[t][e] = 0.f;
+  const size_t ends = ((size_t)seg.seq * s.Hv + hv) * state + (size_t)s_row * s.K + s_col;
+  float* init = const_cast<float*>(kUpper ? a.dS_final : a.s_init);
+  if (plan.resume)
+    each(states + (chunk_slot(s, seg, seg.t0 + begin(0)) * s.Hv + hv) * state, load);
+  else if (init)
+    each(init + ends, load);
+  planes();
+  __syncthreads();  // the first decays
+  if (n) fill(0);
+  fence_proxy_async_smem();
+  tmem_fence_before_sync();
+  __syncthreads();
+  tmem_fence_after_sync();
+  const uint32_t tm = sm.tmem, mine = tm + ((uint32_t)(sub * 32) << 16);
+  Patience wait{a.status};
+  for (int i = 0; i < n; ++i) {
+    const Decays& d = sm.d[i & 1];
+    wait(&sm.scored, i);
+    tmem_fence_after_sync();
+    if (kUpper ? quarter >= sub : quarter <= sub) {
+      float x[32];
+      tc_read(x, mine + kScore + 32 * quarter);
+      decayed<kUpper>(x, d, row, quarter, s.scale);
+      store_parts<3>(mine + kP + 48 * quarter, x);
+    } else {
+      store_zeros<3>(mine + kP + 48 * quarter);
+    }
+    wkv7::tmem_wait_st();
+    tmem_fence_before_sync();
+    announce(kBarP, kPair);
+    wait(&sm.summed, i);
+    tmem_fence_after_sync();
+    {
+      float x[2][4];
+      tc_load_tiles(x, mine + kU + 16 * quarter);
+#pragma unroll
+      for (int j = 0; j < 2; ++j)
+#pragma unroll
+        for (int e = 0; e < 4; ++e) S[j][e] = fmaf(d.whole, S[j][e], x[j][e]);
+    }
+    meet(kBarFree, kPair);
+    planes();
+    wait(&sm.out, i);
+    tmem_fence_after_sync();
+    // rows through shared memory (a's place): 16 pieces of four values, permuted by the row
+    float4* stage = reinterpret_cast<float4*>(sm.a);
+    {
+      float x[16], y[16];
+      tc_read(x, mine + kIn + 16 * quarter);
+      tc_read(y, mine + kO + 16 * quarter);
+      const float w = (kUpper ? d.tail : d.head)[row];
+#pragma unroll
+      for (int p = 0; p < 4; ++p)
+        stage[row * 16 + ((4 * quarter + p) ^ (row & 15))] =
+            make_float4(fmaf(w, x[4 * p], y[4 * p]), fmaf(w, x[4 * p + 1], y[4 * p + 1]), fmaf(w, x[4 * p + 2], y[4 * p + 2]), fmaf(w, x[4 * p + 3], y[4 * p + 3]));
+    }
+    fence_proxy_async_smem();
+    if (i + 1 < n) ask(i + 1);
+    meet(kBarOut, kPair);
+    {
+      const int len = length(i);
+      float* p = out + (size_t)begin(i) * s.Hv * s.V;
+#pragma unroll
+      for (int e = 0; e < 4; ++e) {
+        const int r = (e * kWorkers + tid) >> 4, c = tid & 15;
+        const float4 v = stage[r * 16 + (c ^ (r & 15))];
+        if (r < len && 4 * c < vn) *reinterpret_cast<float4*>(p + (size_t)r * s.Hv * s.V + 4 * c) = v;
+      }
+    }
+    meet(kBarRows, kWorkers);
+    if (i + 1 < n) fill(i + 1);
+    tmem_fence_before_sync();
+    __syncthreads();
+    tmem_fence_after_sync();
+  }
+  float* last = kUpper ? a.dS_init : a.s_final;
+  if (!plan.resume && last) each(last + ends, store);
+  __syncthreads();
+  if (warp == 0) wkv7::tmem_dealloc(tm, kCols);
+}
+
+template <bool kUpper>
+cudaError_t launch(const Args& a, const Plan& plan, cudaStream_t stream) {
+  static std::atomic<unsigned long long> done{0};
+  const cudaError_t e = allow_smem(reinterpret_cast<const void*>(chain32_kernel<kUpper>), sizeof(Smem), done);
+  if (e != cudaSuccess) return e;
+  const Shape& s = a.s;
+  const long long segs = plan.resume ? slot_count(s.B, s.T, s.nseq, s.packed, kCT * plan.chunks) : s.nseq;
+  chain32_kernel<kUpper><<<(unsigned)(segs * s.Hv * ((s.V + 63) / 64)), kThreads, sizeof(Smem), stream>>>(a, plan);
+  return cudaGetLastError();
+}
+
+}  // namespace
+
+cudaError_t launch_chain32(const Args& a, bool backward, int chunks, bool resume, bool keep, cudaStream_t stream) {
+  const Plan plan{chunks, resume, keep};
+  return backward ? launch<true>(a, plan, stream) : launch<false>(a, plan, stream);
+}
+
+}  // namespace linattn

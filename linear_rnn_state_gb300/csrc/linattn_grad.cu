@@ -1,4 +1,5 @@
-// Linear attention with a decay, bfloat16: dq, dk and dg of every chunk, all chunks at once, on tcgen05.
+// Linear attention with a decay: dq, dk and dg of every chunk, all chunks at once, on tcgen05 (bfloat16, and fp32
+// with heads of up to 64).
 //
 // With G the running sum of the chunk's log decays, Gc the whole sum, S the state before the chunk and D the
 // gradient of the state after it:
@@ -11,8 +12,8 @@
 // all of them sums: no differences of large ones.
 //
 // A block takes a chunk and a key head, one of its value heads after the other. A thread has a row of the
-// products, half of its columns; A enters as a pair of bfloat16 (16 bits, for bfloat16 results), S and D in
-// three parts, 64 keys of them at a time (24 bits: dg is an fp32 result).
+// products, a half or (kQ = 4) a quarter of its columns. bfloat16: A enters as a pair (16 bits, for bfloat16
+// results), S and D in three parts, 64 keys of them at a time (24 bits: dg is an fp32 result). fp32: all in three.
 #include <type_traits>
 
 #include "linattn_tc.cuh"
@@ -20,17 +21,16 @@
 namespace linattn {
 namespace {
 
-constexpr int kThreads = 256;
-
-template <int KP, int VP>
+template <typename T, int KP, int VP, int kQ>
 struct Smem {
-  bf16_t q[kCT * KP], k[kCT * KP], v[kCT * VP], d[kCT * VP];
-  bf16_t s[3 * VP * 64];  // 64 keys of S or D; then rows on their way out
+  static constexpr int kN = In<T>::kParts;
+  bf16_t q[kN * kCT * KP], k[kN * kCT * KP], v[kN * kCT * VP], d[kN * kCT * VP];
+  bf16_t s[3 * VP * 64];  // 64 keys of S or D; then (bfloat16) rows on their way out
   Decays dec;
-  float total[4][kCT];    // of a row's A_ij (q_i.k_j), by blocks of 32 columns
-  float pairs[4][kCT];    // of a block of 32 rows: the sums over j < t
-  float dots[2][2][kCT];  // q.(S's part of dq), k.(D's part of dk), by halves of the columns
-  float whole[8];
+  float total[3][kCT];     // of a row's A_ij (q_i.k_j), by blocks of 32 columns
+  float pairs[4][kCT];     // of a block of 32 rows: the sums over j < t
+  float dots[2][kQ][kCT];  // q.(S's part of dq), k.(D's part of dk), by parts of the columns
+  float whole[4 * kQ];
   uint64_t done[2], full[2];  // products; tiles of q and k or of v and do, the state
   uint32_t tmem;
 };
@@ -51,14 +51,18 @@ __device__ __forceinline__ float warp_sum(float x) {
   return x;
 }
 
-template <int KP, int VP, bool kShared>
-__global__ void __launch_bounds__(kThreads, KP == 64 && VP == 64 && !kShared ? 2 : 1) grad_kernel(const __grid_constant__ Maps maps, const Args a) {
+template <typename T, int KP, int VP, bool kShared, int kQ>
+__global__ void __launch_bounds__(128 * kQ, kQ == 2 ? 2 : 1) grad_kernel(const __grid_constant__ Maps maps, const Args a) {
   extern __shared__ __align__(1024) unsigned char raw[];
-  Smem<KP, VP>& sm = *reinterpret_cast<Smem<KP, VP>*>(raw);
-  constexpr int kSlices = KP / 64, kCols = KP == 64 ? 256 : 512;
-  enum { kE = 0, kQk = 128, kOut = 128, kIn = 128 + KP };
+  Smem<T, KP, VP, kQ>& sm = *reinterpret_cast<Smem<T, KP, VP, kQ>*>(raw);
+  constexpr bool kF32 = sizeof(T) == 4;
+  constexpr int kThreads = 128 * kQ, kSlices = KP / 64, kN = In<T>::kParts, kA = kF32 ? 3 : 2, kW = 64 / kQ;
+  constexpr int kCols = !kF32 && KP == 64 ? 256 : 512;
+  // E; A (bfloat16: in its place); q k^T; then, where what was there has been read, the chunk's and the state's products
+  enum { kE = 0, kAt = kF32 ? 128 : 0, kQk = kF32 ? 320 : 128, kOut = kF32 ? 0 : 128, kIn = kF32 ? 64 : 128 + KP };
+  static_assert(!kF32 || (KP == 64 && VP == 64 && kQ == 4), "fp32 tiles of 64 columns fill shared memory");
   const Shape& s = a.s;
-  const int tid = threadIdx.x, lane = tid & 31, warp = __shfl_sync(0xffffffffu, tid >> 5, 0), sub = warp & 3, half = warp >> 2;
+  const int tid = threadIdx.x, lane = tid & 31, warp = __shfl_sync(0xffffffffu, tid >> 5, 0), sub = warp & 3, part_of = warp >> 2;
   const int hk = blockIdx.x % s.Hk, slot = blockIdx.x / s.Hk, group = kShared ? s.Hv / s.Hk : 1, row = 32 * sub + lane;
   ChunkAt c;
   if (!chunk_at(s, slot, kCT, c)) return;
@@ -69,36 +73,40 @@ __global__ void __launch_bounds__(kThreads, KP == 64 && VP == 64 && !kShared ? 2
     mbar_init(&sm.done[0], 1), mbar_init(&sm.done[1], 1), mbar_init(&sm.full[0], 1), mbar_init(&sm.full[1], 1);
     wkv7::fence_mbar_init();
   }
-  float acc[2][kShared ? 32 * kSlices : 1];
+  float acc[2][kShared ? kW * kSlices : 1];
 #pragma unroll
   for (int i = 0; i < 2; ++i)
 #pragma unroll
-    for (int j = 0; j < (kShared ? 32 * kSlices : 1); ++j) acc[i][j] = 0.f;
+    for (int j = 0; j < (kShared ? kW * kSlices : 1); ++j) acc[i][j] = 0.f;
   Patience wait{a.status};
   uint32_t turn0 = 0, turn1 = 0, turn2 = 0, turn3 = 0, tm = 0;
   __syncthreads();
-  // 64 columns of rows from shared memory to dq or dk
-  auto leave = [&](bf16_t* to, int sl) {
-    __syncthreads();
-    bf16_t* p = to + (tok * s.Hk + hk) * s.K + 64 * sl;
+  // The thread's kW columns of 64 to dq or dk. bfloat16: through shared memory (called by all threads).
+  auto leave = [&](T* to, int sl, const float* x) {
+    T* p = to + (tok * s.Hk + hk) * s.K + 64 * sl;
+    if constexpr (kF32) {
 #pragma unroll
-    for (int e = 0; e < 4; ++e) {
-      const int r = (e * kThreads + tid) >> 3, col = (tid & 7) * 8;
-      if (r < c.len && 64 * sl + col < s.K)
-        *reinterpret_cast<uint4*>(p + (size_t)r * s.Hk * s.K + col) = *reinterpret_cast<const uint4*>(sm.s + at(kCT, r, col));
+      for (int j = 0; j < kW; j += 4)
+        if (row < c.len && 64 * sl + kW * part_of + j < s.K)
+          *reinterpret_cast<float4*>(p + (size_t)row * s.Hk * s.K + kW * part_of + j) = make_float4(x[j], x[j + 1], x[j + 2], x[j + 3]);
+    } else {
+#pragma unroll
+      for (int j = 0; j < kW; j += 8)
+        *reinterpret_cast<uint4*>(sm.s + at(kCT, row, kW * part_of + j)) =
+            make_uint4(pack2(x[j], x[j + 1]), pack2(x[j + 2], x[j + 3]), pack2(x[j + 4], x[j + 5]), pack2(x[j + 6], x[j + 7]));
+      __syncthreads();
+#pragma unroll
+      for (int e = 0; e < 8 / kQ; ++e) {
+        const int r = (e * kThreads + tid) >> 3, col = (tid & 7) * 8;
+        if (r < c.len && 64 * sl + col < s.K)
+          *reinterpret_cast<uint4*>(p + (size_t)r * s.Hk * s.K + col) = *reinterpret_cast<const uint4*>(sm.s + at(kCT, r, col));
+      }
+      fence_proxy_async_smem();
+      __syncthreads();
     }
-    fence_proxy_async_smem();
-    __syncthreads();
-  };
-  auto put_row = [&](const float* x) {  // the thread's 32 columns
-#pragma unroll
-    for (int p = 0; p < 4; ++p)
-      *reinterpret_cast<uint4*>(sm.s + at(kCT, row, 32 * half + 8 * p)) =
-          make_uint4(pack2(x[8 * p], x[8 * p + 1]), pack2(x[8 * p + 2], x[8 * p + 3]), pack2(x[8 * p + 4], x[8 * p + 5]),
-                     pack2(x[8 * p + 6], x[8 * p + 7]));
   };
   for (int hv = hk * group; hv < hk * group + group; ++hv) {
-    if (tid == 0) {
+    if (!kF32 && tid == 0) {
       const bool all = hv == hk * group;
       wkv7::mbar_arrive_expect_tx(&sm.full[0], (all ? sizeof sm.q + sizeof sm.k : 0) + sizeof sm.v + sizeof sm.d);
       if (all) {
@@ -108,15 +116,24 @@ __global__ void __launch_bounds__(kThreads, KP == 64 && VP == 64 && !kShared ? 2
       load_tile<VP>(sm.v, &maps.v, &sm.full[0], 0, hv, c.t0, s.v_b ? c.b : 0);
       load_tile<VP>(sm.d, &maps.d, &sm.full[0], 0, hv, c.t0, c.b);
     }
-    if (warp == 7) {
+    if (warp == 4 * kQ - 1) {
       float r[4];
       load_decays(r, s.fixed ? a.g + hv : a.g + tok * s.Hv + hv, s.fixed ? 0 : s.Hv, c.len, lane);
       make_decays(sm.dec, r, s.scale, lane);
     }
     const size_t image = ((size_t)slot * s.Hv + hv) * image_bytes(s.K, s.V);
     const char *S = static_cast<const char*>(a.images) + image, *D = static_cast<const char*>(a.dimages) + image;
-    wait(&sm.full[0], turn2++);
-    if (s.packed && c.len < kCT) {
+    if constexpr (kF32) {
+      if (hv == hk * group) {
+        fill_tile<3, kCT>(sm.q, static_cast<const float*>(a.q) + c.b * s.q_b + c.t0 * s.q_t + (size_t)hk * s.K, s.q_t, c.len, s.K, nullptr, tid, kThreads);
+        fill_tile<3, kCT>(sm.k, static_cast<const float*>(a.k) + c.b * s.k_b + c.t0 * s.k_t + (size_t)hk * s.K, s.k_t, c.len, s.K, nullptr, tid, kThreads);
+      }
+      fill_tile<3, kCT>(sm.v, static_cast<const float*>(a.v) + c.b * s.v_b + c.t0 * s.v_t + (size_t)hv * s.V, s.v_t, c.len, s.V, nullptr, tid, kThreads);
+      fill_tile<3, kCT>(sm.d, static_cast<const float*>(a.d_o) + (tok * s.Hv + hv) * s.V, (long long)s.Hv * s.V, c.len, s.V, nullptr, tid, kThreads);
+    } else {
+      wait(&sm.full[0], turn2++);
+    }
+    if (!kF32 && s.packed && c.len < kCT) {
       if (hv == hk * group) clear_rows<KP>(sm.q, c.len, tid, kThreads), clear_rows<KP>(sm.k, c.len, tid, kThreads);
       clear_rows<VP>(sm.v, c.len, tid, kThreads);
       clear_rows<VP>(sm.d, c.len, tid, kThreads);
@@ -133,14 +150,17 @@ __global__ void __launch_bounds__(kThreads, KP == 64 && VP == 64 && !kShared ? 2
       const bf16_t *ta = kUpper ? sm.v : sm.d, *tb = kUpper ? sm.d : sm.v, *tx = kUpper ? sm.q : sm.k, *td = kUpper ? sm.k : sm.q;
       if (warp == 0) {
         if (elected()) {
-          const uint64_t da = desc(ta), db = desc(tb);
+          auto rows = [&](uint32_t at_d, uint64_t da, uint64_t db, auto cols) {
+            constexpr int D = decltype(cols)::value;
+            terms<kN, kN>([&](int p, int r, bool first) {
 #pragma unroll
-          for (int ks = 0; ks < VP / 16; ++ks) tc_mma(tm + kE, da + along<kCT>(ks), db + along<kCT>(ks), product_of(128, 128, false, false), ks > 0);
-          if (!kUpper && dg) {
-            const uint64_t dq = desc(sm.q), dk = desc(sm.k);
-#pragma unroll
-            for (int ks = 0; ks < KP / 16; ++ks) tc_mma(tm + kQk, dq + along<kCT>(ks), dk + along<kCT>(ks), product_of(128, 128, false, false), ks > 0);
-          }
+              for (int ks = 0; ks < D / 16; ++ks)
+                tc_mma(tm + at_d, da + along<kCT>(ks) + p * (kCT * D * 2 >> 4), db + along<kCT>(ks) + r * (kCT * D * 2 >> 4),
+                       product_of(128, 128, false, false), !first || ks > 0);
+            });
+          };
+          rows(kE, desc(ta), desc(tb), std::integral_constant<int, VP>{});
+          if (!kUpper && dg) rows(kQk, desc(sm.q), desc(sm.k), std::integral_constant<int, KP>{});
           tc_commit(&sm.done[0]);
         }
         __syncwarp();
@@ -180,27 +200,26 @@ __global__ void __launch_bounds__(kThreads, KP == 64 && VP == 64 && !kShared ? 2
       };
       auto inter = [&](int sl) {
         const uint64_t da = desc(ta), ds = desc(sm.s);
-#pragma unroll
-        for (int part = 2; part >= 0; --part)
+        terms<kN, 3>([&](int p, int r, bool first) {
 #pragma unroll
           for (int ks = 0; ks < VP / 16; ++ks)
-            tc_mma(tm + kIn + 64 * sl, da + along<kCT>(ks), ds + across(ks) + part * (VP * 128 >> 4), product_of(128, 64, false, true), part < 2 || ks > 0);
+            tc_mma(tm + kIn + 64 * sl, da + along<kCT>(ks) + p * (kCT * VP * 2 >> 4), ds + across(ks) + r * (VP * 128 >> 4),
+                   product_of(128, 64, false, true), !first || ks > 0);
+        });
       };
       fetch(0);
       wait(&sm.done[0], turn0++);
       tmem_fence_after_sync();
 #pragma unroll 1
-      for (int blk = half; blk < 4; blk += 2) {
+      for (int blk = part_of; blk < 4; blk += kQ) {
         if (kUpper ? blk >= sub : blk <= sub) {
           float x[32];
-          tc_load32(x, mine + kE + 32 * blk);
-          tc_loaded32(x);
+          tc_read(x, mine + kE + 32 * blk);
           decayed<kUpper>(x, sm.dec, row, blk, s.scale);
-          store_pairs(mine + kE + 32 * blk, x);
+          store_parts<kA>(mine + kAt + 16 * kA * blk, x);
           if (!kUpper && dg) {
             float y[32], run = 0.f;
-            tc_load32(y, mine + kQk + 32 * blk);
-            tc_loaded32(y);
+            tc_read(y, mine + kQk + 32 * blk);
 #pragma unroll
             for (int j = 0; j < 32; ++j) {
               const int col = 32 * blk + j;
@@ -208,11 +227,11 @@ __global__ void __launch_bounds__(kThreads, KP == 64 && VP == 64 && !kShared ? 2
               y[j] = col <= row ? run : 0.f;
               run += z;
             }
-            sm.total[blk][row] = run;
+            if (blk < 3) sm.total[blk][row] = run;
             sm.pairs[sub][32 * blk + lane] = warp_columns(y, lane);
           }
         } else {
-          store_zeros(mine + kE + 32 * blk);
+          store_zeros<kA>(mine + kAt + 16 * kA * blk);
         }
       }
       fetched(0);
@@ -225,12 +244,12 @@ __global__ void __launch_bounds__(kThreads, KP == 64 && VP == 64 && !kShared ? 2
           const uint64_t dx = desc(tx);
 #pragma unroll
           for (int sl = 0; sl < kSlices; ++sl)
-#pragma unroll
-            for (int part = 1; part >= 0; --part)
+            terms<kA, kN>([&](int p, int r, bool first) {
 #pragma unroll
               for (int ks = 0; ks < kCT / 16; ++ks)
-                tc_mma_t(tm + kOut + 64 * sl, tm + kE + pair_at(ks, part), dx + across(ks) + sl * (kRowPanel >> 4), product_of(128, 64, false, true),
-                         part == 0 || ks > 0);
+                tc_mma_t(tm + kOut + 64 * sl, tm + kAt + part_at<kA>(ks, p), dx + across(ks) + sl * (kRowPanel >> 4) + r * (kCT * KP * 2 >> 4),
+                         product_of(128, 64, false, true), !first || ks > 0);
+            });
           inter(0);
           tc_commit(&sm.done[1]);
         }
@@ -258,35 +277,38 @@ __global__ void __launch_bounds__(kThreads, KP == 64 && VP == 64 && !kShared ? 2
       float dot = 0.f;
 #pragma unroll
       for (int sl = 0; sl < kSlices; ++sl) {
-        float x[32], y[32];
-        tc_load32(x, mine + kIn + 64 * sl + 32 * half);
-        tc_load32(y, mine + kOut + 64 * sl + 32 * half);
-        tc_loaded32(x);
-        tc_loaded32(y);
+        float x[kW], y[kW];
+        tc_read(x, mine + kIn + 64 * sl + kW * part_of);
+        tc_read(y, mine + kOut + 64 * sl + kW * part_of);
 #pragma unroll
-        for (int j = 0; j < 32; ++j) x[j] *= w;
+        for (int j = 0; j < kW; ++j) x[j] *= w;
         if (dg) {
 #pragma unroll
-          for (int p = 0; p < 4; ++p) {
+          for (int j = 0; j < kW; j += 8) {
+            const bf16_t* z0 = td + at(kCT, row, 64 * sl + kW * part_of + j);
             float z[8];
-            load8(z, td + at(kCT, row, 64 * sl + 32 * half + 8 * p));
+            load8(z, z0);
 #pragma unroll
-            for (int j = 0; j < 8; ++j) dot = fmaf(z[j], x[8 * p + j], dot);
+            for (int p = 1; p < kN; ++p) {
+              float t[8];
+              load8(t, z0 + p * kCT * KP);
+#pragma unroll
+              for (int e = 0; e < 8; ++e) z[e] += t[e];
+            }
+#pragma unroll
+            for (int e = 0; e < 8; ++e) dot = fmaf(z[e], x[j + e], dot);
           }
         }
 #pragma unroll
-        for (int j = 0; j < 32; ++j) {
+        for (int j = 0; j < kW; ++j) {
           if (kShared)
-            acc[kUpper][32 * sl + j] += x[j] + y[j];
+            acc[kUpper][kW * sl + j] += x[j] + y[j];
           else
             x[j] += y[j];
         }
-        if (!kShared) {
-          put_row(x);
-          leave(static_cast<bf16_t*>(kUpper ? a.dk : a.dq), sl);
-        }
+        if (!kShared) leave(static_cast<T*>(kUpper ? a.dk : a.dq), sl, x);
       }
-      if (dg) sm.dots[kUpper][half][row] = dot;
+      if (dg) sm.dots[kUpper][part_of][row] = dot;
       tmem_fence_before_sync();
       __syncthreads();
       tmem_fence_after_sync();
@@ -299,18 +321,24 @@ __global__ void __launch_bounds__(kThreads, KP == 64 && VP == 64 && !kShared ? 2
       __syncthreads();
       if (warp < 4) {  // 32 tokens, one a lane
         const int b = warp, t = 32 * b + lane;
+        auto rows_of = [&](int which, int i) {
+          float x = sm.dots[which][0][i];
+#pragma unroll
+          for (int q = 1; q < kQ; ++q) x += sm.dots[which][q][i];
+          return x;
+        };
         // terms of rows from t on: the state's part, and pairs with columns of the blocks before t's
         auto term = [&](int i) {
-          float x = sm.dots[0][0][i] + sm.dots[0][1][i];
+          float x = rows_of(0, i);
           for (int q = 0; q < b; ++q) x += sm.total[q][i];
           return x;
         };
         float later = 0.f, before = 0.f, pairs = 0.f;
         for (int q = b + 1; q < 4; ++q) later += term(32 * q + lane);
-        for (int q = 0; q < b; ++q) before += sm.dots[1][0][32 * q + lane] + sm.dots[1][1][32 * q + lane];
+        for (int q = 0; q < b; ++q) before += rows_of(1, 32 * q + lane);
         for (int q = b; q < 4; ++q) pairs += sm.pairs[q][t];
         later = warp_sum(later), before = warp_sum(before);
-        float from = term(t), upto = sm.dots[1][0][t] + sm.dots[1][1][t];
+        float from = term(t), upto = rows_of(1, t);
 #pragma unroll
         for (int o = 1; o < 32; o <<= 1) {
           const float x = __shfl_down_sync(0xffffffffu, from, o), y = __shfl_up_sync(0xffffffffu, upto, o);
@@ -321,7 +349,7 @@ __global__ void __launch_bounds__(kThreads, KP == 64 && VP == 64 && !kShared ? 2
         if (lane == 0) upto = 0.f;
         float pass = 0.f;
 #pragma unroll
-        for (int i = 0; i < 8; ++i) pass += sm.whole[i];
+        for (int i = 0; i < 4 * kQ; ++i) pass += sm.whole[i];
         if (t < c.len) a.dg[(tok + t) * s.Hv + hv] = ((from + later) + (upto + before)) + (pairs + sm.dec.whole * pass);
       }
       if (kShared) __syncthreads();
@@ -331,34 +359,35 @@ __global__ void __launch_bounds__(kThreads, KP == 64 && VP == 64 && !kShared ? 2
 #pragma unroll
     for (int i = 0; i < 2; ++i)
 #pragma unroll
-      for (int sl = 0; sl < kSlices; ++sl) {
-        put_row(acc[i] + 32 * sl);
-        leave(static_cast<bf16_t*>(i ? a.dk : a.dq), sl);
-      }
+      for (int sl = 0; sl < kSlices; ++sl) leave(static_cast<T*>(i ? a.dk : a.dq), sl, acc[i] + kW * sl);
   }
   __syncthreads();
   if (warp == 0) wkv7::tmem_dealloc(tm, kCols);
 }
 
-template <int KP, int VP, bool kShared>
+template <typename T, int KP, int VP, bool kShared>
 cudaError_t launch(const Maps& maps, const Args& a, cudaStream_t stream) {
-  const size_t smem = sizeof(Smem<KP, VP>);
+  // two blocks of 256 threads an SM where they fit, else one of 512
+  constexpr int kQ = sizeof(T) == 2 && KP == 64 && VP == 64 && !kShared ? 2 : 4;
+  using M = Smem<T, KP, VP, kQ>;
+  static_assert(sizeof(M) <= 232448, "shared memory of a block");
   static std::atomic<unsigned long long> done{0};
-  const cudaError_t e = allow_smem(reinterpret_cast<const void*>(grad_kernel<KP, VP, kShared>), smem, done);
+  const cudaError_t e = allow_smem(reinterpret_cast<const void*>(grad_kernel<T, KP, VP, kShared, kQ>), sizeof(M), done);
   if (e != cudaSuccess) return e;
-  grad_kernel<KP, VP, kShared><<<(unsigned)((size_t)a.s.slots * a.s.Hk), kThreads, smem, stream>>>(maps, a);
+  grad_kernel<T, KP, VP, kShared, kQ><<<(unsigned)((size_t)a.s.slots * a.s.Hk), 128 * kQ, sizeof(M), stream>>>(maps, a);
   return cudaGetLastError();
 }
-template <int KP, int VP>
+template <typename T, int KP, int VP>
 cudaError_t shared(const Maps& maps, const Args& a, cudaStream_t stream) {
-  return a.s.Hv > a.s.Hk ? launch<KP, VP, true>(maps, a, stream) : launch<KP, VP, false>(maps, a, stream);
+  return a.s.Hv > a.s.Hk ? launch<T, KP, VP, true>(maps, a, stream) : launch<T, KP, VP, false>(maps, a, stream);
 }
 
 }  // namespace
 
-cudaError_t launch_grad(const Maps& maps, const Args& a, cudaStream_t stream) {
-  if (a.s.K <= 64) return a.s.V <= 64 ? shared<64, 64>(maps, a, stream) : shared<64, 128>(maps, a, stream);
-  return a.s.V <= 64 ? shared<128, 64>(maps, a, stream) : shared<128, 128>(maps, a, stream);
+cudaError_t launch_grad(const Maps& maps, const Args& a, bool bf16, cudaStream_t stream) {
+  if (!bf16) return shared<float, 64, 64>(maps, a, stream);
+  if (a.s.K <= 64) return a.s.V <= 64 ? shared<bf16_t, 64, 64>(maps, a, stream) : shared<bf16_t, 64, 128>(maps, a, stream);
+  return a.s.V <= 64 ? shared<bf16_t, 128, 64>(maps, a, stream) : shared<bf16_t, 128, 128>(maps, a, stream);
 }
 
 }  // namespace linattn

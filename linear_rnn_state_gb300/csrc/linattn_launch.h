@@ -10,8 +10,9 @@
 
 namespace linattn {
 
-// Tokens of a chunk: those that fill the rows of a tcgen05 product, or (fp32, mma.sync) 64.
+// Tokens of a chunk: those that fill the rows of a tcgen05 product, or (mma.sync: fp32 with heads above 64) 64.
 constexpr int kCBf16 = 128, kCF32 = 64;
+inline bool on_tcgen05(int K, int V, bool bf16) { return bf16 || (K <= 64 && V <= 64); }
 constexpr int kMaxDim = 128;  // largest head size
 
 // What a call's sequences and heads look like.
@@ -46,7 +47,7 @@ struct Args {
   float *states;       // [slots][Hv][V][K]: the state before each chunk
   float *dstates;      // the gradient of the state after each chunk
   float *decay;        // [slots][Hv]: the whole decay of each chunk
-  void *images, *dimages;  // bfloat16: states and dstates as the gradients' products read them (linattn_tc.cuh)
+  void *images, *dimages;  // states and dstates as the gradients' products read them (linattn_tc.cuh)
   double *part;        // [kParts][Hv]: sums of dg over tokens
   unsigned* status;    // the device's status word
 };
@@ -54,15 +55,16 @@ constexpr int kParts = 256;
 
 // The states before all chunks, or the gradients of those after them, and the last one (s_final, dS_init).
 cudaError_t launch_states(const Args& a, bool bf16, bool backward, cudaStream_t stream);
-// fp32: o; dv, dq, dk and dg of all chunks at once.
+// fp32 with heads above 64: o; dv, dq, dk and dg of all chunks at once.
 cudaError_t launch_rows_o(const Args& a, cudaStream_t stream);
 cudaError_t launch_rows_grad(const Args& a, cudaStream_t stream);
-// bfloat16: o (backward: dv), segments of `chunks` chunks one after the other in a block. resume: from `states` (or
+// On tcgen05: o (backward: dv), segments of `chunks` chunks one after the other in a block. resume: from `states` (or
 // dstates); else whole sequences, and the last state is written. keep: images (or dimages) too.
 struct Maps;
+cudaError_t launch_chain32(const Args& a, bool backward, int chunks, bool resume, bool keep, cudaStream_t stream);  // fp32
 cudaError_t launch_chain(const Maps& maps, const Args& a, bool backward, int chunks, bool resume, bool keep, cudaStream_t stream);
-// bfloat16: dq, dk and dg of all chunks at once.
-cudaError_t launch_grad(const Maps& maps, const Args& a, cudaStream_t stream);
+// dq, dk and dg of all chunks at once, from the images.
+cudaError_t launch_grad(const Maps& maps, const Args& a, bool bf16, cudaStream_t stream);
 // The tensor maps of q, k, v and (where not null) do; false: the driver has no encoder or refuses.
 bool make_maps(Maps& maps, const Args& a);
 cudaError_t launch_dg_sums(const Args& a, cudaStream_t stream);          // dg_fixed from dg

@@ -14,13 +14,11 @@ namespace linattn {
 namespace {
 
 constexpr int kThreads = 128;
-template <typename T>
-constexpr int kChunk = sizeof(T) == 2 ? kCBf16 : kCF32;
 
 // A block: a chunk, a value head, 64 values (16 a warp) by all keys.
-template <typename T, bool kBack, int kTiles>
+template <typename T, bool kBack, int kTiles, int kC>
 __global__ void __launch_bounds__(kThreads) sums_kernel(const Args a, float* out) {
-  constexpr int kP = In<T>::kParts, kKp = kTiles * 8, kC = kChunk<T>;
+  constexpr int kP = In<T>::kParts, kKp = kTiles * 8;
   extern __shared__ __align__(128) unsigned char smem[];
   bf16_t* xs = reinterpret_cast<bf16_t*>(smem);  // [64 tokens][64 values], 3 parts
   bf16_t* bs = xs + 3 * kC * 64;                 // [64 tokens][keys]
@@ -108,20 +106,25 @@ __global__ void __launch_bounds__(256) join_kernel(const Args a, float* states) 
   if (last) reinterpret_cast<float4*>(last)[mine] = S;
 }
 
-template <typename T, bool kBack, int kTiles>
+template <typename T, bool kBack, int kTiles, int kC>
 cudaError_t sums(const Args& a, float* out, cudaStream_t stream) {
-  constexpr int kC = kChunk<T>;
   constexpr size_t smem = (3 * kC * 64 + In<T>::kParts * kC * kTiles * 8) * sizeof(bf16_t) + kC * 12;
   static std::atomic<unsigned long long> done{0};
-  const cudaError_t e = allow_smem(reinterpret_cast<const void*>(sums_kernel<T, kBack, kTiles>), smem, done);
+  const cudaError_t e = allow_smem(reinterpret_cast<const void*>(sums_kernel<T, kBack, kTiles, kC>), smem, done);
   if (e != cudaSuccess) return e;
-  sums_kernel<T, kBack, kTiles><<<(unsigned)((size_t)a.s.slots * a.s.Hv * ((a.s.V + 63) / 64)), kThreads, smem, stream>>>(a, out);
+  sums_kernel<T, kBack, kTiles, kC><<<(unsigned)((size_t)a.s.slots * a.s.Hv * ((a.s.V + 63) / 64)), kThreads, smem, stream>>>(a, out);
   return cudaGetLastError();
 }
 template <typename T, bool kBack>
 cudaError_t states(const Args& a, cudaStream_t stream) {
   float* out = kBack ? a.dstates : a.states;
-  const cudaError_t e = a.s.K <= 64 ? sums<T, kBack, 8>(a, out, stream) : sums<T, kBack, 16>(a, out, stream);
+  cudaError_t e;
+  if constexpr (sizeof(T) == 2)
+    e = a.s.K <= 64 ? sums<T, kBack, 8, kCBf16>(a, out, stream) : sums<T, kBack, 16, kCBf16>(a, out, stream);
+  else if (a.s.C == kCBf16)
+    e = sums<T, kBack, 8, kCBf16>(a, out, stream);
+  else
+    e = a.s.K <= 64 ? sums<T, kBack, 8, kCF32>(a, out, stream) : sums<T, kBack, 16, kCF32>(a, out, stream);
   if (e != cudaSuccess) return e;
   const int per = (a.s.V * a.s.K / 4 + 255) / 256;
   join_kernel<kBack><<<(unsigned)((size_t)a.s.nseq * a.s.Hv * per), 256, 0, stream>>>(a, out);

@@ -17,7 +17,6 @@ using wkv7::mbar_init;
 using wkv7::mbar_wait_bounded;
 using wkv7::tmem_fence_after_sync;
 using wkv7::tmem_fence_before_sync;
-using wkv7::tmem_st;
 
 constexpr int kCT = kCBf16;
 constexpr int kRowPanel = kCT * 128;  // bytes of a panel of 128 rows
@@ -64,10 +63,6 @@ __device__ __forceinline__ constexpr uint32_t along(int ks) {
 // MN-major: block ks of its rows.
 __device__ __forceinline__ constexpr uint32_t across(int ks) { return ks * 2048 >> 4; }
 
-// The pair of a 128 x 128 operand in tensor memory, in the place of the fp32 values it was made of: of each 32
-// columns 16 hold the high parts, 16 the low.
-__device__ __forceinline__ constexpr uint32_t pair_at(int ks, int part) { return (ks >> 1) * 32 + part * 16 + (ks & 1) * 8; }
-
 // 32 columns of a thread's lane, complete.
 __device__ __forceinline__ void tc_load32(float (&v)[32], uint32_t taddr) { wkv7::tmem_ld<32>(taddr, v); }
 __device__ __forceinline__ void tc_loaded32(float (&v)[32]) {
@@ -92,6 +87,16 @@ __device__ __forceinline__ void tc_loaded16(float (&v)[16]) {
                  "+f"(v[10]), "+f"(v[11]), "+f"(v[12]), "+f"(v[13]), "+f"(v[14]), "+f"(v[15])
                :
                : "memory");
+}
+template <int N>
+__device__ __forceinline__ void tc_read(float (&v)[N], uint32_t taddr) {
+  if constexpr (N == 16) {
+    tc_load16(v, taddr);
+    tc_loaded16(v);
+  } else {
+    tc_load32(v, taddr);
+    tc_loaded32(v);
+  }
 }
 // 16 or 32 columns of 16 rows (those of a 64-row accumulator) as mma.sync's accumulator tiles.
 __device__ __forceinline__ void tc_load_tiles(float (&x)[2][4], uint32_t taddr) {
@@ -248,22 +253,49 @@ __device__ __forceinline__ void decayed(float (&x)[32], const Decays& d, int row
       if (kUpper ? j < at : j > at) x[j] = 0.f;
   }
 }
-// 32 values as pairs into their place in tensor memory.
-__device__ __forceinline__ void store_pairs(uint32_t taddr, const float (&x)[32]) {
-  float v[32];
+// 32 columns of a left operand in kP parts into tensor memory, 16 columns a part, or zeros.
+__device__ __forceinline__ void tc_store16(uint32_t taddr, const uint32_t (&v)[16]) {
+  asm volatile("tcgen05.st.sync.aligned.32x32b.x16.b32 [%0], {%1, %2, %3, %4, %5, %6, %7, %8, %9, %10, %11, %12, %13, %14, %15, %16};" ::"r"(taddr),
+               "r"(v[0]), "r"(v[1]), "r"(v[2]), "r"(v[3]), "r"(v[4]), "r"(v[5]), "r"(v[6]), "r"(v[7]), "r"(v[8]), "r"(v[9]), "r"(v[10]),
+               "r"(v[11]), "r"(v[12]), "r"(v[13]), "r"(v[14]), "r"(v[15])
+               : "memory");
+}
+template <int kP>
+__device__ __forceinline__ void store_parts(uint32_t taddr, const float (&x)[32]) {
+  uint32_t v[kP][16];
 #pragma unroll
   for (int j = 0; j < 16; ++j) {
-    uint32_t p[2];
-    split2<2>(x[2 * j], x[2 * j + 1], p);
-    v[j] = __uint_as_float(p[0]), v[16 + j] = __uint_as_float(p[1]);
-  }
-  tmem_st<32>(taddr, v);
-}
-__device__ __forceinline__ void store_zeros(uint32_t taddr) {
-  float v[32];
+    uint32_t p[kP];
+    split2<kP>(x[2 * j], x[2 * j + 1], p);
 #pragma unroll
-  for (int j = 0; j < 32; ++j) v[j] = 0.f;
-  tmem_st<32>(taddr, v);
+    for (int i = 0; i < kP; ++i) v[i][j] = p[i];
+  }
+#pragma unroll
+  for (int i = 0; i < kP; ++i) tc_store16(taddr + 16 * i, v[i]);
+}
+template <int kP>
+__device__ __forceinline__ void store_zeros(uint32_t taddr) {
+  const uint32_t v[16] = {0, 0, 0, 0, 0, 0, 0, 0, 0, 0, 0, 0, 0, 0, 0, 0};
+#pragma unroll
+  for (int i = 0; i < kP; ++i) tc_store16(taddr + 16 * i, v);
+}
+// Where part `part` of the columns 16 ks .. of that operand lies.
+template <int kP>
+__device__ __forceinline__ constexpr uint32_t part_at(int ks, int part) {
+  return (ks >> 1) * 16 * kP + part * 16 + (ks & 1) * 8;
+}
+// The products of the parts of operands with kA and kB of them: f(part of a, part of b, whether it is the first),
+// the small ones first.
+template <int kA, int kB, typename F>
+__device__ __forceinline__ void terms(F f) {
+  constexpr int kMost = kA + kB - 2 < 2 ? kA + kB - 2 : 2;
+#pragma unroll
+  for (int sum = kMost; sum >= 0; --sum)
+#pragma unroll
+    for (int i = 0; i < kA; ++i)
+#pragma unroll
+      for (int j = 0; j < kB; ++j)
+        if (i + j == sum) f(i, j, sum == kMost && i == (kMost < kB ? 0 : kMost - kB + 1));
 }
 
 }  // namespace linattn
