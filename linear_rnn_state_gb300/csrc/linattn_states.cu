@@ -163,13 +163,20 @@ __global__ void __launch_bounds__(256) dg_part_kernel(const Args a, long long to
     __syncthreads();
   }
 }
-__global__ void dg_sum_kernel(const Args a) {
-  const int h = blockIdx.x * blockDim.x + threadIdx.x;
-  if (h >= a.s.Hv) return;
-  double x = 0;
-#pragma unroll 8
-  for (int i = 0; i < kParts; ++i) x += a.part[(size_t)i * a.s.Hv + h];
-  a.dg_fixed[h] = (float)x;
+// A block: a head.
+__global__ void __launch_bounds__(kParts) dg_sum_kernel(const Args a) {
+  __shared__ double red[kParts / 32];
+  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+  double x = a.part[(size_t)threadIdx.x * a.s.Hv + blockIdx.x];
+#pragma unroll
+  for (int o = 16; o >= 1; o >>= 1) x += __shfl_down_sync(0xffffffffu, x, o);
+  if (lane == 0) red[warp] = x;
+  __syncthreads();
+  if (threadIdx.x == 0) {
+#pragma unroll
+    for (int i = 1; i < kParts / 32; ++i) x += red[i];
+    a.dg_fixed[blockIdx.x] = (float)x;
+  }
 }
 
 }  // namespace
@@ -186,7 +193,7 @@ cudaError_t launch_dg_sums(const Args& a, cudaStream_t stream) {
   dg_part_kernel<<<kParts, 256, 0, stream>>>(a, (long long)a.s.B * a.s.T);
   cudaError_t e = cudaGetLastError();
   if (e != cudaSuccess) return e;
-  dg_sum_kernel<<<(a.s.Hv + 31) / 32, 32, 0, stream>>>(a);
+  dg_sum_kernel<<<a.s.Hv, kParts, 0, stream>>>(a);
   return cudaGetLastError();
 }
 

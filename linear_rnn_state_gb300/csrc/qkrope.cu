@@ -5,9 +5,9 @@
 //   backward: d = R^T dy, u = x r, t = d w:  dx = r (t - u mean(t u)),  dw = sum over rows of d u
 //
 // Bound by memory. A row belongs to a group of kGroup lanes with eight values each (16-byte
-// loads); a block takes a stretch of rows, heads of a token beside one another, and a thread has
-// kIter of them on their way at once. The cosines and sines of the tokens of a stretch are
-// formed once, by all threads, in shared memory, and serve all heads of a token.
+// loads), and up to kIter heads of q or of k of a token to a group, all on their way at once. The cosines and sines
+// of a block's tokens are formed once, by all threads, in shared memory; a lane takes those of its values, and its
+// weights, once for its heads.
 //
 // Angles. freq / (2 pi) as a 64-bit fraction of a turn, times the position modulo 2^64, is the angle as a
 // fraction of a turn, off by no more than position * 2^-63; its upper 32 bits go to fp32 as a signed
@@ -37,24 +37,24 @@ __device__ __forceinline__ void fetch(Raw<float>& r, const float* p) {
 }
 __device__ __forceinline__ void clear(Raw<bf16_t>& r) { r.u = make_uint4(0, 0, 0, 0); }
 __device__ __forceinline__ void clear(Raw<float>& r) { r.a = r.b = make_float4(0.f, 0.f, 0.f, 0.f); }
-__device__ __forceinline__ void values(float (&x)[8], const Raw<bf16_t>& r) {
+__device__ __forceinline__ void values(float2 (&x)[4], const Raw<bf16_t>& r) {
   const uint32_t w[4] = {r.u.x, r.u.y, r.u.z, r.u.w};
 #pragma unroll
-  for (int i = 0; i < 4; ++i) x[2 * i] = __uint_as_float(w[i] << 16), x[2 * i + 1] = __uint_as_float(w[i] & 0xFFFF0000u);
+  for (int i = 0; i < 4; ++i) x[i] = make_float2(__uint_as_float(w[i] << 16), __uint_as_float(w[i] & 0xFFFF0000u));
 }
-__device__ __forceinline__ void values(float (&x)[8], const Raw<float>& r) {
-  x[0] = r.a.x, x[1] = r.a.y, x[2] = r.a.z, x[3] = r.a.w, x[4] = r.b.x, x[5] = r.b.y, x[6] = r.b.z, x[7] = r.b.w;
+__device__ __forceinline__ void values(float2 (&x)[4], const Raw<float>& r) {
+  x[0] = make_float2(r.a.x, r.a.y), x[1] = make_float2(r.a.z, r.a.w), x[2] = make_float2(r.b.x, r.b.y), x[3] = make_float2(r.b.z, r.b.w);
 }
 __device__ __forceinline__ uint32_t pack2(float lo, float hi) {
   const __nv_bfloat162 v = __floats2bfloat162_rn(lo, hi);
   return *reinterpret_cast<const uint32_t*>(&v);
 }
-__device__ __forceinline__ void put(bf16_t* p, const float (&x)[8]) {
-  *reinterpret_cast<uint4*>(p) = make_uint4(pack2(x[0], x[1]), pack2(x[2], x[3]), pack2(x[4], x[5]), pack2(x[6], x[7]));
+__device__ __forceinline__ void put(bf16_t* p, const float2 (&x)[4]) {
+  *reinterpret_cast<uint4*>(p) = make_uint4(pack2(x[0].x, x[0].y), pack2(x[1].x, x[1].y), pack2(x[2].x, x[2].y), pack2(x[3].x, x[3].y));
 }
-__device__ __forceinline__ void put(float* p, const float (&x)[8]) {
-  reinterpret_cast<float4*>(p)[0] = make_float4(x[0], x[1], x[2], x[3]);
-  reinterpret_cast<float4*>(p)[1] = make_float4(x[4], x[5], x[6], x[7]);
+__device__ __forceinline__ void put(float* p, const float2 (&x)[4]) {
+  reinterpret_cast<float4*>(p)[0] = make_float4(x[0].x, x[0].y, x[1].x, x[1].y);
+  reinterpret_cast<float4*>(p)[1] = make_float4(x[2].x, x[2].y, x[3].x, x[3].y);
 }
 template <int kGroup>
 __device__ __forceinline__ float group_sum(float x) {
@@ -98,49 +98,69 @@ __device__ __forceinline__ float2 cos_sin(unsigned long long turns, int position
   return make_float2(c, s);
 }
 
-// The stretch [r0, r1) of rows: the table of its tokens, [token][half].
-__device__ __forceinline__ void fill_table(float2* table, const Args& p, long long r0, long long r1, int H) {
-  const unsigned t0 = (unsigned)r0 / (unsigned)H;
-  const int n = (int)((unsigned)(r1 - 1) / (unsigned)H - t0 + 1) * p.half;
-  for (int i = threadIdx.x; i < n; i += kThreads) {
-    const int t = i / p.half, j = i - t * p.half;
-    const unsigned tok = t0 + t;
-    table[i] = cos_sin(turns_of(p.freq[j]), p.positions ? p.positions[tok] : (int)(tok % p.T));
-  }
+// A lane's cosines and sines of a token, the sines with the signs that its values' partners take in forward (the
+// backward turns the other way). kHalves: of its eight values; kInterleaved: of its four pairs.
+template <int kHow>
+struct Turn {
+  float2 c[kHow == kHalves ? 4 : 2], s[kHow == kHalves ? 4 : 2];
+  bool first, in;
+};
+__device__ __forceinline__ float2 mul2(float2 a, float2 b) {
+  float2 d;
+  asm("{\n .reg .b64 x, y;\n mov.b64 x, {%2, %3};\n mov.b64 y, {%4, %5};\n mul.rn.f32x2 x, x, y;\n mov.b64 {%0, %1}, x;\n}"
+      : "=f"(d.x), "=f"(d.y)
+      : "f"(a.x), "f"(a.y), "f"(b.x), "f"(b.y));
+  return d;
 }
-
-// x's pairs turned (kBack: back) in the group's row. c: where the lane's eight values begin; cs: the token's table.
-template <int kHow, int kGroup, bool kBack>
-__device__ __forceinline__ void rotate(float (&x)[8], const float2* cs, int c, int half, int lane, float* row) {
+__device__ __forceinline__ float2 fma2(float2 a, float2 b, float2 c) {
+  float2 d;
+  asm("{\n .reg .b64 x, y, z;\n mov.b64 x, {%2, %3};\n mov.b64 y, {%4, %5};\n mov.b64 z, {%6, %7};\n fma.rn.f32x2 x, x, y, z;\n"
+      " mov.b64 {%0, %1}, x;\n}"
+      : "=f"(d.x), "=f"(d.y)
+      : "f"(a.x), "f"(a.y), "f"(b.x), "f"(b.y), "f"(c.x), "f"(c.y));
+  return d;
+}
+template <int kHow, bool kBack>
+__device__ __forceinline__ void take_turn(Turn<kHow>& t, const float2* cs, int c, int half) {
   if constexpr (kHow == kInterleaved) {
 #pragma unroll
-    for (int e = 0; e < 8; e += 2) {
-      const int j = (c + e) >> 1;
-      if (j < half) {
-        const float2 f = cs[j];
-        const float s = kBack ? -f.y : f.y, a = x[e], b = x[e + 1];
-        x[e] = fmaf(a, f.x, -b * s), x[e + 1] = fmaf(a, s, b * f.x);
+    for (int p = 0; p < 2; ++p)
+#pragma unroll
+      for (int e = 0; e < 2; ++e) {
+        const int j = (c >> 1) + 2 * p + e;
+        const float2 f = j < half ? cs[j] : make_float2(1.f, 0.f);
+        (&t.c[p].x)[e] = f.x, (&t.s[p].x)[e] = kBack ? -f.y : f.y;
       }
+  } else if constexpr (kHow == kHalves) {
+    t.first = c < half, t.in = c < 2 * half;
+    const float sign = t.first != kBack ? -1.f : 1.f;
+#pragma unroll
+    for (int p = 0; p < 4; ++p) {
+      const float4 g = t.in ? *reinterpret_cast<const float4*>(cs + (t.first ? c : c - half) + 2 * p) : make_float4(1.f, 0.f, 1.f, 0.f);
+      t.c[p] = make_float2(g.x, g.z), t.s[p] = make_float2(sign * g.y, sign * g.w);
+    }
+  }
+}
+// A row's values turned (kBack: back), four pairs of neighbours a lane. c: where they begin; row: the group's, for odd halves.
+template <int kHow, int kGroup, bool kBack>
+__device__ __forceinline__ void rotate(float2 (&x)[4], const Turn<kHow>& t, const float2* cs, int c, int half, int lane, float* row) {
+  if constexpr (kHow == kInterleaved) {
+#pragma unroll
+    for (int p = 0; p < 4; ++p) {
+      const float co = (&t.c[p / 2].x)[p % 2], si = (&t.s[p / 2].x)[p % 2], a = x[p].x, b = x[p].y;
+      x[p] = make_float2(fmaf(a, co, -b * si), fmaf(a, si, b * co));
     }
   } else if constexpr (kHow == kHalves) {
-    const bool first = c < half, in = c < 2 * half;
-    const int src = (lane & ~(kGroup - 1)) + (in ? (first ? c + half : c - half) >> 3 : lane & (kGroup - 1));
-    float o[8];
+    const int own = lane & (kGroup - 1), src = (lane & ~(kGroup - 1)) + (t.in ? own + (t.first ? half : -half) / 8 : own);
 #pragma unroll
-    for (int e = 0; e < 8; ++e) o[e] = __shfl_sync(0xffffffffu, x[e], src);
-    if (in) {
-      const float2* f = cs + (first ? c : c - half);
-#pragma unroll
-      for (int e = 0; e < 8; e += 2) {
-        const float4 g = *reinterpret_cast<const float4*>(f + e);
-        const float s0 = first != kBack ? -g.y : g.y, s1 = first != kBack ? -g.w : g.w;
-        x[e] = fmaf(x[e], g.x, o[e] * s0), x[e + 1] = fmaf(x[e + 1], g.z, o[e + 1] * s1);
-      }
+    for (int p = 0; p < 4; ++p) {
+      const float2 o = make_float2(__shfl_sync(0xffffffffu, x[p].x, src), __shfl_sync(0xffffffffu, x[p].y, src));
+      x[p] = fma2(x[p], t.c[p], mul2(o, t.s[p]));
     }
   } else {
     __syncwarp();
 #pragma unroll
-    for (int e = 0; e < 8; ++e) row[c + e] = x[e];
+    for (int p = 0; p < 4; ++p) *reinterpret_cast<float2*>(row + c + 2 * p) = x[p];
     __syncwarp();
 #pragma unroll
     for (int e = 0; e < 8; ++e) {
@@ -148,34 +168,49 @@ __device__ __forceinline__ void rotate(float (&x)[8], const float2* cs, int c, i
       if (i < 2 * half) {
         const bool first = i < half;
         const float2 f = cs[first ? i : i - half];
-        x[e] = fmaf(x[e], f.x, row[first ? i + half : i - half] * (first != kBack ? -f.y : f.y));
+        float& v = (&x[e / 2].x)[e % 2];
+        v = fmaf(v, f.x, row[first ? i + half : i - half] * (first != kBack ? -f.y : f.y));
       }
     }
   }
 }
 
-template <typename T>
-struct Row {
-  const T *x, *dy;
-  T* out;
+// A unit: up to kIter heads of q or of k of a token, for a group of lanes.
+struct Unit {
+  unsigned tok;
+  int h, heads, of;  // first head, heads in the unit, all heads
   bool key;
 };
-template <typename T>
-__device__ __forceinline__ Row<T> row_at(const Args& p, long long row, int H) {
-  const long long tok = (unsigned)row / (unsigned)H;  // (fewer than 2^31 rows)
-  const int h = (int)(row - tok * H);
-  Row<T> r;
-  r.key = h >= p.Hq;
-  if (r.key) {
-    const long long at = (tok * p.Hk + h - p.Hq) * p.D;
-    r.x = static_cast<const T*>(p.k) + tok * p.k_t + (long long)(h - p.Hq) * p.D;
-    r.dy = static_cast<const T*>(p.dko) + at, r.out = static_cast<T*>(p.ko) + at;
-  } else {
-    const long long at = (tok * p.Hq + h) * p.D;
-    r.x = static_cast<const T*>(p.q) + tok * p.q_t + (long long)h * p.D;
-    r.dy = static_cast<const T*>(p.dqo) + at, r.out = static_cast<T*>(p.qo) + at;
+template <int kIter>
+__device__ __forceinline__ int units_of(const Args& p) {  // of a token
+  return (p.Hq + kIter - 1) / kIter + (p.Hk + kIter - 1) / kIter;
+}
+template <int kIter>
+__device__ __forceinline__ Unit unit_at(const Args& p, unsigned u, unsigned units) {
+  const int nq = (p.Hq + kIter - 1) / kIter;
+  Unit x;
+  x.tok = u / units;
+  const int r = (int)(u - x.tok * units);
+  x.key = r >= nq;
+  x.h = (x.key ? r - nq : r) * kIter, x.of = x.key ? p.Hk : p.Hq, x.heads = min(kIter, x.of - x.h);
+  return x;
+}
+// The cosines and sines of the tokens of units [u0, u1): [token][half].
+__device__ __forceinline__ void fill_table(float2* table, const Args& p, unsigned t0, unsigned t1) {
+  const int n = (int)(t1 - t0 + 1) * p.half;
+  for (int i = threadIdx.x; i < n; i += kThreads) {
+    const int t = i / p.half, j = i - t * p.half;
+    table[i] = cos_sin(turns_of(p.freq[j]), p.positions ? p.positions[t0 + t] : (int)((t0 + t) % p.T));
   }
-  return r;
+}
+// Eight weights of a lane.
+__device__ __forceinline__ void weights(float2 (&w)[4], const float* p, int c, int D) {
+#pragma unroll
+  for (int i = 0; i < 4; ++i) w[i] = make_float2(0.f, 0.f);
+  if (c < D) {
+    const float4 a = __ldg(reinterpret_cast<const float4*>(p + c)), b = __ldg(reinterpret_cast<const float4*>(p + c + 4));
+    w[0] = make_float2(a.x, a.y), w[1] = make_float2(a.z, a.w), w[2] = make_float2(b.x, b.y), w[3] = make_float2(b.z, b.w);
+  }
 }
 
 // What a block keeps in shared memory: for odd halves its groups' rows, then the table.
@@ -183,107 +218,110 @@ template <int kHow>
 constexpr int kRowBytes = kHow == kOddHalves ? kThreads * 8 * 4 : 0;
 
 template <typename T, int kHow, int kGroup, int kIter>
-__global__ void __launch_bounds__(kThreads) forward_kernel(const Args p) {
+__global__ void __launch_bounds__(kThreads) forward_kernel(const Args p, unsigned units) {
   extern __shared__ __align__(16) unsigned char smem[];
   constexpr int kGroups = kThreads / kGroup;
   float2* table = reinterpret_cast<float2*>(smem + kRowBytes<kHow>);
-  const int lane = threadIdx.x & 31, group = threadIdx.x / kGroup, c = threadIdx.x % kGroup * 8, H = p.Hq + p.Hk;
+  const int lane = threadIdx.x & 31, group = threadIdx.x / kGroup, c = threadIdx.x % kGroup * 8;
   float* line = reinterpret_cast<float*>(smem) + group * kGroup * 8;
-  const long long r0 = (long long)blockIdx.x * kGroups * kIter, r1 = min(r0 + kGroups * kIter, p.rows);
+  const unsigned u0 = blockIdx.x * kGroups, per = units_of<kIter>(p), u = min(u0 + group, units - 1);
+  const bool live = u0 + group < units && c < p.D;
+  const Unit x = unit_at<kIter>(p, u, per);
+  const T* src = (x.key ? static_cast<const T*>(p.k) + x.tok * p.k_t : static_cast<const T*>(p.q) + x.tok * p.q_t) + x.h * p.D + c;
+  T* dst = static_cast<T*>(x.key ? p.ko : p.qo) + ((long long)x.tok * x.of + x.h) * p.D + c;
   Raw<T> raw[kIter];
 #pragma unroll
   for (int i = 0; i < kIter; ++i) {
-    const long long row = r0 + i * kGroups + group;
     clear(raw[i]);
-    if (row < r1 && c < p.D) fetch(raw[i], row_at<T>(p, row, H).x + c);
+    if (live && i < x.heads) fetch(raw[i], src + i * p.D);
   }
-  fill_table(table, p, r0, r1, H);
+  float2 w[4];
+  weights(w, x.key ? p.wk : p.wq, c, p.D);
+  const unsigned t0 = u0 / per;
+  fill_table(table, p, t0, min(u0 + kGroups, units) == 0 ? t0 : (min(u0 + kGroups, units) - 1) / per);
   __syncthreads();
+  const float2* cs = table + (x.tok - t0) * p.half;
+  Turn<kHow> turn;
+  take_turn<kHow, false>(turn, cs, c, p.half);
+  const float inv = 1.f / (float)p.D;
 #pragma unroll
   for (int i = 0; i < kIter; ++i) {
-    const long long row = r0 + i * kGroups + group;
-    const bool in = row < r1;
-    const Row<T> at = row_at<T>(p, in ? row : r0, H);
-    const float2* cs = table + ((unsigned)(in ? row : r0) / (unsigned)H - (unsigned)r0 / (unsigned)H) * p.half;
-    float x[8], w[8];
-    values(x, raw[i]);
-    if (c < p.D) {
-      Raw<float> rw;
-      fetch(rw, (at.key ? p.wk : p.wq) + c);
-      values(w, rw);
-    } else {
+    float2 v[4], s2 = make_float2(0.f, 0.f);
+    values(v, raw[i]);
 #pragma unroll
-      for (int e = 0; e < 8; ++e) w[e] = 0.f;
-    }
-    float s2 = 0.f;
+    for (int e = 0; e < 4; ++e) s2 = fma2(v[e], v[e], s2);
+    const float r = 1.f / sqrtf(fmaf(group_sum<kGroup>(s2.x + s2.y), inv, p.eps));
 #pragma unroll
-    for (int e = 0; e < 8; ++e) s2 = fmaf(x[e], x[e], s2);
-    const float r = 1.f / sqrtf(group_sum<kGroup>(s2) / (float)p.D + p.eps);
-#pragma unroll
-    for (int e = 0; e < 8; ++e) x[e] *= r * w[e];
-    rotate<kHow, kGroup, false>(x, cs, c, p.half, lane, line);
-    if (in && c < p.D) put(at.out + c, x);
+    for (int e = 0; e < 4; ++e) v[e] = mul2(mul2(v[e], make_float2(r, r)), w[e]);
+    rotate<kHow, kGroup, false>(v, turn, cs, c, p.half, lane, line);
+    if (live && i < x.heads) put(dst + i * p.D, v);
   }
 }
 
-template <typename T, int kHow, int kGroup>
-__global__ void __launch_bounds__(kThreads) backward_kernel(const Args p) {
+template <typename T, int kHow, int kGroup, int kIter>
+__global__ void __launch_bounds__(kThreads, 2) backward_kernel(const Args p, unsigned units) {
   extern __shared__ __align__(16) unsigned char smem[];
-  constexpr int kGroups = kThreads / kGroup, kIter = 2;
+  constexpr int kGroups = kThreads / kGroup;
   __shared__ float join[kThreads * 8];
   float2* table = reinterpret_cast<float2*>(smem + kRowBytes<kHow>);
-  const int lane = threadIdx.x & 31, group = threadIdx.x / kGroup, c = threadIdx.x % kGroup * 8, H = p.Hq + p.Hk;
+  const int lane = threadIdx.x & 31, group = threadIdx.x / kGroup, c = threadIdx.x % kGroup * 8;
   float* line = reinterpret_cast<float*>(smem) + group * kGroup * 8;
-  float dwq[8], dwk[8];
+  const unsigned per = units_of<kIter>(p);
+  const float inv = 1.f / (float)p.D;
+  float2 dwq[4], dwk[4];
 #pragma unroll
-  for (int e = 0; e < 8; ++e) dwq[e] = dwk[e] = 0.f;
-  for (long long r0 = (long long)blockIdx.x * kGroups * kIter; r0 < p.rows; r0 += (long long)gridDim.x * kGroups * kIter) {
-    const long long r1 = min(r0 + kGroups * kIter, p.rows);
+  for (int e = 0; e < 4; ++e) dwq[e] = dwk[e] = make_float2(0.f, 0.f);
+  for (unsigned u0 = blockIdx.x * kGroups; u0 < units; u0 += gridDim.x * kGroups) {
+    const unsigned u = min(u0 + group, units - 1);
+    const bool live = u0 + group < units && c < p.D;
+    const Unit x = unit_at<kIter>(p, u, per);
+    const T* src = (x.key ? static_cast<const T*>(p.k) + x.tok * p.k_t : static_cast<const T*>(p.q) + x.tok * p.q_t) + x.h * p.D + c;
+    const long long at = ((long long)x.tok * x.of + x.h) * p.D + c;
+    const T* up = static_cast<const T*>(x.key ? p.dko : p.dqo) + at;
+    T* dst = static_cast<T*>(x.key ? p.ko : p.qo) + at;
     Raw<T> raw[kIter], rawd[kIter];
 #pragma unroll
     for (int i = 0; i < kIter; ++i) {
-      const long long row = r0 + i * kGroups + group;
       clear(raw[i]), clear(rawd[i]);
-      if (row < r1 && c < p.D) {
-        const Row<T> at = row_at<T>(p, row, H);
-        fetch(raw[i], at.x + c), fetch(rawd[i], at.dy + c);
-      }
+      if (live && i < x.heads) fetch(raw[i], src + i * p.D), fetch(rawd[i], up + i * p.D);
     }
-    __syncthreads();  // the stretch before is done with the table
-    fill_table(table, p, r0, r1, H);
+    float2 w[4];
+    weights(w, x.key ? p.wk : p.wq, c, p.D);
+    const unsigned t0 = u0 / per;
+    __syncthreads();  // the units before are done with the table
+    fill_table(table, p, t0, (min(u0 + kGroups, units) - 1) / per);
     __syncthreads();
+    const float2* cs = table + (x.tok - t0) * p.half;
+    Turn<kHow> turn;
+    take_turn<kHow, true>(turn, cs, c, p.half);
+    float2 dw[4];
+#pragma unroll
+    for (int e = 0; e < 4; ++e) dw[e] = make_float2(0.f, 0.f);
 #pragma unroll
     for (int i = 0; i < kIter; ++i) {
-      const long long row = r0 + i * kGroups + group;
-      const bool in = row < r1;
-      const Row<T> at = row_at<T>(p, in ? row : r0, H);
-      const float2* cs = table + ((unsigned)(in ? row : r0) / (unsigned)H - (unsigned)r0 / (unsigned)H) * p.half;
-      float x[8], d[8], t[8], w[8];
-      values(x, raw[i]), values(d, rawd[i]);
-      if (c < p.D) {
-        Raw<float> rw;
-        fetch(rw, (at.key ? p.wk : p.wq) + c);
-        values(w, rw);
-      } else {
+      float2 v[4], d[4], s2 = make_float2(0.f, 0.f), c1 = s2;
+      values(v, raw[i]), values(d, rawd[i]);  // (0 where there is no row)
+      rotate<kHow, kGroup, true>(d, turn, cs, c, p.half, lane, line);
 #pragma unroll
-        for (int e = 0; e < 8; ++e) w[e] = 0.f;
+      for (int e = 0; e < 4; ++e) s2 = fma2(v[e], v[e], s2), c1 = fma2(mul2(d[e], w[e]), v[e], c1);
+      const float r = 1.f / sqrtf(fmaf(group_sum<kGroup>(s2.x + s2.y), inv, p.eps));
+      const float m = -(group_sum<kGroup>(c1.x + c1.y) * r * inv);
+      const float2 rr = make_float2(r, r), mm = make_float2(m, m);
+#pragma unroll
+      for (int e = 0; e < 4; ++e) {
+        const float2 z = mul2(v[e], rr);
+        dw[e] = fma2(d[e], z, dw[e]);
+        d[e] = mul2(fma2(z, mm, mul2(d[e], w[e])), rr);
       }
-      rotate<kHow, kGroup, true>(d, cs, c, p.half, lane, line);
-      float s2 = 0.f, c1 = 0.f;
+      if (live && i < x.heads) put(dst + i * p.D, d);
+    }
 #pragma unroll
-      for (int e = 0; e < 8; ++e) t[e] = d[e] * w[e], s2 = fmaf(x[e], x[e], s2), c1 = fmaf(t[e], x[e], c1);
-      const float r = 1.f / sqrtf(group_sum<kGroup>(s2) / (float)p.D + p.eps);
-      const float m = group_sum<kGroup>(c1) * r / (float)p.D;
-#pragma unroll
-      for (int e = 0; e < 8; ++e) {
-        const float u = x[e] * r, g = d[e] * u;
-        if (at.key)
-          dwk[e] += in ? g : 0.f;
-        else
-          dwq[e] += in ? g : 0.f;
-        t[e] = r * fmaf(-u, m, t[e]);
-      }
-      if (in && c < p.D) put(at.out + c, t);
+    for (int e = 0; e < 4; ++e) {
+      // (units past the last repeat it with rows of zeros)
+      if (x.key)
+        dwk[e].x += dw[e].x, dwk[e].y += dw[e].y;
+      else
+        dwq[e].x += dw[e].x, dwq[e].y += dw[e].y;
     }
   }
   // the block's sums as one row: [block][q, k][D]
@@ -292,10 +330,11 @@ __global__ void __launch_bounds__(kThreads) backward_kernel(const Args p) {
   for (int s = 0; s < 2; ++s) {
     __syncthreads();
 #pragma unroll
-    for (int e = 0; e < 8; ++e) join[threadIdx.x * 8 + e] = s ? dwk[e] : dwq[e];
+    for (int e = 0; e < 4; ++e) reinterpret_cast<float2*>(join)[threadIdx.x * 4 + e] = s ? dwk[e] : dwq[e];
     __syncthreads();
     for (int i = threadIdx.x; i < p.D; i += kThreads) {
       float x = 0.f;
+#pragma unroll 8
       for (int g = 0; g < kGroups; ++g) x += join[g * kGroup * 8 + i];
       part[s * p.D + i] = x;
     }
@@ -322,35 +361,56 @@ __global__ void __launch_bounds__(kSumThreads) sums_kernel(const Args p, int par
 }
 
 int group_of(int D) { return D <= 32 ? 4 : D <= 64 ? 8 : D <= 128 ? 16 : 32; }
-// Bytes of the table of a stretch of `rows` rows: the tokens it can touch.
-size_t table_bytes(const Args& p, int rows) {
-  const int H = p.Hq + p.Hk;
-  return (size_t)((rows + 2 * H - 2) / H) * p.half * 8;
+// Heads of a unit: four where the units that hold fewer are few and there are units enough for the GPU, else two or
+// one (cosines, sines and weights are fetched once a unit; see the kernels' head).
+int heads_of(const Args& p, long long tokens) {
+  for (int n : {4, 2}) {
+    const long long units = (long long)((p.Hq + n - 1) / n) + (p.Hk + n - 1) / n;
+    if (units * n <= 5 * (p.Hq + p.Hk) / 4 && tokens * units >= 152 * 4 * (kThreads / group_of(p.D))) return n;
+  }
+  return 1;
+}
+unsigned units_in(const Args& p, int heads) {
+  const long long tokens = p.rows / (p.Hq + p.Hk);
+  return (unsigned)(tokens * ((p.Hq + heads - 1) / heads + (p.Hk + heads - 1) / heads));
+}
+// Bytes of the table of the tokens that a block's units can touch.
+size_t table_bytes(const Args& p, int groups, int heads) {
+  const int per = (p.Hq + heads - 1) / heads + (p.Hk + heads - 1) / heads;
+  return (size_t)((groups + 2 * per - 2) / per) * p.half * 8;
 }
 
 template <typename T, int kHow, int kGroup, int kIter>
-cudaError_t forward(const Args& p, cudaStream_t s) {
-  constexpr int rows = kThreads / kGroup * kIter;
-  forward_kernel<T, kHow, kGroup, kIter><<<(unsigned)((p.rows + rows - 1) / rows), kThreads, kRowBytes<kHow> + table_bytes(p, rows), s>>>(p);
+cudaError_t run(const Args& p, bool backward, cudaStream_t s) {
+  constexpr int kGroups = kThreads / kGroup;
+  const unsigned units = units_in(p, kIter);
+  const size_t smem = kRowBytes<kHow> + table_bytes(p, kGroups, kIter);
+  if (!backward) {
+    forward_kernel<T, kHow, kGroup, kIter><<<(units + kGroups - 1) / kGroups, kThreads, smem, s>>>(p, units);
+    return cudaGetLastError();
+  }
+  const unsigned blocks = (units + kGroups - 1) / kGroups, parts = blocks < (unsigned)kParts ? blocks : kParts;
+  backward_kernel<T, kHow, kGroup, kIter><<<parts, kThreads, smem, s>>>(p, units);
+  cudaError_t e = cudaGetLastError();
+  if (e != cudaSuccess) return e;
+  sums_kernel<<<(unsigned)((2 * p.D + 31) / 32), kSumThreads, 0, s>>>(p, (int)parts);
   return cudaGetLastError();
 }
 template <typename T, int kHow, int kGroup>
-cudaError_t run(const Args& p, bool backward, cudaStream_t s) {
-  if (!backward) return p.rows <= 152 * 2 * (kThreads / kGroup) ? forward<T, kHow, kGroup, 1>(p, s) : forward<T, kHow, kGroup, 2>(p, s);
-  const int parts = part_rows(p.rows, p.D);
-  backward_kernel<T, kHow, kGroup><<<parts, kThreads, kRowBytes<kHow> + table_bytes(p, kThreads / kGroup * 2), s>>>(p);
-  cudaError_t e = cudaGetLastError();
-  if (e != cudaSuccess) return e;
-  sums_kernel<<<(unsigned)((2 * p.D + 31) / 32), kSumThreads, 0, s>>>(p, parts);
-  return cudaGetLastError();
+cudaError_t heads(const Args& p, bool backward, cudaStream_t s) {
+  switch (heads_of(p, p.rows / (p.Hq + p.Hk))) {
+    case 4: return run<T, kHow, kGroup, sizeof(T) == 2 ? 4 : 2>(p, backward, s);
+    case 2: return run<T, kHow, kGroup, 2>(p, backward, s);
+    default: return run<T, kHow, kGroup, 1>(p, backward, s);
+  }
 }
 template <typename T, int kHow>
 cudaError_t pick(const Args& p, bool backward, cudaStream_t s) {
   switch (group_of(p.D)) {
-    case 4: return run<T, kHow, 4>(p, backward, s);
-    case 8: return run<T, kHow, 8>(p, backward, s);
-    case 16: return run<T, kHow, 16>(p, backward, s);
-    default: return run<T, kHow, 32>(p, backward, s);
+    case 4: return heads<T, kHow, 4>(p, backward, s);
+    case 8: return heads<T, kHow, 8>(p, backward, s);
+    case 16: return heads<T, kHow, 16>(p, backward, s);
+    default: return heads<T, kHow, 32>(p, backward, s);
   }
 }
 template <typename T>
@@ -361,10 +421,7 @@ cudaError_t how(const Args& p, bool backward, cudaStream_t s) {
 
 }  // namespace
 
-int part_rows(long long rows, int D) {
-  const long long each = kThreads / group_of(D) * 2, blocks = (rows + each - 1) / each;
-  return (int)(blocks < kParts ? (blocks < 1 ? 1 : blocks) : kParts);
-}
+int part_rows(long long rows, int) { return (int)(rows < kParts ? (rows < 1 ? 1 : rows) : kParts); }
 cudaError_t launch(const Args& p, bool bf16, bool backward, cudaStream_t s) {
   return bf16 ? how<bf16_t>(p, backward, s) : how<float>(p, backward, s);
 }

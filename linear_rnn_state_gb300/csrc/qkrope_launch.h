@@ -9,7 +9,7 @@
 namespace qkrope {
 
 constexpr int kMaxD = 256;
-constexpr int kParts = 152 * 4;  // partial rows of the weights' gradients: four blocks an SM
+constexpr int kParts = 152 * 2;  // partial rows of the weights' gradients: two blocks an SM
 
 struct Args {
   const void *q, *k;
