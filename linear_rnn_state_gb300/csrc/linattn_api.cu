@@ -76,10 +76,34 @@ struct Place {
     return p;
   }
 };
-// On tcgen05: whether the chains of all sequences, heads and slices of 64 values would leave most of the GPU idle, so
-// that they go in segments, from states made before.
-bool resumes(const Shape& s) {
-  return (long long)s.nseq * s.Hv * ((s.V + 63) / 64) < 76 && (s.T + s.C - 1) / s.C > 4;
+// On tcgen05: into how many segments of how many chunks a chain goes; 1: none. Chains (sequences, heads and slices of
+// 64 values) run one an SM at a time. Segments fill the GPU, at the price of a pass for their sums, measured at a
+// third of the chain itself, and a few launches; they are taken where they save a tenth of the steps that follow
+// one another. (Packed sequences may be one long and many short ones: the count is that of the longest possible.)
+constexpr int kSms = 152;
+int segment_chunks(const Shape& s) {
+  const long long heads = (long long)s.Hv * ((s.V + 63) / 64), lines = heads * s.nseq;
+  const int chunks = (s.T + s.C - 1) / s.C;
+  if (chunks < 8 || !lines) return 0;
+  auto steps = [&](long long blocks, int each) { return (blocks + kSms - 1) / kSms * each; };
+  // whole chains: dense batches, or packed ones of like lengths with a longest of three times the mean
+  const long long total = s.packed ? (s.T / s.C + s.nseq) * heads : chunks * lines;
+  const long long longest = s.packed ? (chunks * 3 + s.nseq - 1) / s.nseq : chunks;
+  const long long whole = s.packed ? (longest > total / kSms ? longest : total / kSms) : steps(lines, chunks);
+  int best = 0;
+  long long least = whole * 9;
+  for (int n = 2; n <= 64 && n <= chunks / 2; ++n) {
+    const int each = (chunks + n - 1) / n;
+    const long long cost = steps(s.packed ? (total + each - 1) / each : lines * n, each) * 10 * 4 / 3 + 20;
+    if (cost < least) least = cost, best = each;
+  }
+  return best;
+}
+// How many chunks or segments have their states in fp32.
+long long stretches(const Shape& s, bool tc) {
+  if (!tc) return s.slots;
+  const int each = segment_chunks(s);
+  return each ? slot_count(s.B, s.T, s.nseq, s.packed, each * s.C) : 0;
 }
 // The regions of `saved`, and of the backward's workspace, from p on; returns the bytes.
 size_t place_saved(Args& a, bool bf16, bool for_backward, char* p) {
@@ -88,10 +112,9 @@ size_t place_saved(Args& a, bool bf16, bool for_backward, char* p) {
   Place x{p, p};
   const bool tc = on_tcgen05(s.K, s.V, bf16);
   if (tc && for_backward) a.images = x.bytes(n * image_bytes(s.K, s.V));
-  if (!tc || resumes(s)) {
-    x.take(a.states, n * s.V * s.K);
-    x.take(a.decay, n);
-  }
+  const size_t m = (size_t)stretches(s, tc) * s.Hv;
+  x.take(a.states, m * s.V * s.K);
+  x.take(a.decay, m);
   return x.at - x.start;
 }
 size_t place_workspace(Args& a, bool bf16, char* p) {
@@ -100,10 +123,9 @@ size_t place_workspace(Args& a, bool bf16, char* p) {
   Place x{p, p};
   const bool tc = on_tcgen05(s.K, s.V, bf16);
   if (tc) a.dimages = x.bytes(n * image_bytes(s.K, s.V));
-  if (!tc || resumes(s)) {
-    x.take(a.dstates, n * s.V * s.K);
-    x.take(a.decay, n);
-  }
+  const size_t m = (size_t)stretches(s, tc) * s.Hv;
+  x.take(a.dstates, m * s.V * s.K);
+  x.take(a.decay, m);
   if (s.fixed) {
     x.take(a.dg, (size_t)s.B * s.T * s.Hv);
     x.take(a.part, (size_t)kParts * s.Hv);
@@ -128,11 +150,14 @@ int launched(cudaError_t e, const char* what) {
 }
 // On tcgen05: o, or dv.
 int chains(const Maps& maps, const Args& a, bool bf16, bool backward, bool keep, cudaStream_t stream) {
-  const bool resume = resumes(a.s);
-  const int chunks = resume ? 2 : 0;
-  const int rc = resume ? launched(launch_states(a, bf16, backward, stream), "states") : WKV7_OK;
-  if (rc) return rc;
-  return launched(bf16 ? launch_chain(maps, a, backward, chunks, resume, keep, stream) : launch_chain32(a, backward, chunks, resume, keep, stream), "chain");
+  const int each = segment_chunks(a.s);
+  auto run = [&](Way way, bool images) {
+    return launched(bf16 ? launch_chain(maps, a, backward, each, way, images, stream) : launch_chain32(a, backward, each, way, images, stream), "chain");
+  };
+  if (!each) return run(kWhole, keep);
+  int rc = run(kSums, false);
+  if (!rc) rc = launched(launch_join(a, backward, each * a.s.C, stream), "join");
+  return rc ? rc : run(kResume, keep);
 }
 uint32_t* words(void* p) { return static_cast<uint32_t*>(p); }
 
@@ -213,7 +238,7 @@ int linattn_forward(const void* q, const void* k, const void* v, const float* g,
     if (bf16 && !make_maps(maps, a)) return fail(WKV7_ERR_CUDA, "no tensor maps of q, k and v");
     if ((rc = wkv7::api_status_word(&a.status)) || (rc = chains(maps, a, bf16, false, for_backward, stream))) return rc;
   } else {
-    if ((rc = launched(launch_states(a, false, false, stream), "states"))) return rc;
+    if ((rc = launched(launch_states(a, false, stream), "states"))) return rc;
     if ((rc = launched(launch_rows_o(a, stream), "forward"))) return rc;
   }
   if (!a.s.packed) return WKV7_OK;
@@ -268,7 +293,7 @@ int linattn_backward(const void* q, const void* k, const void* v, const float* g
     if ((rc = wkv7::api_status_word(&a.status)) || (rc = chains(maps, a, bf16, true, true, stream))) return rc;
     if ((rc = launched(launch_grad(maps, a, bf16, stream), "gradients"))) return rc;
   } else {
-    if ((rc = launched(launch_states(a, false, true, stream), "states"))) return rc;
+    if ((rc = launched(launch_states(a, true, stream), "states"))) return rc;
     if ((rc = launched(launch_rows_grad(a, stream), "gradients"))) return rc;
   }
   if (a.s.packed) {

@@ -38,7 +38,8 @@ struct Smem {
 
 struct Plan {
   int chunks;  // of a segment
-  int resume, keep;
+  Way way;
+  int keep;
 };
 
 template <int KP, bool kUpper>
@@ -57,7 +58,8 @@ __global__ void __launch_bounds__(kThreads, 1) chain_kernel(const __grid_constan
   const int slices = (s.V + 63) >> 6, slice = blockIdx.x % slices, hv = blockIdx.x / slices % s.Hv, slot = blockIdx.x / slices / s.Hv;
   const int hk = hv / (s.Hv / s.Hk), v0 = slice * 64, vn = min(64, s.V - v0);
   ChunkAt seg;
-  if (plan.resume) {
+  const bool sums = plan.way == kSums;
+  if (plan.way != kWhole) {
     if (!chunk_at(s, slot, kCT * plan.chunks, seg)) return;
   } else {  // a whole sequence, which may be empty: its state passes through
     const SeqRange r = seq_range(s, slot, kCT);
@@ -108,9 +110,9 @@ __global__ void __launch_bounds__(kThreads, 1) chain_kernel(const __grid_constan
         if (i < n && lane == 0) {
           auto& st = sm.stage[i % kSt];
           uint64_t* bar = &sm.full[i % kSt];
-          wkv7::mbar_arrive_expect_tx(bar, sizeof st);
+          wkv7::mbar_arrive_expect_tx(bar, sums ? sizeof st.b + sizeof st.x : sizeof st);
           const int t = seg.t0 + begin(i);
-          load_tile<KP>(st.a, ma, bar, 0, hk, t, seg.b * b_a);
+          if (!sums) load_tile<KP>(st.a, ma, bar, 0, hk, t, seg.b * b_a);
           load_tile<KP>(st.b, mb, bar, 0, hk, t, seg.b * b_b);
           load_tile<64>(st.x, mx, bar, v0, hv, t, seg.b * b_x);
         }
@@ -120,7 +122,7 @@ __global__ void __launch_bounds__(kThreads, 1) chain_kernel(const __grid_constan
         wait(&sm.full[i % kSt], i / kSt);
         if (s.packed && length(i) < kCT) {
           auto& st = sm.stage[i % kSt];
-          clear_rows<KP>(st.a, length(i), lane, 32);
+          if (!sums) clear_rows<KP>(st.a, length(i), lane, 32);
           clear_rows<KP>(st.b, length(i), lane, 32);
           clear_rows<64>(st.x, length(i), lane, 32);
           fence_proxy_async_smem();
@@ -152,11 +154,13 @@ __global__ void __launch_bounds__(kThreads, 1) chain_kernel(const __grid_constan
       for (int i = 0; i < n; ++i) {
         if (lane == 0) bulk_wait_read();
         __syncwarp();
-        announce(kBarFree, kPair);
+        if (!sums) announce(kBarFree, kPair);
         bring(i + kLead);
         brought(i + kLead);
-        meet(kBarOut, kPair);
-        leave(i + 1);
+        if (!sums) {
+          meet(kBarOut, kPair);
+          leave(i + 1);
+        }
         __syncthreads();
       }
       if (lane == 0) bulk_wait_all();
@@ -198,13 +202,13 @@ __global__ void __launch_bounds__(kThreads, 1) chain_kernel(const __grid_constan
           tc_mma(tm + kU, dx + across(ks) + part * (kXt * 128 >> 4), db + across(ks), product_of(64, KP, true, true), h > 0 || part < 2 || ks > 0);
     };
     if (kEarly) {
-      if (n && elected()) scores(0);
+      if (n && !sums && elected()) scores(0);
       __syncwarp();
       __syncthreads();
       tmem_fence_after_sync();
     }
     for (int i = 0; i < n; ++i) {
-      if (elected()) {
+      if (!sums && elected()) {
         if (!kEarly) scores(i);
         if (kEarly && i + 1 < n) scores(i + 1);
         from_state(i);
@@ -221,13 +225,15 @@ __global__ void __launch_bounds__(kThreads, 1) chain_kernel(const __grid_constan
       }
       __syncwarp();
       if (!kEarly) {
-        meet(kBarP, kPair);
-        tmem_fence_after_sync();
-        if (elected()) {
-          from_chunk(i);
-          tc_commit(&sm.out);
+        if (!sums) {
+          meet(kBarP, kPair);
+          tmem_fence_after_sync();
+          if (elected()) {
+            from_chunk(i);
+            tc_commit(&sm.out);
+          }
+          __syncwarp();
         }
-        __syncwarp();
         meet(kBarX2, kPair);
         if (elected()) {
           sum(i, 1);
@@ -279,9 +285,9 @@ __global__ void __launch_bounds__(kThreads, 1) chain_kernel(const __grid_constan
     for (int e = 0; e < 4; ++e) S[t][e] = 0.f;
   const size_t ends = ((size_t)seg.seq * s.Hv + hv) * state + (size_t)s_row * s.K + s_col;
   float* init = const_cast<float*>(kUpper ? a.dS_final : a.s_init);
-  if (plan.resume)
-    each(states + (chunk_slot(s, seg, seg.t0 + begin(0)) * s.Hv + hv) * state, load);
-  else if (init)
+  if (plan.way == kResume)
+    each(states + ((size_t)slot * s.Hv + hv) * state, load);
+  else if (plan.way == kWhole && init)
     each(init + ends, load);
   planes(sm.stage[kSt - 1].b);
   fence_proxy_async_smem();
@@ -328,20 +334,23 @@ __global__ void __launch_bounds__(kThreads, 1) chain_kernel(const __grid_constan
     fence_proxy_async_smem();
   };
   if (kEarly) {
-    if (n) score(0);
+    if (n && !sums) score(0);
     __syncthreads();
   }
+  float passed = 1.f;  // the decay of the segment so far
   for (int i = 0; i < n; ++i) {
-    const auto& d = sm.d[i % 3];
+    const Decays& d = sm.d[i % 3];
     auto& st = sm.stage[i % kSt];
     wait(&sm.full[i % kSt], i / kSt);
     scaled(i, 0);
     announce(kBarX, kPair);
     if (kEarly) {
-      if (i + 1 < n) score(i + 1);
+      if (!sums && i + 1 < n) score(i + 1);
     } else {
-      score(i);
-      announce(kBarP, kPair);
+      if (!sums) {
+        score(i);
+        announce(kBarP, kPair);
+      }
       wait(&sm.first, i);
       scaled(i, 1);
       announce(kBarX2, kPair);
@@ -356,6 +365,13 @@ __global__ void __launch_bounds__(kThreads, 1) chain_kernel(const __grid_constan
       for (int j = 0; j < 2; ++j)
 #pragma unroll
         for (int e = 0; e < 4; ++e) S[t + j][e] = fmaf(d.whole, S[t + j][e], x[j][e]);
+    }
+    passed *= d.whole;
+    if (sums) {
+      tmem_fence_before_sync();
+      __syncthreads();
+      tmem_fence_after_sync();
+      continue;
     }
     meet(kBarFree, kPair);
     planes(st.b);
@@ -394,7 +410,11 @@ __global__ void __launch_bounds__(kThreads, 1) chain_kernel(const __grid_constan
     tmem_fence_after_sync();
   }
   float* last = kUpper ? a.dS_init : a.s_final;
-  if (!plan.resume && last) each(last + ends, store);
+  if (plan.way == kWhole && last) each(last + ends, store);
+  if (sums) {
+    each(states + ((size_t)slot * s.Hv + hv) * state, store);
+    if (tid == 0 && slice == 0) a.decay[(size_t)slot * s.Hv + hv] = passed;
+  }
   __syncthreads();
   if (warp == 0) wkv7::tmem_dealloc(tm, kCols);
 }
@@ -407,15 +427,15 @@ cudaError_t launch(const Maps& maps, const Args& a, const Plan& plan, cudaStream
   const cudaError_t e = allow_smem(reinterpret_cast<const void*>(chain_kernel<KP, kUpper>), smem, done);
   if (e != cudaSuccess) return e;
   const Shape& s = a.s;
-  const long long segs = plan.resume ? slot_count(s.B, s.T, s.nseq, s.packed, kCT * plan.chunks) : s.nseq;
+  const long long segs = plan.way != kWhole ? slot_count(s.B, s.T, s.nseq, s.packed, kCT * plan.chunks) : s.nseq;
   chain_kernel<KP, kUpper><<<(unsigned)(segs * s.Hv * ((s.V + 63) / 64)), kThreads, smem, stream>>>(maps, a, plan);
   return cudaGetLastError();
 }
 
 }  // namespace
 
-cudaError_t launch_chain(const Maps& maps, const Args& a, bool backward, int chunks, bool resume, bool keep, cudaStream_t stream) {
-  const Plan plan{chunks, resume, keep};
+cudaError_t launch_chain(const Maps& maps, const Args& a, bool backward, int chunks, Way way, bool keep, cudaStream_t stream) {
+  const Plan plan{chunks, way, keep};
   if (a.s.K <= 64) return backward ? launch<64, true>(maps, a, plan, stream) : launch<64, false>(maps, a, plan, stream);
   return backward ? launch<128, true>(maps, a, plan, stream) : launch<128, false>(maps, a, plan, stream);
 }

@@ -2,7 +2,7 @@
 //
 // As linattn_chain.cu, with every operand in three bfloat16 parts (24 bits) and six products of parts for each
 // product. The tiles of a chunk (a, b, x and u . x, 192 KB) leave room for one stage: threads split the values of
-// the next chunk when the products of this one are done; a warp has brought them to L2 by then.
+// the next chunk when the products that read the places are done (P x runs beside it); a warp has brought them to L2.
 //
 // Tensor memory: the scores (128 columns, later the rows' P x), P (192), a S^T (64), the state's sum (64).
 #include "linattn_tc.cuh"
@@ -24,10 +24,11 @@ static_assert(sizeof(Smem) <= 232448, "shared memory of a block");
 
 struct Plan {
   int chunks;  // of a segment
-  int resume, keep;
+  Way way;
+  int keep;
 };
 
-template <bool kUpper>
+template <bool kUpper, bool kSumsOnly>
 __global__ void __launch_bounds__(kThreads, 1) chain32_kernel(const Args a, const Plan plan) {
   extern __shared__ __align__(1024) unsigned char raw[];
   Smem& sm = *reinterpret_cast<Smem*>(raw);
@@ -39,7 +40,8 @@ __global__ void __launch_bounds__(kThreads, 1) chain32_kernel(const Args a, cons
   const int slices = (s.V + 63) >> 6, slice = blockIdx.x % slices, hv = blockIdx.x / slices % s.Hv, slot = blockIdx.x / slices / s.Hv;
   const int hk = hv / (s.Hv / s.Hk), v0 = slice * 64, vn = min(64, s.V - v0);
   ChunkAt seg;
-  if (plan.resume) {
+  constexpr bool sums = kSumsOnly;
+  if (plan.way != kWhole) {
     if (!chunk_at(s, slot, kCT * plan.chunks, seg)) return;
   } else {  // a whole sequence, which may be empty: its state passes through
     const SeqRange r = seq_range(s, slot, kCT);
@@ -95,16 +97,19 @@ __global__ void __launch_bounds__(kThreads, 1) chain32_kernel(const Args a, cons
     __syncthreads();
     leave(0);
     for (int i = 0; i < n; ++i) {
+      make(i + 1);
       if (lane == 0) bulk_wait_read();
       __syncwarp();
       announce(kBarFree, kPair);
-      make(i + 1);
-      if (i + 1 < n) {
-        const int t = begin(i + 1), len = length(i + 1);
-        prefetch(pa + t * st_a, st_a, s.K, len), prefetch(pb + t * st_b, st_b, s.K, len), prefetch(px + t * st_x, st_x, vn, len);
+      if (i + 2 < n) {
+        const int t = begin(i + 2), len = length(i + 2);
+        if (!sums) prefetch(pa + t * st_a, st_a, s.K, len);
+        prefetch(pb + t * st_b, st_b, s.K, len), prefetch(px + t * st_x, st_x, vn, len);
       }
-      meet(kBarOut, kPair);
-      leave(i + 1);
+      if (!sums) {
+        meet(kBarOut, kPair);
+        leave(i + 1);
+      }
       __syncthreads();
     }
     if (lane == 0) bulk_wait_all();
@@ -119,19 +124,21 @@ __global__ void __launch_bounds__(kThreads, 1) chain32_kernel(const Args a, cons
     for (int i = 0; i < n; ++i) {
       if (elected()) {
         const uint64_t da = desc(sm.a), db = desc(sm.b), ds = desc(sm.s), du = desc(sm.xt);
-        terms<3, 3>([&](int p, int r, bool first) {
+        if (!sums) {
+          terms<3, 3>([&](int p, int r, bool first) {
 #pragma unroll
-          for (int ks = 0; ks < 4; ++ks)
-            tc_mma(tm + kScore, da + along<kCT>(ks) + p * (kRowPanel >> 4), db + along<kCT>(ks) + r * (kRowPanel >> 4),
-                   product_of(128, 128, false, false), !first || ks > 0);
-        });
-        tc_commit(&sm.scored);
-        terms<3, 3>([&](int p, int r, bool first) {
+            for (int ks = 0; ks < 4; ++ks)
+              tc_mma(tm + kScore, da + along<kCT>(ks) + p * (kRowPanel >> 4), db + along<kCT>(ks) + r * (kRowPanel >> 4),
+                     product_of(128, 128, false, false), !first || ks > 0);
+          });
+          tc_commit(&sm.scored);
+          terms<3, 3>([&](int p, int r, bool first) {
 #pragma unroll
-          for (int ks = 0; ks < 4; ++ks)
-            tc_mma(tm + kIn, da + along<kCT>(ks) + p * (kRowPanel >> 4), ds + along<64>(ks) + r * (64 * 128 >> 4),
-                   product_of(128, 64, false, false), !first || ks > 0);
-        });
+            for (int ks = 0; ks < 4; ++ks)
+              tc_mma(tm + kIn, da + along<kCT>(ks) + p * (kRowPanel >> 4), ds + along<64>(ks) + r * (64 * 128 >> 4),
+                     product_of(128, 64, false, false), !first || ks > 0);
+          });
+        }
         terms<3, 3>([&](int p, int r, bool first) {
 #pragma unroll
           for (int ks = 0; ks < kCT / 16; ++ks)
@@ -141,9 +148,9 @@ __global__ void __launch_bounds__(kThreads, 1) chain32_kernel(const Args a, cons
         tc_commit(&sm.summed);
       }
       __syncwarp();
-      meet(kBarP, kPair);
+      if (!sums) meet(kBarP, kPair);
       tmem_fence_after_sync();
-      if (elected()) {
+      if (!sums && elected()) {
         const uint64_t dx = desc(sm.x);
         terms<3, 3>([&](int p, int r, bool first) {
 #pragma unroll
@@ -163,8 +170,8 @@ __global__ void __launch_bounds__(kThreads, 1) chain32_kernel(const Args a, cons
   // ------------------------------------------------------------------ rows ---
   const int row = sub * 32 + lane;
   float* out = static_cast<float*>(kUpper ? a.dv : a.o) + (tok * s.Hv + hv) * s.V + v0;
-  // A chunk's values: two pieces of eight of each of a, b and x a thread, the first two asked for early.
-  float va[2][8], vb[2][8];
+  // A chunk's values: two pieces of eight of each of a, b and x a thread.
+  float va[sums ? 1 : 2][8], vb[2][8];
   const int piece = (tid & 7) * 8;
   auto ask = [&](int i) {
     const int t0 = begin(i), len = length(i);
@@ -172,14 +179,18 @@ __global__ void __launch_bounds__(kThreads, 1) chain32_kernel(const Args a, cons
     for (int e = 0; e < 2; ++e) {
       const int r = (e * kWorkers + tid) >> 3;
 #pragma unroll
-      for (int j = 0; j < 8; ++j) va[e][j] = vb[e][j] = 0.f;
-      if (r < len && piece < s.K) load8(va[e], pa + (t0 + r) * st_a + piece), load8(vb[e], pb + (t0 + r) * st_b + piece);
+      for (int j = 0; j < 8; ++j) {
+        if (!sums) va[e][j] = 0.f;
+        vb[e][j] = 0.f;
+      }
+      if (r < len && piece < s.K) {
+        if (!sums) load8(va[e], pa + (t0 + r) * st_a + piece);
+        load8(vb[e], pb + (t0 + r) * st_b + piece);
+      }
     }
   };
-  auto fill = [&](int i) {
-    const float* u = kUpper ? sm.d[i & 1].head : sm.d[i & 1].tail;
+  auto ask_x = [&](int i, float (&vx)[2][8]) {
     const int t0 = begin(i), len = length(i);
-    float vx[2][8];
 #pragma unroll
     for (int e = 0; e < 2; ++e) {
       const int r = (e * kWorkers + tid) >> 3;
@@ -187,18 +198,30 @@ __global__ void __launch_bounds__(kThreads, 1) chain32_kernel(const Args a, cons
       for (int j = 0; j < 8; ++j) vx[e][j] = 0.f;
       if (r < len && piece < vn) load8(vx[e], px + (t0 + r) * st_x + piece);
     }
+  };
+  auto fill = [&] {  // a and b
 #pragma unroll
     for (int e = 0; e < 2; ++e) {
-      const int r = (e * kWorkers + tid) >> 3, o = at(kCT, r, piece);
-      put8<3>(sm.a + o, kPart, va[e]);
+      const int o = at(kCT, (e * kWorkers + tid) >> 3, piece);
+      if (!sums) put8<3>(sm.a + o, kPart, va[e]);
       put8<3>(sm.b + o, kPart, vb[e]);
-      put8<3>(sm.x + o, kPart, vx[e]);
-      const float f = u[r];
-#pragma unroll
-      for (int j = 0; j < 8; ++j) vx[e][j] *= f;
-      put8<3>(sm.xt + o, kPart, vx[e]);
     }
-    fence_proxy_async_smem();
+  };
+  auto fill_x = [&](const float (&vx)[2][8]) {
+#pragma unroll
+    for (int e = 0; e < 2; ++e) put8<3>(sm.x + at(kCT, (e * kWorkers + tid) >> 3, piece), kPart, vx[e]);
+  };
+  auto fill_u = [&](int i, const float (&vx)[2][8]) {  // u . x
+    const float* u = kUpper ? sm.d[i & 1].head : sm.d[i & 1].tail;
+#pragma unroll
+    for (int e = 0; e < 2; ++e) {
+      const int r = (e * kWorkers + tid) >> 3;
+      const float f = u[r];
+      float y[8];
+#pragma unroll
+      for (int j = 0; j < 8; ++j) y[j] = vx[e][j] * f;
+      put8<3>(sm.xt + at(kCT, r, piece), kPart, y);
+    }
   };
   if (n) ask(0);
   // The state: rows 16 sub .., keys 16 quarter .. in accumulator tiles.
@@ -231,34 +254,44 @@ __global__ void __launch_bounds__(kThreads, 1) chain32_kernel(const Args a, cons
     for (int e = 0; e < 4; ++e) S[t][e] = 0.f;
   const size_t ends = ((size_t)seg.seq * s.Hv + hv) * state + (size_t)s_row * s.K + s_col;
   float* init = const_cast<float*>(kUpper ? a.dS_final : a.s_init);
-  if (plan.resume)
-    each(states + (chunk_slot(s, seg, seg.t0 + begin(0)) * s.Hv + hv) * state, load);
-  else if (init)
+  if (plan.way == kResume)
+    each(states + ((size_t)slot * s.Hv + hv) * state, load);
+  else if (plan.way == kWhole && init)
     each(init + ends, load);
   planes();
   __syncthreads();  // the first decays
-  if (n) fill(0);
+  if (n) {
+    float vx[2][8];
+    ask_x(0, vx);
+    fill(), fill_u(0, vx);
+    if (!sums) fill_x(vx);
+  }
   fence_proxy_async_smem();
   tmem_fence_before_sync();
   __syncthreads();
   tmem_fence_after_sync();
   const uint32_t tm = sm.tmem, mine = tm + ((uint32_t)(sub * 32) << 16);
   Patience wait{a.status};
+  float passed = 1.f;  // the decay of the segment so far
   for (int i = 0; i < n; ++i) {
     const Decays& d = sm.d[i & 1];
-    wait(&sm.scored, i);
-    tmem_fence_after_sync();
-    if (kUpper ? quarter >= sub : quarter <= sub) {
-      float x[32];
-      tc_read(x, mine + kScore + 32 * quarter);
-      decayed<kUpper>(x, d, row, quarter, s.scale);
-      store_parts<3>(mine + kP + 48 * quarter, x);
-    } else {
-      store_zeros<3>(mine + kP + 48 * quarter);
+    if (!sums) {
+      wait(&sm.scored, i);
+      tmem_fence_after_sync();
+      if (kUpper ? quarter >= sub : quarter <= sub) {
+        float x[32];
+        tc_read(x, mine + kScore + 32 * quarter);
+        decayed<kUpper>(x, d, row, quarter, s.scale);
+        store_parts<3>(mine + kP + 48 * quarter, x);
+      } else {
+        store_zeros<3>(mine + kP + 48 * quarter);
+      }
+      wkv7::tmem_wait_st();
+      tmem_fence_before_sync();
+      announce(kBarP, kPair);
     }
-    wkv7::tmem_wait_st();
-    tmem_fence_before_sync();
-    announce(kBarP, kPair);
+    const bool more = i + 1 < n;
+    if (more) ask(i + 1);
     wait(&sm.summed, i);
     tmem_fence_after_sync();
     {
@@ -269,12 +302,25 @@ __global__ void __launch_bounds__(kThreads, 1) chain32_kernel(const Args a, cons
 #pragma unroll
         for (int e = 0; e < 4; ++e) S[j][e] = fmaf(d.whole, S[j][e], x[j][e]);
     }
-    meet(kBarFree, kPair);
-    planes();
+    passed *= d.whole;
+    meet(kBarFree, kPair);  // the next decays are there, the last state has left
+    if (!sums) planes();
+    float vx[2][8];
+    if (more) {
+      ask_x(i + 1, vx);
+      fill(), fill_u(i + 1, vx);
+    }
+    if (sums) {
+      fence_proxy_async_smem();
+      tmem_fence_before_sync();
+      __syncthreads();
+      tmem_fence_after_sync();
+      continue;
+    }
     wait(&sm.out, i);
     tmem_fence_after_sync();
-    // rows through shared memory (a's place): 16 pieces of four values, permuted by the row
-    float4* stage = reinterpret_cast<float4*>(sm.a);
+    // rows through shared memory (x's place): 16 pieces of four values, permuted by the row
+    float4* stage = reinterpret_cast<float4*>(sm.x);
     {
       float x[16], y[16];
       tc_read(x, mine + kIn + 16 * quarter);
@@ -286,7 +332,6 @@ __global__ void __launch_bounds__(kThreads, 1) chain32_kernel(const Args a, cons
             make_float4(fmaf(w, x[4 * p], y[4 * p]), fmaf(w, x[4 * p + 1], y[4 * p + 1]), fmaf(w, x[4 * p + 2], y[4 * p + 2]), fmaf(w, x[4 * p + 3], y[4 * p + 3]));
     }
     fence_proxy_async_smem();
-    if (i + 1 < n) ask(i + 1);
     meet(kBarOut, kPair);
     {
       const int len = length(i);
@@ -299,33 +344,39 @@ __global__ void __launch_bounds__(kThreads, 1) chain32_kernel(const Args a, cons
       }
     }
     meet(kBarRows, kWorkers);
-    if (i + 1 < n) fill(i + 1);
+    if (more) fill_x(vx);
+    fence_proxy_async_smem();
     tmem_fence_before_sync();
     __syncthreads();
     tmem_fence_after_sync();
   }
   float* last = kUpper ? a.dS_init : a.s_final;
-  if (!plan.resume && last) each(last + ends, store);
+  if (plan.way == kWhole && last) each(last + ends, store);
+  if (sums) {
+    each(states + ((size_t)slot * s.Hv + hv) * state, store);
+    if (tid == 0 && slice == 0) a.decay[(size_t)slot * s.Hv + hv] = passed;
+  }
   __syncthreads();
   if (warp == 0) wkv7::tmem_dealloc(tm, kCols);
 }
 
-template <bool kUpper>
+template <bool kUpper, bool kSumsOnly>
 cudaError_t launch(const Args& a, const Plan& plan, cudaStream_t stream) {
   static std::atomic<unsigned long long> done{0};
-  const cudaError_t e = allow_smem(reinterpret_cast<const void*>(chain32_kernel<kUpper>), sizeof(Smem), done);
+  const cudaError_t e = allow_smem(reinterpret_cast<const void*>(chain32_kernel<kUpper, kSumsOnly>), sizeof(Smem), done);
   if (e != cudaSuccess) return e;
   const Shape& s = a.s;
-  const long long segs = plan.resume ? slot_count(s.B, s.T, s.nseq, s.packed, kCT * plan.chunks) : s.nseq;
-  chain32_kernel<kUpper><<<(unsigned)(segs * s.Hv * ((s.V + 63) / 64)), kThreads, sizeof(Smem), stream>>>(a, plan);
+  const long long segs = plan.way != kWhole ? slot_count(s.B, s.T, s.nseq, s.packed, kCT * plan.chunks) : s.nseq;
+  chain32_kernel<kUpper, kSumsOnly><<<(unsigned)(segs * s.Hv * ((s.V + 63) / 64)), kThreads, sizeof(Smem), stream>>>(a, plan);
   return cudaGetLastError();
 }
 
 }  // namespace
 
-cudaError_t launch_chain32(const Args& a, bool backward, int chunks, bool resume, bool keep, cudaStream_t stream) {
-  const Plan plan{chunks, resume, keep};
-  return backward ? launch<true>(a, plan, stream) : launch<false>(a, plan, stream);
+cudaError_t launch_chain32(const Args& a, bool backward, int chunks, Way way, bool keep, cudaStream_t stream) {
+  const Plan plan{chunks, way, keep};
+  if (way == kSums) return backward ? launch<true, true>(a, plan, stream) : launch<false, true>(a, plan, stream);
+  return backward ? launch<true, false>(a, plan, stream) : launch<false, false>(a, plan, stream);
 }
 
 }  // namespace linattn

@@ -152,6 +152,15 @@ __device__ __forceinline__ void mma_parts(float (&d0)[4], float (&d1)[4], const 
           mma16(d1, a.p[i], b.p[j][2], b.p[j][3]);
         }
 }
+// The same added to the tiles in fp32: the tensor cores cut what they add to an accumulator (2^-23 of it, always
+// towards 0), which over the tens of steps of these sums came to 1e-6.
+template <int kA, int kB>
+__device__ __forceinline__ void mma_added(float (&d0)[4], float (&d1)[4], const Frag<kA>& a, const Frag<kB>& b) {
+  float x[4] = {0.f, 0.f, 0.f, 0.f}, y[4] = {0.f, 0.f, 0.f, 0.f};
+  mma_parts(x, y, a, b);
+#pragma unroll
+  for (int e = 0; e < 4; ++e) d0[e] += x[e], d1[e] += y[e];
+}
 // Two accumulator tiles (columns k0 .. k0+7 and k0+8 .. k0+15 of 16 rows) as the A
 // fragment of a product over those columns.
 template <int kP>

@@ -44,25 +44,31 @@ struct Args {
   float *s_final, *dS_init;
   float *dg;           // [B][T][Hv] (a workspace where g is fixed)
   float *dg_fixed;     // [Hv], where g is fixed
-  float *states;       // [slots][Hv][V][K]: the state before each chunk
-  float *dstates;      // the gradient of the state after each chunk
-  float *decay;        // [slots][Hv]: the whole decay of each chunk
+  float *states;       // [slots][Hv][V][K]: the state before each chunk or segment
+  float *dstates;      // the gradient of the state after each
+  float *decay;        // [slots][Hv]: the whole decay of each
   void *images, *dimages;  // states and dstates as the gradients' products read them (linattn_tc.cuh)
   double *part;        // [kParts][Hv]: sums of dg over tokens
   unsigned* status;    // the device's status word
 };
 constexpr int kParts = 256;
 
-// The states before all chunks, or the gradients of those after them, and the last one (s_final, dS_init).
-cudaError_t launch_states(const Args& a, bool bf16, bool backward, cudaStream_t stream);
-// fp32 with heads above 64: o; dv, dq, dk and dg of all chunks at once.
+// fp32 with heads above 64: the states before all chunks, or the gradients of those after them, and the last one
+// (s_final, dS_init); o; dv, dq, dk and dg of all chunks at once.
+cudaError_t launch_states(const Args& a, bool backward, cudaStream_t stream);
 cudaError_t launch_rows_o(const Args& a, cudaStream_t stream);
 cudaError_t launch_rows_grad(const Args& a, cudaStream_t stream);
-// On tcgen05: o (backward: dv), segments of `chunks` chunks one after the other in a block. resume: from `states` (or
-// dstates); else whole sequences, and the last state is written. keep: images (or dimages) too.
+// On tcgen05: o (backward: dv), from chunk to chunk.
+//   kWhole: whole sequences, from s_init (dS_final) to s_final (dS_init)
+//   kSums: segments of `chunks` chunks from zeros: only the sum of each, to `states` (dstates), and its whole decay
+//   kResume: segments from `states`, where join has put the state before each
+// keep: images (or dimages) of the states before (after) the chunks too.
 struct Maps;
-cudaError_t launch_chain32(const Args& a, bool backward, int chunks, bool resume, bool keep, cudaStream_t stream);  // fp32
-cudaError_t launch_chain(const Maps& maps, const Args& a, bool backward, int chunks, bool resume, bool keep, cudaStream_t stream);
+enum Way { kWhole, kSums, kResume };
+cudaError_t launch_chain(const Maps& maps, const Args& a, bool backward, int chunks, Way way, bool keep, cudaStream_t stream);
+cudaError_t launch_chain32(const Args& a, bool backward, int chunks, Way way, bool keep, cudaStream_t stream);  // fp32
+// From sums of stretches of `tokens` tokens to the states before (the gradients after) them, and the last one.
+cudaError_t launch_join(const Args& a, bool backward, int tokens, cudaStream_t stream);
 // dq, dk and dg of all chunks at once, from the images.
 cudaError_t launch_grad(const Maps& maps, const Args& a, bool bf16, cudaStream_t stream);
 // The tensor maps of q, k, v and (where not null) do; false: the driver has no encoder or refuses.

@@ -58,7 +58,7 @@ __device__ __forceinline__ void scores(float (&x)[8][4], const bf16_t* as, const
       if (kUpper ? n >= warp : n <= warp) {
         Frag<kP> fb;
         b_nk(fb, bs, kC, kC * Dp, 16 * n, k0, lane);
-        mma_parts(x[2 * n], x[2 * n + 1], fa, fb);
+        mma_added(x[2 * n], x[2 * n + 1], fa, fb);
       }
   }
 }
@@ -219,7 +219,7 @@ __global__ void __launch_bounds__(kThreads) rows_kernel(const Args a) {
               b_kn(fb, ss, Dp, 64 * Dp, 16 * n, k0, lane);
             else
               b_nk(fb, ss, 64, 64 * Dp, 16 * n, k0, lane);
-            mma_parts(y0, y1, fa, fb);
+            mma_added(y0, y1, fa, fb);
           }
           const float w0 = w[16 * warp + gr], w1 = w[16 * warp + gr + 8];
 #pragma unroll
@@ -250,7 +250,7 @@ __global__ void __launch_bounds__(kThreads) rows_kernel(const Args a) {
             if (kUpper ? j >= warp : j <= warp) {
               Frag<kP> fx;
               b_kn(fx, xs, kC, kC * 64, 16 * n, 16 * j, lane);
-              mma_parts(acc[sl][2 * n], acc[sl][2 * n + 1], pf[j], fx);
+              mma_added(acc[sl][2 * n], acc[sl][2 * n + 1], pf[j], fx);
             }
         }
     }

@@ -1,5 +1,5 @@
 // Linear attention with a decay: the states before every chunk, and backward the gradients of the
-// states after every chunk.
+// states after every chunk (fp32 with heads above 64; the joining serves segments of the others too).
 //
 // Within a chunk, with G the running sum of its log decays and Gc the whole sum:
 //   forward   S' = e^{Gc} S + sum_j e^{Gc - G_j} v_j k_j^T
@@ -13,11 +13,12 @@
 namespace linattn {
 namespace {
 
-constexpr int kThreads = 128;
+constexpr int kThreads = 128, kC = kCF32;
 
 // A block: a chunk, a value head, 64 values (16 a warp) by all keys.
-template <typename T, bool kBack, int kTiles, int kC>
+template <bool kBack, int kTiles>
 __global__ void __launch_bounds__(kThreads) sums_kernel(const Args a, float* out) {
+  typedef float T;
   constexpr int kP = In<T>::kParts, kKp = kTiles * 8;
   extern __shared__ __align__(128) unsigned char smem[];
   bf16_t* xs = reinterpret_cast<bf16_t*>(smem);  // [64 tokens][64 values], 3 parts
@@ -56,7 +57,7 @@ __global__ void __launch_bounds__(kThreads) sums_kernel(const Args a, float* out
     for (int n = 0; n < kTiles / 2; ++n) {
       Frag<kP> fb;
       b_kn(fb, bs, kC, kC * kKp, 16 * n, k0, lane);
-      mma_parts(acc[2 * n], acc[2 * n + 1], fa, fb);
+      mma_added(acc[2 * n], acc[2 * n + 1], fa, fb);
     }
   }
   float* dst = out + ((size_t)slot * s.Hv + hv) * s.V * s.K;
@@ -72,13 +73,13 @@ __global__ void __launch_bounds__(kThreads) sums_kernel(const Args a, float* out
 // A thread: four numbers of a state, over the chunks of its sequence, kAhead of them on their way.
 constexpr int kAhead = 8;
 template <bool kBack>
-__global__ void __launch_bounds__(256) join_kernel(const Args a, float* states) {
+__global__ void __launch_bounds__(256) join_kernel(const Args a, float* states, int tokens) {
   const Shape& s = a.s;
   const int quads = s.V * s.K / 4, per = (quads + 255) / 256, piece = (blockIdx.x % per) * 256 + threadIdx.x;
   const int hv = blockIdx.x / per % s.Hv, seq = blockIdx.x / per / s.Hv;
   if (piece >= quads) return;
-  const SeqRange r = seq_range(s, seq, s.C);
-  const int n = (r.t1 - r.t0 + s.C - 1) / s.C;
+  const SeqRange r = seq_range(s, seq, tokens);
+  const int n = (r.t1 - r.t0 + tokens - 1) / tokens;
   const size_t mine = ((size_t)seq * s.Hv + hv) * quads + piece;
   const float* init = kBack ? a.dS_final : a.s_init;
   float4 S = init ? reinterpret_cast<const float4*>(init)[mine] : make_float4(0.f, 0.f, 0.f, 0.f);
@@ -106,28 +107,13 @@ __global__ void __launch_bounds__(256) join_kernel(const Args a, float* states) 
   if (last) reinterpret_cast<float4*>(last)[mine] = S;
 }
 
-template <typename T, bool kBack, int kTiles, int kC>
-cudaError_t sums(const Args& a, float* out, cudaStream_t stream) {
-  constexpr size_t smem = (3 * kC * 64 + In<T>::kParts * kC * kTiles * 8) * sizeof(bf16_t) + kC * 12;
+template <bool kBack, int kTiles>
+cudaError_t sums(const Args& a, cudaStream_t stream) {
+  constexpr size_t smem = (3 * kC * 64 + 3 * kC * kTiles * 8) * sizeof(bf16_t) + kC * 12;
   static std::atomic<unsigned long long> done{0};
-  const cudaError_t e = allow_smem(reinterpret_cast<const void*>(sums_kernel<T, kBack, kTiles, kC>), smem, done);
+  const cudaError_t e = allow_smem(reinterpret_cast<const void*>(sums_kernel<kBack, kTiles>), smem, done);
   if (e != cudaSuccess) return e;
-  sums_kernel<T, kBack, kTiles, kC><<<(unsigned)((size_t)a.s.slots * a.s.Hv * ((a.s.V + 63) / 64)), kThreads, smem, stream>>>(a, out);
-  return cudaGetLastError();
-}
-template <typename T, bool kBack>
-cudaError_t states(const Args& a, cudaStream_t stream) {
-  float* out = kBack ? a.dstates : a.states;
-  cudaError_t e;
-  if constexpr (sizeof(T) == 2)
-    e = a.s.K <= 64 ? sums<T, kBack, 8, kCBf16>(a, out, stream) : sums<T, kBack, 16, kCBf16>(a, out, stream);
-  else if (a.s.C == kCBf16)
-    e = sums<T, kBack, 8, kCBf16>(a, out, stream);
-  else
-    e = a.s.K <= 64 ? sums<T, kBack, 8, kCF32>(a, out, stream) : sums<T, kBack, 16, kCF32>(a, out, stream);
-  if (e != cudaSuccess) return e;
-  const int per = (a.s.V * a.s.K / 4 + 255) / 256;
-  join_kernel<kBack><<<(unsigned)((size_t)a.s.nseq * a.s.Hv * per), 256, 0, stream>>>(a, out);
+  sums_kernel<kBack, kTiles><<<(unsigned)((size_t)a.s.slots * a.s.Hv * ((a.s.V + 63) / 64)), kThreads, smem, stream>>>(a, kBack ? a.dstates : a.states);
   return cudaGetLastError();
 }
 
@@ -181,9 +167,21 @@ __global__ void __launch_bounds__(kParts) dg_sum_kernel(const Args a) {
 
 }  // namespace
 
-cudaError_t launch_states(const Args& a, bool bf16, bool backward, cudaStream_t stream) {
-  if (bf16) return backward ? states<bf16_t, true>(a, stream) : states<bf16_t, false>(a, stream);
-  return backward ? states<float, true>(a, stream) : states<float, false>(a, stream);
+cudaError_t launch_join(const Args& a, bool backward, int tokens, cudaStream_t stream) {
+  const unsigned blocks = (unsigned)((size_t)a.s.nseq * a.s.Hv * ((a.s.V * a.s.K / 4 + 255) / 256));
+  if (backward)
+    join_kernel<true><<<blocks, 256, 0, stream>>>(a, a.dstates, tokens);
+  else
+    join_kernel<false><<<blocks, 256, 0, stream>>>(a, a.states, tokens);
+  return cudaGetLastError();
+}
+cudaError_t launch_states(const Args& a, bool backward, cudaStream_t stream) {
+  cudaError_t e;
+  if (backward)
+    e = a.s.K <= 64 ? sums<true, 8>(a, stream) : sums<true, 16>(a, stream);
+  else
+    e = a.s.K <= 64 ? sums<false, 8>(a, stream) : sums<false, 16>(a, stream);
+  return e == cudaSuccess ? launch_join(a, backward, a.s.C, stream) : e;
 }
 cudaError_t launch_gaps(const Args& a, const Gaps& g, cudaStream_t stream) {
   gaps_kernel<<<(unsigned)(a.s.T < 256 ? a.s.T : 256), 256, 0, stream>>>(a, g);
