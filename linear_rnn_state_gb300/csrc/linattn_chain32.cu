@@ -10,8 +10,8 @@
 namespace linattn {
 namespace {
 
-constexpr int kWorkers = 512, kThreads = kWorkers + 64;
-constexpr int kHelpWarp = 16;  // and 17 issues
+constexpr int kWorkers = 512, kMembers = kWorkers + 64, kThreads = kWorkers + 128;  // (registers go by four warps)
+constexpr int kHelpWarp = 16;                                                          // and 17 issues
 
 struct Smem {
   bf16_t a[3 * kCT * 64], b[3 * kCT * 64], x[3 * kCT * 64], xt[3 * kCT * 64];
@@ -64,6 +64,8 @@ __global__ void __launch_bounds__(kThreads, 1) chain32_kernel(const Args a, cons
   const float* px = kUpper ? static_cast<const float*>(a.d_o) + (tok * s.Hv + hv) * s.V + v0
                            : static_cast<const float*>(a.v) + seg.b * s.v_b + seg.t0 * s.v_t + (size_t)hv * s.V + v0;
 
+  if (warp >= kHelpWarp) fewer_registers<40>();
+  if (warp > kHelpWarp + 1) return;
   if (warp == kHelpWarp) {
     const float* g = s.fixed ? a.g + hv : a.g + tok * s.Hv + hv;
     float r[4];
@@ -93,8 +95,8 @@ __global__ void __launch_bounds__(kThreads, 1) chain32_kernel(const Args a, cons
       }
     };
     ask(0), make(0);
-    __syncthreads();
-    __syncthreads();
+    meet(0, kMembers);
+    meet(0, kMembers);
     leave(0);
     for (int i = 0; i < n; ++i) {
       make(i + 1);
@@ -110,15 +112,15 @@ __global__ void __launch_bounds__(kThreads, 1) chain32_kernel(const Args a, cons
         meet(kBarOut, kPair);
         leave(i + 1);
       }
-      __syncthreads();
+      meet(0, kMembers);
     }
     if (lane == 0) bulk_wait_all();
-    __syncthreads();
+    meet(0, kMembers);
     return;
   }
   if (warp > kHelpWarp) {
-    __syncthreads();
-    __syncthreads();
+    meet(0, kMembers);
+    meet(0, kMembers);
     tmem_fence_after_sync();
     const uint32_t tm = sm.tmem;
     for (int i = 0; i < n; ++i) {
@@ -126,21 +128,21 @@ __global__ void __launch_bounds__(kThreads, 1) chain32_kernel(const Args a, cons
         const uint64_t da = desc(sm.a), db = desc(sm.b), ds = desc(sm.s), du = desc(sm.xt);
         if (!sums) {
           terms<3, 3>([&](int p, int r, bool first) {
-#pragma unroll
+#pragma unroll 1
             for (int ks = 0; ks < 4; ++ks)
               tc_mma(tm + kScore, da + along<kCT>(ks) + p * (kRowPanel >> 4), db + along<kCT>(ks) + r * (kRowPanel >> 4),
                      product_of(128, 128, false, false), !first || ks > 0);
           });
           tc_commit(&sm.scored);
           terms<3, 3>([&](int p, int r, bool first) {
-#pragma unroll
+#pragma unroll 1
             for (int ks = 0; ks < 4; ++ks)
               tc_mma(tm + kIn, da + along<kCT>(ks) + p * (kRowPanel >> 4), ds + along<64>(ks) + r * (64 * 128 >> 4),
                      product_of(128, 64, false, false), !first || ks > 0);
           });
         }
         terms<3, 3>([&](int p, int r, bool first) {
-#pragma unroll
+#pragma unroll 1
           for (int ks = 0; ks < kCT / 16; ++ks)
             tc_mma(tm + kU, du + across(ks) + p * (kRowPanel >> 4), db + across(ks) + r * (kRowPanel >> 4), product_of(64, 64, true, true),
                    !first || ks > 0);
@@ -153,21 +155,22 @@ __global__ void __launch_bounds__(kThreads, 1) chain32_kernel(const Args a, cons
       if (!sums && elected()) {
         const uint64_t dx = desc(sm.x);
         terms<3, 3>([&](int p, int r, bool first) {
-#pragma unroll
+#pragma unroll 1
           for (int ks = 0; ks < kCT / 16; ++ks)
             tc_mma_t(tm + kO, tm + kP + part_at<3>(ks, p), dx + across(ks) + r * (kRowPanel >> 4), product_of(128, 64, false, true), !first || ks > 0);
         });
         tc_commit(&sm.out);
       }
       __syncwarp();
-      __syncthreads();
+      meet(0, kMembers);
       tmem_fence_after_sync();
     }
-    __syncthreads();
+    meet(0, kMembers);
     return;
   }
 
   // ------------------------------------------------------------------ rows ---
+  more_registers<104>();
   const int row = sub * 32 + lane;
   float* out = static_cast<float*>(kUpper ? a.dv : a.o) + (tok * s.Hv + hv) * s.V + v0;
   // A chunk's values: two pieces of eight of each of a, b and x a thread.
@@ -259,7 +262,7 @@ __global__ void __launch_bounds__(kThreads, 1) chain32_kernel(const Args a, cons
   else if (plan.way == kWhole && init)
     each(init + ends, load);
   planes();
-  __syncthreads();  // the first decays
+  meet(0, kMembers);  // the first decays
   if (n) {
     float vx[2][8];
     ask_x(0, vx);
@@ -268,7 +271,7 @@ __global__ void __launch_bounds__(kThreads, 1) chain32_kernel(const Args a, cons
   }
   fence_proxy_async_smem();
   tmem_fence_before_sync();
-  __syncthreads();
+  meet(0, kMembers);
   tmem_fence_after_sync();
   const uint32_t tm = sm.tmem, mine = tm + ((uint32_t)(sub * 32) << 16);
   Patience wait{a.status};
@@ -291,7 +294,6 @@ __global__ void __launch_bounds__(kThreads, 1) chain32_kernel(const Args a, cons
       announce(kBarP, kPair);
     }
     const bool more = i + 1 < n;
-    if (more) ask(i + 1);
     wait(&sm.summed, i);
     tmem_fence_after_sync();
     {
@@ -304,6 +306,7 @@ __global__ void __launch_bounds__(kThreads, 1) chain32_kernel(const Args a, cons
     }
     passed *= d.whole;
     meet(kBarFree, kPair);  // the next decays are there, the last state has left
+    if (more) ask(i + 1);
     if (!sums) planes();
     float vx[2][8];
     if (more) {
@@ -313,7 +316,7 @@ __global__ void __launch_bounds__(kThreads, 1) chain32_kernel(const Args a, cons
     if (sums) {
       fence_proxy_async_smem();
       tmem_fence_before_sync();
-      __syncthreads();
+      meet(0, kMembers);
       tmem_fence_after_sync();
       continue;
     }
@@ -347,7 +350,7 @@ __global__ void __launch_bounds__(kThreads, 1) chain32_kernel(const Args a, cons
     if (more) fill_x(vx);
     fence_proxy_async_smem();
     tmem_fence_before_sync();
-    __syncthreads();
+    meet(0, kMembers);
     tmem_fence_after_sync();
   }
   float* last = kUpper ? a.dS_init : a.s_final;
@@ -356,7 +359,7 @@ __global__ void __launch_bounds__(kThreads, 1) chain32_kernel(const Args a, cons
     each(states + ((size_t)slot * s.Hv + hv) * state, store);
     if (tid == 0 && slice == 0) a.decay[(size_t)slot * s.Hv + hv] = passed;
   }
-  __syncthreads();
+  meet(0, kMembers);
   if (warp == 0) wkv7::tmem_dealloc(tm, kCols);
 }
 

@@ -128,6 +128,12 @@ __device__ __forceinline__ void stsm4(bf16_t* p, const uint32_t (&r)[4]) {
                : "memory");
 }
 
+// Registers of a thread of the calling four warps, of those the block was launched with.
+template <int N>
+__device__ __forceinline__ void more_registers() { asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(N)); }
+template <int N>
+__device__ __forceinline__ void fewer_registers() { asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(N)); }
+
 // Barrier `id` of some of a block's warps: `n` threads in all meet there, or announce themselves and go on.
 __device__ __forceinline__ void meet(int id, int n) { asm volatile("bar.sync %0, %1;" ::"r"(id), "r"(n) : "memory"); }
 __device__ __forceinline__ void announce(int id, int n) { asm volatile("bar.arrive %0, %1;" ::"r"(id), "r"(n) : "memory"); }
@@ -253,31 +259,34 @@ __device__ __forceinline__ void decayed(float (&x)[32], const Decays& d, int row
       if (kUpper ? j < at : j > at) x[j] = 0.f;
   }
 }
-// 32 columns of a left operand in kP parts into tensor memory, 16 columns a part, or zeros.
-__device__ __forceinline__ void tc_store16(uint32_t taddr, const uint32_t (&v)[16]) {
-  asm volatile("tcgen05.st.sync.aligned.32x32b.x16.b32 [%0], {%1, %2, %3, %4, %5, %6, %7, %8, %9, %10, %11, %12, %13, %14, %15, %16};" ::"r"(taddr),
-               "r"(v[0]), "r"(v[1]), "r"(v[2]), "r"(v[3]), "r"(v[4]), "r"(v[5]), "r"(v[6]), "r"(v[7]), "r"(v[8]), "r"(v[9]), "r"(v[10]),
-               "r"(v[11]), "r"(v[12]), "r"(v[13]), "r"(v[14]), "r"(v[15])
+// 32 columns of a left operand in kP parts into tensor memory, 16 columns a part (eight at a time, for fewer
+// registers), or zeros.
+__device__ __forceinline__ void tc_store8(uint32_t taddr, const uint32_t (&v)[8]) {
+  asm volatile("tcgen05.st.sync.aligned.32x32b.x8.b32 [%0], {%1, %2, %3, %4, %5, %6, %7, %8};" ::"r"(taddr), "r"(v[0]), "r"(v[1]), "r"(v[2]),
+               "r"(v[3]), "r"(v[4]), "r"(v[5]), "r"(v[6]), "r"(v[7])
                : "memory");
 }
 template <int kP>
 __device__ __forceinline__ void store_parts(uint32_t taddr, const float (&x)[32]) {
-  uint32_t v[kP][16];
 #pragma unroll
-  for (int j = 0; j < 16; ++j) {
-    uint32_t p[kP];
-    split2<kP>(x[2 * j], x[2 * j + 1], p);
+  for (int h = 0; h < 2; ++h) {
+    uint32_t v[kP][8];
 #pragma unroll
-    for (int i = 0; i < kP; ++i) v[i][j] = p[i];
+    for (int j = 0; j < 8; ++j) {
+      uint32_t p[kP];
+      split2<kP>(x[16 * h + 2 * j], x[16 * h + 2 * j + 1], p);
+#pragma unroll
+      for (int i = 0; i < kP; ++i) v[i][j] = p[i];
+    }
+#pragma unroll
+    for (int i = 0; i < kP; ++i) tc_store8(taddr + 16 * i + 8 * h, v[i]);
   }
-#pragma unroll
-  for (int i = 0; i < kP; ++i) tc_store16(taddr + 16 * i, v[i]);
 }
 template <int kP>
 __device__ __forceinline__ void store_zeros(uint32_t taddr) {
-  const uint32_t v[16] = {0, 0, 0, 0, 0, 0, 0, 0, 0, 0, 0, 0, 0, 0, 0, 0};
+  const uint32_t v[8] = {0, 0, 0, 0, 0, 0, 0, 0};
 #pragma unroll
-  for (int i = 0; i < kP; ++i) tc_store16(taddr + 16 * i, v);
+  for (int i = 0; i < 2 * kP; ++i) tc_store8(taddr + 8 * i, v);
 }
 // Where part `part` of the columns 16 ks .. of that operand lies.
 template <int kP>
