@@ -7,7 +7,8 @@
 // P x and a S^T end as bfloat16 values, so P and S enter them as pairs of bfloat16 (16 bits); u . x enters
 // the state, an fp32 result, in three parts (24 bits).
 //
-// Sixteen warps work on rows; one brings the tiles of a chunk to come (TMA), one forms its decays, one issues the products.
+// Eight warps make P and the rows that leave, eight at the same time u . x and the state; one brings the tiles of a chunk
+// to come (TMA), one forms its decays, one issues the products.
 // For the gradients (linattn_grad.cu) the state before each chunk leaves as the tiles that products read, its pair
 // and a third part, by bulk copies. With up to 64 keys
 // the scores of chunk i + 1 are made and decayed while the other products of chunk i run (three stages of
@@ -17,7 +18,7 @@
 namespace linattn {
 namespace {
 
-constexpr int kWorkers = 512, kThreads = kWorkers + 96;
+constexpr int kTeam = 256, kThreads = 2 * kTeam + 96;
 constexpr int kBringWarp = 16, kDecayWarp = 17;  // and 18 issues
 
 template <int KP>
@@ -47,14 +48,14 @@ __global__ void __launch_bounds__(kThreads, 1) chain_kernel(const __grid_constan
   extern __shared__ __align__(1024) unsigned char raw[];
   using M = Smem<KP>;
   M& sm = *reinterpret_cast<M*>(raw);
-  constexpr int kTiles = KP / 32;  // n8 tiles of a warp's quarter of the keys
+  constexpr int kTiles = KP / 16;  // n8 tiles of a warp's half of the keys
   constexpr bool kEarly = M::kEarly;
   constexpr int kSt = M::kStages, kXt = M::kXt;
   enum { kP = 0, kIn = kEarly ? 256 : 128, kO = kIn + 64, kU = kO + 64, kCols = 512 };
-  enum { kBarX = 1, kBarP, kBarX2, kBarOut, kBarFree };
-  constexpr int kPair = kWorkers + 32;
+  enum { kBarX = 1, kBarP, kBarX2, kBarPlanes, kBarFree, kBarOut };
+  constexpr int kPair = kTeam + 32;  // a team and a warp beside it
   const Shape& s = a.s;
-  const int tid = threadIdx.x, lane = tid & 31, warp = __shfl_sync(0xffffffffu, tid >> 5, 0), sub = warp & 3, quarter = warp >> 2;
+  const int tid = threadIdx.x, lane = tid & 31, warp = __shfl_sync(0xffffffffu, tid >> 5, 0), sub = warp & 3, half = warp >> 2 & 1;
   const int slices = (s.V + 63) >> 6, slice = blockIdx.x % slices, hv = blockIdx.x / slices % s.Hv, slot = blockIdx.x / slices / s.Hv;
   const int hk = hv / (s.Hv / s.Hk), v0 = slice * 64, vn = min(64, s.V - v0);
   ChunkAt seg;
@@ -77,7 +78,7 @@ __global__ void __launch_bounds__(kThreads, 1) chain_kernel(const __grid_constan
   auto begin = [&](int i) { return (kUpper ? n - 1 - i : i) * kCT; };  // first token of the i-th chunk, from the segment's
   auto length = [&](int i) { return min(kCT, seg.len - begin(i)); };
 
-  if (warp >= kWorkers / 32) {
+  if (warp >= kBringWarp) {
     Patience wait{a.status};
     if (warp == kDecayWarp) {
       const float* g = s.fixed ? a.g + hv : a.g + tok * s.Hv + hv;
@@ -158,7 +159,7 @@ __global__ void __launch_bounds__(kThreads, 1) chain_kernel(const __grid_constan
         bring(i + kLead);
         brought(i + kLead);
         if (!sums) {
-          meet(kBarOut, kPair);
+          meet(kBarPlanes, kPair);
           leave(i + 1);
         }
         __syncthreads();
@@ -248,12 +249,89 @@ __global__ void __launch_bounds__(kThreads, 1) chain_kernel(const __grid_constan
     return;
   }
 
-  // ------------------------------------------------------------------ rows ---
-  const int row = sub * 32 + lane;
-  bf16_t* out = static_cast<bf16_t*>(kUpper ? a.dv : a.o) + (tok * s.Hv + hv) * s.V + v0;
-  // The state: rows 16 sub .., keys KP / 4 quarter .. in accumulator tiles.
+  Patience wait{a.status};
+  const int team_tid = tid & (kTeam - 1);
+  auto turn = [&] {  // every role's end of a chunk
+    fence_proxy_async_smem();
+    tmem_fence_before_sync();
+    __syncthreads();
+    tmem_fence_after_sync();
+  };
+  if (warp < kTeam / 32) {  // ------------------------------------------------ P, and the rows that leave ---
+    const int row = sub * 32 + lane;
+    bf16_t* out = static_cast<bf16_t*>(kUpper ? a.dv : a.o) + (tok * s.Hv + hv) * s.V + v0;
+    turn();
+    const uint32_t mine = sm.tmem + ((uint32_t)(sub * 32) << 16);
+    // The scores of chunk i, decayed, as pairs.
+    auto score = [&](int i) {
+      const uint32_t at_p = mine + kP + (kEarly ? i % 2 * 128 : 0);
+      wait(&sm.scored, i);
+      tmem_fence_after_sync();
+#pragma unroll 1
+      for (int blk = half; blk < 4; blk += 2) {
+        if (kUpper ? blk >= sub : blk <= sub) {
+          float x[32];
+          tc_read(x, at_p + 32 * blk);
+          decayed<kUpper>(x, sm.d[i % 3], row, blk, s.scale);
+          store_parts<2>(at_p + 32 * blk, x);
+        } else {
+          store_zeros<2>(at_p + 32 * blk);
+        }
+      }
+      wkv7::tmem_wait_st();
+      tmem_fence_before_sync();
+    };
+    if (kEarly) {
+      if (n && !sums) score(0);
+      __syncthreads();
+    }
+    for (int i = 0; i < n; ++i) {
+      if (!sums) {
+        const Decays& d = sm.d[i % 3];
+        bf16_t* stage = sm.stage[i % kSt].a;
+        if (kEarly) {
+          if (i + 1 < n) score(i + 1);
+        } else {
+          score(i);
+          announce(kBarP, kPair);
+        }
+        wait(&sm.out, i);
+        tmem_fence_after_sync();
+        const float w = (kUpper ? d.tail : d.head)[row];
+#pragma unroll
+        for (int h = 0; h < 2; ++h) {
+          float x[16], y[16];
+          tc_read(x, mine + kIn + 32 * half + 16 * h);
+          tc_read(y, mine + kO + 32 * half + 16 * h);
+#pragma unroll
+          for (int p = 0; p < 2; ++p) {
+            uint32_t o[4];
+#pragma unroll
+            for (int j = 0; j < 4; ++j) o[j] = pack2(fmaf(w, x[8 * p + 2 * j], y[8 * p + 2 * j]), fmaf(w, x[8 * p + 2 * j + 1], y[8 * p + 2 * j + 1]));
+            *reinterpret_cast<uint4*>(stage + at(kCT, row, 32 * half + 16 * h + 8 * p)) = make_uint4(o[0], o[1], o[2], o[3]);
+          }
+        }
+        meet(kBarOut, kTeam);
+        const int len = length(i);
+        bf16_t* p = out + (size_t)begin(i) * s.Hv * s.V;
+#pragma unroll
+        for (int e = 0; e < 4; ++e) {
+          const int r = (e * kTeam + team_tid) >> 3, c = (team_tid & 7) * 8;
+          const uint4 v = *reinterpret_cast<const uint4*>(stage + at(kCT, r, c));
+          if (r < len && c < vn) *reinterpret_cast<uint4*>(p + (size_t)r * s.Hv * s.V + c) = v;
+        }
+      }
+      turn();
+    }
+    __syncthreads();
+    if (warp == 0) wkv7::tmem_dealloc(sm.tmem, kCols);
+    return;
+  }
+
+  // ------------------------------------------------------------------ u . x, and the state ---
+  // The state: rows 16 sub .., keys KP / 2 half .. in accumulator tiles.
   float S[kTiles][4];
-  const int s_row = v0 + 16 * sub + (lane >> 2), s_col = quarter * (KP / 4) + 2 * (lane & 3);
+  const int s_row = v0 + 16 * sub + (lane >> 2), s_col = half * (KP / 2) + 2 * (lane & 3);
   float* const states = (kUpper ? a.dstates : a.states) + ((size_t)s_row * s.K + s_col);
   const size_t state = (size_t)s.V * s.K;
   auto each = [&](float* m, auto f) {  // pairs of the state's numbers that exist; m is where its first is
@@ -273,7 +351,7 @@ __global__ void __launch_bounds__(kThreads, 1) chain_kernel(const __grid_constan
     for (int t = 0; t < kTiles; t += 2) {
       Frag<3> f;
       to_a(f, S[t], S[t + 1]);
-      const int o = at(64, 16 * sub + (lane & 15), quarter * (KP / 4) + 8 * t + (lane >> 4) * 8);
+      const int o = at(64, 16 * sub + (lane & 15), half * (KP / 2) + 8 * t + (lane >> 4) * 8);
       stsm4(sm.s + o, f.p[0]);
       stsm4(sm.s + 64 * KP + o, f.p[1]);
       if (plan.keep) stsm4(third + o, f.p[2]);
@@ -290,36 +368,14 @@ __global__ void __launch_bounds__(kThreads, 1) chain_kernel(const __grid_constan
   else if (plan.way == kWhole && init)
     each(init + ends, load);
   planes(sm.stage[kSt - 1].b);
-  fence_proxy_async_smem();
-  tmem_fence_before_sync();
-  __syncthreads();
-  tmem_fence_after_sync();
-  const uint32_t tm = sm.tmem, mine = tm + ((uint32_t)(sub * 32) << 16);
-  Patience wait{a.status};
-  // The scores of chunk i, decayed, as pairs.
-  auto score = [&](int i) {
-    const uint32_t at_p = mine + kP + (kEarly ? i % 2 * 128 : 0);
-    wait(&sm.scored, i);
-    tmem_fence_after_sync();
-    const int blk = quarter;
-    if (kUpper ? blk >= sub : blk <= sub) {
-      float x[32];
-      tc_load32(x, at_p + 32 * blk);
-      tc_loaded32(x);
-      decayed<kUpper>(x, sm.d[i % 3], row, blk, s.scale);
-      store_parts<2>(at_p + 32 * blk, x);
-    } else {
-      store_zeros<2>(at_p + 32 * blk);
-    }
-    wkv7::tmem_wait_st();
-    tmem_fence_before_sync();
-  };
+  turn();
+  const uint32_t mine = sm.tmem + ((uint32_t)(sub * 32) << 16);
   // u . x of half h of the tokens
   auto scaled = [&](int i, int h) {
     const bf16_t* x0 = sm.stage[i % kSt].x;
     const float* u = kUpper ? sm.d[i % 3].head : sm.d[i % 3].tail;
 #pragma unroll 2
-    for (int e = tid; e < kXt * 8; e += kWorkers) {
+    for (int e = team_tid; e < kXt * 8; e += kTeam) {
       const int r = e >> 3;
       float x[8];
       load8(x, x0 + at(kCT, h * kXt + r, (e & 7) * 8));
@@ -333,24 +389,14 @@ __global__ void __launch_bounds__(kThreads, 1) chain_kernel(const __grid_constan
     }
     fence_proxy_async_smem();
   };
-  if (kEarly) {
-    if (n && !sums) score(0);
-    __syncthreads();
-  }
+  if (kEarly) __syncthreads();
   float passed = 1.f;  // the decay of the segment so far
   for (int i = 0; i < n; ++i) {
     const Decays& d = sm.d[i % 3];
-    auto& st = sm.stage[i % kSt];
     wait(&sm.full[i % kSt], i / kSt);
     scaled(i, 0);
     announce(kBarX, kPair);
-    if (kEarly) {
-      if (!sums && i + 1 < n) score(i + 1);
-    } else {
-      if (!sums) {
-        score(i);
-        announce(kBarP, kPair);
-      }
+    if (!kEarly) {
       wait(&sm.first, i);
       scaled(i, 1);
       announce(kBarX2, kPair);
@@ -358,65 +404,31 @@ __global__ void __launch_bounds__(kThreads, 1) chain_kernel(const __grid_constan
     wait(&sm.summed, i);
     tmem_fence_after_sync();
 #pragma unroll
-    for (int t = 0; t < kTiles; t += 2) {
-      float x[2][4];
-      tc_load_tiles(x, mine + kU + quarter * (KP / 4) + 8 * t);
+    for (int t = 0; t < kTiles; t += 4) {
+      float x[4][4];
+      tc_load_tiles(x, mine + kU + half * (KP / 2) + 8 * t);
 #pragma unroll
-      for (int j = 0; j < 2; ++j)
+      for (int j = 0; j < 4; ++j)
 #pragma unroll
         for (int e = 0; e < 4; ++e) S[t + j][e] = fmaf(d.whole, S[t + j][e], x[j][e]);
     }
     passed *= d.whole;
-    if (sums) {
-      tmem_fence_before_sync();
-      __syncthreads();
-      tmem_fence_after_sync();
-      continue;
+    if (!sums) {
+      // (the state's products and copies have read it: the sum was issued after the former)
+      meet(kBarFree, kPair);
+      planes(sm.stage[i % kSt].b);
+      fence_proxy_async_smem();
+      announce(kBarPlanes, kPair);
     }
-    meet(kBarFree, kPair);
-    planes(st.b);
-    wait(&sm.out, i);
-    tmem_fence_after_sync();
-    {
-      float x[16], y[16];
-      tc_load16(x, mine + kIn + 16 * quarter);
-      tc_load16(y, mine + kO + 16 * quarter);
-      tc_loaded16(x);
-      tc_loaded16(y);
-      const float w = (kUpper ? d.tail : d.head)[row];
-#pragma unroll
-      for (int p = 0; p < 2; ++p) {
-        uint32_t o[4];
-#pragma unroll
-        for (int j = 0; j < 4; ++j) o[j] = pack2(fmaf(w, x[8 * p + 2 * j], y[8 * p + 2 * j]), fmaf(w, x[8 * p + 2 * j + 1], y[8 * p + 2 * j + 1]));
-        *reinterpret_cast<uint4*>(st.a + at(kCT, row, 16 * quarter + 8 * p)) = make_uint4(o[0], o[1], o[2], o[3]);
-      }
-    }
-    fence_proxy_async_smem();
-    meet(kBarOut, kPair);
-    {
-      const int len = length(i);
-      bf16_t* p = out + (size_t)begin(i) * s.Hv * s.V;
-#pragma unroll
-      for (int e = 0; e < 2; ++e) {
-        const int r = (e * kWorkers + tid) >> 3, c = (tid & 7) * 8;
-        const uint4 v = *reinterpret_cast<const uint4*>(st.a + at(kCT, r, c));
-        if (r < len && c < vn) *reinterpret_cast<uint4*>(p + (size_t)r * s.Hv * s.V + c) = v;
-      }
-    }
-    fence_proxy_async_smem();
-    tmem_fence_before_sync();
-    __syncthreads();
-    tmem_fence_after_sync();
+    turn();
   }
   float* last = kUpper ? a.dS_init : a.s_final;
   if (plan.way == kWhole && last) each(last + ends, store);
   if (sums) {
     each(states + ((size_t)slot * s.Hv + hv) * state, store);
-    if (tid == 0 && slice == 0) a.decay[(size_t)slot * s.Hv + hv] = passed;
+    if (team_tid == 0 && slice == 0) a.decay[(size_t)slot * s.Hv + hv] = passed;
   }
   __syncthreads();
-  if (warp == 0) wkv7::tmem_dealloc(tm, kCols);
 }
 
 template <int KP, bool kUpper>
