@@ -31,6 +31,7 @@ struct Smem {
   Stage stage[kStages];
   bf16_t xt[3 * kXt * 64];  // u . x
   bf16_t s[2 * 64 * KP];    // the state's pair
+  bf16_t third[kEarly ? 64 * KP : 8];  // its third part; wider keys: in the place of the keys of the chunk before
   Decays d[3];
   uint64_t full[kStages];               // the tiles are there
   uint64_t scored, first, summed, out;  // the scores; the first half of the state's sum, all of it; the rows
@@ -93,8 +94,9 @@ __global__ void __launch_bounds__(kThreads, 1) chain_kernel(const __grid_constan
           make_decays(sm.d[i % 3], x, s.scale, lane);
         }
       };
-      ask(0), make(0), make(1);
+      ask(0), make(0);
       __syncthreads();
+      make(1);
       if (kEarly) __syncthreads();
       for (int i = 0; i < n; ++i) {
         make(i + 2);
@@ -107,15 +109,18 @@ __global__ void __launch_bounds__(kThreads, 1) chain_kernel(const __grid_constan
       constexpr int kLead = kEarly ? 2 : 1;  // chunks ahead
       const CUtensorMap *ma = kUpper ? &maps.k : &maps.q, *mb = kUpper ? &maps.q : &maps.k, *mx = kUpper ? &maps.d : &maps.v;
       const int b_a = kUpper ? s.k_b != 0 : s.q_b != 0, b_b = kUpper ? s.q_b != 0 : s.k_b != 0, b_x = kUpper || s.v_b != 0;
-      auto bring = [&](int i) {
+      auto bring = [&](int i, bool keys) {  // b, or a and x
         if (i < n && lane == 0) {
           auto& st = sm.stage[i % kSt];
           uint64_t* bar = &sm.full[i % kSt];
-          wkv7::mbar_arrive_expect_tx(bar, sums ? sizeof st.b + sizeof st.x : sizeof st);
           const int t = seg.t0 + begin(i);
-          if (!sums) load_tile<KP>(st.a, ma, bar, 0, hk, t, seg.b * b_a);
-          load_tile<KP>(st.b, mb, bar, 0, hk, t, seg.b * b_b);
-          load_tile<64>(st.x, mx, bar, v0, hv, t, seg.b * b_x);
+          if (keys) {
+            load_tile<KP>(st.b, mb, bar, 0, hk, t, seg.b * b_b);
+          } else {
+            wkv7::mbar_arrive_expect_tx(bar, sums ? sizeof st.b + sizeof st.x : sizeof st);
+            if (!sums) load_tile<KP>(st.a, ma, bar, 0, hk, t, seg.b * b_a);
+            load_tile<64>(st.x, mx, bar, v0, hv, t, seg.b * b_x);
+          }
         }
       };
       auto brought = [&](int i) {
@@ -140,23 +145,27 @@ __global__ void __launch_bounds__(kThreads, 1) chain_kernel(const __grid_constan
 #pragma unroll
             for (int c = 0; c < KP / 64; ++c)
               bulk_store(to + (size_t)(part * (KP / 64) + c) * slices * kImagePiece,
-                         (part < 2 ? sm.s + part * 64 * KP : sm.stage[(i + kSt - 1) % kSt].b) + c * 64 * 64, kImagePiece);
+                         (part < 2 ? sm.s + part * 64 * KP : kEarly ? sm.third : sm.stage[(i + kSt - 1) % kSt].b) + c * 64 * 64, kImagePiece);
           bulk_commit();
           to += next;
         }
       };
-      bring(0);
-      if (kEarly) bring(1);
+      bring(0, false), bring(0, true);
+      if (kEarly) bring(1, false), bring(1, true);
       brought(0);
-      if (kEarly) brought(1);
       __syncthreads();
       leave(0);
-      if (kEarly) __syncthreads();
+      if (kEarly) {
+        brought(1);
+        __syncthreads();
+      }
       for (int i = 0; i < n; ++i) {
+        bring(i + kLead, false);
+        if (kEarly) bring(i + kLead, true);
         if (lane == 0) bulk_wait_read();
         __syncwarp();
+        if (!kEarly) bring(i + kLead, true);
         if (!sums) announce(kBarFree, kPair);
-        bring(i + kLead);
         brought(i + kLead);
         if (!sums) {
           meet(kBarPlanes, kPair);
@@ -281,20 +290,18 @@ __global__ void __launch_bounds__(kThreads, 1) chain_kernel(const __grid_constan
       wkv7::tmem_wait_st();
       tmem_fence_before_sync();
     };
-    if (kEarly) {
-      if (n && !sums) score(0);
-      __syncthreads();
-    }
-    for (int i = 0; i < n; ++i) {
+    for (int i = kEarly ? -1 : 0; i < n; ++i) {
       if (!sums) {
-        const Decays& d = sm.d[i % 3];
-        bf16_t* stage = sm.stage[i % kSt].a;
         if (kEarly) {
           if (i + 1 < n) score(i + 1);
         } else {
           score(i);
           announce(kBarP, kPair);
         }
+      }
+      if (!sums && i >= 0) {
+        const Decays& d = sm.d[i % 3];
+        bf16_t* stage = sm.stage[i % kSt].a;
         wait(&sm.out, i);
         tmem_fence_after_sync();
         const float w = (kUpper ? d.tail : d.head)[row];
@@ -367,7 +374,7 @@ __global__ void __launch_bounds__(kThreads, 1) chain_kernel(const __grid_constan
     each(states + ((size_t)slot * s.Hv + hv) * state, load);
   else if (plan.way == kWhole && init)
     each(init + ends, load);
-  planes(sm.stage[kSt - 1].b);
+  planes(kEarly ? sm.third : sm.stage[kSt - 1].b);
   turn();
   const uint32_t mine = sm.tmem + ((uint32_t)(sub * 32) << 16);
   // u . x of half h of the tokens
@@ -416,7 +423,7 @@ __global__ void __launch_bounds__(kThreads, 1) chain_kernel(const __grid_constan
     if (!sums) {
       // (the state's products and copies have read it: the sum was issued after the former)
       meet(kBarFree, kPair);
-      planes(sm.stage[i % kSt].b);
+      planes(kEarly ? sm.third : sm.stage[i % kSt].b);
       fence_proxy_async_smem();
       announce(kBarPlanes, kPair);
     }
