@@ -31,7 +31,7 @@ struct Smem {
   float pairs[4][kCT];     // of a block of 32 rows: the sums over j < t
   float dots[2][kQ][kCT];  // q.(S's part of dq), k.(D's part of dk), by parts of the columns
   float whole[4 * kQ];
-  uint64_t done[2], full[2];  // products; tiles of q and k or of v and do, the state
+  uint64_t done[3], full[2];  // products: scores, rows, of the state's first 64 keys; tiles, the state
   uint32_t tmem;
 };
 
@@ -60,6 +60,7 @@ __global__ void __launch_bounds__(128 * kQ, kQ == 2 ? 2 : 1) grad_kernel(const _
   constexpr int kCols = !kF32 && KP == 64 ? 256 : 512;
   // E; A (bfloat16: in its place); q k^T; then, where what was there has been read, the chunk's and the state's products
   enum { kE = 0, kAt = kF32 ? 128 : 0, kQk = kF32 ? 320 : 128, kOut = kF32 ? 0 : 128, kIn = kF32 ? 64 : 128 + KP };
+  constexpr bool kEarlyIn = !kF32 && KP == 128;  // the state's products have columns of their own
   static_assert(!kF32 || (KP == 64 && VP == 64 && kQ == 4), "fp32 tiles of 64 columns fill shared memory");
   const Shape& s = a.s;
   const int tid = threadIdx.x, lane = tid & 31, warp = __shfl_sync(0xffffffffu, tid >> 5, 0), sub = warp & 3, part_of = warp >> 2;
@@ -70,7 +71,7 @@ __global__ void __launch_bounds__(128 * kQ, kQ == 2 ? 2 : 1) grad_kernel(const _
   const bool dg = a.dg != nullptr;
   if (warp == 0) wkv7::tmem_alloc(&sm.tmem, kCols);
   if (tid == 0) {
-    mbar_init(&sm.done[0], 1), mbar_init(&sm.done[1], 1), mbar_init(&sm.full[0], 1), mbar_init(&sm.full[1], 1);
+    for (uint64_t* b : {sm.done, sm.done + 1, sm.done + 2, sm.full, sm.full + 1}) mbar_init(b, 1);
     wkv7::fence_mbar_init();
   }
   float acc[2][kShared ? kW * kSlices : 1];
@@ -79,7 +80,7 @@ __global__ void __launch_bounds__(128 * kQ, kQ == 2 ? 2 : 1) grad_kernel(const _
 #pragma unroll
     for (int j = 0; j < (kShared ? kW * kSlices : 1); ++j) acc[i][j] = 0.f;
   Patience wait{a.status};
-  uint32_t turn0 = 0, turn1 = 0, turn2 = 0, turn3 = 0, tm = 0;
+  uint32_t turn0 = 0, turn1 = 0, turn2 = 0, turn3 = 0, turn4 = 0, tm = 0;
   __syncthreads();
   // The thread's kW columns of 64 to dq or dk. bfloat16: through shared memory (called by all threads).
   auto leave = [&](T* to, int sl, const float* x) {
@@ -106,6 +107,18 @@ __global__ void __launch_bounds__(128 * kQ, kQ == 2 ? 2 : 1) grad_kernel(const _
     }
   };
   for (int hv = hk * group; hv < hk * group + group; ++hv) {
+    const size_t image = ((size_t)slot * s.Hv + hv) * image_bytes(s.K, s.V);
+    const char *S = static_cast<const char*>(a.images) + image, *D = static_cast<const char*>(a.dimages) + image;
+    // 64 keys of a state. (What was there has been read: the products that did are waited for.)
+    auto fetch = [&](const char* from, int sl) {
+      if (tid == 0) {
+        wkv7::mbar_arrive_expect_tx(&sm.full[1], sizeof sm.s);
+#pragma unroll
+        for (int part = 0; part < 3; ++part)
+          bulk_load(sm.s + part * VP * 64, from + (size_t)(part * kSlices + sl) * VP * 128, VP * 128, &sm.full[1]);
+      }
+    };
+    fetch(S, 0);
     if (!kF32 && tid == 0) {
       const bool all = hv == hk * group;
       wkv7::mbar_arrive_expect_tx(&sm.full[0], (all ? sizeof sm.q + sizeof sm.k : 0) + sizeof sm.v + sizeof sm.d);
@@ -121,8 +134,6 @@ __global__ void __launch_bounds__(128 * kQ, kQ == 2 ? 2 : 1) grad_kernel(const _
       load_decays(r, s.fixed ? a.g + hv : a.g + tok * s.Hv + hv, s.fixed ? 0 : s.Hv, c.len, lane);
       make_decays(sm.dec, r, s.scale, lane);
     }
-    const size_t image = ((size_t)slot * s.Hv + hv) * image_bytes(s.K, s.V);
-    const char *S = static_cast<const char*>(a.images) + image, *D = static_cast<const char*>(a.dimages) + image;
     if constexpr (kF32) {
       if (hv == hk * group) {
         fill_tile<3, kCT>(sm.q, static_cast<const float*>(a.q) + c.b * s.q_b + c.t0 * s.q_t + (size_t)hk * s.K, s.q_t, c.len, s.K, nullptr, tid, kThreads);
@@ -140,7 +151,8 @@ __global__ void __launch_bounds__(128 * kQ, kQ == 2 ? 2 : 1) grad_kernel(const _
     }
     fence_proxy_async_smem();
     tmem_fence_before_sync();
-    __syncthreads();
+    const bool ready = !kF32 && !(s.packed && c.len < kCT);  // the tiles are as they came: the first products need not wait for the decays
+    if (!ready) __syncthreads();
     tmem_fence_after_sync();
     tm = sm.tmem;
     const uint32_t mine = tm + ((uint32_t)(32 * sub) << 16);
@@ -165,16 +177,7 @@ __global__ void __launch_bounds__(128 * kQ, kQ == 2 ? 2 : 1) grad_kernel(const _
         }
         __syncwarp();
       }
-      // 64 keys of the state. (What was there has been read: the products that did are waited for.)
-      auto fetch = [&](int sl) {
-        if (tid == 0) {
-          wkv7::mbar_arrive_expect_tx(&sm.full[1], sizeof sm.s);
-#pragma unroll
-          for (int part = 0; part < 3; ++part)
-            bulk_load(sm.s + part * VP * 64, (kUpper ? D : S) + (size_t)(part * kSlices + sl) * VP * 128, VP * 128, &sm.full[1]);
-        }
-      };
-      // and their part of <S, D>
+      // They are there; their part of <S, D>.
       auto fetched = [&](int sl) {
         wait(&sm.full[1], turn3++);
         if (!kUpper && dg) {
@@ -207,7 +210,15 @@ __global__ void __launch_bounds__(128 * kQ, kQ == 2 ? 2 : 1) grad_kernel(const _
                    product_of(128, 64, false, true), !first || ks > 0);
         });
       };
-      fetch(0);
+      if (kEarlyIn && warp == 0) {
+        wait(&sm.full[1], turn3);
+        if (elected()) {
+          inter(0);
+          tc_commit(&sm.done[2]);
+        }
+        __syncwarp();
+      }
+      if (!kUpper && ready) __syncthreads();  // the decays
       wait(&sm.done[0], turn0++);
       tmem_fence_after_sync();
 #pragma unroll 1
@@ -235,9 +246,11 @@ __global__ void __launch_bounds__(128 * kQ, kQ == 2 ? 2 : 1) grad_kernel(const _
         }
       }
       fetched(0);
+      if (kEarlyIn) wait(&sm.done[2], turn4++);
       wkv7::tmem_wait_st();
       tmem_fence_before_sync();
       __syncthreads();
+      if (kEarlyIn) fetch(kUpper ? D : S, 1);
       if (warp == 0) {
         tmem_fence_after_sync();
         if (elected()) {
@@ -250,28 +263,27 @@ __global__ void __launch_bounds__(128 * kQ, kQ == 2 ? 2 : 1) grad_kernel(const _
                 tc_mma_t(tm + kOut + 64 * sl, tm + kAt + part_at<kA>(ks, p), dx + across(ks) + sl * (kRowPanel >> 4) + r * (kCT * KP * 2 >> 4),
                          product_of(128, 64, false, true), !first || ks > 0);
             });
-          inter(0);
-          tc_commit(&sm.done[1]);
+          if (!kEarlyIn) {
+            inter(0);
+            tc_commit(&sm.done[1]);
+          }
         }
         __syncwarp();
-      }
-      wait(&sm.done[1], turn1++);
-      if (kSlices == 2) {
-        __syncthreads();  // <S, D> has been read
-        fetch(1);
-        fetched(1);
-        tmem_fence_before_sync();
-        __syncthreads();
-        if (warp == 0) {
-          tmem_fence_after_sync();
+        if (kEarlyIn) {
+          wait(&sm.full[1], turn3);
           if (elected()) {
             inter(1);
             tc_commit(&sm.done[1]);
           }
           __syncwarp();
         }
-        wait(&sm.done[1], turn1++);
       }
+      if (kEarlyIn) {
+        fetched(1);
+        if (!kShared) __syncthreads();  // <S, D> has been read: rows take its place
+      }
+      wait(&sm.done[1], turn1++);
+      if (!kUpper && !kEarlyIn && (kShared || kF32)) fetch(D, 0);
       tmem_fence_after_sync();
       const float w = (kUpper ? sm.dec.tail : sm.dec.head)[row];
       float dot = 0.f;
@@ -312,6 +324,7 @@ __global__ void __launch_bounds__(128 * kQ, kQ == 2 ? 2 : 1) grad_kernel(const _
       tmem_fence_before_sync();
       __syncthreads();
       tmem_fence_after_sync();
+      if (!kUpper && (kEarlyIn || !(kShared || kF32))) fetch(D, 0);  // (all threads are done with the place)
     };
     phase(std::false_type{});
     phase(std::true_type{});
