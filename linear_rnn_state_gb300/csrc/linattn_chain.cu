@@ -34,6 +34,7 @@ struct Smem {
   bf16_t third[kEarly ? 64 * KP : 8];  // its third part; wider keys: in the place of the keys of the chunk before
   Decays d[3];
   uint64_t full[kStages];               // the tiles are there
+  uint64_t end;                         // nothing is in flight
   uint64_t scored, first, summed, out;  // the scores; the first half of the state's sum, all of it; the rows
   uint32_t tmem;
 };
@@ -69,7 +70,7 @@ __global__ void __launch_bounds__(kThreads, 1) chain_kernel(const __grid_constan
   }
   if (warp == 0) wkv7::tmem_alloc(&sm.tmem, kCols);
   if (tid == 0) {
-    for (uint64_t* b : {&sm.scored, &sm.first, &sm.summed, &sm.out}) mbar_init(b, 1);
+    for (uint64_t* b : {&sm.scored, &sm.first, &sm.summed, &sm.out, &sm.end}) mbar_init(b, 1);
     for (uint64_t& b : sm.full) mbar_init(&b, 1);
     wkv7::fence_mbar_init();
   }
@@ -174,6 +175,8 @@ __global__ void __launch_bounds__(kThreads, 1) chain_kernel(const __grid_constan
         __syncthreads();
       }
       if (lane == 0) bulk_wait_all();
+      if (!wait.ok)
+        for (int st = 0; st < kSt; ++st) finish_copies(&sm.full[st], (n - st + kSt - 1) / kSt);
       __syncthreads();
       return;
     }
@@ -254,6 +257,7 @@ __global__ void __launch_bounds__(kThreads, 1) chain_kernel(const __grid_constan
       __syncthreads();
       tmem_fence_after_sync();
     }
+    finish_products(&sm.end);
     __syncthreads();
     return;
   }

@@ -17,7 +17,7 @@ struct Smem {
   bf16_t a[3 * kCT * 64], b[3 * kCT * 64], x[3 * kCT * 64], xt[3 * kCT * 64];
   bf16_t s[3 * 64 * 64];
   Decays d[2];
-  uint64_t scored, summed, out;
+  uint64_t scored, summed, out, end;
   uint32_t tmem;
 };
 static_assert(sizeof(Smem) <= 232448, "shared memory of a block");
@@ -49,7 +49,7 @@ __global__ void __launch_bounds__(kThreads, 1) chain32_kernel(const Args a, cons
   }
   if (warp == 0) wkv7::tmem_alloc(&sm.tmem, kCols);
   if (tid == 0) {
-    for (uint64_t* b : {&sm.scored, &sm.summed, &sm.out}) mbar_init(b, 1);
+    for (uint64_t* b : {&sm.scored, &sm.summed, &sm.out, &sm.end}) mbar_init(b, 1);
     wkv7::fence_mbar_init();
   }
   const int n = (seg.len + kCT - 1) / kCT;
@@ -165,6 +165,7 @@ __global__ void __launch_bounds__(kThreads, 1) chain32_kernel(const Args a, cons
       meet(0, kMembers);
       tmem_fence_after_sync();
     }
+    finish_products(&sm.end);
     meet(0, kMembers);
     return;
   }

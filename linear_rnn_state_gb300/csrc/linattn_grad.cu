@@ -31,7 +31,7 @@ struct Smem {
   float pairs[4][kCT];     // of a block of 32 rows: the sums over j < t
   float dots[2][kQ][kCT];  // q.(S's part of dq), k.(D's part of dk), by parts of the columns
   float whole[4 * kQ];
-  uint64_t done[3], full[2];  // products: scores, rows, of the state's first 64 keys; tiles, the state
+  uint64_t done[3], end, full[2];  // products: scores, rows, of the state's first 64 keys; tiles, the state
   uint32_t tmem;
 };
 
@@ -71,7 +71,7 @@ __global__ void __launch_bounds__(128 * kQ, kQ == 2 ? 2 : 1) grad_kernel(const _
   const bool dg = a.dg != nullptr;
   if (warp == 0) wkv7::tmem_alloc(&sm.tmem, kCols);
   if (tid == 0) {
-    for (uint64_t* b : {sm.done, sm.done + 1, sm.done + 2, sm.full, sm.full + 1}) mbar_init(b, 1);
+    for (uint64_t* b : {sm.done, sm.done + 1, sm.done + 2, &sm.end, sm.full, sm.full + 1}) mbar_init(b, 1);
     wkv7::fence_mbar_init();
   }
   float acc[2][kShared ? kW * kSlices : 1];
@@ -373,6 +373,12 @@ __global__ void __launch_bounds__(128 * kQ, kQ == 2 ? 2 : 1) grad_kernel(const _
     for (int i = 0; i < 2; ++i)
 #pragma unroll
       for (int sl = 0; sl < kSlices; ++sl) leave(static_cast<T*>(i ? a.dk : a.dq), sl, acc[i] + kW * sl);
+  }
+  if (warp == 0) {
+    if (!__all_sync(0xffffffffu, wait.ok)) {
+      finish_products(&sm.end);
+      if (lane == 0) finish_copies(&sm.full[0], turn2), finish_copies(&sm.full[1], turn3);
+    }
   }
   __syncthreads();
   if (warp == 0) wkv7::tmem_dealloc(tm, kCols);

@@ -148,6 +148,18 @@ struct Patience {
   }
 };
 
+// Where a wait was given up, before the block ends: no product and (by the thread that started them) no copy is left in
+// flight, a millisecond at most for each.
+constexpr uint64_t kLastWaitNs = 1000000;
+__device__ __forceinline__ void finish_products(uint64_t* bar) {  // by the issuing warp; bar's first use
+  if (elected()) tc_commit(bar);
+  __syncwarp();
+  mbar_wait_bounded(nullptr, bar, 0, kLastWaitNs);
+}
+__device__ __forceinline__ void finish_copies(uint64_t* bar, uint32_t phases) {  // bar had so many phases
+  if (phases) mbar_wait_bounded(nullptr, bar, (phases - 1) & 1, kLastWaitNs);
+}
+
 // ---------------------------------------------------------------- copies ---
 
 // kCols columns of a tile from token t on; the bytes that will arrive.
