@@ -238,7 +238,7 @@ __global__ void __launch_bounds__(kThreads) forward_kernel(const Args p, unsigne
   float2 w[4];
   weights(w, x.key ? p.wk : p.wq, c, p.D);
   const unsigned t0 = u0 / per;
-  fill_table(table, p, t0, min(u0 + kGroups, units) == 0 ? t0 : (min(u0 + kGroups, units) - 1) / per);
+  fill_table(table, p, t0, (min(u0 + kGroups, units) - 1) / per);
   __syncthreads();
   const float2* cs = table + (x.tok - t0) * p.half;
   Turn<kHow> turn;

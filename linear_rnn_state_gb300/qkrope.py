@@ -65,8 +65,8 @@ def _inputs(q, k, q_weight, k_weight, freq, positions):
     if positions is not None and not (positions.shape == qs[:-2] and positions.dtype is torch.int32 and positions.device == dev
                                       and positions.is_contiguous()):
         _check_tensor("positions", positions, qs[:-2], torch.int32, dev)
-    tokens, qt = _rows("q", q, 2)
-    return bf16, (qt, _rows("k", k, 2)[1], tokens, qs[-3], qs[-2], ks[-2], D, half), dev
+    (nq, qt), (nk, kt) = _rows("q", q, 2), _rows("k", k, 2)
+    return bf16, (qt, kt, max(nq, nk), qs[-3], qs[-2], ks[-2], D, half), dev  # (without heads a tensor has no rows)
 
 
 def forward(q, k, q_weight, k_weight, freq, positions=None, *, interleaved: bool = False, eps: float = 1e-6, stream=None):
