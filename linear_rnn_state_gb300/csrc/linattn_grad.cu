@@ -21,17 +21,19 @@
 namespace linattn {
 namespace {
 
-template <typename T, int KP, int VP, int kQ>
+constexpr int kAtOnce = 152;  // SMs
+
+template <typename T, int KP, int VP, int kQ, int kDecays>
 struct Smem {
   static constexpr int kN = In<T>::kParts;
   bf16_t q[kN * kCT * KP], k[kN * kCT * KP], v[kN * kCT * VP], d[kN * kCT * VP];
   bf16_t s[3 * VP * 64];  // 64 keys of S or D; then (bfloat16) rows on their way out
-  Decays dec;
+  Decays dec[kDecays];
   float total[3][kCT];     // of a row's A_ij (q_i.k_j), by blocks of 32 columns
   float pairs[4][kCT];     // of a block of 32 rows: the sums over j < t
   float dots[2][kQ][kCT];  // q.(S's part of dq), k.(D's part of dk), by parts of the columns
   float whole[4 * kQ];
-  uint64_t done[3], end, full[2];  // products: scores, rows, of the state's first 64 keys; tiles, the state
+  uint64_t done[4], end, full[2];  // products: scores, rows, of the state's first 64 keys, q k^T; tiles, the state
   uint32_t tmem;
 };
 
@@ -51,15 +53,22 @@ __device__ __forceinline__ float warp_sum(float x) {
   return x;
 }
 
+// Of heads that share keys the next one's decays are made while dg of the last is added up, where a second set of
+// them fits.
+template <typename T, bool kShared>
+constexpr int kDecaySets = kShared && sizeof(T) == 2 ? 2 : 1;
+
 template <typename T, int KP, int VP, bool kShared, int kQ>
 __global__ void __launch_bounds__(128 * kQ, kQ == 2 ? 2 : 1) grad_kernel(const __grid_constant__ Maps maps, const Args a) {
   extern __shared__ __align__(1024) unsigned char raw[];
-  Smem<T, KP, VP, kQ>& sm = *reinterpret_cast<Smem<T, KP, VP, kQ>*>(raw);
+  using M = Smem<T, KP, VP, kQ, kDecaySets<T, kShared>>;
+  M& sm = *reinterpret_cast<M*>(raw);
   constexpr bool kF32 = sizeof(T) == 4;
   constexpr int kThreads = 128 * kQ, kSlices = KP / 64, kN = In<T>::kParts, kA = kF32 ? 3 : 2, kW = 64 / kQ;
   constexpr int kCols = !kF32 && KP == 64 ? 256 : 512;
-  // E; A (bfloat16: in its place); q k^T; then, where what was there has been read, the chunk's and the state's products
-  enum { kE = 0, kAt = kF32 ? 128 : 0, kQk = kF32 ? 320 : 128, kOut = kF32 ? 0 : 128, kIn = kF32 ? 64 : 128 + KP };
+  // E of dq and of dk; A (bfloat16: in its place); q k^T; then, where what was there has been read, the chunk's and the
+  // state's products
+  enum { kE = 0, kQk = kF32 ? 320 : 128, kE2 = kF32 ? kQk : kE, kAt = kF32 ? 128 : 0, kOut = kF32 ? 0 : 128, kIn = kF32 ? 64 : 128 + KP };
   constexpr bool kEarlyIn = !kF32 && KP == 128;  // the state's products have columns of their own
   static_assert(!kF32 || (KP == 64 && VP == 64 && kQ == 4), "fp32 tiles of 64 columns fill shared memory");
   const Shape& s = a.s;
@@ -71,7 +80,7 @@ __global__ void __launch_bounds__(128 * kQ, kQ == 2 ? 2 : 1) grad_kernel(const _
   const bool dg = a.dg != nullptr;
   if (warp == 0) wkv7::tmem_alloc(&sm.tmem, kCols);
   if (tid == 0) {
-    for (uint64_t* b : {sm.done, sm.done + 1, sm.done + 2, &sm.end, sm.full, sm.full + 1}) mbar_init(b, 1);
+    for (uint64_t* b : {sm.done, sm.done + 1, sm.done + 2, sm.done + 3, &sm.end, sm.full, sm.full + 1}) mbar_init(b, 1);
     wkv7::fence_mbar_init();
   }
   float acc[2][kShared ? kW * kSlices : 1];
@@ -80,16 +89,29 @@ __global__ void __launch_bounds__(128 * kQ, kQ == 2 ? 2 : 1) grad_kernel(const _
 #pragma unroll
     for (int j = 0; j < (kShared ? kW * kSlices : 1); ++j) acc[i][j] = 0.f;
   Patience wait{a.status};
-  uint32_t turn0 = 0, turn1 = 0, turn2 = 0, turn3 = 0, turn4 = 0, tm = 0;
+  uint32_t turn0 = 0, turn1 = 0, turn2 = 0, turn3 = 0, turn4 = 0, turn5 = 0, tm = 0;
   __syncthreads();
-  // The thread's kW columns of 64 to dq or dk. bfloat16: through shared memory (called by all threads).
-  auto leave = [&](T* to, int sl, const float* x) {
+  // The thread's kW columns of 64 to dq or dk (called by all threads). fp32: four lanes exchange four columns each, and a
+  // store is of 64 bytes of eight rows instead of 16 of 32. bfloat16: through shared memory.
+  auto leave = [&](T* to, int sl, float* x) {
     T* p = to + (tok * s.Hk + hk) * s.K + 64 * sl;
     if constexpr (kF32) {
 #pragma unroll
-      for (int j = 0; j < kW; j += 4)
-        if (row < c.len && 64 * sl + kW * part_of + j < s.K)
-          *reinterpret_cast<float4*>(p + (size_t)row * s.Hk * s.K + kW * part_of + j) = make_float4(x[j], x[j + 1], x[j + 2], x[j + 3]);
+      for (int n = 1; n < 4; n *= 2)
+#pragma unroll
+        for (int j = 0; j < 16; ++j)
+          if (!(j & 4 * n)) {
+            const bool up = lane & n;
+            float &lo = x[j], &hi = x[j + 4 * n];
+            const float got = __shfl_xor_sync(0xffffffffu, up ? lo : hi, n);
+            (up ? lo : hi) = got;
+          }
+      const int col = 16 * part_of + 4 * (lane & 3);
+#pragma unroll
+      for (int j = 0; j < 4; ++j) {
+        const int r = (row & ~3) + j;
+        if (r < c.len && col < s.K) *reinterpret_cast<float4*>(p + (size_t)r * s.Hk * s.K + col) = make_float4(x[4 * j], x[4 * j + 1], x[4 * j + 2], x[4 * j + 3]);
+      }
     } else {
 #pragma unroll
       for (int j = 0; j < kW; j += 8)
@@ -106,52 +128,131 @@ __global__ void __launch_bounds__(128 * kQ, kQ == 2 ? 2 : 1) grad_kernel(const _
       __syncthreads();
     }
   };
-  for (int hv = hk * group; hv < hk * group + group; ++hv) {
-    const size_t image = ((size_t)slot * s.Hv + hv) * image_bytes(s.K, s.V);
-    const char *S = static_cast<const char*>(a.images) + image, *D = static_cast<const char*>(a.dimages) + image;
-    // 64 keys of a state. (What was there has been read: the products that did are waited for.)
-    auto fetch = [&](const char* from, int sl) {
-      if (tid == 0) {
-        wkv7::mbar_arrive_expect_tx(&sm.full[1], sizeof sm.s);
+  const int first = hk * group, last = first + group - 1;
+  auto image_of = [&](const void* images, int hv) {
+    return static_cast<const char*>(images) + ((size_t)slot * s.Hv + hv) * image_bytes(s.K, s.V);
+  };
+  // 64 keys of a state. (What was there has been read: the products that did are waited for.)
+  auto fetch = [&](const char* from, int sl) {
+    if (tid == 0) {
+      wkv7::mbar_arrive_expect_tx(&sm.full[1], sizeof sm.s);
 #pragma unroll
-        for (int part = 0; part < 3; ++part)
-          bulk_load(sm.s + part * VP * 64, from + (size_t)(part * kSlices + sl) * VP * 128, VP * 128, &sm.full[1]);
-      }
-    };
-    fetch(S, 0);
+      for (int part = 0; part < 3; ++part)
+        bulk_load(sm.s + part * VP * 64, from + (size_t)(part * kSlices + sl) * VP * 128, VP * 128, &sm.full[1]);
+    }
+  };
+  // The state before the chunk and (bfloat16) the tiles of a value head.
+  auto begin = [&](int hv) {
+    fetch(image_of(a.images, hv), 0);
     if (!kF32 && tid == 0) {
-      const bool all = hv == hk * group;
-      wkv7::mbar_arrive_expect_tx(&sm.full[0], (all ? sizeof sm.q + sizeof sm.k : 0) + sizeof sm.v + sizeof sm.d);
-      if (all) {
+      wkv7::mbar_arrive_expect_tx(&sm.full[0], (hv == first ? sizeof sm.q + sizeof sm.k : 0) + sizeof sm.v + sizeof sm.d);
+      load_tile<VP>(sm.v, &maps.v, &sm.full[0], 0, hv, c.t0, s.v_b ? c.b : 0);
+      load_tile<VP>(sm.d, &maps.d, &sm.full[0], 0, hv, c.t0, c.b);
+      if (hv == first) {
         load_tile<KP>(sm.q, &maps.q, &sm.full[0], 0, hk, c.t0, s.q_b ? c.b : 0);
         load_tile<KP>(sm.k, &maps.k, &sm.full[0], 0, hk, c.t0, s.k_b ? c.b : 0);
       }
-      load_tile<VP>(sm.v, &maps.v, &sm.full[0], 0, hv, c.t0, s.v_b ? c.b : 0);
-      load_tile<VP>(sm.d, &maps.d, &sm.full[0], 0, hv, c.t0, c.b);
+    }
+  };
+  // fp32: what the block that takes this one's place will read first, into the L2, by one of `of` warps: the memory is
+  // read while the products run instead of by all blocks of the next wave at once (8 x 4096 x 12 x 64: 386 -> 362 us;
+  // bfloat16, with half the bytes a chunk, loses by it: 4 x 4096 x 32 x 64 176 -> 186).
+  auto ahead = [&](int who, int of) {
+    const unsigned next = blockIdx.x + kAtOnce;
+    ChunkAt n;
+    if (next >= gridDim.x || !chunk_at(s, (int)(next / s.Hk), kCT, n)) return;
+    const int k_head = (int)(next % s.Hk), v_head = k_head * group;
+    auto rows = [&](const void* base, long long offset, long long stride, int cols) {
+      for (int r = 32 * who + lane; r < n.len; r += 32 * of)
+        for (int x = 0; x < cols; x += 128 / (int)sizeof(T))
+          asm volatile("prefetch.global.L2 [%0];" ::"l"(static_cast<const T*>(base) + offset + r * stride + x));
+    };
+    rows(a.v, n.b * s.v_b + n.t0 * s.v_t + (long long)v_head * s.V, s.v_t, s.V);
+    rows(a.d_o, (((long long)n.b * s.T + n.t0) * s.Hv + v_head) * s.V, (long long)s.Hv * s.V, s.V);
+    rows(a.q, n.b * s.q_b + n.t0 * s.q_t + (long long)k_head * s.K, s.q_t, s.K);
+    rows(a.k, n.b * s.k_b + n.t0 * s.k_t + (long long)k_head * s.K, s.k_t, s.K);
+    const char* S = static_cast<const char*>(a.images) + ((size_t)(next / s.Hk) * s.Hv + v_head) * image_bytes(s.K, s.V);
+    for (int i = 32 * who + lane; i < 3 * VP; i += 32 * of)
+      asm volatile("prefetch.global.L2 [%0];" ::"l"(S + ((size_t)(i / VP) * kSlices * VP + i % VP) * 128));
+  };
+  begin(first);
+  for (int hv = first; hv <= last; ++hv) {
+    const char *S = image_of(a.images, hv), *D = image_of(a.dimages, hv);
+    Decays& dec = sm.dec[(hv - first) % kDecaySets<T, kShared>];
+    // fp32: all values on their way at once, 16 of a tile a thread
+    float4 raw_q[4], raw_k[4], raw_v[4], raw_d[4];
+    auto bring = [&](float4 (&x)[4], const void* base, long long offset, long long stride, int cols) {
+#pragma unroll
+      for (int e = 0; e < 2; ++e) {
+        const int r = (tid >> 3) + 64 * e, col = (tid & 7) * 8;
+        const float4* from = reinterpret_cast<const float4*>(static_cast<const float*>(base) + offset + r * stride + col);
+        const bool in = r < c.len && col < cols;
+        x[2 * e] = in ? __ldg(from) : make_float4(0.f, 0.f, 0.f, 0.f), x[2 * e + 1] = in ? __ldg(from + 1) : make_float4(0.f, 0.f, 0.f, 0.f);
+      }
+    };
+    auto place = [&](bf16_t* tile, const float4 (&x)[4]) {
+#pragma unroll
+      for (int e = 0; e < 2; ++e) {
+        const float4 lo = x[2 * e], hi = x[2 * e + 1];
+        const float y[8] = {lo.x, lo.y, lo.z, lo.w, hi.x, hi.y, hi.z, hi.w};
+        put8<3>(tile + at(kCT, (tid >> 3) + 64 * e, (tid & 7) * 8), kCT * 64, y);
+      }
+    };
+    if constexpr (kF32) {
+      bring(raw_v, a.v, c.b * s.v_b + c.t0 * s.v_t + (long long)hv * s.V, s.v_t, s.V);
+      bring(raw_d, a.d_o, (tok * s.Hv + hv) * s.V, (long long)s.Hv * s.V, s.V);
+      if (hv == first) {
+        bring(raw_q, a.q, c.b * s.q_b + c.t0 * s.q_t + (long long)hk * s.K, s.q_t, s.K);
+        bring(raw_k, a.k, c.b * s.k_b + c.t0 * s.k_t + (long long)hk * s.K, s.k_t, s.K);
+      }
     }
     if (warp == 4 * kQ - 1) {
       float r[4];
       load_decays(r, s.fixed ? a.g + hv : a.g + tok * s.Hv + hv, s.fixed ? 0 : s.Hv, c.len, lane);
-      make_decays(sm.dec, r, s.scale, lane);
+      make_decays(dec, r, s.scale, lane);
     }
-    if constexpr (kF32) {
-      if (hv == hk * group) {
-        fill_tile<3, kCT>(sm.q, static_cast<const float*>(a.q) + c.b * s.q_b + c.t0 * s.q_t + (size_t)hk * s.K, s.q_t, c.len, s.K, nullptr, tid, kThreads);
-        fill_tile<3, kCT>(sm.k, static_cast<const float*>(a.k) + c.b * s.k_b + c.t0 * s.k_t + (size_t)hk * s.K, s.k_t, c.len, s.K, nullptr, tid, kThreads);
+    // A product of two tiles along their rows, in tensor memory from column `to` on.
+    auto scores = [&](uint32_t to, const bf16_t* ta, const bf16_t* tb, auto cols) {
+      constexpr int D = decltype(cols)::value;
+      const uint64_t da = desc(ta), db = desc(tb);
+      terms<kN, kN>([&](int p, int r, bool start) {
+#pragma unroll
+        for (int ks = 0; ks < D / 16; ++ks)
+          tc_mma(tm + to, da + along<kCT>(ks) + p * (kCT * D * 2 >> 4), db + along<kCT>(ks) + r * (kCT * D * 2 >> 4),
+                 product_of(128, 128, false, false), !start || ks > 0);
+      });
+    };
+    using Keys = std::integral_constant<int, KP>;
+    using Values = std::integral_constant<int, VP>;
+    auto first_products = [&] {
+      if (warp == 0) {
+        if (elected()) {
+          scores(kE, sm.d, sm.v, Values{});
+          tc_commit(&sm.done[0]);
+        }
+        __syncwarp();
       }
-      fill_tile<3, kCT>(sm.v, static_cast<const float*>(a.v) + c.b * s.v_b + c.t0 * s.v_t + (size_t)hv * s.V, s.v_t, c.len, s.V, nullptr, tid, kThreads);
-      fill_tile<3, kCT>(sm.d, static_cast<const float*>(a.d_o) + (tok * s.Hv + hv) * s.V, (long long)s.Hv * s.V, c.len, s.V, nullptr, tid, kThreads);
+    };
+    const bool ready = !kF32 && !(s.packed && c.len < kCT);  // the tiles are as they came: the first products need not wait for the decays
+    if constexpr (kF32) {
+      place(sm.v, raw_v), place(sm.d, raw_d);
+      fence_proxy_async_smem();
+      tmem_fence_before_sync();
+      __syncthreads();
+      tmem_fence_after_sync();
+      tm = sm.tmem;
+      first_products();
+      if (hv == first) place(sm.q, raw_q), place(sm.k, raw_k);
     } else {
       wait(&sm.full[0], turn2++);
-    }
-    if (!kF32 && s.packed && c.len < kCT) {
-      if (hv == hk * group) clear_rows<KP>(sm.q, c.len, tid, kThreads), clear_rows<KP>(sm.k, c.len, tid, kThreads);
-      clear_rows<VP>(sm.v, c.len, tid, kThreads);
-      clear_rows<VP>(sm.d, c.len, tid, kThreads);
+      if (!ready) {
+        if (hv == first) clear_rows<KP>(sm.q, c.len, tid, kThreads), clear_rows<KP>(sm.k, c.len, tid, kThreads);
+        clear_rows<VP>(sm.v, c.len, tid, kThreads);
+        clear_rows<VP>(sm.d, c.len, tid, kThreads);
+      }
     }
     fence_proxy_async_smem();
     tmem_fence_before_sync();
-    const bool ready = !kF32 && !(s.packed && c.len < kCT);  // the tiles are as they came: the first products need not wait for the decays
     if (!ready) __syncthreads();
     tmem_fence_after_sync();
     tm = sm.tmem;
@@ -159,23 +260,16 @@ __global__ void __launch_bounds__(128 * kQ, kQ == 2 ? 2 : 1) grad_kernel(const _
     float whole = 0.f;
     auto phase = [&](auto upper) {
       constexpr bool kUpper = decltype(upper)::value;
-      const bf16_t *ta = kUpper ? sm.v : sm.d, *tb = kUpper ? sm.d : sm.v, *tx = kUpper ? sm.q : sm.k, *td = kUpper ? sm.k : sm.q;
-      if (warp == 0) {
-        if (elected()) {
-          auto rows = [&](uint32_t at_d, uint64_t da, uint64_t db, auto cols) {
-            constexpr int D = decltype(cols)::value;
-            terms<kN, kN>([&](int p, int r, bool first) {
-#pragma unroll
-              for (int ks = 0; ks < D / 16; ++ks)
-                tc_mma(tm + at_d, da + along<kCT>(ks) + p * (kCT * D * 2 >> 4), db + along<kCT>(ks) + r * (kCT * D * 2 >> 4),
-                       product_of(128, 128, false, false), !first || ks > 0);
-            });
-          };
-          rows(kE, desc(ta), desc(tb), std::integral_constant<int, VP>{});
-          if (!kUpper && dg) rows(kQk, desc(sm.q), desc(sm.k), std::integral_constant<int, KP>{});
-          tc_commit(&sm.done[0]);
+      const bf16_t *ta = kUpper ? sm.v : sm.d, *tx = kUpper ? sm.q : sm.k, *td = kUpper ? sm.k : sm.q;
+      if (!kUpper) {
+        if (!kF32) first_products();
+        if (dg && warp == 0) {
+          if (elected()) {
+            scores(kQk, sm.q, sm.k, Keys{});
+            tc_commit(&sm.done[3]);
+          }
+          __syncwarp();
         }
-        __syncwarp();
       }
       // They are there; their part of <S, D>.
       auto fetched = [&](int sl) {
@@ -218,18 +312,22 @@ __global__ void __launch_bounds__(128 * kQ, kQ == 2 ? 2 : 1) grad_kernel(const _
         }
         __syncwarp();
       }
+      if (!kUpper && kF32) fetched(0);  // (while the products of parts run)
       if (!kUpper && ready) __syncthreads();  // the decays
       wait(&sm.done[0], turn0++);
       tmem_fence_after_sync();
+      if (kF32 && !kUpper && hv == first && sub == 0 && part_of) ahead(part_of - 1, kQ - 1);  // (these have nothing else to do now)
 #pragma unroll 1
       for (int blk = part_of; blk < 4; blk += kQ) {
         if (kUpper ? blk >= sub : blk <= sub) {
           float x[32];
-          tc_read(x, mine + kE + 32 * blk);
-          decayed<kUpper>(x, sm.dec, row, blk, s.scale);
+          tc_read(x, mine + (kUpper ? kE2 : kE) + 32 * blk);
+          decayed<kUpper>(x, dec, row, blk, s.scale);
           store_parts<kA>(mine + kAt + 16 * kA * blk, x);
           if (!kUpper && dg) {
             float y[32], run = 0.f;
+            wait(&sm.done[3], turn5);
+            tmem_fence_after_sync();
             tc_read(y, mine + kQk + 32 * blk);
 #pragma unroll
             for (int j = 0; j < 32; ++j) {
@@ -245,7 +343,8 @@ __global__ void __launch_bounds__(128 * kQ, kQ == 2 ? 2 : 1) grad_kernel(const _
           store_zeros<kA>(mine + kAt + 16 * kA * blk);
         }
       }
-      fetched(0);
+      if (kUpper || !kF32) fetched(0);
+      if (!kUpper && dg) ++turn5;
       if (kEarlyIn) wait(&sm.done[2], turn4++);
       wkv7::tmem_wait_st();
       tmem_fence_before_sync();
@@ -283,9 +382,17 @@ __global__ void __launch_bounds__(128 * kQ, kQ == 2 ? 2 : 1) grad_kernel(const _
         if (!kShared) __syncthreads();  // <S, D> has been read: rows take its place
       }
       wait(&sm.done[1], turn1++);
-      if (!kUpper && !kEarlyIn && (kShared || kF32)) fetch(D, 0);
       tmem_fence_after_sync();
-      const float w = (kUpper ? sm.dec.tail : sm.dec.head)[row];
+      if (!kUpper && !kEarlyIn && (kShared || kF32)) fetch(D, 0);
+      if (!kUpper && warp == 0) {  // (where A was, or q k^T: both have been read)
+        if (elected()) {
+          scores(kE2, sm.v, sm.d, Values{});
+          tc_commit(&sm.done[0]);
+        }
+        __syncwarp();
+      }
+      if (kUpper && kShared && hv < last) begin(hv + 1);  // (the products that read v, do and D are done)
+      const float w = (kUpper ? dec.tail : dec.head)[row];
       float dot = 0.f;
 #pragma unroll
       for (int sl = 0; sl < kSlices; ++sl) {
@@ -363,9 +470,9 @@ __global__ void __launch_bounds__(128 * kQ, kQ == 2 ? 2 : 1) grad_kernel(const _
         float pass = 0.f;
 #pragma unroll
         for (int i = 0; i < 4 * kQ; ++i) pass += sm.whole[i];
-        if (t < c.len) a.dg[(tok + t) * s.Hv + hv] = ((from + later) + (upto + before)) + (pairs + sm.dec.whole * pass);
+        if (t < c.len) a.dg[(tok + t) * s.Hv + hv] = ((from + later) + (upto + before)) + (pairs + dec.whole * pass);
       }
-      if (kShared) __syncthreads();
+      if (kShared && kDecaySets<T, kShared> == 1) __syncthreads();
     }
   }
   if (kShared) {
@@ -388,7 +495,7 @@ template <typename T, int KP, int VP, bool kShared>
 cudaError_t launch(const Maps& maps, const Args& a, cudaStream_t stream) {
   // two blocks of 256 threads an SM where they fit, else one of 512
   constexpr int kQ = sizeof(T) == 2 && KP == 64 && VP == 64 && !kShared ? 2 : 4;
-  using M = Smem<T, KP, VP, kQ>;
+  using M = Smem<T, KP, VP, kQ, kDecaySets<T, kShared>>;
   static_assert(sizeof(M) <= 232448, "shared memory of a block");
   static std::atomic<unsigned long long> done{0};
   const cudaError_t e = allow_smem(reinterpret_cast<const void*>(grad_kernel<T, KP, VP, kShared, kQ>), sizeof(M), done);
