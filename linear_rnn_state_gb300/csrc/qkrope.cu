@@ -23,7 +23,7 @@
 namespace qkrope {
 namespace {
 
-constexpr int kThreads = 256, kSumThreads = 256;
+constexpr int kThreads = 256, kSumThreads = 1024;
 enum How { kInterleaved, kHalves, kOddHalves };
 typedef __nv_bfloat16 bf16_t;
 
@@ -61,6 +61,12 @@ __device__ __forceinline__ float group_sum(float x) {
 #pragma unroll
   for (int o = 1; o < kGroup; o <<= 1) x += __shfl_xor_sync(0xffffffffu, x, o);
   return x;
+}
+
+// 1 / sqrt(x) by a step of Newton's from the fast one. (0, and what is so small that the fast one overflows, stays as it gives.)
+__device__ __forceinline__ float inverse_root(float x) {
+  const float r = rsqrtf(x), y = fmaf(0.5f * r, fmaf(-x * r, r, 1.f), r);
+  return x > 1e-37f && x < 1e37f ? y : r;
 }
 
 // freq / (2 pi) modulo 1 as a 64-bit fraction: freq = m 2^e, m of 53 bits, times 2^66 / (2 pi), by integers.
@@ -218,7 +224,7 @@ template <int kHow>
 constexpr int kRowBytes = kHow == kOddHalves ? kThreads * 8 * 4 : 0;
 
 template <typename T, int kHow, int kGroup, int kIter>
-__global__ void __launch_bounds__(kThreads) forward_kernel(const Args p, unsigned units) {
+__global__ void __launch_bounds__(kThreads, kIter == 8 ? 3 : 4) forward_kernel(const Args p, unsigned units) {
   extern __shared__ __align__(16) unsigned char smem[];
   constexpr int kGroups = kThreads / kGroup;
   float2* table = reinterpret_cast<float2*>(smem + kRowBytes<kHow>);
@@ -250,7 +256,7 @@ __global__ void __launch_bounds__(kThreads) forward_kernel(const Args p, unsigne
     values(v, raw[i]);
 #pragma unroll
     for (int e = 0; e < 4; ++e) s2 = fma2(v[e], v[e], s2);
-    const float r = 1.f / sqrtf(fmaf(group_sum<kGroup>(s2.x + s2.y), inv, p.eps));
+    const float r = inverse_root(fmaf(group_sum<kGroup>(s2.x + s2.y), inv, p.eps));
 #pragma unroll
     for (int e = 0; e < 4; ++e) v[e] = mul2(mul2(v[e], make_float2(r, r)), w[e]);
     rotate<kHow, kGroup, false>(v, turn, cs, c, p.half, lane, line);
@@ -304,7 +310,7 @@ __global__ void __launch_bounds__(kThreads, 2) backward_kernel(const Args p, uns
       rotate<kHow, kGroup, true>(d, turn, cs, c, p.half, lane, line);
 #pragma unroll
       for (int e = 0; e < 4; ++e) s2 = fma2(v[e], v[e], s2), c1 = fma2(mul2(d[e], w[e]), v[e], c1);
-      const float r = 1.f / sqrtf(fmaf(group_sum<kGroup>(s2.x + s2.y), inv, p.eps));
+      const float r = inverse_root(fmaf(group_sum<kGroup>(s2.x + s2.y), inv, p.eps));
       const float m = -(group_sum<kGroup>(c1.x + c1.y) * r * inv);
       const float2 rr = make_float2(r, r), mm = make_float2(m, m);
 #pragma unroll
@@ -341,18 +347,21 @@ __global__ void __launch_bounds__(kThreads, 2) backward_kernel(const Args p, uns
   }
 }
 
-// The partial rows' sums, column by column: 32 columns a block, eight threads each.
+// The partial rows' sums, column by column: 32 columns a block, 32 threads each, whose loads are on their way together.
 __global__ void __launch_bounds__(kSumThreads) sums_kernel(const Args p, int parts) {
-  __shared__ float red[8][33];
+  __shared__ float red[32][33];
+  constexpr int kMost = (kParts + 31) / 32;
   const int x = threadIdx.x & 31, y = threadIdx.x >> 5, c = blockIdx.x * 32 + x, n = 2 * p.D;
-  float s = 0.f;
-  if (c < n)
-    for (int q = y; q < parts; q += 8) s += p.part[(size_t)q * n + c];
+  float v[kMost], s = 0.f;
+#pragma unroll
+  for (int i = 0; i < kMost; ++i) v[i] = c < n && y + 32 * i < parts ? p.part[(size_t)(y + 32 * i) * n + c] : 0.f;
+#pragma unroll
+  for (int i = 0; i < kMost; ++i) s += v[i];
   red[y][x] = s;
   __syncthreads();
   if (y == 0 && c < n) {
 #pragma unroll
-    for (int q = 1; q < 8; ++q) s += red[q][x];
+    for (int q = 1; q < 32; ++q) s += red[q][x];
     if (c < p.D)
       p.dwq[c] = s;
     else
@@ -361,10 +370,12 @@ __global__ void __launch_bounds__(kSumThreads) sums_kernel(const Args p, int par
 }
 
 int group_of(int D) { return D <= 32 ? 4 : D <= 64 ? 8 : D <= 128 ? 16 : 32; }
-// Heads of a unit: four where the units that hold fewer are few and there are units enough for the GPU, else two or
-// one (cosines, sines and weights are fetched once a unit; see the kernels' head).
-int heads_of(const Args& p, long long tokens) {
-  for (int n : {4, 2}) {
+// Heads of a unit, `most` of them where the units that hold fewer are few and there are units enough for the GPU, else
+// a half, a quarter or an eighth as many: what a unit costs besides its rows (its place, cosines, sines and weights) is 1.4 heads of
+// bfloat16's forward (16384 x 64 x 64: 97, 68, 51 and 48 us with 1, 2, 4 and 8 heads; backward 135, 110 and 87 with 1, 2 and 4)
+// and 0.4 of fp32's (32768 x 24 x 64: 74 and 63 us with 1 and 2). More would not fit the registers.
+int heads_of(const Args& p, long long tokens, int most) {
+  for (int n = most; n > 1; n /= 2) {
     const long long units = (long long)((p.Hq + n - 1) / n) + (p.Hk + n - 1) / n;
     if (units * n <= 5 * (p.Hq + p.Hk) / 4 && tokens * units >= 152 * 4 * (kThreads / group_of(p.D))) return n;
   }
@@ -385,24 +396,29 @@ cudaError_t run(const Args& p, bool backward, cudaStream_t s) {
   constexpr int kGroups = kThreads / kGroup;
   const unsigned units = units_in(p, kIter);
   const size_t smem = kRowBytes<kHow> + table_bytes(p, kGroups, kIter);
+  const unsigned blocks = (units + kGroups - 1) / kGroups;
   if (!backward) {
-    forward_kernel<T, kHow, kGroup, kIter><<<(units + kGroups - 1) / kGroups, kThreads, smem, s>>>(p, units);
+    forward_kernel<T, kHow, kGroup, kIter><<<blocks, kThreads, smem, s>>>(p, units);
     return cudaGetLastError();
   }
-  const unsigned blocks = (units + kGroups - 1) / kGroups, parts = blocks < (unsigned)kParts ? blocks : kParts;
-  backward_kernel<T, kHow, kGroup, kIter><<<parts, kThreads, smem, s>>>(p, units);
-  cudaError_t e = cudaGetLastError();
-  if (e != cudaSuccess) return e;
-  sums_kernel<<<(unsigned)((2 * p.D + 31) / 32), kSumThreads, 0, s>>>(p, (int)parts);
+  if constexpr (kIter < 8) {
+    const unsigned parts = blocks < (unsigned)kParts ? blocks : kParts;
+    backward_kernel<T, kHow, kGroup, kIter><<<parts, kThreads, smem, s>>>(p, units);
+    const cudaError_t e = cudaGetLastError();
+    if (e != cudaSuccess) return e;
+    sums_kernel<<<(unsigned)((2 * p.D + 31) / 32), kSumThreads, 0, s>>>(p, (int)parts);
+  }
   return cudaGetLastError();
 }
 template <typename T, int kHow, int kGroup>
 cudaError_t heads(const Args& p, bool backward, cudaStream_t s) {
-  switch (heads_of(p, p.rows / (p.Hq + p.Hk))) {
-    case 4: return run<T, kHow, kGroup, sizeof(T) == 2 ? 4 : 2>(p, backward, s);
-    case 2: return run<T, kHow, kGroup, 2>(p, backward, s);
-    default: return run<T, kHow, kGroup, 1>(p, backward, s);
+  constexpr bool kBf16 = sizeof(T) == 2;
+  const int n = heads_of(p, p.rows / (p.Hq + p.Hk), kBf16 ? backward ? 4 : 8 : 2);
+  if constexpr (kBf16) {
+    if (n == 8) return run<T, kHow, kGroup, 8>(p, false, s);
+    if (n == 4) return run<T, kHow, kGroup, 4>(p, backward, s);
   }
+  return n == 2 ? run<T, kHow, kGroup, 2>(p, backward, s) : run<T, kHow, kGroup, 1>(p, backward, s);
 }
 template <typename T, int kHow>
 cudaError_t pick(const Args& p, bool backward, cudaStream_t s) {
