@@ -18,8 +18,35 @@
 namespace linattn {
 namespace {
 
+// A block that has not begun gives its place up: `reply` gets its number, or that there is none, and `bar` 16 bytes.
+__device__ __forceinline__ void claim_block(uint4* reply, uint64_t* bar) {
+  asm volatile("clusterlaunchcontrol.try_cancel.async.shared::cta.mbarrier::complete_tx::bytes.b128 [%0], [%1];" ::"r"(smem_addr(reply)),
+               "r"(smem_addr(bar))
+               : "memory");
+}
+__device__ __forceinline__ bool claimed_block(const uint4* reply, unsigned& block) {
+  uint32_t there;
+  asm volatile("{\n .reg .b128 h;\n .reg .pred p;\n ld.shared.b128 h, [%2];\n"
+               " clusterlaunchcontrol.query_cancel.is_canceled.pred.b128 p, h;\n selp.u32 %0, 1, 0, p;\n mov.u32 %1, 0;\n"
+               " @p clusterlaunchcontrol.query_cancel.get_first_ctaid::x.b32.b128 %1, h;\n}"
+               : "=r"(there), "=r"(block)
+               : "r"(smem_addr(reply))
+               : "memory");
+  return there;
+}
+
 constexpr int kTeam = 256, kThreads = 2 * kTeam + 96;
 constexpr int kBringWarp = 16, kDecayWarp = 17;  // and 18 issues
+
+// A chunk of the block's run, on the way from the warp that brings the tiles to all others.
+struct alignas(16) Step {
+  int live, last, len;   // there is one; of its sequence or segment (for this head and slice); its tokens, 0 for a sequence of none
+  int b, t;              // batch row, first token
+  int hv, hk, slice;     // value and key head, which 64 values
+  int ends;              // whose states at the ends (the sequence or segment)
+  long long image;       // bytes from the first image to the piece of the state before it
+};
+constexpr int kSteps = 8, kAhead = 4;
 
 template <int KP>
 struct Smem {
@@ -33,6 +60,9 @@ struct Smem {
   bf16_t s[2 * 64 * KP];    // the state's pair
   bf16_t third[kEarly ? 64 * KP : 8];  // its third part; wider keys: in the place of the keys of the chunk before
   Decays d[3];
+  Step step[kSteps];
+  uint4 reply;                          // to a claim
+  uint64_t claimed;                     // it is there
   uint64_t full[kStages];               // the tiles are there
   uint64_t end;                         // nothing is in flight
   uint64_t scored, first, summed, out;  // the scores; the first half of the state's sum, all of it; the rows
@@ -58,51 +88,103 @@ __global__ void __launch_bounds__(kThreads, 1) chain_kernel(const __grid_constan
   constexpr int kPair = kTeam + 32;  // a team and a warp beside it
   const Shape& s = a.s;
   const int tid = threadIdx.x, lane = tid & 31, warp = __shfl_sync(0xffffffffu, tid >> 5, 0), sub = warp & 3, half = warp >> 2 & 1;
-  const int slices = (s.V + 63) >> 6, slice = blockIdx.x % slices, hv = blockIdx.x / slices % s.Hv, slot = blockIdx.x / slices / s.Hv;
-  const int hk = hv / (s.Hv / s.Hk), v0 = slice * 64, vn = min(64, s.V - v0);
-  ChunkAt seg;
+  const int slices = (s.V + 63) >> 6, group = s.Hv / s.Hk;
   const bool sums = plan.way == kSums;
-  if (plan.way != kWhole) {
-    if (!chunk_at(s, slot, kCT * plan.chunks, seg)) return;
-  } else {  // a whole sequence, which may be empty: its state passes through
-    const SeqRange r = seq_range(s, slot, kCT);
-    seg.b = r.b, seg.t0 = seg.first = r.t0, seg.len = r.t1 - r.t0, seg.seq = slot;
-  }
   if (warp == 0) wkv7::tmem_alloc(&sm.tmem, kCols);
   if (tid == 0) {
-    for (uint64_t* b : {&sm.scored, &sm.first, &sm.summed, &sm.out, &sm.end}) mbar_init(b, 1);
+    for (uint64_t* b : {&sm.scored, &sm.first, &sm.summed, &sm.out, &sm.end, &sm.claimed}) mbar_init(b, 1);
     for (uint64_t& b : sm.full) mbar_init(&b, 1);
     wkv7::fence_mbar_init();
   }
+  auto step = [&](int i) -> const Step& { return sm.step[i & (kSteps - 1)]; };
+  // The run of a block's chunks: of its own sequence or segment, head and slice, then of those of blocks that have not begun.
+  Patience wait{a.status};
+  ChunkAt seg;
+  int run_hv = 0, run_slice = 0, run_ends = 0, run_n = 0, run_i = 0, claims = 0;
+  bool more = true;
+  auto begin_run = [&](unsigned block) {
+    run_slice = block % slices, run_hv = block / slices % s.Hv, run_ends = block / slices / s.Hv;
+    if (plan.way != kWhole) {
+      if (!chunk_at(s, run_ends, kCT * plan.chunks, seg)) return false;
+    } else {  // a whole sequence, which may be empty: its state passes through a chunk of no tokens
+      const SeqRange r = seq_range(s, run_ends, kCT);
+      seg.b = r.b, seg.t0 = seg.first = r.t0, seg.len = r.t1 - r.t0, seg.seq = run_ends;
+    }
+    run_n = max(1, (seg.len + kCT - 1) / kCT), run_i = 0;
+    return true;
+  };
+  auto claim = [&] {
+    __syncwarp();
+    if (lane == 0) {
+      fence_proxy_async_smem();
+      wkv7::mbar_arrive_expect_tx(&sm.claimed, sizeof sm.reply);
+      claim_block(&sm.reply, &sm.claimed);
+    }
+    ++claims;
+  };
+  auto taken = [&](unsigned& block) {
+    wait(&sm.claimed, claims - 1);
+    return wait.ok && claimed_block(&sm.reply, block);
+  };
+  auto next_step = [&] {
+    Step x{};
+    const int off = (kUpper ? run_n - 1 - run_i : run_i) * kCT;
+    x.live = 1, x.last = ++run_i == run_n, x.len = min(kCT, seg.len - off), x.b = seg.b, x.t = seg.t0 + off;
+    x.hv = run_hv, x.hk = run_hv / group, x.slice = run_slice, x.ends = run_ends;
+    x.image = x.len ? (chunk_slot(s, seg, x.t) * s.Hv + x.hv) * (long long)image_bytes(s.K, s.V) + x.slice * kImagePiece : 0;
+    return x;
+  };
+  auto produce = [&](int j) {  // step j, by one warp
+    while (more && run_i == run_n) {
+      unsigned block;
+      more = taken(block);
+      if (more && !begin_run(block)) claim();
+    }
+    Step x{};
+    if (more) {
+      x = next_step();
+      if (x.last) claim();
+    }
+    if (lane == 0) sm.step[j & (kSteps - 1)] = x;
+    __syncwarp();
+  };
   __syncthreads();
-  const int n = (seg.len + kCT - 1) / kCT;
-  const size_t tok = (size_t)seg.b * s.T + seg.t0;
-  auto begin = [&](int i) { return (kUpper ? n - 1 - i : i) * kCT; };  // first token of the i-th chunk, from the segment's
-  auto length = [&](int i) { return min(kCT, seg.len - begin(i)); };
+  if (warp != kBringWarp && warp != kDecayWarp) {
+    __syncthreads();  // the first steps
+    if (!step(0).live) {
+      if (warp == 0) wkv7::tmem_dealloc(sm.tmem, kCols);
+      return;
+    }
+  }
 
   if (warp >= kBringWarp) {
-    Patience wait{a.status};
     if (warp == kDecayWarp) {
-      const float* g = s.fixed ? a.g + hv : a.g + tok * s.Hv + hv;
       float r[4];
       auto ask = [&](int i) {
-        if (i < n) load_decays(r, s.fixed ? g : g + (size_t)begin(i) * s.Hv, s.fixed ? 0 : s.Hv, length(i), lane);
+        const Step& x = step(i);
+        if (x.live) load_decays(r, a.g + x.hv + (s.fixed ? 0 : ((size_t)x.b * s.T + x.t) * s.Hv), s.fixed ? 0 : s.Hv, x.len, lane);
       };
       auto make = [&](int i) {  // and the next chunk's are asked for
-        if (i < n) {
-          float x[4] = {r[0], r[1], r[2], r[3]};
+        if (step(i).live) {
+          const float x[4] = {r[0], r[1], r[2], r[3]};
           ask(i + 1);
           make_decays(sm.d[i % 3], x, s.scale, lane);
         }
       };
-      ask(0), make(0);
-      __syncthreads();
-      make(1);
-      if (kEarly) __syncthreads();
-      for (int i = 0; i < n; ++i) {
-        make(i + 2);
-        __syncthreads();
+      if (!begin_run(blockIdx.x)) claim();
+      // (one loop for what comes before the first chunk and after: code runs cold once)
+#pragma unroll 1
+      for (int k = -kAhead;; ++k) {
+        if (k >= 0) make(k);
+        if (k < 0 || k >= 2) produce(k < 0 ? k + kAhead : k - 2 + kAhead);
+        if (k >= 0 ? kEarly || k != 1 : k == -1) __syncthreads();
+        if (k == -1) {
+          if (!step(0).live) return;
+          ask(0);
+        }
+        if (k >= 2 && !step(k - 1).live) break;
       }
+      if (!wait.ok) finish_copies(&sm.claimed, claims);
       __syncthreads();
       return;
     }
@@ -110,37 +192,42 @@ __global__ void __launch_bounds__(kThreads, 1) chain_kernel(const __grid_constan
       constexpr int kLead = kEarly ? 2 : 1;  // chunks ahead
       const CUtensorMap *ma = kUpper ? &maps.k : &maps.q, *mb = kUpper ? &maps.q : &maps.k, *mx = kUpper ? &maps.d : &maps.v;
       const int b_a = kUpper ? s.k_b != 0 : s.q_b != 0, b_b = kUpper ? s.q_b != 0 : s.k_b != 0, b_x = kUpper || s.v_b != 0;
-      auto bring = [&](int i, bool keys) {  // b, or a and x
-        if (i < n && lane == 0) {
+      auto bring_of = [&](const Step& w, int i, bool keys) {  // b, or a and x
+        if (w.live && lane == 0) {
           auto& st = sm.stage[i % kSt];
           uint64_t* bar = &sm.full[i % kSt];
-          const int t = seg.t0 + begin(i);
           if (keys) {
-            load_tile<KP>(st.b, mb, bar, 0, hk, t, seg.b * b_b);
+            load_tile<KP>(st.b, mb, bar, 0, w.hk, w.t, w.b * b_b);
           } else {
             wkv7::mbar_arrive_expect_tx(bar, sums ? sizeof st.b + sizeof st.x : sizeof st);
-            if (!sums) load_tile<KP>(st.a, ma, bar, 0, hk, t, seg.b * b_a);
-            load_tile<64>(st.x, mx, bar, v0, hv, t, seg.b * b_x);
+            if (!sums) load_tile<KP>(st.a, ma, bar, 0, w.hk, w.t, w.b * b_a);
+            load_tile<64>(st.x, mx, bar, 64 * w.slice, w.hv, w.t, w.b * b_x);
           }
         }
       };
+      auto bring = [&](int i, bool keys) { bring_of(step(i), i, keys); };
+      int n = 0;  // chunks brought
       auto brought = [&](int i) {
-        if (i >= n) return;
+        const Step& w = step(i);
+        if (!w.live) return;
+        n = i + 1;
         wait(&sm.full[i % kSt], i / kSt);
-        if (s.packed && length(i) < kCT) {
+        if (s.packed && w.len < kCT) {
           auto& st = sm.stage[i % kSt];
-          if (!sums) clear_rows<KP>(st.a, length(i), lane, 32);
-          clear_rows<KP>(st.b, length(i), lane, 32);
-          clear_rows<64>(st.x, length(i), lane, 32);
+          if (!sums) clear_rows<KP>(st.a, w.len, lane, 32);
+          clear_rows<KP>(st.b, w.len, lane, 32);
+          clear_rows<64>(st.x, w.len, lane, 32);
           fence_proxy_async_smem();
         }
       };
       // the state before chunk i: its pair, and the third part in the place of the keys of the chunk before
       char* const images = static_cast<char*>(kUpper ? a.dimages : a.images);
-      char* to = images + ((size_t)(n ? chunk_slot(s, seg, seg.t0 + begin(0)) : 0) * s.Hv + hv) * image_bytes(s.K, s.V) + slice * kImagePiece;
-      const long long next = (kUpper ? -1 : 1) * (long long)(s.Hv * image_bytes(s.K, s.V));
-      auto leave = [&](int i) {
-        if (plan.keep && i < n && lane == 0) {
+      auto place_of = [&](int i) {
+        const Step& w = step(i);
+        return plan.keep && w.live && w.len && lane == 0 ? images + w.image : nullptr;
+      };
+      auto leave = [&](int i, char* to) {
+        if (to) {
 #pragma unroll
           for (int part = 0; part < 3; ++part)
 #pragma unroll
@@ -148,19 +235,25 @@ __global__ void __launch_bounds__(kThreads, 1) chain_kernel(const __grid_constan
               bulk_store(to + (size_t)(part * (KP / 64) + c) * slices * kImagePiece,
                          (part < 2 ? sm.s + part * 64 * KP : kEarly ? sm.third : sm.stage[(i + kSt - 1) % kSt].b) + c * 64 * 64, kImagePiece);
           bulk_commit();
-          to += next;
         }
       };
-      bring(0, false), bring(0, true);
+      const bool own = begin_run(blockIdx.x);
+      if (own) {  // (the first tiles before the steps are there)
+        const Step x = next_step();
+        bring_of(x, 0, false), bring_of(x, 0, true);
+      }
+      __syncthreads();
+      if (!step(0).live) return;
+      if (!own) bring(0, false), bring(0, true);
       if (kEarly) bring(1, false), bring(1, true);
       brought(0);
       __syncthreads();
-      leave(0);
+      leave(0, place_of(0));
       if (kEarly) {
         brought(1);
         __syncthreads();
       }
-      for (int i = 0; i < n; ++i) {
+      for (int i = 0, live = 1; live; ++i) {
         bring(i + kLead, false);
         if (kEarly) bring(i + kLead, true);
         if (lane == 0) bulk_wait_read();
@@ -168,9 +261,11 @@ __global__ void __launch_bounds__(kThreads, 1) chain_kernel(const __grid_constan
         if (!kEarly) bring(i + kLead, true);
         if (!sums) announce(kBarFree, kPair);
         brought(i + kLead);
+        live = step(i + 1).live;
+        char* const to = place_of(i + 1);
         if (!sums) {
           meet(kBarPlanes, kPair);
-          leave(i + 1);
+          leave(i + 1, to);
         }
         __syncthreads();
       }
@@ -215,15 +310,15 @@ __global__ void __launch_bounds__(kThreads, 1) chain_kernel(const __grid_constan
           tc_mma(tm + kU, dx + across(ks) + part * (kXt * 128 >> 4), db + across(ks), product_of(64, KP, true, true), h > 0 || part < 2 || ks > 0);
     };
     if (kEarly) {
-      if (n && !sums && elected()) scores(0);
+      if (!sums && elected()) scores(0);
       __syncwarp();
       __syncthreads();
       tmem_fence_after_sync();
     }
-    for (int i = 0; i < n; ++i) {
+    for (int i = 0, live = 1, next = step(1).live; live; ++i) {
       if (!sums && elected()) {
         if (!kEarly) scores(i);
-        if (kEarly && i + 1 < n) scores(i + 1);
+        if (kEarly && next) scores(i + 1);
         from_state(i);
         if (kEarly) {
           from_chunk(i);
@@ -231,6 +326,7 @@ __global__ void __launch_bounds__(kThreads, 1) chain_kernel(const __grid_constan
         }
       }
       __syncwarp();
+      live = next, next = step(i + 2).live;
       meet(kBarX, kPair);
       if (elected()) {
         sum(i, 0);
@@ -262,7 +358,6 @@ __global__ void __launch_bounds__(kThreads, 1) chain_kernel(const __grid_constan
     return;
   }
 
-  Patience wait{a.status};
   const int team_tid = tid & (kTeam - 1);
   auto turn = [&] {  // every role's end of a chunk
     fence_proxy_async_smem();
@@ -272,7 +367,6 @@ __global__ void __launch_bounds__(kThreads, 1) chain_kernel(const __grid_constan
   };
   if (warp < kTeam / 32) {  // ------------------------------------------------ P, and the rows that leave ---
     const int row = sub * 32 + lane;
-    bf16_t* out = static_cast<bf16_t*>(kUpper ? a.dv : a.o) + (tok * s.Hv + hv) * s.V + v0;
     turn();
     const uint32_t mine = sm.tmem + ((uint32_t)(sub * 32) << 16);
     // The scores of chunk i, decayed, as pairs.
@@ -294,10 +388,11 @@ __global__ void __launch_bounds__(kThreads, 1) chain_kernel(const __grid_constan
       wkv7::tmem_wait_st();
       tmem_fence_before_sync();
     };
-    for (int i = kEarly ? -1 : 0; i < n; ++i) {
+    for (int i = kEarly ? -1 : 0, live = 1; live; ++i) {
+      live = step(i + 1).live;
       if (!sums) {
         if (kEarly) {
-          if (i + 1 < n) score(i + 1);
+          if (live) score(i + 1);
         } else {
           score(i);
           announce(kBarP, kPair);
@@ -306,6 +401,9 @@ __global__ void __launch_bounds__(kThreads, 1) chain_kernel(const __grid_constan
       if (!sums && i >= 0) {
         const Decays& d = sm.d[i % 3];
         bf16_t* stage = sm.stage[i % kSt].a;
+        const Step& to = step(i);
+        const int len = to.len, vn = s.V - 64 * to.slice;
+        bf16_t* p = static_cast<bf16_t*>(kUpper ? a.dv : a.o) + (((size_t)to.b * s.T + to.t) * s.Hv + to.hv) * s.V + 64 * to.slice;
         wait(&sm.out, i);
         tmem_fence_after_sync();
         const float w = (kUpper ? d.tail : d.head)[row];
@@ -323,8 +421,6 @@ __global__ void __launch_bounds__(kThreads, 1) chain_kernel(const __grid_constan
           }
         }
         meet(kBarOut, kTeam);
-        const int len = length(i);
-        bf16_t* p = out + (size_t)begin(i) * s.Hv * s.V;
 #pragma unroll
         for (int e = 0; e < 4; ++e) {
           const int r = (e * kTeam + team_tid) >> 3, c = (team_tid & 7) * 8;
@@ -342,15 +438,15 @@ __global__ void __launch_bounds__(kThreads, 1) chain_kernel(const __grid_constan
   // ------------------------------------------------------------------ u . x, and the state ---
   // The state: rows 16 sub .., keys KP / 2 half .. in accumulator tiles.
   float S[kTiles][4];
-  const int s_row = v0 + 16 * sub + (lane >> 2), s_col = half * (KP / 2) + 2 * (lane & 3);
-  float* const states = (kUpper ? a.dstates : a.states) + ((size_t)s_row * s.K + s_col);
-  const size_t state = (size_t)s.V * s.K;
-  auto each = [&](float* m, auto f) {  // pairs of the state's numbers that exist; m is where its first is
+  const int s_row = 16 * sub + (lane >> 2), s_col = half * (KP / 2) + 2 * (lane & 3);
+  auto each = [&](float* m, const Step& of, auto f) {  // pairs of the state's numbers that exist; m: [ends][Hv][V][K]
+    const int v0 = 64 * of.slice + s_row;
+    m += (((size_t)of.ends * s.Hv + of.hv) * s.V + v0) * s.K + s_col;
 #pragma unroll
     for (int t = 0; t < kTiles; ++t)
 #pragma unroll
       for (int h = 0; h < 2; ++h)
-        if (s_row + 8 * h < s.V && s_col + 8 * t < s.K) f(reinterpret_cast<float2*>(m + (h ? 8 * s.K : 0) + 8 * t), S[t][2 * h], S[t][2 * h + 1]);
+        if (v0 + 8 * h < s.V && s_col + 8 * t < s.K) f(reinterpret_cast<float2*>(m + (h ? 8 * s.K : 0) + 8 * t), S[t][2 * h], S[t][2 * h + 1]);
   };
   auto load = [](float2* p, float& x, float& y) {
     const float2 v = *p;
@@ -368,18 +464,16 @@ __global__ void __launch_bounds__(kThreads, 1) chain_kernel(const __grid_constan
       if (plan.keep) stsm4(third + o, f.p[2]);
     }
   };
+  float* const states = kUpper ? a.dstates : a.states;
+  float* const init = plan.way == kResume ? states : plan.way == kWhole ? const_cast<float*>(kUpper ? a.dS_final : a.s_init) : nullptr;
+  float* const last = sums ? states : plan.way == kWhole ? (kUpper ? a.dS_init : a.s_final) : nullptr;
+  auto start = [&](const Step& of) {  // the state that a sequence or segment begins with
 #pragma unroll
-  for (int t = 0; t < kTiles; ++t)
+    for (int t = 0; t < kTiles; ++t)
 #pragma unroll
-    for (int e = 0; e < 4; ++e) S[t][e] = 0.f;
-  const size_t ends = ((size_t)seg.seq * s.Hv + hv) * state + (size_t)s_row * s.K + s_col;
-  float* init = const_cast<float*>(kUpper ? a.dS_final : a.s_init);
-  if (plan.way == kResume)
-    each(states + ((size_t)slot * s.Hv + hv) * state, load);
-  else if (plan.way == kWhole && init)
-    each(init + ends, load);
-  planes(kEarly ? sm.third : sm.stage[kSt - 1].b);
-  turn();
+      for (int e = 0; e < 4; ++e) S[t][e] = 0.f;
+    if (init) each(init, of, load);
+  };
   const uint32_t mine = sm.tmem + ((uint32_t)(sub * 32) << 16);
   // u . x of half h of the tokens
   auto scaled = [&](int i, int h) {
@@ -400,44 +494,57 @@ __global__ void __launch_bounds__(kThreads, 1) chain_kernel(const __grid_constan
     }
     fence_proxy_async_smem();
   };
-  if (kEarly) __syncthreads();
   float passed = 1.f;  // the decay of the segment so far
-  for (int i = 0; i < n; ++i) {
-    const Decays& d = sm.d[i % 3];
-    wait(&sm.full[i % kSt], i / kSt);
-    scaled(i, 0);
-    announce(kBarX, kPair);
-    if (!kEarly) {
-      wait(&sm.first, i);
-      scaled(i, 1);
-      announce(kBarX2, kPair);
+#pragma unroll 1
+  for (int i = -1, live = 1; live; ++i) {  // from -1, where the first state begins
+    const Step &now = step(max(i, 0)), &next = step(i + 1);
+    const bool ends = i < 0 || now.last;
+    live = next.live;
+    if (i >= 0) {
+      const Decays& d = sm.d[i % 3];
+      wait(&sm.full[i % kSt], i / kSt);
+#pragma unroll 1
+      for (int h = 0; h < M::kHalves; ++h) {
+        if (h) wait(&sm.first, i);
+        scaled(i, h);
+        announce(h ? kBarX2 : kBarX, kPair);
+      }
+      if (ends && live && init) {  // the next state's 64 rows, one piece after the other
+        const size_t from = (((size_t)next.ends * s.Hv + next.hv) * s.V + 64 * next.slice) * s.K + 32 * team_tid;
+        if (32 * team_tid < min(64, s.V - 64 * next.slice) * s.K) asm volatile("prefetch.global.L2 [%0];" ::"l"(init + from));
+      }
+      wait(&sm.summed, i);
+      tmem_fence_after_sync();
+#pragma unroll
+      for (int t = 0; t < kTiles; t += 4) {
+        float x[4][4];
+        tc_load_tiles(x, mine + kU + half * (KP / 2) + 8 * t);
+#pragma unroll
+        for (int j = 0; j < 4; ++j)
+#pragma unroll
+          for (int e = 0; e < 4; ++e) S[t + j][e] = fmaf(d.whole, S[t + j][e], x[j][e]);
+      }
+      passed *= d.whole;
     }
-    wait(&sm.summed, i);
-    tmem_fence_after_sync();
-#pragma unroll
-    for (int t = 0; t < kTiles; t += 4) {
-      float x[4][4];
-      tc_load_tiles(x, mine + kU + half * (KP / 2) + 8 * t);
-#pragma unroll
-      for (int j = 0; j < 4; ++j)
-#pragma unroll
-        for (int e = 0; e < 4; ++e) S[t + j][e] = fmaf(d.whole, S[t + j][e], x[j][e]);
+    if (ends) {
+      if (i >= 0) {
+        if (last) each(last, now, store);
+        if (sums && team_tid == 0 && now.slice == 0) a.decay[(size_t)now.ends * s.Hv + now.hv] = passed;
+        passed = 1.f;
+      }
+      if (live) start(next);
     }
-    passed *= d.whole;
     if (!sums) {
       // (the state's products and copies have read it: the sum was issued after the former)
-      meet(kBarFree, kPair);
-      planes(kEarly ? sm.third : sm.stage[i % kSt].b);
-      fence_proxy_async_smem();
-      announce(kBarPlanes, kPair);
+      if (i >= 0) meet(kBarFree, kPair);
+      planes(kEarly ? sm.third : sm.stage[(i + kSt) % kSt].b);
+      if (i >= 0) {
+        fence_proxy_async_smem();
+        announce(kBarPlanes, kPair);
+      }
     }
     turn();
-  }
-  float* last = kUpper ? a.dS_init : a.s_final;
-  if (plan.way == kWhole && last) each(last + ends, store);
-  if (sums) {
-    each(states + ((size_t)slot * s.Hv + hv) * state, store);
-    if (team_tid == 0 && slice == 0) a.decay[(size_t)slot * s.Hv + hv] = passed;
+    if (kEarly && i < 0) __syncthreads();
   }
   __syncthreads();
 }
