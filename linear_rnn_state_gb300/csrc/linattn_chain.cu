@@ -287,7 +287,7 @@ __global__ void __launch_bounds__(kThreads, 1) chain_kernel(const __grid_constan
     };
     auto from_state = [&](int i) {
       const uint64_t da = desc(sm.stage[i % kSt].a), ds = desc(sm.s);
-#pragma unroll
+#pragma unroll 1
       for (int part = 1; part >= 0; --part)
 #pragma unroll
         for (int ks = 0; ks < KP / 16; ++ks)
@@ -295,7 +295,7 @@ __global__ void __launch_bounds__(kThreads, 1) chain_kernel(const __grid_constan
     };
     auto from_chunk = [&](int i) {
       const uint64_t dx = desc(sm.stage[i % kSt].x);
-#pragma unroll
+#pragma unroll 1
       for (int part = 1; part >= 0; --part)
 #pragma unroll
         for (int ks = 0; ks < kCT / 16; ++ks)
@@ -303,7 +303,7 @@ __global__ void __launch_bounds__(kThreads, 1) chain_kernel(const __grid_constan
     };
     auto sum = [&](int i, int h) {  // of half h of the tokens
       const uint64_t dx = desc(sm.xt), db = desc(sm.stage[i % kSt].b, kRowPanel) + across(h * (kXt / 16));
-#pragma unroll
+#pragma unroll 1
       for (int part = 2; part >= 0; --part)
 #pragma unroll
         for (int ks = 0; ks < kXt / 16; ++ks)
@@ -327,14 +327,9 @@ __global__ void __launch_bounds__(kThreads, 1) chain_kernel(const __grid_constan
       }
       __syncwarp();
       live = next, next = step(i + 2).live;
-      meet(kBarX, kPair);
-      if (elected()) {
-        sum(i, 0);
-        tc_commit(kEarly ? &sm.summed : &sm.first);
-      }
-      __syncwarp();
-      if (!kEarly) {
-        if (!sums) {
+#pragma unroll 1
+      for (int h = 0; h < M::kHalves; ++h) {
+        if (h && !sums) {
           meet(kBarP, kPair);
           tmem_fence_after_sync();
           if (elected()) {
@@ -343,10 +338,10 @@ __global__ void __launch_bounds__(kThreads, 1) chain_kernel(const __grid_constan
           }
           __syncwarp();
         }
-        meet(kBarX2, kPair);
+        meet(h ? kBarX2 : kBarX, kPair);
         if (elected()) {
-          sum(i, 1);
-          tc_commit(&sm.summed);
+          sum(i, h);
+          tc_commit(h == M::kHalves - 1 ? &sm.summed : &sm.first);
         }
         __syncwarp();
       }
