@@ -2,7 +2,8 @@
 //
 // As linattn_chain.cu, with every operand in three bfloat16 parts (24 bits) and six products of parts for each
 // product. The tiles of a chunk (a, b, x and u . x, 192 KB) leave room for one stage: threads split the values of
-// the next chunk when the products that read the places are done (P x runs beside it); a warp has brought them to L2.
+// the next chunk when the products that read the places are done (P x runs beside it); they ask for them while the
+// products before run, and a warp has brought them to L2. Sums alone need b and u . x only, and have two places for each.
 //
 // Tensor memory: the scores (128 columns, later the rows' P x), P (192), a S^T (64), the state's sum (64).
 #include "linattn_tc.cuh"
@@ -16,7 +17,7 @@ constexpr int kHelpWarp = 16;                                                   
 struct Smem {
   bf16_t a[3 * kCT * 64], b[3 * kCT * 64], x[3 * kCT * 64], xt[3 * kCT * 64];
   bf16_t s[3 * 64 * 64];
-  Decays d[2];
+  Decays d[3];
   uint64_t scored, summed, out, end;
   uint32_t tmem;
 };
@@ -76,7 +77,7 @@ __global__ void __launch_bounds__(kThreads, 1) chain32_kernel(const Args a, cons
       if (i < n) {
         float x[4] = {r[0], r[1], r[2], r[3]};
         ask(i + 1);
-        make_decays(sm.d[i & 1], x, s.scale, lane);
+        make_decays(sm.d[i % 3], x, s.scale, lane);
       }
     };
     auto prefetch = [&](const float* p, long long stride, int cols, int len) {
@@ -96,15 +97,19 @@ __global__ void __launch_bounds__(kThreads, 1) chain32_kernel(const Args a, cons
     };
     ask(0), make(0);
     meet(0, kMembers);
+    make(1);
     meet(0, kMembers);
     leave(0);
     for (int i = 0; i < n; ++i) {
-      make(i + 1);
-      if (lane == 0) bulk_wait_read();
-      __syncwarp();
-      announce(kBarFree, kPair);
-      if (i + 2 < n) {
-        const int t = begin(i + 2), len = length(i + 2);
+      if (!sums) {
+        if (lane == 0) bulk_wait_read();
+        __syncwarp();
+        announce(kBarFree, kPair);
+      }
+      make(i + 2);
+      constexpr int kLead = sums ? 3 : 2;
+      if (i + kLead < n) {
+        const int t = begin(i + kLead), len = length(i + kLead);
         if (!sums) prefetch(pa + t * st_a, st_a, s.K, len);
         prefetch(pb + t * st_b, st_b, s.K, len), prefetch(px + t * st_x, st_x, vn, len);
       }
@@ -125,24 +130,24 @@ __global__ void __launch_bounds__(kThreads, 1) chain32_kernel(const Args a, cons
     const uint32_t tm = sm.tmem;
     for (int i = 0; i < n; ++i) {
       if (elected()) {
-        const uint64_t da = desc(sm.a), db = desc(sm.b), ds = desc(sm.s), du = desc(sm.xt);
+        const uint64_t da = desc(sm.a), db = desc(sums && i & 1 ? sm.a : sm.b), ds = desc(sm.s), du = desc(sums && i & 1 ? sm.x : sm.xt);
         if (!sums) {
           terms<3, 3>([&](int p, int r, bool first) {
-#pragma unroll 1
+#pragma unroll
             for (int ks = 0; ks < 4; ++ks)
               tc_mma(tm + kScore, da + along<kCT>(ks) + p * (kRowPanel >> 4), db + along<kCT>(ks) + r * (kRowPanel >> 4),
                      product_of(128, 128, false, false), !first || ks > 0);
           });
           tc_commit(&sm.scored);
           terms<3, 3>([&](int p, int r, bool first) {
-#pragma unroll 1
+#pragma unroll
             for (int ks = 0; ks < 4; ++ks)
               tc_mma(tm + kIn, da + along<kCT>(ks) + p * (kRowPanel >> 4), ds + along<64>(ks) + r * (64 * 128 >> 4),
                      product_of(128, 64, false, false), !first || ks > 0);
           });
         }
         terms<3, 3>([&](int p, int r, bool first) {
-#pragma unroll 1
+#pragma unroll
           for (int ks = 0; ks < kCT / 16; ++ks)
             tc_mma(tm + kU, du + across(ks) + p * (kRowPanel >> 4), db + across(ks) + r * (kRowPanel >> 4), product_of(64, 64, true, true),
                    !first || ks > 0);
@@ -155,7 +160,7 @@ __global__ void __launch_bounds__(kThreads, 1) chain32_kernel(const Args a, cons
       if (!sums && elected()) {
         const uint64_t dx = desc(sm.x);
         terms<3, 3>([&](int p, int r, bool first) {
-#pragma unroll 1
+#pragma unroll
           for (int ks = 0; ks < kCT / 16; ++ks)
             tc_mma_t(tm + kO, tm + kP + part_at<3>(ks, p), dx + across(ks) + r * (kRowPanel >> 4), product_of(128, 64, false, true), !first || ks > 0);
         });
@@ -203,12 +208,12 @@ __global__ void __launch_bounds__(kThreads, 1) chain32_kernel(const Args a, cons
       if (r < len && piece < vn) load8(vx[e], px + (t0 + r) * st_x + piece);
     }
   };
-  auto fill = [&] {  // a and b
+  auto fill = [&](int i) {  // a and b
 #pragma unroll
     for (int e = 0; e < 2; ++e) {
       const int o = at(kCT, (e * kWorkers + tid) >> 3, piece);
       if (!sums) put8<3>(sm.a + o, kPart, va[e]);
-      put8<3>(sm.b + o, kPart, vb[e]);
+      put8<3>((sums && i & 1 ? sm.a : sm.b) + o, kPart, vb[e]);
     }
   };
   auto fill_x = [&](const float (&vx)[2][8]) {
@@ -216,7 +221,7 @@ __global__ void __launch_bounds__(kThreads, 1) chain32_kernel(const Args a, cons
     for (int e = 0; e < 2; ++e) put8<3>(sm.x + at(kCT, (e * kWorkers + tid) >> 3, piece), kPart, vx[e]);
   };
   auto fill_u = [&](int i, const float (&vx)[2][8]) {  // u . x
-    const float* u = kUpper ? sm.d[i & 1].head : sm.d[i & 1].tail;
+    const float* u = kUpper ? sm.d[i % 3].head : sm.d[i % 3].tail;
 #pragma unroll
     for (int e = 0; e < 2; ++e) {
       const int r = (e * kWorkers + tid) >> 3;
@@ -224,7 +229,7 @@ __global__ void __launch_bounds__(kThreads, 1) chain32_kernel(const Args a, cons
       float y[8];
 #pragma unroll
       for (int j = 0; j < 8; ++j) y[j] = vx[e][j] * f;
-      put8<3>(sm.xt + at(kCT, r, piece), kPart, y);
+      put8<3>((sums && i & 1 ? sm.x : sm.xt) + at(kCT, r, piece), kPart, y);
     }
   };
   if (n) ask(0);
@@ -264,11 +269,12 @@ __global__ void __launch_bounds__(kThreads, 1) chain32_kernel(const Args a, cons
     each(init + ends, load);
   planes();
   meet(0, kMembers);  // the first decays
+  float vx[2][8];
   if (n) {
-    float vx[2][8];
     ask_x(0, vx);
-    fill(), fill_u(0, vx);
+    fill(0), fill_u(0, vx);
     if (!sums) fill_x(vx);
+    if (sums && n > 1) ask(1), ask_x(1, vx);
   }
   fence_proxy_async_smem();
   tmem_fence_before_sync();
@@ -278,7 +284,7 @@ __global__ void __launch_bounds__(kThreads, 1) chain32_kernel(const Args a, cons
   Patience wait{a.status};
   float passed = 1.f;  // the decay of the segment so far
   for (int i = 0; i < n; ++i) {
-    const Decays& d = sm.d[i & 1];
+    const Decays& d = sm.d[i % 3];
     if (!sums) {
       wait(&sm.scored, i);
       tmem_fence_after_sync();
@@ -295,6 +301,12 @@ __global__ void __launch_bounds__(kThreads, 1) chain32_kernel(const Args a, cons
       announce(kBarP, kPair);
     }
     const bool more = i + 1 < n;
+    if (sums) {  // the next chunk's places beside the products, and the one's after it on their way
+      if (more) fill(i + 1), fill_u(i + 1, vx);
+      if (i + 2 < n) ask(i + 2), ask_x(i + 2, vx);
+    } else if (more) {  // (on their way while the products run)
+      ask(i + 1), ask_x(i + 1, vx);
+    }
     wait(&sm.summed, i);
     tmem_fence_after_sync();
     {
@@ -306,14 +318,6 @@ __global__ void __launch_bounds__(kThreads, 1) chain32_kernel(const Args a, cons
         for (int e = 0; e < 4; ++e) S[j][e] = fmaf(d.whole, S[j][e], x[j][e]);
     }
     passed *= d.whole;
-    meet(kBarFree, kPair);  // the next decays are there, the last state has left
-    if (more) ask(i + 1);
-    if (!sums) planes();
-    float vx[2][8];
-    if (more) {
-      ask_x(i + 1, vx);
-      fill(), fill_u(i + 1, vx);
-    }
     if (sums) {
       fence_proxy_async_smem();
       tmem_fence_before_sync();
@@ -321,6 +325,9 @@ __global__ void __launch_bounds__(kThreads, 1) chain32_kernel(const Args a, cons
       tmem_fence_after_sync();
       continue;
     }
+    meet(kBarFree, kPair);  // the last state has left
+    planes();
+    if (more) fill(i + 1), fill_u(i + 1, vx);
     wait(&sm.out, i);
     tmem_fence_after_sync();
     // rows through shared memory (x's place): 16 pieces of four values, permuted by the row

@@ -306,17 +306,21 @@ __device__ __forceinline__ constexpr uint32_t part_at(int ks, int part) {
   return (ks >> 1) * 16 * kP + part * 16 + (ks & 1) * 8;
 }
 // The products of the parts of operands with kA and kB of them: f(part of a, part of b, whether it is the first),
-// the small ones first.
+// the small ones first. A loop: most kernels run it a few times only, and code that runs cold costs more than the loop.
+struct Terms {
+  int count = 0;
+  uint32_t a = 0, b = 0;  // two bits each
+  __host__ __device__ constexpr Terms(int parts_a, int parts_b) {
+    for (int sum = parts_a + parts_b - 2 < 2 ? parts_a + parts_b - 2 : 2; sum >= 0; --sum)
+      for (int i = 0; i < parts_a; ++i)
+        if (sum - i >= 0 && sum - i < parts_b) a |= (uint32_t)i << 2 * count, b |= (uint32_t)(sum - i) << 2 * count, ++count;
+  }
+};
 template <int kA, int kB, typename F>
 __device__ __forceinline__ void terms(F f) {
-  constexpr int kMost = kA + kB - 2 < 2 ? kA + kB - 2 : 2;
-#pragma unroll
-  for (int sum = kMost; sum >= 0; --sum)
-#pragma unroll
-    for (int i = 0; i < kA; ++i)
-#pragma unroll
-      for (int j = 0; j < kB; ++j)
-        if (i + j == sum) f(i, j, sum == kMost && i == (kMost < kB ? 0 : kMost - kB + 1));
+  constexpr Terms t(kA, kB);
+#pragma unroll 1
+  for (int n = 0; n < t.count; ++n) f((int)(t.a >> 2 * n & 3u), (int)(t.b >> 2 * n & 3u), n == 0);
 }
 
 }  // namespace linattn
