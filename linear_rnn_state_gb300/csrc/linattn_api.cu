@@ -76,33 +76,35 @@ struct Place {
     return p;
   }
 };
-// On tcgen05: into how many segments of how many chunks a chain goes; 1: none. Chains (sequences, heads and slices of
-// 64 values) run one an SM at a time. Segments fill the GPU, at the price of a pass for their sums, measured at a
-// third of the chain itself, and a few launches; they are taken where they save a tenth of the steps that follow
-// one another. (Packed sequences may be one long and many short ones: the count is that of the longest possible.)
+// On tcgen05: how many chunks a segment of a chain has; 0: chains go whole. Chains (sequences, heads and slices of
+// 64 values) run one an SM at a time. Segments fill the GPU, at the price of a pass for their sums, which measures as
+// much as the chain itself in bfloat16 and half of it in fp32, of launches and the join (4 steps' worth, and 6), and of two steps'
+// worth for each block's beginning; they are taken where that saves a tenth of the steps that follow one another. 8192
+// tokens, us whole and in segments: bfloat16 32 heads of 64 150 and 91, 64 heads 150 and 160; fp32 32 heads 347 and 160, 64 heads
+// 351 and 300, 80 heads 359 and 519. (Packed sequences may be one long and many short ones: the longest is taken for
+// three times the mean.)
 constexpr int kSms = 152;
-int segment_chunks(const Shape& s) {
+int segment_chunks(const Shape& s, bool bf16) {
   const long long heads = (long long)s.Hv * ((s.V + 63) / 64), lines = heads * s.nseq;
   const int chunks = (s.T + s.C - 1) / s.C;
   if (chunks < 8 || !lines) return 0;
-  auto steps = [&](long long blocks, int each) { return (blocks + kSms - 1) / kSms * each; };
-  // whole chains: dense batches, or packed ones of like lengths with a longest of three times the mean
+  auto steps = [&](long long blocks, int each) { return (blocks + kSms - 1) / kSms * (each + 2); };
   const long long total = s.packed ? (s.T / s.C + s.nseq) * heads : chunks * lines;
   const long long longest = s.packed ? (chunks * 3 + s.nseq - 1) / s.nseq : chunks;
-  const long long whole = s.packed ? (longest > total / kSms ? longest : total / kSms) : steps(lines, chunks);
+  const long long whole = s.packed ? (longest > total / kSms ? longest : total / kSms) + 2 : steps(lines, chunks);
   int best = 0;
   long long least = whole * 9;
   for (int n = 2; n <= 64 && n <= chunks / 2; ++n) {
     const int each = (chunks + n - 1) / n;
-    const long long cost = steps(s.packed ? (total + each - 1) / each : lines * n, each) * 10 * 4 / 3 + 20;
+    const long long cost = steps(s.packed ? (total + each - 1) / each : lines * n, each) * (bf16 ? 20 : 15) + (bf16 ? 40 : 60);
     if (cost < least) least = cost, best = each;
   }
   return best;
 }
 // How many chunks or segments have their states in fp32.
-long long stretches(const Shape& s, bool tc) {
-  if (!tc) return s.slots;
-  const int each = segment_chunks(s);
+long long stretches(const Shape& s, bool bf16) {
+  if (!on_tcgen05(s.K, s.V, bf16)) return s.slots;
+  const int each = segment_chunks(s, bf16);
   return each ? slot_count(s.B, s.T, s.nseq, s.packed, each * s.C) : 0;
 }
 // The regions of `saved`, and of the backward's workspace, from p on; returns the bytes.
@@ -112,7 +114,7 @@ size_t place_saved(Args& a, bool bf16, bool for_backward, char* p) {
   Place x{p, p};
   const bool tc = on_tcgen05(s.K, s.V, bf16);
   if (tc && for_backward) a.images = x.bytes(n * image_bytes(s.K, s.V));
-  const size_t m = (size_t)stretches(s, tc) * s.Hv;
+  const size_t m = (size_t)stretches(s, bf16) * s.Hv;
   x.take(a.states, m * s.V * s.K);
   x.take(a.decay, m);
   return x.at - x.start;
@@ -123,7 +125,7 @@ size_t place_workspace(Args& a, bool bf16, char* p) {
   Place x{p, p};
   const bool tc = on_tcgen05(s.K, s.V, bf16);
   if (tc) a.dimages = x.bytes(n * image_bytes(s.K, s.V));
-  const size_t m = (size_t)stretches(s, tc) * s.Hv;
+  const size_t m = (size_t)stretches(s, bf16) * s.Hv;
   x.take(a.dstates, m * s.V * s.K);
   x.take(a.decay, m);
   if (s.fixed) {
@@ -150,7 +152,7 @@ int launched(cudaError_t e, const char* what) {
 }
 // On tcgen05: o, or dv.
 int chains(const Maps& maps, const Args& a, bool bf16, bool backward, bool keep, cudaStream_t stream) {
-  const int each = segment_chunks(a.s);
+  const int each = segment_chunks(a.s, bf16);
   auto run = [&](Way way, bool images) {
     return launched(bf16 ? launch_chain(maps, a, backward, each, way, images, stream) : launch_chain32(a, backward, each, way, images, stream), "chain");
   };

@@ -13,6 +13,14 @@
 // and a third part, by bulk copies. With up to 64 keys
 // the scores of chunk i + 1 are made and decayed while the other products of chunk i run (three stages of
 // tiles, two places for the scores); wider keys leave room for two stages, and u . x goes by halves of the tokens.
+//
+// A block that is done takes the place of one that has not begun and goes on with its chunks as if they were its own, a
+// list of steps ahead of the roles: no pause between short sequences (8191 tokens in 24 sequences, 32 heads of 128: 121 us for 147).
+// The first chunks of a block are slow (10 thousand cycles, then 6), for its code is cold: each role has one copy of what it does.
+//
+// Bound by the steps' latency, 5200 cycles a chunk with 64 keys and 6000 with 128, of which the products take 1100 to 1700
+// and shared memory's traffic 3100. Measured: 4 x 4096 x 32 x 64 86 us (369 MB with the images, 4.3 TB/s), 2 x 4095 x 32 x 128
+// 106 us (403 MB, 3.8 TB/s; 128 blocks of 64 values). One team of warps for all of it took 101 for 95 us.
 #include "linattn_tc.cuh"
 
 namespace linattn {

@@ -11,6 +11,9 @@
 //   dg_t = sum_{j<t<=i} X_ij + sum_{i>=t} q_i.(scale e^{G_i} S^T do_i) + sum_{j<t} k_j.(e^{Gc - G_j} D^T v_j)
 //          + e^{Gc} <S, D>,   X_ij = scale e^{G_i - G_j} (q_i.k_j)(do_i.v_j),
 // all of them sums: no differences of large ones.
+//
+// For fp32 heads above 64: three parts of the four tiles of a chunk (393 KB at 128) would not fit the shared memory that
+// tcgen05 reads, so products are mma.sync's, of 64 tokens and 64 columns at a time.
 #include "linattn_common.cuh"
 
 namespace linattn {

@@ -1,4 +1,4 @@
-// The fifth-generation tensor cores (tcgen05) as linear attention's bfloat16 kernels use them: chunks of 128
+// The fifth-generation tensor cores (tcgen05) as linear attention's kernels use them: chunks of 128
 // tokens, which are the 128 rows (lanes of tensor memory) of a product's accumulator.
 //
 // A tile (linattn_common.cuh) is an operand as it lies: rows of 128 bytes with permuted pieces are
@@ -193,7 +193,8 @@ __device__ __forceinline__ void bulk_wait_all() { asm volatile("cp.async.bulk.wa
 //     or the other way round (backward)
 //   to, from: e^{G - m} and e^{m - G} with m the middle of the range of G in a token's block of 32. Where that range is
 //     at most kNear, products of them are the decays of the diagonal's blocks, and with e^{G_i - m} those of the others
-//     (at most 1 times e^30 where no log decay is above 0)
+//     (at most 1 times e^30 where no log decay is above 0). Exponentials of every element instead cost 30 us of 86 in a
+//     chain at 4 x 4096 x 32 x 64, and 40 of 176 in the gradients
 constexpr float kNear = 60.f;
 struct alignas(16) Decays {
   float2 G[kCT];

@@ -49,7 +49,7 @@ extern "C" {
 
 size_t qkrope_part_bytes(long long tokens, int Hq, int Hk, int D) {
   if (tokens < 0 || tokens >= 1ll << 31 || Hq < 0 || Hk < 0 || D < 8 || D > kMaxD || D % 8) return 0;
-  return (size_t)part_rows(tokens * ((long long)Hq + Hk), D) * 2 * D * 4;
+  return (size_t)part_rows(tokens * ((long long)Hq + Hk)) * 2 * D * 4;
 }
 
 int qkrope_forward(const void* q, const void* k, const float* q_weight, const float* k_weight, const double* freq,

@@ -24,7 +24,7 @@ struct Args {
   float eps;
 };
 // The partial rows a backward writes (its blocks).
-int part_rows(long long rows, int D);
+int part_rows(long long rows);
 cudaError_t launch(const Args& p, bool bf16, bool backward, cudaStream_t s);
 
 }  // namespace qkrope

@@ -373,6 +373,23 @@ def test_packed_sequences(env, starts, Hk, Hv, K, V, dtype):
     _close("dS_init", out["dS_init"], np.concatenate([x["dS_init"] for x in bwd]))
 
 
+@pytest.mark.parametrize("dtype,K,V,Hk,Hv", [(BF16, 64, 72, 2, 4), (BF16, 128, 64, 1, 5), (BF16, 16, 64, 3, 3), (F32, 64, 64, 2, 4)])
+def test_many_short_packed_sequences(env, dtype, K, V, Hk, Hv):
+    """More chains than the GPU has SMs, of lengths from none to a few chunks in any order, from and to states of their own."""
+    orc, la = env
+    lengths = [0, 1, 130, 0, 0, 64, 7, 257, 128, 2] * 6 + [0]
+    starts = np.concatenate(([0], np.cumsum(lengths))).tolist()
+    d = _make(1, starts[-1], Hk, Hv, K, V, dtype, 23, states=len(lengths))
+    out = _raw(la, d, starts)
+    h = _np(d)
+    fwd = orc.packed(orc.forward, starts, [h[m] for m in INS], {"s_init": h["s_init"]}, scale=0.25)
+    _close("o", out["o"], np.concatenate([x[0] for x in fwd], 1)), _close("s_final", out["s_final"], np.concatenate([x[1] for x in fwd]))
+    bwd = orc.packed(orc.backward, starts, [h[m] for m in INS + ("do",)], {"s_init": h["s_init"], "dS_final": h["dS_final"]}, scale=0.25)
+    for m in ("dq", "dk", "dv", "dg"):
+        _close(m, out[m], np.concatenate([x[m] for x in bwd], 1))
+    _close("dS_init", out["dS_init"], np.concatenate([x["dS_init"] for x in bwd]))
+
+
 @pytest.mark.parametrize("dtype,Hk,Hv,K,T,starts,fixed", [
     (BF16, 1, 2, 64, 100, [0, 40, 70], False),
     (F32, 2, 2, 72, 333, [10, 40, 40, 70], False),
