@@ -16,8 +16,8 @@
 // results), S and D in three parts, 64 keys of them at a time (24 bits: dg is an fp32 result). fp32: all in three.
 //
 // Bound by latency: a chunk's tiles and states come, are multiplied, decayed, multiplied again and read out, twice, one
-// step after the other, with one block an SM but for bfloat16's heads of 64. Measured: 4 x 4096 x 32 x 64 bfloat16 176 us
-// (605 MB with the states' images: 3.4 TB/s), 2 x 4095 x 16 and 32 x 128 225 us (670 MB, 3.0 TB/s), fp32 8 x 4096 x 12 x 64
+// step after the other, with one block an SM but for bfloat16's heads of 64. Measured: 4 x 4096 x 32 x 64 bfloat16 168 us
+// (605 MB with the states' images: 3.6 TB/s), 2 x 4095 x 16 and 32 x 128 225 us (670 MB, 3.0 TB/s), fp32 8 x 4096 x 12 x 64
 // 361 us (755 MB, 2.1 TB/s; six products of parts for each product, 105 us of them at the tensor cores' rate).
 #include <type_traits>
 
@@ -74,6 +74,7 @@ __global__ void __launch_bounds__(128 * kQ, kQ == 2 ? 2 : 1) grad_kernel(const _
   // E of dq and of dk; A (bfloat16: in its place); q k^T; then, where what was there has been read, the chunk's and the
   // state's products
   enum { kE = 0, kQk = kF32 ? 320 : 128, kE2 = kF32 ? kQk : kE, kAt = kF32 ? 128 : 0, kOut = kF32 ? 0 : 128, kIn = kF32 ? 64 : 128 + KP };
+  constexpr bool kHold = kQ == 2;  // registers for S's numbers, so that <S, D> need not read D from global memory (4 x 4096 x 32 x 64: 177 -> 168 us)
   constexpr bool kEarlyIn = !kF32 && KP == 128;  // the state's products have columns of their own
   static_assert(!kF32 || (KP == 64 && VP == 64 && kQ == 4), "fp32 tiles of 64 columns fill shared memory");
   const Shape& s = a.s;
@@ -262,7 +263,7 @@ __global__ void __launch_bounds__(128 * kQ, kQ == 2 ? 2 : 1) grad_kernel(const _
     tmem_fence_after_sync();
     tm = sm.tmem;
     const uint32_t mine = tm + ((uint32_t)(32 * sub) << 16);
-    float whole = 0.f;
+    float whole = 0.f, held[kHold ? VP * 8 / kThreads : 1][8];  // kHold: S, until D is there
     auto phase = [&](auto upper) {
       constexpr bool kUpper = decltype(upper)::value;
       const bf16_t *ta = kUpper ? sm.v : sm.d, *tx = kUpper ? sm.q : sm.k, *td = kUpper ? sm.k : sm.q;
@@ -279,7 +280,29 @@ __global__ void __launch_bounds__(128 * kQ, kQ == 2 ? 2 : 1) grad_kernel(const _
       // They are there; their part of <S, D>.
       auto fetched = [&](int sl) {
         wait(&sm.full[1], turn3++);
-        if (!kUpper && dg) {
+        if (kHold && dg) {
+#pragma unroll
+          for (int e = 0; e < VP * 8 / kThreads; ++e) {
+            const bf16_t* at = sm.s + 8 * (e * kThreads + tid);
+            float x[8], t[8];
+            load8(x, at);
+#pragma unroll
+            for (int part = 1; part < 3; ++part) {
+              load8(t, at + part * VP * 64);
+#pragma unroll
+              for (int j = 0; j < 8; ++j) x[j] += t[j];
+            }
+#pragma unroll
+            for (int j = 0; j < 8; ++j) {
+              if (kUpper)
+                whole = fmaf(x[j], held[e][j], whole);
+              else
+                held[e][j] = x[j];
+            }
+          }
+          fence_proxy_async_smem();
+        }
+        if (!kHold && !kUpper && dg) {
           const bf16_t* other = reinterpret_cast<const bf16_t*>(D + (size_t)sl * VP * 128);
 #pragma unroll 2
           for (int i = tid; i < VP * 8; i += kThreads) {
@@ -498,7 +521,7 @@ __global__ void __launch_bounds__(128 * kQ, kQ == 2 ? 2 : 1) grad_kernel(const _
 
 template <typename T, int KP, int VP, bool kShared>
 cudaError_t launch(const Maps& maps, const Args& a, cudaStream_t stream) {
-  // two blocks of 256 threads an SM where they fit, else one of 512 (4 x 4096 x 32 x 64: 176 us for 281)
+  // two blocks of 256 threads an SM where they fit, else one of 512 (4 x 4096 x 32 x 64: 176 us for 281 when it was measured)
   constexpr int kQ = sizeof(T) == 2 && KP == 64 && VP == 64 && !kShared ? 2 : 4;
   using M = Smem<T, KP, VP, kQ, kDecaySets<T, kShared>>;
   static_assert(sizeof(M) <= 232448, "shared memory of a block");
