@@ -8,7 +8,7 @@
 // the state, an fp32 result, in three parts (24 bits).
 //
 // Eight warps make P and the rows that leave, eight at the same time u . x and the state; one brings the tiles of a chunk
-// to come (TMA), one forms its decays, one issues the products.
+// to come (TMA), one forms its decays and says which chunks follow, one issues the products.
 // For the gradients (linattn_grad.cu) the state before each chunk leaves as the tiles that products read, its pair
 // and a third part, by bulk copies. With up to 64 keys
 // the scores of chunk i + 1 are made and decayed while the other products of chunk i run (three stages of
@@ -46,7 +46,7 @@ __device__ __forceinline__ bool claimed_block(const uint4* reply, unsigned& bloc
 constexpr int kTeam = 256, kThreads = 2 * kTeam + 96;
 constexpr int kBringWarp = 16, kDecayWarp = 17;  // and 18 issues
 
-// A chunk of the block's run, on the way from the warp that brings the tiles to all others.
+// A chunk of the block's run, as the warp of the decays tells all others, four ahead.
 struct alignas(16) Step {
   int live, last, len;   // there is one; of its sequence or segment (for this head and slice); its tokens, 0 for a sequence of none
   int b, t;              // batch row, first token

@@ -390,6 +390,30 @@ def test_many_short_packed_sequences(env, dtype, K, V, Hk, Hv):
     _close("dS_init", out["dS_init"], np.concatenate([x["dS_init"] for x in bwd]))
 
 
+@pytest.mark.parametrize("dtype,K,Hv", [(BF16, 64, 4), (BF16, 128, 5), (F32, 64, 4)])
+def test_many_short_sequences_do_not_meet(env, dtype, K, Hv):
+    """Which block takes which sequence changes no bit, and what is not a number stays in its sequence and head."""
+    _, la = env
+    lengths = [3, 140, 0, 129, 60] * 13
+    starts = np.concatenate(([0], np.cumsum(lengths))).tolist()
+    d = _make(1, starts[-1], 1, Hv, K, 64, dtype, 24, states=len(lengths))
+    want = _raw(la, d, starts)
+    again = _raw(la, d, starts)
+    assert all(torch.equal(want[m], again[m]) for m in want)
+    bad = [(1, 0), (10, 2), (35, 1), (61, 3)]  # sequences (of any length above 0) and heads
+    for s, h in bad:
+        assert lengths[s] > 0
+        d["v"][0, starts[s], h] = float("nan") if s % 2 else float("inf")
+        d["do"][0, starts[s], h] = float("nan")
+    got = _raw(la, d, starts)
+    for m in ("o", "dv", "s_final", "dS_init", "dg"):
+        keep = torch.ones(want[m].shape[:2] if m in ("s_final", "dS_init") else want[m].shape[1:3], dtype=torch.bool, device="cuda")
+        for s, h in bad:
+            keep[s if m in ("s_final", "dS_init") else slice(starts[s], starts[s + 1]), h] = False
+        x, y = (t if m in ("s_final", "dS_init") else t[0] for t in (want[m], got[m]))
+        assert torch.equal(x[keep], y[keep]), m
+
+
 @pytest.mark.parametrize("dtype,Hk,Hv,K,T,starts,fixed", [
     (BF16, 1, 2, 64, 100, [0, 40, 70], False),
     (F32, 2, 2, 72, 333, [10, 40, 40, 70], False),

@@ -204,6 +204,21 @@ def test_another_stream_a_graph_and_the_same_bits(env, dtype):
     assert all(torch.equal(x, y) for x, y in zip(want, again))
 
 
+@BOTH
+def test_values_that_are_not_numbers_stay_in_their_row(env, dtype):
+    _, qr = env
+    d = _make(500, 6, 3, 64, 32, dtype, 11)
+    run = lambda: (*qr.forward(*(d[n] for n in ARGS), d["positions"]),
+                   *(qr.backward(*(d[n] for n in ARGS), d["dq"], d["dk"], d["positions"])[n] for n in ("dq", "dk")))
+    want = run()
+    keep = torch.ones(500, 6, dtype=torch.bool, device="cuda")
+    for t, h in ((0, 0), (17, 5), (499, 2)):
+        d["q"][t, h, 5], keep[t, h] = float("nan"), False
+    d["dq"][250, 1, 60], keep[250, 1] = float("inf"), False
+    got = run()
+    assert all(torch.equal(x[keep] if x.shape[1] == 6 else x, y[keep] if y.shape[1] == 6 else y) for x, y in zip(want, got))
+
+
 def test_refusals(env):
     _, qr = env
     d = _make(8, 4, 2, 64, 32, BF16, 10)
