@@ -109,10 +109,11 @@ def forward(q, k, v, g, s_init=None, *, scale: float | None = None, seq_starts=N
         _check_tensor("s_init", s_init, (n, Hv, V, K), torch.float32, dev)
     o = torch.empty((B, T, Hv, V), dtype=q.dtype, device=dev)
     s_final = torch.empty((n, Hv, V, K), dtype=torch.float32, device=dev) if want_s_final else None
-    saved = torch.empty(_saved_bytes(B, T, Hk, Hv, K, V, nseq, bf16, int(want_saved)), dtype=torch.uint8, device=dev)
+    need = _saved_bytes(B, T, Hk, Hv, K, V, nseq, bf16, int(want_saved))
+    saved = torch.empty(need, dtype=torch.uint8, device=dev) if need or want_saved else None
     rc = lib.linattn_forward(
         q.data_ptr(), k.data_ptr(), v.data_ptr(), g.data_ptr(), _addr(s_init), _addr(seq_starts), o.data_ptr(), _addr(s_final),
-        saved.data_ptr(), _strides(q, k, v), K ** -0.5 if scale is None else scale, fixed, want_saved, B, T, Hk, Hv, K, V, nseq,
+        _addr(saved), _strides(q, k, v), K ** -0.5 if scale is None else scale, fixed, want_saved, B, T, Hk, Hv, K, V, nseq,
         bf16, gdr._raw_stream(dev.index))
     if rc:
         wkv7._check(rc)

@@ -46,6 +46,16 @@ def load(path: str | None = None):
     return lib
 
 
+def _tokens(name, t):
+    """(tokens, elements from token to token)."""
+    if t.dim() == 3:  # the usual form, checked at less cost
+        tokens, _, D = t.shape
+        a, b, c = t.stride()
+        if c == 1 and b == D:
+            return tokens, a
+    return _rows(name, t, 2)
+
+
 def _inputs(q, k, q_weight, k_weight, freq, positions):
     """The inputs checked: bf16, (q's, k's token stride, tokens, T, Hq, Hk, D, half), device."""
     torch = gdr._torch
@@ -65,7 +75,7 @@ def _inputs(q, k, q_weight, k_weight, freq, positions):
     if positions is not None and not (positions.shape == qs[:-2] and positions.dtype is torch.int32 and positions.device == dev
                                       and positions.is_contiguous()):
         _check_tensor("positions", positions, qs[:-2], torch.int32, dev)
-    (nq, qt), (nk, kt) = _rows("q", q, 2), _rows("k", k, 2)
+    (nq, qt), (nk, kt) = _tokens("q", q), _tokens("k", k)
     return bf16, (qt, kt, max(nq, nk), qs[-3], qs[-2], ks[-2], D, half), dev  # (without heads a tensor has no rows)
 
 
