@@ -139,8 +139,8 @@ __global__ void __launch_bounds__(128 * kQ, kQ == 2 ? 2 : 1) grad_kernel(const _
     return static_cast<const char*>(images) + ((size_t)slot * s.Hv + hv) * image_bytes(s.K, s.V);
   };
   // 64 keys of a state. (What was there has been read: the products that did are waited for.)
-  auto fetch = [&](const char* from, int sl) {
-    if (tid == 0) {
+  auto fetch = [&](const char* from, int sl, int who = 0) {
+    if (tid == who) {
       wkv7::mbar_arrive_expect_tx(&sm.full[1], sizeof sm.s);
 #pragma unroll
       for (int part = 0; part < 3; ++part)
@@ -342,6 +342,21 @@ __global__ void __launch_bounds__(128 * kQ, kQ == 2 ? 2 : 1) grad_kernel(const _
       }
       if (!kUpper && kF32) fetched(0);  // (while the products of parts run)
       if (!kUpper && ready) __syncthreads();  // the decays
+      // The other 64 keys come while the scores are decayed: brought by a warp that has none (S: once <S, D> has read its first half).
+      if (kEarlyIn) {
+        if (kUpper) {
+          ++turn3;  // (the products that read D wait for it, and who brings the rest for them)
+        } else {
+          fetched(0);
+          __syncthreads();
+        }
+        constexpr int kWho = kUpper ? 1 : 4;
+        if (warp == kWho) {
+          wait(&sm.done[2], turn4);
+          fetch(kUpper ? D : S, 1, 32 * kWho);
+        }
+        ++turn4;
+      }
       wait(&sm.done[0], turn0++);
       tmem_fence_after_sync();
       if (kF32 && !kUpper && hv == first && sub == 0 && part_of) ahead(part_of - 1, kQ - 1);  // (these have nothing else to do now)
@@ -371,13 +386,11 @@ __global__ void __launch_bounds__(128 * kQ, kQ == 2 ? 2 : 1) grad_kernel(const _
           store_zeros<kA>(mine + kAt + 16 * kA * blk);
         }
       }
-      if (kUpper || !kF32) fetched(0);
+      if (!kEarlyIn && (kUpper || !kF32)) fetched(0);
       if (!kUpper && dg) ++turn5;
-      if (kEarlyIn) wait(&sm.done[2], turn4++);
       wkv7::tmem_wait_st();
       tmem_fence_before_sync();
       __syncthreads();
-      if (kEarlyIn) fetch(kUpper ? D : S, 1);
       if (warp == 0) {
         tmem_fence_after_sync();
         if (elected()) {
