@@ -17,7 +17,7 @@
 //
 // Bound by latency: a chunk's tiles and states come, are multiplied, decayed, multiplied again and read out, twice, one
 // step after the other, with one block an SM but for bfloat16's heads of 64. Measured: 4 x 4096 x 32 x 64 bfloat16 168 us
-// (605 MB with the states' images: 3.6 TB/s), 2 x 4095 x 16 and 32 x 128 225 us (670 MB, 3.0 TB/s), fp32 8 x 4096 x 12 x 64
+// (605 MB with the states' images: 3.6 TB/s), 2 x 4095 x 16 and 32 x 128 220 us (670 MB, 3.0 TB/s), fp32 8 x 4096 x 12 x 64
 // 361 us (755 MB, 2.1 TB/s; six products of parts for each product, 105 us of them at the tensor cores' rate).
 #include <type_traits>
 
