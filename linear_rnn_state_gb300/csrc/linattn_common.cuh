@@ -188,19 +188,28 @@ __device__ __forceinline__ void zero(float (&x)[N][4]) {
 template <int kP, int kRows, typename T>
 __device__ __forceinline__ void fill_tile(bf16_t* dst, const T* src, long long stride, int len, int cols, const float* w,
                                           int tid, int threads) {
-  const int pieces = ((cols + 63) >> 6) * 8, part = pieces * 8 * kRows;
-  for (int i = tid; i < kRows * pieces; i += threads) {
-    const int row = i / pieces, col = (i - row * pieces) * 8;
-    float x[8] = {0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f};
-    if (row < len && col < cols) {
-      load8(x, src + row * stride + col);
+  constexpr int kBatch = 8;  // loads on their way together
+  const int shift = cols > 64 ? 4 : 3, total = kRows << shift, part = total * 8;
+  for (int i0 = tid; i0 < total; i0 += kBatch * threads) {
+    float x[kBatch][8];
+#pragma unroll
+    for (int b = 0; b < kBatch; ++b) {
+      const int i = i0 + b * threads, row = i >> shift, col = (i - (row << shift)) * 8;
+#pragma unroll
+      for (int e = 0; e < 8; ++e) x[b][e] = 0.f;
+      if (row < len && col < cols) load8(x[b], src + row * stride + col);  // (len <= kRows)
+    }
+#pragma unroll
+    for (int b = 0; b < kBatch; ++b) {
+      const int i = i0 + b * threads, row = i >> shift, col = (i - (row << shift)) * 8;
+      if (i >= total) break;
       if (w) {
         const float f = w[row];
 #pragma unroll
-        for (int e = 0; e < 8; ++e) x[e] *= f;
+        for (int e = 0; e < 8; ++e) x[b][e] *= f;
       }
+      put8<kP>(dst + at(kRows, row, col), part, x[b]);
     }
-    put8<kP>(dst + at(kRows, row, col), part, x);
   }
 }
 
