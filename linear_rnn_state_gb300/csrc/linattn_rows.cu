@@ -19,7 +19,7 @@
 namespace linattn {
 namespace {
 
-constexpr int kThreads = 128, kC = kCF32;
+constexpr int kThreads = 256, kC = kCF32;
 enum Mode { kO, kDv, kDq, kDk };
 
 template <typename T>
@@ -46,7 +46,7 @@ struct Layout {
   __host__ __device__ static constexpr size_t x(int D) { return 2 * b(D); }
   __host__ __device__ static constexpr size_t s(int D) { return x(D) + (size_t)kP * kC * 64 * 2; }
   __host__ __device__ static constexpr size_t g(int D) { return s(D) + (size_t)kStateParts * 64 * D * 2; }
-  __host__ __device__ static constexpr size_t size(int D) { return g(D) + kC * 8 + kC * 4 + 6 * kC * 4; }
+  __host__ __device__ static constexpr size_t size(int D) { return g(D) + kC * 8 + kC * 4 + 7 * kC * 4; }
 };
 
 // rows += a b^T of the warp's 16 rows and the columns that the mask leaves it.
@@ -66,8 +66,9 @@ __device__ __forceinline__ void scores(float (&x)[8][4], const bf16_t* as, const
   }
 }
 
-// A block: a chunk and a value head (o, dv), or a key head with all its value heads (dq, dk). 16 tokens a
-// warp; kSlices x 64 columns of the output.
+// A block: a chunk and a value head (o, dv), or a key head with all its value heads (dq, dk). 16 tokens and half of each
+// 64 columns of the output a warp; kSlices x 64 columns. (One block's tiles fill shared memory. Both warps of 16 tokens make
+// their scores: four warps that made each once took 436 us for o at 2 x 4096 x 16 x 128.)
 template <typename T, int kMode, int kSlices>
 __global__ void __launch_bounds__(kThreads) rows_kernel(const Args a) {
   constexpr bool kUpper = kMode == kDv || kMode == kDk, kKeys = kMode == kDq || kMode == kDk;  // kKeys: the output is a key's
@@ -82,8 +83,8 @@ __global__ void __launch_bounds__(kThreads) rows_kernel(const Args a) {
   bf16_t* ss = reinterpret_cast<bf16_t*>(smem + L::s(Dp));
   float2* G = reinterpret_cast<float2*>(smem + L::g(Dp));
   float* w = reinterpret_cast<float*>(G + kC);
-  float* red = w + kC;  // [6][kC]: dg of the warps' rows, the rows' terms, the state's
-  const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5, gr = lane >> 2, tq = lane & 3;
+  float* red = w + kC;  // [7][kC]: dg of the warps' rows, the rows' terms by halves, the state's
+  const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5 & 3, half = tid >> 7, gr = lane >> 2, tq = lane & 3;
   const int heads = kKeys ? s.Hk : s.Hv, head = blockIdx.x % heads, slot = blockIdx.x / heads, group = s.Hv / s.Hk;
   ChunkAt c;
   if (!chunk_at(s, slot, kC, c)) return;
@@ -103,7 +104,7 @@ __global__ void __launch_bounds__(kThreads) rows_kernel(const Args a) {
     const float* state = (kUpper ? a.dstates : a.states) + ((size_t)slot * s.Hv + hv) * s.V * s.K;
     const bool dg = kKeys && a.dg;
     __syncthreads();  // the head before is done with shared memory
-    if (warp == 0) {
+    if (tid < 32) {
       running_sums<2>(G, s.fixed ? a.g + hv : a.g + tok * s.Hv + hv, s.fixed ? 0 : s.Hv, c.len, lane);
       __syncwarp();
 #pragma unroll
@@ -122,12 +123,12 @@ __global__ void __launch_bounds__(kThreads) rows_kernel(const Args a) {
           fill_tile<kP, kC>(as, q.p + 64 * h, q.stride, c.len, h ? s.K - 64 : 64, nullptr, tid, kThreads);
           fill_tile<kP, kC>(bs, k.p + 64 * h, k.stride, c.len, h ? s.K - 64 : 64, nullptr, tid, kThreads);
           __syncthreads();
-          float half[8][4];
-          scores<kP, false>(half, as, bs, h ? s.K - 64 : 64, 64, warp, lane);
+          float part[8][4];
+          scores<kP, false>(part, as, bs, h ? s.K - 64 : 64, 64, warp, lane);
 #pragma unroll
           for (int n = 0; n < 8; ++n)
 #pragma unroll
-            for (int e = 0; e < 4; ++e) qk[n][e] = h ? qk[n][e] + half[n][e] : half[n][e];
+            for (int e = 0; e < 4; ++e) qk[n][e] = h ? qk[n][e] + part[n][e] : part[n][e];
           __syncthreads();
         }
       }
@@ -183,7 +184,7 @@ __global__ void __launch_bounds__(kThreads) rows_kernel(const Args a) {
           x += __shfl_xor_sync(0xffffffffu, x, 4);
           x += __shfl_xor_sync(0xffffffffu, x, 8);
           x += __shfl_xor_sync(0xffffffffu, x, 16);
-          if (gr == 0) red[warp * kC + 8 * n + 2 * tq + e] = x;
+          if (gr == 0 && half == 0) red[warp * kC + 8 * n + 2 * tq + e] = x;
         }
     }
     float dots[2] = {0.f, 0.f}, whole = 0.f;
@@ -212,7 +213,7 @@ __global__ void __launch_bounds__(kThreads) rows_kernel(const Args a) {
       __syncthreads();
 #pragma unroll
       for (int n = 0; n < 4; ++n)
-        if (16 * n < xn) {
+        if ((n >> 1) == half && 16 * n < xn) {
           float y0[4] = {0.f, 0.f, 0.f, 0.f}, y1[4] = {0.f, 0.f, 0.f, 0.f};
           for (int k0 = 0; k0 < D; k0 += 16) {
             Frag<kP> fa;
@@ -263,17 +264,17 @@ __global__ void __launch_bounds__(kThreads) rows_kernel(const Args a) {
         float x = dots[h];
         x += __shfl_xor_sync(0xffffffffu, x, 1);
         x += __shfl_xor_sync(0xffffffffu, x, 2);
-        if (tq == 0) red[4 * kC + 16 * warp + gr + 8 * h] = x;
+        if (tq == 0) red[(4 + half) * kC + 16 * warp + gr + 8 * h] = x;
       }
       if (kMode == kDq) {
 #pragma unroll
         for (int o = 16; o >= 1; o >>= 1) whole += __shfl_xor_sync(0xffffffffu, whole, o);
-        if (lane == 0) red[5 * kC + warp] = whole;
+        if (lane == 0) red[6 * kC + 4 * half + warp] = whole;
       }
       __syncthreads();
-      if (warp == 0) {  // two tokens a lane
+      if (tid < 32) {  // two tokens a lane
         float* out = a.dg + tok * s.Hv + hv;
-        const float x0 = red[4 * kC + 2 * lane], x1 = red[4 * kC + 2 * lane + 1];
+        const float x0 = red[4 * kC + 2 * lane] + red[5 * kC + 2 * lane], x1 = red[4 * kC + 2 * lane + 1] + red[5 * kC + 2 * lane + 1];
         float run = x0 + x1;
 #pragma unroll
         for (int o = 1; o < 32; o <<= 1) {
@@ -283,7 +284,12 @@ __global__ void __launch_bounds__(kThreads) rows_kernel(const Args a) {
         float other = kMode == kDq ? __shfl_down_sync(0xffffffffu, run, 1) : __shfl_up_sync(0xffffffffu, run, 1);
         if (lane == (kMode == kDq ? 31 : 0)) other = 0.f;
         const float y0 = kMode == kDq ? run : other, y1 = kMode == kDq ? other + x1 : other + x0;
-        const float pass = kMode == kDq ? expf(G[kC - 1].x + G[kC - 1].y) * ((red[5 * kC] + red[5 * kC + 1]) + (red[5 * kC + 2] + red[5 * kC + 3])) : 0.f;
+        float pass = 0.f;
+        if (kMode == kDq) {
+#pragma unroll
+          for (int i = 0; i < 8; ++i) pass += red[6 * kC + i];
+          pass *= expf(G[kC - 1].x + G[kC - 1].y);
+        }
 #pragma unroll
         for (int e = 0; e < 2; ++e) {
           const int t = 2 * lane + e;
@@ -311,7 +317,7 @@ __global__ void __launch_bounds__(kThreads) rows_kernel(const Args a) {
 #pragma unroll
       for (int h = 0; h < 2; ++h) {
         const int row = 16 * warp + gr + 8 * h, col = 64 * sl + 8 * n + 2 * tq;
-        if (row < c.len && col < Dx) store2(out + (size_t)row * heads * Dx + col, acc[sl][n][2 * h], acc[sl][n][2 * h + 1]);
+        if ((n >> 2) == half && row < c.len && col < Dx) store2(out + (size_t)row * heads * Dx + col, acc[sl][n][2 * h], acc[sl][n][2 * h + 1]);
       }
 }
 
