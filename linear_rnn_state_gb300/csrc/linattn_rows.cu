@@ -13,7 +13,8 @@
 // all of them sums: no differences of large ones.
 //
 // For fp32 heads above 64: three parts of the four tiles of a chunk (393 KB at 128) would not fit the shared memory that
-// tcgen05 reads, so products are mma.sync's, of 64 tokens and 64 columns at a time.
+// tcgen05 reads, so products are mma.sync's, of 64 tokens and 64 columns at a time. Bound by latency with eight warps
+// an SM: 2 x 4096 x 16 x 128 takes 269 us for o, 266 dv, 475 dq and dg, 361 dk.
 #include "linattn_common.cuh"
 
 namespace linattn {
@@ -68,7 +69,7 @@ __device__ __forceinline__ void scores(float (&x)[8][4], const bf16_t* as, const
 
 // A block: a chunk and a value head (o, dv), or a key head with all its value heads (dq, dk). 16 tokens and half of each
 // 64 columns of the output a warp; kSlices x 64 columns. (One block's tiles fill shared memory. Both warps of 16 tokens make
-// their scores: four warps that made each once took 436 us for o at 2 x 4096 x 16 x 128.)
+// their scores: four warps that made each once took 436 us for 327 for o at 2 x 4096 x 16 x 128.)
 template <typename T, int kMode, int kSlices>
 __global__ void __launch_bounds__(kThreads) rows_kernel(const Args a) {
   constexpr bool kUpper = kMode == kDv || kMode == kDk, kKeys = kMode == kDq || kMode == kDk;  // kKeys: the output is a key's
@@ -194,21 +195,31 @@ __global__ void __launch_bounds__(kThreads) rows_kernel(const Args a) {
       __syncthreads();
       fill_tile<kP, kC>(xs, tx.p + x0, tx.stride, c.len, xn, nullptr, tid, kThreads);
       // the state's slice: rows of values and 64 keys (kKeys), or 64 rows and all keys
-      const int rows = kKeys ? Dp : 64, pieces = kKeys ? 8 : Dp / 8;
-      for (int i = tid; i < rows * pieces; i += kThreads) {
-        const int r = i / pieces, col = (i - r * pieces) * 8;
-        const int sr = kKeys ? r : x0 + r, scol = kKeys ? x0 + col : col;
-        float f[8] = {0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f};
-        if (sr < s.V && scol < s.K) {
-          load8(f, state + (size_t)sr * s.K + scol);
-          if (kMode == kDq && dg) {
+      const int rows = kKeys ? Dp : 64, shift = kKeys || Dp == 64 ? 3 : 4, total = rows << shift;
+      constexpr int kBatch = 4;  // loads on their way together
+      for (int i0 = tid; i0 < total; i0 += kBatch * kThreads) {
+        float f[kBatch][8];
+#pragma unroll
+        for (int b = 0; b < kBatch; ++b) {
+          const int i = i0 + b * kThreads, r = i >> shift, col = (i - (r << shift)) * 8;
+          const int sr = kKeys ? r : x0 + r, scol = kKeys ? x0 + col : col;
+#pragma unroll
+          for (int e = 0; e < 8; ++e) f[b][e] = 0.f;
+          if (i < total && sr < s.V && scol < s.K) load8(f[b], state + (size_t)sr * s.K + scol);
+        }
+#pragma unroll
+        for (int b = 0; b < kBatch; ++b) {
+          const int i = i0 + b * kThreads, r = i >> shift, col = (i - (r << shift)) * 8;
+          if (i >= total) break;
+          const int sr = kKeys ? r : x0 + r, scol = kKeys ? x0 + col : col;
+          if (kMode == kDq && dg && sr < s.V && scol < s.K) {
             float f2[8];
             load8(f2, a.dstates + ((size_t)slot * s.Hv + hv) * s.V * s.K + (size_t)sr * s.K + scol);
 #pragma unroll
-            for (int e = 0; e < 8; ++e) whole = fmaf(f[e], f2[e], whole);
+            for (int e = 0; e < 8; ++e) whole = fmaf(f[b][e], f2[e], whole);
           }
+          put8<kPs>(ss + at(rows, r, col), 64 * Dp, f[b]);
         }
-        put8<kPs>(ss + at(rows, r, col), 64 * Dp, f);
       }
       __syncthreads();
 #pragma unroll
