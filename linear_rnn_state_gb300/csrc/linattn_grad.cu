@@ -419,7 +419,12 @@ __global__ void __launch_bounds__(128 * kQ, kQ == 2 ? 2 : 1) grad_kernel(const _
         }
       }
       if (kEarlyIn) {
-        fetched(1);
+        // (Shared heads' upper phase: who reads D are the products, and warp 0 has waited for it. A wait of the others here
+        // could come after the next head's S has been asked for, and would then see neither copy's phase.)
+        if (kUpper && kShared)
+          ++turn3;
+        else
+          fetched(1);
         if (!kShared) __syncthreads();  // <S, D> has been read: rows take its place
       }
       wait(&sm.done[1], turn1++);
