@@ -18,7 +18,7 @@ struct Sizes {
 int check(Sizes* z, Args& p, long long tokens, long long T, int es) {
   if (tokens < 0 || p.Hq < 0 || p.Hk < 0) return fail(WKV7_ERR_INVALID, "tokens and heads must be >= 0 (got %lld, %d, %d)", tokens, p.Hq, p.Hk);
   if (p.D < 8 || p.D > kMaxD || p.D % 8) return fail(WKV7_ERR_INVALID, "D must be a multiple of 8 from 8 to %d (got %d)", kMaxD, p.D);
-  if (p.half < 0 || 2 * p.half > p.D) return fail(WKV7_ERR_INVALID, "half must be 0 to D / 2 (got %d of %d)", p.half, p.D);
+  if (p.half < 0 || p.half > p.D / 2) return fail(WKV7_ERR_INVALID, "half must be 0 to D / 2 (got %d of %d)", p.half, p.D);
   if (!p.positions && tokens && (T < 1 || T > 1ll << 31)) return fail(WKV7_ERR_INVALID, "T must be 1 to 2^31 without positions (got %lld)", T);
   const unsigned long long H = (unsigned long long)p.Hq + p.Hk;
   if (tokens >= 1ll << 31 || H >= 1ull << 20 || (unsigned long long)tokens * H >= 1ull << 31 || (unsigned long long)tokens * H * p.D * 4 >= kMaxBytes)

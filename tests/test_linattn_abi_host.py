@@ -182,6 +182,15 @@ def test_rotation_rejects_invalid_arguments(libs, case, over):
     assert _rope(lib, "qkrope_backward", ROPE_B, over) == -2
 
 
+@pytest.mark.parametrize("half", [(1 << 31) - 1, 1 << 30, (1 << 30) + 5])
+def test_rotation_rejects_counts_of_pairs_past_32_bits(libs, half):
+    """Twice the number is below 0 or small in 32 bits."""
+    lib = libs[1].load()
+    assert _rope(lib, "qkrope_forward", ROPE_F, {"half": half, "freq": FAKE + 1000 * GB}) == -2
+    assert _rope(lib, "qkrope_backward", ROPE_B, {"half": half, "freq": FAKE + 1000 * GB}) == -2
+    assert "half" in libs[1].wkv7.last_error()
+
+
 def test_rotation_rejects_mismatched_buffers(libs):
     lib = libs[1].load()
     assert _rope(lib, "qkrope_forward", ROPE_F, {"q_out": FAKE}) == -2  # over q
