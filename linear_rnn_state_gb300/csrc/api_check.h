@@ -1,4 +1,4 @@
-// Argument checks shared by the C entry points of gdr.h and blocknorm.h.
+// Argument checks shared by the C entry points of gdr.h, blocknorm.h, linattn.h and qkrope.h.
 #pragma once
 
 #include <stdarg.h>
@@ -33,6 +33,14 @@ struct Span {
   bool required;
   unsigned align = 16;
 };
+
+// Bytes from a tensor's first value to its last row's end: n steps of a and m of b elements, then a row of `row`. What does not fit
+// 64 bits is the largest number there is.
+inline unsigned long long span_bytes(unsigned long long n, unsigned long long a, unsigned long long m, unsigned long long b,
+                                     unsigned long long row, int es) {
+  const unsigned __int128 x = ((unsigned __int128)n * a + (unsigned __int128)m * b + row) * (unsigned)es;
+  return x > ~0ull ? ~0ull : (unsigned long long)x;
+}
 
 inline bool overlaps(const Span& x, const Span& y) {
   if (!x.p || !y.p || !x.bytes || !y.bytes) return false;

@@ -22,7 +22,7 @@ int check_dims(long long rows, int H, int D) {
 int span_bytes(unsigned long long* out, long long* stride, long long rows, long long row, int es, const char* name) {
   if (rows <= 1) *stride = row;
   if (*stride < row || *stride >= 1ll << 40) return fail(WKV7_ERR_INVALID, "%s: rows of %lld values %lld apart", name, row, *stride);
-  *out = rows ? ((unsigned long long)(rows - 1) * *stride + row) * es : 0;
+  *out = rows ? api::span_bytes(rows - 1, *stride, 0, 0, row, es) : 0;
   return *out < kMaxBytes ? WKV7_OK : fail(WKV7_ERR_INVALID, "%s too large", name);
 }
 int check_types(int bf16, int residual_bf16) {

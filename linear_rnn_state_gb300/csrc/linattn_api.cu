@@ -39,7 +39,7 @@ int set_strides(long long (&out)[6], unsigned long long (&bytes)[3], const long 
     if (B <= 1) b = 0;
     if (T <= 1) t = 0;
     out[2 * i] = b, out[2 * i + 1] = t;
-    bytes[i] = B && T && Hv ? ((unsigned long long)(B - 1) * b + (unsigned long long)(T - 1) * t + row[i]) * es : 0;
+    bytes[i] = B && T && Hv ? api::span_bytes(B - 1, b, T - 1, t, row[i], es) : 0;
     if (bytes[i] >= kMaxBytes) return fail(WKV7_ERR_INVALID, "%s too large", names[i]);
   }
   return WKV7_OK;

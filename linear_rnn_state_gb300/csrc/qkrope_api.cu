@@ -31,7 +31,7 @@ int check(Sizes* z, Args& p, long long tokens, long long T, int es) {
     if (tokens <= 1 || !row) *strides[i] = row;
     if (*strides[i] < row || *strides[i] % 8 || *strides[i] >= 1ll << 40)
       return fail(WKV7_ERR_INVALID, "%s: tokens of %lld values %lld apart (a multiple of 8, at least the heads)", i ? "k" : "q", row, *strides[i]);
-    *spans[i] = tokens && row ? ((unsigned long long)(tokens - 1) * *strides[i] + row) * es : 0;
+    *spans[i] = tokens && row ? api::span_bytes(tokens - 1, *strides[i], 0, 0, row, es) : 0;
     if (*spans[i] >= kMaxBytes) return fail(WKV7_ERR_INVALID, "%s too large", i ? "k" : "q");
   }
   z->qd = (unsigned long long)tokens * p.Hq * p.D * es, z->kd = (unsigned long long)tokens * p.Hk * p.D * es;
