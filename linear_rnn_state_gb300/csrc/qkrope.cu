@@ -311,7 +311,9 @@ __global__ void __launch_bounds__(kThreads, 2) backward_kernel(const Args p, uns
       rotate<kHow, kGroup, true>(d, turn, cs, c, p.half, lane, line);
 #pragma unroll
       for (int e = 0; e < 4; ++e) s2 = fma2(v[e], v[e], s2), c1 = fma2(mul2(d[e], w[e]), v[e], c1);
-      const float r = inverse_root(fmaf(group_sum<kGroup>(s2.x + s2.y), inv, p.eps));
+      // (places without a head hold rows of zeros: they add nothing to dw, whatever eps is)
+      const float mean = fmaf(group_sum<kGroup>(s2.x + s2.y), inv, p.eps);
+      const float r = u0 + group < units && i < x.heads ? inverse_root(mean) : 0.f;
       const float m = -(group_sum<kGroup>(c1.x + c1.y) * r * inv);
       const float2 rr = make_float2(r, r), mm = make_float2(m, m);
 #pragma unroll
@@ -324,7 +326,7 @@ __global__ void __launch_bounds__(kThreads, 2) backward_kernel(const Args p, uns
     }
 #pragma unroll
     for (int e = 0; e < 4; ++e) {
-      // (units past the last repeat it with rows of zeros)
+      // (units past the last repeat it, its rows' sums being zeros)
       if (x.key)
         dwk[e].x += dw[e].x, dwk[e].y += dw[e].y;
       else

@@ -247,6 +247,15 @@ def test_refusals(env):
         qr.backward(*ins, d["dq"][:4], d["dk"], d["positions"])
 
 
+@BOTH
+@pytest.mark.parametrize("eps", [0.0, 1e-2])
+@pytest.mark.parametrize("tokens,Hq,Hk,D", [(5, 3, 2, 64), (37, 3, 2, 24), (600, 33, 9, 64), (2500, 6, 2, 128), (1, 1, 1, 256)])
+def test_other_eps(env, tokens, Hq, Hk, D, eps, dtype):
+    """Also none at all: places of a block without a head, and heads that do not fill a unit, add nothing to the weights'
+    gradients (rows of zeros there have no norm where eps is 0)."""
+    _check(env, _make(tokens, Hq, Hk, D, D // 4, dtype, tokens + D), eps=eps)
+
+
 # ------------------------------------------------------------- a layer of them all ---
 
 
