@@ -1,5 +1,6 @@
 // C ABI of linear attention with a decay (linattn.h): argument checks, the
 // regions of the caller's buffers, and the launches.
+#include <algorithm>
 #include <initializer_list>
 
 #include "api_check.h"
@@ -81,22 +82,25 @@ struct Place {
 // much as the chain itself in bfloat16 and half of it in fp32, of launches and the join (4 steps' worth, and 6), and of two steps'
 // worth for each block's beginning; they are taken where that saves a tenth of the steps that follow one another. 8192
 // tokens, us whole and in segments: bfloat16 32 heads of 64 150 and 91, 64 heads 150 and 160; fp32 32 heads 347 and 160, 64 heads
-// 351 and 300, 80 heads 359 and 519. (Packed sequences may be one long and many short ones: the longest is taken for
-// three times the mean.)
+// 351 and 300, 80 heads 359 and 519. Of packed sequences the lengths are not known here, and may be alike or one long and
+// some short ones: the longest is taken for three times the mean, or for all there is. 8190 tokens, 32 heads of 64, bfloat16: three
+// alike 67 whole and 121 in segments, one of 7900 and two short ones 154 and 102; six 71 and 126, 153 and 105 (16 heads: 42 and
+// 76, 150 and 66); fp32, three: 134 and 226, 344 and 169. Whole loses more where it loses.
 constexpr int kSms = 152;
 int segment_chunks(const Shape& s, bool bf16) {
   const long long heads = (long long)s.Hv * ((s.V + 63) / 64), lines = heads * s.nseq;
   const int chunks = (s.T + s.C - 1) / s.C;
   if (chunks < 8 || !lines) return 0;
   auto steps = [&](long long blocks, int each) { return (blocks + kSms - 1) / kSms * (each + 2); };
-  const long long total = s.packed ? (s.T / s.C + s.nseq) * heads : chunks * lines;
-  const long long longest = s.packed ? (chunks * 3 + s.nseq - 1) / s.nseq : chunks;
-  const long long whole = s.packed ? (longest > total / kSms ? longest : total / kSms) + 2 : steps(lines, chunks);
+  const bool several = s.packed && s.nseq > 1;  // (one packed sequence is a dense one)
+  const long long total = several ? (s.T / s.C + s.nseq) * heads : chunks * lines;
+  const long long longest = several ? std::min<long long>(chunks, (chunks * 3ll + s.nseq - 1) / s.nseq) : chunks;
+  const long long whole = several ? std::max(longest, total / kSms) + 2 : steps(lines, chunks);
   int best = 0;
   long long least = whole * 9;
   for (int n = 2; n <= 64 && n <= chunks / 2; ++n) {
     const int each = (chunks + n - 1) / n;
-    const long long cost = steps(s.packed ? (total + each - 1) / each : lines * n, each) * (bf16 ? 20 : 15) + (bf16 ? 40 : 60);
+    const long long cost = steps(several ? (total + each - 1) / each : lines * n, each) * (bf16 ? 20 : 15) + (bf16 ? 40 : 60);
     if (cost < least) least = cost, best = each;
   }
   return best;

@@ -49,6 +49,27 @@ def test_buffer_sizes(libs):
     assert lib.linattn_backward_bytes(1, 128, 1, 1, 64, 64, -1, 1, 1) > per_token > 0  # fixed decays: dg of the tokens
 
 
+@pytest.mark.parametrize("bf16,K,V", [(True, 64, 64), (True, 128, 128), (True, 16, 72), (False, 64, 64), (False, 32, 16)])
+def test_one_packed_sequence_is_planned_as_a_dense_one(libs, bf16, K, V):
+    """In segments, which need states of their own, or whole: no more than the sequence is taken for its length. (Were it three
+    times that, 96 heads of 64 and 8192 tokens would go in segments: 100 steps after one another for 66.)"""
+    size = lambda T, H, nseq: libs[0].saved_bytes(1, T, H, H, K, V, nseq, bf16=bf16, for_backward=False)
+    ways = set()
+    for T in (100, 1024, 2100, 4096, 8192, 20000, 65536):
+        for H in (1, 2, 8, 17, 32, 40, 64, 76, 80, 96, 128, 152, 160, 300):
+            dense, packed = size(T, H, -1), size(T, H, 1)
+            assert (dense == 0) == (packed == 0), (T, H)
+            ways.add(dense == 0)
+    assert ways == {True, False}
+
+
+def test_packed_sequences_are_not_longer_than_all_tokens(libs):
+    """Two and three sequences: at most as in one, beside the others."""
+    size = lambda H, nseq: libs[0].saved_bytes(1, 8192, H, H, 64, 64, nseq, bf16=True, for_backward=False)
+    assert all(size(H, n) == 0 for H in (96, 128) for n in (1, 2, 3))
+    assert all(size(4, n) > 0 for n in (1, 2, 3))
+
+
 FWD = ("q", "k", "v", "g", "s_init", "seq_starts", "o", "s_final", "saved")
 BWD = ("q", "k", "v", "g", "d_o", "dS_final", "seq_starts", "saved", "workspace", "dq", "dk", "dv", "dg", "dS_init")
 STEP = ("q", "k", "v", "g", "state", "slots", "o")
