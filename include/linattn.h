@@ -31,10 +31,9 @@
  *
  * Arithmetic. The forward and backward work on chunks of tokens: products run on
  * the tensor cores with operands as sums of bfloat16 parts and fp32 accumulation.
- * bfloat16 inputs are exact in one part, what is computed of them is held in two (16 bits)
- * where it enters a bfloat16 result and in three (24 bits) where it enters a state, its
- * gradient or dg; fp32 inputs are held in three. States, sums and decays are fp32. Parts
- * have fp32's exponents: no value loses bits beside a larger one. A value of infinity or
+ * bfloat16 inputs are exact in one part, fp32 inputs and what is computed are held in three
+ * (24 bits); bfloat16 outputs are fp32 results rounded once. States, sums and decays are
+ * fp32. Parts have fp32's exponents: no value loses bits beside a larger one. A value of infinity or
  * NaN makes its chunk and those after it (before it, for gradients) non-finite in its
  * head. (linattn_step computes in fp32 throughout.)
  *

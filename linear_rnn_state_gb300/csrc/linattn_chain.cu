@@ -4,13 +4,14 @@
 // its chunks of 128 tokens with the state in registers. With a, b, x = q, k, v forward and k, q, do
 // backward (there in reverse, the state being the gradient D of the state after the chunk):
 //   P = mask . decay . (a b^T),  out = P x + w . (a S^T),  S <- e^{Gc} S + (u . x)^T b
-// P x and a S^T end as bfloat16 values, so P and S enter them as pairs of bfloat16 (16 bits); u . x enters
-// the state, an fp32 result, in three parts (24 bits).
+// P, S and u . x enter the products in three parts of bfloat16 (24 bits), so that o and dv are fp32 results rounded once. (P and S
+// in pairs, 16 bits, gave another neighbour of the exact value in 2 of 1000 places: 1e-4 in the 2-norm for 2e-5, at 4 % of a chain's
+// time with 64 keys and 14 % with 128.)
 //
 // Eight warps make P and the rows that leave, eight at the same time u . x and the state; one brings the tiles of a chunk
 // to come (TMA), one forms its decays and says which chunks follow, one issues the products.
-// For the gradients (linattn_grad.cu) the state before each chunk leaves as the tiles that products read, its pair
-// and a third part, by bulk copies. With up to 64 keys
+// For the gradients (linattn_grad.cu) the state before each chunk leaves as the tiles that products read, by bulk copies. With
+// up to 64 keys
 // the scores of chunk i + 1 are made and decayed while the other products of chunk i run (three stages of
 // tiles, two places for the scores); wider keys leave room for two stages, and u . x goes by halves of the tokens.
 //
@@ -66,8 +67,8 @@ struct Smem {
   };
   Stage stage[kStages];
   bf16_t xt[3 * kXt * 64];  // u . x
-  bf16_t s[2 * 64 * KP];    // the state's pair
-  bf16_t third[kEarly ? 64 * KP : 8];  // its third part; wider keys: in the place of the keys of the chunk before
+  bf16_t s[2 * 64 * KP];    // two parts of the state
+  bf16_t third[kEarly ? 64 * KP : 8];  // its third; wider keys: in the place of the keys of the chunk before
   Decays d[3];
   Step step[kSteps];
   uint8_t order[kSorted];               // packed sequences, the longest first
@@ -76,6 +77,7 @@ struct Smem {
   uint64_t full[kStages];               // the tiles are there
   uint64_t end;                         // nothing is in flight
   uint64_t scored, first, summed, out;  // the scores; the first half of the state's sum, all of it; the rows
+  uint64_t fed;                         // wider keys: the state before the chunk has been multiplied
   uint32_t tmem;
 };
 
@@ -93,7 +95,7 @@ __global__ void __launch_bounds__(kThreads, 1) chain_kernel(const __grid_constan
   constexpr int kTiles = KP / 16;  // n8 tiles of a warp's half of the keys
   constexpr bool kEarly = M::kEarly;
   constexpr int kSt = M::kStages, kXt = M::kXt;
-  enum { kP = 0, kIn = kEarly ? 256 : 128, kO = kIn + 64, kU = kO + 64, kCols = 512 };
+  enum { kP = 0, kIn = kEarly ? 256 : 128, kO = kIn + 64, kU = kO + 64, kThird = 448, kCols = 512 };
   enum { kBarX = 1, kBarP, kBarX2, kBarPlanes, kBarFree, kBarOut };
   constexpr int kPair = kTeam + 32;  // a team and a warp beside it
   const Shape& s = a.s;
@@ -110,7 +112,7 @@ __global__ void __launch_bounds__(kThreads, 1) chain_kernel(const __grid_constan
   }
   if (warp == 0) wkv7::tmem_alloc(&sm.tmem, kCols);
   if (tid == 0) {
-    for (uint64_t* b : {&sm.scored, &sm.first, &sm.summed, &sm.out, &sm.end, &sm.claimed}) mbar_init(b, 1);
+    for (uint64_t* b : {&sm.scored, &sm.first, &sm.summed, &sm.out, &sm.fed, &sm.end, &sm.claimed}) mbar_init(b, 1);
     for (uint64_t& b : sm.full) mbar_init(&b, 1);
     wkv7::fence_mbar_init();
   }
@@ -248,7 +250,7 @@ __global__ void __launch_bounds__(kThreads, 1) chain_kernel(const __grid_constan
           fence_proxy_async_smem();
         }
       };
-      // the state before chunk i: its pair, and the third part in the place of the keys of the chunk before
+      // the state before chunk i
       char* const images = static_cast<char*>(kUpper ? a.dimages : a.images);
       auto place_of = [&](int i) {
         const Step& w = step(i);
@@ -286,7 +288,10 @@ __global__ void __launch_bounds__(kThreads, 1) chain_kernel(const __grid_constan
         if (kEarly) bring(i + kLead, true);
         if (lane == 0) bulk_wait_read();
         __syncwarp();
-        if (!kEarly) bring(i + kLead, true);
+        if (!kEarly) {  // (where the state's third part has been until now)
+          if (!sums) wait(&sm.fed, i);
+          bring(i + kLead, true);
+        }
         if (!sums) announce(kBarFree, kPair);
         brought(i + kLead);
         live = step(i + 1).live;
@@ -314,20 +319,23 @@ __global__ void __launch_bounds__(kThreads, 1) chain_kernel(const __grid_constan
       tc_commit(&sm.scored);
     };
     auto from_state = [&](int i) {
-      const uint64_t da = desc(sm.stage[i % kSt].a), ds = desc(sm.s);
+      const uint64_t da = desc(sm.stage[i % kSt].a), ds = desc(sm.s), dt = desc(kEarly ? sm.third : sm.stage[(i + kSt - 1) % kSt].b);
 #pragma unroll 1
-      for (int part = 1; part >= 0; --part)
+      for (int part = 2; part >= 0; --part) {
+        const uint64_t d = part == 2 ? dt : ds + part * (64 * KP * 2 >> 4);
 #pragma unroll
-        for (int ks = 0; ks < KP / 16; ++ks)
-          tc_mma(tm + kIn, da + along<kCT>(ks), ds + along<64>(ks) + part * (64 * KP * 2 >> 4), product_of(128, 64, false, false), part == 0 || ks > 0);
+        for (int ks = 0; ks < KP / 16; ++ks) tc_mma(tm + kIn, da + along<kCT>(ks), d + along<64>(ks), product_of(128, 64, false, false), part < 2 || ks > 0);
+      }
     };
     auto from_chunk = [&](int i) {
       const uint64_t dx = desc(sm.stage[i % kSt].x);
 #pragma unroll 1
-      for (int part = 1; part >= 0; --part)
+      for (int part = 2; part >= 0; --part)
 #pragma unroll
-        for (int ks = 0; ks < kCT / 16; ++ks)
-          tc_mma_t(tm + kO, tm + kP + (kEarly ? i % 2 * 128 : 0) + part_at<2>(ks, part), dx + across(ks), product_of(128, 64, false, true), part == 0 || ks > 0);
+        for (int ks = 0; ks < kCT / 16; ++ks) {
+          const int place = kP + (kEarly ? i % 2 * 128 : 0);
+          tc_mma_t(tm + kO, tm + place + two_and_third(ks, part, kThird - place + (ks >> 1) * 16), dx + across(ks), product_of(128, 64, false, true), part < 2 || ks > 0);
+        }
     };
     auto sum = [&](int i, int h) {  // of half h of the tokens
       const uint64_t dx = desc(sm.xt), db = desc(sm.stage[i % kSt].b, kRowPanel) + across(h * (kXt / 16));
@@ -348,6 +356,7 @@ __global__ void __launch_bounds__(kThreads, 1) chain_kernel(const __grid_constan
         if (!kEarly) scores(i);
         if (kEarly && next) scores(i + 1);
         from_state(i);
+        if (!kEarly) tc_commit(&sm.fed);
         if (kEarly) {
           from_chunk(i);
           tc_commit(&sm.out);
@@ -392,21 +401,33 @@ __global__ void __launch_bounds__(kThreads, 1) chain_kernel(const __grid_constan
     const int row = sub * 32 + lane;
     turn();
     const uint32_t mine = sm.tmem + ((uint32_t)(sub * 32) << 16);
-    // The scores of chunk i, decayed, as pairs.
+    // The scores of chunk i, decayed, in three parts. Where there are two places for the scores, there is one for the third parts,
+    // which the chunk before still reads: they are held until its rows are done.
+    uint32_t held[kEarly ? 2 : 1][16];
     auto score = [&](int i) {
       const uint32_t at_p = mine + kP + (kEarly ? i % 2 * 128 : 0);
       wait(&sm.scored, i);
       tmem_fence_after_sync();
 #pragma unroll 1
       for (int blk = half; blk < 4; blk += 2) {
+        uint32_t(&third)[16] = held[kEarly];
+#pragma unroll
+        for (int j = 0; j < 16; ++j) held[0][j] = third[j], third[j] = 0;
         if (kUpper ? blk >= sub : blk <= sub) {
           float x[32];
           tc_read(x, at_p + 32 * blk);
           decayed<kUpper>(x, sm.d[i % 3], row, blk, s.scale);
-          store_parts<2>(at_p + 32 * blk, x);
+          store_two(at_p + 32 * blk, x, third);
         } else {
           store_zeros<2>(at_p + 32 * blk);
         }
+        if (!kEarly) tc_store16(mine + kThird + 16 * blk, third);
+      }
+    };
+    auto stored = [&] {
+      if (kEarly) {
+#pragma unroll
+        for (int b = 0; b < 2; ++b) tc_store16(mine + kThird + 16 * (half + 2 * b), held[kEarly && b]);
       }
       wkv7::tmem_wait_st();
       tmem_fence_before_sync();
@@ -416,8 +437,9 @@ __global__ void __launch_bounds__(kThreads, 1) chain_kernel(const __grid_constan
       if (!sums) {
         if (kEarly) {
           if (live) score(i + 1);
+          if (i < 0) stored();
         } else {
-          score(i);
+          score(i), stored();
           announce(kBarP, kPair);
         }
       }
@@ -429,6 +451,7 @@ __global__ void __launch_bounds__(kThreads, 1) chain_kernel(const __grid_constan
         bf16_t* p = static_cast<bf16_t*>(kUpper ? a.dv : a.o) + (((size_t)to.b * s.T + to.t) * s.Hv + to.hv) * s.V + 64 * to.slice;
         wait(&sm.out, i);
         tmem_fence_after_sync();
+        if (kEarly && live) stored();
         const float w = (kUpper ? d.tail : d.head)[row];
 #pragma unroll
         for (int h = 0; h < 2; ++h) {
@@ -484,7 +507,7 @@ __global__ void __launch_bounds__(kThreads, 1) chain_kernel(const __grid_constan
       const int o = at(64, 16 * sub + (lane & 15), half * (KP / 2) + 8 * t + (lane >> 4) * 8);
       stsm4(sm.s + o, f.p[0]);
       stsm4(sm.s + 64 * KP + o, f.p[1]);
-      if (plan.keep) stsm4(third + o, f.p[2]);
+      stsm4(third + o, f.p[2]);
     }
   };
   float* const states = kUpper ? a.dstates : a.states;

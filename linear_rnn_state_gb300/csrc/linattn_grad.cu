@@ -12,8 +12,9 @@
 // all of them sums: no differences of large ones.
 //
 // A block takes a chunk and a key head, one of its value heads after the other. A thread has a row of the
-// products, a half or (kQ = 4) a quarter of its columns. bfloat16: A enters as a pair (16 bits, for bfloat16
-// results), S and D in three parts, 64 keys of them at a time (24 bits: dg is an fp32 result). fp32: all in three.
+// products, a half or (kQ = 4) a quarter of its columns. A, S and D enter in three parts (24 bits), S and D 64 keys of them
+// at a time, and fp32 inputs too. (A as a pair, for bfloat16 results: 1e-4 from the exact values rounded for 2e-5, at 6 % of the
+// gradients' time.)
 //
 // Bound by latency: a chunk's tiles and states come, are multiplied, decayed, multiplied again and read out, twice, one
 // step after the other, with one block an SM but for bfloat16's heads of 64. Measured: 4 x 4096 x 32 x 64 bfloat16 168 us
@@ -69,12 +70,16 @@ __global__ void __launch_bounds__(128 * kQ, kQ == 2 ? 2 : 1) grad_kernel(const _
   using M = Smem<T, KP, VP, kQ, kDecaySets<T, kShared>>;
   M& sm = *reinterpret_cast<M*>(raw);
   constexpr bool kF32 = sizeof(T) == 4;
-  constexpr int kThreads = 128 * kQ, kSlices = KP / 64, kN = In<T>::kParts, kA = kF32 ? 3 : 2, kW = 64 / kQ;
-  constexpr int kCols = !kF32 && KP == 64 ? 256 : 512;
-  // E of dq and of dk; A (bfloat16: in its place); q k^T; then, where what was there has been read, the chunk's and the
-  // state's products
-  enum { kE = 0, kQk = kF32 ? 320 : 128, kE2 = kF32 ? kQk : kE, kAt = kF32 ? 128 : 0, kOut = kF32 ? 0 : 128, kIn = kF32 ? 64 : 128 + KP };
+  constexpr int kThreads = 128 * kQ, kSlices = KP / 64, kN = In<T>::kParts, kW = 64 / kQ;
+  constexpr int kCols = kQ == 2 ? 256 : 512;
+  // E of dq and of dk; A (bfloat16: two parts in its place, the third from kThird on); q k^T; then, where what was there has been
+  // read, the chunk's and the state's products
+  enum { kE = 0, kQk = kF32 ? 320 : 128, kE2 = kF32 ? kQk : kE, kAt = kF32 ? 128 : 0, kOut = kF32 ? 0 : 128, kIn = kF32 ? 64 : 128 + KP, kThird = kQ == 2 ? kIn : kIn + KP };
   constexpr bool kHold = kQ == 2;  // registers for S's numbers, so that <S, D> need not read D from global memory (4 x 4096 x 32 x 64: 177 -> 168 us)
+  // A block's columns when two share an SM: A's third part is where q k^T was (a thread stores it when it has read that, its
+  // last columns first) and where the state's products come to be, which wait for the chunk's.
+  constexpr bool kTight = kQ == 2;
+  auto third_of = [](int blk) { return kThird + (kTight ? 32 * (blk & 1) + 16 * (blk >> 1) : 16 * blk); };
   constexpr bool kEarlyIn = !kF32 && KP == 128;  // the state's products have columns of their own
   static_assert(!kF32 || (KP == 64 && VP == 64 && kQ == 4), "fp32 tiles of 64 columns fill shared memory");
   const Shape& s = a.s;
@@ -361,12 +366,12 @@ __global__ void __launch_bounds__(128 * kQ, kQ == 2 ? 2 : 1) grad_kernel(const _
       tmem_fence_after_sync();
       if (kF32 && !kUpper && hv == first && sub == 0 && part_of) ahead(part_of - 1, kQ - 1);  // (these have nothing else to do now)
 #pragma unroll 1
-      for (int blk = part_of; blk < 4; blk += kQ) {
+      for (int blk = part_of + 4 - kQ; blk >= 0; blk -= kQ) {
         if (kUpper ? blk >= sub : blk <= sub) {
           float x[32];
           tc_read(x, mine + (kUpper ? kE2 : kE) + 32 * blk);
           decayed<kUpper>(x, dec, row, blk, s.scale);
-          store_parts<kA>(mine + kAt + 16 * kA * blk, x);
+          if (kF32) store_parts<3>(mine + kAt + 48 * blk, x);
           if (!kUpper && dg) {
             float y[32], run = 0.f;
             wait(&sm.done[3], turn5);
@@ -382,8 +387,20 @@ __global__ void __launch_bounds__(128 * kQ, kQ == 2 ? 2 : 1) grad_kernel(const _
             if (blk < 3) sm.total[blk][row] = run;
             sm.pairs[sub][32 * blk + lane] = warp_columns(y, lane);
           }
+          if (!kF32) {
+            uint32_t third[16];
+            store_two(mine + kAt + 32 * blk, x, third);
+            tc_store16(mine + third_of(blk), third);
+          }
+        } else if (kF32) {
+          store_zeros<3>(mine + kAt + 48 * blk);
         } else {
-          store_zeros<kA>(mine + kAt + 16 * kA * blk);
+          if (kTight && !kUpper && dg) {  // (q k^T comes to be where the third part goes)
+            wait(&sm.done[3], turn5);
+            tmem_fence_after_sync();
+          }
+          const uint32_t third[16] = {};
+          store_zeros<2>(mine + kAt + 32 * blk), tc_store16(mine + third_of(blk), third);
         }
       }
       if (!kEarlyIn && (kUpper || !kF32)) fetched(0);
@@ -397,18 +414,28 @@ __global__ void __launch_bounds__(128 * kQ, kQ == 2 ? 2 : 1) grad_kernel(const _
           const uint64_t dx = desc(tx);
 #pragma unroll
           for (int sl = 0; sl < kSlices; ++sl)
-            terms<kA, kN>([&](int p, int r, bool first) {
+            terms<3, kN>([&](int p, int r, bool first) {
 #pragma unroll
               for (int ks = 0; ks < kCT / 16; ++ks)
-                tc_mma_t(tm + kOut + 64 * sl, tm + kAt + part_at<kA>(ks, p), dx + across(ks) + sl * (kRowPanel >> 4) + r * (kCT * KP * 2 >> 4),
-                         product_of(128, 64, false, true), !first || ks > 0);
+                tc_mma_t(tm + kOut + 64 * sl, tm + kAt + (kF32 ? part_at<3>(ks, p) : two_and_third(ks, p, third_of(ks >> 1) - kAt)),
+                         dx + across(ks) + sl * (kRowPanel >> 4) + r * (kCT * KP * 2 >> 4), product_of(128, 64, false, true), !first || ks > 0);
             });
-          if (!kEarlyIn) {
+          if (kTight) tc_commit(&sm.done[2]);
+          if (!kEarlyIn && !kTight) {
             inter(0);
             tc_commit(&sm.done[1]);
           }
         }
         __syncwarp();
+        if (kTight) {
+          wait(&sm.done[2], turn4);
+          tmem_fence_after_sync();
+          if (elected()) {
+            inter(0);
+            tc_commit(&sm.done[1]);
+          }
+          __syncwarp();
+        }
         if (kEarlyIn) {
           wait(&sm.full[1], turn3);
           if (elected()) {
@@ -418,6 +445,7 @@ __global__ void __launch_bounds__(128 * kQ, kQ == 2 ? 2 : 1) grad_kernel(const _
           __syncwarp();
         }
       }
+      if (kTight) ++turn4;
       if (kEarlyIn) {
         // (Shared heads' upper phase: who reads D are the products, and warp 0 has waited for it. A wait of the others here
         // could come after the next head's S has been asked for, and would then see neither copy's phase.)

@@ -301,6 +301,31 @@ __device__ __forceinline__ void store_zeros(uint32_t taddr) {
 #pragma unroll
   for (int i = 0; i < 2 * kP; ++i) tc_store8(taddr + 8 * i, v);
 }
+// The same in three parts of which two take the 32 columns' own place, where a product left them, and the third is handed
+// back: 16 columns, for tc_store16.
+__device__ __forceinline__ void store_two(uint32_t taddr, const float (&x)[32], uint32_t (&third)[16]) {
+#pragma unroll
+  for (int h = 0; h < 2; ++h) {
+    uint32_t v[2][8];
+#pragma unroll
+    for (int j = 0; j < 8; ++j) {
+      uint32_t p[3];
+      split2<3>(x[16 * h + 2 * j], x[16 * h + 2 * j + 1], p);
+      v[0][j] = p[0], v[1][j] = p[1], third[8 * h + j] = p[2];
+    }
+    tc_store8(taddr + 8 * h, v[0]), tc_store8(taddr + 16 + 8 * h, v[1]);
+  }
+}
+__device__ __forceinline__ void tc_store16(uint32_t taddr, const uint32_t (&v)[16]) {
+  asm volatile("tcgen05.st.sync.aligned.32x32b.x16.b32 [%0], {%1, %2, %3, %4, %5, %6, %7, %8, %9, %10, %11, %12, %13, %14, %15, %16};" ::"r"(taddr),
+               "r"(v[0]), "r"(v[1]), "r"(v[2]), "r"(v[3]), "r"(v[4]), "r"(v[5]), "r"(v[6]), "r"(v[7]), "r"(v[8]), "r"(v[9]), "r"(v[10]),
+               "r"(v[11]), "r"(v[12]), "r"(v[13]), "r"(v[14]), "r"(v[15])
+               : "memory");
+}
+// Where part `part` of the columns 16 ks .. of that operand lies; `third`: of the block of 32 columns, from the first part's place on.
+__device__ __forceinline__ uint32_t two_and_third(int ks, int part, int third) {
+  return (part < 2 ? (ks >> 1) * 32 + part * 16 : third) + (ks & 1) * 8;
+}
 // Where part `part` of the columns 16 ks .. of that operand lies.
 template <int kP>
 __device__ __forceinline__ constexpr uint32_t part_at(int ks, int part) {
