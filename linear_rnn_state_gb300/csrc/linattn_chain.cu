@@ -198,7 +198,7 @@ __global__ void __launch_bounds__(kThreads, 1) chain_kernel(const __grid_constan
         if (step(i).live) {
           const float x[4] = {r[0], r[1], r[2], r[3]};
           ask(i + 1);
-          make_decays(sm.d[i % 3], x, s.scale, lane);
+          make_decays<false>(sm.d[i % 3], x, s.scale, lane);
         }
       };
       if (!begin_run(blockIdx.x)) claim();
@@ -416,7 +416,7 @@ __global__ void __launch_bounds__(kThreads, 1) chain_kernel(const __grid_constan
         if (kUpper ? blk >= sub : blk <= sub) {
           float x[32];
           tc_read(x, at_p + 32 * blk);
-          decayed<kUpper>(x, sm.d[i % 3], row, blk, s.scale);
+          decayed<kUpper, false>(x, sm.d[i % 3], row, blk, s.scale);
           store_two(at_p + 32 * blk, x, third);
         } else {
           store_zeros<2>(at_p + 32 * blk);

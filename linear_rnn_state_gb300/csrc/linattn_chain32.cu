@@ -81,7 +81,7 @@ __global__ void __launch_bounds__(kThreads, 1) chain32_kernel(const Args a, cons
       if (i < n) {
         float x[4] = {r[0], r[1], r[2], r[3]};
         ask(i + 1);
-        make_decays(sm.d[i % 3], x, s.scale, lane);
+        make_decays<true>(sm.d[i % 3], x, s.scale, lane);
       }
     };
     auto prefetch = [&](const float* p, long long stride, int cols, int len) {
@@ -295,7 +295,7 @@ __global__ void __launch_bounds__(kThreads, 1) chain32_kernel(const Args a, cons
       if (kUpper ? quarter >= sub : quarter <= sub) {
         float x[32];
         tc_read(x, mine + kScore + 32 * quarter);
-        decayed<kUpper>(x, d, row, quarter, s.scale);
+        decayed<kUpper, true>(x, d, row, quarter, s.scale);
         store_parts<3>(mine + kP + 48 * quarter, x);
       } else {
         store_zeros<3>(mine + kP + 48 * quarter);

@@ -226,6 +226,10 @@ __device__ __forceinline__ float2 two_sum(float2 a, float2 b) {
   return make_float2(h, e - (h - s));
 }
 __device__ __forceinline__ float minus(float2 a, float2 b) { return (a.x - b.x) + (a.y - b.y); }
+// The difference as two floats, and e to it: an exponent of tens loses up to 2^-20 when it is rounded to one float, and e^x as much
+// of itself. (The second float is at most half a unit of the first.)
+__device__ __forceinline__ float2 minus_both(float2 a, float2 b) { return two_sum(a, make_float2(-b.x, -b.y)); }
+__device__ __forceinline__ float exp_both(float2 x) { return expf(x.x) * (1.f + x.y); }
 // The running sums of 32 kPer tokens by a warp, kPer a lane: of r, log decays.
 template <int kPer>
 __device__ __forceinline__ void running_sums(float2 (&G)[kPer], const float (&r)[kPer], int lane) {

@@ -220,7 +220,7 @@ __global__ void __launch_bounds__(128 * kQ, kQ == 2 ? 2 : 1) grad_kernel(const _
     if (warp == 4 * kQ - 1) {
       float r[4];
       load_decays(r, s.fixed ? a.g + hv : a.g + tok * s.Hv + hv, s.fixed ? 0 : s.Hv, c.len, lane);
-      make_decays(dec, r, s.scale, lane);
+      make_decays<kF32>(dec, r, s.scale, lane);
     }
     // A product of two tiles along their rows, in tensor memory from column `to` on.
     auto scores = [&](uint32_t to, const bf16_t* ta, const bf16_t* tb, auto cols) {
@@ -370,7 +370,7 @@ __global__ void __launch_bounds__(128 * kQ, kQ == 2 ? 2 : 1) grad_kernel(const _
         if (kUpper ? blk >= sub : blk <= sub) {
           float x[32];
           tc_read(x, mine + (kUpper ? kE2 : kE) + 32 * blk);
-          decayed<kUpper>(x, dec, row, blk, s.scale);
+          decayed<kUpper, kF32>(x, dec, row, blk, s.scale);
           if (kF32) store_parts<3>(mine + kAt + 48 * blk, x);
           if (!kUpper && dg) {
             float y[32], run = 0.f;

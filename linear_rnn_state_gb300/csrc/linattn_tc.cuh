@@ -204,6 +204,17 @@ struct alignas(16) Decays {
   int up;           // a log decay is above 0 (or NaN)
   int near;         // bit b: block b's range is at most kNear
 };
+// kFull: for fp32 results, exponents in two floats (those of 32 tokens span tens: rounded to one, each factor is off by up to 1e-6; 2 % of
+// the time in fp32, 4 % of a bfloat16 chain's, whose results do not show it).
+template <bool kFull>
+__device__ __forceinline__ float exp_of(float2 x) {
+  return kFull ? exp_both(x) : expf(x.x + x.y);
+}
+template <bool kFull>
+__device__ __forceinline__ float2 apart(float2 a, float2 b) {
+  return kFull ? minus_both(a, b) : make_float2(minus(a, b), 0.f);
+}
+template <bool kFull>
 __device__ __forceinline__ void make_decays(Decays& d, const float (&r)[4], float scale, int lane) {
   float2 G[4];
   running_sums(G, r, lane);
@@ -218,9 +229,9 @@ __device__ __forceinline__ void make_decays(Decays& d, const float (&r)[4], floa
   float4 head, tail, to, from;
 #pragma unroll
   for (int i = 0; i < 4; ++i) {
-    const float x = (G[i].x - m) + G[i].y;
-    (&head.x)[i] = scale * expf(G[i].x + G[i].y), (&tail.x)[i] = expf(minus(last, G[i]));
-    (&to.x)[i] = expf(x), (&from.x)[i] = expf(-x);
+    const float2 x = apart<kFull>(G[i], make_float2(m, 0.f));
+    (&head.x)[i] = scale * exp_of<kFull>(G[i]), (&tail.x)[i] = exp_of<kFull>(apart<kFull>(last, G[i]));
+    (&to.x)[i] = exp_of<kFull>(x), (&from.x)[i] = exp_of<kFull>(make_float2(-x.x, -x.y));
   }
   reinterpret_cast<float4*>(d.G)[2 * lane] = make_float4(G[0].x, G[0].y, G[1].x, G[1].y);
   reinterpret_cast<float4*>(d.G)[2 * lane + 1] = make_float4(G[2].x, G[2].y, G[3].x, G[3].y);
@@ -228,15 +239,16 @@ __device__ __forceinline__ void make_decays(Decays& d, const float (&r)[4], floa
   reinterpret_cast<float4*>(d.to)[lane] = to, reinterpret_cast<float4*>(d.from)[lane] = from;
   if ((lane & 7) == 0) d.middle[lane >> 3] = m;
   if (lane == 0) {
-    d.whole = expf(last.x + last.y), d.up = up;
+    d.whole = exp_of<kFull>(last), d.up = up;
     d.near = 0;
 #pragma unroll
     for (int b = 0; b < 4; ++b) d.near |= ((near >> 8 * b & 255u) == 255u) << b;
   }
 }
 
-// 32 columns (block `blk`) of a row's products times scale e^{G_i - G_j}, 0 outside the mask.
-template <bool kUpper>
+// 32 columns (block `blk`) of a row's products times scale e^{G_i - G_j}, 0 outside the mask. kFull: for fp32 results (the fast
+// exponential is off by 1.2 |x| + 2 units in the last place).
+template <bool kUpper, bool kFull>
 __device__ __forceinline__ void decayed(float (&x)[32], const Decays& d, int row, int blk, float scale) {
   const bool diagonal = blk == row >> 5;
   const int at = row - 32 * blk;  // the diagonal's column
@@ -249,14 +261,16 @@ __device__ __forceinline__ void decayed(float (&x)[32], const Decays& d, int row
       const float d0 = minus(Gr, make_float2(g.x, g.y)), d1 = minus(Gr, make_float2(g.z, g.w));
       // (selects, no branches: a masked place takes the exponent 0)
       const bool k0 = kUpper ? j >= at : j <= at, k1 = kUpper ? j + 1 >= at : j + 1 <= at;
-      const float e0 = scale * __expf(k0 ? (kUpper ? -d0 : d0) : 0.f), e1 = scale * __expf(k1 ? (kUpper ? -d1 : d1) : 0.f);
+      const float x0 = k0 ? (kUpper ? -d0 : d0) : 0.f, x1 = k1 ? (kUpper ? -d1 : d1) : 0.f;
+      const float e0 = scale * (kFull ? expf(x0) : __expf(x0)), e1 = scale * (kFull ? expf(x1) : __expf(x1));
       x[j] = k0 ? x[j] * e0 : 0.f, x[j + 1] = k1 ? x[j + 1] * e1 : 0.f;
     }
     return;
   }
-  const float2 Gr = d.G[row];
-  const float y = (Gr.x - d.middle[blk]) + Gr.y;
-  const float r = scale * (diagonal ? (kUpper ? d.from : d.to)[row] : __expf(kUpper ? -y : y));
+  const float2 y = apart<kFull>(d.G[row], make_float2(d.middle[blk], 0.f));
+  const float r = scale * (diagonal ? (kUpper ? d.from : d.to)[row]
+                           : kFull  ? exp_both(kUpper ? make_float2(-y.x, -y.y) : y)
+                                    : __expf(kUpper ? -y.x : y.x));
   const float4* c = reinterpret_cast<const float4*>((kUpper ? d.to : d.from) + 32 * blk);
   const float2 rr = make_float2(r, r);
 #pragma unroll
