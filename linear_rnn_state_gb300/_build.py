@@ -7,8 +7,8 @@ both see the same current device).
 It also links the debug build, libwkv7_debug.so: the same objects, the C ABI
 and the WKV7 scan kernels recompiled with WKV7_DEBUG (every plain global load
 and store checked against its buffer, 1 ms mbarrier wait limit, and the hooks
-of include/wkv7_debug.h), and with it the gated delta rule's C ABI, chains and
-gradients (1 ms and include/gdr_debug.h). Only the tests of those checks and of the timeout
+of include/wkv7_debug.h), and with it the gated delta rule's and linear attention's
+C ABI, chains and gradients (1 ms, include/gdr_debug.h and include/linattn_debug.h). Only the tests of those checks and of the timeout
 paths load it.
 """
 from __future__ import annotations
@@ -27,7 +27,8 @@ LIB = os.path.join(PKG, "libwkv7.so")
 DEBUG_LIB = os.path.join(PKG, "libwkv7_debug.so")
 DEBUG_SOURCES = ["wkv7_api.cu", "wkv7_fwd2.cu", "wkv7_fwd3.cu", "wkv7_bwd2.cu", "wkv7_bwd3.cu",
                  "wkv7_bwd4.cu", "wkv7_bwd4_f32.cu", "gdr_api.cu", "gdr_fwd.cu", "gdr_bwd.cu",
-                 "gdr_grad.cu"]  # recompiled with -DWKV7_DEBUG for the debug build
+                 "gdr_grad.cu", "linattn_api.cu", "linattn_chain.cu", "linattn_chain32.cu",
+                 "linattn_grad.cu"]  # recompiled with -DWKV7_DEBUG for the debug build
 
 SOURCES = ["wkv7_api.cu", "wkv7_fwd2.cu", "wkv7_fwd3.cu", "wkv7_bwd2.cu", "wkv7_bwd3.cu", "wkv7_bwd4.cu",
            "wkv7_bwd4_f32.cu", "rwkv8_api.cu",
@@ -68,7 +69,7 @@ def build(force: bool = False, verbose: bool = False, extra_flags=()) -> str:
     os.makedirs(BUILD_DIR, exist_ok=True)
     headers = [os.path.join(CSRC, h) for h in HEADERS] + [os.path.join(INCLUDE, h)
                                                           for h in ("wkv7.h", "rwkv8.h", "wkv7_debug.h", "gdr.h", "gdr_debug.h", "blocknorm.h",
-                                                                "linattn.h", "qkrope.h")]
+                                                                "linattn.h", "linattn_debug.h", "qkrope.h")]
     objs, dobjs, jobs = [], [], []
     for src in SOURCES:
         s = os.path.join(CSRC, src)

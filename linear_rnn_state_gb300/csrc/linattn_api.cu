@@ -3,6 +3,10 @@
 #include <algorithm>
 #include <initializer_list>
 
+#ifdef WKV7_DEBUG
+#include <atomic>
+#endif
+
 #include "api_check.h"
 #include "linattn.h"
 #include "linattn_launch.h"
@@ -15,6 +19,10 @@ using api::fail;
 using api::Span;
 
 constexpr unsigned long long kMaxBytes = 1ull << 46, kMaxBlocks = 1ull << 31;
+
+#ifdef WKV7_DEBUG
+std::atomic<int> g_debug_what{0}, g_debug_n{0};  // linattn_debug.h
+#endif
 
 int check_dims(int B, int T, int Hk, int Hv, int K, int V, const char* rows) {
   if (B < 0 || T < 0 || Hk < 0 || Hv < 0) return fail(WKV7_ERR_INVALID, "%s, T, Hk and Hv must be >= 0 (got %d, %d, %d, %d)", rows, B, T, Hk, Hv);
@@ -155,7 +163,10 @@ int launched(cudaError_t e, const char* what) {
   return e == cudaSuccess ? WKV7_OK : fail(WKV7_ERR_CUDA, "%s launch: %s", what, cudaGetErrorString(e));
 }
 // On tcgen05: o, or dv.
-int chains(const Maps& maps, const Args& a, bool bf16, bool backward, bool keep, cudaStream_t stream) {
+int chains(const Maps& maps, Args& a, bool bf16, bool backward, bool keep, cudaStream_t stream) {
+#ifdef WKV7_DEBUG
+  a.skip_what = g_debug_what.load(), a.skip_n = g_debug_n.load();
+#endif
   const int each = segment_chunks(a.s, bf16);
   auto run = [&](Way way, bool images) {
     return launched(bf16 ? launch_chain(maps, a, backward, each, way, images, stream) : launch_chain32(a, backward, each, way, images, stream), "chain");
@@ -200,6 +211,13 @@ bool make_maps(Maps& m, const Args& a) {
 using namespace linattn;
 
 extern "C" {
+
+#ifdef WKV7_DEBUG
+int linattn_debug_skip(int what, int n) {
+  linattn::g_debug_what.store(n > 0 ? what : 0), linattn::g_debug_n.store(n);
+  return WKV7_OK;
+}
+#endif
 
 size_t linattn_saved_bytes(int B, int T, int Hk, int Hv, int K, int V, int nseq, int bf16, int for_backward) {
   Args a{};

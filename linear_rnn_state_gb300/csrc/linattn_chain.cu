@@ -136,12 +136,12 @@ __global__ void __launch_bounds__(kThreads, 1) chain_kernel(const __grid_constan
   };
   auto claim = [&] {
     __syncwarp();
-    if (lane == 0) {
+    ++claims;
+    if (lane == 0 && !LINATTN_SKIPPED(LINATTN_SKIP_CLAIM, claims)) {
       fence_proxy_async_smem();
       wkv7::mbar_arrive_expect_tx(&sm.claimed, sizeof sm.reply);
       claim_block(&sm.reply, &sm.claimed);
     }
-    ++claims;
   };
   auto taken = [&](unsigned& block) {
     wait(&sm.claimed, claims - 1);
@@ -209,12 +209,15 @@ __global__ void __launch_bounds__(kThreads, 1) chain_kernel(const __grid_constan
         if (k < 0 || k >= 2) produce(k < 0 ? k + kAhead : k - 2 + kAhead);
         if (k >= 0 ? kEarly || k != 1 : k == -1) __syncthreads();
         if (k == -1) {
-          if (!step(0).live) return;
+          if (!step(0).live) {
+            if (!wait.ok) finish_copies(&sm.claimed);
+            return;
+          }
           ask(0);
         }
         if (k >= 2 && !step(k - 1).live) break;
       }
-      if (!wait.ok) finish_copies(&sm.claimed, claims);
+      if (!wait.ok) finish_copies(&sm.claimed);
       __syncthreads();
       return;
     }
@@ -223,7 +226,7 @@ __global__ void __launch_bounds__(kThreads, 1) chain_kernel(const __grid_constan
       const CUtensorMap *ma = kUpper ? &maps.k : &maps.q, *mb = kUpper ? &maps.q : &maps.k, *mx = kUpper ? &maps.d : &maps.v;
       const int b_a = kUpper ? s.k_b != 0 : s.q_b != 0, b_b = kUpper ? s.q_b != 0 : s.k_b != 0, b_x = kUpper || s.v_b != 0;
       auto bring_of = [&](const Step& w, int i, bool keys) {  // b, or a and x
-        if (w.live && lane == 0) {
+        if (w.live && (wait.ok & (lane == 0)) && !LINATTN_SKIPPED(LINATTN_SKIP_TILES, i + 1)) {
           auto& st = sm.stage[i % kSt];
           uint64_t* bar = &sm.full[i % kSt];
           if (keys) {
@@ -236,11 +239,9 @@ __global__ void __launch_bounds__(kThreads, 1) chain_kernel(const __grid_constan
         }
       };
       auto bring = [&](int i, bool keys) { bring_of(step(i), i, keys); };
-      int n = 0;  // chunks brought
       auto brought = [&](int i) {
         const Step& w = step(i);
         if (!w.live) return;
-        n = i + 1;
         wait(&sm.full[i % kSt], i / kSt);
         if (s.packed && w.len < kCT) {
           auto& st = sm.stage[i % kSt];
@@ -304,7 +305,7 @@ __global__ void __launch_bounds__(kThreads, 1) chain_kernel(const __grid_constan
       }
       if (lane == 0) bulk_wait_all();
       if (!wait.ok)
-        for (int st = 0; st < kSt; ++st) finish_copies(&sm.full[st], (n - st + kSt - 1) / kSt);
+        for (uint64_t& full : sm.full) finish_copies(&full);
       __syncthreads();
       return;
     }
@@ -316,7 +317,7 @@ __global__ void __launch_bounds__(kThreads, 1) chain_kernel(const __grid_constan
 #pragma unroll
       for (int ks = 0; ks < KP / 16; ++ks)
         tc_mma(tm + kP + (kEarly ? i % 2 * 128 : 0), da + along<kCT>(ks), db + along<kCT>(ks), product_of(128, 128, false, false), ks > 0);
-      tc_commit(&sm.scored);
+      if (!LINATTN_SKIPPED(LINATTN_SKIP_SCORES, i + 1)) tc_commit(&sm.scored);
     };
     auto from_state = [&](int i) {
       const uint64_t da = desc(sm.stage[i % kSt].a), ds = desc(sm.s), dt = desc(kEarly ? sm.third : sm.stage[(i + kSt - 1) % kSt].b);

@@ -142,7 +142,7 @@ __global__ void __launch_bounds__(kThreads, 1) chain32_kernel(const Args a, cons
               tc_mma(tm + kScore, da + along<kCT>(ks) + p * (kRowPanel >> 4), db + along<kCT>(ks) + r * (kRowPanel >> 4),
                      product_of(128, 128, false, false), !first || ks > 0);
           });
-          tc_commit(&sm.scored);
+          if (!LINATTN_SKIPPED(LINATTN_SKIP_SCORES, i + 1)) tc_commit(&sm.scored);
           terms<3, 3>([&](int p, int r, bool first) {
 #pragma unroll
             for (int ks = 0; ks < 4; ++ks)

@@ -39,7 +39,9 @@ struct Smem {
   float pairs[4][kCT];     // of a block of 32 rows: the sums over j < t
   float dots[2][kQ][kCT];  // q.(S's part of dq), k.(D's part of dk), by parts of the columns
   float whole[4 * kQ];
-  uint64_t done[4], end, full[2];  // products: scores, rows, of the state's first 64 keys, q k^T; tiles, the state
+  // Products: scores, rows, of the state's first 64 keys (two blocks an SM: of the chunk), each twice a value head, for dq and for dk; q k^T,
+  // once. Copies: the tiles, once a head; the state and its gradient, 64 keys at a time.
+  uint64_t done[4], end, full[2];
   uint32_t tmem;
 };
 
@@ -100,7 +102,7 @@ __global__ void __launch_bounds__(128 * kQ, kQ == 2 ? 2 : 1) grad_kernel(const _
 #pragma unroll
     for (int j = 0; j < (kShared ? kW * kSlices : 1); ++j) acc[i][j] = 0.f;
   Patience wait{a.status};
-  uint32_t turn0 = 0, turn1 = 0, turn2 = 0, turn3 = 0, turn4 = 0, turn5 = 0, tm = 0;
+  uint32_t tm = 0;
   __syncthreads();
   // The thread's kW columns of 64 to dq or dk (called by all threads). fp32: four lanes exchange four columns each, and a
   // store is of 64 bytes of eight rows instead of 16 of 32. bfloat16: through shared memory.
@@ -145,7 +147,7 @@ __global__ void __launch_bounds__(128 * kQ, kQ == 2 ? 2 : 1) grad_kernel(const _
   };
   // 64 keys of a state. (What was there has been read: the products that did are waited for.)
   auto fetch = [&](const char* from, int sl, int who = 0) {
-    if (tid == who) {
+    if (wait.ok & (tid == who)) {
       wkv7::mbar_arrive_expect_tx(&sm.full[1], sizeof sm.s);
 #pragma unroll
       for (int part = 0; part < 3; ++part)
@@ -154,8 +156,8 @@ __global__ void __launch_bounds__(128 * kQ, kQ == 2 ? 2 : 1) grad_kernel(const _
   };
   // The state before the chunk and (bfloat16) the tiles of a value head.
   auto begin = [&](int hv) {
-    fetch(image_of(a.images, hv), 0);
-    if (!kF32 && tid == 0) {
+    if (!LINATTN_SKIPPED(LINATTN_SKIP_STATE, hv - first + 1)) fetch(image_of(a.images, hv), 0);
+    if (!kF32 && (wait.ok & (tid == 0)) && !LINATTN_SKIPPED(LINATTN_SKIP_TILES, hv - first + 1)) {
       wkv7::mbar_arrive_expect_tx(&sm.full[0], (hv == first ? sizeof sm.q + sizeof sm.k : 0) + sizeof sm.v + sizeof sm.d);
       load_tile<VP>(sm.v, &maps.v, &sm.full[0], 0, hv, c.t0, s.v_b ? c.b : 0);
       load_tile<VP>(sm.d, &maps.d, &sm.full[0], 0, hv, c.t0, c.b);
@@ -239,7 +241,7 @@ __global__ void __launch_bounds__(128 * kQ, kQ == 2 ? 2 : 1) grad_kernel(const _
       if (warp == 0) {
         if (elected()) {
           scores(kE, sm.d, sm.v, Values{});
-          tc_commit(&sm.done[0]);
+          if (!LINATTN_SKIPPED(LINATTN_SKIP_SCORES, 2 * (hv - first) + 1)) tc_commit(&sm.done[0]);
         }
         __syncwarp();
       }
@@ -255,7 +257,7 @@ __global__ void __launch_bounds__(128 * kQ, kQ == 2 ? 2 : 1) grad_kernel(const _
       first_products();
       if (hv == first) place(sm.q, raw_q), place(sm.k, raw_k);
     } else {
-      wait(&sm.full[0], turn2++);
+      wait(&sm.full[0], hv - first);
       if (!ready) {
         if (hv == first) clear_rows<KP>(sm.q, c.len, tid, kThreads), clear_rows<KP>(sm.k, c.len, tid, kThreads);
         clear_rows<VP>(sm.v, c.len, tid, kThreads);
@@ -284,7 +286,7 @@ __global__ void __launch_bounds__(128 * kQ, kQ == 2 ? 2 : 1) grad_kernel(const _
       }
       // They are there; their part of <S, D>.
       auto fetched = [&](int sl) {
-        wait(&sm.full[1], turn3++);
+        wait(&sm.full[1], kEarlyIn ? sl : kUpper);
         if (kHold && dg) {
 #pragma unroll
           for (int e = 0; e < VP * 8 / kThreads; ++e) {
@@ -338,7 +340,7 @@ __global__ void __launch_bounds__(128 * kQ, kQ == 2 ? 2 : 1) grad_kernel(const _
         });
       };
       if (kEarlyIn && warp == 0) {
-        wait(&sm.full[1], turn3);
+        wait(&sm.full[1], 0);
         if (elected()) {
           inter(0);
           tc_commit(&sm.done[2]);
@@ -349,20 +351,17 @@ __global__ void __launch_bounds__(128 * kQ, kQ == 2 ? 2 : 1) grad_kernel(const _
       if (!kUpper && ready) __syncthreads();  // the decays
       // The other 64 keys come while the scores are decayed: brought by a warp that has none (S: once <S, D> has read its first half).
       if (kEarlyIn) {
-        if (kUpper) {
-          ++turn3;  // (the products that read D wait for it, and who brings the rest for them)
-        } else {
+        if (!kUpper) {  // (D: the products that read it wait for it, and who brings the rest for them)
           fetched(0);
           __syncthreads();
         }
         constexpr int kWho = kUpper ? 1 : 4;
         if (warp == kWho) {
-          wait(&sm.done[2], turn4);
+          wait(&sm.done[2], kUpper);
           fetch(kUpper ? D : S, 1, 32 * kWho);
         }
-        ++turn4;
       }
-      wait(&sm.done[0], turn0++);
+      wait(&sm.done[0], kUpper);
       tmem_fence_after_sync();
       if (kF32 && !kUpper && hv == first && sub == 0 && part_of) ahead(part_of - 1, kQ - 1);  // (these have nothing else to do now)
 #pragma unroll 1
@@ -374,7 +373,7 @@ __global__ void __launch_bounds__(128 * kQ, kQ == 2 ? 2 : 1) grad_kernel(const _
           if (kF32) store_parts<3>(mine + kAt + 48 * blk, x);
           if (!kUpper && dg) {
             float y[32], run = 0.f;
-            wait(&sm.done[3], turn5);
+            wait(&sm.done[3], hv - first);
             tmem_fence_after_sync();
             tc_read(y, mine + kQk + 32 * blk);
 #pragma unroll
@@ -396,7 +395,7 @@ __global__ void __launch_bounds__(128 * kQ, kQ == 2 ? 2 : 1) grad_kernel(const _
           store_zeros<3>(mine + kAt + 48 * blk);
         } else {
           if (kTight && !kUpper && dg) {  // (q k^T comes to be where the third part goes)
-            wait(&sm.done[3], turn5);
+            wait(&sm.done[3], hv - first);
             tmem_fence_after_sync();
           }
           const uint32_t third[16] = {};
@@ -404,7 +403,6 @@ __global__ void __launch_bounds__(128 * kQ, kQ == 2 ? 2 : 1) grad_kernel(const _
         }
       }
       if (!kEarlyIn && (kUpper || !kF32)) fetched(0);
-      if (!kUpper && dg) ++turn5;
       wkv7::tmem_wait_st();
       tmem_fence_before_sync();
       __syncthreads();
@@ -428,7 +426,7 @@ __global__ void __launch_bounds__(128 * kQ, kQ == 2 ? 2 : 1) grad_kernel(const _
         }
         __syncwarp();
         if (kTight) {
-          wait(&sm.done[2], turn4);
+          wait(&sm.done[2], kUpper);
           tmem_fence_after_sync();
           if (elected()) {
             inter(0);
@@ -437,7 +435,7 @@ __global__ void __launch_bounds__(128 * kQ, kQ == 2 ? 2 : 1) grad_kernel(const _
           __syncwarp();
         }
         if (kEarlyIn) {
-          wait(&sm.full[1], turn3);
+          wait(&sm.full[1], 1);
           if (elected()) {
             inter(1);
             tc_commit(&sm.done[1]);
@@ -445,23 +443,20 @@ __global__ void __launch_bounds__(128 * kQ, kQ == 2 ? 2 : 1) grad_kernel(const _
           __syncwarp();
         }
       }
-      if (kTight) ++turn4;
       if (kEarlyIn) {
         // (Shared heads' upper phase: who reads D are the products, and warp 0 has waited for it. A wait of the others here
         // could come after the next head's S has been asked for, and would then see neither copy's phase.)
-        if (kUpper && kShared)
-          ++turn3;
-        else
-          fetched(1);
+        if (!kUpper || !kShared) fetched(1);
         if (!kShared) __syncthreads();  // <S, D> has been read: rows take its place
       }
-      wait(&sm.done[1], turn1++);
+      wait(&sm.done[1], kUpper);
       tmem_fence_after_sync();
-      if (!kUpper && !kEarlyIn && (kShared || kF32)) fetch(D, 0);
+      const bool back = !LINATTN_SKIPPED(LINATTN_SKIP_BACK, hv - first + 1);
+      if (!kUpper && back && !kEarlyIn && (kShared || kF32)) fetch(D, 0);
       if (!kUpper && warp == 0) {  // (where A was, or q k^T: both have been read)
         if (elected()) {
           scores(kE2, sm.v, sm.d, Values{});
-          tc_commit(&sm.done[0]);
+          if (!LINATTN_SKIPPED(LINATTN_SKIP_SCORES, 2 * (hv - first) + 2)) tc_commit(&sm.done[0]);
         }
         __syncwarp();
       }
@@ -505,7 +500,7 @@ __global__ void __launch_bounds__(128 * kQ, kQ == 2 ? 2 : 1) grad_kernel(const _
       tmem_fence_before_sync();
       __syncthreads();
       tmem_fence_after_sync();
-      if (!kUpper && (kEarlyIn || !(kShared || kF32))) fetch(D, 0);  // (all threads are done with the place)
+      if (!kUpper && back && (kEarlyIn || !(kShared || kF32))) fetch(D, 0);  // (all threads are done with the place)
     };
     phase(std::false_type{});
     phase(std::true_type{});
@@ -558,7 +553,7 @@ __global__ void __launch_bounds__(128 * kQ, kQ == 2 ? 2 : 1) grad_kernel(const _
   if (warp == 0) {
     if (!__all_sync(0xffffffffu, wait.ok)) {
       finish_products(&sm.end);
-      if (lane == 0) finish_copies(&sm.full[0], turn2), finish_copies(&sm.full[1], turn3);
+      if (lane == 0) finish_copies(&sm.full[0]), finish_copies(&sm.full[1]);
     }
   }
   __syncthreads();

@@ -8,6 +8,10 @@
 #include <stddef.h>
 #include <stdint.h>
 
+#ifdef WKV7_DEBUG
+#include "linattn_debug.h"
+#endif
+
 namespace linattn {
 
 // Tokens of a chunk: those that fill the rows of a tcgen05 product, or (mma.sync: fp32 with heads above 64) 64.
@@ -50,6 +54,7 @@ struct Args {
   void *images, *dimages;  // states and dstates as the gradients' products read them (linattn_tc.cuh)
   double *part;        // [kParts][Hv]: sums of dg over tokens
   unsigned* status;    // the device's status word
+  int skip_what, skip_n;   // debug build only: linattn_debug.h
 };
 constexpr int kParts = 256;
 

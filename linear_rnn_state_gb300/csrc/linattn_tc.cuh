@@ -139,7 +139,7 @@ __device__ __forceinline__ void meet(int id, int n) { asm volatile("bar.sync %0,
 __device__ __forceinline__ void announce(int id, int n) { asm volatile("bar.arrive %0, %1;" ::"r"(id), "r"(n) : "memory"); }
 
 // A wait that a warp gives up on once: from then on it goes through its steps without waiting (all accesses
-// are in bounds whatever the data), so that barriers and tensor memory are left in order.
+// are in bounds whatever the data) and starts no copy, so that barriers and tensor memory are left in order.
 struct Patience {
   unsigned* status;
   bool ok = true;
@@ -149,16 +149,22 @@ struct Patience {
 };
 
 // Where a wait was given up, before the block ends: no product and (by the thread that started them) no copy is left in
-// flight, a millisecond at most for each.
+// flight, a millisecond or two at most for each. (Which of a barrier's phases the copy in flight completes is not known then.)
 constexpr uint64_t kLastWaitNs = 1000000;
 __device__ __forceinline__ void finish_products(uint64_t* bar) {  // by the issuing warp; bar's first use
   if (elected()) tc_commit(bar);
   __syncwarp();
   mbar_wait_bounded(nullptr, bar, 0, kLastWaitNs);
 }
-__device__ __forceinline__ void finish_copies(uint64_t* bar, uint32_t phases) {  // bar had so many phases
-  if (phases) mbar_wait_bounded(nullptr, bar, (phases - 1) & 1, kLastWaitNs);
+__device__ __forceinline__ void finish_copies(uint64_t* bar) {
+  for (uint32_t parity = 0; parity < 2; ++parity) mbar_wait_bounded(nullptr, bar, parity, kLastWaitNs);
 }
+#ifdef WKV7_DEBUG
+__device__ __forceinline__ bool skipped(const Args& a, int what, int n) { return a.skip_what == what && a.skip_n == n; }
+#define LINATTN_SKIPPED(what, n) skipped(a, what, n)
+#else
+#define LINATTN_SKIPPED(what, n) false
+#endif
 
 // ---------------------------------------------------------------- copies ---
 
