@@ -10,7 +10,9 @@
  * where pair j is the values (j, half + j), or with interleaved != 0 (2 j, 2 j + 1).
  * The values from 2 half on are not turned. All arithmetic is fp32, but the
  * angles: position * freq_j is formed in turns as an integer of 64 bits (modulo a
- * whole turn), so a far position costs no accuracy (cosines and sines within 2e-7).
+ * whole turn), so a far position costs no accuracy (cosines and sines within 2e-7). Rows
+ * whose squares leave fp32's range (values from 3e18 on, or below 1e-15 without an eps)
+ * are normed times a power of two.
  *
  * Sizes: D a multiple of 8 up to 256, half from 0 to D / 2. q [tokens][Hq][D] and k
  * [tokens][Hk][D] have one type (bfloat16 with bf16 != 0, else fp32), as have the

@@ -70,6 +70,24 @@ __device__ __forceinline__ float inverse_root(float x) {
   return x > 1e-37f && x < 1e37f ? y : r;
 }
 
+// Values from 3e18 on, or below 1e-15 without an eps, have squares outside fp32's range: such a row is done once more,
+// times a power of two.
+__device__ __forceinline__ bool in_range(float mean) { return mean <= 1e37f && mean >= 1e-30f; }
+// The mean square of a row so scaled; unit: 1 for rows in range.
+template <int kGroup>
+__device__ __forceinline__ float scaled_mean(float2 (&v)[4], float& unit, float inv, float eps) {
+  float mean = 0.f;
+#pragma unroll
+  for (int again = 0; again < 2; ++again) {
+    unit = !again || in_range(mean) ? 1.f : mean > 1.f ? 0x1p-66f : 0x1p66f;
+    float2 s2 = make_float2(0.f, 0.f);
+#pragma unroll
+    for (int e = 0; e < 4; ++e) v[e].x *= unit, v[e].y *= unit, s2.x = fmaf(v[e].x, v[e].x, s2.x), s2.y = fmaf(v[e].y, v[e].y, s2.y);
+    mean = fmaf(group_sum<kGroup>(s2.x + s2.y), inv, eps * unit * unit);
+  }
+  return mean;
+}
+
 // freq / (2 pi) modulo 1 as a 64-bit fraction: freq = m 2^e, m of 53 bits, times 2^66 / (2 pi), by integers.
 __device__ __forceinline__ unsigned long long turns_of(double freq) {
   const unsigned long long bits = (unsigned long long)__double_as_longlong(freq);
@@ -251,17 +269,35 @@ __global__ void __launch_bounds__(kThreads, kIter == 8 ? 3 : 4) forward_kernel(c
   Turn<kHow> turn;
   take_turn<kHow, false>(turn, cs, c, p.half);
   const float inv = 1.f / (float)p.D;
+  auto finish = [&](float2 (&v)[4], float mean, int i, bool mine) {
+    const float r = inverse_root(mean);
+#pragma unroll
+    for (int e = 0; e < 4; ++e) v[e] = mul2(mul2(v[e], make_float2(r, r)), w[e]);
+    rotate<kHow, kGroup, false>(v, turn, cs, c, p.half, lane, line);
+    if (mine && live && i < x.heads) put(dst + i * p.D, v);
+  };
+  bool again = false;
 #pragma unroll
   for (int i = 0; i < kIter; ++i) {
     float2 v[4], s2 = make_float2(0.f, 0.f);
     values(v, raw[i]);
 #pragma unroll
     for (int e = 0; e < 4; ++e) s2 = fma2(v[e], v[e], s2);
-    const float r = inverse_root(fmaf(group_sum<kGroup>(s2.x + s2.y), inv, p.eps));
-#pragma unroll
-    for (int e = 0; e < 4; ++e) v[e] = mul2(mul2(v[e], make_float2(r, r)), w[e]);
-    rotate<kHow, kGroup, false>(v, turn, cs, c, p.half, lane, line);
-    if (live && i < x.heads) put(dst + i * p.D, v);
+    const float mean = fmaf(group_sum<kGroup>(s2.x + s2.y), inv, p.eps);
+    again |= live && i < x.heads && !in_range(mean);
+    finish(v, mean, i, true);
+  }
+  if (!__any_sync(0xffffffffu, again)) return;
+#pragma unroll 1
+  for (int i = 0; i < kIter; ++i) {
+    Raw<T> z;
+    clear(z);
+    if (live && i < x.heads) fetch(z, src + i * p.D);
+    float2 v[4];
+    values(v, z);
+    float unit;
+    const float mean = scaled_mean<kGroup>(v, unit, inv, p.eps);
+    finish(v, mean, i, unit != 1.f);
   }
 }
 
@@ -302,6 +338,7 @@ __global__ void __launch_bounds__(kThreads, 2) backward_kernel(const Args p, uns
     Turn<kHow> turn;
     take_turn<kHow, true>(turn, cs, c, p.half);
     float2 dw[4];
+    bool again = false;
 #pragma unroll
     for (int e = 0; e < 4; ++e) dw[e] = make_float2(0.f, 0.f);
 #pragma unroll
@@ -313,7 +350,9 @@ __global__ void __launch_bounds__(kThreads, 2) backward_kernel(const Args p, uns
       for (int e = 0; e < 4; ++e) s2 = fma2(v[e], v[e], s2), c1 = fma2(mul2(d[e], w[e]), v[e], c1);
       // (places without a head hold rows of zeros: they add nothing to dw, whatever eps is)
       const float mean = fmaf(group_sum<kGroup>(s2.x + s2.y), inv, p.eps);
-      const float r = u0 + group < units && i < x.heads ? inverse_root(mean) : 0.f;
+      const bool here = u0 + group < units && i < x.heads;
+      again |= here && !in_range(mean);
+      const float r = here && in_range(mean) ? inverse_root(mean) : 0.f;
       const float m = -(group_sum<kGroup>(c1.x + c1.y) * r * inv);
       const float2 rr = make_float2(r, r), mm = make_float2(m, m);
 #pragma unroll
@@ -323,6 +362,31 @@ __global__ void __launch_bounds__(kThreads, 2) backward_kernel(const Args p, uns
         d[e] = mul2(fma2(z, mm, mul2(d[e], w[e])), rr);
       }
       if (live && i < x.heads) put(dst + i * p.D, d);
+    }
+    if (__any_sync(0xffffffffu, again)) {
+#pragma unroll 1
+      for (int i = 0; i < kIter; ++i) {
+        Raw<T> y, z;
+        clear(y), clear(z);
+        if (live && i < x.heads) fetch(y, src + i * p.D), fetch(z, up + i * p.D);
+        float2 v[4], d[4], c1 = make_float2(0.f, 0.f);
+        values(v, y), values(d, z);
+        rotate<kHow, kGroup, true>(d, turn, cs, c, p.half, lane, line);
+        float unit;
+        const float mean = scaled_mean<kGroup>(v, unit, inv, p.eps);
+        const bool mine = unit != 1.f && u0 + group < units && i < x.heads;
+        const float r = mine ? inverse_root(mean) : 0.f;
+#pragma unroll
+        for (int e = 0; e < 4; ++e) c1 = fma2(mul2(d[e], w[e]), v[e], c1);
+        const float m = -(group_sum<kGroup>(c1.x + c1.y) * r * inv);
+#pragma unroll
+        for (int e = 0; e < 4; ++e) {
+          const float2 u = mul2(v[e], make_float2(r, r)), t = fma2(u, make_float2(m, m), mul2(d[e], w[e]));
+          if (mine) dw[e] = fma2(d[e], u, dw[e]);
+          d[e] = mul2(mul2(t, make_float2(r, r)), make_float2(unit, unit));
+        }
+        if (mine && c < p.D) put(dst + i * p.D, d);
+      }
     }
 #pragma unroll
     for (int e = 0; e < 4; ++e) {

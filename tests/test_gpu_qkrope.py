@@ -256,6 +256,40 @@ def test_other_eps(env, tokens, Hq, Hk, D, eps, dtype):
     _check(env, _make(tokens, Hq, Hk, D, D // 4, dtype, tokens + D), eps=eps)
 
 
+@BOTH
+@pytest.mark.parametrize("interleaved,half", [(False, 32), (False, 13), (True, 20)])
+def test_rows_whose_squares_leave_fp32(env, interleaved, half, dtype):
+    """Rows of 1e25 and 1e30, and (without an eps) of 1e-25, beside others: each by itself as exact as they are, and the others' bits stay."""
+    orc, qr = env
+    d = _make(70, 7, 3, 64, half, dtype, 14)
+    opts = {"interleaved": interleaved, "eps": 0.0}
+    run = lambda: (*qr.forward(*(d[n] for n in ARGS), d["positions"], **opts),
+                   *qr.backward(*(d[n] for n in ARGS), d["dq"], d["dk"], d["positions"], **opts).values())
+    want = run()
+    for t, h, size in ((0, 0, 1e25), (3, 6, 1e30), (40, 2, 1e-25), (69, 5, 1e25)):
+        d["q"][t, h] *= size
+    d["k"][::9, 1] *= 1e30
+    d["k"][5, 2] *= 1e-25
+    got = run()
+    for i, (name, x) in enumerate((("q", "q"), ("k", "k"), ("q", "dq"), ("k", "dk"))):
+        a, w, f, at = _n(d[name]), _n(d["w" + name]), _n(d["freq"]), _n(d["positions"])
+        ref = orc.forward(a, w, f, at, **opts) if i < 2 else orc.backward(a, w, f, at, _n(d["d" + name]), **opts)[0]
+        y = got[i].double().cpu().numpy()
+        off = np.linalg.norm(y - ref, axis=-1) / np.linalg.norm(ref, axis=-1)
+        # (one row's 64 roundings to bfloat16: 2^-8 of each at most)
+        assert off.max() <= (2.0 ** -8 if dtype is BF16 else 4e-6), (x, off.max())
+        moved = torch.ones(70, got[i].shape[1], dtype=torch.bool, device="cuda")
+        if name == "q":
+            for t, h in ((0, 0), (3, 6), (40, 2), (69, 5)):
+                moved[t, h] = False
+        else:
+            moved[::9, 1] = moved[5, 2] = False
+        assert torch.equal(got[i][moved], want[i][moved])
+    for i, name in ((4, "q"), (5, "k")):
+        ref = orc.backward(_n(d[name]), _n(d["w" + name]), _n(d["freq"]), _n(d["positions"]), _n(d["d" + name]), **opts)[1]
+        _close("dw" + name, got[i], ref)
+
+
 # ------------------------------------------------------------- a layer of them all ---
 
 
