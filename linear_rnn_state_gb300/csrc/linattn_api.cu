@@ -94,7 +94,6 @@ struct Place {
 // some short ones: the longest is taken for three times the mean, or for all there is. 8190 tokens, 32 heads of 64, bfloat16: three
 // alike 67 whole and 121 in segments, one of 7900 and two short ones 154 and 102; six 71 and 126, 153 and 105 (16 heads: 42 and
 // 76, 150 and 66); fp32, three: 134 and 226, 344 and 169. Whole loses more where it loses.
-constexpr int kSms = 152;
 int segment_chunks(const Shape& s, bool bf16) {
   const long long heads = (long long)s.Hv * ((s.V + 63) / 64), lines = heads * s.nseq;
   const int chunks = (s.T + s.C - 1) / s.C;

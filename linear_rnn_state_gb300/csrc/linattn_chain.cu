@@ -56,7 +56,7 @@ struct alignas(16) Step {
   long long image;       // bytes from the first image to the piece of the state before it
 };
 constexpr int kSteps = 8, kAhead = 4;
-constexpr int kSms = 152, kSorted = 256;  // packed sequences that are taken by length
+constexpr int kSorted = 256;  // packed sequences that are taken by length
 
 template <int KP>
 struct Smem {

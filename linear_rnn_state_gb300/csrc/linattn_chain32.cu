@@ -42,8 +42,7 @@ __global__ void __launch_bounds__(kThreads, 1) chain32_kernel(const Args a, cons
   constexpr int kPair = kWorkers + 32, kPart = kCT * 64;
   const Shape& s = a.s;
   const int tid = threadIdx.x, lane = tid & 31, warp = __shfl_sync(0xffffffffu, tid >> 5, 0), sub = warp & 3, quarter = warp >> 2;
-  const int slices = (s.V + 63) >> 6, slice = blockIdx.x % slices, hv = blockIdx.x / slices % s.Hv, slot = blockIdx.x / slices / s.Hv;
-  const int hk = hv / (s.Hv / s.Hk), v0 = slice * 64, vn = min(64, s.V - v0);
+  const int hv = blockIdx.x % s.Hv, slot = blockIdx.x / s.Hv, hk = hv / (s.Hv / s.Hk);
   ChunkAt seg;
   constexpr bool sums = kSumsOnly;
   if (plan.way != kWhole) {
@@ -66,8 +65,8 @@ __global__ void __launch_bounds__(kThreads, 1) chain32_kernel(const Args a, cons
   const float* k = static_cast<const float*>(a.k) + seg.b * s.k_b + seg.t0 * s.k_t + (size_t)hk * s.K;
   const float* pa = kUpper ? k : q;
   const float* pb = kUpper ? q : k;
-  const float* px = kUpper ? static_cast<const float*>(a.d_o) + (tok * s.Hv + hv) * s.V + v0
-                           : static_cast<const float*>(a.v) + seg.b * s.v_b + seg.t0 * s.v_t + (size_t)hv * s.V + v0;
+  const float* px = kUpper ? static_cast<const float*>(a.d_o) + (tok * s.Hv + hv) * s.V
+                           : static_cast<const float*>(a.v) + seg.b * s.v_b + seg.t0 * s.v_t + (size_t)hv * s.V;
 
   if (warp >= kHelpWarp) fewer_registers<40>();
   if (warp > kHelpWarp + 1) return;
@@ -89,12 +88,12 @@ __global__ void __launch_bounds__(kThreads, 1) chain32_kernel(const Args a, cons
         for (int c = 0; c < cols; c += 32) asm volatile("prefetch.global.L2 [%0];" ::"l"(p + r * stride + c));
     };
     char* to = static_cast<char*>(kUpper ? a.dimages : a.images) +
-               ((size_t)(n ? chunk_slot(s, seg, seg.t0 + begin(0)) : 0) * s.Hv + hv) * image_bytes(s.K, s.V) + slice * kImagePiece;
+               ((size_t)(n ? chunk_slot(s, seg, seg.t0 + begin(0)) : 0) * s.Hv + hv) * image_bytes(s.K, s.V);
     const long long next = (kUpper ? -1 : 1) * (long long)(s.Hv * image_bytes(s.K, s.V));
     auto leave = [&](int i) {  // the state before chunk i
       if (plan.keep && i < n && lane == 0) {
 #pragma unroll
-        for (int part = 0; part < 3; ++part) bulk_store(to + (size_t)part * slices * kImagePiece, sm.s + part * 64 * 64, kImagePiece);
+        for (int part = 0; part < 3; ++part) bulk_store(to + (size_t)part * kImagePiece, sm.s + part * 64 * 64, kImagePiece);
         bulk_commit();
         to += next;
       }
@@ -115,7 +114,7 @@ __global__ void __launch_bounds__(kThreads, 1) chain32_kernel(const Args a, cons
       if (i + kLead < n) {
         const int t = begin(i + kLead), len = length(i + kLead);
         if (!sums) prefetch(pa + t * st_a, st_a, s.K, len);
-        prefetch(pb + t * st_b, st_b, s.K, len), prefetch(px + t * st_x, st_x, vn, len);
+        prefetch(pb + t * st_b, st_b, s.K, len), prefetch(px + t * st_x, st_x, s.V, len);
       }
       if (!sums) {
         meet(kBarOut, kPair);
@@ -182,7 +181,7 @@ __global__ void __launch_bounds__(kThreads, 1) chain32_kernel(const Args a, cons
   // ------------------------------------------------------------------ rows ---
   more_registers<104>();
   const int row = sub * 32 + lane;
-  float* out = static_cast<float*>(kUpper ? a.dv : a.o) + (tok * s.Hv + hv) * s.V + v0;
+  float* out = static_cast<float*>(kUpper ? a.dv : a.o) + (tok * s.Hv + hv) * s.V;
   // A chunk's values: two pieces of eight of each of a, b and x a thread.
   float va[sums ? 1 : 2][8], vb[2][8];
   const int piece = (tid & 7) * 8;
@@ -209,7 +208,7 @@ __global__ void __launch_bounds__(kThreads, 1) chain32_kernel(const Args a, cons
       const int r = (e * kWorkers + tid) >> 3;
 #pragma unroll
       for (int j = 0; j < 8; ++j) vx[e][j] = 0.f;
-      if (r < len && piece < vn) load8(vx[e], px + (t0 + r) * st_x + piece);
+      if (r < len && piece < s.V) load8(vx[e], px + (t0 + r) * st_x + piece);
     }
   };
   auto fill = [&](int i) {  // a and b
@@ -239,7 +238,7 @@ __global__ void __launch_bounds__(kThreads, 1) chain32_kernel(const Args a, cons
   if (n) ask(0);
   // The state: rows 16 sub .., keys 16 quarter .. in accumulator tiles.
   float S[2][4];
-  const int s_row = v0 + 16 * sub + (lane >> 2), s_col = quarter * 16 + 2 * (lane & 3);
+  const int s_row = 16 * sub + (lane >> 2), s_col = quarter * 16 + 2 * (lane & 3);
   float* const states = (kUpper ? a.dstates : a.states) + ((size_t)s_row * s.K + s_col);
   const size_t state = (size_t)s.V * s.K;
   auto each = [&](float* m, auto f) {  // pairs of the state's numbers that exist; m is where its first is
@@ -355,7 +354,7 @@ __global__ void __launch_bounds__(kThreads, 1) chain32_kernel(const Args a, cons
       for (int e = 0; e < 4; ++e) {
         const int r = (e * kWorkers + tid) >> 4, c = tid & 15;
         const float4 v = stage[r * 16 + (c ^ (r & 15))];
-        if (r < len && 4 * c < vn) *reinterpret_cast<float4*>(p + (size_t)r * s.Hv * s.V + 4 * c) = v;
+        if (r < len && 4 * c < s.V) *reinterpret_cast<float4*>(p + (size_t)r * s.Hv * s.V + 4 * c) = v;
       }
     }
     meet(kBarRows, kWorkers);
@@ -369,7 +368,7 @@ __global__ void __launch_bounds__(kThreads, 1) chain32_kernel(const Args a, cons
   if (plan.way == kWhole && last) each(last + ends, store);
   if (sums) {
     each(states + ((size_t)slot * s.Hv + hv) * state, store);
-    if (tid == 0 && slice == 0) a.decay[(size_t)slot * s.Hv + hv] = passed;
+    if (tid == 0) a.decay[(size_t)slot * s.Hv + hv] = passed;
   }
   meet(0, kMembers);
   if (warp == 0) wkv7::tmem_dealloc(tm, kCols);
@@ -382,7 +381,7 @@ cudaError_t launch(const Args& a, const Plan& plan, cudaStream_t stream) {
   if (e != cudaSuccess) return e;
   const Shape& s = a.s;
   const long long segs = plan.way != kWhole ? slot_count(s.B, s.T, s.nseq, s.packed, kCT * plan.chunks) : s.nseq;
-  chain32_kernel<kUpper, kSumsOnly><<<(unsigned)(segs * s.Hv * ((s.V + 63) / 64)), kThreads, sizeof(Smem), stream>>>(a, plan);
+  chain32_kernel<kUpper, kSumsOnly><<<(unsigned)(segs * s.Hv), kThreads, sizeof(Smem), stream>>>(a, plan);
   return cudaGetLastError();
 }
 

@@ -27,8 +27,6 @@
 namespace linattn {
 namespace {
 
-constexpr int kAtOnce = 152;  // SMs
-
 template <typename T, int KP, int VP, int kQ, int kDecays>
 struct Smem {
   static constexpr int kN = In<T>::kParts;
@@ -171,7 +169,7 @@ __global__ void __launch_bounds__(128 * kQ, kQ == 2 ? 2 : 1) grad_kernel(const _
   // read while the products run instead of by all blocks of the next wave at once (8 x 4096 x 12 x 64: 386 -> 362 us;
   // bfloat16, with half the bytes a chunk, loses by it: 4 x 4096 x 32 x 64 176 -> 186).
   auto ahead = [&](int who, int of) {
-    const unsigned next = blockIdx.x + kAtOnce;
+    const unsigned next = blockIdx.x + kSms;  // (one block an SM)
     ChunkAt n;
     if (next >= gridDim.x || !chunk_at(s, (int)(next / s.Hk), kCT, n)) return;
     const int k_head = (int)(next % s.Hk), v_head = k_head * group;

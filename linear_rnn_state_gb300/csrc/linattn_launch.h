@@ -18,6 +18,7 @@ namespace linattn {
 constexpr int kCBf16 = 128, kCF32 = 64;
 inline bool on_tcgen05(int K, int V, bool bf16) { return bf16 || (K <= 64 && V <= 64); }
 constexpr int kMaxDim = 128;  // largest head size
+constexpr int kSms = 152;     // of the GPU that plans go by
 
 // What a call's sequences and heads look like.
 struct Shape {
@@ -80,10 +81,11 @@ cudaError_t launch_grad(const Maps& maps, const Args& a, bool bf16, cudaStream_t
 bool make_maps(Maps& maps, const Args& a);
 cudaError_t launch_dg_sums(const Args& a, cudaStream_t stream);          // dg_fixed from dg
 
-// Zeros in up to five outputs of a packed call at the tokens of no sequence.
+// Zeros in the outputs of a packed call (null: none) at the tokens of no sequence.
+constexpr int kGapOutputs = 4;
 struct Gaps {
-  uint32_t* at[5];
-  long long words[5];  // of a token
+  uint32_t* at[kGapOutputs];
+  long long words[kGapOutputs];  // of a token
 };
 cudaError_t launch_gaps(const Args& a, const Gaps& g, cudaStream_t stream);
 

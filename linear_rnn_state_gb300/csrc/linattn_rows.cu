@@ -20,38 +20,28 @@
 namespace linattn {
 namespace {
 
-constexpr int kThreads = 256, kC = kCF32;
+constexpr int kThreads = 256, kC = kCF32, kP = In<float>::kParts;
 enum Mode { kO, kDv, kDq, kDk };
 
-template <typename T>
-__device__ __forceinline__ void store2(T* p, float x, float y);
-template <>
-__device__ __forceinline__ void store2<float>(float* p, float x, float y) {
-  *reinterpret_cast<float2*>(p) = make_float2(x, y);
-}
 __device__ __forceinline__ float2 load2(const float* p) { return *reinterpret_cast<const float2*>(p); }
 
-template <typename T>
 struct Tokens {  // a chunk's rows of one head
-  const T* p;
+  const float* p;
   long long stride;
   int cols;
 };
 
 // What a block keeps in shared memory; D: the (padded) size of the products' inner dimension.
-template <typename T, int kStateParts>
 struct Layout {
-  static constexpr int kP = In<T>::kParts;
-  __host__ __device__ static constexpr size_t a(int) { return 0; }
   __host__ __device__ static constexpr size_t b(int D) { return (size_t)kP * kC * D * 2; }
   __host__ __device__ static constexpr size_t x(int D) { return 2 * b(D); }
   __host__ __device__ static constexpr size_t s(int D) { return x(D) + (size_t)kP * kC * 64 * 2; }
-  __host__ __device__ static constexpr size_t g(int D) { return s(D) + (size_t)kStateParts * 64 * D * 2; }
+  __host__ __device__ static constexpr size_t g(int D) { return s(D) + (size_t)kP * 64 * D * 2; }
   __host__ __device__ static constexpr size_t size(int D) { return g(D) + kC * 8 + kC * 4 + 7 * kC * 4; }
 };
 
 // rows += a b^T of the warp's 16 rows and the columns that the mask leaves it.
-template <int kP, bool kUpper>
+template <bool kUpper>
 __device__ __forceinline__ void scores(float (&x)[8][4], const bf16_t* as, const bf16_t* bs, int D, int Dp, int warp, int lane) {
   zero(x);
   for (int k0 = 0; k0 < D; k0 += 16) {
@@ -70,11 +60,10 @@ __device__ __forceinline__ void scores(float (&x)[8][4], const bf16_t* as, const
 // A block: a chunk and a value head (o, dv), or a key head with all its value heads (dq, dk). 16 tokens and half of each
 // 64 columns of the output a warp; kSlices x 64 columns. (One block's tiles fill shared memory. Both warps of 16 tokens make
 // their scores: four warps that made each once took 436 us for 327 for o at 2 x 4096 x 16 x 128.)
-template <typename T, int kMode, int kSlices>
+template <int kMode, int kSlices>
 __global__ void __launch_bounds__(kThreads) rows_kernel(const Args a) {
   constexpr bool kUpper = kMode == kDv || kMode == kDk, kKeys = kMode == kDq || kMode == kDk;  // kKeys: the output is a key's
-  constexpr int kP = In<T>::kParts, kPc = kP == 1 ? 2 : 3, kPs = kKeys ? 3 : kPc;
-  using L = Layout<T, kPs>;
+  using L = Layout;
   extern __shared__ __align__(128) unsigned char smem[];
   const Shape& s = a.s;
   const int D = kKeys ? s.V : s.K, Dx = kKeys ? s.K : s.V, Dp = (D + 63) & ~63;
@@ -94,14 +83,14 @@ __global__ void __launch_bounds__(kThreads) rows_kernel(const Args a) {
 #pragma unroll
   for (int i = 0; i < kSlices; ++i) zero(acc[i]);
   const int hk = kKeys ? head : head / group;
-  const Tokens<T> q{static_cast<const T*>(a.q) + c.b * s.q_b + c.t0 * s.q_t + (size_t)hk * s.K, s.q_t, s.K};
-  const Tokens<T> k{static_cast<const T*>(a.k) + c.b * s.k_b + c.t0 * s.k_t + (size_t)hk * s.K, s.k_t, s.K};
+  const Tokens q{static_cast<const float*>(a.q) + c.b * s.q_b + c.t0 * s.q_t + (size_t)hk * s.K, s.q_t, s.K};
+  const Tokens k{static_cast<const float*>(a.k) + c.b * s.k_b + c.t0 * s.k_t + (size_t)hk * s.K, s.k_t, s.K};
   for (int hv = kKeys ? hk * group : head; hv < (kKeys ? (hk + 1) * group : head + 1); ++hv) {
-    const Tokens<T> v{static_cast<const T*>(a.v) + c.b * s.v_b + c.t0 * s.v_t + (size_t)hv * s.V, s.v_t, s.V};
-    const Tokens<T> d{static_cast<const T*>(a.d_o) + (tok * s.Hv + hv) * s.V, (long long)s.Hv * s.V, s.V};
-    const Tokens<T>&ta = kMode == kO ? q : kMode == kDv ? k : kMode == kDq ? d : v;
-    const Tokens<T>&tb = kMode == kO ? k : kMode == kDv ? q : kMode == kDq ? v : d;
-    const Tokens<T>&tx = kMode == kO ? v : kMode == kDv ? d : kMode == kDq ? k : q;
+    const Tokens v{static_cast<const float*>(a.v) + c.b * s.v_b + c.t0 * s.v_t + (size_t)hv * s.V, s.v_t, s.V};
+    const Tokens d{static_cast<const float*>(a.d_o) + (tok * s.Hv + hv) * s.V, (long long)s.Hv * s.V, s.V};
+    const Tokens&ta = kMode == kO ? q : kMode == kDv ? k : kMode == kDq ? d : v;
+    const Tokens&tb = kMode == kO ? k : kMode == kDv ? q : kMode == kDq ? v : d;
+    const Tokens&tx = kMode == kO ? v : kMode == kDv ? d : kMode == kDq ? k : q;
     const float* state = (kUpper ? a.dstates : a.states) + ((size_t)slot * s.Hv + hv) * s.V * s.K;
     const bool dg = kKeys && a.dg;
     __syncthreads();  // the head before is done with shared memory
@@ -118,14 +107,14 @@ __global__ void __launch_bounds__(kThreads) rows_kernel(const Args a) {
         fill_tile<kP, kC>(as, q.p, q.stride, c.len, s.K, nullptr, tid, kThreads);
         fill_tile<kP, kC>(bs, k.p, k.stride, c.len, s.K, nullptr, tid, kThreads);
         __syncthreads();
-        scores<kP, false>(qk, as, bs, s.K, Kp, warp, lane);
+        scores<false>(qk, as, bs, s.K, Kp, warp, lane);
       } else {  // in two halves
         for (int h = 0; h < 2; ++h) {
           fill_tile<kP, kC>(as, q.p + 64 * h, q.stride, c.len, h ? s.K - 64 : 64, nullptr, tid, kThreads);
           fill_tile<kP, kC>(bs, k.p + 64 * h, k.stride, c.len, h ? s.K - 64 : 64, nullptr, tid, kThreads);
           __syncthreads();
           float part[8][4];
-          scores<kP, false>(part, as, bs, h ? s.K - 64 : 64, 64, warp, lane);
+          scores<false>(part, as, bs, h ? s.K - 64 : 64, 64, warp, lane);
 #pragma unroll
           for (int n = 0; n < 8; ++n)
 #pragma unroll
@@ -138,10 +127,10 @@ __global__ void __launch_bounds__(kThreads) rows_kernel(const Args a) {
     fill_tile<kP, kC>(as, ta.p, ta.stride, c.len, D, nullptr, tid, kThreads);
     fill_tile<kP, kC>(bs, tb.p, tb.stride, c.len, D, nullptr, tid, kThreads);
     __syncthreads();
-    Frag<kPc> pf[4];
+    Frag<kP> pf[4];
     {
       float x[8][4];
-      scores<kP, kUpper>(x, as, bs, D, Dp, warp, lane);
+      scores<kUpper>(x, as, bs, D, Dp, warp, lane);
 #pragma unroll
       for (int h = 0; h < 2; ++h) {
         const int i = 16 * warp + gr + 8 * h;
@@ -218,7 +207,7 @@ __global__ void __launch_bounds__(kThreads) rows_kernel(const Args a) {
 #pragma unroll
             for (int e = 0; e < 8; ++e) whole = fmaf(f[b][e], f2[e], whole);
           }
-          put8<kPs>(ss + at(rows, r, col), 64 * Dp, f[b]);
+          put8<kP>(ss + at(rows, r, col), 64 * Dp, f[b]);
         }
       }
       __syncthreads();
@@ -228,7 +217,7 @@ __global__ void __launch_bounds__(kThreads) rows_kernel(const Args a) {
           float y0[4] = {0.f, 0.f, 0.f, 0.f}, y1[4] = {0.f, 0.f, 0.f, 0.f};
           for (int k0 = 0; k0 < D; k0 += 16) {
             Frag<kP> fa;
-            Frag<kPs> fb;
+            Frag<kP> fb;
             a_mk(fa, as, kC, kC * Dp, 16 * warp, k0, lane);
             if (kKeys)
               b_kn(fb, ss, Dp, 64 * Dp, 16 * n, k0, lane);
@@ -243,12 +232,12 @@ __global__ void __launch_bounds__(kThreads) rows_kernel(const Args a) {
             acc[sl][2 * n][e] += y0[e], acc[sl][2 * n + 1][e] += y1[e];
           }
           if (dg) {  // q.(the state's part of dq), or k.(that of dk)
-            const Tokens<T>& t = kMode == kDq ? q : k;
+            const Tokens& t = kMode == kDq ? q : k;
 #pragma unroll
             for (int h = 0; h < 2; ++h) {
               const int row = 16 * warp + gr + 8 * h, col = x0 + 16 * n + 2 * tq;
               if (row < c.len) {
-                const T* p = t.p + row * t.stride + col;
+                const float* p = t.p + row * t.stride + col;
                 if (col < Dx) {
                   const float2 z = load2(p);
                   dots[h] = fmaf(z.x, y0[2 * h], fmaf(z.y, y0[2 * h + 1], dots[h]));
@@ -316,10 +305,7 @@ __global__ void __launch_bounds__(kThreads) rows_kernel(const Args a) {
       }
     }
   }
-  T* out = kMode == kO   ? static_cast<T*>(a.o)
-           : kMode == kDv ? static_cast<T*>(a.dv)
-           : kMode == kDq ? static_cast<T*>(a.dq)
-                          : static_cast<T*>(a.dk);
+  float* out = static_cast<float*>(kMode == kO ? a.o : kMode == kDv ? a.dv : kMode == kDq ? a.dq : a.dk);
   out += (tok * heads + head) * Dx;
 #pragma unroll
   for (int sl = 0; sl < kSlices; ++sl)
@@ -328,37 +314,35 @@ __global__ void __launch_bounds__(kThreads) rows_kernel(const Args a) {
 #pragma unroll
       for (int h = 0; h < 2; ++h) {
         const int row = 16 * warp + gr + 8 * h, col = 64 * sl + 8 * n + 2 * tq;
-        if ((n >> 2) == half && row < c.len && col < Dx) store2(out + (size_t)row * heads * Dx + col, acc[sl][n][2 * h], acc[sl][n][2 * h + 1]);
+        if ((n >> 2) == half && row < c.len && col < Dx)
+          *reinterpret_cast<float2*>(out + (size_t)row * heads * Dx + col) = make_float2(acc[sl][n][2 * h], acc[sl][n][2 * h + 1]);
       }
 }
 
-template <typename T, int kMode, int kSlices>
+template <int kMode, int kSlices>
 cudaError_t launch(const Args& a, cudaStream_t stream) {
   constexpr bool kKeys = kMode == kDq || kMode == kDk;
-  using L = Layout<T, kKeys ? 3 : In<T>::kParts == 1 ? 2 : 3>;
   const int D = kKeys ? a.s.V : a.s.K;
   static std::atomic<unsigned long long> done{0};
-  const cudaError_t e = allow_smem(reinterpret_cast<const void*>(rows_kernel<T, kMode, kSlices>), L::size(kMaxDim), done);
+  const cudaError_t e = allow_smem(reinterpret_cast<const void*>(rows_kernel<kMode, kSlices>), Layout::size(kMaxDim), done);
   if (e != cudaSuccess) return e;
-  rows_kernel<T, kMode, kSlices><<<(unsigned)((size_t)a.s.slots * (kKeys ? a.s.Hk : a.s.Hv)), kThreads, L::size((D + 63) & ~63), stream>>>(a);
+  rows_kernel<kMode, kSlices><<<(unsigned)((size_t)a.s.slots * (kKeys ? a.s.Hk : a.s.Hv)), kThreads, Layout::size((D + 63) & ~63), stream>>>(a);
   return cudaGetLastError();
 }
-template <typename T, int kMode>
+template <int kMode>
 cudaError_t pick(const Args& a, cudaStream_t stream) {
   const int Dx = kMode == kDq || kMode == kDk ? a.s.K : a.s.V;
-  return Dx <= 64 ? launch<T, kMode, 1>(a, stream) : launch<T, kMode, 2>(a, stream);
-}
-template <typename T>
-cudaError_t grad(const Args& a, cudaStream_t stream) {
-  cudaError_t e = pick<T, kDv>(a, stream);
-  if (e == cudaSuccess) e = pick<T, kDq>(a, stream);
-  if (e == cudaSuccess) e = pick<T, kDk>(a, stream);
-  return e;
+  return Dx <= 64 ? launch<kMode, 1>(a, stream) : launch<kMode, 2>(a, stream);
 }
 
 }  // namespace
 
-cudaError_t launch_rows_o(const Args& a, cudaStream_t stream) { return pick<float, kO>(a, stream); }
-cudaError_t launch_rows_grad(const Args& a, cudaStream_t stream) { return grad<float>(a, stream); }
+cudaError_t launch_rows_o(const Args& a, cudaStream_t stream) { return pick<kO>(a, stream); }
+cudaError_t launch_rows_grad(const Args& a, cudaStream_t stream) {
+  cudaError_t e = pick<kDv>(a, stream);
+  if (e == cudaSuccess) e = pick<kDq>(a, stream);
+  if (e == cudaSuccess) e = pick<kDk>(a, stream);
+  return e;
+}
 
 }  // namespace linattn

@@ -13,16 +13,15 @@
 namespace linattn {
 namespace {
 
-constexpr int kThreads = 128, kC = kCF32;
+constexpr int kThreads = 128, kC = kCF32, kP = In<float>::kParts;
 
 // A block: a chunk, a value head, 64 values (16 a warp) by all keys.
 template <bool kBack, int kTiles>
 __global__ void __launch_bounds__(kThreads) sums_kernel(const Args a, float* out) {
-  typedef float T;
-  constexpr int kP = In<T>::kParts, kKp = kTiles * 8;
+  constexpr int kKp = kTiles * 8;
   extern __shared__ __align__(128) unsigned char smem[];
   bf16_t* xs = reinterpret_cast<bf16_t*>(smem);  // [64 tokens][64 values], 3 parts
-  bf16_t* bs = xs + 3 * kC * 64;                 // [64 tokens][keys]
+  bf16_t* bs = xs + kP * kC * 64;                // [64 tokens][keys]
   float2* G = reinterpret_cast<float2*>(bs + kP * kC * kKp);
   float* u = reinterpret_cast<float*>(G + kC);
   const Shape& s = a.s;
@@ -40,18 +39,18 @@ __global__ void __launch_bounds__(kThreads) sums_kernel(const Args a, float* out
     if (lane == 0 && slice == 0) a.decay[(size_t)slot * s.Hv + hv] = expf(G[kC - 1].x + G[kC - 1].y);
   }
   __syncthreads();
-  const T* x = kBack ? static_cast<const T*>(a.d_o) + (tok * s.Hv + hv) * s.V + v0
-                     : static_cast<const T*>(a.v) + c.b * s.v_b + c.t0 * s.v_t + (size_t)hv * s.V + v0;
-  const T* b = kBack ? static_cast<const T*>(a.q) + c.b * s.q_b + c.t0 * s.q_t + (size_t)hk * s.K
-                     : static_cast<const T*>(a.k) + c.b * s.k_b + c.t0 * s.k_t + (size_t)hk * s.K;
-  fill_tile<3, kC>(xs, x, kBack ? (long long)s.Hv * s.V : s.v_t, c.len, min(64, s.V - v0), u, tid, kThreads);
+  const float* x = kBack ? static_cast<const float*>(a.d_o) + (tok * s.Hv + hv) * s.V + v0
+                     : static_cast<const float*>(a.v) + c.b * s.v_b + c.t0 * s.v_t + (size_t)hv * s.V + v0;
+  const float* b = kBack ? static_cast<const float*>(a.q) + c.b * s.q_b + c.t0 * s.q_t + (size_t)hk * s.K
+                     : static_cast<const float*>(a.k) + c.b * s.k_b + c.t0 * s.k_t + (size_t)hk * s.K;
+  fill_tile<kP, kC>(xs, x, kBack ? (long long)s.Hv * s.V : s.v_t, c.len, min(64, s.V - v0), u, tid, kThreads);
   fill_tile<kP, kC>(bs, b, kBack ? s.q_t : s.k_t, c.len, s.K, nullptr, tid, kThreads);
   __syncthreads();
   float acc[kTiles][4];
   zero(acc);
 #pragma unroll
   for (int k0 = 0; k0 < kC; k0 += 16) {
-    Frag<3> fa;
+    Frag<kP> fa;
     a_km(fa, xs, kC, kC * 64, 16 * warp, k0, lane);
 #pragma unroll
     for (int n = 0; n < kTiles / 2; ++n) {
@@ -109,7 +108,7 @@ __global__ void __launch_bounds__(256) join_kernel(const Args a, float* states, 
 
 template <bool kBack, int kTiles>
 cudaError_t sums(const Args& a, cudaStream_t stream) {
-  constexpr size_t smem = (3 * kC * 64 + 3 * kC * kTiles * 8) * sizeof(bf16_t) + kC * 12;
+  constexpr size_t smem = (kP * kC * 64 + kP * kC * kTiles * 8) * sizeof(bf16_t) + kC * 12;
   static std::atomic<unsigned long long> done{0};
   const cudaError_t e = allow_smem(reinterpret_cast<const void*>(sums_kernel<kBack, kTiles>), smem, done);
   if (e != cudaSuccess) return e;
@@ -120,7 +119,7 @@ cudaError_t sums(const Args& a, cudaStream_t stream) {
 // Tokens in front of the first packed sequence and behind the last.
 __global__ void gaps_kernel(const Args a, const Gaps g) {
   const int t0 = seq_range(a.s, 0, a.s.C).t0, t1 = seq_range(a.s, a.s.nseq - 1, a.s.C).t1, none = a.s.T - max(t1 - t0, 0);
-  for (int i = 0; i < 5; ++i) {
+  for (int i = 0; i < kGapOutputs; ++i) {
     if (!g.at[i]) continue;
     for (int n = blockIdx.x; n < none; n += gridDim.x) {
       const long long t = n < t0 ? n : n + max(t1 - t0, 0);

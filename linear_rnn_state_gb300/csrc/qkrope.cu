@@ -444,7 +444,7 @@ int group_of(int D) { return D <= 32 ? 4 : D <= 64 ? 8 : D <= 128 ? 16 : 32; }
 int heads_of(const Args& p, long long tokens, int most) {
   for (int n = most; n > 1; n /= 2) {
     const long long units = (long long)((p.Hq + n - 1) / n) + (p.Hk + n - 1) / n;
-    if (units * n <= 5 * (p.Hq + p.Hk) / 4 && tokens * units >= 152 * 4 * (kThreads / group_of(p.D))) return n;
+    if (units * n <= 5 * (p.Hq + p.Hk) / 4 && tokens * units >= kSms * 4 * (kThreads / group_of(p.D))) return n;
   }
   return 1;
 }

@@ -9,7 +9,8 @@
 namespace qkrope {
 
 constexpr int kMaxD = 256;
-constexpr int kParts = 152 * 2;  // partial rows of the weights' gradients: two blocks an SM
+constexpr int kSms = 152;        // of the GPU that plans go by
+constexpr int kParts = kSms * 2;  // partial rows of the weights' gradients: two blocks an SM
 
 struct Args {
   const void *q, *k;
