@@ -37,7 +37,7 @@ struct Smem {
   float pairs[4][kCT];     // of a block of 32 rows: the sums over j < t
   float dots[2][kQ][kCT];  // q.(S's part of dq), k.(D's part of dk), by parts of the columns
   float whole[4 * kQ];
-  // Products: scores, rows, of the state's first 64 keys (two blocks an SM: of the chunk), each twice a value head, for dq and for dk; q k^T,
+  // Products: scores, rows, of the state's first 64 keys (two blocks an SM: of A's third part), each twice a value head, for dq and for dk; q k^T,
   // once. Copies: the tiles, once a head; the state and its gradient, 64 keys at a time.
   uint64_t done[4], end, full[2];
   uint32_t tmem;
@@ -77,7 +77,7 @@ __global__ void __launch_bounds__(128 * kQ, kQ == 2 ? 2 : 1) grad_kernel(const _
   enum { kE = 0, kQk = kF32 ? 320 : 128, kE2 = kF32 ? kQk : kE, kAt = kF32 ? 128 : 0, kOut = kF32 ? 0 : 128, kIn = kF32 ? 64 : 128 + KP, kThird = kQ == 2 ? kIn : kIn + KP };
   constexpr bool kHold = kQ == 2;  // registers for S's numbers, so that <S, D> need not read D from global memory (4 x 4096 x 32 x 64: 177 -> 168 us)
   // A block's columns when two share an SM: A's third part is where q k^T was (a thread stores it when it has read that, its
-  // last columns first) and where the state's products come to be, which wait for the chunk's.
+  // last columns first) and where the state's products come to be: those wait for its own, which are the chunk's first.
   constexpr bool kTight = kQ == 2;
   auto third_of = [](int blk) { return kThird + (kTight ? 32 * (blk & 1) + 16 * (blk >> 1) : 16 * blk); };
   constexpr bool kEarlyIn = !kF32 && KP == 128;  // the state's products have columns of their own
@@ -415,8 +415,8 @@ __global__ void __launch_bounds__(128 * kQ, kQ == 2 ? 2 : 1) grad_kernel(const _
               for (int ks = 0; ks < kCT / 16; ++ks)
                 tc_mma_t(tm + kOut + 64 * sl, tm + kAt + (kF32 ? part_at<3>(ks, p) : two_and_third(ks, p, third_of(ks >> 1) - kAt)),
                          dx + across(ks) + sl * (kRowPanel >> 4) + r * (kCT * KP * 2 >> 4), product_of(128, 64, false, true), !first || ks > 0);
+              if (kTight && first) tc_commit(&sm.done[2]);  // (the third part)
             });
-          if (kTight) tc_commit(&sm.done[2]);
           if (!kEarlyIn && !kTight) {
             inter(0);
             tc_commit(&sm.done[1]);
