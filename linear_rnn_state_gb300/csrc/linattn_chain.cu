@@ -5,8 +5,8 @@
 // backward (there in reverse, the state being the gradient D of the state after the chunk):
 //   P = mask . decay . (a b^T),  out = P x + w . (a S^T),  S <- e^{Gc} S + (u . x)^T b
 // P, S and u . x enter the products in three parts of bfloat16 (24 bits), so that o and dv are fp32 results rounded once. (P and S
-// in pairs, 16 bits, gave another neighbour of the exact value in 2 of 1000 places: 1e-4 in the 2-norm for 2e-5, at 4 % of a chain's
-// time with 64 keys and 14 % with 128.)
+// in pairs, 16 bits, gave another neighbour of the exact value in 2 of 1000 places: 1e-4 in the 2-norm for 2e-5, at 4 % less of a chain's
+// time with 64 keys and 10 % with 128.)
 //
 // Eight warps make P and the rows that leave, eight at the same time u . x and the state; one brings the tiles of a chunk
 // to come (TMA), one forms its decays and says which chunks follow, one issues the products.
@@ -16,12 +16,13 @@
 // tiles, two places for the scores); wider keys leave room for two stages, and u . x goes by halves of the tokens.
 //
 // A block that is done takes the place of one that has not begun and goes on with its chunks as if they were its own, a
-// list of steps ahead of the roles: no pause between short sequences (8191 tokens in 24 sequences, 32 heads of 128: 121 us for 147).
+// list of steps ahead of the roles: no pause between short sequences (8191 tokens in 24 sequences, 32 heads of 128: 121 us for 147 when
+// it was measured, 133 since the operands have three parts).
 // The first chunks of a block are slow (10 thousand cycles, then 6), for its code is cold: each role has one copy of what it does.
 //
-// Bound by the steps' latency, 5200 cycles a chunk with 64 keys and 6000 with 128, of which the products take 1100 to 1700
-// and shared memory's traffic 3100. Measured: 4 x 4096 x 32 x 64 86 us (369 MB with the images, 4.3 TB/s), 2 x 4095 x 32 x 128
-// 106 us (403 MB, 3.8 TB/s; 128 blocks of 64 values). One team of warps for all of it took 101 for 95 us.
+// Bound by the steps' latency, 5600 cycles a chunk with 64 keys and 6700 with 128, of which the products take 1500 to 2200
+// and shared memory's traffic 3100. Measured: 4 x 4096 x 32 x 64 94 us, backward 92 (369 MB with the images, 3.9 TB/s), 2 x 4095 x 32 x
+// 128 119 us (403 MB, 3.4 TB/s; 128 blocks of 64 values). One team of warps for all of it took 101 for 95 us when that was tried.
 #include "linattn_tc.cuh"
 
 namespace linattn {
@@ -105,7 +106,7 @@ __global__ void __launch_bounds__(kThreads, 1) chain_kernel(const __grid_constan
   const int slices = (s.V + 63) >> 6, group = s.Hv / s.Hk;
   const bool sums = plan.way == kSums;
   // More packed sequences than fit the GPU at once: long ones first, so that none is begun when the others end (24 in 8191
-  // tokens, 32 heads of 128, eight draws: 127 us for 130).
+  // tokens, 32 heads of 128, eight draws: 127 us for 130 when it was measured).
   const bool sorted = plan.way == kWhole && s.starts && s.nseq <= kSorted && gridDim.x > kSms;
   int* const lengths = reinterpret_cast<int*>(sm.xt);
   if (sorted && tid < s.nseq) {

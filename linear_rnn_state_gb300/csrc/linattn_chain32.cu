@@ -5,8 +5,8 @@
 // the next chunk when the products that read the places are done (P x runs beside it); they ask for them while the
 // products before run, and a warp has brought them to L2. Sums alone need b and u . x only, and have two places for each.
 //
-// Bound by the products: the tensor cores of a block's SM are busy 70 % of the time. 8 x 4096 x 12 x 64 takes 197 us (96
-// blocks, 6.1 us a chunk); 65536 x 40 x 64 in segments 382 us for the sums (1.3 GB, 3.5 TB/s) and 787 us for the
+// Bound by the products: the tensor cores of a block's SM are busy 68 % of the time. 8 x 4096 x 12 x 64 takes 201 us (96
+// blocks, 6.2 us a chunk); 65536 x 40 x 64 in segments 384 us for the sums (1.3 GB, 3.5 TB/s) and 790 us for the
 // rest (2.7 GB, 3.4 TB/s; 490 of products at the rate of the largest ones).
 //
 // Tensor memory: the scores (128 columns, later the rows' P x), P (192), a S^T (64), the state's sum (64).

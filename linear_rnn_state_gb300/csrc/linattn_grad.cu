@@ -13,13 +13,13 @@
 //
 // A block takes a chunk and a key head, one of its value heads after the other. A thread has a row of the
 // products, a half or (kQ = 4) a quarter of its columns. A, S and D enter in three parts (24 bits), S and D 64 keys of them
-// at a time, and fp32 inputs too. (A as a pair, for bfloat16 results: 1e-4 from the exact values rounded for 2e-5, at 6 % of the
+// at a time, and fp32 inputs too. (A as a pair, for bfloat16 results: 1e-4 from the exact values rounded for 2e-5, at 7 % less of the
 // gradients' time.)
 //
 // Bound by latency: a chunk's tiles and states come, are multiplied, decayed, multiplied again and read out, twice, one
-// step after the other, with one block an SM but for bfloat16's heads of 64. Measured: 4 x 4096 x 32 x 64 bfloat16 168 us
-// (605 MB with the states' images: 3.6 TB/s), 2 x 4095 x 16 and 32 x 128 220 us (670 MB, 3.0 TB/s), fp32 8 x 4096 x 12 x 64
-// 361 us (755 MB, 2.1 TB/s; six products of parts for each product, 105 us of them at the tensor cores' rate).
+// step after the other, with one block an SM but for bfloat16's heads of 64. Measured: 4 x 4096 x 32 x 64 bfloat16 183 us
+// (605 MB with the states' images: 3.3 TB/s), 2 x 4095 x 16 and 32 x 128 234 us (670 MB, 2.9 TB/s), fp32 8 x 4096 x 12 x 64
+// 362 us (755 MB, 2.1 TB/s; six products of parts for each product, 105 us of them at the tensor cores' rate).
 #include <type_traits>
 
 #include "linattn_tc.cuh"
@@ -75,7 +75,7 @@ __global__ void __launch_bounds__(128 * kQ, kQ == 2 ? 2 : 1) grad_kernel(const _
   // E of dq and of dk; A (bfloat16: two parts in its place, the third from kThird on); q k^T; then, where what was there has been
   // read, the chunk's and the state's products
   enum { kE = 0, kQk = kF32 ? 320 : 128, kE2 = kF32 ? kQk : kE, kAt = kF32 ? 128 : 0, kOut = kF32 ? 0 : 128, kIn = kF32 ? 64 : 128 + KP, kThird = kQ == 2 ? kIn : kIn + KP };
-  constexpr bool kHold = kQ == 2;  // registers for S's numbers, so that <S, D> need not read D from global memory (4 x 4096 x 32 x 64: 177 -> 168 us)
+  constexpr bool kHold = kQ == 2;  // registers for S's numbers, so that <S, D> need not read D from global memory (4 x 4096 x 32 x 64: 177 -> 168 us when it was measured)
   // A block's columns when two share an SM: A's third part is where q k^T was (a thread stores it when it has read that, its
   // last columns first) and where the state's products come to be: those wait for its own, which are the chunk's first.
   constexpr bool kTight = kQ == 2;

@@ -7,8 +7,8 @@
 // Bound by memory. A row belongs to a group of kGroup lanes with eight values each (16-byte
 // loads), and up to kIter heads of q or of k of a token to a group, all on their way at once. The cosines and sines
 // of a block's tokens are formed once, by all threads, in shared memory; a lane takes those of its values, and its
-// weights, once for its heads. Measured: 16384 x 64 x 64 bfloat16 47 us forward (5.7 TB/s) and 86 + 3 backward (4.7), bound
-// by instructions and latency at 12 to 24 warps an SM; 32768 x 24 x 64 fp32 63 us (6.4) and 105 + 3 (5.8).
+// weights, once for its heads. Measured: 16384 x 64 x 64 bfloat16 47 us forward (5.7 TB/s) and 92 + 3 backward (4.4), bound
+// by instructions and latency at 12 to 24 warps an SM; 32768 x 24 x 64 fp32 66 us (6.1) and 111 + 3 (5.4).
 //
 // Angles. freq / (2 pi) as a 64-bit fraction of a turn, times the position modulo 2^64, is the angle as a
 // fraction of a turn, off by no more than position * 2^-63; its upper 32 bits go to fp32 as a signed
